@@ -59,6 +59,30 @@ class MoeRouting(ctypes.Structure):
                  "block_map", "num_tiles", "logits")]
 
 
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("delta_f32", ctypes.c_int), ("quant_group", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong), ("delta_stride", ctypes.c_longlong),
+                ("out_stride", ctypes.c_longlong)]
+
+
+class MoeScoreDesc(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+class MoeLinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int), ("out_features", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("max_rank", ctypes.c_int),
+                ("wait_limit_ms", ctypes.c_int)]
+
+
+class MoeLora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n", ctypes.c_int), ("rank", ctypes.c_int)]
+
+
 class MoeTiming(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * len(KERNEL_KINDS)),
                 ("launches", ctypes.c_longlong * len(KERNEL_KINDS))]
@@ -98,6 +122,17 @@ def load_library(path: Optional[str] = None):
         "moe_read_timing": (S, [P, ctypes.POINTER(MoeTiming)]),
         "moe_last_gemm_path": (I, [P]),
         "moe_debug_buffer": (P, [P, I]),
+        "moe_norm_quant": (S, [ctypes.POINTER(MoeNormDesc), P, P, P, I, P, P, P, P, P]),
+        "moe_router_logits": (S, [P, P, I, P, P, P, P]),
+        "moe_route_scored": (S, [P, P, I, ctypes.POINTER(MoeScoreDesc),
+                                 ctypes.POINTER(MoeRouting), P]),
+        "moe_linear_scratch_bytes": (S, [ctypes.POINTER(MoeLinearDesc),
+                                         ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_linear_create": (S, [ctypes.POINTER(MoeLinearDesc), I, ctypes.POINTER(P)]),
+        "moe_linear_destroy": (S, [P]),
+        "moe_linear_forward": (S, [P, P, I, ctypes.c_longlong, P, I, ctypes.POINTER(MoeW4),
+                                   ctypes.POINTER(MoeLora), P, P, ctypes.c_longlong, P]),
+        "moe_linear_get_error": (S, [P]),
         "moe_route_noalloc": (S, [P, I, I, P, P, I, I, ctypes.POINTER(MoeRouting), P]),
         "moe_route_noalloc_get_error": (S, []),
         "moe_route_noalloc_debug_wait_timeout": (S, [I, P]),
@@ -241,6 +276,96 @@ def moe_residual_add(plan: int, x, y, T: int, alpha: float, x_out=None, xn_out=N
                      stream=None) -> None:
     _check(load_library().moe_residual_add(plan, _ptr(x), _ptr(y), T, float(alpha), _ptr(x_out),
                                            _ptr(xn_out), _stream(stream)), "moe_residual_add")
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def norm_desc(hidden: int, eps: float = 1e-6, alpha: float = 1.0, delta_f32: bool = False,
+              quant_group: int = 0, x_stride: int = 0, delta_stride: int = 0,
+              out_stride: int = 0) -> MoeNormDesc:
+    return MoeNormDesc(hidden, float(eps), float(alpha), int(bool(delta_f32)), quant_group,
+                       x_stride, delta_stride, out_stride)
+
+
+def moe_norm_quant(desc: MoeNormDesc, x, delta, weight, T: int, x_out=None, xn_out=None,
+                   q_out=None, q_scale=None, stream=None) -> None:
+    """Residual addition, RMS norm and e4m3 output (see header)."""
+    _check(load_library().moe_norm_quant(ctypes.byref(desc), _ptr(x), _ptr(delta), _ptr(weight), T,
+                                         _ptr(x_out), _ptr(xn_out), _ptr(q_out), _ptr(q_scale),
+                                         _stream(stream)), "moe_norm_quant")
+
+
+def moe_router_logits(plan: int, x, T: int, router_w, router_bias, logits, stream=None) -> None:
+    _check(load_library().moe_router_logits(plan, _ptr(x), T, _ptr(router_w), _ptr(router_bias),
+                                            _ptr(logits), _stream(stream)), "moe_router_logits")
+
+
+def score_desc(score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+               renormalise: bool = True, scale: float = 1.0) -> MoeScoreDesc:
+    """How ``moe_route_scored`` chooses (``bias`` must outlive the struct's use)."""
+    return MoeScoreDesc(SCORES[score], groups, topk_groups, int(bool(renormalise)), float(scale),
+                        _ptr(bias))
+
+
+def moe_route_scored(plan: int, logits, T: int, desc: MoeScoreDesc,
+                     routing: Optional[MoeRouting] = None, stream=None) -> MoeRouting:
+    """Routing by scores into the buffers that ``routing`` names; its empty
+    fields receive the plan's own."""
+    out = MoeRouting() if routing is None else routing
+    _check(load_library().moe_route_scored(plan, _ptr(logits), T, ctypes.byref(desc),
+                                           ctypes.byref(out), _stream(stream)),
+           "moe_route_scored")
+    return out
+
+
+def linear_desc(in_features: int, out_features: int, max_tokens: int = 4096, max_rank: int = 0,
+                wait_limit_ms: int = 0) -> MoeLinearDesc:
+    return MoeLinearDesc(in_features, out_features, max_tokens, max_rank, wait_limit_ms)
+
+
+def moe_linear_scratch_bytes(desc: MoeLinearDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().moe_linear_scratch_bytes(ctypes.byref(desc), ctypes.byref(out)),
+           "moe_linear_scratch_bytes")
+    return out.value
+
+
+def moe_linear_create(desc: MoeLinearDesc, device: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(load_library().moe_linear_create(ctypes.byref(desc), device, ctypes.byref(h)),
+           "moe_linear_create")
+    return h.value
+
+
+def moe_linear_destroy(linear: int) -> None:
+    _check(load_library().moe_linear_destroy(linear), "moe_linear_destroy")
+
+
+def w4(qweight, scales, biases) -> MoeW4:
+    """``MoeW4`` of one matrix from its three tensors (which must outlive it)."""
+    return MoeW4(_ptr(qweight), _ptr(scales), _ptr(biases))
+
+
+def lora(a, b, scale=None) -> MoeLora:
+    """``MoeLora`` from tensors a [n, r, K], b [n, N, r] and scale [n]."""
+    return MoeLora(_ptr(a), _ptr(b), _ptr(scale), a.shape[0], a.shape[1])
+
+
+def moe_linear_forward(linear: int, x, T: int, weight: MoeW4, y, x_scale=None,
+                       lora: Optional[MoeLora] = None, adapter=None, x_stride: int = 0,
+                       y_stride: int = 0, stream=None) -> None:
+    """4-bit projection with adapters; x is a bf16 or float8_e4m3fn tensor."""
+    x_type = 1 if x.element_size() == 1 else 0
+    _check(load_library().moe_linear_forward(
+        linear, _ptr(x), x_type, x_stride, _ptr(x_scale), T, ctypes.byref(weight),
+        ctypes.byref(lora) if lora is not None else None, _ptr(adapter), _ptr(y), y_stride,
+        _stream(stream)), "moe_linear_forward")
+
+
+def moe_linear_get_error(linear: int) -> int:
+    """Status code of the projection's device error word (read and cleared)."""
+    return load_library().moe_linear_get_error(linear)
 
 
 def moe_get_error(plan: int) -> int:

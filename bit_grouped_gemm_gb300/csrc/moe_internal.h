@@ -81,6 +81,22 @@ cudaError_t launch_route_large(const float* logits, int T, int E, int k, int32_t
                                int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
                                DevErr err, const uint16_t* x, uint16_t* xs, int H,
                                int with_shared, cudaStream_t st);
+// Routing by scores, from given logits (moe_route_scored): the same two forms
+// as launch_route_large and launch_router_select.
+struct ScoreArgs {
+  int sigmoid, groups, topk_groups, renorm;
+  float scale;
+  const float* bias;
+};
+bool score_large_fits(int T, int E, int k, int num_sms);
+cudaError_t launch_score_large(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                               int32_t* topk_idx, float* topk_w, uint8_t* cnt8, int32_t* cnt,
+                               int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
+                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
+                               DevErr err, cudaStream_t st);
+cudaError_t launch_score_select(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                                int32_t* topk_idx, float* topk_w, int32_t* blk_cnt,
+                                cudaStream_t st);
 cudaError_t launch_gather_rows(const uint16_t* x, const int32_t* perm, int T, int k, int H,
                                int with_shared, uint16_t* xs, DevErr err, cudaStream_t st);
 // Checks the fp16 operand range of n scales and biases (bf16) of a 4-bit
@@ -198,5 +214,24 @@ bool encode_router_slices(CUtensorMap* m, const void* base, int H, int E);
 // 3D map of a packed-word matrix uint32 [rows][K/8] as boxes of 32 words x
 // box_rows rows x K/256 chunks (one box = box_rows whole rows), 128-byte swizzle.
 bool encode_slab_3d(CUtensorMap* m, const void* base, uint64_t rows, int K, uint32_t box_rows);
+
+// ------------------------------------------------- 4-bit projection, adapters ---
+struct LinearArgs {
+  int T, K, N;
+  const void* x;                 // bf16 or e4m3 rows
+  int e4m3;
+  long long x_ld;                // elements
+  const float* x_scale;          // [T] or null
+  W4Dev w;
+  uint16_t* y;
+  long long y_ld;
+  const uint16_t *la, *lb;       // adapters, null: none
+  const float* lscale;
+  int n_adapters, rank;
+  const int32_t* adapter;
+  float* h;                      // scratch [T][rank]: scale * x A^T
+};
+cudaError_t launch_lora_shrink(const LinearArgs& a, cudaStream_t st);
+cudaError_t launch_linear_simple(const LinearArgs& a, cudaStream_t st);
 
 }  // namespace moe

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <set>
 #include <tuple>
+#include <type_traits>
 #include <vector>
 
 #include "moe_internal.h"
@@ -697,6 +698,74 @@ moe_status moe_grouped_w4_ffn(moe_plan_t p, const uint16_t* x, int T, const moe_
   moe_status s = check_ffn_args(p, x, T, r, routed, shared, y);
   if (s != MOE_OK) return s;
   return ffn_impl(p, x, T, r, routed, shared, y, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_router_logits(moe_plan_t p, const uint16_t* x, int T, const uint16_t* router_w,
+                             const float* router_bias, float* logits, moe_stream_t stream) {
+  if (!p || !logits || !aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  moe_status s = check_route_args(p, x, T, router_w, router_bias);
+  if (s != MOE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return st_of(timed(p, 0, st, [&] {
+    return launch_router_logits(x, T, p->d.hidden, router_w, router_bias, p->d.num_experts, logits,
+                                p->err(), st);
+  }));
+}
+
+moe_status moe_route_scored(moe_plan_t p, const float* logits, int T, const moe_score_desc* d,
+                            moe_routing* r, moe_stream_t stream) {
+  if (!p || !d || !r) return MOE_ERR_INVALID_ARG;
+  moe_status s = check_T(p, T);
+  if (s != MOE_OK) return s;
+  const int E = p->d.num_experts, k = p->d.top_k;
+  if (!logits || !aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  if (d->score < 0 || d->score > 1 || d->renormalise < 0 || d->renormalise > 1)
+    return MOE_ERR_INVALID_ARG;
+  if (d->groups < 1 || d->groups > 32 || E % d->groups || d->topk_groups < 1 ||
+      d->topk_groups > d->groups || d->topk_groups * (E / d->groups) < k)
+    return MOE_ERR_INVALID_ARG;
+  if (!(d->scale > -3e38f && d->scale < 3e38f)) return MOE_ERR_INVALID_ARG;
+  void* const outs[] = {r->topk_idx, r->topk_w, r->counts, r->offsets, r->tile_offsets,
+                        r->perm, r->inv, r->block_map, r->num_tiles, (void*)d->bias};
+  for (void* q : outs)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return MOE_ERR_INVALID_ARG;
+  auto own = [&](auto*& field, size_t off) {
+    if (!field) field = reinterpret_cast<std::remove_reference_t<decltype(field)>>(p->scratch + off);
+  };
+  own(r->topk_idx, p->L.topk_idx);
+  own(r->topk_w, p->L.topk_w);
+  own(r->counts, p->L.cnt);
+  own(r->offsets, p->L.off);
+  own(r->tile_offsets, p->L.tile_off);
+  own(r->perm, p->L.perm);
+  own(r->inv, p->L.inv);
+  own(r->block_map, p->L.bmap);
+  own(r->num_tiles, p->L.num_tiles);
+  const ScoreArgs a{d->score, d->groups, d->topk_groups, d->renormalise, d->scale, d->bias};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (score_large_fits(T, E, k, p->num_sms)) {
+    unsigned* w = p->at<unsigned>(p->L.arrive);
+    return st_of(timed(p, 8, st, [&] {
+      return launch_score_large(a, logits, T, E, k, r->topk_idx, r->topk_w,
+                                p->at<uint8_t>(p->L.cnt8), r->counts, r->offsets, r->tile_offsets,
+                                r->block_map, r->num_tiles, r->perm, r->inv, w, w + 1, p->err(), st);
+    }));
+  }
+  const int nblk = (T + kRouterTB - 1) / kRouterTB;
+  int32_t* blk = p->at<int32_t>(p->L.blk_cnt);
+  cudaError_t e = timed(p, 8, st, [&] {
+    return launch_score_select(a, logits, T, E, k, r->topk_idx, r->topk_w, blk, st);
+  });
+  if (e == cudaSuccess)
+    e = timed(p, 1, st, [&] {
+      return launch_route_scan(blk, nblk, T, k, E, r->counts, r->offsets, r->tile_offsets,
+                               r->block_map, r->num_tiles, st);
+    });
+  if (e == cudaSuccess)
+    e = timed(p, 2, st, [&] {
+      return launch_route_scatter(r->topk_idx, blk, T, k, E, r->perm, r->inv, st);
+    });
+  return st_of(e);
 }
 
 moe_status moe_forward_layer(moe_plan_t p, const uint16_t* x, int T, const uint16_t* router_w,

@@ -291,6 +291,137 @@ moe_status moe_route_noalloc_get_error(void);
  * or hanging the GPU. */
 moe_status moe_route_noalloc_debug_wait_timeout(int limit_us, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the layer around the expert block. The pages describe only the
+ * block; these are its neighbours in a served pre-norm layer: the residual's
+ * addition and RMS norm before it, a router's choice by scores, bias and
+ * groups, and 4-bit projections that carry the low-rank adapters of many
+ * requests at once.
+ * ------------------------------------------------------------------------- */
+
+/* Residual addition, RMS norm and 8-bit output. */
+typedef struct {
+  int hidden;              /* H: columns of a row; a multiple of 8, 8..16384 */
+  float eps;               /* added to the mean of squares; >= 0, finite */
+  float alpha;             /* factor of delta; finite */
+  int delta_f32;           /* delta's type: 0 bf16, 1 f32 (an expert block's y) */
+  int quant_group;         /* columns per 8-bit scale: 0 the whole row, or 128 */
+  long long x_stride;      /* elements between rows of x and of x_out; 0 = H */
+  long long delta_stride;  /* of delta; 0 = H */
+  long long out_stride;    /* of xn_out and of q_out; 0 = H */
+} moe_norm_desc;
+
+/* For every row t of T:
+ *   x_out = bf16(x + alpha * delta)              (x when delta is NULL)
+ *   v     = x_out / sqrt(mean_h x_out^2 + eps) * weight   (weight NULL: 1)
+ *   xn_out = bf16(v)
+ *   q_scale = max|v| / 448 over the row or over each 128 columns (the last
+ *             group of a row may be shorter)
+ *   q_out   = e4m3(v * 448 / max|v|), round to nearest even
+ * FP32 arithmetic; the mean of squares is over the bf16-rounded x_out, and v
+ * is quantised from its FP32 value, not from xn_out. A group whose max|v| is
+ * below 2^-100 gets scale 0 and codes 0. A NaN in a row makes its outputs and
+ * scales NaN.
+ * x bf16, delta bf16 or f32, weight bf16 [H] or NULL; x_out and xn_out bf16,
+ * q_out e4m3 bytes, q_scale f32 [T][1 or ceil(H/128)]. Each output may be
+ * NULL, but not all; q_out and q_scale come together. x_out may equal x (with
+ * the same rows); no other output may overlap an input or another output.
+ * Pointers 16-byte aligned, strides multiples of 8 and at least H. Needs no
+ * plan; runs on the current device. T >= 1. */
+moe_status moe_norm_quant(const moe_norm_desc* desc, const uint16_t* x, const void* delta,
+                          const uint16_t* weight, int T, uint16_t* x_out, uint16_t* xn_out,
+                          uint8_t* q_out, float* q_scale, moe_stream_t stream);
+
+/* How moe_route_scored scores and chooses. */
+typedef struct {
+  int score;               /* p = 0: softmax over all E, 1: sigmoid of the logit */
+  int groups;              /* the E experts in this many equal runs; 1..32, divides E */
+  int topk_groups;         /* groups a token may choose from; 1..groups */
+  int renormalise;         /* 1: the k weights are divided by their sum */
+  float scale;             /* factor of the weights, last; finite */
+  const float* bias;       /* f32 [E] added to p for the choice only, or NULL */
+} moe_score_desc;
+
+/* Router logits alone (the first step of moe_route, the same bits):
+ *   logits[t][e] = sum_h x[t][h] * router_w[h][e] + router_bias[e]
+ * logits: f32 [T][E], 16-byte aligned, caller's. Other arguments as moe_route. */
+moe_status moe_router_logits(moe_plan_t plan, const uint16_t* x, int T, const uint16_t* router_w,
+                             const float* router_bias, float* logits, moe_stream_t stream);
+
+/* Routing by scores, from given logits f32 [T][E]:
+ *   p = softmax or sigmoid of the logits; c = p + bias (no bias: the logits'
+ *   own order); with groups, a group's score is the sum of its two largest c
+ *   (p without a bias; its one c in groups of one), and only the topk_groups
+ *   best groups' experts are eligible; the k largest c of those are chosen, in
+ *   descending order; weight = p, over the chosen ones' sum if renormalise,
+ *   times scale.
+ * Equal values go to the lower index, of experts and of groups. The choice is
+ * that of 64-bit scores: where 32-bit ones lie too close to tell, they are
+ * taken again in 64 bits. A NaN logit counts as -infinity; a row with no
+ * finite maximum has p = 0 under softmax. An expert whose bias is -infinity
+ * or NaN is closed: chosen only when nothing else is eligible, and then with
+ * weight 0. Weights whose sum is 0 stay 0.
+ * Then counts, offsets, tile offsets, perm, inv and block map as moe_route
+ * makes them. `routing`: every field that is NULL receives the plan's scratch
+ * pointer; the others are the caller's device buffers (layouts of
+ * moe_routing, 4-byte aligned; block_map holds ceil(T*k/128) + E triples, of
+ * which num_tiles are written); `logits` is ignored. The result can be given
+ * to moe_grouped_w4_ffn. Errors: MOE_ERR_INVALID_ARG also when the eligible
+ * groups hold fewer than k experts. */
+moe_status moe_route_scored(moe_plan_t plan, const float* logits, int T,
+                            const moe_score_desc* desc, moe_routing* routing,
+                            moe_stream_t stream);
+
+/* A 4-bit projection with adapters: its sizes. */
+typedef struct {
+  int in_features;         /* K: a multiple of 64, at most 16384 */
+  int out_features;        /* N: 1..1048576 */
+  int max_tokens;          /* capacity: scratch is sized for this T, once */
+  int max_rank;            /* largest adapter rank: a multiple of 8, 0..128; 0: none */
+  int wait_limit_ms;       /* device bounded-wait limit (default 1000 if 0) */
+} moe_linear_desc;
+
+typedef struct moe_linear* moe_linear_t;
+
+/* n low-rank adapters of one rank r on a K -> N projection. */
+typedef struct {
+  const uint16_t* a;       /* bf16 [n][r][K] */
+  const uint16_t* b;       /* bf16 [n][N][r] */
+  const float* scale;      /* f32 [n], or NULL: 1 */
+  int n;                   /* adapters, 1..65536 */
+  int rank;                /* r: a multiple of 8, 8..max_rank */
+} moe_lora;
+
+typedef enum { MOE_X_BF16 = 0, MOE_X_E4M3 = 1 } moe_x_type;
+
+moe_status moe_linear_create(const moe_linear_desc* desc, int device, moe_linear_t* out);
+moe_status moe_linear_destroy(moe_linear_t linear);
+moe_status moe_linear_scratch_bytes(const moe_linear_desc* desc, size_t* bytes);
+
+/* For every row t of T, with W as in moe_w4 (E = 1) and a = adapter[t]:
+ *   y[t] = bf16(x_scale[t] * (x[t] W^T + scale[a] * (x[t] A[a]^T) B[a]^T))
+ * adapter: int32 [T]; a value outside 0..n-1 (such as -1) means no adapter.
+ * lora and adapter are both NULL or both given. x: bf16 with x_scale NULL, or
+ * e4m3 bytes with x_scale f32 [T] (moe_norm_quant's row scales) or NULL (1).
+ * x_stride and y_stride: elements between rows, 0 = K and N; x_stride is a
+ * multiple of 16, y_stride at least N. x, x_scale and the weights 16-byte
+ * aligned, y and adapter 4-byte. y overlaps no input. Rows may come in any
+ * order of adapters; rows of one adapter next to each other are fastest.
+ * The sums are FP32; weights are rebuilt as fp16(q * scale + bias) and bf16
+ * rows enter as fp16 under the operand contract above, reported by
+ * moe_linear_get_error; x A^T is kept to 16 significant bits. Weights and
+ * adapters are read under the rule for weights above; like them, `adapter`
+ * and x must not be written by a kernel that the call's own launches could
+ * overtake: any launch before the call on the same stream is waited for.
+ * Calls on one handle must be ordered on the device. */
+moe_status moe_linear_forward(moe_linear_t linear, const void* x, int x_type, long long x_stride,
+                              const float* x_scale, int T, const moe_w4* w,
+                              const moe_lora* lora, const int32_t* adapter, uint16_t* y,
+                              long long y_stride, moe_stream_t stream);
+
+/* As moe_get_error, for a projection. */
+moe_status moe_linear_get_error(moe_linear_t linear);
+
 /* Reads and clears the plan's device error word. Synchronises the device:
  * call it between layers or steps, never inside one. Returns MOE_OK,
  * MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out; reported first),
