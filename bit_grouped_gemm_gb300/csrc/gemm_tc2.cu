@@ -41,7 +41,7 @@
 // Every wait is bounded: on timeout a CTA latches the error, lets its own
 // copies land, stops, and both CTAs meet at the final cluster barrier
 // before the tensor memory is released.
-#include "moe_common.cuh"
+#include "pair.cuh"
 
 namespace moe {
 namespace tc2 {
@@ -126,48 +126,6 @@ __device__ __forceinline__ Unit make_unit(const Params& p, int u, int n_routed, 
 // N of the pair MMA: rows rounded up to 32 (each CTA's half a multiple of 16)
 __device__ __forceinline__ int unit_n(int rows) { return (rows + 31) & ~31; }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Address, in the leader CTA (rank 0), of this CTA's shared variable `p`.
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
-  return r;
-}
-// Arrival on a barrier given by its cluster address, after a release fence
-// restricted to shared::cta memory: orders the shared-memory writes this
-// thread has observed (a token tile landed by TMA) before the arrival. A full
-// release at cluster scope would also wait for every global access in flight
-// and cost about a microsecond per arrival.
-__device__ __forceinline__ void arrive_cluster_shared(uint32_t cluster_addr) {
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// Relaxed arrival on a barrier given by its cluster address: for a thread
-// whose tensor-memory accesses completed (tcgen05.wait) and are ordered by
-// tcgen05.fence::before_thread_sync, so the arrival does not wait for the
-// thread's unrelated global loads and stores to drain.
-__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
-
 // Suspend-time hint of the waits: a thread whose phase is not complete
 // sleeps at most this long before it looks again.
 constexpr uint32_t kHintNs = 100000;
@@ -220,16 +178,6 @@ __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsig
   }
 }
 
-__device__ __forceinline__ void tmem_alloc2(uint32_t* slot) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
-               "r"(kTmemCols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols)
-               : "memory");
-}
 // D[tmem] (+)= A[tmem] * B[smem desc] over the pair; kind::f16.
 __device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -237,15 +185,6 @@ __device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at `bar`'s offset in both CTAs once every MMA issued
-// so far by this thread is done.
-__device__ __forceinline__ void mma2_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((unsigned short)3)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -304,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_grouped_gemm_tc2(const __grid_
       tma_prefetch_desc(&p.maps.sq1);
     }
   }
-  if (warp == 1) tmem_alloc2(tmem_slot);
+  if (warp == 1) tmem_alloc2(tmem_slot, kTmemCols);
   tc_fence_before();
   // both CTAs' barriers initialised and TMEM allocated before any remote arrival
   cluster_sync_all();
@@ -626,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_grouped_gemm_tc2(const __grid_
   // neither CTA leaves (or frees TMEM) while the other may still touch it
   cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc2(tmem);
+  if (warp == 1) tmem_dealloc2(tmem, kTmemCols);
 }
 
 }  // namespace tc2

@@ -11,8 +11,10 @@ namespace {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-  size_t err, h, total;
+  size_t err, h, x16, w16, total;
 };
+
+constexpr int kWidths = 8;   // tile widths of the large product: 32, 64, .. 256
 
 Layout make_layout(const moe_linear_desc& d) {
   Layout L;
@@ -24,6 +26,12 @@ Layout make_layout(const moe_linear_desc& d) {
   };
   L.err = take(16);
   L.h = take((size_t)d.max_tokens * d.max_rank * 4);
+  if (d.max_tokens > kLinearSmallT) {
+    L.x16 = take((size_t)d.max_tokens * d.in_features * 2);
+    L.w16 = take((size_t)d.out_features * d.in_features * 2);
+  } else {
+    L.x16 = L.w16 = 0;
+  }
   L.total = o;
   return L;
 }
@@ -55,6 +63,7 @@ struct moe_linear {
   int num_sms = 0;
   Layout L;
   uint8_t* scratch = nullptr;
+  CUtensorMap mx, mw[kWidths];   // x16, and w16 by tile width
 
   DevErr err() const {
     DevErr e;
@@ -62,6 +71,19 @@ struct moe_linear {
     e.where = e.word + 1;
     e.limit_ns = (unsigned long long)(d.wait_limit_ms > 0 ? d.wait_limit_ms : 1000) * 1000000ull;
     return e;
+  }
+  template <class T>
+  T* at(size_t off) const {
+    return reinterpret_cast<T*>(scratch + off);
+  }
+  bool encode() {
+    if (d.max_tokens <= kLinearSmallT) return true;
+    bool ok = encode_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, at<uint16_t>(L.x16), d.max_tokens,
+                        d.in_features, 64, 128);
+    for (int i = 0; i < kWidths && ok; ++i)
+      ok = encode_2d(&mw[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, at<uint16_t>(L.w16),
+                     d.out_features, d.in_features, 64, 16 * (i + 1));
+    return ok;
   }
 };
 
@@ -102,7 +124,7 @@ moe_status moe_linear_create(const moe_linear_desc* desc, int device, moe_linear
     p->L = make_layout(*desc);
     if (cudaMalloc(&p->scratch, p->L.total) != cudaSuccess) {
       res = MOE_ERR_CUDA;
-    } else if (cudaMemset(p->scratch + p->L.err, 0, 16) != cudaSuccess ||
+    } else if (!p->encode() || cudaMemset(p->scratch + p->L.err, 0, 16) != cudaSuccess ||
                cudaDeviceSynchronize() != cudaSuccess) {
       cudaFree(p->scratch);
       res = MOE_ERR_CUDA;
@@ -184,8 +206,18 @@ moe_status moe_linear_forward(moe_linear_t p, const void* x, int x_type, long lo
     a.h = reinterpret_cast<float*>(p->scratch + p->L.h);
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (lora && launch_lora_shrink(a, st) != cudaSuccess) return MOE_ERR_CUDA;
-  return launch_linear_simple(a, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (T <= kLinearSmallT) {
+    if (lora) e = launch_lora_shrink(a, st);
+    if (e == cudaSuccess) e = launch_linear_small(a, p->err(), st);
+  } else {
+    e = launch_linear_prep(a, p->at<uint16_t>(p->L.x16), p->at<uint16_t>(p->L.w16), p->err(), st);
+    if (e == cudaSuccess) {
+      const int bn = linear_tile_n(T, N, p->num_sms);
+      e = launch_linear_tc(a, p->mx, p->mw[bn / 32 - 1], bn, p->err(), p->num_sms, st);
+    }
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_linear_get_error(moe_linear_t p) {

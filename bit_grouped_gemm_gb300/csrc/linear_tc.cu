@@ -1,0 +1,437 @@
+// linear_tc.cu -- the projection's product for more than a decode batch, on
+// pairs of SMs (tcgen05 cta_group::2):
+//   y[t][n] = x_scale[t] (sum_k x16[t][k] W16[n][k] + sum_r h[t][r] B[a_t][n][r])
+// from the fp16 rows, the fp16 weights and the adapters' h = scale x A^T that
+// the launch before it wrote (w4_linear.cu).
+//
+// A tile is 256 tokens x BN outputs; each CTA of the pair holds 128 token rows
+// (operand A) and BN / 2 weight rows (operand B), and its 128 rows of the
+// accumulator, of which TMEM holds two, so that a tile's epilogue runs under
+// the next tile's MMAs. K goes by in chunks of 64.
+//
+// The adapters are more columns of K. For every adapter that occurs among the
+// tile's tokens the tile gets K columns with h in A, zero in the rows of other
+// tokens, and B[a] in B: the MMAs then add each token's own product, whatever
+// the order of the tokens. h goes in as two bf16 (the value and what its
+// rounding left), against B's own bf16: the products are exact to 16 bits of h.
+// Four warps write these chunks, spread between the tile's other chunks.
+//
+// Every wait is bounded, as in gemm_tc2.cu.
+#include "pair.cuh"
+
+namespace moe {
+namespace lin {
+
+constexpr int kThreads = 320;             // TMA, MMA, 4 adapter, 4 epilogue warps
+constexpr int kTileM = 256;
+constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr uint32_t kTmemCols = 512;
+
+template <bool kLora>
+struct Smem {
+  static constexpr int kStages = kLora ? 5 : 6;
+  static constexpr int kOffLora = kStages * kStageBytes;
+  static constexpr int kOffIds = kOffLora + (kLora ? kStageBytes : 0);
+  static constexpr int kOffBar = kOffIds + (kLora ? 2 * kTileM * 4 : 0);
+  static constexpr int kBytes = kOffBar + 512 + 1024;   // barriers, alignment slack
+};
+static_assert(Smem<true>::kBytes <= 227 * 1024 && Smem<false>::kBytes <= 227 * 1024, "shared memory");
+
+struct Params {
+  CUtensorMap mx;       // x16 [rows][K], boxes 64 x 128
+  CUtensorMap mw;       // W16 [N][K], boxes 64 x BN / 2
+  LinearArgs a;
+  int bn, mt, tiles;    // tile width, token tiles, all tiles
+  DevErr err;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          const DevErr& err, int site) {
+  bool ok = try_wait_cluster(bar, parity, 0);
+  if (!ok) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+      if (try_wait_cluster(bar, parity, 100000)) {
+        ok = true;
+        break;
+      }
+      if (*abort_flag) break;
+      if (globaltimer_ns() - t0 > err.limit_ns) break;
+    }
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) {
+    if ((threadIdx.x & 31) == 0 && !*abort_flag) report_timeout(err, site);
+    *abort_flag = 1;
+  }
+  return ok;
+}
+
+__device__ __forceinline__ int token_adapter(const LinearArgs& a, int t) {
+  const int id = t < a.T ? __ldg(a.adapter + t) : -1;
+  return (unsigned)id < (unsigned)a.n_adapters ? id : -1;
+}
+
+// h[0..15] of one 16-column block as bf16: the rounded values (lo = false) or
+// what the rounding left.
+__device__ __forceinline__ void split_h(const float4 (&v)[4], bool rest, uint32_t (&o)[8]) {
+  const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                       v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    o[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    if (rest) o[i] = pack_bf16x2(f[2 * i] - bf16_lo(o[i]), f[2 * i + 1] - bf16_hi(o[i]));
+  }
+}
+
+// Barrier of the 128 adapter threads that tells whether all of them go on, so
+// that they leave their loop together and none is waited for in vain.
+__device__ __forceinline__ bool bar_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, 1, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// Instruction descriptor with bf16 operands (else as idesc_f16_f32).
+__device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
+  return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);
+}
+
+template <bool kLora>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_tc_kernel(const __grid_constant__ Params p) {
+  using S = Smem<kLora>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
+  uint8_t* lora_a = smem + S::kOffLora;
+  uint8_t* lora_b = lora_a + kOpBytes;
+  int* s_ids = reinterpret_cast<int*>(smem + S::kOffIds);   // the tile's adapter per token
+  int* s_list = s_ids + kTileM;                             // its distinct adapters
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t* full = bars;                   // leader: both CTAs' operands landed
+  uint64_t* empty = full + 6;              // chunk's MMAs done (both CTAs)
+  uint64_t* acc_full = empty + 6;          // [2] tile's MMAs done (both CTAs)
+  uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
+  uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs wrote an adapter chunk
+  uint64_t* lora_empty = lora_full + 1;    // adapter chunk's MMAs done (both CTAs)
+  uint64_t* list_full = lora_empty + 1;    // [2] the tile's adapter steps are known (own CTA)
+  uint64_t* drain = list_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_steps = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2] by tile parity
+  int* s_cnt = reinterpret_cast<int*>(tmem_slot + 4);       // [8] adapters per 32 tokens
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+      mbar_init(&list_full[i], 1);
+    }
+    mbar_init(lora_full, 2);
+    mbar_init(lora_empty, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.mx);
+    tma_prefetch_desc(&p.mw);
+  }
+  if (warp == 1) tmem_alloc2(tmem_slot, kTmemCols);
+  tc_fence_before();
+  cluster_sync_all();   // barriers and TMEM of both CTAs, before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_begin();          // operands come from the launch before
+
+  const int nk = p.a.K / 64;
+  const int half = p.bn >> 1;
+  const int rb = (p.a.rank + 15) >> 4;   // 16-column steps per adapter and part
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA, own halves
+    const uint32_t bytes = 2u * (kOpBytes + (uint32_t)half * 128u);   // of both CTAs
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int u = pair; u < p.tiles && ok; u += npairs) {
+      const int m0 = (u % p.mt) * kTileM + 128 * (int)rank;
+      const int n0 = (u / p.mt) * p.bn + half * (int)rank;
+      for (int c = 0; c < nk; ++c, ++cnt) {
+        const int s = cnt % kStages;
+        if (!(ok = warp_wait(&empty[s], ((cnt / kStages) & 1) ^ 1, abort_flag, p.err, 80))) break;
+        if (elect_one_sync()) {
+          uint8_t* dst = smem + s * kStageBytes;
+          if (leader) mbar_arrive_expect_tx(&full[s], bytes);
+          tma_load_2d_pair(dst, &p.mx, 64 * c, m0, leader_addr(&full[s]));
+          tma_load_2d_pair(dst + kOpBytes, &p.mw, 64 * c, n0, leader_addr(&full[s]));
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      // Gave up: the copies in flight land on the leader's barriers, which the
+      // other CTA cannot wait on; both leave them a millisecond.
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------- MMA issuer, leader
+    if (leader) {
+      const uint32_t idesc = idesc_f16_f32(256, p.bn), idesc_l = idesc_bf16(256, p.bn);
+      uint32_t cnt = 0, lcnt = 0, it = 0;
+      bool ok = true;
+      for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
+        const uint32_t acc = tmem + 256 * (it & 1);
+        int steps = 0;
+        if (kLora) {
+          if (!(ok = warp_wait(&list_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 81))) break;
+          steps = s_steps[it & 1];
+        }
+        const int nl = (steps + 3) >> 2;
+        int j = 0;
+        if (!(ok = warp_wait(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
+        tc_fence_after();
+        for (int c = 0; c < nk; ++c, ++cnt) {
+          const int s = cnt % kStages;
+          if (!(ok = warp_wait(&full[s], (cnt / kStages) & 1, abort_flag, p.err, 83))) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint32_t base = smem_u32(smem + s * kStageBytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma2_f16_ss(acc, smem_desc_sw128(base + 32 * kk),
+                          smem_desc_sw128(base + kOpBytes + 32 * kk), idesc, (c | kk) != 0);
+            mma2_commit_both(&empty[s]);
+          }
+          __syncwarp();
+          // the adapter chunks that are due, evenly among the others
+          while (kLora && j < nl && c + 1 >= ((j + 1) * nk) / (nl + 1)) {
+            if (!(ok = warp_wait(lora_full, lcnt & 1, abort_flag, p.err, 84))) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+              const uint32_t ab = smem_u32(lora_a), bb = smem_u32(lora_b);
+              const int n = min(4, steps - 4 * j);
+              for (int kk = 0; kk < n; ++kk)
+                mma2_f16_ss(acc, smem_desc_sw128(ab + 32 * kk), smem_desc_sw128(bb + 32 * kk), idesc_l, 1);
+              mma2_commit_both(lora_empty);
+            }
+            __syncwarp();
+            ++j;
+            ++lcnt;
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        if (elect_one_sync()) mma2_commit_both(&acc_full[it & 1]);
+        __syncwarp();
+      }
+      if (elect_one_sync()) mma2_commit_both(drain);
+      __syncwarp();
+    }
+    // every MMA that reads this CTA's memory is done before it is released
+    const unsigned long long t0 = globaltimer_ns();
+    while (!try_wait_cluster(drain, 0, 100000) && globaltimer_ns() - t0 < 2 * p.err.limit_ns) {
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------- adapters' K columns
+    if (kLora) {
+      const int i = threadIdx.x - 64;   // 0..127: A row and B row of this thread
+      uint32_t lcnt = 0, it = 0;
+      bool ok = true;
+      const uint32_t lora_full_l = leader_addr(lora_full);
+      for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
+        const int m0 = (u % p.mt) * kTileM, n0 = (u / p.mt) * p.bn;
+        // the tile's distinct adapters, in the order of their first tokens
+        const int id0 = token_adapter(p.a, m0 + i), id1 = token_adapter(p.a, m0 + 128 + i);
+        s_ids[i] = id0;
+        s_ids[128 + i] = id1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        unsigned first[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int pos = i + 128 * q, id = q ? id1 : id0;
+          bool is = id >= 0 && (pos == 0 || s_ids[pos - 1] != id);
+          for (int e = 0; is && e < pos; ++e) is = s_ids[e] != id;
+          first[q] = __ballot_sync(0xffffffffu, is);
+          if (lane == 0) s_cnt[4 * q + (i >> 5)] = __popc(first[q]);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        int nad = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if ((w & 3) == (i >> 5) && ((first[w >> 2] >> lane) & 1u))
+            s_list[nad + __popc(first[w >> 2] & ((1u << lane) - 1u))] = w < 4 ? id0 : id1;
+          nad += s_cnt[w];
+        }
+        const int steps = 2 * rb * nad, nl = (steps + 3) >> 2;
+        // the count of two tiles ago has been read once that tile is done
+        if (it >= 2) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
+        if (!(ok = bar_and(ok))) break;
+        if (i == 0) {
+          s_steps[it & 1] = steps;
+          mbar_arrive(&list_full[it & 1]);
+        }
+        const int my_id = rank ? id1 : id0;
+        const float* hrow = p.a.h + (size_t)min(m0 + 128 * (int)rank + i, p.a.T - 1) * p.a.rank;
+        const int n = n0 + half * (int)rank + i;
+        const bool brow = i < half && n < p.a.N;
+        for (int j = 0; j < nl && ok; ++j, ++lcnt) {
+          uint32_t va[4][8], vb[4][8];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int st = 4 * j + kk;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) va[kk][e] = vb[kk][e] = 0u;
+            if (st >= steps) continue;
+            const int ad = s_list[st / (2 * rb)], rem = st % (2 * rb);
+            const int blk = rem >= rb ? rem - rb : rem;
+            const bool two = 16 * blk + 16 <= p.a.rank;   // else the last 8 columns are zero
+            if (ad == my_id) {
+              const float4* h4 = reinterpret_cast<const float4*>(hrow + 16 * blk);
+              float4 v[4];
+              const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+              v[0] = __ldcg(h4);
+              v[1] = __ldcg(h4 + 1);
+              v[2] = two ? __ldcg(h4 + 2) : z;
+              v[3] = two ? __ldcg(h4 + 3) : z;
+              split_h(v, rem >= rb, va[kk]);
+            }
+            if (brow) {
+              const uint4* b4 = reinterpret_cast<const uint4*>(
+                  p.a.lb + ((size_t)ad * p.a.N + n) * p.a.rank + 16 * blk);
+              const uint4 x0 = __ldg(b4);
+              const uint4 x1 = two ? __ldg(b4 + 1) : make_uint4(0u, 0u, 0u, 0u);
+              vb[kk][0] = x0.x; vb[kk][1] = x0.y; vb[kk][2] = x0.z; vb[kk][3] = x0.w;
+              vb[kk][4] = x1.x; vb[kk][5] = x1.y; vb[kk][6] = x1.z; vb[kk][7] = x1.w;
+            }
+          }
+          if (lcnt >= 1) ok = warp_wait(lora_empty, (lcnt - 1) & 1, abort_flag, p.err, 86);
+          if (!(ok = bar_and(ok))) break;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t off = i * 128 + (((2 * kk + q) ^ (i & 7)) << 4);
+              *reinterpret_cast<uint4*>(lora_a + off) =
+                  make_uint4(va[kk][4 * q], va[kk][4 * q + 1], va[kk][4 * q + 2], va[kk][4 * q + 3]);
+              if (i < half)
+                *reinterpret_cast<uint4*>(lora_b + off) =
+                    make_uint4(vb[kk][4 * q], vb[kk][4 * q + 1], vb[kk][4 * q + 2], vb[kk][4 * q + 3]);
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (i == 0) arrive_cluster_shared(lora_full_l);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, row = 32 * quarter + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t acc_empty_l = leader_addr(acc_empty);
+    const bool wide = (p.a.y_ld & 7) == 0 && (reinterpret_cast<uintptr_t>(p.a.y) & 15u) == 0;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
+      const int t = (u % p.mt) * kTileM + 128 * (int)rank + row, n0 = (u / p.mt) * p.bn;
+      const bool live = t < p.a.T;
+      const float sc = live && p.a.x_scale ? __ldg(p.a.x_scale + t) : 1.f;
+      if (!(ok = warp_wait(&acc_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 87))) break;
+      tc_fence_after();
+      for (int c0 = 0; c0 < p.bn; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + lane_base + 256 * (it & 1) + c0, v);
+        tmem_wait_ld();
+        if (c0 + 32 >= p.bn) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster_relaxed(acc_empty_l + 8 * (it & 1));
+        }
+        const int n = n0 + c0;
+        uint16_t* o = p.a.y + t * p.a.y_ld + n;
+        if (!live) {
+        } else if (wide && n + 32 <= p.a.N) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * sc,
+                                 __uint_as_float(v[8 * q + 2 * e + 1]) * sc);
+            reinterpret_cast<uint4*>(o)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (n + e < p.a.N) o[e] = f32_to_bf16(__uint_as_float(v[e]) * sc);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, kTmemCols);
+  }
+}
+
+}  // namespace lin
+
+// Tile width: rounds of tiles over the pairs, each at the slower of its MMAs
+// (2 cycles per column and chunk) and its operands' copies (about 50 bytes per
+// cycle and SM).
+int linear_tile_n(int T, int N, int num_sms) {
+  const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2;
+  int best = 256;
+  double cost = 1e30;
+  for (int bn = 256; bn >= 32; bn -= 32) {
+    const long long tiles = (long long)mt * ((N + bn - 1) / bn);
+    const double chunk = fmax(2.0 * bn, (16384.0 + 64.0 * bn) / 50.0);
+    const double c = (double)((tiles + pairs - 1) / pairs) * chunk;
+    if (c < cost * 0.999) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap& mw,
+                             int bn, DevErr err, int num_sms, cudaStream_t st) {
+  lin::Params p;
+  p.mx = mx;
+  p.mw = mw;
+  p.a = a;
+  p.bn = bn;
+  p.mt = (a.T + lin::kTileM - 1) / lin::kTileM;
+  p.tiles = p.mt * ((a.N + bn - 1) / bn);
+  p.err = err;
+  int pairs = num_sms / 2;
+  if (pairs > p.tiles) pairs = p.tiles;
+  auto go = [&](auto kern, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(2 * pairs), dim3(lin::kThreads), smem, st, p);
+  };
+  return a.la ? go(lin::linear_tc_kernel<true>, lin::Smem<true>::kBytes)
+              : go(lin::linear_tc_kernel<false>, lin::Smem<false>::kBytes);
+}
+
+}  // namespace moe

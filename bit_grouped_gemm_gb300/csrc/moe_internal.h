@@ -231,7 +231,18 @@ struct LinearArgs {
   const int32_t* adapter;
   float* h;                      // scratch [T][rank]: scale * x A^T
 };
+// Decode batches (T <= kLinearSmallT): the adapters' h, then the product on
+// mma.sync straight from the packed weights.
+constexpr int kLinearSmallT = 64;
 cudaError_t launch_lora_shrink(const LinearArgs& a, cudaStream_t st);
-cudaError_t launch_linear_simple(const LinearArgs& a, cudaStream_t st);
+cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st);
+// Above: x as fp16 rows x16 [T][K], W as fp16 w16 [N][K] (both with every
+// block of 8 columns in perm8 order) and the adapters' h in one launch, then
+// the product on SM pairs. mw: w16 with boxes of 64 x linear_tile_n / 2.
+cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
+                               cudaStream_t st);
+int linear_tile_n(int T, int N, int num_sms);
+cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap& mw,
+                             int bn, DevErr err, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -556,6 +556,16 @@ def test_linear_in_a_graph(T):
     bg.moe_linear_destroy(h)
 
 
+@pytest.mark.parametrize("T", [1, 200])
+def test_linear_flags_values_beyond_the_operands(T):
+    c = Linear(T, 256, 128)
+    c.x[T - 1, 9] = 1e6
+    assert c.run() == 6                            # MOE_ERR_OPERAND_RANGE
+    c = Linear(T, 256, 128)
+    c.w[1][5, 1] = 3e-6
+    assert c.run() == 6
+
+
 def test_linear_refusals_with_a_handle():
     import ctypes
     lib = bg.load_library()
