@@ -81,22 +81,24 @@ cudaError_t launch_route_large(const float* logits, int T, int E, int k, int32_t
                                int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
                                DevErr err, const uint16_t* x, uint16_t* xs, int H,
                                int with_shared, cudaStream_t st);
-// Routing by scores, from given logits (moe_route_scored): the same two forms
-// as launch_route_large and launch_router_select.
+// Routing by scores, from given logits (moe_route_scored): in one launch
+// (cooperative unless one CTA is enough; `table` holds E bytes per CTA, at
+// most one per 16 tokens; `arrive` and `gen` as for launch_route_large), or, beyond
+// score_route_fits, the choice alone, to be followed by launch_route_scan and
+// launch_route_scatter.
 struct ScoreArgs {
   int sigmoid, groups, topk_groups, renorm;
   float scale;
   const float* bias;
 };
-bool score_large_fits(int T, int E, int k, int num_sms);
-cudaError_t launch_score_large(const ScoreArgs& a, const float* logits, int T, int E, int k,
-                               int32_t* topk_idx, float* topk_w, uint8_t* cnt8, int32_t* cnt,
+bool score_route_fits(int T, int num_sms);
+cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                               int32_t* topk_idx, float* topk_w, uint8_t* table, int32_t* cnt,
                                int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
                                int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
-                               DevErr err, cudaStream_t st);
-cudaError_t launch_score_select(const ScoreArgs& a, const float* logits, int T, int E, int k,
-                                int32_t* topk_idx, float* topk_w, int32_t* blk_cnt,
-                                cudaStream_t st);
+                               DevErr err, int num_sms, cudaStream_t st);
+cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                              int32_t* topk_idx, float* topk_w, int32_t* blk_cnt, cudaStream_t st);
 cudaError_t launch_gather_rows(const uint16_t* x, const int32_t* perm, int T, int k, int H,
                                int with_shared, uint16_t* xs, DevErr err, cudaStream_t st);
 // Checks the fp16 operand range of n scales and biases (bf16) of a 4-bit

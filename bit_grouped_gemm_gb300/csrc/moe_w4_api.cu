@@ -743,18 +743,20 @@ moe_status moe_route_scored(moe_plan_t p, const float* logits, int T, const moe_
   own(r->num_tiles, p->L.num_tiles);
   const ScoreArgs a{d->score, d->groups, d->topk_groups, d->renormalise, d->scale, d->bias};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (score_large_fits(T, E, k, p->num_sms)) {
+  if (score_route_fits(T, p->num_sms)) {
+    // (the CTAs' byte table, a row per 16 tokens at most, fits the blocks' counts)
     unsigned* w = p->at<unsigned>(p->L.arrive);
     return st_of(timed(p, 8, st, [&] {
-      return launch_score_large(a, logits, T, E, k, r->topk_idx, r->topk_w,
-                                p->at<uint8_t>(p->L.cnt8), r->counts, r->offsets, r->tile_offsets,
-                                r->block_map, r->num_tiles, r->perm, r->inv, w, w + 1, p->err(), st);
+      return launch_score_route(a, logits, T, E, k, r->topk_idx, r->topk_w,
+                                p->at<uint8_t>(p->L.blk_cnt), r->counts, r->offsets,
+                                r->tile_offsets, r->block_map, r->num_tiles, r->perm, r->inv, w,
+                                w + 1, p->err(), p->num_sms, st);
     }));
   }
   const int nblk = (T + kRouterTB - 1) / kRouterTB;
   int32_t* blk = p->at<int32_t>(p->L.blk_cnt);
   cudaError_t e = timed(p, 8, st, [&] {
-    return launch_score_select(a, logits, T, E, k, r->topk_idx, r->topk_w, blk, st);
+    return launch_score_topk(a, logits, T, E, k, r->topk_idx, r->topk_w, blk, st);
   });
   if (e == cudaSuccess)
     e = timed(p, 1, st, [&] {

@@ -13,7 +13,6 @@
 #include <mutex>
 
 #include "moe_common.cuh"
-#include "score_topk.cuh"
 #include "topk.cuh"
 
 namespace moe {
@@ -217,25 +216,6 @@ __global__ void __launch_bounds__(256) router_logits_kernel(
   }
 }
 
-// How a warp picks a token's experts: by softmax of the logits (moe_route),
-// or by scores, bias and groups (moe_route_scored).
-struct SoftmaxPick {
-  template <int VPL>
-  __device__ __forceinline__ void pick(const float* row, int E, int k, int& idx, float& w) const {
-    topk_warp<VPL>(row, E, k, idx, w);
-  }
-};
-struct ScorePick {
-  ScoreDev s;
-  template <int VPL>
-  __device__ __forceinline__ void pick(const float* row, int E, int k, int& idx, float& w) const {
-    score_select<VPL>(row, E, k, s, idx, w);
-  }
-};
-static ScorePick score_pick(const ScoreArgs& a) {
-  return ScorePick{ScoreDev{a.sigmoid, a.groups, a.topk_groups, a.renorm, a.scale, a.bias}};
-}
-
 // ---------------------------------------------------------------------------
 // Top-k + per-block histogram. One CTA = 32 tokens, one warp per token.
 // Each of the k rounds takes the largest not-yet-selected logit (a lower
@@ -247,9 +227,9 @@ static ScorePick score_pick(const ScoreArgs& a) {
 // logits (equal to softmax over all E renormalised over the k). The block
 // writes its per-expert counts to blk_cnt[block][E].
 // ---------------------------------------------------------------------------
-template <int VPL, class Sel>
+template <int VPL>
 __global__ void __launch_bounds__(1024) router_topk_kernel(
-    const Sel sel, const float* __restrict__ logits, int T, int E, int k, int32_t* __restrict__ topk_idx,
+    const float* __restrict__ logits, int T, int E, int k, int32_t* __restrict__ topk_idx,
     float* __restrict__ topk_w, int32_t* __restrict__ blk_cnt) {
   pdl_begin();
   __shared__ int cnt_s[1024];
@@ -261,7 +241,7 @@ __global__ void __launch_bounds__(1024) router_topk_kernel(
     const int t = t0 + warp;
     int idx;
     float w;
-    sel.template pick<VPL>(logits + (size_t)t * E, E, k, idx, w);
+    topk_warp<VPL>(logits + (size_t)t * E, E, k, idx, w);
     if (lane < k) {
       topk_idx[(size_t)t * k + lane] = idx;
       topk_w[(size_t)t * k + lane] = w;
@@ -588,27 +568,14 @@ cudaError_t launch_router_logits(const uint16_t* x, int T, int H, const uint16_t
   return launch_pdl(router_logits_kernel, grid, dim3(256), smem, st, x, T, H, wr, bias, E, logits);
 }
 
-template <class Sel>
-static cudaError_t router_select(const Sel& sel, const float* logits, int T, int E, int k,
-                                 int32_t* topk_idx, float* topk_w, int32_t* blk_cnt,
-                                 cudaStream_t st) {
-  const int nblk = (T + kRouterTB - 1) / kRouterTB;
-  if (E <= 256)
-    return launch_pdl(router_topk_kernel<8, Sel>, dim3(nblk), dim3(32 * kRouterTB), 0, st, sel,
-                      logits, T, E, k, topk_idx, topk_w, blk_cnt);
-  return launch_pdl(router_topk_kernel<16, Sel>, dim3(nblk), dim3(32 * kRouterTB), 0, st, sel,
-                    logits, T, E, k, topk_idx, topk_w, blk_cnt);
-}
-
 cudaError_t launch_router_select(const float* logits, int T, int E, int k, int32_t* topk_idx,
                                  float* topk_w, int32_t* blk_cnt, cudaStream_t st) {
-  return router_select(SoftmaxPick{}, logits, T, E, k, topk_idx, topk_w, blk_cnt, st);
-}
-
-cudaError_t launch_score_select(const ScoreArgs& a, const float* logits, int T, int E, int k,
-                                int32_t* topk_idx, float* topk_w, int32_t* blk_cnt,
-                                cudaStream_t st) {
-  return router_select(score_pick(a), logits, T, E, k, topk_idx, topk_w, blk_cnt, st);
+  const int nblk = (T + kRouterTB - 1) / kRouterTB;
+  if (E <= 256)
+    return launch_pdl(router_topk_kernel<8>, dim3(nblk), dim3(32 * kRouterTB), 0, st, logits, T, E,
+                      k, topk_idx, topk_w, blk_cnt);
+  return launch_pdl(router_topk_kernel<16>, dim3(nblk), dim3(32 * kRouterTB), 0, st, logits, T, E,
+                    k, topk_idx, topk_w, blk_cnt);
 }
 
 cudaError_t launch_router_topk(const uint16_t* x, int T, int H, const uint16_t* wr,
@@ -919,9 +886,9 @@ __host__ __device__ inline int rl_tpe(int E) {
   return tpe;
 }
 
-template <int VPL, class Sel>
+template <int VPL>
 __global__ void __launch_bounds__(kRlThreads) route_large_kernel(
-    const Sel sel, const float* __restrict__ logits, int T, int E, int k, int32_t* __restrict__ topk_idx,
+    const float* __restrict__ logits, int T, int E, int k, int32_t* __restrict__ topk_idx,
     float* __restrict__ topk_w, uint8_t* cnt8, int np, int32_t* __restrict__ cnt,
     int32_t* __restrict__ off, int32_t* __restrict__ tile_off, int32_t* __restrict__ bmap,
     int32_t* __restrict__ num_tiles, int32_t* __restrict__ perm, int32_t* __restrict__ inv,
@@ -951,7 +918,7 @@ __global__ void __launch_bounds__(kRlThreads) route_large_kernel(
     const int t = t0 + warp;
     int idx;
     float w;
-    sel.template pick<VPL>(logits + (size_t)t * E, E, k, idx, w);
+    topk_warp<VPL>(logits + (size_t)t * E, E, k, idx, w);
     if (lane < k) {
       topk_idx[(size_t)t * k + lane] = idx;
       topk_w[(size_t)t * k + lane] = w;
@@ -1125,8 +1092,7 @@ size_t route_large_cnt8_bytes(int nblk, int E) {
 }
 
 // Blocks the cooperative launch needs resident at once, and whether they fit.
-template <class Sel>
-static bool large_fits(int T, int E, int k, int num_sms) {
+bool route_large_fits(int T, int E, int k, int num_sms) {
   if (E > 512 || k > 32 || T < 1) return false;
   const int nblk = (T + kRouterTB - 1) / kRouterTB;
   const int tpe = rl_tpe(E);
@@ -1138,21 +1104,13 @@ static bool large_fits(int T, int E, int k, int num_sms) {
   auto occ = [&](auto kern) {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRlThreads, 0);
   };
-  const cudaError_t e = E <= 256 ? occ(route_large_kernel<8, Sel>) : occ(route_large_kernel<16, Sel>);
+  const cudaError_t e = E <= 256 ? occ(route_large_kernel<8>) : occ(route_large_kernel<16>);
   return e == cudaSuccess && nblk <= per_sm * num_sms;
 }
 
-bool route_large_fits(int T, int E, int k, int num_sms) {
-  return large_fits<SoftmaxPick>(T, E, k, num_sms);
-}
-bool score_large_fits(int T, int E, int k, int num_sms) {
-  return large_fits<ScorePick>(T, E, k, num_sms);
-}
-
-template <class Sel>
-static cudaError_t route_large(const Sel& sel, const float* logits, int T, int E, int k,
-                               int32_t* topk_idx, float* topk_w, uint8_t* cnt8, int32_t* cnt,
-                               int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
+cudaError_t launch_route_large(const float* logits, int T, int E, int k, int32_t* topk_idx,
+                               float* topk_w, uint8_t* cnt8, int32_t* cnt, int32_t* off,
+                               int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
                                int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
                                DevErr err, const uint16_t* x, uint16_t* xs, int H,
                                int with_shared, cudaStream_t st) {
@@ -1170,31 +1128,13 @@ static cudaError_t route_large(const Sel& sel, const float* logits, int T, int E
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto kern) {
-    return cudaLaunchKernelEx(&cfg, kern, sel, logits, T, E, k, topk_idx, topk_w, cnt8, np, cnt,
-                              off, tile_off, bmap, num_tiles, perm, inv, arrive, gen, err, x, xs,
-                              H, with_shared);
-  };
-  return E <= 256 ? go(route_large_kernel<8, Sel>) : go(route_large_kernel<16, Sel>);
-}
-
-cudaError_t launch_route_large(const float* logits, int T, int E, int k, int32_t* topk_idx,
-                               float* topk_w, uint8_t* cnt8, int32_t* cnt, int32_t* off,
-                               int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
-                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
-                               DevErr err, const uint16_t* x, uint16_t* xs, int H,
-                               int with_shared, cudaStream_t st) {
-  return route_large(SoftmaxPick{}, logits, T, E, k, topk_idx, topk_w, cnt8, cnt, off, tile_off,
-                     bmap, num_tiles, perm, inv, arrive, gen, err, x, xs, H, with_shared, st);
-}
-
-cudaError_t launch_score_large(const ScoreArgs& a, const float* logits, int T, int E, int k,
-                               int32_t* topk_idx, float* topk_w, uint8_t* cnt8, int32_t* cnt,
-                               int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
-                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
-                               DevErr err, cudaStream_t st) {
-  return route_large(score_pick(a), logits, T, E, k, topk_idx, topk_w, cnt8, cnt, off, tile_off,
-                     bmap, num_tiles, perm, inv, arrive, gen, err, nullptr, nullptr, 0, 0, st);
+  if (E <= 256)
+    return cudaLaunchKernelEx(&cfg, route_large_kernel<8>, logits, T, E, k, topk_idx, topk_w, cnt8,
+                              np, cnt, off, tile_off, bmap, num_tiles, perm, inv, arrive, gen, err,
+                              x, xs, H, with_shared);
+  return cudaLaunchKernelEx(&cfg, route_large_kernel<16>, logits, T, E, k, topk_idx, topk_w, cnt8,
+                            np, cnt, off, tile_off, bmap, num_tiles, perm, inv, arrive, gen, err,
+                            x, xs, H, with_shared);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,301 @@
+// route_scored.cu -- routing by scores (moe_route_scored): each token's choice
+// (score_topk.cuh), then counts, offsets, tile offsets, the stable scatter and
+// the block map, as moe_route makes them.
+//
+// One launch: CTA b takes tokens [b C, (b + 1) C), a warp a token at a time,
+// and keeps its choices and, per expert, a bit for each of its tokens in
+// shared memory. Its counts go to a byte table [CTA][expert]; after a grid
+// barrier every CTA reads the whole table, which gives it all totals and its
+// own starting positions, and writes its slots: position = start + earlier
+// tokens of the CTA that chose the expert (a popcount of the bits below). The
+// block map is dealt over the CTAs by expert.
+#include "score_topk.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kScThreads = 1024;
+constexpr int kScMaxC = 224;          // tokens per CTA: counts fit a byte
+constexpr int kScWords = kScMaxC / 32;
+
+struct ScParams {
+  ScoreDev s;
+  const float* logits;
+  int T, E, k, C;
+  int32_t *idx;
+  float* w;
+  uint8_t* table;                     // [CTAs][E]
+  int32_t *cnt, *off, *tile_off, *bmap, *num_tiles, *perm, *inv;
+  unsigned *arrive, *gen;
+  DevErr err;
+};
+
+__device__ __forceinline__ unsigned ld_relaxed(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Grid barrier of a cooperative launch: the last CTA to arrive resets the
+// counter and advances the generation; bounded.
+__device__ __forceinline__ bool grid_barrier(unsigned* arrive, unsigned* gen, const DevErr& err,
+                                             int site) {
+  __shared__ int go;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const unsigned g0 = ld_relaxed(gen);   // moves only after every arrival
+    int ok = 1;
+    if (atomicAdd(arrive, 1u) == gridDim.x - 1) {
+      *arrive = 0u;
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(gen), "r"(g0 + 1u) : "memory");
+    } else {
+      const unsigned long long start = globaltimer_ns();
+      while (ld_relaxed(gen) == g0) {
+        __nanosleep(40);
+        if (globaltimer_ns() - start > err.limit_ns) {
+          report_timeout(err, site);
+          ok = 0;
+          break;
+        }
+      }
+    }
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    go = ok;
+  }
+  __syncthreads();
+  return go != 0;
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams p) {
+  constexpr int kE = 32 * VPL;
+  extern __shared__ float dyn[];           // [32 warps][kE], later the partial sums
+  __shared__ unsigned mask_s[kScWords * kE];   // [word][expert]
+  __shared__ int start_s[kE];
+  __shared__ int wrows_s[16], wtiles_s[16];
+  pdl_begin();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = p.E, k = p.k, b = blockIdx.x, G = gridDim.x;
+  const int t0 = b * p.C, nt = min(p.C, p.T - t0);
+  const int words = (p.C + 31) / 32;
+  for (int i = tid; i < words * kE; i += kScThreads) mask_s[i] = 0u;
+  __syncthreads();
+
+  for (int tl = warp; tl < nt; tl += kScThreads / 32) {
+    const size_t t = t0 + tl;
+    int idx;
+    float w;
+    score_select<VPL>(p.logits + t * E, E, k, p.s, dyn + warp * kE, idx, w);
+    if (lane < k) {
+      p.idx[t * k + lane] = idx;
+      p.w[t * k + lane] = w;
+      atomicOr(&mask_s[(tl >> 5) * kE + idx], 1u << (tl & 31));
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  int tot = 0, before = 0;                 // thread e < E: all CTAs', earlier CTAs'
+  if (tid < E)
+    for (int i = 0; i < words; ++i) tot += __popc(mask_s[i * kE + tid]);
+  if (G > 1) {
+    if (tid < E) p.table[(size_t)b * E + tid] = (uint8_t)tot;
+    if (!grid_barrier(p.arrive, p.gen, p.err, 60)) return;
+    // the table, 4 experts per thread, the rows dealt over the rest of the
+    // threads: totals in the low halves, earlier CTAs' in the high halves
+    uint32_t* part = reinterpret_cast<uint32_t*>(dyn);   // [rows' share][E]
+    const int e4 = E / 4, shares = min(kScThreads / e4, 32), q = tid / e4, c = tid % e4;
+    if (q < shares) {
+      uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll 8
+      for (int r = q; r < G; r += shares) {
+        const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(p.table + (size_t)r * E) + c);
+        const uint32_t f = r < b ? 0x10001u : 1u;
+        s0 += (v & 0xFFu) * f;
+        s1 += ((v >> 8) & 0xFFu) * f;
+        s2 += ((v >> 16) & 0xFFu) * f;
+        s3 += (v >> 24) * f;
+      }
+      uint32_t* o = part + q * E + 4 * c;
+      o[0] = s0;
+      o[1] = s1;
+      o[2] = s2;
+      o[3] = s3;
+    }
+    __syncthreads();
+    if (tid < E) {
+      tot = 0;
+      for (int i = 0; i < shares; ++i) {
+        const uint32_t v = part[i * E + tid];
+        tot += v & 0xFFFFu;
+        before += v >> 16;
+      }
+    }
+  }
+  // exclusive scans over the experts: rows and tiles
+  const int tiles = (tot + kBM - 1) / kBM;
+  int ri = tot, ti = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int rn = __shfl_up_sync(0xffffffffu, ri, o), tn = __shfl_up_sync(0xffffffffu, ti, o);
+    if (lane >= o) {
+      ri += rn;
+      ti += tn;
+    }
+  }
+  if (lane == 31 && warp < 16) {
+    wrows_s[warp] = ri;
+    wtiles_s[warp] = ti;
+  }
+  __syncthreads();
+  if (tid < E) {
+    int ro = ri - tot, to = ti - tiles;
+#pragma unroll
+    for (int w2 = 0; w2 < 16; ++w2)
+      if (w2 < warp) {
+        ro += wrows_s[w2];
+        to += wtiles_s[w2];
+      }
+    start_s[tid] = ro + before;
+    if (tid % G == b) {
+      p.cnt[tid] = tot;
+      p.off[tid] = ro;
+      p.tile_off[tid] = to;
+      for (int i = 0; i < tiles; ++i) {
+        int32_t* m = p.bmap + 3 * (size_t)(to + i);
+        m[0] = tid;
+        m[1] = ro + kBM * i;
+        m[2] = min(kBM, tot - kBM * i);
+      }
+    }
+    if (b == 0 && tid == E - 1) {
+      p.off[E] = ro + tot;
+      p.tile_off[E] = to + tiles;
+      p.num_tiles[0] = to + tiles;
+    }
+  }
+  __syncthreads();
+  // the CTA's slots, in token order within each expert
+  for (int i = tid; i < nt * k; i += kScThreads) {
+    const int tl = i / k, slot = t0 * k + i;
+    const int e = __ldcg(p.idx + slot);    // this CTA's own store
+    int pos = start_s[e] + __popc(mask_s[(tl >> 5) * kE + e] & ((1u << (tl & 31)) - 1u));
+    for (int wd = 0; wd < (tl >> 5); ++wd) pos += __popc(mask_s[wd * kE + e]);
+    p.perm[pos] = slot;
+    p.inv[slot] = pos;
+  }
+}
+
+// The choice alone, 32 tokens per CTA, with the block's counts as
+// launch_route_scan takes them (batches beyond score_route_kernel's).
+template <int VPL>
+__global__ void __launch_bounds__(kScThreads) score_topk_kernel(const ScoreDev s, const float* logits,
+                                                                int T, int E, int k, int32_t* topk_idx,
+                                                                float* topk_w, int32_t* blk_cnt) {
+  constexpr int kE = 32 * VPL;
+  extern __shared__ float dyn[];
+  __shared__ int cnt_s[kE];
+  pdl_begin();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.x * kRouterTB + warp;
+  for (int i = tid; i < E; i += kScThreads) cnt_s[i] = 0;
+  __syncthreads();
+  if (t < T) {
+    int idx;
+    float w;
+    score_select<VPL>(logits + (size_t)t * E, E, k, s, dyn + warp * kE, idx, w);
+    if (lane < k) {
+      topk_idx[(size_t)t * k + lane] = idx;
+      topk_w[(size_t)t * k + lane] = w;
+      atomicAdd(&cnt_s[idx], 1);
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kScThreads) blk_cnt[(size_t)blockIdx.x * E + e] = cnt_s[e];
+}
+
+ScoreDev dev_of(const ScoreArgs& a) {
+  return ScoreDev{a.sigmoid, a.groups, a.topk_groups, a.renorm, a.scale, a.bias};
+}
+
+// dynamic shared memory: a row per warp; the partial sums take at most as much
+constexpr int dyn_bytes(int vpl) { return 32 * 32 * vpl * 4; }
+
+}  // namespace
+
+// Tokens per CTA and CTAs of the one-launch form. One CTA up to 32 tokens (a
+// token per warp, no grid barrier); then 16 tokens a CTA until every SM has
+// one.
+static void score_grid(int T, int num_sms, int* C, int* G) {
+  int g = T <= 32 ? 1 : (T + 15) / 16;
+  if (g > num_sms) g = num_sms;
+  *C = (T + g - 1) / g;
+  *G = (T + *C - 1) / *C;
+}
+
+bool score_route_fits(int T, int num_sms) {
+  int C, G;
+  score_grid(T, num_sms, &C, &G);
+  return C <= kScMaxC;
+}
+
+cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                               int32_t* topk_idx, float* topk_w, uint8_t* table, int32_t* cnt,
+                               int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
+                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
+                               DevErr err, int num_sms, cudaStream_t st) {
+  ScParams p;
+  int G;
+  score_grid(T, num_sms, &p.C, &G);
+  if (p.C > kScMaxC || E > 512 || k > 32) return cudaErrorInvalidValue;
+  p.s = dev_of(a);
+  p.logits = logits;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.idx = topk_idx;
+  p.w = topk_w;
+  p.table = table;
+  p.cnt = cnt;
+  p.off = off;
+  p.tile_off = tile_off;
+  p.bmap = bmap;
+  p.num_tiles = num_tiles;
+  p.perm = perm;
+  p.inv = inv;
+  p.arrive = arrive;
+  p.gen = gen;
+  p.err = err;
+  auto go = [&](auto kern, int smem) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (G == 1) return launch_pdl(kern, dim3(1), dim3(kScThreads), smem, st, p);
+    // cooperative (the CTAs wait on the last one), in ordinary stream order
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G);
+    cfg.blockDim = dim3(kScThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+  };
+  return E <= 256 ? go(score_route_kernel<8>, dyn_bytes(8)) : go(score_route_kernel<16>, dyn_bytes(16));
+}
+
+cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, int E, int k,
+                              int32_t* topk_idx, float* topk_w, int32_t* blk_cnt, cudaStream_t st) {
+  const int nblk = (T + kRouterTB - 1) / kRouterTB;
+  auto go = [&](auto kern, int smem) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(nblk), dim3(kScThreads), smem, st, dev_of(a), logits, T, E, k,
+                      topk_idx, topk_w, blk_cnt);
+  };
+  return E <= 256 ? go(score_topk_kernel<8>, dyn_bytes(8)) : go(score_topk_kernel<16>, dyn_bytes(16));
+}
+
+}  // namespace moe
