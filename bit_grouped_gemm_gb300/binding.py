@@ -160,10 +160,16 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """Handle of torch's current stream (the raw query: building a Stream
+    object for it takes 3 us a call)."""
+    from torch import _C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+
+
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
     const size_t t = t0 + tl;
     int idx;
     float w;
-    score_select<VPL>(p.logits + t * E, E, k, p.s, dyn + warp * kE, idx, w);
+    score_select<VPL>(p.logits + t * E, E, k, p.s, dyn + warp * max(kE, 64), idx, w);
     if (lane < k) {
       p.idx[t * k + lane] = idx;
       p.w[t * k + lane] = w;
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kScThreads) score_topk_kernel(const ScoreDev s
   if (t < T) {
     int idx;
     float w;
-    score_select<VPL>(logits + (size_t)t * E, E, k, s, dyn + warp * kE, idx, w);
+    score_select<VPL>(logits + (size_t)t * E, E, k, s, dyn + warp * max(kE, 64), idx, w);
     if (lane < k) {
       topk_idx[(size_t)t * k + lane] = idx;
       topk_w[(size_t)t * k + lane] = w;
@@ -219,7 +219,7 @@ ScoreDev dev_of(const ScoreArgs& a) {
 }
 
 // dynamic shared memory: a row per warp; the partial sums take at most as much
-constexpr int dyn_bytes(int vpl) { return 32 * 32 * vpl * 4; }
+constexpr int dyn_bytes(int vpl) { return 32 * 32 * (vpl < 4 ? 4 : vpl) * 4; }
 
 }  // namespace
 
@@ -283,7 +283,10 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
-  return E <= 256 ? go(score_route_kernel<8>, dyn_bytes(8)) : go(score_route_kernel<16>, dyn_bytes(16));
+  return E <= 64    ? go(score_route_kernel<2>, dyn_bytes(2))
+         : E <= 128 ? go(score_route_kernel<4>, dyn_bytes(4))
+         : E <= 256 ? go(score_route_kernel<8>, dyn_bytes(8))
+                    : go(score_route_kernel<16>, dyn_bytes(16));
 }
 
 cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, int E, int k,
@@ -295,7 +298,10 @@ cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, in
     return launch_pdl(kern, dim3(nblk), dim3(kScThreads), smem, st, dev_of(a), logits, T, E, k,
                       topk_idx, topk_w, blk_cnt);
   };
-  return E <= 256 ? go(score_topk_kernel<8>, dyn_bytes(8)) : go(score_topk_kernel<16>, dyn_bytes(16));
+  return E <= 64    ? go(score_topk_kernel<2>, dyn_bytes(2))
+         : E <= 128 ? go(score_topk_kernel<4>, dyn_bytes(4))
+         : E <= 256 ? go(score_topk_kernel<8>, dyn_bytes(8))
+                    : go(score_topk_kernel<16>, dyn_bytes(16));
 }
 
 }  // namespace moe

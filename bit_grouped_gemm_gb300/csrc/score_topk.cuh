@@ -14,9 +14,11 @@
 // among the first k (one per lane), or of all where the groups are in doubt.
 // Without a bias and groups the order is that of the logits, which is exact.
 //
-// Lane l holds experts VPL l .. VPL l + VPL - 1: its logits are two or four
-// 16-byte loads, and of equal keys in several lanes the lowest lane's comes
-// first.
+// Lane l holds experts VPL l .. VPL l + VPL - 1. The choice itself takes no
+// rounds: the (k + 1)-th largest of the lanes' largest keys bounds the
+// (k + 1)-th largest key from below, so the few keys at or above it are put
+// into a list, in index order, one per lane, and each lane counts how many of
+// the list come before its own.
 #pragma once
 
 #include "topk.cuh"
@@ -79,26 +81,37 @@ __device__ __forceinline__ double prob64(const ScoreDev& s, float l, double m, d
   return z > 0.0 ? exp((double)l - m) / z : 0.0;
 }
 
-// Lane j's expert of the choice, from 64-bit scores of every expert.
+// Lane j's expert of the choice, from 64-bit scores of every expert, each
+// taken once.
+template <int VPL>
 __device__ __noinline__ int score_exact_all(const float* row, int E, int k, const ScoreDev s) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, gsz = E / s.groups;
   double m = 0.0, z = 1.0;
   if (!s.sigmoid) softmax64(row, E, m, z);
-  auto score = [&](int e) {
-    double c = prob64(s, clean_logit(__ldcg(row + e)), m, z);
-    if (s.bias) c += (double)score_bias(s, e);
-    return order_key64(c + 0.0);
-  };
+  unsigned long long key[VPL];
+#pragma unroll 1
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0ull;
+    if (e < E) {
+      double c = prob64(s, clean_logit(__ldcg(row + e)), m, z);
+      if (s.bias) c += (double)score_bias(s, e);
+      key[i] = order_key64(c + 0.0);
+    }
+  }
   unsigned keep = 0xffffffffu;
-  const int gsz = E / s.groups;
   if (s.groups > 1) {
     double mine = 0.0;   // lane g < groups: group g's score
     for (int g = 0; g < s.groups; ++g) {
       unsigned long long k1 = 0ull, k2 = 0ull;   // the lane's two largest
-      for (int i = lane; i < gsz; i += 32) {
-        const unsigned long long v = score(g * gsz + i);
-        k2 = v > k1 ? k1 : v > k2 ? v : k2;
-        k1 = v > k1 ? v : k1;
+#pragma unroll 1
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= g * gsz && e < (g + 1) * gsz) {
+          const unsigned long long v = key[i];
+          k2 = v > k1 ? k1 : v > k2 ? v : k2;
+          k1 = v > k1 ? v : k1;
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -117,55 +130,80 @@ __device__ __noinline__ int score_exact_all(const float* row, int E, int k, cons
     }
     keep = __ballot_sync(0xffffffffu, lane < s.groups && rank < s.topk_groups);
   }
-  // k rounds, each the largest key below the last one taken (equal keys: the
-  // next higher index)
-  unsigned long long last = ~0ull;
-  int last_e = -1, mine = 0;
+#pragma unroll 1
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    if (e >= E) continue;
+    if (!((keep >> (e / gsz)) & 1u)) key[i] = 0ull;
+    // without a bias the experts rank by their logits
+    else if (!s.bias) key[i] = order_key(clean_logit(__ldcg(row + e)));
+  }
+  int mine = 0;
   for (int j = 0; j < k; ++j) {
     unsigned long long bk = 0ull;
     int bi = 0x7fffffff;
-    for (int e = lane; e < E; e += 32) {
-      if (!((keep >> (e / gsz)) & 1u)) continue;
-      // without a bias the experts rank by their logits
-      const unsigned long long v = s.bias ? score(e) : (unsigned long long)order_key(clean_logit(__ldcg(row + e)));
-      if ((v < last || (v == last && e > last_e)) && v > bk) {
-        bk = v;
-        bi = e;
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i)
+      if (key[i] > bk) {
+        bk = key[i];
+        bi = lane + 32 * i;
       }
-    }
     warp_best64(bk, bi);
-    last = bk;
-    last_e = bi;
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i)
+      if (bi == lane + 32 * i) key[i] = 0ull;
     if (lane == j) mine = bi;
   }
   return mine;
 }
 
-// The same where only the order of the experts with an FP32 score of at least
-// `thr` is in doubt, `cand` of which (bits by the lane's VPL experts) are
-// eligible: at most one 64-bit score a lane. `list`: 32 ints of the warp's
-// shared memory.
-__device__ __noinline__ int score_exact_some(const float* row, int E, int k, const ScoreDev s,
-                                             unsigned cand, int e0, int* list) {
-  const int lane = threadIdx.x & 31;
-  int n = __popc(cand), before = n;
+// The FP32 score of an expert (without its bias) under a row's softmax
+// maximum and sum.
+__device__ __forceinline__ float score_prob(const ScoreDev& s, float l, float m, float z) {
+  if (s.sigmoid) return 1.0f / (1.0f + expf(-l));
+  return isinf(m) ? 0.f : expf(l - m) / z;
+}
+
+// Writes the lane's experts e0 + i, i in the set `cand`, into `list` (32
+// entries of the warp's shared memory) in index order; returns the warp's
+// count, and writes nothing if that is above 32.
+__device__ __forceinline__ int list_candidates(unsigned cand, int e0, int* list) {
+  const int lane = threadIdx.x & 31, n = __popc(cand);
+  int before = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += v;
   }
   const int total = __shfl_sync(0xffffffffu, before, 31);
-  if (total > 32) return score_exact_all(row, E, k, s);
-  before -= n;
-  for (; cand; cand &= cand - 1) list[before++] = e0 + __ffs(cand) - 1;
+  if (total <= 32)
+    for (before -= n; cand; cand &= cand - 1) list[before++] = e0 + __ffs(cand) - 1;
   __syncwarp();
+  return total;
+}
+
+// The same where only the order of the experts with an FP32 score of at least
+// `thr` is in doubt: of the eligible ones (bits `elig` of the lane's experts)
+// at most 32, one 64-bit score a lane.
+template <int VPL>
+__device__ __noinline__ int score_exact_some(const float* row, int E, int k, const ScoreDev s,
+                                             float m32, float z32, unsigned elig, float thr, int* list) {
+  const int lane = threadIdx.x & 31, e0 = VPL * lane;
+  unsigned cand = 0u;
+  for (int i = 0; i < VPL; ++i)
+    if ((elig >> i) & 1u) {
+      const float c = score_prob(s, clean_logit(__ldcg(row + e0 + i)), m32, z32) + score_bias(s, e0 + i);
+      if (!(c < thr)) cand |= 1u << i;
+    }
+  const int total = list_candidates(cand, e0, list);
+  if (total > 32) return score_exact_all<VPL>(row, E, k, s);
   double m = 0.0, z = 1.0;
   if (!s.sigmoid) softmax64(row, E, m, z);
   const int e = lane < total ? list[lane] : 0;
   unsigned long long key = 0ull;
   if (lane < total)
     key = order_key64(prob64(s, clean_logit(__ldcg(row + e)), m, z) + (double)score_bias(s, e) + 0.0);
-  int rank = 0;   // (the list is in index order)
+  int rank = 0;
   for (int j = 0; j < total; ++j) {
     const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
     rank += o > key || (o == key && j < lane);
@@ -176,42 +214,29 @@ __device__ __noinline__ int score_exact_some(const float* row, int E, int k, con
   return lane < k ? list[lane] : 0;
 }
 
-// Sorts a lane's 8 (key, expert) pairs: descending, the lower expert first.
-__device__ __forceinline__ void sort8(uint32_t (&key)[8], int (&ix)[8]) {
-  auto cswap = [&](int a, int b) {
-    const bool sw = key[b] > key[a] || (key[b] == key[a] && ix[b] < ix[a]);
-    const uint32_t ka = key[a], kb = key[b];
-    const int ia = ix[a], ib = ix[b];
-    key[a] = sw ? kb : ka;
-    key[b] = sw ? ka : kb;
-    ix[a] = sw ? ib : ia;
-    ix[b] = sw ? ia : ib;
-  };
-  cswap(0, 2); cswap(1, 3); cswap(4, 6); cswap(5, 7);
-  cswap(0, 4); cswap(1, 5); cswap(2, 6); cswap(3, 7);
-  cswap(0, 1); cswap(2, 3); cswap(4, 5); cswap(6, 7);
-  cswap(2, 4); cswap(3, 5);
-  cswap(1, 4); cswap(3, 6);
-  cswap(1, 2); cswap(3, 4); cswap(5, 6);
-}
-
-// Lane j < k gets the j-th chosen expert and its weight. `sm`: E floats (at
-// least 32) of the warp's own shared memory.
+// Lane j < k gets the j-th chosen expert and its weight. `sm`: max(E, 64)
+// floats of the warp's own shared memory.
 template <int VPL>   // experts per lane, E <= 32 * VPL
 __device__ __forceinline__ void score_select(const float* __restrict__ row, int E, int k,
                                              const ScoreDev& s, float* sm, int& idx, float& w) {
   const int lane = threadIdx.x & 31;
   const int e0 = VPL * lane;
-  const bool live = e0 < E;   // E is a multiple of 8: a lane's 8 are all below E or none
   float l[VPL];
+  if constexpr (VPL == 2) {
+    float2 v = make_float2(-INFINITY, -INFINITY);
+    if (e0 < E) v = __ldcg(reinterpret_cast<const float2*>(row + e0));
+    l[0] = clean_logit(v.x);
+    l[1] = clean_logit(v.y);
+  } else {
 #pragma unroll
-  for (int i = 0; i < VPL; i += 4) {
-    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (e0 + i < E) v = __ldcg(reinterpret_cast<const float4*>(row + e0 + i));
-    l[i] = clean_logit(v.x);
-    l[i + 1] = clean_logit(v.y);
-    l[i + 2] = clean_logit(v.z);
-    l[i + 3] = clean_logit(v.w);
+    for (int i = 0; i < VPL; i += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e0 + i < E) v = __ldcg(reinterpret_cast<const float4*>(row + e0 + i));
+      l[i] = clean_logit(v.x);
+      l[i + 1] = clean_logit(v.y);
+      l[i + 2] = clean_logit(v.z);
+      l[i + 3] = clean_logit(v.w);
+    }
   }
   // softmax: maximum and sum over all experts
   float m = 0.f, z = 1.f;
@@ -228,24 +253,18 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
   }
-  auto prob = [&](float v) {
-    if (s.sigmoid) return 1.0f / (1.0f + expf(-v));
-    return isinf(m) ? 0.f : expf(v - m) / z;
-  };
   // Bound of a pair's FP32 error: expf within 2 ulp, the additions and the
   // division half an ulp each (sigmoid: below 3.6e-7 p); softmax's argument
   // and sum bring that to 2e-6 p. p <= 1, and softmax's largest p is 1 / z.
   // The bias' addition: half an ulp of c.
   const float perr = s.sigmoid ? 1.2e-6f : 6e-6f / z;
   uint32_t key[VPL];   // every real key is above 0
-  int ix[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    ix[i] = e0 + i;
     key[i] = 0u;
-    if (e0 + i < E) key[i] = order_key(s.bias ? prob(l[i]) + score_bias(s, e0 + i) + 0.0f : l[i]);
+    if (e0 + i < E)
+      key[i] = order_key(s.bias ? score_prob(s, l[i], m, z) + score_bias(s, e0 + i) + 0.0f : l[i]);
   }
-  if constexpr (VPL == 8) sort8(key, ix);
   bool unsure_groups = false;
   if (s.groups > 1) {
     const int gsz = E / s.groups;
@@ -255,11 +274,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     float m1 = -INFINITY, m2 = -INFINITY, big = 0.f;
     int span = per;   // lanes that hold one group's parts: group lane / span
     if (whole) {
-      // a lane's two largest; without a bias their p
-      if constexpr (VPL == 8) {
-        m1 = key_value(key[0]);
-        m2 = key_value(key[1]);
-      } else {
+      if (e0 < E) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
           const float v = key_value(key[i]);
@@ -267,7 +282,6 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
           m1 = fmaxf(m1, v);
         }
       }
-      if (!live) m1 = m2 = -INFINITY;
     } else {
       // through shared memory: `span` lanes a group, each every span-th expert
       int g2 = 1;
@@ -275,7 +289,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       span = 32 / g2;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (live && ix[i] < E) sm[ix[i]] = key_value(key[i]);
+        if (e0 + i < E) sm[e0 + i] = key_value(key[i]);
       __syncwarp();
       const int g = lane / span;
       if (g < s.groups)
@@ -295,8 +309,8 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     float sum = -INFINITY;
     if (g < s.groups) {
       if (!s.bias) {
-        m1 = prob(m1);
-        m2 = prob(m2);
+        m1 = score_prob(s, m1, m, z);
+        m2 = score_prob(s, m2, m, z);
       }
       sum = gsz > 1 ? m1 + m2 : m1;
       if (!isinf(m1)) big = fabsf(m1);
@@ -325,114 +339,100 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
         for (int i = 0; i < VPL; ++i) key[i] = 0u;
       }
     } else {
-      if constexpr (VPL == 8) {
-        // the dropped ones leave the sorted list
-        int n = 0;
-        uint32_t k2[8];
-        int i2[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          k2[i] = 0u;
-          i2[i] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (key[i] && ((keep >> (ix[i] / gsz * span)) & 1u)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j == n) {
-                k2[j] = key[i];
-                i2[j] = ix[i];
-              }
-            ++n;
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          key[i] = k2[i];
-          ix[i] = i2[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[i] && !((keep >> (ix[i] / gsz * span)) & 1u)) key[i] = 0u;
-      }
-    }
-  }
-  unsigned eligible = 0u;   // bits by position e0 + i, for the 64-bit path
-  if (s.bias) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i]) eligible |= 1u << (ix[i] - e0);
-  }
-  // k rounds, and one more where the order may be unsure: lane j keeps the
-  // j-th key
-  const int rounds = s.bias ? k + 1 : k;
-  uint32_t my_key = 0u;
-  int mine = 0;
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t top = key[0];
-    int ti = ix[0];
-    if constexpr (VPL > 8) {
-#pragma unroll
-      for (int i = 1; i < VPL; ++i)
-        if (key[i] > top) {
-          top = key[i];
-          ti = ix[i];
-        }
-    }
-    const uint32_t mk = __reduce_max_sync(0xffffffffu, top);
-    const unsigned has = __ballot_sync(0xffffffffu, top == mk);
-    const int src = __ffs(has) - 1;   // the lowest lane holds the lowest expert
-    const int be = __shfl_sync(0xffffffffu, ti, src);
-    if (lane == src) {
-      if constexpr (VPL == 8) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i) {
-          key[i] = key[i + 1];
-          ix[i] = ix[i + 1];
-        }
-        key[7] = 0u;
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (ix[i] == be) key[i] = 0u;
-      }
-    }
-    if (lane == (j & 31)) {
-      // (round 32 of k = 32 looks at the next key only, and lane 0 has it)
-      if (j < 32) {
-        my_key = mk;
-        mine = be;
-      }
-    }
-    if (j == 32 && lane == 31) sm[0] = key_value(mk), sm[1] = mk ? 1.f : 0.f;
-  }
-  if (s.bias) {
-    // neighbours in the order: lane j against j + 1 <= k
-    uint32_t nk = __shfl_down_sync(0xffffffffu, my_key, 1);
-    if (k == 32) {
-      __syncwarp();
-      if (lane == 31) nk = sm[1] != 0.f ? order_key(sm[0]) : 0u;
-      __syncwarp();
-    }
-    const float a = key_value(my_key), b = key_value(nk);
-    // (equal infinities are certain: closed experts, by index)
-    const bool close = lane < k && nk != 0u && !(isinf(a) && a == b) &&
-                       !(a - b > perr + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)));
-    if (unsure_groups) {
-      mine = score_exact_all(row, E, k, s);
-    } else if (__any_sync(0xffffffffu, close)) {
-      const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
-      const float thr = vk - 2.f * (perr + 2.5e-7f * fabsf(vk));
-      unsigned cand = 0u;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if ((eligible >> i) & 1u)
-          if (!(prob(l[i]) + score_bias(s, e0 + i) < thr)) cand |= 1u << i;
-      mine = score_exact_some(row, E, k, s, cand, e0, reinterpret_cast<int*>(sm));
+        if (key[i] && !((keep >> ((e0 + i) / gsz * span)) & 1u)) key[i] = 0u;
     }
-  } else if (unsure_groups) {
-    mine = score_exact_all(row, E, k, s);
+  }
+  int mine = 0;
+  if (unsure_groups) {
+    mine = score_exact_all<VPL>(row, E, k, s);
+  } else {
+    // `need` keys in order: the k chosen, and with a bias the next one
+    const int need = s.bias ? k + 1 : k;
+    uint32_t top = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = max(top, key[i]);
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t o = __shfl_sync(0xffffffffu, top, j);
+      rank += o > top || (o == top && j < lane);
+    }
+    const unsigned at = __ballot_sync(0xffffffffu, rank == need - 1);   // 0 if need is 33
+    const uint32_t floor_key = at ? max(__shfl_sync(0xffffffffu, top, __ffs(at) - 1), 1u) : 1u;
+    unsigned cand = 0u, elig = 0u;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (key[i]) elig |= 1u << i;
+      if (key[i] >= floor_key) cand |= 1u << i;
+    }
+    int* list = reinterpret_cast<int*>(sm);
+    uint32_t* lkey = reinterpret_cast<uint32_t*>(sm) + 32;
+    const int total = list_candidates(cand, e0, list);
+    uint32_t my_key = 0u, next_key = 0u;
+    if (total <= 32) {
+      // the list's order: rank by key, then by place
+      const int e = lane < total ? list[lane] : 0;
+      uint32_t ck = 0u;
+      if (lane < total) {
+        const float v = clean_logit(__ldcg(row + e));
+        ck = order_key(s.bias ? score_prob(s, v, m, z) + score_bias(s, e) + 0.0f : v);
+      }
+      int r = 0;
+      for (int j = 0; j < total; ++j) {
+        const uint32_t o = __shfl_sync(0xffffffffu, ck, j);
+        r += o > ck || (o == ck && j < lane);
+      }
+      __syncwarp();
+      if (lane < total) {
+        list[r] = e;
+        lkey[r] = ck;
+      }
+      __syncwarp();
+      if (lane < total) {
+        mine = list[lane];
+        my_key = lkey[lane];
+      }
+      __syncwarp();
+      next_key = __shfl_down_sync(0xffffffffu, my_key, 1);
+      if (lane == 31) next_key = 0u;
+    } else {
+      // more (many equal keys, few lanes, or k near 32): one round per key,
+      // the lowest lane that holds the largest first
+      for (int j = 0; j < need; ++j) {
+        uint32_t hk = key[0];
+        int hi = 0;
+#pragma unroll
+        for (int i = 1; i < VPL; ++i)
+          if (key[i] > hk) {
+            hk = key[i];
+            hi = i;
+          }
+        const uint32_t mk = __reduce_max_sync(0xffffffffu, hk);
+        const int src = __ffs(__ballot_sync(0xffffffffu, hk == mk)) - 1;
+        const int be = __shfl_sync(0xffffffffu, e0 + hi, src);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (lane == src && i == hi) key[i] = 0u;
+        if (lane == j) {
+          mine = be;
+          my_key = mk;
+        }
+        if (lane == j - 1) next_key = mk;
+      }
+    }
+    if (s.bias) {
+      // neighbours in the order: equal infinities are certain (closed
+      // experts, by index)
+      const float a = key_value(my_key), b = key_value(next_key);
+      const bool close = lane < k && next_key != 0u && !(isinf(a) && a == b) &&
+                         !(a - b > perr + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)));
+      if (__any_sync(0xffffffffu, close)) {
+        const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
+        mine = score_exact_some<VPL>(row, E, k, s, m, z, elig, vk - 2.f * (perr + 2.5e-7f * fabsf(vk)), list);
+      }
+    }
   }
   // the chosen experts' weights, lane j the j-th
   float lj = -INFINITY;
@@ -456,7 +456,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     pj = sum > 0.f ? pj / sum : 0.f;
   } else if (open) {
-    pj = prob(lj);
+    pj = score_prob(s, lj, m, z);
   }
   idx = mine;
   w = pj * s.scale;
