@@ -9,10 +9,10 @@
 // The choice has to be that of 64-bit scores, but nearly every token's order
 // is already certain in 32 bits: the warp works in FP32 with a bound on the
 // scores' error and looks whether two neighbours in the order (or the last
-// group kept and the first dropped) lie closer than twice that bound. Only
-// then does it take scores again in 64 bits: those of the experts that may be
-// among the first k (one per lane), or of all where the groups are in doubt.
-// Without a bias and groups the order is that of the logits, which is exact.
+// group kept and the first dropped) lie closer than that allows. Only then does
+// it look again, in pairs of floats, and in 64 bits where these cannot tell
+// either. Without a bias and groups the order is that of the logits, which is
+// exact.
 //
 // Lane l holds experts VPL l .. VPL l + VPL - 1. The choice itself takes no
 // rounds: the (k + 1)-th largest of the lanes' largest keys bounds the
@@ -182,36 +182,205 @@ __device__ __forceinline__ int list_candidates(unsigned cand, int e0, int* list)
   return total;
 }
 
-// The same where only the order of the experts with an FP32 score of at least
-// `thr` is in doubt: of the eligible ones (bits `elig` of the lane's experts)
-// at most 32, one 64-bit score a lane.
+// ---------------------------------------------------------------------------
+// Scores between FP32 and FP64. A warp's FP64 exponential takes about a
+// microsecond here, so the second look is taken in pairs of floats (a value
+// and what its rounding left), good to 1e-11, and only what 2e-10 cannot tell
+// goes to FP64. One score per lane, of the experts in doubt alone: a look at
+// every expert of the row took 8 us unrolled (its code is cold on the SM) and
+// 11 us in loops (each score is one long chain).
+// ---------------------------------------------------------------------------
+struct F2 {
+  float h, l;
+};
+__device__ __forceinline__ F2 sum_ordered(float a, float b) {   // |a| >= |b| or a = 0
+  const float s = a + b;
+  return {s, b - (s - a)};
+}
+__device__ __forceinline__ F2 sum_any(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+// c + a b for a constant c above |a b|
+__device__ __forceinline__ F2 mul_add(F2 a, F2 b, float ch, float cl) {
+  const float p = a.h * b.h;
+  const float e = fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h);
+  const F2 s = sum_ordered(ch, p);
+  return sum_ordered(s.h, s.l + (e + cl));
+}
+
+// exp(x), |x| <= 80, to a relative 1e-11: x = n ln 2 + 2 r with ln 2 split as
+// 355/512 less a remainder (n 355/512 and its difference from x are exact),
+// then the exponential's series at r, |r| <= 0.174, up to r^3 in pairs and
+// from r^4 in floats (r^4/24's rounding: 2e-12), squared.
+__device__ __forceinline__ F2 exp_f2(float x) {
+  const float n = rintf(x * 1.44269504f);
+  const float t = fmaf(n, -0.693359375f, x);
+  const float ch = 0x1.bd0106p-13f, cl = -0x1.cf79acp-40f;   // 355/512 - ln 2
+  const float p = n * ch;
+  F2 r = sum_any(t, p);
+  r.l += fmaf(n, ch, -p) + n * cl;
+  r.h *= 0.5f;
+  r.l *= 0.5f;
+  const float tail = r.h * fmaf(r.h, fmaf(r.h, fmaf(r.h, 1.f / 40320.f, 1.f / 5040.f), 1.f / 720.f), 1.f / 120.f);
+  F2 g = {1.f / 24.f + tail, 0.f};
+  g = mul_add(r, g, 0x1.555556p-3f, -0x1.555556p-28f);   // 1/6
+  g = mul_add(r, g, 0.5f, 0.f);
+  g = mul_add(r, g, 1.f, 0.f);
+  g = mul_add(r, g, 1.f, 0.f);
+  const float sq = g.h * g.h;
+  const F2 e = sum_ordered(sq, fmaf(g.h, g.h, -sq) + 2.f * g.h * g.l);
+  const float k = __int_as_float(((int)n + 127) << 23);   // 2^n, |n| <= 116
+  return {e.h * k, e.l * k};
+}
+// a / d
+__device__ __forceinline__ F2 div_f2(F2 a, F2 d) {
+  const float q = a.h / d.h;
+  const float r = (fmaf(-q, d.h, a.h) + a.l) - q * d.l;
+  return sum_ordered(q, r / d.h);
+}
+
+// Units of 2^-40 of a score. A score is off by at most 30 of them, so two
+// sums of two by 120.
+constexpr long long kFineSure = 256;
+__device__ __forceinline__ long long fine_units(F2 v) {
+  return __float2ll_rn(v.h * 0x1p40f) + __float2ll_rn(v.l * 0x1p40f);
+}
+
+// The row's softmax sum (0 where p is 0 throughout), maximum m, four terms at
+// a time.
 template <int VPL>
-__device__ __noinline__ int score_exact_some(const float* row, int E, int k, const ScoreDev s,
-                                             float m32, float z32, unsigned elig, float thr, int* list) {
-  const int lane = threadIdx.x & 31, e0 = VPL * lane;
-  unsigned cand = 0u;
-  for (int i = 0; i < VPL; ++i)
-    if ((elig >> i) & 1u) {
-      const float c = score_prob(s, clean_logit(__ldcg(row + e0 + i)), m32, z32) + score_bias(s, e0 + i);
-      if (!(c < thr)) cand |= 1u << i;
+__device__ __noinline__ F2 softmax_f2(const float* row, int E, float m) {
+  const int lane = threadIdx.x & 31;
+  F2 z = {0.f, 0.f};
+  if (isinf(m)) return z;
+  constexpr int kStep = VPL < 4 ? VPL : 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < VPL; i0 += kStep) {
+    F2 t[kStep];
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      const int e = lane + 32 * (i0 + i);
+      const float l = e < E ? clean_logit(__ldcg(row + e)) : -INFINITY;
+      const F2 d = sum_any(fmaxf(l, m - 80.f), -m);   // (l - m in a pair: its rounding would cost 1e-7)
+      t[i] = exp_f2(fmaxf(d.h, -80.f));
+      t[i].l += t[i].h * d.l;
+      if (!(l - m > -80.f)) t[i] = {0.f, 0.f};
     }
-  const int total = list_candidates(cand, e0, list);
-  if (total > 32) return score_exact_all<VPL>(row, E, k, s);
-  double m = 0.0, z = 1.0;
-  if (!s.sigmoid) softmax64(row, E, m, z);
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      const F2 u = sum_any(z.h, t[i].h);
+      z = sum_ordered(u.h, u.l + (z.l + t[i].l));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float oh = __shfl_xor_sync(0xffffffffu, z.h, o), ol = __shfl_xor_sync(0xffffffffu, z.l, o);
+    const F2 u = sum_any(z.h, oh);
+    z = sum_ordered(u.h, u.l + (z.l + ol));
+  }
+  return z;
+}
+
+// A score (p, and the bias of an open expert) in units of 2^-40 above 2^62; 1
+// for a closed expert, 0 where the bias is beyond the units.
+__device__ __noinline__ unsigned long long fine_score(int sigmoid, float l, float b, float m, F2 z) {
+  if (b == -INFINITY) return 1ull;
+  if (!(fabsf(b) < 0x1p18f)) return 0ull;
+  F2 p = {0.f, 0.f};
+  const F2 d = sigmoid ? F2{fminf(fmaxf(-l, -80.f), 80.f), 0.f} : sum_any(fmaxf(l, m - 80.f), -m);
+  if (sigmoid || (z.h > 0.f && l - m > -80.f)) {
+    F2 x = exp_f2(d.h);
+    x.l += x.h * d.l;
+    F2 y = z;
+    if (sigmoid) {
+      const F2 u = sum_any(1.f, x.h);
+      y = sum_ordered(u.h, u.l + x.l);
+      x = {1.f, 0.f};
+    }
+    p = div_f2(x, y);
+  }
+  const F2 c = sum_any(p.h, b);
+  return (1ull << 62) + (unsigned long long)fine_units({c.h, c.l + p.l});
+}
+
+// Lane j's expert of the choice among the `total` <= 32 listed ones, by fine
+// scores; -1 in every lane where these cannot tell.
+__device__ __noinline__ int fine_order(const float* row, int k, const ScoreDev s, float m, F2 z,
+                                       int* list, int total) {
+  const int lane = threadIdx.x & 31;
   const int e = lane < total ? list[lane] : 0;
-  unsigned long long key = 0ull;
-  if (lane < total)
-    key = order_key64(prob64(s, clean_logit(__ldcg(row + e)), m, z) + (double)score_bias(s, e) + 0.0);
+  const float l = clean_logit(__ldcg(row + e)), b = score_bias(s, e);
+  const unsigned long long key = lane < total ? fine_score(s.sigmoid, l, b, m, z) : 0ull;
   int rank = 0;
+#pragma unroll 4
   for (int j = 0; j < total; ++j) {
     const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
     rank += o > key || (o == key && j < lane);
   }
+  // the lane that comes right after this one in the order
   __syncwarp();
-  if (lane < total) list[rank] = e;
+  if (lane < total) list[rank] = lane;
   __syncwarp();
-  return lane < k ? list[lane] : 0;
+  const int nx = rank + 1 < total ? list[rank + 1] : lane;
+  const int mine_lane = lane < total ? list[lane] : 0;
+  __syncwarp();
+  const unsigned long long nk = __shfl_sync(0xffffffffu, key, nx);
+  const float nl = __shfl_sync(0xffffffffu, l, nx), nb = __shfl_sync(0xffffffffu, b, nx);
+  // too close, unless the two are the same score by definition
+  const bool bad = lane < total && (key == 0ull || (rank < k && nx != lane && nk > 1ull &&
+                                                    key - nk <= (unsigned long long)kFineSure &&
+                                                    !(l == nl && b == nb)));
+  const int mine = __shfl_sync(0xffffffffu, e, mine_lane);
+  return __any_sync(0xffffffffu, bad) ? -1 : mine;
+}
+
+// Which of the doubtful groups (bits by group) stay, `want` of them, from the
+// `total` <= 32 listed experts, which hold each one's two best; returns the
+// kept ones' bits, 0 where fine scores cannot tell.
+__device__ __noinline__ unsigned fine_groups(const float* row, int gsz, const ScoreDev s, float m, F2 z,
+                                             const int* list, int total, unsigned doubt, int want) {
+  const int lane = threadIdx.x & 31;
+  const int e = lane < total ? list[lane] : 0, grp = lane < total ? e / gsz : -1;
+  unsigned long long key = 0ull;
+  if (lane < total)
+    key = fine_score(s.sigmoid, clean_logit(__ldcg(row + e)), s.bias ? score_bias(s, e) : 0.f, m, z);
+  const bool beyond = lane < total && key == 0ull;
+  long long mine = 0;   // lane g: group g's sum
+  for (unsigned left = doubt; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    unsigned long long k1 = grp == g ? key : 0ull, k2 = 0ull;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long a = __shfl_xor_sync(0xffffffffu, k1, o);
+      const unsigned long long b = __shfl_xor_sync(0xffffffffu, k2, o);
+      const unsigned long long lo = a < k1 ? a : k1, hi = b > k2 ? b : k2;
+      k1 = a > k1 ? a : k1;
+      k2 = lo > hi ? lo : hi;
+    }
+    // (a group with a closed expert among its two best is -infinity)
+    const bool shut = k1 <= 1ull || (gsz > 1 && k2 <= 1ull);
+    const long long one = 1ll << 62;
+    if (lane == g)
+      mine = shut ? -(1ll << 61) : ((long long)k1 - one) + (gsz > 1 ? (long long)k2 - one : 0ll);
+  }
+  int rank = 0;
+  for (unsigned left = doubt; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    const long long o = __shfl_sync(0xffffffffu, mine, g);
+    rank += o > mine || (o == mine && g < lane);
+  }
+  const bool in = (doubt >> lane) & 1u;
+  const unsigned keep = __ballot_sync(0xffffffffu, in && rank < want);
+  const unsigned last = __ballot_sync(0xffffffffu, in && rank == want - 1);
+  const unsigned next = __ballot_sync(0xffffffffu, in && rank == want);
+  bool bad = beyond || !last;
+  if (last && next) {
+    const long long a = __shfl_sync(0xffffffffu, mine, __ffs(last) - 1);
+    const long long b = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
+    bad |= a - b <= kFineSure;
+  }
+  return __any_sync(0xffffffffu, bad) ? 0u : keep;
 }
 
 // Lane j < k gets the j-th chosen expert and its weight. `sm`: max(E, 64)
@@ -253,11 +422,13 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
   }
-  // Bound of a pair's FP32 error: expf within 2 ulp, the additions and the
-  // division half an ulp each (sigmoid: below 3.6e-7 p); softmax's argument
-  // and sum bring that to 2e-6 p. p <= 1, and softmax's largest p is 1 / z.
-  // The bias' addition: half an ulp of c.
-  const float perr = s.sigmoid ? 1.2e-6f : 6e-6f / z;
+  // Bound of a pair's FP32 error, from expf's 2 ulp and half an ulp for every
+  // addition and division. Sigmoid: e = exp(-l) enters p = 1 / (1 + e) by
+  // e / (1 + e) = 1 - p, so p is off by p (1 - p) 2^-22 + p 2^-23 < 1.8e-7.
+  // Softmax, of the largest p, 1 / z: 3.2e-7 by the exponential (its argument
+  // too) and the division, for each of the two, and 1.6e-6 by z (at most 21
+  // additions), which both share. The bias' addition: half an ulp of c.
+  const float perr = s.sigmoid ? 4e-7f : 2.5e-6f / z;
   uint32_t key[VPL];   // every real key is above 0
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -306,6 +477,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       m1 = fmaxf(m1, a);
     }
     const int g = lane / span;
+    const float low = m2 > -INFINITY ? m2 : m1;   // the second largest, in the keys' terms
     float sum = -INFINITY;
     if (g < s.groups) {
       if (!s.bias) {
@@ -323,7 +495,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       rank += o > sum || (o == sum && j < g);
     }
     const bool head = lane % span == 0 && g < s.groups;
-    const unsigned keep = __ballot_sync(0xffffffffu, head && rank < s.topk_groups);
+    unsigned keep = __ballot_sync(0xffffffffu, head && rank < s.topk_groups);
     // the last group kept and the first dropped: four scores' errors and the
     // sums' roundings
     const unsigned last = __ballot_sync(0xffffffffu, head && rank == s.topk_groups - 1);
@@ -331,7 +503,39 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     if (next) {
       const float a = __shfl_sync(0xffffffffu, sum, __ffs(last) - 1);
       const float b = __shfl_sync(0xffffffffu, sum, __ffs(next) - 1);
-      unsure_groups = !(a - b > 2.f * perr + 5e-7f * fmaxf(big, 1.f));
+      const float wide = 2.f * perr + 5e-7f * fmaxf(big, 1.f);
+      if (!(a - b > wide)) {
+        // doubtful: the groups between b and a, within the bound; their experts
+        // that may be among their two best go into the list
+        const bool dub = head && sum >= b - wide && sum <= a + wide;
+        const unsigned dheads = __ballot_sync(0xffffffffu, dub);
+        unsigned doubt = 0u;
+        for (unsigned left = dheads; left; left &= left - 1) doubt |= 1u << ((__ffs(left) - 1) / span);
+        const int want = s.topk_groups - __popc(keep & ~dheads);
+        unsigned cand = 0u;
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+          const int eg = min(e0 + i, E - 1) / gsz;
+          const float lw = __shfl_sync(0xffffffffu, low, eg * span);
+          if (e0 + i < E && ((doubt >> eg) & 1u)) {
+            const float c = clean_logit(__ldcg(row + e0 + i));
+            const float cv = s.bias ? score_prob(s, c, m, z) + score_bias(s, e0 + i) : c;
+            if (!(cv < (s.bias ? lw - 2.f * (perr + 2.5e-7f * fabsf(lw)) : lw))) cand |= 1u << i;
+          }
+        }
+        int* list = reinterpret_cast<int*>(sm);
+        const int total = list_candidates(cand, e0, list);
+        unsigned kept = 0u;
+        if (total <= 32) {
+          F2 z2 = {1.f, 0.f};
+          if (!s.sigmoid) z2 = softmax_f2<VPL>(row, E, m);
+          kept = fine_groups(row, gsz, s, m, z2, list, total, doubt, want);
+        }
+        __syncwarp();
+        unsure_groups = kept == 0u;
+        keep &= ~dheads;
+        for (; kept; kept &= kept - 1) keep |= 1u << ((__ffs(kept) - 1) * span);
+      }
     }
     if (whole) {
       if (!((keep >> (g * span)) & 1u)) {
@@ -361,12 +565,10 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     }
     const unsigned at = __ballot_sync(0xffffffffu, rank == need - 1);   // 0 if need is 33
     const uint32_t floor_key = at ? max(__shfl_sync(0xffffffffu, top, __ffs(at) - 1), 1u) : 1u;
-    unsigned cand = 0u, elig = 0u;
+    unsigned cand = 0u;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (key[i]) elig |= 1u << i;
+    for (int i = 0; i < VPL; ++i)
       if (key[i] >= floor_key) cand |= 1u << i;
-    }
     int* list = reinterpret_cast<int*>(sm);
     uint32_t* lkey = reinterpret_cast<uint32_t*>(sm) + 32;
     const int total = list_candidates(cand, e0, list);
@@ -429,8 +631,22 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       const bool close = lane < k && next_key != 0u && !(isinf(a) && a == b) &&
                          !(a - b > perr + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)));
       if (__any_sync(0xffffffffu, close)) {
-        const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
-        mine = score_exact_some<VPL>(row, E, k, s, m, z, elig, vk - 2.f * (perr + 2.5e-7f * fabsf(vk)), list);
+        int fine = -1;
+        if (total <= 32) {   // (else the keys are used up)
+          const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
+          const uint32_t thr = order_key(vk - 2.f * (perr + 2.5e-7f * fabsf(vk)));
+          cand = 0u;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (key[i] && key[i] >= thr) cand |= 1u << i;
+          const int n = list_candidates(cand, e0, list);
+          if (n <= 32) {
+            F2 z2 = {1.f, 0.f};
+            if (!s.sigmoid) z2 = softmax_f2<VPL>(row, E, m);
+            fine = fine_order(row, k, s, m, z2, list, n);
+          }
+        }
+        mine = fine >= 0 ? fine : score_exact_all<VPL>(row, E, k, s);
       }
     }
   }
