@@ -726,9 +726,10 @@ moe_status moe_route_scored(moe_plan_t p, const float* logits, int T, const moe_
     return MOE_ERR_INVALID_ARG;
   if (!(d->scale > -3e38f && d->scale < 3e38f)) return MOE_ERR_INVALID_ARG;
   void* const outs[] = {r->topk_idx, r->topk_w, r->counts, r->offsets, r->tile_offsets,
-                        r->perm, r->inv, r->block_map, r->num_tiles, (void*)d->bias};
+                        r->perm, r->inv, r->block_map, r->num_tiles};
   for (void* q : outs)
     if (reinterpret_cast<uintptr_t>(q) & 3u) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d->bias)) return MOE_ERR_INVALID_ARG;
   auto own = [&](auto*& field, size_t off) {
     if (!field) field = reinterpret_cast<std::remove_reference_t<decltype(field)>>(p->scratch + off);
   };

@@ -53,25 +53,25 @@ __device__ __forceinline__ void warp_best64(unsigned long long& key, int& ix) {
   }
 }
 
-__device__ __forceinline__ float clean_logit(float v) { return isnan(v) ? -INFINITY : v + 0.0f; }
+// NaN as -infinity, -0 as +0
+__device__ __forceinline__ float clean_logit(float v) { return fmaxf(v, -INFINITY) + 0.0f; }
 
 // The bias of expert e, -infinity where the expert is closed.
 __device__ __forceinline__ float score_bias(const ScoreDev& s, int e) {
-  const float b = __ldg(s.bias + e);
-  return isnan(b) ? -INFINITY : b;
+  return fmaxf(__ldg(s.bias + e), -INFINITY);
 }
 
 // Softmax's maximum and sum in 64 bits (the sum 0 where p is 0 throughout).
 __device__ __forceinline__ void softmax64(const float* row, int E, double& m, double& z) {
   const int lane = threadIdx.x & 31;
   float mf = -INFINITY;
-  for (int e = lane; e < E; e += 32) mf = fmaxf(mf, clean_logit(__ldcg(row + e)));
+  for (int e = lane; e < E; e += 32) mf = fmaxf(mf, clean_logit(__ldg(row + e)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
   m = mf;
   z = 0.0;
   if (isinf(mf)) return;
-  for (int e = lane; e < E; e += 32) z += exp((double)clean_logit(__ldcg(row + e)) - m);
+  for (int e = lane; e < E; e += 32) z += exp((double)clean_logit(__ldg(row + e)) - m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 }
@@ -94,7 +94,7 @@ __device__ __noinline__ int score_exact_all(const float* row, int E, int k, cons
     const int e = lane + 32 * i;
     key[i] = 0ull;
     if (e < E) {
-      double c = prob64(s, clean_logit(__ldcg(row + e)), m, z);
+      double c = prob64(s, clean_logit(__ldg(row + e)), m, z);
       if (s.bias) c += (double)score_bias(s, e);
       key[i] = order_key64(c + 0.0);
     }
@@ -136,7 +136,7 @@ __device__ __noinline__ int score_exact_all(const float* row, int E, int k, cons
     if (e >= E) continue;
     if (!((keep >> (e / gsz)) & 1u)) key[i] = 0ull;
     // without a bias the experts rank by their logits
-    else if (!s.bias) key[i] = order_key(clean_logit(__ldcg(row + e)));
+    else if (!s.bias) key[i] = order_key(clean_logit(__ldg(row + e)));
   }
   int mine = 0;
   for (int j = 0; j < k; ++j) {
@@ -157,11 +157,18 @@ __device__ __noinline__ int score_exact_all(const float* row, int E, int k, cons
   return mine;
 }
 
-// The FP32 score of an expert (without its bias) under a row's softmax
-// maximum and sum.
-__device__ __forceinline__ float score_prob(const ScoreDev& s, float l, float m, float z) {
-  if (s.sigmoid) return 1.0f / (1.0f + expf(-l));
-  return isinf(m) ? 0.f : expf(l - m) / z;
+// 1 / v to 1 ulp
+__device__ __forceinline__ float rcp_1ulp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The FP32 score of an expert (without its bias); softmax: from the row's
+// maximum and the reciprocal of its sum (0 where p is 0 throughout).
+__device__ __forceinline__ float score_prob(const ScoreDev& s, float l, float m, float rz) {
+  if (s.sigmoid) return rcp_1ulp(1.0f + expf(-l));
+  return rz > 0.f ? __fmul_rn(expf(l - m), rz) : 0.f;
 }
 
 // Writes the lane's experts e0 + i, i in the set `cand`, into `list` (32
@@ -261,7 +268,7 @@ __device__ __noinline__ F2 softmax_f2(const float* row, int E, float m) {
 #pragma unroll
     for (int i = 0; i < kStep; ++i) {
       const int e = lane + 32 * (i0 + i);
-      const float l = e < E ? clean_logit(__ldcg(row + e)) : -INFINITY;
+      const float l = e < E ? clean_logit(__ldg(row + e)) : -INFINITY;
       const F2 d = sum_any(fmaxf(l, m - 80.f), -m);   // (l - m in a pair: its rounding would cost 1e-7)
       t[i] = exp_f2(fmaxf(d.h, -80.f));
       t[i].l += t[i].h * d.l;
@@ -310,7 +317,7 @@ __device__ __noinline__ int fine_order(const float* row, int k, const ScoreDev s
                                        int* list, int total) {
   const int lane = threadIdx.x & 31;
   const int e = lane < total ? list[lane] : 0;
-  const float l = clean_logit(__ldcg(row + e)), b = score_bias(s, e);
+  const float l = clean_logit(__ldg(row + e)), b = score_bias(s, e);
   const unsigned long long key = lane < total ? fine_score(s.sigmoid, l, b, m, z) : 0ull;
   int rank = 0;
 #pragma unroll 4
@@ -344,7 +351,7 @@ __device__ __noinline__ unsigned fine_groups(const float* row, int gsz, const Sc
   const int e = lane < total ? list[lane] : 0, grp = lane < total ? e / gsz : -1;
   unsigned long long key = 0ull;
   if (lane < total)
-    key = fine_score(s.sigmoid, clean_logit(__ldcg(row + e)), s.bias ? score_bias(s, e) : 0.f, m, z);
+    key = fine_score(s.sigmoid, clean_logit(__ldg(row + e)), s.bias ? score_bias(s, e) : 0.f, m, z);
   const bool beyond = lane < total && key == 0ull;
   long long mine = 0;   // lane g: group g's sum
   for (unsigned left = doubt; left; left &= left - 1) {
@@ -383,6 +390,50 @@ __device__ __noinline__ unsigned fine_groups(const float* row, int gsz, const Sc
   return __any_sync(0xffffffffu, bad) ? 0u : keep;
 }
 
+// The choice in rounds of one key each, among the keys (0: not eligible) of
+// the lane's experts; lane j gets the j-th of `need`, its key and the next.
+template <int VPL>
+__device__ __noinline__ int choose_in_rounds(const float* row, int E, const ScoreDev s, float m, float rz,
+                                             unsigned elig, int need, uint32_t& my_key,
+                                             uint32_t& next_key) {
+  const int lane = threadIdx.x & 31, e0 = VPL * lane;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    key[i] = 0u;
+    if ((elig >> i) & 1u) {
+      const float l = clean_logit(__ldg(row + e0 + i));
+      key[i] = order_key(s.bias ? score_prob(s, l, m, rz) + score_bias(s, e0 + i) : l);
+    }
+  }
+  int mine = 0;
+  my_key = next_key = 0u;
+#pragma unroll 1
+  for (int j = 0; j < need; ++j) {
+    uint32_t hk = key[0];
+    int hi = 0;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > hk) {
+        hk = key[i];
+        hi = i;
+      }
+    const uint32_t mk = __reduce_max_sync(0xffffffffu, hk);
+    // the lowest lane that holds it has the lowest expert
+    const int src = __ffs(__ballot_sync(0xffffffffu, hk == mk)) - 1;
+    const int be = __shfl_sync(0xffffffffu, e0 + hi, src);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane == src && i == hi) key[i] = 0u;
+    if (lane == j) {
+      mine = be;
+      my_key = mk;
+    }
+    if (lane == j - 1) next_key = mk;
+  }
+  return mine;
+}
+
 // Lane j < k gets the j-th chosen expert and its weight. `sm`: max(E, 64)
 // floats of the warp's own shared memory.
 template <int VPL>   // experts per lane, E <= 32 * VPL
@@ -390,79 +441,91 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
                                              const ScoreDev& s, float* sm, int& idx, float& w) {
   const int lane = threadIdx.x & 31;
   const int e0 = VPL * lane;
-  float l[VPL];
-  if constexpr (VPL == 2) {
-    float2 v = make_float2(-INFINITY, -INFINITY);
-    if (e0 < E) v = __ldcg(reinterpret_cast<const float2*>(row + e0));
-    l[0] = clean_logit(v.x);
-    l[1] = clean_logit(v.y);
-  } else {
+  // the lane's logits, then its scores c (without a bias: the logits still)
+  float c[VPL];
+  // (through L1, where the bias stays: every token reads the same one)
+  auto load_row = [&](const float* src, auto&& put) {
+    if constexpr (VPL == 2) {
+      float2 v = make_float2(-INFINITY, -INFINITY);
+      if (e0 < E) v = __ldg(reinterpret_cast<const float2*>(src + e0));
+      put(0, v.x);
+      put(1, v.y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPL; i += 4) {
-      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (e0 + i < E) v = __ldcg(reinterpret_cast<const float4*>(row + e0 + i));
-      l[i] = clean_logit(v.x);
-      l[i + 1] = clean_logit(v.y);
-      l[i + 2] = clean_logit(v.z);
-      l[i + 3] = clean_logit(v.w);
+      for (int i = 0; i < VPL; i += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e0 + i < E) v = __ldg(reinterpret_cast<const float4*>(src + e0 + i));
+        put(i, v.x);
+        put(i + 1, v.y);
+        put(i + 2, v.z);
+        put(i + 3, v.w);
+      }
     }
-  }
-  // softmax: maximum and sum over all experts
-  float m = 0.f, z = 1.f;
+  };
+  load_row(row, [&](int i, float v) { c[i] = clean_logit(v); });
+  float m = 0.f, rz = 1.f;
   if (!s.sigmoid && (s.bias || s.groups > 1 || !s.renorm)) {
-    m = l[0];
+    m = c[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
     m = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
-    if (!isinf(m)) {
-      z = 0.f;
+    const float mm = isinf(m) ? 0.f : m;
+    float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) z += expf(l[i] - m);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    for (int i = 0; i < VPL; ++i) {
+      const float p = expf(c[i] - mm);
+      if (s.bias) c[i] = p;
+      z += p;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    rz = isinf(m) ? 0.f : 1.0f / z;
   }
-  // Bound of a pair's FP32 error, from expf's 2 ulp and half an ulp for every
-  // addition and division. Sigmoid: e = exp(-l) enters p = 1 / (1 + e) by
-  // e / (1 + e) = 1 - p, so p is off by p (1 - p) 2^-22 + p 2^-23 < 1.8e-7.
-  // Softmax, of the largest p, 1 / z: 3.2e-7 by the exponential (its argument
-  // too) and the division, for each of the two, and 1.6e-6 by z (at most 21
-  // additions), which both share. The bias' addition: half an ulp of c.
-  const float perr = s.sigmoid ? 4e-7f : 2.5e-6f / z;
-  uint32_t key[VPL];   // every real key is above 0
+  if (s.bias) {
+    if (s.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = rcp_1ulp(1.0f + expf(-c[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = rz > 0.f ? __fmul_rn(c[i], rz) : 0.f;
+    }
+    load_row(s.bias, [&](int i, float v) { c[i] = __fadd_rn(c[i], fmaxf(v, -INFINITY)); });
+  }
+  // Bound of a pair's FP32 error, from expf's 2 ulp, the reciprocal's 1 and
+  // half an ulp for every other operation. Sigmoid: e = exp(-l) enters
+  // p = 1 / (1 + e) by e / (1 + e) = 1 - p, so p is off by p (1 - p) 2^-22 +
+  // 1.5 p 2^-23 < 2.4e-7. Softmax, of the largest p, 1 / z: 3.4e-7 by the
+  // exponential (its argument too) and the product, for each of the two, and
+  // 1.8e-6 by 1 / z (at most 21 additions), which both share. The bias'
+  // addition: half an ulp of c.
+  const float perr = s.sigmoid ? 5e-7f : 2.8e-6f * rz;
+  float m1 = -INFINITY, m2 = -INFINITY;   // the lane's two largest
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    key[i] = 0u;
-    if (e0 + i < E)
-      key[i] = order_key(s.bias ? score_prob(s, l[i], m, z) + score_bias(s, e0 + i) + 0.0f : l[i]);
+    m2 = fmaxf(m2, fminf(m1, c[i]));
+    m1 = fmaxf(m1, c[i]);
   }
+  float top = m1;
   bool unsure_groups = false;
+  constexpr unsigned kAll = (unsigned)((1ull << VPL) - 1ull);
+  unsigned elig = e0 + VPL <= E ? kAll : e0 >= E ? 0u : (1u << (E - e0)) - 1u;
   if (s.groups > 1) {
     const int gsz = E / s.groups;
     // lanes per group where no lane's experts belong to two groups
     const int per = gsz / VPL;
     const bool whole = gsz % VPL == 0 && (per & (per - 1)) == 0;
-    float m1 = -INFINITY, m2 = -INFINITY, big = 0.f;
     int span = per;   // lanes that hold one group's parts: group lane / span
-    if (whole) {
-      if (e0 < E) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float v = key_value(key[i]);
-          m2 = fmaxf(m2, fminf(m1, v));
-          m1 = fmaxf(m1, v);
-        }
-      }
-    } else {
+    if (!whole) {
       // through shared memory: `span` lanes a group, each every span-th expert
       int g2 = 1;
       while (g2 < s.groups) g2 <<= 1;
       span = 32 / g2;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (e0 + i < E) sm[e0 + i] = key_value(key[i]);
+        if (e0 + i < E) sm[e0 + i] = c[i];
       __syncwarp();
       const int g = lane / span;
+      m1 = m2 = -INFINITY;
       if (g < s.groups)
         for (int i = lane % span; i < gsz; i += span) {
           const float v = sm[g * gsz + i];
@@ -477,12 +540,12 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       m1 = fmaxf(m1, a);
     }
     const int g = lane / span;
-    const float low = m2 > -INFINITY ? m2 : m1;   // the second largest, in the keys' terms
-    float sum = -INFINITY;
+    const float low = m2 > -INFINITY ? m2 : m1;   // the second largest
+    float sum = -INFINITY, big = 0.f;
     if (g < s.groups) {
       if (!s.bias) {
-        m1 = score_prob(s, m1, m, z);
-        m2 = score_prob(s, m2, m, z);
+        m1 = score_prob(s, m1, m, rz);
+        m2 = score_prob(s, m2, m, rz);
       }
       sum = gsz > 1 ? m1 + m2 : m1;
       if (!isinf(m1)) big = fabsf(m1);
@@ -513,15 +576,12 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
         for (unsigned left = dheads; left; left &= left - 1) doubt |= 1u << ((__ffs(left) - 1) / span);
         const int want = s.topk_groups - __popc(keep & ~dheads);
         unsigned cand = 0u;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < VPL; ++i) {
           const int eg = min(e0 + i, E - 1) / gsz;
           const float lw = __shfl_sync(0xffffffffu, low, eg * span);
-          if (e0 + i < E && ((doubt >> eg) & 1u)) {
-            const float c = clean_logit(__ldcg(row + e0 + i));
-            const float cv = s.bias ? score_prob(s, c, m, z) + score_bias(s, e0 + i) : c;
-            if (!(cv < (s.bias ? lw - 2.f * (perr + 2.5e-7f * fabsf(lw)) : lw))) cand |= 1u << i;
-          }
+          const float thr = s.bias ? lw - 2.f * (perr + 2.5e-7f * fabsf(lw)) : lw;
+          if (e0 + i < E && ((doubt >> eg) & 1u) && !(c[i] < thr)) cand |= 1u << i;
         }
         int* list = reinterpret_cast<int*>(sm);
         const int total = list_candidates(cand, e0, list);
@@ -537,51 +597,62 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
         for (; kept; kept &= kept - 1) keep |= 1u << ((__ffs(kept) - 1) * span);
       }
     }
+    // the dropped groups' experts leave: -infinity, and not eligible
     if (whole) {
       if (!((keep >> (g * span)) & 1u)) {
+        elig = 0u;
+        top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = 0u;
+        for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
       }
     } else {
+      top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] && !((keep >> ((e0 + i) / gsz * span)) & 1u)) key[i] = 0u;
+      for (int i = 0; i < VPL; ++i) {
+        if (e0 + i < E && !((keep >> ((e0 + i) / gsz * span)) & 1u)) {
+          c[i] = -INFINITY;
+          elig &= ~(1u << i);
+        }
+        top = fmaxf(top, c[i]);
+      }
     }
   }
   int mine = 0;
   if (unsure_groups) {
     mine = score_exact_all<VPL>(row, E, k, s);
   } else {
-    // `need` keys in order: the k chosen, and with a bias the next one
+    // `need` scores in order: the k chosen, and with a bias the next one. The
+    // lanes' need-th largest maximum bounds them from below.
     const int need = s.bias ? k + 1 : k;
-    uint32_t top = key[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) top = max(top, key[i]);
     int rank = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const uint32_t o = __shfl_sync(0xffffffffu, top, j);
+      const float o = __shfl_sync(0xffffffffu, top, j);
       rank += o > top || (o == top && j < lane);
     }
     const unsigned at = __ballot_sync(0xffffffffu, rank == need - 1);   // 0 if need is 33
-    const uint32_t floor_key = at ? max(__shfl_sync(0xffffffffu, top, __ffs(at) - 1), 1u) : 1u;
-    unsigned cand = 0u;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] >= floor_key) cand |= 1u << i;
+    const float bound = at ? __shfl_sync(0xffffffffu, top, __ffs(at) - 1) : -INFINITY;
     int* list = reinterpret_cast<int*>(sm);
     uint32_t* lkey = reinterpret_cast<uint32_t*>(sm) + 32;
-    const int total = list_candidates(cand, e0, list);
+    int total = 33;
+    if (bound > -INFINITY) {
+      unsigned cand = 0u;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (c[i] >= bound) cand |= 1u << i;
+      total = list_candidates(cand, e0, list);
+    }
     uint32_t my_key = 0u, next_key = 0u;
     if (total <= 32) {
       // the list's order: rank by key, then by place
       const int e = lane < total ? list[lane] : 0;
       uint32_t ck = 0u;
       if (lane < total) {
-        const float v = clean_logit(__ldcg(row + e));
-        ck = order_key(s.bias ? score_prob(s, v, m, z) + score_bias(s, e) + 0.0f : v);
+        const float v = clean_logit(__ldg(row + e));
+        ck = order_key(s.bias ? __fadd_rn(score_prob(s, v, m, rz), score_bias(s, e)) : v);
       }
       int r = 0;
+#pragma unroll 4
       for (int j = 0; j < total; ++j) {
         const uint32_t o = __shfl_sync(0xffffffffu, ck, j);
         r += o > ck || (o == ck && j < lane);
@@ -600,29 +671,8 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       next_key = __shfl_down_sync(0xffffffffu, my_key, 1);
       if (lane == 31) next_key = 0u;
     } else {
-      // more (many equal keys, few lanes, or k near 32): one round per key,
-      // the lowest lane that holds the largest first
-      for (int j = 0; j < need; ++j) {
-        uint32_t hk = key[0];
-        int hi = 0;
-#pragma unroll
-        for (int i = 1; i < VPL; ++i)
-          if (key[i] > hk) {
-            hk = key[i];
-            hi = i;
-          }
-        const uint32_t mk = __reduce_max_sync(0xffffffffu, hk);
-        const int src = __ffs(__ballot_sync(0xffffffffu, hk == mk)) - 1;
-        const int be = __shfl_sync(0xffffffffu, e0 + hi, src);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane == src && i == hi) key[i] = 0u;
-        if (lane == j) {
-          mine = be;
-          my_key = mk;
-        }
-        if (lane == j - 1) next_key = mk;
-      }
+      // many equal scores, fewer open ones than needed, few lanes, or k near 32
+      mine = choose_in_rounds<VPL>(row, E, s, m, rz, elig, need, my_key, next_key);
     }
     if (s.bias) {
       // neighbours in the order: equal infinities are certain (closed
@@ -631,20 +681,18 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       const bool close = lane < k && next_key != 0u && !(isinf(a) && a == b) &&
                          !(a - b > perr + 2.5e-7f * fmaxf(fabsf(a), fabsf(b)));
       if (__any_sync(0xffffffffu, close)) {
-        int fine = -1;
-        if (total <= 32) {   // (else the keys are used up)
-          const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
-          const uint32_t thr = order_key(vk - 2.f * (perr + 2.5e-7f * fabsf(vk)));
-          cand = 0u;
+        const float vk = key_value(__shfl_sync(0xffffffffu, my_key, k - 1));
+        const float thr = vk - 2.f * (perr + 2.5e-7f * fabsf(vk));
+        unsigned cand = 0u;
 #pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (key[i] && key[i] >= thr) cand |= 1u << i;
-          const int n = list_candidates(cand, e0, list);
-          if (n <= 32) {
-            F2 z2 = {1.f, 0.f};
-            if (!s.sigmoid) z2 = softmax_f2<VPL>(row, E, m);
-            fine = fine_order(row, k, s, m, z2, list, n);
-          }
+        for (int i = 0; i < VPL; ++i)
+          if (((elig >> i) & 1u) && !(c[i] < thr)) cand |= 1u << i;
+        const int n = list_candidates(cand, e0, list);
+        int fine = -1;
+        if (n <= 32) {
+          F2 z2 = {1.f, 0.f};
+          if (!s.sigmoid) z2 = softmax_f2<VPL>(row, E, m);
+          fine = fine_order(row, k, s, m, z2, list, n);
         }
         mine = fine >= 0 ? fine : score_exact_all<VPL>(row, E, k, s);
       }
@@ -654,7 +702,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
   float lj = -INFINITY;
   bool open = false;
   if (lane < k) {
-    lj = clean_logit(__ldcg(row + mine));
+    lj = clean_logit(__ldg(row + mine));
     open = !s.bias || score_bias(s, mine) > -INFINITY;
   }
   float pj = 0.f;
@@ -662,17 +710,17 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     // relative to the largest chosen logit, so that no sum underflows; a
     // sigmoid far below zero is the exponential, and below -745 (a row of
     // masks of the type's lowest value) it is 0 in 64 bits too
-    const float top = key_value(__reduce_max_sync(0xffffffffu, order_key(open ? lj : -INFINITY)));
-    if (open && top > (s.sigmoid ? -745.f : -INFINITY)) {
-      if (s.sigmoid) pj = top < -40.f ? expf(lj - top) : 1.0f / (1.0f + expf(-lj));
-      else if (!isinf(top) && !isinf(m)) pj = expf(lj - top);
+    const float best = key_value(__reduce_max_sync(0xffffffffu, order_key(open ? lj : -INFINITY)));
+    if (open && best > (s.sigmoid ? -745.f : -INFINITY)) {
+      if (s.sigmoid) pj = best < -40.f ? expf(lj - best) : 1.0f / (1.0f + expf(-lj));
+      else if (!isinf(best) && rz > 0.f) pj = expf(lj - best);
     }
     float sum = pj;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     pj = sum > 0.f ? pj / sum : 0.f;
   } else if (open) {
-    pj = score_prob(s, lj, m, z);
+    pj = score_prob(s, lj, m, rz);
   }
   idx = mine;
   w = pj * s.scale;
