@@ -10,11 +10,12 @@
 // the next tile's MMAs. K goes by in chunks of 64.
 //
 // The adapters are more columns of K. For every adapter that occurs among the
-// tile's tokens the tile gets K columns with h in A, zero in the rows of other
-// tokens, and B[a] in B: the MMAs then add each token's own product, whatever
-// the order of the tokens. h goes in as two bf16 (the value and what its
-// rounding left), against B's own bf16: the products are exact to 16 bits of h.
-// Four warps write these chunks, spread between the tile's other chunks.
+// tile's tokens the tile gets rank K columns with h in A, zero in the rows of
+// other tokens, and B[a] in B: the MMAs then add each token's own product,
+// whatever the order of the tokens. They go by in stages of 16 columns, spread
+// between the tile's other chunks: four warps write A, B comes by TMA. h goes in
+// as two bf16 (the value and what its rounding left), each multiplied with B's
+// own bf16: the products are exact to 16 bits of h.
 //
 // Every wait is bounded, as in gemm_tc2.cu.
 #include "pair.cuh"
@@ -28,12 +29,17 @@ constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kTmemCols = 512;
 
+// An adapter stage: h and its rest (A, 128 rows x 16 bf16 each), B's rows.
+constexpr int kLoraStages = 2;
+constexpr int kLoraTile = 128 * 32;
+constexpr int kLoraStageBytes = 3 * kLoraTile;
+
 template <bool kLora>
 struct Smem {
-  static constexpr int kStages = kLora ? 5 : 6;
+  static constexpr int kStages = kLora ? 6 : 7;
   static constexpr int kOffLora = kStages * kStageBytes;
-  static constexpr int kOffIds = kOffLora + (kLora ? kStageBytes : 0);
-  static constexpr int kOffBar = kOffIds + (kLora ? 2 * kTileM * 4 : 0);
+  static constexpr int kOffIds = kOffLora + (kLora ? kLoraStages * kLoraStageBytes : 0);
+  static constexpr int kOffBar = kOffIds + (kLora ? 3 * kTileM * 4 : 0);
   static constexpr int kBytes = kOffBar + 512 + 1024;   // barriers, alignment slack
 };
 static_assert(Smem<true>::kBytes <= 227 * 1024 && Smem<false>::kBytes <= 227 * 1024, "shared memory");
@@ -41,6 +47,7 @@ static_assert(Smem<true>::kBytes <= 227 * 1024 && Smem<false>::kBytes <= 227 * 1
 struct Params {
   CUtensorMap mx;       // x16 [rows][K], boxes 64 x 128
   CUtensorMap mw;       // W16 [N][K], boxes 64 x BN / 2
+  CUtensorMap mb;       // B [n][N][r], boxes 16 x BN / 2 x 1, 32-byte swizzle
   LinearArgs a;
   int bn, mt, tiles;    // tile width, token tiles, all tiles
   DevErr err;
@@ -73,16 +80,27 @@ __device__ __forceinline__ int token_adapter(const LinearArgs& a, int t) {
   return (unsigned)id < (unsigned)a.n_adapters ? id : -1;
 }
 
-// h[0..15] of one 16-column block as bf16: the rounded values (lo = false) or
-// what the rounding left.
-__device__ __forceinline__ void split_h(const float4 (&v)[4], bool rest, uint32_t (&o)[8]) {
-  const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
-                       v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    o[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    if (rest) o[i] = pack_bf16x2(f[2 * i] - bf16_lo(o[i]), f[2 * i + 1] - bf16_hi(o[i]));
-  }
+// Operand descriptor of a tile of 16 K columns: K-major, 32-byte rows with
+// 32-byte swizzle (a row's two 16-byte halves change places in rows 4..7 of
+// every 8), 8-row groups 256 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);        // start address
+  d |= static_cast<uint64_t>(1u) << 16;                           // LBO (unused)
+  d |= static_cast<uint64_t>(256u >> 4) << 32;                    // SBO: 8 rows * 32 B
+  d |= static_cast<uint64_t>(1u) << 46;                           // descriptor version
+  d |= static_cast<uint64_t>(6u) << 61;                           // 32-byte swizzle
+  return d;
+}
+
+// 3D tiled load of this CTA's half of B, as tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, int x, int y, int z,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+      : "memory");
 }
 
 // Barrier of the 128 adapter threads that tells whether all of them go on, so
@@ -103,6 +121,28 @@ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
   return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);
 }
 
+// Places of the flagged entries among 256 (thread i of 128 holds entries i
+// and 128 + i) in their order, and their number. `cnt`: 8 ints.
+__device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra, int& rb) {
+  const int lane = i & 31, w = i >> 5;
+  const unsigned ma = __ballot_sync(0xffffffffu, a), mb = __ballot_sync(0xffffffffu, b);
+  if (lane == 0) {
+    cnt[w] = __popc(ma);
+    cnt[4 + w] = __popc(mb);
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  int n = 0;
+  ra = rb = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j == w) ra = n + __popc(ma & ((1u << lane) - 1u));
+    if (j == 4 + w) rb = n + __popc(mb & ((1u << lane) - 1u));
+    n += cnt[j];
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  return n;
+}
+
 template <bool kLora>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ Params p) {
@@ -111,18 +151,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
-  uint8_t* lora_a = smem + S::kOffLora;
-  uint8_t* lora_b = lora_a + kOpBytes;
+  uint8_t* lora = smem + S::kOffLora;
   int* s_ids = reinterpret_cast<int*>(smem + S::kOffIds);   // the tile's adapter per token
-  int* s_list = s_ids + kTileM;                             // its distinct adapters
+  int* s_runs = s_ids + kTileM;                             // its runs' adapters
+  int* s_list = s_runs + kTileM;                            // its distinct adapters
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
   uint64_t* full = bars;                   // leader: both CTAs' operands landed
-  uint64_t* empty = full + 6;              // chunk's MMAs done (both CTAs)
-  uint64_t* acc_full = empty + 6;          // [2] tile's MMAs done (both CTAs)
+  uint64_t* empty = full + 7;              // chunk's MMAs done (both CTAs)
+  uint64_t* acc_full = empty + 7;          // [2] tile's MMAs done (both CTAs)
   uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
-  uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs wrote an adapter chunk
-  uint64_t* lora_empty = lora_full + 1;    // adapter chunk's MMAs done (both CTAs)
-  uint64_t* list_full = lora_empty + 1;    // [2] the tile's adapter steps are known (own CTA)
+  uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs' adapter stage is there
+  uint64_t* lora_empty = lora_full + kLoraStages;   // adapter stage's MMAs done (both CTAs)
+  uint64_t* list_full = lora_empty + kLoraStages;   // [2] the tile's adapter stages are known (own CTA)
   uint64_t* drain = list_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -144,13 +184,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[i], 8);
       mbar_init(&list_full[i], 1);
     }
-    mbar_init(lora_full, 2);
-    mbar_init(lora_empty, 1);
+    for (int i = 0; i < kLoraStages; ++i) {
+      mbar_init(&lora_full[i], 2);
+      mbar_init(&lora_empty[i], 1);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.mx);
     tma_prefetch_desc(&p.mw);
+    if (kLora) tma_prefetch_desc(&p.mb);
   }
   if (warp == 1) tmem_alloc2(tmem_slot, kTmemCols);
   tc_fence_before();
@@ -161,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const int nk = p.a.K / 64;
   const int half = p.bn >> 1;
-  const int rb = (p.a.rank + 15) >> 4;   // 16-column steps per adapter and part
+  const int rb = (p.a.rank + 15) >> 4;   // stages per adapter
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA, own halves
@@ -197,12 +240,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const uint32_t acc = tmem + 256 * (it & 1);
-        int steps = 0;
+        int nl = 0;
         if (kLora) {
           if (!(ok = warp_wait(&list_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 81))) break;
-          steps = s_steps[it & 1];
+          nl = s_steps[it & 1];
         }
-        const int nl = (steps + 3) >> 2;
         int j = 0;
         if (!(ok = warp_wait(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
         tc_fence_after();
@@ -219,16 +261,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma2_commit_both(&empty[s]);
           }
           __syncwarp();
-          // the adapter chunks that are due, evenly among the others
-          while (kLora && j < nl && c + 1 >= ((j + 1) * nk) / (nl + 1)) {
-            if (!(ok = warp_wait(lora_full, lcnt & 1, abort_flag, p.err, 84))) break;
+          // the adapter stages that are due, evenly among the second half's
+          // chunks (fixed places: the sums' order is that of every run)
+          while (kLora && j < nl && c + 1 >= nk / 2 + ((j + 1) * (nk - nk / 2)) / (nl + 1)) {
+            const int ls = lcnt % kLoraStages;
+            if (!(ok = warp_wait(&lora_full[ls], (lcnt / kLoraStages) & 1, abort_flag, p.err, 84))) break;
             tc_fence_after();
             if (elect_one_sync()) {
-              const uint32_t ab = smem_u32(lora_a), bb = smem_u32(lora_b);
-              const int n = min(4, steps - 4 * j);
-              for (int kk = 0; kk < n; ++kk)
-                mma2_f16_ss(acc, smem_desc_sw128(ab + 32 * kk), smem_desc_sw128(bb + 32 * kk), idesc_l, 1);
-              mma2_commit_both(lora_empty);
+              const uint32_t base = smem_u32(lora + ls * kLoraStageBytes);
+              const uint64_t bd = smem_desc_sw32(base + 2 * kLoraTile);
+              mma2_f16_ss(acc, smem_desc_sw32(base), bd, idesc_l, 1);
+              mma2_f16_ss(acc, smem_desc_sw32(base + kLoraTile), bd, idesc_l, 1);
+              mma2_commit_both(&lora_empty[ls]);
             }
             __syncwarp();
             ++j;
@@ -250,7 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp < 6) {
     // ------------------------------------------------- adapters' K columns
     if (kLora) {
-      const int i = threadIdx.x - 64;   // 0..127: A row and B row of this thread
+      const int i = threadIdx.x - 64;   // 0..127: this thread's A row
+      int r0, r1;
       uint32_t lcnt = 0, it = 0;
       bool ok = true;
       const uint32_t lora_full_l = leader_addr(lora_full);
@@ -261,82 +306,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         s_ids[i] = id0;
         s_ids[128 + i] = id1;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        unsigned first[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int pos = i + 128 * q, id = q ? id1 : id0;
-          bool is = id >= 0 && (pos == 0 || s_ids[pos - 1] != id);
-          for (int e = 0; is && e < pos; ++e) is = s_ids[e] != id;
-          first[q] = __ballot_sync(0xffffffffu, is);
-          if (lane == 0) s_cnt[4 * q + (i >> 5)] = __popc(first[q]);
-        }
+        // where an adapter's run of tokens starts, then its first run
+        const bool st0 = id0 >= 0 && (i == 0 || s_ids[i - 1] != id0);
+        const bool st1 = id1 >= 0 && s_ids[127 + i] != id1;
+        const int runs = rank_of(st0, st1, i, s_cnt, r0, r1);
+        if (st0) s_runs[r0] = id0;
+        if (st1) s_runs[r1] = id1;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        int nad = 0;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          if ((w & 3) == (i >> 5) && ((first[w >> 2] >> lane) & 1u))
-            s_list[nad + __popc(first[w >> 2] & ((1u << lane) - 1u))] = w < 4 ? id0 : id1;
-          nad += s_cnt[w];
-        }
-        const int steps = 2 * rb * nad, nl = (steps + 3) >> 2;
+        bool f0 = i < runs, f1 = 128 + i < runs;
+        const int ru0 = f0 ? s_runs[i] : -1, ru1 = f1 ? s_runs[128 + i] : -1;
+        const int upto = f1 ? 128 + i : i;
+        if (f0)
+          for (int e = 0; e < upto; e += 4) {
+            const int4 o = *reinterpret_cast<const int4*>(s_runs + e);
+            f0 &= !((o.x == ru0 && e < i) || (o.y == ru0 && e + 1 < i) || (o.z == ru0 && e + 2 < i) ||
+                    (o.w == ru0 && e + 3 < i));
+            f1 &= !((o.x == ru1 && e < upto) || (o.y == ru1 && e + 1 < upto) ||
+                    (o.z == ru1 && e + 2 < upto) || (o.w == ru1 && e + 3 < upto));
+          }
+        const int nad = rank_of(f0, f1, i, s_cnt, r0, r1);
+        if (f0) s_list[r0] = ru0;
+        if (f1) s_list[r1] = ru1;
+        const int nl = rb * nad;
         // the count of two tiles ago has been read once that tile is done
         if (it >= 2) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
         if (!(ok = bar_and(ok))) break;
         if (i == 0) {
-          s_steps[it & 1] = steps;
+          s_steps[it & 1] = nl;
           mbar_arrive(&list_full[it & 1]);
         }
         const int my_id = rank ? id1 : id0;
         const float* hrow = p.a.h + (size_t)min(m0 + 128 * (int)rank + i, p.a.T - 1) * p.a.rank;
-        const int n = n0 + half * (int)rank + i;
-        const bool brow = i < half && n < p.a.N;
-        for (int j = 0; j < nl && ok; ++j, ++lcnt) {
-          uint32_t va[4][8], vb[4][8];
+        // stage j: columns 16 (j % rb) .. + 15 of adapter j / rb of the list;
+        // this thread's h is loaded a stage ahead
+        float4 v[4], nv[4];
+        auto load_h = [&](int j) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int st = 4 * j + kk;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) va[kk][e] = vb[kk][e] = 0u;
-            if (st >= steps) continue;
-            const int ad = s_list[st / (2 * rb)], rem = st % (2 * rb);
-            const int blk = rem >= rb ? rem - rb : rem;
-            const bool two = 16 * blk + 16 <= p.a.rank;   // else the last 8 columns are zero
-            if (ad == my_id) {
-              const float4* h4 = reinterpret_cast<const float4*>(hrow + 16 * blk);
-              float4 v[4];
-              const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-              v[0] = __ldcg(h4);
-              v[1] = __ldcg(h4 + 1);
-              v[2] = two ? __ldcg(h4 + 2) : z;
-              v[3] = two ? __ldcg(h4 + 3) : z;
-              split_h(v, rem >= rb, va[kk]);
-            }
-            if (brow) {
-              const uint4* b4 = reinterpret_cast<const uint4*>(
-                  p.a.lb + ((size_t)ad * p.a.N + n) * p.a.rank + 16 * blk);
-              const uint4 x0 = __ldg(b4);
-              const uint4 x1 = two ? __ldg(b4 + 1) : make_uint4(0u, 0u, 0u, 0u);
-              vb[kk][0] = x0.x; vb[kk][1] = x0.y; vb[kk][2] = x0.z; vb[kk][3] = x0.w;
-              vb[kk][4] = x1.x; vb[kk][5] = x1.y; vb[kk][6] = x1.z; vb[kk][7] = x1.w;
+          for (int e = 0; e < 4; ++e) nv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < nl && s_list[j / rb] == my_id) {
+            const int c = 16 * (j % rb);
+            const float4* h4 = reinterpret_cast<const float4*>(hrow + c);
+            nv[0] = __ldcg(h4);
+            nv[1] = __ldcg(h4 + 1);
+            if (c + 16 <= p.a.rank) {
+              nv[2] = __ldcg(h4 + 2);
+              nv[3] = __ldcg(h4 + 3);
             }
           }
-          if (lcnt >= 1) ok = warp_wait(lora_empty, (lcnt - 1) & 1, abort_flag, p.err, 86);
+        };
+        load_h(0);
+        for (int j = 0; j < nl; ++j, ++lcnt) {
+          const int ls = lcnt % kLoraStages;
+          uint8_t* stage = lora + ls * kLoraStageBytes;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = nv[e];
+          load_h(j + 1);
+          if (lcnt >= kLoraStages)
+            ok = warp_wait(&lora_empty[ls], ((lcnt / kLoraStages) & 1) ^ 1, abort_flag, p.err, 86);
           if (!(ok = bar_and(ok))) break;
+          const uint32_t full_l = leader_addr(&lora_full[ls]);
+          if (i == 0)
+            tma_load_3d_pair(stage + 2 * kLoraTile, &p.mb, 16 * (j % rb), n0 + half * (int)rank,
+                             s_list[j / rb], full_l);
+          const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                               v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t off = i * 128 + (((2 * kk + q) ^ (i & 7)) << 4);
-              *reinterpret_cast<uint4*>(lora_a + off) =
-                  make_uint4(va[kk][4 * q], va[kk][4 * q + 1], va[kk][4 * q + 2], va[kk][4 * q + 3]);
-              if (i < half)
-                *reinterpret_cast<uint4*>(lora_b + off) =
-                    make_uint4(vb[kk][4 * q], vb[kk][4 * q + 1], vb[kk][4 * q + 2], vb[kk][4 * q + 3]);
-            }
+          for (int e = 0; e < 8; ++e) {
+            hi[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            lo[e] = pack_bf16x2(f[2 * e] - bf16_lo(hi[e]), f[2 * e + 1] - bf16_hi(hi[e]));
+          }
+          uint8_t* row = stage + i * 32;
+          const int sw = ((i >> 2) & 1) << 4;
+          *reinterpret_cast<uint4*>(row + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(row + (16 ^ sw)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          *reinterpret_cast<uint4*>(row + kLoraTile + sw) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(row + kLoraTile + (16 ^ sw)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (i == 0) arrive_cluster_shared(lora_full_l);
+          if (i == 0) {
+            if (leader) mbar_arrive_expect_tx(&lora_full[ls], 2u * (uint32_t)half * 32u);
+            else arrive_cluster_shared(full_l);
+          }
         }
+        // (the next tile rewrites the list: every thread has read it)
+        if (!bar_and(ok)) break;
+      }
+      if (!ok) {   // the copies in flight land (see above)
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
       }
     }
   } else {
@@ -419,6 +477,7 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   lin::Params p;
   p.mx = mx;
   p.mw = mw;
+  if (a.la && !encode_lora_b(&p.mb, a.lb, a.n_adapters, a.N, a.rank, bn / 2)) return cudaErrorInvalidValue;
   p.a = a;
   p.bn = bn;
   p.mt = (a.T + lin::kTileM - 1) / lin::kTileM;

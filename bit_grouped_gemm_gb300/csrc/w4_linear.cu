@@ -219,104 +219,136 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const LinearArgs a, c
 }
 
 // ---------------------------------------------------------------------------
-// Larger batches, first launch. CTAs [0, nw): 8192 packed weights each, as
-// fp16 in perm8 order. The others: 16 tokens each, x as fp16 rows in perm8
-// order and, for every adapter among the 16 tokens, h on mma.sync (bf16, the
-// 8 warps every 8th block of 32 K, their sums added in a fixed order). A
-// lane's 16 bytes of x are at once what it converts and its fragment: the K
-// order inside a block of 32 is the same for x and A, so it need not be the
-// MMA's.
+// Larger batches, first launch, in clusters of 4 CTAs. The first nx CTAs are
+// token CTAs (they take longer): a cluster takes 32 tokens, each of its CTAs a
+// quarter of K. A CTA writes its part of x as fp16 rows in perm8 order and
+// keeps it in shared memory as bf16; then its 8 warps take jobs of (adapter
+// among the 32 tokens, 8 ranks) on mma.sync, each over the CTA's whole part of
+// K, and put the rows of the adapter's own tokens into shared memory. The
+// cluster adds its CTAs' sums in order, over distributed shared memory, into h.
+// (One CTA per 16 tokens that went through the adapters one by one, its warps
+// splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
+// 16 adapters: one chain of L2 round trips per adapter.)
+// The other CTAs rebuild 16384 packed weights each as fp16 in perm8 order.
 // ---------------------------------------------------------------------------
-constexpr int kPrepWords = 1024;   // packed words per weight CTA
+constexpr int kPrepTok = 32;
+constexpr int kPrepSplit = 4;
+constexpr int kPrepWords = 2048;   // packed words per weight CTA
 
-__global__ void __launch_bounds__(256) linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16,
-                                                          uint16_t* __restrict__ w16, int nw,
-                                                          const DevErr err) {
-  __shared__ float red[8][16][33];
-  pdl_begin();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if ((int)blockIdx.x < nw) {
-    const long long words = (long long)a.N * (a.K / 8);
-    bool bad = false;
+// K columns of a token CTA (a multiple of 32), and bytes of a row of its tile
+// (64 more: 8 lanes of one 16-byte load then touch all banks)
+__host__ __device__ inline int prep_cols(int K) { return (K / 32 + kPrepSplit - 1) / kPrepSplit * 32; }
+__host__ __device__ inline int prep_row_bytes(int K) { return prep_cols(K) * 2 + 64; }
+
+__device__ __forceinline__ void prep_weights(const LinearArgs& a, uint16_t* __restrict__ w16, int cta,
+                                             const DevErr& err) {
+  const long long words = (long long)a.N * (a.K / 8);
+  bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kPrepWords / 256; ++i) {
-      const long long wi = (long long)blockIdx.x * kPrepWords + 256 * i + tid;
-      if (wi < words) {
-        const uint32_t s = __ldg(a.w.s + (wi >> 3)), b = __ldg(a.w.b + (wi >> 3));
-        bad |= sb_out_of_range(s, b);
-        uint32_t o[4];
-        dequant_word_f16_perm8(__ldg(a.w.q + wi), __half2half2(__float2half_rn(bf16_to_f32((uint16_t)s))),
-                               __half2half2(__float2half_rn(bf16_to_f32((uint16_t)b))), o);
-        reinterpret_cast<uint4*>(w16)[wi] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+  for (int i = 0; i < kPrepWords / 256; ++i) {
+    const long long wi = (long long)cta * kPrepWords + 256 * i + threadIdx.x;
+    if (wi < words) {
+      const uint32_t s = __ldg(a.w.s + (wi >> 3)), b = __ldg(a.w.b + (wi >> 3));
+      bad |= sb_out_of_range(s, b);
+      uint32_t o[4];
+      dequant_word_f16_perm8(__ldg(a.w.q + wi), __half2half2(__float2half_rn(bf16_to_f32((uint16_t)s))),
+                             __half2half2(__float2half_rn(bf16_to_f32((uint16_t)b))), o);
+      reinterpret_cast<uint4*>(w16)[wi] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    report_range_warp(err, bad);
+  }
+  report_range_warp(err, bad);
+}
+
+__global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256)
+    linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
+                       const DevErr err) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_id[kPrepTok], s_list[kPrepTok];
+  pdl_begin();
+  if ((int)blockIdx.x >= nx) {
+    prep_weights(a, w16, (int)blockIdx.x - nx, err);
     return;
   }
-  const int t0 = ((int)blockIdx.x - nw) * 16;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int part_k = (int)blockIdx.x % kPrepSplit, t0 = (int)blockIdx.x / kPrepSplit * kPrepTok;
+  const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
+  const int row_bytes = prep_row_bytes(a.K);
+  float* part = reinterpret_cast<float*>(smem + kPrepTok * row_bytes);   // [token][rank]
+  if (tid < kPrepTok) s_id[tid] = adapter_of(a, t0 + tid);
+  // x: 8 columns at a time
   uint32_t over = 0u;
-  const int my_id = adapter_of(a, t0 + (lane & 15));
-  unsigned todo = __ballot_sync(0xffffffffu, lane < 16 && my_id >= 0);
+  const int vec = kn / 8;
+#pragma unroll 4
+  for (int i = tid; i < kPrepTok * vec; i += 256) {
+    const int tl = i / vec, k = 8 * (i - tl * vec), t = t0 + tl;
+    if (t < a.T) {
+      const Raw8 v = load8(a, t, k0 + k);
+      *reinterpret_cast<uint4*>(x16 + (size_t)t * a.K + k0 + k) = f16x8_to_perm8(to_f16(a, v, over));
+      if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = to_bf16(a, v);
+    } else if (a.la) {
+      *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  report_range_warp(err, over != 0u);
+  if (!a.la) return;
+  __syncthreads();
+  // the tokens' distinct adapters, in order (every warp alike; warp 0 lists)
+  const int id = s_id[lane];
+  bool first = id >= 0;
+  for (int j = 0; j < 31; ++j) {
+    const int o = __shfl_sync(0xffffffffu, id, j);
+    if (j < lane && o == id) first = false;
+  }
+  const unsigned firsts = __ballot_sync(0xffffffffu, first);
+  if (warp == 0 && first) s_list[__popc(firsts & ((1u << lane) - 1u))] = id;
+  __syncthreads();
+  const int tiles = a.rank / 8, jobs = __popc(firsts) * tiles;
   const int g = lane >> 2, q = lane & 3;
-  const int ta = t0 + g, tb = t0 + g + 8;
-  bool convert = true;
-  do {
-    const int cur = todo ? __shfl_sync(0xffffffffu, my_id, __ffs(todo) - 1) : -1;
-    const unsigned mine = __ballot_sync(0xffffffffu, lane < 16 && my_id == cur);
-    todo &= ~mine;
-    for (int rc = 0; rc == 0 || (cur >= 0 && rc < a.rank); rc += 32) {
-      float acc[4][4];
+  for (int job = warp; job < jobs; job += 8) {
+    const int ad = s_list[job / tiles], r0 = 8 * (job % tiles);
+    const uint16_t* ar = a.la + ((size_t)ad * a.rank + r0 + g) * a.K + k0 + 8 * q;
+    const uint8_t* xr = smem + g * row_bytes + 16 * q;
+    float acc[2][4] = {};
+#pragma unroll 8
+    for (int kb = 0; kb < kn; kb += 32) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(ar + kb));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 2
-      for (int kb = 32 * warp; kb < a.K; kb += 256) {
-        const int k = kb + 8 * q;
-        Raw8 va{make_uint4(0u, 0u, 0u, 0u)}, vb{make_uint4(0u, 0u, 0u, 0u)};
-        if (ta < a.T) va = load8(a, ta, k);
-        if (tb < a.T) vb = load8(a, tb, k);
-        if (convert) {
-          if (ta < a.T)
-            *reinterpret_cast<uint4*>(x16 + (size_t)ta * a.K + k) = f16x8_to_perm8(to_f16(a, va, over));
-          if (tb < a.T)
-            *reinterpret_cast<uint4*>(x16 + (size_t)tb * a.K + k) = f16x8_to_perm8(to_f16(a, vb, over));
-        }
-        if (cur >= 0) {
-          const uint4 xa = to_bf16(a, va), xb = to_bf16(a, vb);
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            const int r = rc + 8 * nt;
-            if (r < a.rank) {
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-                  a.la + ((size_t)cur * a.rank + r + g) * a.K + k));
-              mma_bf16(acc[nt], xa.x, xb.x, xa.y, xb.y, w.x, w.y);
-              mma_bf16(acc[nt], xa.z, xb.z, xa.w, xb.w, w.z, w.w);
-            }
-          }
-        }
-      }
-      convert = false;
-      if (cur < 0) break;
-      __syncthreads();   // the last block's sums have been read
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[warp][g + 8 * (j >> 1)][8 * nt + 2 * q + (j & 1)] = acc[nt][j];
-      __syncthreads();
-      const float sc = a.lscale ? __ldg(a.lscale + cur) : 1.f;
-      for (int o = tid; o < 16 * 32; o += 256) {
-        const int t = o >> 5, r = o & 31;
-        if (((mine >> t) & 1u) && rc + r < a.rank) {
-          float v = 0.f;
-#pragma unroll
-          for (int w = 0; w < 8; ++w) v += red[w][t][r];
-          a.h[(size_t)(t0 + t) * a.rank + rc + r] = v * sc;
-        }
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint4 xa = *reinterpret_cast<const uint4*>(xr + (16 * mt) * row_bytes + 2 * kb);
+        const uint4 xb = *reinterpret_cast<const uint4*>(xr + (16 * mt + 8) * row_bytes + 2 * kb);
+        mma_bf16(acc[mt], xa.x, xb.x, xa.y, xb.y, w.x, w.y);
+        mma_bf16(acc[mt], xa.z, xb.z, xa.w, xb.w, w.z, w.w);
       }
     }
-  } while (todo);
-  report_range_warp(err, over != 0u);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tl = 16 * mt + 8 * h + g;
+        if (s_id[tl] == ad)
+          *reinterpret_cast<float2*>(part + tl * a.rank + r0 + 2 * q) =
+              make_float2(acc[mt][2 * h], acc[mt][2 * h + 1]);
+      }
+  }
+  // the cluster's sums, each CTA a quarter of the entries
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int n = kPrepTok * a.rank;
+  for (int i = part_k * 256 + tid; i < n; i += 256 * kPrepSplit) {
+    const int tl = i / a.rank, ad = s_id[tl];
+    if (ad < 0) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int c = 0; c < kPrepSplit; ++c) {
+      uint32_t addr;
+      float o;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(part + i)), "r"(c));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(addr) : "memory");
+      v += o;
+    }
+    a.h[(size_t)(t0 + tl) * a.rank + i % a.rank] = v * (a.lscale ? __ldg(a.lscale + ad) : 1.f);
+  }
+  // no CTA leaves while another still reads its sums
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace
@@ -339,8 +371,13 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
                                cudaStream_t st) {
   const long long words = (long long)a.N * (a.K / 8);
-  const int nw = (int)((words + kPrepWords - 1) / kPrepWords);
-  return launch_pdl(linear_prep_kernel, dim3(nw + (a.T + 15) / 16), dim3(256), 0, st, a, x16, w16, nw, err);
+  int nw = (int)((words + kPrepWords - 1) / kPrepWords);
+  nw = (nw + kPrepSplit - 1) / kPrepSplit * kPrepSplit;   // whole clusters
+  const int nx = (a.T + kPrepTok - 1) / kPrepTok * kPrepSplit;
+  const int smem = a.la ? kPrepTok * (prep_row_bytes(a.K) + a.rank * 4) : 0;
+  cudaError_t e = cudaFuncSetAttribute(linear_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(linear_prep_kernel, dim3(nx + nw), dim3(256), (size_t)smem, st, a, x16, w16, nx, err);
 }
 
 }  // namespace moe
