@@ -208,10 +208,10 @@ moe_status moe_linear_forward(moe_linear_t p, const void* x, int x_type, long lo
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (T <= kLinearSmallT) {
-    if (lora) e = launch_lora_shrink(a, st);
-    if (e == cudaSuccess) e = launch_linear_small(a, p->err(), st);
+    e = launch_linear_small(a, p->err(), st);
   } else {
-    e = launch_linear_prep(a, p->at<uint16_t>(p->L.x16), p->at<uint16_t>(p->L.w16), p->err(), st);
+    e = launch_linear_prep(a, p->at<uint16_t>(p->L.x16), p->at<uint16_t>(p->L.w16), p->err(),
+                           p->num_sms, st);
     if (e == cudaSuccess) {
       const int bn = linear_tile_n(T, N, p->num_sms);
       e = launch_linear_tc(a, p->mx, p->mw[bn / 32 - 1], bn, p->err(), p->num_sms, st);

@@ -26,23 +26,24 @@ namespace lin {
 constexpr int kThreads = 320;             // TMA, MMA, 4 adapter, 4 epilogue warps
 constexpr int kTileM = 256;
 constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
-constexpr int kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kTmemCols = 512;
 
-// An adapter stage: h and its rest (A, 128 rows x 16 bf16 each), B's rows.
-constexpr int kLoraStages = 2;
+// An adapter stage: h and its rest (A, 128 rows x 16 bf16 each), B's BN / 2
+// rows. Narrow tiles leave shared memory for more of them than the two of a
+// full tile, and need them: a pair has one such tile, whose adapters all come at
+// once.
 constexpr int kLoraTile = 128 * 32;
-constexpr int kLoraStageBytes = 3 * kLoraTile;
+constexpr int kMaxLoraStages = 8;
 
+// Shared memory: the ring of operand chunks, the adapter stages, ids and runs and
+// list of the tile's adapters, barriers.
+constexpr int kIdsBytes = 3 * kTileM * 4;
+constexpr int kBarBytes = 512;
+constexpr int kSmemMax = 227 * 1024 - 1024;   // less alignment slack
 template <bool kLora>
-struct Smem {
-  static constexpr int kStages = kLora ? 6 : 7;
-  static constexpr int kOffLora = kStages * kStageBytes;
-  static constexpr int kOffIds = kOffLora + (kLora ? kLoraStages * kLoraStageBytes : 0);
-  static constexpr int kOffBar = kOffIds + (kLora ? 3 * kTileM * 4 : 0);
-  static constexpr int kBytes = kOffBar + 512 + 1024;   // barriers, alignment slack
-};
-static_assert(Smem<true>::kBytes <= 227 * 1024 && Smem<false>::kBytes <= 227 * 1024, "shared memory");
+__host__ __device__ constexpr int stages() { return kLora ? 6 : 7; }
+inline int stage_bytes(int bn) { return kOpBytes + (bn / 2) * 128; }
+inline int lora_stage_bytes(int bn) { return 2 * kLoraTile + (bn / 2) * 32; }
 
 struct Params {
   CUtensorMap mx;       // x16 [rows][K], boxes 64 x 128
@@ -50,6 +51,7 @@ struct Params {
   CUtensorMap mb;       // B [n][N][r], boxes 16 x BN / 2 x 1, 32-byte swizzle
   LinearArgs a;
   int bn, mt, tiles;    // tile width, token tiles, all tiles
+  int stage_bytes, lora_stages, lora_stage_bytes;
   DevErr err;
 };
 
@@ -146,23 +148,22 @@ __device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra,
 template <bool kLora>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ Params p) {
-  using S = Smem<kLora>;
-  constexpr int kStages = S::kStages;
+  constexpr int kStages = stages<kLora>();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
-  uint8_t* lora = smem + S::kOffLora;
-  int* s_ids = reinterpret_cast<int*>(smem + S::kOffIds);   // the tile's adapter per token
+  uint8_t* lora = smem + kStages * p.stage_bytes;
+  int* s_ids = reinterpret_cast<int*>(lora + p.lora_stages * p.lora_stage_bytes);   // adapter per token
   int* s_runs = s_ids + kTileM;                             // its runs' adapters
   int* s_list = s_runs + kTileM;                            // its distinct adapters
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ids + (kLora ? 3 * kTileM : 0));
   uint64_t* full = bars;                   // leader: both CTAs' operands landed
   uint64_t* empty = full + 7;              // chunk's MMAs done (both CTAs)
   uint64_t* acc_full = empty + 7;          // [2] tile's MMAs done (both CTAs)
   uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
   uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs' adapter stage is there
-  uint64_t* lora_empty = lora_full + kLoraStages;   // adapter stage's MMAs done (both CTAs)
-  uint64_t* list_full = lora_empty + kLoraStages;   // [2] the tile's adapter stages are known (own CTA)
+  uint64_t* lora_empty = lora_full + kMaxLoraStages;   // adapter stage's MMAs done (both CTAs)
+  uint64_t* list_full = lora_empty + kMaxLoraStages;   // [2] the tile's adapter stages are known (own CTA)
   uint64_t* drain = list_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -184,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[i], 8);
       mbar_init(&list_full[i], 1);
     }
-    for (int i = 0; i < kLoraStages; ++i) {
+    for (int i = 0; i < p.lora_stages; ++i) {
       mbar_init(&lora_full[i], 2);
       mbar_init(&lora_empty[i], 1);
     }
@@ -200,7 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();   // barriers and TMEM of both CTAs, before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_begin();          // operands come from the launch before
+  // What the launch before wrote (x16, W16, h) is read after pdl_wait; the
+  // adapters' ids are older: that launch waited for all before it.
 
   const int nk = p.a.K / 64;
   const int half = p.bn >> 1;
@@ -208,6 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA, own halves
+    pdl_begin();
     const uint32_t bytes = 2u * (kOpBytes + (uint32_t)half * 128u);   // of both CTAs
     uint32_t cnt = 0;
     bool ok = true;
@@ -218,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int s = cnt % kStages;
         if (!(ok = warp_wait(&empty[s], ((cnt / kStages) & 1) ^ 1, abort_flag, p.err, 80))) break;
         if (elect_one_sync()) {
-          uint8_t* dst = smem + s * kStageBytes;
+          uint8_t* dst = smem + s * p.stage_bytes;
           if (leader) mbar_arrive_expect_tx(&full[s], bytes);
           tma_load_2d_pair(dst, &p.mx, 64 * c, m0, leader_addr(&full[s]));
           tma_load_2d_pair(dst + kOpBytes, &p.mw, 64 * c, n0, leader_addr(&full[s]));
@@ -255,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&full[s], (cnt / kStages) & 1, abort_flag, p.err, 83))) break;
           tc_fence_after();
           if (elect_one_sync()) {
-            const uint32_t base = smem_u32(smem + s * kStageBytes);
+            const uint32_t base = smem_u32(smem + s * p.stage_bytes);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma2_f16_ss(acc, smem_desc_sw128(base + 32 * kk),
@@ -266,11 +269,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // the adapter stages that are due, evenly among the second half's
           // chunks (fixed places: the sums' order is that of every run)
           while (kLora && c + 1 >= due) {
-            const int ls = lcnt % kLoraStages;
-            if (!(ok = warp_wait(&lora_full[ls], (lcnt / kLoraStages) & 1, abort_flag, p.err, 84))) break;
+            const int ls = lcnt % p.lora_stages;
+            if (!(ok = warp_wait(&lora_full[ls], (lcnt / p.lora_stages) & 1, abort_flag, p.err, 84))) break;
             tc_fence_after();
             if (elect_one_sync()) {
-              const uint32_t base = smem_u32(lora + ls * kLoraStageBytes);
+              const uint32_t base = smem_u32(lora + ls * p.lora_stage_bytes);
               const uint64_t bd = smem_desc_sw32(base + 2 * kLoraTile);
               mma2_f16_ss(acc, smem_desc_sw32(base), bd, idesc_l, 1);
               mma2_f16_ss(acc, smem_desc_sw32(base + kLoraTile), bd, idesc_l, 1);
@@ -357,15 +360,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         };
+        if (it == 0) pdl_wait();
         load_h(0);
         for (int j = 0; j < nl; ++j, ++lcnt) {
-          const int ls = lcnt % kLoraStages;
-          uint8_t* stage = lora + ls * kLoraStageBytes;
+          const int ls = lcnt % p.lora_stages;
+          uint8_t* stage = lora + ls * p.lora_stage_bytes;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = nv[e];
           load_h(j + 1);
-          if (lcnt >= kLoraStages)
-            ok = warp_wait(&lora_empty[ls], ((lcnt / kLoraStages) & 1) ^ 1, abort_flag, p.err, 86);
+          if (lcnt >= (uint32_t)p.lora_stages)
+            ok = warp_wait(&lora_empty[ls], ((lcnt / p.lora_stages) & 1) ^ 1, abort_flag, p.err, 86);
           if (!(ok = bar_and(ok))) break;
           const uint32_t full_l = leader_addr(&lora_full[ls]);
           if (i == 0)
@@ -402,6 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    pdl_wait();   // (y may still be read by an older launch)
     const int quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t acc_empty_l = leader_addr(acc_empty);
@@ -488,12 +493,18 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   p.err = err;
   int pairs = num_sms / 2;
   if (pairs > p.tiles) pairs = p.tiles;
-  auto go = [&](auto kern, int smem) {
+  p.stage_bytes = lin::stage_bytes(bn);
+  p.lora_stage_bytes = lin::lora_stage_bytes(bn);
+  const int ns = a.la ? lin::stages<true>() : lin::stages<false>();
+  const int fixed = ns * p.stage_bytes + (a.la ? lin::kIdsBytes : 0) + lin::kBarBytes;
+  p.lora_stages = a.la ? (lin::kSmemMax - fixed) / p.lora_stage_bytes : 0;
+  if (p.lora_stages > lin::kMaxLoraStages) p.lora_stages = lin::kMaxLoraStages;
+  const int smem = fixed + p.lora_stages * p.lora_stage_bytes + 1024;
+  auto go = [&](auto kern) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return e != cudaSuccess ? e : launch_pdl(kern, dim3(2 * pairs), dim3(lin::kThreads), smem, st, p);
   };
-  return a.la ? go(lin::linear_tc_kernel<true>, lin::Smem<true>::kBytes)
-              : go(lin::linear_tc_kernel<false>, lin::Smem<false>::kBytes);
+  return a.la ? go(lin::linear_tc_kernel<true>) : go(lin::linear_tc_kernel<false>);
 }
 
 }  // namespace moe

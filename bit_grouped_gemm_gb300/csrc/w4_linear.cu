@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LinearArgs a) {
   float s = 0.f;
   if (id >= 0) {
     const uint16_t* ar = a.la + ((size_t)id * a.rank + r) * a.K;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 8 * lane; k < a.K; k += 256) {
       const uint4 xv = to_bf16(a, load8(a, t, k));
       const uint4 av = __ldg(reinterpret_cast<const uint4*>(ar + k));
@@ -113,18 +113,24 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LinearArgs a) {
 
 // ---------------------------------------------------------------------------
 // Decode batches, the product: a CTA takes 16 weight rows and all tokens, its
-// 8 warps every 8th group of 64 K each. The packed words are the MMA's A rows:
-// lane (g, q) rebuilds the 16 weights of words 2q and 2q + 1 of rows g and
-// g + 8, in the order in which the nibbles come out (perm8), and takes the
-// same K positions of token g's row as B. Weights are loaded before the wait
-// for the launch before; x too when that launch is this call's own (it is then
-// older). The warps' sums are added in a fixed order through shared memory.
+// 16 warps every 16th group of 64 K each. The packed words are the MMA's A
+// rows: lane (g, q) rebuilds the 16 weights of words 2q and 2q + 1 of rows g
+// and g + 8, in the order in which the nibbles come out (perm8), and takes the
+// same K positions of token g's row as B. The warps' sums are added in a fixed
+// order through shared memory. Weights are loaded before the wait for the
+// launch before. With adapters that launch is lora_shrink_kernel, and x and the
+// adapters' ids are older than it: all that does not need h runs beside it.
+// (h taken in this launch instead, once per cluster of 8 CTAs and shared over
+// distributed shared memory, was slower: 6.6 against 4.7 us at one token of
+// 2048 x 2048 and rank 16, 12.4 against 6.6 us at 16. Against 8 warps of twice
+// the groups, 16 warps: 3.2 against 4.6 us at one token without adapters.)
 // ---------------------------------------------------------------------------
 constexpr int kSmRows = 16;
+constexpr int kSmWarps = 16;
 
 template <int NT>   // tiles of 8 tokens
-__global__ void __launch_bounds__(256) linear_small_kernel(const LinearArgs a, const DevErr err) {
-  __shared__ float red[8][kSmRows][8 * NT + 1];
+__global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const LinearArgs a, const DevErr err) {
+  __shared__ float red[kSmWarps][kSmRows][8 * NT + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int n0 = blockIdx.x * kSmRows, kg = a.K / 64;
@@ -136,13 +142,31 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const LinearArgs a, c
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   uint32_t over = 0u;
   bool bad = false, waited = a.la != nullptr;
-  constexpr int kAhead = 4;
-  for (int gb = warp; gb < kg; gb += 8 * kAhead) {
+  // This thread's output: row tid % 16 of token tid / 16. What its adapter adds
+  // is loaded ahead, up to 16 ranks, so that only h is left to come when the
+  // sums are done.
+  const int to = tid / kSmRows, no = n0 + tid % kSmRows;
+  int id = -1;
+  uint4 b0v = make_uint4(0u, 0u, 0u, 0u), b1v = b0v;
+  float xsc = 1.f;
+  auto ahead = [&] {
+    if (to >= a.T) return;
+    id = adapter_of(a, to);
+    if (a.x_scale) xsc = __ldcg(a.x_scale + to);
+    if (id >= 0 && no < a.N) {
+      const uint4* br = reinterpret_cast<const uint4*>(a.lb + ((size_t)id * a.N + no) * a.rank);
+      b0v = __ldg(br);
+      if (a.rank > 8) b1v = __ldg(br + 1);
+    }
+  };
+  if (waited) ahead();
+  constexpr int kAhead = 2;
+  for (int gb = warp; gb < kg || !waited; gb += kSmWarps * kAhead) {
     uint2 w0[kAhead], w1[kAhead];
     uint32_t s0[kAhead], s1[kAhead], b0[kAhead], b1[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int gr = gb + 8 * i;
+      const int gr = gb + kSmWarps * i;
       w0[i] = w1[i] = make_uint2(0u, 0u);
       s0[i] = s1[i] = b0[i] = b1[i] = 0u;
       if (gr < kg) {
@@ -155,12 +179,13 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const LinearArgs a, c
       }
     }
     if (!waited) {
-      pdl_wait();
+      pdl_begin();
       waited = true;
+      ahead();
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int gr = gb + 8 * i;
+      const int gr = gb + kSmWarps * i;
       if (gr >= kg) break;
       bad |= sb_out_of_range(s0[i], b0[i]) || sb_out_of_range(s1[i], b1[i]);
       const __half2 sa = __half2half2(__float2half_rn(bf16_to_f32((uint16_t)s0[i])));
@@ -184,38 +209,37 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const LinearArgs a, c
       }
     }
   }
-  if (!waited || a.la) pdl_wait();   // h; and every thread waits before it stores
-  pdl_trigger();
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 4; ++j) red[warp][g + 8 * (j >> 1)][8 * nt + 2 * q + (j & 1)] = acc[nt][j];
   if (__any_sync(0xffffffffu, over != 0u || bad) && lane == 0) atomicOr(err.word, DEVERR_RANGE);
   __syncthreads();
-  for (int o = tid; o < kSmRows * a.T; o += 256) {
-    const int t = o / kSmRows, r = o % kSmRows, n = n0 + r;
-    if (n >= a.N) continue;
-    float v = 0.f;
+  float v = 0.f;
+  if (to < 8 * NT) {
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += red[w][r][t];
-    const int id = adapter_of(a, t);
-    if (id >= 0) {
-      const uint4* br = reinterpret_cast<const uint4*>(a.lb + ((size_t)id * a.N + n) * a.rank);
-      const float4* hr = reinterpret_cast<const float4*>(a.h + (size_t)t * a.rank);
-      float e = 0.f;
-      for (int i = 0; i < a.rank / 8; ++i) {
-        const uint4 b = __ldg(br + i);
-        const float4 h0 = __ldcg(hr + 2 * i), h1 = __ldcg(hr + 2 * i + 1);
-        e = fmaf(h0.x, bf16_lo(b.x), fmaf(h0.y, bf16_hi(b.x), e));
-        e = fmaf(h0.z, bf16_lo(b.y), fmaf(h0.w, bf16_hi(b.y), e));
-        e = fmaf(h1.x, bf16_lo(b.z), fmaf(h1.y, bf16_hi(b.z), e));
-        e = fmaf(h1.z, bf16_lo(b.w), fmaf(h1.w, bf16_hi(b.w), e));
-      }
-      v += e;
-    }
-    if (a.x_scale) v *= __ldcg(a.x_scale + t);
-    a.y[t * a.y_ld + n] = f32_to_bf16(v);
+    for (int w = 0; w < kSmWarps; ++w) v += red[w][tid % kSmRows][to];
   }
+  if (a.la) pdl_begin();   // h
+  if (to >= a.T || no >= a.N) return;
+  if (id >= 0) {
+    const uint4* br = reinterpret_cast<const uint4*>(a.lb + ((size_t)id * a.N + no) * a.rank);
+    const float4* hr = reinterpret_cast<const float4*>(a.h + (size_t)to * a.rank);
+    float e = 0.f;
+    auto eight = [&](int c, const uint4& b) {
+      const float4 h0 = __ldcg(hr + 2 * c), h1 = __ldcg(hr + 2 * c + 1);
+      e = fmaf(h0.x, bf16_lo(b.x), fmaf(h0.y, bf16_hi(b.x), e));
+      e = fmaf(h0.z, bf16_lo(b.y), fmaf(h0.w, bf16_hi(b.y), e));
+      e = fmaf(h1.x, bf16_lo(b.z), fmaf(h1.y, bf16_hi(b.z), e));
+      e = fmaf(h1.z, bf16_lo(b.w), fmaf(h1.w, bf16_hi(b.w), e));
+    };
+    eight(0, b0v);
+    if (a.rank > 8) eight(1, b1v);
+#pragma unroll 2
+    for (int c = 2; c < a.rank / 8; ++c) eight(c, __ldg(br + c));
+    v += e;
+  }
+  a.y[to * a.y_ld + no] = f32_to_bf16(v * xsc);
 }
 
 // ---------------------------------------------------------------------------
@@ -259,7 +283,11 @@ __device__ __forceinline__ void prep_weights(const LinearArgs& a, uint16_t* __re
   report_range_warp(err, bad);
 }
 
-__global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256)
+// kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
+// where the launch has at most two CTAs per SM (1024 tokens of 2048 x 2048: 20.3
+// against 22.9 us for the call), slower beyond (4096 tokens: 40.2 against 35.9).
+template <bool kDeep>
+__global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
     linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
                        const DevErr err) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -274,50 +302,82 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256)
   const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
   const int row_bytes = prep_row_bytes(a.K);
   float* part = reinterpret_cast<float*>(smem + kPrepTok * row_bytes);   // [token][rank]
-  if (tid < kPrepTok) s_id[tid] = adapter_of(a, t0 + tid);
-  // x: 8 columns at a time
+  const int id = adapter_of(a, t0 + lane);   // every warp holds all 32 tokens' ids
+  // x: 8 columns at a time, kBatch loads in flight per thread
+  constexpr int kBatch = kDeep ? 8 : 4, kABatch = kDeep ? 16 : 8;
   uint32_t over = 0u;
-  const int vec = kn / 8;
-#pragma unroll 4
-  for (int i = tid; i < kPrepTok * vec; i += 256) {
+  const int vec = kn / 8, total = kPrepTok * vec;
+  auto put_x = [&](int i, const Raw8& v) {
     const int tl = i / vec, k = 8 * (i - tl * vec), t = t0 + tl;
-    if (t < a.T) {
-      const Raw8 v = load8(a, t, k0 + k);
+    if (t < a.T)
       *reinterpret_cast<uint4*>(x16 + (size_t)t * a.K + k0 + k) = f16x8_to_perm8(to_f16(a, v, over));
-      if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = to_bf16(a, v);
-    } else if (a.la) {
-      *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = make_uint4(0u, 0u, 0u, 0u);
+    if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = to_bf16(a, v);
+  };
+  auto get_x = [&](int i) {
+    Raw8 v{make_uint4(0u, 0u, 0u, 0u)};
+    if (i < total) {
+      const int tl = i / vec;
+      if (t0 + tl < a.T) v = load8(a, t0 + tl, k0 + 8 * (i - tl * vec));
     }
+    return v;
+  };
+  Raw8 xv[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) xv[j] = get_x(tid + 256 * j);
+  // meanwhile the tokens' distinct adapters, in order
+  int jobs = 0;
+  const int tiles = a.rank / 8;
+  if (a.la) {
+    bool first = id >= 0;
+#pragma unroll
+    for (int j = 0; j < 31; ++j) {
+      const int o = __shfl_sync(0xffffffffu, id, j);
+      if (j < lane && o == id) first = false;
+    }
+    const unsigned firsts = __ballot_sync(0xffffffffu, first);
+    if (warp == 0) {
+      s_id[lane] = id;
+      if (first) s_list[__popc(firsts & ((1u << lane) - 1u))] = id;
+    }
+    jobs = __popc(firsts) * tiles;
+  }
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (tid + 256 * j < total) put_x(tid + 256 * j, xv[j]);
+  for (int i0 = tid + 256 * kBatch; i0 < total; i0 += 256 * kBatch) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) xv[j] = get_x(i0 + 256 * j);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (i0 + 256 * j < total) put_x(i0 + 256 * j, xv[j]);
   }
   report_range_warp(err, over != 0u);
   if (!a.la) return;
   __syncthreads();
-  // the tokens' distinct adapters, in order (every warp alike; warp 0 lists)
-  const int id = s_id[lane];
-  bool first = id >= 0;
-  for (int j = 0; j < 31; ++j) {
-    const int o = __shfl_sync(0xffffffffu, id, j);
-    if (j < lane && o == id) first = false;
-  }
-  const unsigned firsts = __ballot_sync(0xffffffffu, first);
-  if (warp == 0 && first) s_list[__popc(firsts & ((1u << lane) - 1u))] = id;
-  __syncthreads();
-  const int tiles = a.rank / 8, jobs = __popc(firsts) * tiles;
   const int g = lane >> 2, q = lane & 3;
   for (int job = warp; job < jobs; job += 8) {
     const int ad = s_list[job / tiles], r0 = 8 * (job % tiles);
     const uint16_t* ar = a.la + ((size_t)ad * a.rank + r0 + g) * a.K + k0 + 8 * q;
     const uint8_t* xr = smem + g * row_bytes + 16 * q;
     float acc[2][4] = {};
-#pragma unroll 8
-    for (int kb = 0; kb < kn; kb += 32) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(ar + kb));
+    for (int kb0 = 0; kb0 < kn; kb0 += 32 * kABatch) {
+      uint4 w[kABatch];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint4 xa = *reinterpret_cast<const uint4*>(xr + (16 * mt) * row_bytes + 2 * kb);
-        const uint4 xb = *reinterpret_cast<const uint4*>(xr + (16 * mt + 8) * row_bytes + 2 * kb);
-        mma_bf16(acc[mt], xa.x, xb.x, xa.y, xb.y, w.x, w.y);
-        mma_bf16(acc[mt], xa.z, xb.z, xa.w, xb.w, w.z, w.w);
+      for (int j = 0; j < kABatch; ++j)
+        w[j] = kb0 + 32 * j < kn ? __ldg(reinterpret_cast<const uint4*>(ar + kb0 + 32 * j))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < kABatch; ++j) {
+        const int kb = kb0 + 32 * j;
+        if (kb < kn) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const uint4 xa = *reinterpret_cast<const uint4*>(xr + (16 * mt) * row_bytes + 2 * kb);
+            const uint4 xb = *reinterpret_cast<const uint4*>(xr + (16 * mt + 8) * row_bytes + 2 * kb);
+            mma_bf16(acc[mt], xa.x, xb.x, xa.y, xb.y, w[j].x, w[j].y);
+            mma_bf16(acc[mt], xa.z, xb.z, xa.w, xb.w, w[j].z, w[j].w);
+          }
+        }
       }
     }
 #pragma unroll
@@ -353,31 +413,35 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_lora_shrink(const LinearArgs& a, cudaStream_t st) {
-  return launch_pdl(lora_shrink_kernel, dim3((a.T * a.rank + 7) / 8), dim3(256), 0, st, a);
-}
-
 cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st) {
+  static_assert(kLinearSmallT <= 32, "one output per thread: 16 rows of at most 32 tokens");
+  if (a.la) {
+    const cudaError_t e = launch_pdl(lora_shrink_kernel, dim3((a.T * a.rank + 7) / 8), dim3(256), 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
   const int nt = (a.T + 7) / 8;
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3((a.N + kSmRows - 1) / kSmRows), dim3(256), 0, st, a, err);
+    return launch_pdl(kern, dim3((a.N + kSmRows - 1) / kSmRows), dim3(32 * kSmWarps), 0, st, a, err);
   };
-  return nt <= 1 ? go(linear_small_kernel<1>)
+  return nt <= 1   ? go(linear_small_kernel<1>)
          : nt <= 2 ? go(linear_small_kernel<2>)
-         : nt <= 4 ? go(linear_small_kernel<4>)
-                   : go(linear_small_kernel<8>);
+                   : go(linear_small_kernel<4>);
 }
 
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
-                               cudaStream_t st) {
+                               int num_sms, cudaStream_t st) {
   const long long words = (long long)a.N * (a.K / 8);
   int nw = (int)((words + kPrepWords - 1) / kPrepWords);
   nw = (nw + kPrepSplit - 1) / kPrepSplit * kPrepSplit;   // whole clusters
   const int nx = (a.T + kPrepTok - 1) / kPrepTok * kPrepSplit;
   const int smem = a.la ? kPrepTok * (prep_row_bytes(a.K) + a.rank * 4) : 0;
-  cudaError_t e = cudaFuncSetAttribute(linear_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(linear_prep_kernel, dim3(nx + nw), dim3(256), (size_t)smem, st, a, x16, w16, nx, err);
+  auto go = [&](auto kern) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess
+               ? e
+               : launch_pdl(kern, dim3(nx + nw), dim3(256), (size_t)smem, st, a, x16, w16, nx, err);
+  };
+  return nx + nw <= 2 * num_sms ? go(linear_prep_kernel<true>) : go(linear_prep_kernel<false>);
 }
 
 }  // namespace moe
