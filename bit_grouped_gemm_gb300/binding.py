@@ -147,6 +147,14 @@ def load_library(path: Optional[str] = None):
     return lib
 
 
+def _status(name: str, *args) -> None:
+    """Calls an entry point that returns a status."""
+    lib = _lib or load_library()
+    status = getattr(lib, name)(*args)
+    if status:
+        raise MoeError(status, name)
+
+
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -160,11 +168,17 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = _device = None
+
+
 def _current_stream() -> int:
     """Handle of torch's current stream (the raw query: building a Stream
     object for it takes 3 us a call)."""
-    from torch import _C
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    global _raw_stream, _device
+    if _raw_stream is None:
+        from torch import _C
+        _device, _raw_stream = _C._cuda_getDevice, _C._cuda_getCurrentRawStream
+    return _raw_stream(_device())
 
 
 def _stream(stream) -> Optional[int]:
@@ -297,14 +311,13 @@ def norm_desc(hidden: int, eps: float = 1e-6, alpha: float = 1.0, delta_f32: boo
 def moe_norm_quant(desc: MoeNormDesc, x, delta, weight, T: int, x_out=None, xn_out=None,
                    q_out=None, q_scale=None, stream=None) -> None:
     """Residual addition, RMS norm and e4m3 output (see header)."""
-    _check(load_library().moe_norm_quant(ctypes.byref(desc), _ptr(x), _ptr(delta), _ptr(weight), T,
-                                         _ptr(x_out), _ptr(xn_out), _ptr(q_out), _ptr(q_scale),
-                                         _stream(stream)), "moe_norm_quant")
+    _status("moe_norm_quant", ctypes.byref(desc), _ptr(x), _ptr(delta), _ptr(weight), T,
+            _ptr(x_out), _ptr(xn_out), _ptr(q_out), _ptr(q_scale), _stream(stream))
 
 
 def moe_router_logits(plan: int, x, T: int, router_w, router_bias, logits, stream=None) -> None:
-    _check(load_library().moe_router_logits(plan, _ptr(x), T, _ptr(router_w), _ptr(router_bias),
-                                            _ptr(logits), _stream(stream)), "moe_router_logits")
+    _status("moe_router_logits", plan, _ptr(x), T, _ptr(router_w), _ptr(router_bias), _ptr(logits),
+            _stream(stream))
 
 
 def score_desc(score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
@@ -319,9 +332,8 @@ def moe_route_scored(plan: int, logits, T: int, desc: MoeScoreDesc,
     """Routing by scores into the buffers that ``routing`` names; its empty
     fields receive the plan's own."""
     out = MoeRouting() if routing is None else routing
-    _check(load_library().moe_route_scored(plan, _ptr(logits), T, ctypes.byref(desc),
-                                           ctypes.byref(out), _stream(stream)),
-           "moe_route_scored")
+    _status("moe_route_scored", plan, _ptr(logits), T, ctypes.byref(desc), ctypes.byref(out),
+            _stream(stream))
     return out
 
 
@@ -363,10 +375,9 @@ def moe_linear_forward(linear: int, x, T: int, weight: MoeW4, y, x_scale=None,
                        y_stride: int = 0, stream=None) -> None:
     """4-bit projection with adapters; x is a bf16 or float8_e4m3fn tensor."""
     x_type = 1 if x.element_size() == 1 else 0
-    _check(load_library().moe_linear_forward(
-        linear, _ptr(x), x_type, x_stride, _ptr(x_scale), T, ctypes.byref(weight),
-        ctypes.byref(lora) if lora is not None else None, _ptr(adapter), _ptr(y), y_stride,
-        _stream(stream)), "moe_linear_forward")
+    _status("moe_linear_forward", linear, _ptr(x), x_type, x_stride, _ptr(x_scale), T,
+            ctypes.byref(weight), None if lora is None else ctypes.byref(lora), _ptr(adapter),
+            _ptr(y), y_stride, _stream(stream))
 
 
 def moe_linear_get_error(linear: int) -> int:

@@ -501,7 +501,7 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   if (p.lora_stages > lin::kMaxLoraStages) p.lora_stages = lin::kMaxLoraStages;
   const int smem = fixed + p.lora_stages * p.lora_stage_bytes + 1024;
   auto go = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     return e != cudaSuccess ? e : launch_pdl(kern, dim3(2 * pairs), dim3(lin::kThreads), smem, st, p);
   };
   return a.la ? go(lin::linear_tc_kernel<true>) : go(lin::linear_tc_kernel<false>);

@@ -30,6 +30,10 @@ struct W4Dev {                    // one matrix set (device pointers)
   const uint16_t* b;
 };
 
+// Lets a kernel take `bytes` of dynamic shared memory on the current device;
+// the runtime is asked only when it has not been allowed as much before.
+cudaError_t allow_smem(const void* kernel, int bytes);
+
 // 2D row-major tensor map: `rows` x `cols` elements, box `box_cols` x
 // `box_rows`, 128-byte swizzle (box_cols * elem == 128); false if the driver
 // entry point is missing or rejects the map.

@@ -10,7 +10,9 @@
 // token order, and no result depends on atomic ordering.
 #include <cuda_pipeline.h>
 
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "moe_common.cuh"
 #include "topk.cuh"
@@ -39,6 +41,20 @@ EncodeTiledFn get_encode() {
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> allowed;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  int& have = allowed[{kernel, dev}];
+  if (bytes <= have) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) have = bytes;
+  return e;
+}
 
 // 2D row-major tensor map: `rows` x `cols` elements, box `box_cols` x `box_rows`,
 // 128-byte swizzle (box_cols * elem == 128).

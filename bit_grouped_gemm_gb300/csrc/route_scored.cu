@@ -267,7 +267,7 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
   p.gen = gen;
   p.err = err;
   auto go = [&](auto kern, int smem) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     if (G == 1) return launch_pdl(kern, dim3(1), dim3(kScThreads), smem, st, p);
     // cooperative (the CTAs wait on the last one), in ordinary stream order
@@ -293,7 +293,7 @@ cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, in
                               int32_t* topk_idx, float* topk_w, int32_t* blk_cnt, cudaStream_t st) {
   const int nblk = (T + kRouterTB - 1) / kRouterTB;
   auto go = [&](auto kern, int smem) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(nblk), dim3(kScThreads), smem, st, dev_of(a), logits, T, E, k,
                       topk_idx, topk_w, blk_cnt);

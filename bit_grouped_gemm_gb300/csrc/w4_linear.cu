@@ -436,7 +436,7 @@ cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16
   const int nx = (a.T + kPrepTok - 1) / kPrepTok * kPrepSplit;
   const int smem = a.la ? kPrepTok * (prep_row_bytes(a.K) + a.rank * 4) : 0;
   auto go = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     return e != cudaSuccess
                ? e
                : launch_pdl(kern, dim3(nx + nw), dim3(256), (size_t)smem, st, a, x16, w16, nx, err);
