@@ -4,18 +4,16 @@
 //   x' = bf16(x + alpha d);  v = x' w / sqrt(mean x'^2 + eps)
 //   xn = bf16(v);  q = e4m3(v 448 / max|v|), scale = max|v| / 448
 //
-// One CTA takes a row and holds it in registers, so every input is read once
-// and every output written once. Both row statistics come from one reduction:
-// the mean of squares needs x', and max|v| is max|x' w| times the row's factor
-// (rounding is monotone, so this is the largest |v| to the bit).
-#include <cuda_fp8.h>
-
+// Bound by memory: every input is read once and every output written once, a
+// row staying in the registers of its threads in between. Both row statistics
+// come from one reduction: the mean of squares needs x', and max|v| is
+// max|x' w| times the row's factor (rounding is monotone, so this is the largest
+// |v| to the bit). CTAs walk the rows and load the next one before they reduce
+// and store the last.
 #include "moe_common.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kNqThreads = 256;
 
 struct NqParams {
   const uint16_t* x;
@@ -52,104 +50,169 @@ __device__ __forceinline__ float nan_max(float a, float b) {
   return r;
 }
 
-// NV vectors of 8 columns per thread: column 8 (tid + kNqThreads i).
-template <int NV>
-__global__ void __launch_bounds__(kNqThreads) norm_quant_kernel(const NqParams p) {
+// TPR threads per row (a power of two from 16), each with NV vectors of 8
+// columns, vector c = lane-in-row + TPR i; kD: delta 0 none, 1 bf16, 2 f32.
+// Several rows share a CTA of 256 threads where TPR is less.
+constexpr int cta_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <int TPR, int NV, int kD>
+__global__ void __launch_bounds__(cta_threads(TPR)) norm_quant_kernel(const NqParams p) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR, kWarps = TPR / 32;
   pdl_begin();
-  __shared__ float s_ss[kNqThreads / 32], s_mx[kNqThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x, nvec = p.H / 8;
-  float v[NV][8];
-  float ss = 0.f, mx = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = tid + kNqThreads * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (c >= nvec) continue;
-    unpack8(*reinterpret_cast<const uint4*>(p.x + t * p.x_ld + 8 * c), v[i]);
-    if (p.d) {
-      float d[8];
-      if (p.d_f32) {
-        const float4* dp = reinterpret_cast<const float4*>(static_cast<const float*>(p.d) + t * p.d_ld + 8 * c);
-        const float4 a = dp[0], b = dp[1];
-        d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w;
-        d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
-      } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d) + t * p.d_ld + 8 * c), d);
-      }
-      uint4 o;
-      uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        ow[j] = pack_bf16x2(fmaf(p.alpha, d[2 * j], v[i][2 * j]), fmaf(p.alpha, d[2 * j + 1], v[i][2 * j + 1]));
-      unpack8(o, v[i]);
-      if (p.xo) *reinterpret_cast<uint4*>(p.xo + t * p.x_ld + 8 * c) = o;
-    } else if (p.xo && p.xo != p.x) {
-      *reinterpret_cast<uint4*>(p.xo + t * p.x_ld + 8 * c) =
-          *reinterpret_cast<const uint4*>(p.x + t * p.x_ld + 8 * c);
-    }
-    float w[8];
-    if (p.w) unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + 8 * c)), w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ss = fmaf(v[i][j], v[i][j], ss);
-      if (p.w) v[i][j] *= w[j];
-      mx = nan_max(mx, fabsf(v[i][j]));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    mx = nan_max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  }
-  if (lane == 0) {
-    s_ss[warp] = ss;
-    s_mx[warp] = mx;
-  }
-  __syncthreads();
-  float tot = 0.f;
-  mx = 0.f;
-#pragma unroll
-  for (int i = 0; i < kNqThreads / 32; ++i) {
-    tot += s_ss[i];
-    mx = nan_max(mx, s_mx[i]);
-  }
-  const float inv = 1.0f / sqrtf(tot / (float)p.H + p.eps);
+  __shared__ float2 s_red[2][kThreads / 32];
+  const int sub = threadIdx.x / TPR, tid = threadIdx.x % TPR, lane = threadIdx.x & 31;
+  const int nvec = p.H / 8;
   const int ngroups = p.group ? (p.H + p.group - 1) / p.group : 1;
+  uint4 xr[NV], dr[NV * (kD == 2 ? 2 : 1)];
+  auto load = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = tid + kNqThreads * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-    if (p.xn && c < nvec) {
-      uint4 o;
-      o.x = pack_bf16x2(v[i][0], v[i][1]);
-      o.y = pack_bf16x2(v[i][2], v[i][3]);
-      o.z = pack_bf16x2(v[i][4], v[i][5]);
-      o.w = pack_bf16x2(v[i][6], v[i][7]);
-      *reinterpret_cast<uint4*>(p.xn + t * p.o_ld + 8 * c) = o;
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + TPR * i;
+      if (t < p.T && c < nvec) {
+        xr[i] = *reinterpret_cast<const uint4*>(p.x + t * p.x_ld + 8 * c);
+        if constexpr (kD == 1)
+          dr[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d) + t * p.d_ld + 8 * c);
+        if constexpr (kD == 2) {
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p.d) + t * p.d_ld + 8 * c);
+          dr[2 * i] = q[0];
+          dr[2 * i + 1] = q[1];
+        }
+      }
     }
-    if (!p.q) continue;
-    float am = mx * inv;
-    if (p.group) {   // 128 columns: 16 neighbouring lanes
-      am = 0.f;
+  };
+  int t = blockIdx.x * kRows + sub;
+  load(t);
+  // (the trip count is the CTA's, not the row's: every thread meets the barrier)
+  int buf = 0;
+  for (int t0 = blockIdx.x * kRows; t0 < p.T; t0 += gridDim.x * kRows, t += gridDim.x * kRows, buf ^= 1) {
+    const bool row = t < p.T;
+    float v[NV][8];
+    float ss = 0.f, mx = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) am = nan_max(am, fabsf(v[i][j]));
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + TPR * i;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) am = nan_max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      if (!row || c >= nvec) continue;
+      unpack8(xr[i], v[i]);
+      if constexpr (kD != 0) {
+        float d[8];
+        if constexpr (kD == 1) {
+          unpack8(dr[i], d);
+        } else {
+          const uint4 q0 = dr[2 * i], q1 = dr[2 * i + 1];
+          const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = __uint_as_float(w[j]);
+        }
+        uint4 o;
+        uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          ow[j] = pack_bf16x2(fmaf(p.alpha, d[2 * j], v[i][2 * j]), fmaf(p.alpha, d[2 * j + 1], v[i][2 * j + 1]));
+        unpack8(o, v[i]);
+        if (p.xo) *reinterpret_cast<uint4*>(p.xo + t * p.x_ld + 8 * c) = o;
+      } else if (p.xo && p.xo != p.x) {
+        *reinterpret_cast<uint4*>(p.xo + t * p.x_ld + 8 * c) = xr[i];
+      }
+      float w[8];
+      if (p.w) unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + 8 * c)), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = fmaf(v[i][j], v[i][j], ss);
+        if (p.w) v[i][j] *= w[j];
+        mx = nan_max(mx, fabsf(v[i][j]));
+      }
     }
-    const bool none = am < 0x1p-100f;
-    const float qk = none ? 0.f : 448.0f / am;
-    if (c < nvec) {
-      uint2 o;
-      o.x = e4m3x2(v[i][0] * qk, v[i][1] * qk) | (e4m3x2(v[i][2] * qk, v[i][3] * qk) << 16);
-      o.y = e4m3x2(v[i][4] * qk, v[i][5] * qk) | (e4m3x2(v[i][6] * qk, v[i][7] * qk) << 16);
-      *reinterpret_cast<uint2*>(p.q + t * p.o_ld + 8 * c) = o;
-      if (p.group ? (c & 15) == 0 : c == 0)
-        p.qs[(size_t)t * ngroups + (p.group ? c / 16 : 0)] = none ? 0.f : am / 448.0f;
+    load(t + gridDim.x * kRows);
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      mx = nan_max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if constexpr (TPR > 32) {
+      if (lane == 0) s_red[buf][threadIdx.x >> 5] = make_float2(ss, mx);
+      __syncthreads();   // (the other buffer is free again after the next one)
+      ss = mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float2 r = s_red[buf][sub * kWarps + i];
+        ss += r.x;
+        mx = nan_max(mx, r.y);
+      }
+    }
+    const float inv = 1.0f / sqrtf(ss / (float)p.H + p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + TPR * i;
+      const bool on = row && c < nvec;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+      if (p.xn && on) {
+        uint4 o;
+        o.x = pack_bf16x2(v[i][0], v[i][1]);
+        o.y = pack_bf16x2(v[i][2], v[i][3]);
+        o.z = pack_bf16x2(v[i][4], v[i][5]);
+        o.w = pack_bf16x2(v[i][6], v[i][7]);
+        *reinterpret_cast<uint4*>(p.xn + t * p.o_ld + 8 * c) = o;
+      }
+      if (!p.q) continue;
+      float am = mx * inv;
+      if (p.group) {   // 128 columns: 16 neighbouring lanes
+        am = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) am = nan_max(am, fabsf(v[i][j]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) am = nan_max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      }
+      const bool none = am < 0x1p-100f;
+      const float qk = none ? 0.f : 448.0f / am;
+      if (on) {
+        uint2 o;
+        o.x = e4m3x2(v[i][0] * qk, v[i][1] * qk) | (e4m3x2(v[i][2] * qk, v[i][3] * qk) << 16);
+        o.y = e4m3x2(v[i][4] * qk, v[i][5] * qk) | (e4m3x2(v[i][6] * qk, v[i][7] * qk) << 16);
+        *reinterpret_cast<uint2*>(p.q + t * p.o_ld + 8 * c) = o;
+        if (p.group ? (c & 15) == 0 : c == 0)
+          p.qs[(size_t)t * ngroups + (p.group ? c / 16 : 0)] = none ? 0.f : am / 448.0f;
+      }
     }
   }
+}
+
+template <int TPR, int NV, int kD>
+cudaError_t launch_nq(const NqParams& p, cudaStream_t st) {
+  constexpr int kRows = cta_threads(TPR) / TPR;
+  const int ctas = (p.T + kRows - 1) / kRows;
+  static int resident[64] = {};   // CTAs the device holds at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int cap = dev < 64 ? resident[dev] : 0;
+  if (!cap) {
+    int sms = 0, per = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, norm_quant_kernel<TPR, NV, kD>, cta_threads(TPR), 0);
+    if (e != cudaSuccess) return e;
+    cap = sms * per;
+    if (dev < 64) resident[dev] = cap;
+  }
+  return launch_pdl(norm_quant_kernel<TPR, NV, kD>, dim3(ctas < cap ? ctas : cap), dim3(cta_threads(TPR)), 0, st, p);
+}
+
+// Threads per row by its width, so that a thread holds one vector, two from
+// 2,056 columns on.
+template <int kD>
+cudaError_t launch_width(const NqParams& p, cudaStream_t st) {
+  const int nvec = p.H / 8;
+  return nvec <= 16     ? launch_nq<16, 1, kD>(p, st)
+         : nvec <= 32   ? launch_nq<32, 1, kD>(p, st)
+         : nvec <= 64   ? launch_nq<64, 1, kD>(p, st)
+         : nvec <= 128  ? launch_nq<128, 1, kD>(p, st)
+         : nvec <= 256  ? launch_nq<256, 1, kD>(p, st)
+         : nvec <= 512  ? launch_nq<256, 2, kD>(p, st)
+         : nvec <= 1024 ? launch_nq<512, 2, kD>(p, st)
+                        : launch_nq<1024, 2, kD>(p, st);
 }
 
 bool al16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
@@ -216,12 +279,8 @@ extern "C" moe_status moe_norm_quant(const moe_norm_desc* d, const uint16_t* x, 
   p.eps = d->eps;
   p.alpha = d->alpha;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int nv = (H / 8 + kNqThreads - 1) / kNqThreads;
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(T), dim3(kNqThreads), 0, st, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-  };
-  return nv <= 1 ? go(norm_quant_kernel<1>)
-         : nv <= 2 ? go(norm_quant_kernel<2>)
-         : nv <= 4 ? go(norm_quant_kernel<4>)
-                   : go(norm_quant_kernel<8>);
+  const cudaError_t e = !delta ? launch_width<0>(p, st)
+                        : d->delta_f32 ? launch_width<2>(p, st)
+                                       : launch_width<1>(p, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
