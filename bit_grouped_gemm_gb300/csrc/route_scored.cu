@@ -74,13 +74,14 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
   __shared__ unsigned mask_s[kScWords * kE];   // [word][expert]
   __shared__ int start_s[kE];
   __shared__ int wrows_s[16], wtiles_s[16];
-  pdl_begin();
+  __shared__ uint16_t idx_s[kScMaxC * 32];     // the CTA's choices, [token][k]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = p.E, k = p.k, b = blockIdx.x, G = gridDim.x;
   const int t0 = b * p.C, nt = min(p.C, p.T - t0);
   const int words = (p.C + 31) / 32;
   for (int i = tid; i < words * kE; i += kScThreads) mask_s[i] = 0u;
   __syncthreads();
+  pdl_begin();
 
   for (int tl = warp; tl < nt; tl += kScThreads / 32) {
     const size_t t = t0 + tl;
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
     if (lane < k) {
       p.idx[t * k + lane] = idx;
       p.w[t * k + lane] = w;
+      idx_s[tl * k + lane] = (uint16_t)idx;
       atomicOr(&mask_s[(tl >> 5) * kE + idx], 1u << (tl & 31));
     }
     __syncwarp();
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
   // the CTA's slots, in token order within each expert
   for (int i = tid; i < nt * k; i += kScThreads) {
     const int tl = i / k, slot = t0 * k + i;
-    const int e = __ldcg(p.idx + slot);    // this CTA's own store
+    const int e = idx_s[i];
     int pos = start_s[e] + __popc(mask_s[(tl >> 5) * kE + e] & ((1u << (tl & 31)) - 1u));
     for (int wd = 0; wd < (tl >> 5); ++wd) pos += __popc(mask_s[wd * kE + e]);
     p.perm[pos] = slot;
@@ -276,11 +278,13 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
     cfg.blockDim = dim3(kScThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
   return E <= 64    ? go(score_route_kernel<2>, dyn_bytes(2))
