@@ -26,7 +26,7 @@ struct ScParams {
   float* w;
   uint8_t* table;                     // [CTAs][E]
   int32_t *cnt, *off, *tile_off, *bmap, *num_tiles, *perm, *inv;
-  unsigned *arrive, *gen;
+  unsigned *arrive, *left;
   DevErr err;
 };
 
@@ -36,28 +36,22 @@ __device__ __forceinline__ unsigned ld_relaxed(const unsigned* p) {
   return v;
 }
 
-// Grid barrier of a cooperative launch: the last CTA to arrive resets the
-// counter and advances the generation; bounded.
-__device__ __forceinline__ bool grid_barrier(unsigned* arrive, unsigned* gen, const DevErr& err,
-                                             int site) {
+// Grid barrier of a cooperative launch, bounded: thread 0 counts its CTA in and
+// polls the count itself (no second word to wait for). The CTAs count
+// themselves out at their end, and the last one sets both words back to 0.
+__device__ __forceinline__ bool grid_arrive_wait(unsigned* arrive, const DevErr& err, int site) {
   __shared__ int go;
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    const unsigned g0 = ld_relaxed(gen);   // moves only after every arrival
+    __threadfence();   // the CTA's table row, before its arrival
+    asm volatile("red.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(arrive) : "memory");
     int ok = 1;
-    if (atomicAdd(arrive, 1u) == gridDim.x - 1) {
-      *arrive = 0u;
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(gen), "r"(g0 + 1u) : "memory");
-    } else {
-      const unsigned long long start = globaltimer_ns();
-      while (ld_relaxed(gen) == g0) {
-        __nanosleep(40);
-        if (globaltimer_ns() - start > err.limit_ns) {
-          report_timeout(err, site);
-          ok = 0;
-          break;
-        }
+    const unsigned long long start = globaltimer_ns();
+    while (ld_relaxed(arrive) < gridDim.x) {
+      if (globaltimer_ns() - start > err.limit_ns) {
+        report_timeout(err, site);
+        ok = 0;
+        break;
       }
     }
     asm volatile("fence.acq_rel.gpu;" ::: "memory");
@@ -65,6 +59,12 @@ __device__ __forceinline__ bool grid_barrier(unsigned* arrive, unsigned* gen, co
   }
   __syncthreads();
   return go != 0;
+}
+__device__ __forceinline__ void grid_leave(unsigned* arrive, unsigned* left) {
+  if (threadIdx.x == 0 && atomicAdd(left, 1u) == gridDim.x - 1) {
+    *left = 0u;
+    *arrive = 0u;
+  }
 }
 
 template <int VPL>
@@ -102,21 +102,28 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
     for (int i = 0; i < words; ++i) tot += __popc(mask_s[i * kE + tid]);
   if (G > 1) {
     if (tid < E) p.table[(size_t)b * E + tid] = (uint8_t)tot;
-    if (!grid_barrier(p.arrive, p.gen, p.err, 60)) return;
+    if (!grid_arrive_wait(p.arrive, p.err, 60)) return;
     // the table, 4 experts per thread, the rows dealt over the rest of the
     // threads: totals in the low halves, earlier CTAs' in the high halves
     uint32_t* part = reinterpret_cast<uint32_t*>(dyn);   // [rows' share][E]
     const int e4 = E / 4, shares = min(kScThreads / e4, 32), q = tid / e4, c = tid % e4;
     if (q < shares) {
       uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
-#pragma unroll 8
-      for (int r = q; r < G; r += shares) {
-        const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(p.table + (size_t)r * E) + c);
-        const uint32_t f = r < b ? 0x10001u : 1u;
-        s0 += (v & 0xFFu) * f;
-        s1 += ((v >> 8) & 0xFFu) * f;
-        s2 += ((v >> 16) & 0xFFu) * f;
-        s3 += (v >> 24) * f;
+      for (int r0 = q; r0 < G; r0 += 10 * shares) {   // 10 rows' loads at once
+        uint32_t v[10];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          const int r = r0 + i * shares;
+          v[i] = r < G ? __ldcg(reinterpret_cast<const uint32_t*>(p.table + (size_t)r * E) + c) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          const uint32_t f = r0 + i * shares < b ? 0x10001u : 1u;
+          s0 += (v[i] & 0xFFu) * f;
+          s1 += ((v[i] >> 8) & 0xFFu) * f;
+          s2 += ((v[i] >> 16) & 0xFFu) * f;
+          s3 += (v[i] >> 24) * f;
+        }
       }
       uint32_t* o = part + q * E + 4 * c;
       o[0] = s0;
@@ -186,6 +193,7 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
     p.perm[pos] = slot;
     p.inv[slot] = pos;
   }
+  if (G > 1) grid_leave(p.arrive, p.left);
 }
 
 // The choice alone, 32 tokens per CTA, with the block's counts as
@@ -216,8 +224,20 @@ __global__ void __launch_bounds__(kScThreads) score_topk_kernel(const ScoreDev s
   for (int e = tid; e < E; e += kScThreads) blk_cnt[(size_t)blockIdx.x * E + e] = cnt_s[e];
 }
 
-ScoreDev dev_of(const ScoreArgs& a) {
-  return ScoreDev{a.sigmoid, a.groups, a.topk_groups, a.renorm, a.scale, a.bias};
+// Experts per lane.
+int vpl_of(int E) { return E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : 16; }
+
+ScoreDev dev_of(const ScoreArgs& a, int E) {
+  ScoreDev s{a.sigmoid, a.groups, a.topk_groups, a.renorm, a.scale, a.bias, E / a.groups, 0, 0, 0};
+  s.gdiv = ((1 << 20) + s.gsz - 1) / s.gsz;
+  const int vpl = vpl_of(E), per = s.gsz / vpl;
+  s.whole = s.gsz % vpl == 0 && (per & (per - 1)) == 0;
+  int lanes = per;
+  if (!s.whole)
+    for (lanes = 32; lanes * a.groups > 32; lanes >>= 1) {
+    }
+  while ((1 << s.span_log2) < lanes) ++s.span_log2;
+  return s;
 }
 
 // dynamic shared memory: a row per warp; the partial sums take at most as much
@@ -244,13 +264,13 @@ bool score_route_fits(int T, int num_sms) {
 cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, int E, int k,
                                int32_t* topk_idx, float* topk_w, uint8_t* table, int32_t* cnt,
                                int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
-                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
+                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* left,
                                DevErr err, int num_sms, cudaStream_t st) {
   ScParams p;
   int G;
   score_grid(T, num_sms, &p.C, &G);
   if (p.C > kScMaxC || E > 512 || k > 32) return cudaErrorInvalidValue;
-  p.s = dev_of(a);
+  p.s = dev_of(a, E);
   p.logits = logits;
   p.T = T;
   p.E = E;
@@ -266,7 +286,7 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
   p.perm = perm;
   p.inv = inv;
   p.arrive = arrive;
-  p.gen = gen;
+  p.left = left;
   p.err = err;
   auto go = [&](auto kern, int smem) -> cudaError_t {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
@@ -287,10 +307,12 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
-  return E <= 64    ? go(score_route_kernel<2>, dyn_bytes(2))
-         : E <= 128 ? go(score_route_kernel<4>, dyn_bytes(4))
-         : E <= 256 ? go(score_route_kernel<8>, dyn_bytes(8))
-                    : go(score_route_kernel<16>, dyn_bytes(16));
+  switch (vpl_of(E)) {
+    case 2: return go(score_route_kernel<2>, dyn_bytes(2));
+    case 4: return go(score_route_kernel<4>, dyn_bytes(4));
+    case 8: return go(score_route_kernel<8>, dyn_bytes(8));
+    default: return go(score_route_kernel<16>, dyn_bytes(16));
+  }
 }
 
 cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, int E, int k,
@@ -299,13 +321,15 @@ cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, in
   auto go = [&](auto kern, int smem) -> cudaError_t {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(nblk), dim3(kScThreads), smem, st, dev_of(a), logits, T, E, k,
+    return launch_pdl(kern, dim3(nblk), dim3(kScThreads), smem, st, dev_of(a, E), logits, T, E, k,
                       topk_idx, topk_w, blk_cnt);
   };
-  return E <= 64    ? go(score_topk_kernel<2>, dyn_bytes(2))
-         : E <= 128 ? go(score_topk_kernel<4>, dyn_bytes(4))
-         : E <= 256 ? go(score_topk_kernel<8>, dyn_bytes(8))
-                    : go(score_topk_kernel<16>, dyn_bytes(16));
+  switch (vpl_of(E)) {
+    case 2: return go(score_topk_kernel<2>, dyn_bytes(2));
+    case 4: return go(score_topk_kernel<4>, dyn_bytes(4));
+    case 8: return go(score_topk_kernel<8>, dyn_bytes(8));
+    default: return go(score_topk_kernel<16>, dyn_bytes(16));
+  }
 }
 
 }  // namespace moe

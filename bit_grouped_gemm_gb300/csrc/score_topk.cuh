@@ -29,7 +29,14 @@ struct ScoreDev {
   int sigmoid, groups, topk_groups, renorm;
   float scale;
   const float* bias;
+  // Groups (more than one): experts per group and the factor of a division by
+  // it (e gdiv >> 20, e < 512); lanes per group, 2^span_log2, each with whole
+  // experts of one group only, or (whole = 0) taking turns at its experts.
+  int gsz, gdiv, span_log2, whole;
 };
+
+// The group of expert e.
+__device__ __forceinline__ int group_of(const ScoreDev& s, int e) { return (e * s.gdiv) >> 20; }
 
 // Monotone double -> uint64 (no NaN, -0 already +0).
 __device__ __forceinline__ unsigned long long order_key64(double f) {
@@ -463,6 +470,8 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     }
   };
   load_row(row, [&](int i, float v) { c[i] = clean_logit(v); });
+  float bias[VPL];
+  if (s.bias) load_row(s.bias, [&](int i, float v) { bias[i] = fmaxf(v, -INFINITY); });
   float m = 0.f, rz = 1.f;
   if (!s.sigmoid && (s.bias || s.groups > 1 || !s.renorm)) {
     m = c[0];
@@ -489,7 +498,8 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = rz > 0.f ? __fmul_rn(c[i], rz) : 0.f;
     }
-    load_row(s.bias, [&](int i, float v) { c[i] = __fadd_rn(c[i], fmaxf(v, -INFINITY)); });
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = __fadd_rn(c[i], bias[i]);
   }
   // Bound of a pair's FP32 error, from expf's 2 ulp, the reciprocal's 1 and
   // half an ulp for every other operation. Sigmoid: e = exp(-l) enters
@@ -499,35 +509,30 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
   // 1.8e-6 by 1 / z (at most 21 additions), which both share. The bias'
   // addition: half an ulp of c.
   const float perr = s.sigmoid ? 5e-7f : 2.8e-6f * rz;
-  float m1 = -INFINITY, m2 = -INFINITY;   // the lane's two largest
+  float top = c[0];   // the lane's largest
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    m2 = fmaxf(m2, fminf(m1, c[i]));
-    m1 = fmaxf(m1, c[i]);
-  }
-  float top = m1;
+  for (int i = 1; i < VPL; ++i) top = fmaxf(top, c[i]);
   bool unsure_groups = false;
   constexpr unsigned kAll = (unsigned)((1ull << VPL) - 1ull);
   unsigned elig = e0 + VPL <= E ? kAll : e0 >= E ? 0u : (1u << (E - e0)) - 1u;
   if (s.groups > 1) {
-    const int gsz = E / s.groups;
-    // lanes per group where no lane's experts belong to two groups
-    const int per = gsz / VPL;
-    const bool whole = gsz % VPL == 0 && (per & (per - 1)) == 0;
-    int span = per;   // lanes that hold one group's parts: group lane / span
-    if (!whole) {
-      // through shared memory: `span` lanes a group, each every span-th expert
-      int g2 = 1;
-      while (g2 < s.groups) g2 <<= 1;
-      span = 32 / g2;
+    const int gsz = s.gsz, span = 1 << s.span_log2, g = lane >> s.span_log2;
+    const bool whole = s.whole != 0;
+    float m1 = -INFINITY, m2 = -INFINITY;   // the lane's two largest of its group
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        m2 = fmaxf(m2, fminf(m1, c[i]));
+        m1 = fmaxf(m1, c[i]);
+      }
+    } else {
+      // through shared memory
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (e0 + i < E) sm[e0 + i] = c[i];
       __syncwarp();
-      const int g = lane / span;
-      m1 = m2 = -INFINITY;
       if (g < s.groups)
-        for (int i = lane % span; i < gsz; i += span) {
+        for (int i = lane & (span - 1); i < gsz; i += span) {
           const float v = sm[g * gsz + i];
           m2 = fmaxf(m2, fminf(m1, v));
           m1 = fmaxf(m1, v);
@@ -539,7 +544,6 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       m2 = fmaxf(fmaxf(m2, b), fminf(m1, a));
       m1 = fmaxf(m1, a);
     }
-    const int g = lane / span;
     const float low = m2 > -INFINITY ? m2 : m1;   // the second largest
     float sum = -INFINITY, big = 0.f;
     if (g < s.groups) {
@@ -557,7 +561,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       const float o = __shfl_sync(0xffffffffu, sum, j * span);
       rank += o > sum || (o == sum && j < g);
     }
-    const bool head = lane % span == 0 && g < s.groups;
+    const bool head = (lane & (span - 1)) == 0 && g < s.groups;
     unsigned keep = __ballot_sync(0xffffffffu, head && rank < s.topk_groups);
     // the last group kept and the first dropped: four scores' errors and the
     // sums' roundings
@@ -573,12 +577,12 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
         const bool dub = head && sum >= b - wide && sum <= a + wide;
         const unsigned dheads = __ballot_sync(0xffffffffu, dub);
         unsigned doubt = 0u;
-        for (unsigned left = dheads; left; left &= left - 1) doubt |= 1u << ((__ffs(left) - 1) / span);
+        for (unsigned left = dheads; left; left &= left - 1) doubt |= 1u << ((__ffs(left) - 1) >> s.span_log2);
         const int want = s.topk_groups - __popc(keep & ~dheads);
         unsigned cand = 0u;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          const int eg = min(e0 + i, E - 1) / gsz;
+          const int eg = group_of(s, min(e0 + i, E - 1));
           const float lw = __shfl_sync(0xffffffffu, low, eg * span);
           const float thr = s.bias ? lw - 2.f * (perr + 2.5e-7f * fabsf(lw)) : lw;
           if (e0 + i < E && ((doubt >> eg) & 1u) && !(c[i] < thr)) cand |= 1u << i;
@@ -609,7 +613,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (e0 + i < E && !((keep >> ((e0 + i) / gsz * span)) & 1u)) {
+        if (e0 + i < E && !((keep >> (group_of(s, e0 + i) * span)) & 1u)) {
           c[i] = -INFINITY;
           elig &= ~(1u << i);
         }
@@ -624,14 +628,14 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     // `need` scores in order: the k chosen, and with a bias the next one. The
     // lanes' need-th largest maximum bounds them from below.
     const int need = s.bias ? k + 1 : k;
-    int rank = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float o = __shfl_sync(0xffffffffu, top, j);
-      rank += o > top || (o == top && j < lane);
+    // (equal maxima count once: the bound is then lower, the list longer)
+    uint32_t tk = need <= 32 ? order_key(top) : 0u, bk = 0u;
+#pragma unroll 1
+    for (int j = 0; j < need; ++j) {
+      bk = __reduce_max_sync(0xffffffffu, tk);
+      if (tk == bk) tk = 0u;
     }
-    const unsigned at = __ballot_sync(0xffffffffu, rank == need - 1);   // 0 if need is 33
-    const float bound = at ? __shfl_sync(0xffffffffu, top, __ffs(at) - 1) : -INFINITY;
+    const float bound = bk ? key_value(bk) : -INFINITY;
     int* list = reinterpret_cast<int*>(sm);
     uint32_t* lkey = reinterpret_cast<uint32_t*>(sm) + 32;
     int total = 33;
