@@ -470,8 +470,10 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     }
   };
   load_row(row, [&](int i, float v) { c[i] = clean_logit(v); });
+  // the bias is loaded ahead where there are registers for it
   float bias[VPL];
-  if (s.bias) load_row(s.bias, [&](int i, float v) { bias[i] = fmaxf(v, -INFINITY); });
+  auto load_bias = [&] { load_row(s.bias, [&](int i, float v) { bias[i] = fmaxf(v, -INFINITY); }); };
+  if (VPL <= 8 && s.bias) load_bias();
   float m = 0.f, rz = 1.f;
   if (!s.sigmoid && (s.bias || s.groups > 1 || !s.renorm)) {
     m = c[0];
@@ -498,6 +500,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = rz > 0.f ? __fmul_rn(c[i], rz) : 0.f;
     }
+    if (VPL > 8) load_bias();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = __fadd_rn(c[i], bias[i]);
   }
