@@ -249,8 +249,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           nl = s_steps[it & 1];
         }
         int j = 0;
-        auto due_after = [&](int j) { return nk / 2 + ((j + 1) * (nk - nk / 2)) / (nl + 1); };
-        int due = nl ? due_after(0) : nk + 1;   // (a division per chunk would cost the issuer 150 cycles)
+        // the first stage's place, and the chunks between two of them
+        const int gap = nl ? (nk - nk / 2) / (nl + 1) : 0;
+        int due = nl ? nk / 2 + gap : nk + 1;
         if (!(ok = warp_wait(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
         tc_fence_after();
         for (int c = 0; c < nk; ++c, ++cnt) {
@@ -268,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           // the adapter stages that are due, evenly among the second half's
           // chunks (fixed places: the sums' order is that of every run)
-          while (kLora && c + 1 >= due) {
+          while (kLora && j < nl && (c + 1 >= due || c + 1 == nk)) {
             const int ls = lcnt % p.lora_stages;
             if (!(ok = warp_wait(&lora_full[ls], (lcnt / p.lora_stages) & 1, abort_flag, p.err, 84))) break;
             tc_fence_after();
@@ -282,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++j;
             ++lcnt;
-            due = j < nl ? due_after(j) : nk + 1;
+            due += gap;
           }
           if (!ok) break;
         }
