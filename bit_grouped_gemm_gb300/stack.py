@@ -4,7 +4,8 @@
 shared expert) on a device from the seeded generator in ``synth`` and keeps
 the ``MoeExperts`` structs the C ABI takes. ``run_stack`` chains layers with
 the residual update ``x <- bf16(x + alpha * moe(rmsnorm(x)))``, every step
-through the C ABI.
+through the C ABI. ``AdaptedLayer`` is a served layer around the block: a 4-bit
+projection with per-request adapters, then the experts on a scored routing.
 """
 from __future__ import annotations
 
@@ -79,3 +80,64 @@ def run_stack(plan: int, x: torch.Tensor, xn: torch.Tensor, layers: List[DeviceL
                                       L.shared_c, y_buf, stream)
             binding.moe_residual_add(plan, x, y_buf, T, alpha, x, xn, stream)
     return x
+
+
+class AdaptedLayer:
+    """A pre-norm layer for the batch of many requests, each with its own
+    low-rank adapter or none, on the residual stream x (bf16 [T, H], in place):
+
+        h8, hs = e4m3(rmsnorm(x + alpha * y) * w1)   y: the last layer's output
+        d = projection(h8) with adapters             4-bit weights, H -> H
+        x = x + d;  xn = rmsnorm(x) * w2
+        y = experts(xn) on moe_route_scored's choice
+
+    The experts' FP32 output y is returned and joins the stream in the next
+    layer's first norm. ``norm1`` and ``norm2`` are bf16 [H]; ``proj`` is a
+    (qweight, scales, biases) triple of an H x H matrix; ``adapters`` a
+    ``binding.MoeLora`` (its tensors must outlive the layer) or None;
+    ``score`` a ``binding.MoeScoreDesc``.
+    """
+
+    def __init__(self, plan: int, layer: DeviceLayer, norm1, norm2, proj, score,
+                 adapters=None, max_tokens: int = 4096, alpha: float = 1.0):
+        H = layer.router_w.shape[0]
+        dev = layer.router_w.device
+        self.plan, self.layer, self.score, self.adapters = plan, layer, score, adapters
+        self.norm1, self.norm2, self.proj = norm1, norm2, proj
+        self.alpha = alpha
+        self.proj_c = binding.w4(*proj)
+        rank = adapters.rank if adapters is not None else 0
+        self.linear = binding.moe_linear_create(binding.linear_desc(H, H, max_tokens, rank),
+                                                dev.index or 0)
+        empty = lambda *shape, dt: torch.empty(shape, dtype=dt, device=dev)
+        self.h8 = empty(max_tokens, H, dt=torch.float8_e4m3fn)
+        self.hs = empty(max_tokens, 1, dt=torch.float32)
+        self.d = empty(max_tokens, H, dt=torch.bfloat16)
+        self.xn = empty(max_tokens, H, dt=torch.bfloat16)
+        self.logits = empty(max_tokens, layer.router_w.shape[1], dt=torch.float32)
+        self.y = empty(max_tokens, H, dt=torch.float32)
+
+    def close(self) -> None:
+        if self.linear:
+            binding.moe_linear_destroy(self.linear)
+            self.linear = None
+
+    def __call__(self, x: torch.Tensor, y: Optional[torch.Tensor], adapter=None,
+                 stream=None) -> torch.Tensor:
+        """One pass over T = len(x) tokens; ``adapter`` is int32 [T] (-1: none)."""
+        T, H = x.shape
+        L = self.layer
+        first = binding.norm_desc(H, alpha=self.alpha, delta_f32=True)
+        binding.moe_norm_quant(first, x, y, self.norm1, T, x_out=x, q_out=self.h8, q_scale=self.hs,
+                               stream=stream)
+        binding.moe_linear_forward(self.linear, self.h8, T, self.proj_c, self.d, x_scale=self.hs,
+                                   lora=self.adapters if adapter is not None else None,
+                                   adapter=adapter, stream=stream)
+        binding.moe_norm_quant(binding.norm_desc(H), x, self.d, self.norm2, T, x_out=x,
+                               xn_out=self.xn, stream=stream)
+        binding.moe_router_logits(self.plan, self.xn, T, L.router_w, L.router_bias, self.logits,
+                                  stream)
+        routing = binding.moe_route_scored(self.plan, self.logits, T, self.score, None, stream)
+        binding.moe_grouped_w4_ffn(self.plan, self.xn, T, routing, L.routed_c, L.shared_c, self.y,
+                                   stream)
+        return self.y[:T]

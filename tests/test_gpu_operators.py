@@ -593,3 +593,98 @@ def test_linear_refusals_with_a_handle():
     assert call(y=p(c.x)) == 1                       # output over the input
     torch.cuda.synchronize()
     bg.moe_linear_destroy(h)
+
+
+# ------------------------------------------------------- long and far offsets
+def test_norm_beyond_31_bits():
+    """More than 2^31 elements per tensor; the last rows are checked."""
+    H, T = 16384, (1 << 31) // 16384 + 40
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    tail = slice(T - 24, T)
+    x[tail] = randn(gen(1), 24, H)
+    xo, xn = torch.empty_like(x), torch.empty_like(x)
+    q = torch.empty(T, H, dtype=torch.float8_e4m3fn, device="cuda")
+    qs = torch.empty(T, 128, device="cuda")
+    bg.moe_norm_quant(bg.norm_desc(H, quant_group=128), x, None, None, T, xo, xn, q, qs)
+    torch.cuda.synchronize()
+    r = dict(x=x[tail].double(), d=None, w=None, xo=xo[tail].double(), xn=xn[tail].double(),
+             q=q[tail].float().double(), qs=qs[tail].double(), alpha=1.0, eps=float(np.float32(1e-6)))
+    check_norm(r, H, True)
+
+
+@pytest.mark.parametrize("T", [9, 40])
+def test_linear_rows_far_apart(T):
+    """Row strides that put the last rows beyond 2^31 elements."""
+    c = Linear(T, 128, 64, rank=8)
+    ld = ((1 << 31) // (T - 1) + 64) // 16 * 16
+    xs = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda")
+    ys = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda")
+    xs.view(T, ld)[:, :128] = c.x
+    h = bg.moe_linear_create(bg.linear_desc(128, 64, T, 8), 0)
+    bg.moe_linear_forward(h, xs, T, bg.w4(*c.w), ys, lora=c.lora, adapter=c.ids, x_stride=ld,
+                          y_stride=ld)
+    torch.cuda.synchronize()
+    assert bg.moe_linear_get_error(h) == 0
+    c.y = ys.view(T, ld)[:, :64].clone()
+    c.compare()
+    bg.moe_linear_destroy(h)
+
+
+# --------------------------------------------------------------- all together
+@pytest.mark.parametrize("T", [1, 5, 96])
+def test_adapted_layer(T):
+    """The operators in the order in which a served layer calls them, each
+    step's output against the 64-bit step on the library's own input to it."""
+    import dataclasses
+    from bit_grouped_gemm_gb300 import stack, synth
+    shape = synth.MoEShape(hidden=256, inter=256, num_experts=32, top_k=4)
+    w = dataclasses.replace(synth.standard_workloads()["t128_uniform"], shape=shape, tokens=T)
+    g = gen(T)
+    H, E, k = 256, 32, 4
+    L = stack.make_layer(w, 0, "cuda")
+    proj = w4_case(g, H, H)
+    a, b = (randn(g, 3, 16, H) / 16).bfloat16(), (0.3 * randn(g, 3, H, 16)).bfloat16()
+    bias = 0.05 * randn(g, E)
+    score = bg.score_desc("sigmoid", bias, groups=4, topk_groups=2, scale=1.5)
+    n1, n2 = ((1 + 0.2 * randn(g, H)).bfloat16() for _ in range(2))
+    plan = bg.moe_plan_create(bg.plan_desc(hidden=H, inter=256, num_experts=E, top_k=k,
+                                           max_tokens=T), 0)
+    layer = stack.AdaptedLayer(plan, L, n1, n2, proj, score, bg.lora(a, b), max_tokens=T, alpha=0.5)
+    x0 = randn(g, T, H).bfloat16()
+    y0 = randn(g, T, H)
+    ids = torch.randint(-1, 3, (T,), generator=g, device="cuda").to(torch.int32)
+    x = x0.clone()
+    y = layer(x, y0, ids).double()
+    torch.cuda.synchronize()
+    assert bg.moe_get_error(plan) == 0 and bg.moe_linear_get_error(layer.linear) == 0
+    # stream after the first norm, from its own rounding
+    x1 = (x0.double() + 0.5 * y0.double()).float().bfloat16().double()
+    d = layer.d[:T].double()
+    want = x1 + d
+    assert ((x.double() - want).abs() <= want.abs() * 2.0 ** -8 + x1.abs() * 2.0 ** -8 + 1e-30).all()
+    # projection on the 8-bit rows
+    c = Linear(T, H, H)
+    c.x, c.xs, c.w, c.rank = layer.h8[:T], layer.hs[:T, 0], proj, 16
+    c.lora, c.a, c.b, c.ls, c.ids, c.y = True, a, b, None, ids, layer.d[:T]
+    c.compare()
+    # routing on the library's logits, then the experts on that routing
+    logits = layer.logits[:T].cpu().numpy()
+    idx, wt = ref_route(logits, bias.cpu().numpy(), E, k, "sigmoid", 4, 2, True, 1.5)
+    got = parity.routing_to_numpy(bg.moe_route_scored(plan, layer.logits, T, score), T, k, E)
+    assert np.array_equal(got["topk_idx"], idx)
+    xf = layer.xn[:T].double()
+
+    def expert(sets, e, row):
+        gate, up, down = (w4_values(*[m[e] for m in sets[n]]) for n in ("gate", "up", "down"))
+        u = gate @ row
+        return down @ (u / (1 + torch.exp(-u)) * (up @ row))
+    rows = list(range(T) if T <= 5 else range(0, T, 24))
+    ref = []
+    for t in rows:
+        out = expert(L.shared, 0, xf[t])
+        for j in range(k):
+            out = out + float(wt[t, j]) * expert(L.routed, int(idx[t, j]), xf[t])
+        ref.append(out)
+    parity.check_y(y[rows].cpu().numpy(), torch.stack(ref).cpu().numpy())
+    layer.close()
+    bg.moe_plan_destroy(plan)
