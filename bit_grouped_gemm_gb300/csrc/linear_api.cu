@@ -212,10 +212,7 @@ moe_status moe_linear_forward(moe_linear_t p, const void* x, int x_type, long lo
   } else {
     e = launch_linear_prep(a, p->at<uint16_t>(p->L.x16), p->at<uint16_t>(p->L.w16), p->err(),
                            p->num_sms, st);
-    if (e == cudaSuccess) {
-      const int bn = linear_tile_n(T, N, p->num_sms);
-      e = launch_linear_tc(a, p->mx, p->mw[bn / 32 - 1], bn, p->err(), p->num_sms, st);
-    }
+    if (e == cudaSuccess) e = launch_linear_tc(a, p->mx, p->mw, p->err(), p->num_sms, st);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -36,12 +36,13 @@ constexpr int kLoraTile = 128 * 32;
 constexpr int kMaxLoraStages = 8;
 
 // Shared memory: the ring of operand chunks, the adapter stages, ids and runs and
-// list of the tile's adapters, barriers.
+// list of the tile's adapters, barriers. A copy takes up to 4,500 cycles to
+// land, so a tile's pace is the ring's depth over that until its MMAs are slower:
+// narrow tiles get as many chunks as fit.
 constexpr int kIdsBytes = 3 * kTileM * 4;
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 227 * 1024 - 1024;   // less alignment slack
-template <bool kLora>
-__host__ __device__ constexpr int stages() { return kLora ? 6 : 7; }
+constexpr int kMaxStages = 12;
 inline int stage_bytes(int bn) { return kOpBytes + (bn / 2) * 128; }
 inline int lora_stage_bytes(int bn) { return 2 * kLoraTile + (bn / 2) * 32; }
 
@@ -51,7 +52,8 @@ struct Params {
   CUtensorMap mb;       // B [n][N][r], boxes 16 x BN / 2 x 1, 32-byte swizzle
   LinearArgs a;
   int bn, mt, tiles;    // tile width, token tiles, all tiles
-  int stage_bytes, lora_stages, lora_stage_bytes;
+  int split;            // pairs per tile, each a part of K (a cluster is 2 x split CTAs)
+  int stages, stage_bytes, lora_stages, lora_stage_bytes;
   DevErr err;
 };
 
@@ -146,20 +148,20 @@ __device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra,
 }
 
 template <bool kLora>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ Params p) {
-  constexpr int kStages = stages<kLora>();
+  const int stages = p.stages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
-  uint8_t* lora = smem + kStages * p.stage_bytes;
+  uint8_t* lora = smem + stages * p.stage_bytes;
   int* s_ids = reinterpret_cast<int*>(lora + p.lora_stages * p.lora_stage_bytes);   // adapter per token
   int* s_runs = s_ids + kTileM;                             // its runs' adapters
   int* s_list = s_runs + kTileM;                            // its distinct adapters
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ids + (kLora ? 3 * kTileM : 0));
   uint64_t* full = bars;                   // leader: both CTAs' operands landed
-  uint64_t* empty = full + 7;              // chunk's MMAs done (both CTAs)
-  uint64_t* acc_full = empty + 7;          // [2] tile's MMAs done (both CTAs)
+  uint64_t* empty = full + kMaxStages;              // chunk's MMAs done (both CTAs)
+  uint64_t* acc_full = empty + kMaxStages;          // [2] tile's MMAs done (both CTAs)
   uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
   uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs' adapter stage is there
   uint64_t* lora_empty = lora_full + kMaxLoraStages;   // adapter stage's MMAs done (both CTAs)
@@ -171,12 +173,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* s_cnt = reinterpret_cast<int*>(tmem_slot + 4);       // [8] adapters per 32 tokens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  // CTA `rank` of pair `part` of the cluster; the pair's leader is its CTA 0
+  const uint32_t crank = cluster_rank(), rank = crank & 1u, lead = crank & ~1u;
+  const int part = (int)(crank >> 1), split = p.split;
   const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int pair = (int)blockIdx.x / (2 * split), npairs = (int)gridDim.x / (2 * split);   // clusters
+  auto leader_addr = [&](const void* q) { return cta_addr(q, lead); };
+  auto commit_both = [&](uint64_t* bar) { mma2_commit_mask(bar, (uint16_t)(3u << lead)); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -204,7 +210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // What the launch before wrote (x16, W16, h) is read after pdl_wait; the
   // adapters' ids are older: that launch waited for all before it.
 
-  const int nk = p.a.K / 64;
+  // this pair's chunks of K
+  const int nk_all = p.a.K / 64, c_lo = part * nk_all / split, nk = (part + 1) * nk_all / split - c_lo;
   const int half = p.bn >> 1;
   const int rb = (p.a.rank + 15) >> 4;   // stages per adapter
 
@@ -212,21 +219,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------- TMA, own halves
     pdl_begin();
     const uint32_t bytes = 2u * (kOpBytes + (uint32_t)half * 128u);   // of both CTAs
-    uint32_t cnt = 0;
+    int s = 0;
+    uint32_t ph = 1;   // slot and the parity of its barrier's last phase
     bool ok = true;
     for (int u = pair; u < p.tiles && ok; u += npairs) {
       const int m0 = (u % p.mt) * kTileM + 128 * (int)rank;
       const int n0 = (u / p.mt) * p.bn + half * (int)rank;
-      for (int c = 0; c < nk; ++c, ++cnt) {
-        const int s = cnt % kStages;
-        if (!(ok = warp_wait(&empty[s], ((cnt / kStages) & 1) ^ 1, abort_flag, p.err, 80))) break;
+      for (int c = 0; c < nk; ++c) {
+        if (!(ok = warp_wait(&empty[s], ph, abort_flag, p.err, 80))) break;
         if (elect_one_sync()) {
           uint8_t* dst = smem + s * p.stage_bytes;
           if (leader) mbar_arrive_expect_tx(&full[s], bytes);
-          tma_load_2d_pair(dst, &p.mx, 64 * c, m0, leader_addr(&full[s]));
-          tma_load_2d_pair(dst + kOpBytes, &p.mw, 64 * c, n0, leader_addr(&full[s]));
+          tma_load_2d_pair(dst, &p.mx, 64 * (c_lo + c), m0, leader_addr(&full[s]));
+          tma_load_2d_pair(dst + kOpBytes, &p.mw, 64 * (c_lo + c), n0, leader_addr(&full[s]));
         }
         __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
     }
     if (!ok) {
@@ -239,7 +250,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- MMA issuer, leader
     if (leader) {
       const uint32_t idesc = idesc_f16_f32(256, p.bn), idesc_l = idesc_bf16(256, p.bn);
-      uint32_t cnt = 0, lcnt = 0, it = 0;
+      uint32_t it = 0;
+      int s = 0, ls = 0;
+      uint32_t ph = 0, lph = 0;
       bool ok = true;
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const uint32_t acc = tmem + 256 * (it & 1);
@@ -254,9 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int due = nl ? nk / 2 + gap : nk + 1;
         if (!(ok = warp_wait(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
         tc_fence_after();
-        for (int c = 0; c < nk; ++c, ++cnt) {
-          const int s = cnt % kStages;
-          if (!(ok = warp_wait(&full[s], (cnt / kStages) & 1, abort_flag, p.err, 83))) break;
+        for (int c = 0; c < nk; ++c) {
+          if (!(ok = warp_wait(&full[s], ph, abort_flag, p.err, 83))) break;
           tc_fence_after();
           if (elect_one_sync()) {
             const uint32_t base = smem_u32(smem + s * p.stage_bytes);
@@ -264,34 +276,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < 4; ++kk)
               mma2_f16_ss(acc, smem_desc_sw128(base + 32 * kk),
                           smem_desc_sw128(base + kOpBytes + 32 * kk), idesc, (c | kk) != 0);
-            mma2_commit_both(&empty[s]);
+            commit_both(&empty[s]);
           }
           __syncwarp();
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
           // the adapter stages that are due, evenly among the second half's
           // chunks (fixed places: the sums' order is that of every run)
           while (kLora && j < nl && (c + 1 >= due || c + 1 == nk)) {
-            const int ls = lcnt % p.lora_stages;
-            if (!(ok = warp_wait(&lora_full[ls], (lcnt / p.lora_stages) & 1, abort_flag, p.err, 84))) break;
+            if (!(ok = warp_wait(&lora_full[ls], lph, abort_flag, p.err, 84))) break;
             tc_fence_after();
             if (elect_one_sync()) {
               const uint32_t base = smem_u32(lora + ls * p.lora_stage_bytes);
               const uint64_t bd = smem_desc_sw32(base + 2 * kLoraTile);
               mma2_f16_ss(acc, smem_desc_sw32(base), bd, idesc_l, 1);
               mma2_f16_ss(acc, smem_desc_sw32(base + kLoraTile), bd, idesc_l, 1);
-              mma2_commit_both(&lora_empty[ls]);
+              commit_both(&lora_empty[ls]);
             }
             __syncwarp();
+            if (++ls == p.lora_stages) {
+              ls = 0;
+              lph ^= 1;
+            }
             ++j;
-            ++lcnt;
             due += gap;
           }
           if (!ok) break;
         }
         if (!ok) break;
-        if (elect_one_sync()) mma2_commit_both(&acc_full[it & 1]);
+        if (elect_one_sync()) commit_both(&acc_full[it & 1]);
         __syncwarp();
       }
-      if (elect_one_sync()) mma2_commit_both(drain);
+      if (elect_one_sync()) commit_both(drain);
       __syncwarp();
     }
     // every MMA that reads this CTA's memory is done before it is released
@@ -305,7 +323,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int r0, r1;
       uint32_t lcnt = 0, it = 0;
       bool ok = true;
-      const uint32_t lora_full_l = leader_addr(lora_full);
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const int m0 = (u % p.mt) * kTileM, n0 = (u / p.mt) * p.bn;
         // the tile's distinct adapters, in the order of their first tokens
@@ -334,7 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int nad = rank_of(f0, f1, i, s_cnt, r0, r1);
         if (f0) s_list[r0] = ru0;
         if (f1) s_list[r1] = ru1;
-        const int nl = rb * nad;
+        // of the tile's rb x nad stages every split-th is this pair's
+        const int nl = (rb * nad - part + split - 1) / split;
         // the count of two tiles ago has been read once that tile is done
         if (it >= 2) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
         if (!(ok = bar_and(ok))) break;
@@ -344,14 +362,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int my_id = rank ? id1 : id0;
         const float* hrow = p.a.h + (size_t)min(m0 + 128 * (int)rank + i, p.a.T - 1) * p.a.rank;
-        // stage j: columns 16 (j % rb) .. + 15 of adapter j / rb of the list;
-        // this thread's h is loaded a stage ahead
+        // the tile's stage g: columns 16 (g % rb) .. + 15 of adapter g / rb of
+        // the list; this thread's h is loaded a stage ahead
         float4 v[4], nv[4];
         auto load_h = [&](int j) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) nv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j < nl && s_list[j / rb] == my_id) {
-            const int c = 16 * (j % rb);
+          const int gj = part + j * split;
+          if (j < nl && s_list[gj / rb] == my_id) {
+            const int c = 16 * (gj % rb);
             const float4* h4 = reinterpret_cast<const float4*>(hrow + c);
             nv[0] = __ldcg(h4);
             nv[1] = __ldcg(h4 + 1);
@@ -374,8 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = bar_and(ok))) break;
           const uint32_t full_l = leader_addr(&lora_full[ls]);
           if (i == 0)
-            tma_load_3d_pair(stage + 2 * kLoraTile, &p.mb, 16 * (j % rb), n0 + half * (int)rank,
-                             s_list[j / rb], full_l);
+            tma_load_3d_pair(stage + 2 * kLoraTile, &p.mb, 16 * ((part + j * split) % rb),
+                             n0 + half * (int)rank, s_list[(part + j * split) / rb], full_l);
           const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
           uint32_t hi[8], lo[8];
@@ -431,7 +450,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int n = n0 + c0;
         uint16_t* o = p.a.y + t * p.a.y_ld + n;
-        if (!live) {
+        if (split > 1) {
+          // this part's sums, [column][row], where the operands were (all
+          // of the pair's MMAs are done)
+          float* sums = reinterpret_cast<float*>(smem) + c0 * 128 + row;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sums[128 * e] = __uint_as_float(v[e]);
+        } else if (!live) {
         } else if (wide && n + 32 <= p.a.N) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -451,6 +476,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (split > 1) {
+    // The parts' sums, added in order over distributed shared memory: pair
+    // `part` writes columns part x BN / split .. of the tile, 8 warps of a CTA
+    // a quarter of its rows and half of these columns each.
+    __syncthreads();
+    cluster_sync_all();
+    if (warp >= 2 && !*abort_flag) {
+      const int row = 32 * (warp & 3) + lane, t = (pair % p.mt) * kTileM + 128 * (int)rank + row;
+      const int cols = p.bn / split, n0 = (pair / p.mt) * p.bn;
+      const bool live = t < p.a.T;
+      const float sc = live && p.a.x_scale ? __ldg(p.a.x_scale + t) : 1.f;
+      const bool wide = (p.a.y_ld & 7) == 0 && (reinterpret_cast<uintptr_t>(p.a.y) & 15u) == 0;
+      const int c_end = part * cols + (warp >= 6 ? cols : cols / 2);
+      for (int c0 = part * cols + (warp >= 6 ? cols / 2 : 0); c0 < c_end; c0 += 16) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int q = 0; q < split; ++q) {
+          const uint32_t src = cta_addr(reinterpret_cast<float*>(smem) + c0 * 128 + row, 2 * q + rank);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float o;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(src + 512u * e) : "memory");
+            v[e] += o;
+          }
+        }
+        const int n = n0 + c0;
+        uint16_t* o = p.a.y + t * p.a.y_ld + n;
+        if (!live) {
+        } else if (wide && n + 16 <= p.a.N) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            reinterpret_cast<uint4*>(o)[q] =
+                make_uint4(pack_bf16x2(v[8 * q] * sc, v[8 * q + 1] * sc),
+                           pack_bf16x2(v[8 * q + 2] * sc, v[8 * q + 3] * sc),
+                           pack_bf16x2(v[8 * q + 4] * sc, v[8 * q + 5] * sc),
+                           pack_bf16x2(v[8 * q + 6] * sc, v[8 * q + 7] * sc));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (n + e < p.a.N) o[e] = f32_to_bf16(v[e] * sc);
+        }
+      }
+    }
+  }
   __syncthreads();
   tc_fence_before();
   cluster_sync_all();
@@ -462,48 +532,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace lin
 
-// Tile width: rounds of tiles over the pairs, each at the slower of its MMAs
-// (2 cycles per column and chunk) and its operands' copies (about 50 bytes per
-// cycle and SM).
-int linear_tile_n(int T, int N, int num_sms) {
-  const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2;
-  int best = 256;
+// Tile width and parts of K, by estimated cycles: rounds of tiles over the
+// pairs, each chunk at the slower of its MMAs (2 cycles per column) and its
+// operands' copies (about 50 bytes per cycle and SM). Where wide tiles leave
+// most SMs idle, narrow ones copy the same token rows over and over; cutting K
+// over 2 or 4 pairs of a cluster keeps the tiles wide, for the sums' exchange.
+static void linear_shape(int T, int N, int K, int num_sms, int* bn_out, int* split_out) {
+  const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2, nk = K / 64;
   double cost = 1e30;
-  for (int bn = 256; bn >= 32; bn -= 32) {
-    const long long tiles = (long long)mt * ((N + bn - 1) / bn);
-    const double chunk = fmax(2.0 * bn, (16384.0 + 64.0 * bn) / 50.0);
-    const double c = (double)((tiles + pairs - 1) / pairs) * chunk;
-    if (c < cost * 0.999) {
-      cost = c;
-      best = bn;
+  for (int split = 1; split <= 4; split *= 2)
+    for (int bn = 256; bn >= 32; bn -= 32) {
+      const long long tiles = (long long)mt * ((N + bn - 1) / bn);
+      // (a slice of whole 32-column steps per part; clusters of 4 and 8 CTAs
+      // that the device holds at once)
+      if (split > 1 && (bn % (32 * split) || nk < 2 * split || tiles > (split == 2 ? 32 : 16))) continue;
+      const double chunk = fmax(2.0 * bn, (16384.0 + 64.0 * bn) / 50.0);
+      const double c = (double)((tiles + pairs - 1) / pairs) * chunk * ((nk + split - 1) / split) +
+                       (split > 1 ? 1500.0 + 8.0 * bn : 0.0);
+      if (c < cost * 0.999) {
+        cost = c;
+        *bn_out = bn;
+        *split_out = split;
+      }
     }
-  }
-  return best;
 }
 
-cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap& mw,
-                             int bn, DevErr err, int num_sms, cudaStream_t st) {
+cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap* mw,
+                             DevErr err, int num_sms, cudaStream_t st) {
+  int bn = 256, split = 1;
+  linear_shape(a.T, a.N, a.K, num_sms, &bn, &split);
   lin::Params p;
   p.mx = mx;
-  p.mw = mw;
+  p.mw = mw[bn / 32 - 1];
+  p.split = split;
   if (a.la && !encode_lora_b(&p.mb, a.lb, a.n_adapters, a.N, a.rank, bn / 2)) return cudaErrorInvalidValue;
   p.a = a;
   p.bn = bn;
   p.mt = (a.T + lin::kTileM - 1) / lin::kTileM;
   p.tiles = p.mt * ((a.N + bn - 1) / bn);
   p.err = err;
-  int pairs = num_sms / 2;
-  if (pairs > p.tiles) pairs = p.tiles;
+  int clusters = split > 1 ? p.tiles : num_sms / 2;
+  if (clusters > p.tiles) clusters = p.tiles;
   p.stage_bytes = lin::stage_bytes(bn);
   p.lora_stage_bytes = lin::lora_stage_bytes(bn);
-  const int ns = a.la ? lin::stages<true>() : lin::stages<false>();
-  const int fixed = ns * p.stage_bytes + (a.la ? lin::kIdsBytes : 0) + lin::kBarBytes;
-  p.lora_stages = a.la ? (lin::kSmemMax - fixed) / p.lora_stage_bytes : 0;
-  if (p.lora_stages > lin::kMaxLoraStages) p.lora_stages = lin::kMaxLoraStages;
-  const int smem = fixed + p.lora_stages * p.lora_stage_bytes + 1024;
+  // two adapter stages at least, four where the tile is narrow
+  p.lora_stages = a.la ? (bn > 128 ? 2 : 4) : 0;
+  const int fixed = (a.la ? lin::kIdsBytes : 0) + lin::kBarBytes + p.lora_stages * p.lora_stage_bytes;
+  p.stages = (lin::kSmemMax - fixed) / p.stage_bytes;
+  if (p.stages > lin::kMaxStages) p.stages = lin::kMaxStages;
+  const int smem = fixed + p.stages * p.stage_bytes + 1024;
   auto go = [&](auto kern) {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(2 * pairs), dim3(lin::kThreads), smem, st, p);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * split * clusters);
+    cfg.blockDim = dim3(lin::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
   };
   return a.la ? go(lin::linear_tc_kernel<true>) : go(lin::linear_tc_kernel<false>);
 }

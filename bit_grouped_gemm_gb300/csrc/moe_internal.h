@@ -243,14 +243,13 @@ constexpr int kLinearSmallT = 32;
 cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st);
 // Above: x as fp16 rows x16 [T][K], W as fp16 w16 [N][K] (both with every
 // block of 8 columns in perm8 order) and the adapters' h in one launch, then
-// the product on SM pairs. mw: w16 with boxes of 64 x linear_tile_n / 2.
+// the product on SM pairs. mw: w16 with boxes of 64 x 16, 32, .. 128 rows.
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
                                int num_sms, cudaStream_t st);
 // 3D map of adapters' B, bf16 [n][N][rank], in boxes of 16 columns x box_rows
 // rows, 32-byte swizzle.
 bool encode_lora_b(CUtensorMap* m, const void* base, int n, int N, int rank, uint32_t box_rows);
-int linear_tile_n(int T, int N, int num_sms);
-cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap& mw,
-                             int bn, DevErr err, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap* mw,
+                             DevErr err, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -20,6 +20,12 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
+// Address, in CTA `rank` of the cluster, of this CTA's shared variable `p`.
+__device__ __forceinline__ uint32_t cta_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
 // Arrival on a barrier given by its cluster address, after a release fence
 // restricted to shared::cta memory: orders the shared-memory writes this
 // thread has observed (a token tile landed by TMA) before the arrival. A full
@@ -57,6 +63,15 @@ __device__ __forceinline__ void tmem_alloc2(uint32_t* slot, uint32_t ncols) {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
+}
+// Arrive on the barrier at `bar`'s offset in the cluster's CTAs of `mask` once
+// every MMA issued so far by this thread is done.
+__device__ __forceinline__ void mma2_commit_mask(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
 }
 // Arrive on the barrier at `bar`'s offset in both CTAs once every MMA issued
 // so far by this thread is done.
