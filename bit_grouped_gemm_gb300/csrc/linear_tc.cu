@@ -57,24 +57,28 @@ struct Params {
   DevErr err;
 };
 
+// Whole-warp bounded wait. kCluster: with the acquire over the cluster that the
+// other CTA's own stores need; copies and MMAs that complete on the barrier do
+// not, and the narrower one is cheaper.
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           const DevErr& err, int site) {
-  bool ok = try_wait_cluster(bar, parity, 0);
-  if (!ok) {
+  auto look = [&](uint32_t hint) {
+    if constexpr (kCluster) return try_wait_cluster(bar, parity, hint);
+    else return hint ? mbar_try_wait_sleep(bar, parity, hint) : mbar_try_wait(bar, parity);
+  };
+  bool ok = look(0);
+  if (!__all_sync(0xffffffffu, ok)) {
     const unsigned long long t0 = globaltimer_ns();
-    while (true) {
-      if (try_wait_cluster(bar, parity, 100000)) {
-        ok = true;
-        break;
-      }
-      if (*abort_flag) break;
-      if (globaltimer_ns() - t0 > err.limit_ns) break;
+    while (!ok) {
+      ok = look(100000);
+      if (ok || *abort_flag || globaltimer_ns() - t0 > err.limit_ns) break;
     }
-  }
-  ok = __all_sync(0xffffffffu, ok);
-  if (!ok) {
-    if ((threadIdx.x & 31) == 0 && !*abort_flag) report_timeout(err, site);
-    *abort_flag = 1;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      if ((threadIdx.x & 31) == 0 && !*abort_flag) report_timeout(err, site);
+      *abort_flag = 1;
+    }
   }
   return ok;
 }
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // -------------------------------------------------- MMA issuer, leader
     if (leader) {
+      const uint64_t ring_desc = smem_desc_sw128(smem_u32(smem));
       const uint32_t idesc = idesc_f16_f32(256, p.bn), idesc_l = idesc_bf16(256, p.bn);
       uint32_t it = 0;
       int s = 0, ls = 0;
@@ -271,11 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&full[s], ph, abort_flag, p.err, 83))) break;
           tc_fence_after();
           if (elect_one_sync()) {
-            const uint32_t base = smem_u32(smem + s * p.stage_bytes);
+            // (a descriptor's low bits are the address over 16)
+            const uint64_t ad = ring_desc + (uint32_t)(s * p.stage_bytes >> 4), bd = ad + (kOpBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma2_f16_ss(acc, smem_desc_sw128(base + 32 * kk),
-                          smem_desc_sw128(base + kOpBytes + 32 * kk), idesc, (c | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk) mma2_f16_ss(acc, ad + 2 * kk, bd + 2 * kk, idesc, (c | kk) != 0);
             commit_both(&empty[s]);
           }
           __syncwarp();
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the adapter stages that are due, evenly among the second half's
           // chunks (fixed places: the sums' order is that of every run)
           while (kLora && j < nl && (c + 1 >= due || c + 1 == nk)) {
-            if (!(ok = warp_wait(&lora_full[ls], lph, abort_flag, p.err, 84))) break;
+            if (!(ok = warp_wait<true>(&lora_full[ls], lph, abort_flag, p.err, 84))) break;
             tc_fence_after();
             if (elect_one_sync()) {
               const uint32_t base = smem_u32(lora + ls * p.lora_stage_bytes);
