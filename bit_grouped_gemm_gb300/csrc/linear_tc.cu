@@ -23,7 +23,8 @@
 namespace moe {
 namespace lin {
 
-constexpr int kThreads = 320;             // TMA, MMA, 4 adapter, 4 epilogue warps
+constexpr int kThreads = 352;             // TMA, 1 or 2 MMA, 4 adapter, 4 epilogue warps
+constexpr int kMma2Warp = 10;
 constexpr int kTileM = 256;
 constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
 constexpr uint32_t kTmemCols = 512;
@@ -151,7 +152,8 @@ __device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra,
   return n;
 }
 
-template <bool kLora>
+// kIssuers: MMA warps, 2 where a pair has one tile, else 1.
+template <bool kLora, int kIssuers>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ Params p) {
   const int stages = p.stages;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_full[i], kIssuers);
       mbar_init(&acc_empty[i], 8);
       mbar_init(&list_full[i], 1);
     }
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&lora_full[i], 2);
       mbar_init(&lora_empty[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, kIssuers);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.mx);
@@ -250,46 +252,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned long long t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------- MMA issuer, leader
-    if (leader) {
+  } else if (warp == 1 || warp == kMma2Warp) {
+    // ------------------------------------------------- MMA issuers, leader
+    // Issuing a chunk (a wait, four MMAs, a commit) takes a warp about 450
+    // cycles, the MMAs themselves 2 cycles per column. With one tile per pair
+    // both accumulators are free for it, so two warps take alternate chunks,
+    // and alternate adapter stages, into one each, and the epilogue adds them.
+    const int me = warp == 1 ? 0 : 1;
+    if (leader && me < kIssuers) {
       const uint64_t ring_desc = smem_desc_sw128(smem_u32(smem));
       const uint32_t idesc = idesc_f16_f32(256, p.bn), idesc_l = idesc_bf16(256, p.bn);
       uint32_t it = 0;
-      int s = 0, ls = 0;
+      int s = me, ls = me;
       uint32_t ph = 0, lph = 0;
+      if (s >= stages) s -= stages, ph ^= 1;
       bool ok = true;
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
-        const uint32_t acc = tmem + 256 * (it & 1);
+        const int buf = kIssuers == 2 ? me : (int)(it & 1);
+        const uint32_t acc = tmem + 256 * buf;
         int nl = 0;
         if (kLora) {
           if (!(ok = warp_wait(&list_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 81))) break;
           nl = s_steps[it & 1];
         }
-        int j = 0;
-        // the first stage's place, and the chunks between two of them
+        // this warp's adapter stages: the first one's place, and the chunks
+        // between two of them
+        int j = me;
         const int gap = nl ? (nk - nk / 2) / (nl + 1) : 0;
-        int due = nl ? nk / 2 + gap : nk + 1;
-        if (!(ok = warp_wait(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
+        int due = nk / 2 + gap * (me + 1);
+        if (kIssuers == 1 && !(ok = warp_wait<true>(&acc_empty[buf], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
         tc_fence_after();
-        for (int c = 0; c < nk; ++c) {
+        for (int c = me; c < nk; c += kIssuers) {
           if (!(ok = warp_wait(&full[s], ph, abort_flag, p.err, 83))) break;
           tc_fence_after();
           if (elect_one_sync()) {
             // (a descriptor's low bits are the address over 16)
             const uint64_t ad = ring_desc + (uint32_t)(s * p.stage_bytes >> 4), bd = ad + (kOpBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma2_f16_ss(acc, ad + 2 * kk, bd + 2 * kk, idesc, (c | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk) mma2_f16_ss(acc, ad + 2 * kk, bd + 2 * kk, idesc, (c != me) | (kk != 0));
             commit_both(&empty[s]);
           }
           __syncwarp();
-          if (++s == stages) {
-            s = 0;
+          s += kIssuers;
+          if (s >= stages) {
+            s -= stages;
             ph ^= 1;
           }
           // the adapter stages that are due, evenly among the second half's
           // chunks (fixed places: the sums' order is that of every run)
-          while (kLora && j < nl && (c + 1 >= due || c + 1 == nk)) {
+          while (kLora && j < nl && (c + 1 >= due || c + kIssuers >= nk)) {
             if (!(ok = warp_wait<true>(&lora_full[ls], lph, abort_flag, p.err, 84))) break;
             tc_fence_after();
             if (elect_one_sync()) {
@@ -300,17 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit_both(&lora_empty[ls]);
             }
             __syncwarp();
-            if (++ls == p.lora_stages) {
-              ls = 0;
+            ls += kIssuers;
+            if (ls >= p.lora_stages) {
+              ls -= p.lora_stages;
               lph ^= 1;
             }
-            ++j;
-            due += gap;
+            j += kIssuers;
+            due += gap * kIssuers;
           }
           if (!ok) break;
         }
         if (!ok) break;
-        if (elect_one_sync()) commit_both(&acc_full[it & 1]);
+        if (elect_one_sync()) commit_both(&acc_full[kIssuers == 2 ? 0 : it & 1]);
         __syncwarp();
       }
       if (elect_one_sync()) commit_both(drain);
@@ -447,6 +459,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[32];
         tmem_ld_32x32b_x32(tmem + lane_base + 256 * (it & 1) + c0, v);
         tmem_wait_ld();
+        if (kIssuers == 2) {
+          uint32_t v2[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + 256 + c0, v2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(v2[e]));
+        }
         if (c0 + 32 >= p.bn) {
           tc_fence_before();
           __syncwarp();
@@ -486,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a quarter of its rows and half of these columns each.
     __syncthreads();
     cluster_sync_all();
-    if (warp >= 2 && !*abort_flag) {
+    if (warp >= 2 && warp < 10 && !*abort_flag) {
       const int row = 32 * (warp & 3) + lane, t = (pair % p.mt) * kTileM + 128 * (int)rank + row;
       const int cols = p.bn / split, n0 = (pair / p.mt) * p.bn;
       const bool live = t < p.a.T;
@@ -537,23 +557,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace lin
 
 // Tile width and parts of K, by estimated cycles: rounds of tiles over the
-// pairs, each chunk at the slower of its MMAs (2 cycles per column) and its
-// operands' copies (about 50 bytes per cycle and SM). Where wide tiles leave
-// most SMs idle, narrow ones copy the same token rows over and over; cutting K
-// over 2 or 4 pairs of a cluster keeps the tiles wide, for the sums' exchange.
+// pairs, each chunk at the slowest of its MMAs (2 cycles per column), its issue
+// (300), its operands' copies at 75 bytes per cycle into an SM, and at 8000 out
+// of L2. Of tiles that come out alike the widest is taken: fewer CTAs then read
+// the same lines. Measured, call by call, at K = 2048 without adapters (widths
+// 64, 128, 192, 224, 256): 512 x 2048 14.7, 13.4, -, -, 17.3 us; 1024 x 2048 -,
+// 16.7, 16.2, 17.3, 18.5; 4096 x 2048 -, 36.5, 33.3, 36.0, 31.2; 4096 x 4096 -,
+// 55.7, 48.9, 46.4, 49.5.
+// With few tiles, two pairs of a cluster take half of K each, for the exchange of
+// their sums: 256 x 2048 11.9 against 13.0 us, with 8 adapters 16.1 against 17.0;
+// but 512 x 2048 16.1 against 13.4. (Four pairs: 19.2 against 12.3 at 128 x 2048;
+// the device holds 15 clusters of 8 such CTAs.)
 static void linear_shape(int T, int N, int K, int num_sms, int* bn_out, int* split_out) {
   const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2, nk = K / 64;
   double cost = 1e30;
-  for (int split = 1; split <= 4; split *= 2)
+  for (int split = 1; split <= 2; ++split)
     for (int bn = 256; bn >= 32; bn -= 32) {
       const long long tiles = (long long)mt * ((N + bn - 1) / bn);
-      // (a slice of whole 32-column steps per part; clusters of 4 and 8 CTAs
-      // that the device holds at once)
-      if (split > 1 && (bn % (32 * split) || nk < 2 * split || tiles > (split == 2 ? 32 : 16))) continue;
-      const double chunk = fmax(2.0 * bn, (16384.0 + 64.0 * bn) / 50.0);
+      if (split > 1 && (bn % 64 || nk < 4 || tiles > 32)) continue;
+      const double bytes = 16384.0 + 64.0 * bn, sms = 2.0 * fmin((double)(tiles * split), (double)pairs);
+      const double chunk = fmax(fmax(2.0 * bn, 300.0), fmax(bytes / 75.0, bytes * sms / 8000.0));
       const double c = (double)((tiles + pairs - 1) / pairs) * chunk * ((nk + split - 1) / split) +
-                       (split > 1 ? 1500.0 + 8.0 * bn : 0.0);
-      if (c < cost * 0.999) {
+                       (split > 1 ? 1500.0 + 21.0 * bn : 0.0);
+      if (c < cost * 0.97) {
         cost = c;
         *bn_out = bn;
         *split_out = split;
@@ -577,6 +603,7 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   p.err = err;
   int clusters = split > 1 ? p.tiles : num_sms / 2;
   if (clusters > p.tiles) clusters = p.tiles;
+  const bool two = p.tiles <= clusters && a.K >= 2 * 64 * split;
   p.stage_bytes = lin::stage_bytes(bn);
   p.lora_stage_bytes = lin::lora_stage_bytes(bn);
   // two adapter stages at least, four where the tile is narrow
@@ -603,7 +630,8 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
-  return a.la ? go(lin::linear_tc_kernel<true>) : go(lin::linear_tc_kernel<false>);
+  return a.la ? (two ? go(lin::linear_tc_kernel<true, 2>) : go(lin::linear_tc_kernel<true, 1>))
+              : (two ? go(lin::linear_tc_kernel<false, 2>) : go(lin::linear_tc_kernel<false, 1>));
 }
 
 }  // namespace moe
