@@ -85,9 +85,8 @@ cudaError_t launch_route_large(const float* logits, int T, int E, int k, int32_t
                                int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* gen,
                                DevErr err, const uint16_t* x, uint16_t* xs, int H,
                                int with_shared, cudaStream_t st);
-// Routing by scores, from given logits (moe_route_scored): in one launch
-// (cooperative unless one CTA is enough; `table` holds E bytes per CTA, at
-// most one per 16 tokens; `arrive` and `left` are 0 between launches), or,
+// Routing by scores, from given logits (moe_route_scored): in one or two
+// launches (`table` holds E bytes per CTA, at most one per 16 tokens), or,
 // beyond score_route_fits, the choice alone, to be followed by
 // launch_route_scan and launch_route_scatter.
 struct ScoreArgs {
@@ -99,8 +98,7 @@ bool score_route_fits(int T, int num_sms);
 cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, int E, int k,
                                int32_t* topk_idx, float* topk_w, uint8_t* table, int32_t* cnt,
                                int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
-                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* left,
-                               DevErr err, int num_sms, cudaStream_t st);
+                               int32_t* perm, int32_t* inv, int num_sms, cudaStream_t st);
 cudaError_t launch_score_topk(const ScoreArgs& a, const float* logits, int T, int E, int k,
                               int32_t* topk_idx, float* topk_w, int32_t* blk_cnt, cudaStream_t st);
 cudaError_t launch_gather_rows(const uint16_t* x, const int32_t* perm, int T, int k, int H,

@@ -66,8 +66,7 @@ Layout make_layout(const moe_plan_desc& d) {
   L.bmap2 = take((size_t)L.max_tiles2 * 3 * 4);
   L.num_tiles2 = take(16);
   L.err = take(16);
-  L.arrive = take(24);   // route_large arrivals and generation, fused-layer barrier, launch
-                         // count, scored routing arrivals and departures
+  L.arrive = take(16);   // route_large arrivals and generation, fused-layer barrier, launch count
   L.tlogits = take(tlogits_bytes(d));
   L.sk_cnt = take(kSplitSlots * 4);
   L.sk_ws = take((size_t)kSplitSlots * kSplitSlotBytes);
@@ -644,7 +643,7 @@ moe_status moe_plan_create(const moe_plan_desc* desc, int device, moe_plan_t* ou
     return MOE_ERR_CUDA;
   }
   cudaMemset(p->scratch + p->L.err, 0, 16);
-  cudaMemset(p->scratch + p->L.arrive, 0, 24);
+  cudaMemset(p->scratch + p->L.arrive, 0, 16);
   cudaMemset(p->scratch + p->L.tlogits, 0, tlogits_bytes(*desc));
   cudaMemset(p->scratch + p->L.sk_cnt, 0, kSplitSlots * 4);
   bool ok = true;
@@ -747,12 +746,11 @@ moe_status moe_route_scored(moe_plan_t p, const float* logits, int T, const moe_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (score_route_fits(T, p->num_sms)) {
     // (the CTAs' byte table, a row per 16 tokens at most, fits the blocks' counts)
-    unsigned* w = p->at<unsigned>(p->L.arrive) + 4;
     return st_of(timed(p, 8, st, [&] {
       return launch_score_route(a, logits, T, E, k, r->topk_idx, r->topk_w,
                                 p->at<uint8_t>(p->L.blk_cnt), r->counts, r->offsets,
-                                r->tile_offsets, r->block_map, r->num_tiles, r->perm, r->inv, w,
-                                w + 1, p->err(), p->num_sms, st);
+                                r->tile_offsets, r->block_map, r->num_tiles, r->perm, r->inv,
+                                p->num_sms, st);
     }));
   }
   const int nblk = (T + kRouterTB - 1) / kRouterTB;
@@ -882,7 +880,7 @@ moe_status moe_get_error(moe_plan_t p) {
   if (e == cudaSuccess) e = cudaMemset(p->at<int>(p->L.err), 0, 8);
   // a launch that gave up at a barrier leaves its arrival counters set, and
   // the fused layer's launch count and tagged logits may disagree
-  if (e == cudaSuccess && (h[0] & DEVERR_TIMEOUT_BIT)) e = cudaMemset(p->at<int>(p->L.arrive), 0, 24);
+  if (e == cudaSuccess && (h[0] & DEVERR_TIMEOUT_BIT)) e = cudaMemset(p->at<int>(p->L.arrive), 0, 16);
   if (e == cudaSuccess && (h[0] & DEVERR_TIMEOUT_BIT))
     e = cudaMemset(p->scratch + p->L.tlogits, 0, tlogits_bytes(p->d));
   // so may the split last round's counters of a GEMM that gave up

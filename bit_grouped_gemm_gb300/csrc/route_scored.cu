@@ -2,13 +2,19 @@
 // (score_topk.cuh), then counts, offsets, tile offsets, the stable scatter and
 // the block map, as moe_route makes them.
 //
-// One launch: CTA b takes tokens [b C, (b + 1) C), a warp a token at a time,
-// and keeps its choices and, per expert, a bit for each of its tokens in
-// shared memory. Its counts go to a byte table [CTA][expert]; after a grid
-// barrier every CTA reads the whole table, which gives it all totals and its
-// own starting positions, and writes its slots: position = start + earlier
-// tokens of the CTA that chose the expert (a popcount of the bits below). The
-// block map is dealt over the CTAs by expert.
+// CTA b takes tokens [b C, (b + 1) C), a warp a token at a time, and keeps, per
+// expert, a bit for each of its tokens that chose it. Its counts go to a byte
+// table [CTA][expert]; once all are there, every CTA reads the whole table, which
+// gives it all totals and its own starting positions, and writes its slots:
+// position = start + earlier tokens of the CTA that chose the expert (a popcount
+// of the bits below). The block map is dealt over the CTAs by expert.
+//
+// Up to 32 tokens are one CTA's, in one launch. More are two launches, the
+// choice and the placing. (With a grid barrier in one cooperative launch the GPU
+// spent as long, 11.6 us at 4096 x 256 with 8 groups in a graph, but in a stream
+// a cooperative launch waits 3 us longer for its turn.)
+#include <type_traits>
+
 #include "score_topk.cuh"
 
 namespace moe {
@@ -26,51 +32,15 @@ struct ScParams {
   float* w;
   uint8_t* table;                     // [CTAs][E]
   int32_t *cnt, *off, *tile_off, *bmap, *num_tiles, *perm, *inv;
-  unsigned *arrive, *left;
-  DevErr err;
 };
 
-__device__ __forceinline__ unsigned ld_relaxed(const unsigned* p) {
-  unsigned v;
-  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
+// kPart: kAll in one CTA, or kChoose and then kPlace.
+enum { kAll, kChoose, kPlace };
 
-// Grid barrier of a cooperative launch, bounded: thread 0 counts its CTA in and
-// polls the count itself (no second word to wait for). The CTAs count
-// themselves out at their end, and the last one sets both words back to 0.
-__device__ __forceinline__ bool grid_arrive_wait(unsigned* arrive, const DevErr& err, int site) {
-  __shared__ int go;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();   // the CTA's table row, before its arrival
-    asm volatile("red.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(arrive) : "memory");
-    int ok = 1;
-    const unsigned long long start = globaltimer_ns();
-    while (ld_relaxed(arrive) < gridDim.x) {
-      if (globaltimer_ns() - start > err.limit_ns) {
-        report_timeout(err, site);
-        ok = 0;
-        break;
-      }
-    }
-    asm volatile("fence.acq_rel.gpu;" ::: "memory");
-    go = ok;
-  }
-  __syncthreads();
-  return go != 0;
-}
-__device__ __forceinline__ void grid_leave(unsigned* arrive, unsigned* left) {
-  if (threadIdx.x == 0 && atomicAdd(left, 1u) == gridDim.x - 1) {
-    *left = 0u;
-    *arrive = 0u;
-  }
-}
-
-template <int VPL>
+template <int VPL, int kPart>
 __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams p) {
   constexpr int kE = 32 * VPL;
-  extern __shared__ float dyn[];           // [32 warps][kE], later the partial sums
+  extern __shared__ float dyn[];           // a row per warp; kPlace: the partial sums
   __shared__ unsigned mask_s[kScWords * kE];   // [word][expert]
   __shared__ int start_s[kE];
   __shared__ int wrows_s[16], wtiles_s[16];
@@ -83,26 +53,36 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
   __syncthreads();
   pdl_begin();
 
-  for (int tl = warp; tl < nt; tl += kScThreads / 32) {
-    const size_t t = t0 + tl;
-    int idx;
-    float w;
-    score_select<VPL>(p.logits + t * E, E, k, p.s, dyn + warp * max(kE, 64), idx, w);
-    if (lane < k) {
-      p.idx[t * k + lane] = idx;
-      p.w[t * k + lane] = w;
-      idx_s[tl * k + lane] = (uint16_t)idx;
-      atomicOr(&mask_s[(tl >> 5) * kE + idx], 1u << (tl & 31));
+  if constexpr (kPart != kPlace) {
+    for (int tl = warp; tl < nt; tl += kScThreads / 32) {
+      const size_t t = t0 + tl;
+      int idx;
+      float w;
+      score_select<VPL>(p.logits + t * E, E, k, p.s, dyn + warp * max(kE, 64), idx, w);
+      if (lane < k) {
+        p.idx[t * k + lane] = idx;
+        p.w[t * k + lane] = w;
+        if (kPart == kAll) idx_s[tl * k + lane] = (uint16_t)idx;
+        atomicOr(&mask_s[(tl >> 5) * kE + idx], 1u << (tl & 31));
+      }
+      __syncwarp();
     }
-    __syncwarp();
+  } else {
+    for (int i = tid; i < nt * k; i += kScThreads) {
+      const int tl = i / k, e = __ldcg(p.idx + (size_t)t0 * k + i);
+      idx_s[i] = (uint16_t)e;
+      atomicOr(&mask_s[(tl >> 5) * kE + e], 1u << (tl & 31));
+    }
   }
   __syncthreads();
   int tot = 0, before = 0;                 // thread e < E: all CTAs', earlier CTAs'
-  if (tid < E)
+  if (kPart != kPlace && tid < E)
     for (int i = 0; i < words; ++i) tot += __popc(mask_s[i * kE + tid]);
-  if (G > 1) {
+  if constexpr (kPart == kChoose) {
     if (tid < E) p.table[(size_t)b * E + tid] = (uint8_t)tot;
-    if (!grid_arrive_wait(p.arrive, p.err, 60)) return;
+    return;
+  }
+  if constexpr (kPart == kPlace) {
     // the table, 4 experts per thread, the rows dealt over the rest of the
     // threads: totals in the low halves, earlier CTAs' in the high halves
     uint32_t* part = reinterpret_cast<uint32_t*>(dyn);   // [rows' share][E]
@@ -193,7 +173,6 @@ __global__ void __launch_bounds__(kScThreads) score_route_kernel(const ScParams 
     p.perm[pos] = slot;
     p.inv[slot] = pos;
   }
-  if (G > 1) grid_leave(p.arrive, p.left);
 }
 
 // The choice alone, 32 tokens per CTA, with the block's counts as
@@ -240,14 +219,14 @@ ScoreDev dev_of(const ScoreArgs& a, int E) {
   return s;
 }
 
-// dynamic shared memory: a row per warp; the partial sums take at most as much
+// dynamic shared memory: a row per warp, or the partial sums (1024 threads' four)
+constexpr int kPartBytes = kScThreads * 16;
 constexpr int dyn_bytes(int vpl) { return 32 * 32 * (vpl < 4 ? 4 : vpl) * 4; }
 
 }  // namespace
 
-// Tokens per CTA and CTAs of the one-launch form. One CTA up to 32 tokens (a
-// token per warp, no grid barrier); then 16 tokens a CTA until every SM has
-// one.
+// Tokens per CTA and CTAs: one CTA up to 32 tokens (a token per warp); then 16
+// tokens a CTA until every SM has one.
 static void score_grid(int T, int num_sms, int* C, int* G) {
   int g = T <= 32 ? 1 : (T + 15) / 16;
   if (g > num_sms) g = num_sms;
@@ -264,8 +243,7 @@ bool score_route_fits(int T, int num_sms) {
 cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, int E, int k,
                                int32_t* topk_idx, float* topk_w, uint8_t* table, int32_t* cnt,
                                int32_t* off, int32_t* tile_off, int32_t* bmap, int32_t* num_tiles,
-                               int32_t* perm, int32_t* inv, unsigned* arrive, unsigned* left,
-                               DevErr err, int num_sms, cudaStream_t st) {
+                               int32_t* perm, int32_t* inv, int num_sms, cudaStream_t st) {
   ScParams p;
   int G;
   score_grid(T, num_sms, &p.C, &G);
@@ -285,33 +263,21 @@ cudaError_t launch_score_route(const ScoreArgs& a, const float* logits, int T, i
   p.num_tiles = num_tiles;
   p.perm = perm;
   p.inv = inv;
-  p.arrive = arrive;
-  p.left = left;
-  p.err = err;
   auto go = [&](auto kern, int smem) -> cudaError_t {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
-    if (e != cudaSuccess) return e;
-    if (G == 1) return launch_pdl(kern, dim3(1), dim3(kScThreads), smem, st, p);
-    // cooperative (the CTAs wait on the last one), in ordinary stream order
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(G);
-    cfg.blockDim = dim3(kScThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(G), dim3(kScThreads), smem, st, p);
+  };
+  auto all = [&](auto vpl) -> cudaError_t {
+    constexpr int V = decltype(vpl)::value;
+    if (G == 1) return go(score_route_kernel<V, kAll>, dyn_bytes(V));
+    const cudaError_t e = go(score_route_kernel<V, kChoose>, dyn_bytes(V));
+    return e != cudaSuccess ? e : go(score_route_kernel<V, kPlace>, kPartBytes);
   };
   switch (vpl_of(E)) {
-    case 2: return go(score_route_kernel<2>, dyn_bytes(2));
-    case 4: return go(score_route_kernel<4>, dyn_bytes(4));
-    case 8: return go(score_route_kernel<8>, dyn_bytes(8));
-    default: return go(score_route_kernel<16>, dyn_bytes(16));
+    case 2: return all(std::integral_constant<int, 2>{});
+    case 4: return all(std::integral_constant<int, 4>{});
+    case 8: return all(std::integral_constant<int, 8>{});
+    default: return all(std::integral_constant<int, 16>{});
   }
 }
 

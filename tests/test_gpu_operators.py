@@ -240,6 +240,12 @@ def test_route_long():
     check_route(logits, 512, 10, bias=bias, score="softmax", renorm=False)
 
 
+def test_route_beyond_a_byte_per_cta():
+    """More tokens than the counts' byte table takes."""
+    g = gen(7)
+    check_route(randn(g, 36001, 32), 32, 3, bias=0.1 * randn(g, 32), score="sigmoid")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,tg", [(1, 1), (8, 4)])
 def test_route_scores_that_32_bits_cannot_order(score, groups, tg):
