@@ -12,10 +12,12 @@
 // The adapters are more columns of K. For every adapter that occurs among the
 // tile's tokens the tile gets rank K columns with h in A, zero in the rows of
 // other tokens, and B[a] in B: the MMAs then add each token's own product,
-// whatever the order of the tokens. They go by in stages of 16 columns, spread
-// between the tile's other chunks: four warps write A, B comes by TMA. h goes in
-// as two bf16 (the value and what its rounding left), each multiplied with B's
-// own bf16: the products are exact to 16 bits of h.
+// whatever the order of the tokens. They go by in stages of 16 columns, written
+// by four warps and spread between the tile's other chunks. h goes in as two
+// bf16 (the value and what its rounding left), each multiplied with B's own
+// bf16: the products are exact to 16 bits of h. A zero times an infinity or a NaN
+// would carry one adapter's broken B into other requests' rows, so B goes in with
+// these as zeros (which is why it does not come by TMA).
 //
 // Every wait is bounded, as in gemm_tc2.cu.
 #include "pair.cuh"
@@ -50,7 +52,6 @@ inline int lora_stage_bytes(int bn) { return 2 * kLoraTile + (bn / 2) * 32; }
 struct Params {
   CUtensorMap mx;       // x16 [rows][K], boxes 64 x 128
   CUtensorMap mw;       // W16 [N][K], boxes 64 x BN / 2
-  CUtensorMap mb;       // B [n][N][r], boxes 16 x BN / 2 x 1, 32-byte swizzle
   LinearArgs a;
   int bn, mt, tiles;    // tile width, token tiles, all tiles
   int split;            // pairs per tile, each a part of K (a cluster is 2 x split CTAs)
@@ -102,14 +103,9 @@ __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t smem_addr) {
   return d;
 }
 
-// 3D tiled load of this CTA's half of B, as tma_load_2d_pair.
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, int x, int y, int z,
-                                                 uint32_t cluster_bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
-      : "memory");
+// Two bf16 with infinities and NaNs as zeros.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
 }
 
 // Barrier of the 128 adapter threads that tells whether all of them go on, so
@@ -169,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + kMaxStages;              // chunk's MMAs done (both CTAs)
   uint64_t* acc_full = empty + kMaxStages;          // [2] tile's MMAs done (both CTAs)
   uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
-  uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs' adapter stage is there
+  uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs wrote their adapter stage
   uint64_t* lora_empty = lora_full + kMaxLoraStages;   // adapter stage's MMAs done (both CTAs)
   uint64_t* list_full = lora_empty + kMaxLoraStages;   // [2] the tile's adapter stages are known (own CTA)
   uint64_t* drain = list_full + 2;
@@ -206,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&p.mx);
     tma_prefetch_desc(&p.mw);
-    if (kLora) tma_prefetch_desc(&p.mb);
   }
   if (warp == 1) tmem_alloc2(tmem_slot, kTmemCols);
   tc_fence_before();
@@ -381,12 +376,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's stage g: columns 16 (g % rb) .. + 15 of adapter g / rb of
         // the list; this thread's h is loaded a stage ahead
         float4 v[4], nv[4];
+        uint4 nb0, nb1;   // and B's row of this thread
+        const int brow = n0 + half * (int)rank + i;
         auto load_h = [&](int j) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) nv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int gj = part + j * split;
-          if (j < nl && s_list[gj / rb] == my_id) {
-            const int c = 16 * (gj % rb);
+          nb0 = nb1 = make_uint4(0u, 0u, 0u, 0u);
+          if (j >= nl) return;
+          const int gj = part + j * split, ad = s_list[gj / rb], c = 16 * (gj % rb);
+          if (i < half && brow < p.a.N) {
+            const uint4* b4 = reinterpret_cast<const uint4*>(p.a.lb + ((size_t)ad * p.a.N + brow) * p.a.rank + c);
+            nb0 = __ldg(b4);
+            if (c + 16 <= p.a.rank) nb1 = __ldg(b4 + 1);
+          }
+          if (ad == my_id) {
             const float4* h4 = reinterpret_cast<const float4*>(hrow + c);
             nv[0] = __ldcg(h4);
             nv[1] = __ldcg(h4 + 1);
@@ -403,14 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* stage = lora + ls * p.lora_stage_bytes;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = nv[e];
+          const uint4 b0 = nb0, b1 = nb1;
           load_h(j + 1);
           if (lcnt >= (uint32_t)p.lora_stages)
             ok = warp_wait(&lora_empty[ls], ((lcnt / p.lora_stages) & 1) ^ 1, abort_flag, p.err, 86);
           if (!(ok = bar_and(ok))) break;
-          const uint32_t full_l = leader_addr(&lora_full[ls]);
-          if (i == 0)
-            tma_load_3d_pair(stage + 2 * kLoraTile, &p.mb, 16 * ((part + j * split) % rb),
-                             n0 + half * (int)rank, s_list[(part + j * split) / rb], full_l);
           const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
           uint32_t hi[8], lo[8];
@@ -425,19 +425,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(row + (16 ^ sw)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
           *reinterpret_cast<uint4*>(row + kLoraTile + sw) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           *reinterpret_cast<uint4*>(row + kLoraTile + (16 ^ sw)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          if (i < half) {
+            *reinterpret_cast<uint4*>(row + 2 * kLoraTile + sw) =
+                make_uint4(finite2(b0.x), finite2(b0.y), finite2(b0.z), finite2(b0.w));
+            *reinterpret_cast<uint4*>(row + 2 * kLoraTile + (16 ^ sw)) =
+                make_uint4(finite2(b1.x), finite2(b1.y), finite2(b1.z), finite2(b1.w));
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (i == 0) {
-            if (leader) mbar_arrive_expect_tx(&lora_full[ls], 2u * (uint32_t)half * 32u);
-            else arrive_cluster_shared(full_l);
-          }
+          if (i == 0) arrive_cluster_shared(leader_addr(&lora_full[ls]));
         }
         // (the next tile rewrites the list: every thread has read it)
         if (!bar_and(ok)) break;
-      }
-      if (!ok) {   // the copies in flight land (see above)
-        const unsigned long long t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
       }
     }
   } else {
@@ -595,7 +594,6 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   p.mx = mx;
   p.mw = mw[bn / 32 - 1];
   p.split = split;
-  if (a.la && !encode_lora_b(&p.mb, a.lb, a.n_adapters, a.N, a.rank, bn / 2)) return cudaErrorInvalidValue;
   p.a = a;
   p.bn = bn;
   p.mt = (a.T + lin::kTileM - 1) / lin::kTileM;

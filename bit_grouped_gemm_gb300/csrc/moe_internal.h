@@ -244,9 +244,6 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st
 // the product on SM pairs. mw: w16 with boxes of 64 x 16, 32, .. 128 rows.
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
                                int num_sms, cudaStream_t st);
-// 3D map of adapters' B, bf16 [n][N][rank], in boxes of 16 columns x box_rows
-// rows, 32-byte swizzle.
-bool encode_lora_b(CUtensorMap* m, const void* base, int n, int N, int rank, uint32_t box_rows);
 cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap* mw,
                              DevErr err, int num_sms, cudaStream_t st);
 

@@ -72,19 +72,6 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const voi
   return r == CUDA_SUCCESS;
 }
 
-bool encode_lora_b(CUtensorMap* m, const void* base, int n, int N, int rank, uint32_t box_rows) {
-  EncodeTiledFn enc = get_encode();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)rank, (cuuint64_t)N, (cuuint64_t)n};
-  cuuint64_t strides[2] = {(cuuint64_t)rank * 2, (cuuint64_t)rank * N * 2};
-  cuuint32_t box[3] = {16, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 bool encode_router_slices(CUtensorMap* m, const void* base, int H, int E) {
   EncodeTiledFn enc = get_encode();
   if (!enc || H % 256 || E % 8) return false;

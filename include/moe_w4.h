@@ -409,7 +409,10 @@ moe_status moe_linear_scratch_bytes(const moe_linear_desc* desc, size_t* bytes);
  * order of adapters; rows of one adapter next to each other are fastest.
  * The sums are FP32; weights are rebuilt as fp16(q * scale + bias) and bf16
  * rows enter as fp16 under the operand contract above, reported by
- * moe_linear_get_error; x A^T is kept to 16 significant bits. Weights and
+ * moe_linear_get_error; x A^T is kept to 16 significant bits. A token's row
+ * depends on its own x, scale and adapter alone: infinities and NaNs of another
+ * token or another adapter do not reach it (an adapter's own tokens get
+ * unspecified values from them). Weights and
  * adapters are read under the rule for weights above; like them, `adapter`
  * and x must not be written by a kernel that the call's own launches could
  * overtake: any launch before the call on the same stream is waited for.

@@ -562,6 +562,29 @@ def test_linear_in_a_graph(T):
     bg.moe_linear_destroy(h)
 
 
+@pytest.mark.parametrize("T", [6, 40, 300])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_linear_keeps_broken_adapters_to_their_own_tokens(T, ids):
+    clean = Linear(T, 256, 200, rank=16, n=4, ids=ids)
+    assert clean.run() == 0
+    c = Linear(T, 256, 200, rank=16, n=4, ids=ids)
+    c.b[1, 5, 3], c.b[1, 77, 0], c.b[1, 150] = float("nan"), float("inf"), float("-inf")
+    c.a[2, 4, 9], c.a[2, 0] = float("nan"), float("inf")
+    c.ls[3] = float("nan")
+    assert c.run() == 0
+    rows = (c.ids <= 0)
+    assert rows.any() and torch.equal(c.y[rows], clean.y[rows])
+    # and a token whose scale is not a number
+    e = Linear(T, 256, 200, x="e4m3", rank=16, n=4, ids=ids)
+    assert e.run() == 0
+    first = e.y.clone()
+    e.xs[1] = float("nan")
+    assert e.run() == 0
+    assert torch.isnan(e.y[1]).all()
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(e.y[keep], first[keep])
+
+
 @pytest.mark.parametrize("T", [1, 200])
 def test_linear_flags_values_beyond_the_operands(T):
     c = Linear(T, 256, 128)
