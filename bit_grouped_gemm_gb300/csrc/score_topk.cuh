@@ -171,11 +171,19 @@ __device__ __forceinline__ float rcp_1ulp(float v) {
   return r;
 }
 
-// The FP32 score of an expert (without its bias); softmax: from the row's
-// maximum and the reciprocal of its sum (0 where p is 0 throughout).
+// exp(v) in two instructions, to a relative 2^-22 + 7.5e-8 |v| (the rounding of
+// v log2(e)): for ranking, where far exponents are small terms.
+__device__ __forceinline__ float exp_rank(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(v, 1.44269504f)));
+  return r;
+}
+
+// The FP32 score of an expert (without its bias) as it is ranked; softmax: from
+// the row's maximum and the reciprocal of its sum (0 where p is 0 throughout).
 __device__ __forceinline__ float score_prob(const ScoreDev& s, float l, float m, float rz) {
-  if (s.sigmoid) return rcp_1ulp(1.0f + expf(-l));
-  return rz > 0.f ? __fmul_rn(expf(l - m), rz) : 0.f;
+  if (s.sigmoid) return rcp_1ulp(1.0f + exp_rank(-l));
+  return rz > 0.f ? __fmul_rn(exp_rank(l - m), rz) : 0.f;
 }
 
 // Writes the lane's experts e0 + i, i in the set `cand`, into `list` (32
@@ -469,10 +477,10 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
       }
     }
   };
-  load_row(row, [&](int i, float v) { c[i] = clean_logit(v); });
+  load_row(row, [&](int i, float v) { c[i] = fmaxf(v, -INFINITY); });   // NaN as -infinity
   // the bias is loaded ahead where there are registers for it
   float bias[VPL];
-  auto load_bias = [&] { load_row(s.bias, [&](int i, float v) { bias[i] = fmaxf(v, -INFINITY); }); };
+  auto load_bias = [&] { load_row(s.bias, [&](int i, float v) { bias[i] = v; }); };
   if (VPL <= 8 && s.bias) load_bias();
   float m = 0.f, rz = 1.f;
   if (!s.sigmoid && (s.bias || s.groups > 1 || !s.renorm)) {
@@ -484,7 +492,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float p = expf(c[i] - mm);
+      const float p = exp_rank(c[i] - mm);
       if (s.bias) c[i] = p;
       z += p;
     }
@@ -495,23 +503,30 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
   if (s.bias) {
     if (s.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = rcp_1ulp(1.0f + expf(-c[i]));
+      for (int i = 0; i < VPL; ++i) c[i] = rcp_1ulp(1.0f + exp_rank(-c[i]));
+    } else if (rz > 0.f) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = __fmul_rn(c[i], rz);
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = rz > 0.f ? __fmul_rn(c[i], rz) : 0.f;
+      for (int i = 0; i < VPL; ++i) c[i] = 0.f;
     }
     if (VPL > 8) load_bias();
+    // (a NaN bias as -infinity: lanes past E keep -infinity this way too)
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] = __fadd_rn(c[i], bias[i]);
+    for (int i = 0; i < VPL; ++i) c[i] = fmaxf(__fadd_rn(c[i], bias[i]), -INFINITY);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] += 0.0f;   // -0 as +0
   }
-  // Bound of a pair's FP32 error, from expf's 2 ulp, the reciprocal's 1 and
+  // Bound of a pair's FP32 error, from exp_rank's, the reciprocal's 1 ulp and
   // half an ulp for every other operation. Sigmoid: e = exp(-l) enters
-  // p = 1 / (1 + e) by e / (1 + e) = 1 - p, so p is off by p (1 - p) 2^-22 +
-  // 1.5 p 2^-23 < 2.4e-7. Softmax, of the largest p, 1 / z: 3.4e-7 by the
-  // exponential (its argument too) and the product, for each of the two, and
-  // 1.8e-6 by 1 / z (at most 21 additions), which both share. The bias'
-  // addition: half an ulp of c.
-  const float perr = s.sigmoid ? 5e-7f : 2.8e-6f * rz;
+  // p = 1 / (1 + e) by 1 - p, so p is off by p (1 - p) (2^-22 + 7.5e-8 |l|) +
+  // 1.5 p 2^-23 < 2.6e-7. Softmax, of the largest p, 1 / z: 3.6e-7 by the
+  // exponential (its argument's two roundings too) and the product, for each of
+  // the two, and 1.9e-6 by 1 / z (at most 21 additions), which both share. The
+  // bias' addition: half an ulp of c.
+  const float perr = s.sigmoid ? 5.5e-7f : 2.8e-6f * rz;
   float top = c[0];   // the lane's largest
 #pragma unroll
   for (int i = 1; i < VPL; ++i) top = fmaxf(top, c[i]);
@@ -633,7 +648,7 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
     const int need = s.bias ? k + 1 : k;
     // (equal maxima count once: the bound is then lower, the list longer)
     uint32_t tk = need <= 32 ? order_key(top) : 0u, bk = 0u;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = 0; j < need; ++j) {
       bk = __reduce_max_sync(0xffffffffu, tk);
       if (tk == bk) tk = 0u;
