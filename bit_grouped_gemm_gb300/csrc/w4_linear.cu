@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const Linea
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepSplit = 4;
+constexpr int kPrepBlock = 512, kPrepRuns = 24;
 constexpr int kPrepWords = 2048;   // packed words per weight CTA
 
 // K columns of a token CTA (a multiple of 32), and bytes of a row of its tile
@@ -291,7 +292,8 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
                        const DevErr err) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_id[kPrepTok], s_list[kPrepTok];
+  __shared__ int s_id[kPrepTok], s_list[kPrepTok], s_tok[kPrepTok];
+  __shared__ __align__(16) int s_key[kPrepBlock];   // the block's adapters, none: the largest int
   pdl_begin();
   if ((int)blockIdx.x >= nx) {
     prep_weights(a, w16, (int)blockIdx.x - nx, err);
@@ -302,32 +304,96 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
   const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
   const int row_bytes = prep_row_bytes(a.K);
   float* part = reinterpret_cast<float*>(smem + kPrepTok * row_bytes);   // [token][rank]
-  const int id = adapter_of(a, t0 + lane);   // every warp holds all 32 tokens' ids
-  // x: 8 columns at a time, kBatch loads in flight per thread
-  constexpr int kBatch = kDeep ? 8 : 4, kABatch = kDeep ? 16 : 8;
+  // x, 8 columns at a time: a warp takes every 8th row, kCols vectors of each of
+  // its 4 rows in flight per lane
+  constexpr int kCols = kDeep ? 2 : 1, kABatch = kDeep ? 16 : 8;
+  const int vec = kn / 8;
   uint32_t over = 0u;
-  const int vec = kn / 8, total = kPrepTok * vec;
-  auto put_x = [&](int i, const Raw8& v) {
-    const int tl = i / vec, k = 8 * (i - tl * vec), t = t0 + tl;
-    if (t < a.T)
-      *reinterpret_cast<uint4*>(x16 + (size_t)t * a.K + k0 + k) = f16x8_to_perm8(to_f16(a, v, over));
-    if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 2 * k) = to_bf16(a, v);
-  };
-  auto get_x = [&](int i) {
-    Raw8 v{make_uint4(0u, 0u, 0u, 0u)};
-    if (i < total) {
-      const int tl = i / vec;
-      if (t0 + tl < a.T) v = load8(a, t0 + tl, k0 + 8 * (i - tl * vec));
-    }
-    return v;
-  };
-  Raw8 xv[kBatch];
+  Raw8 xv[4][kCols];
+  auto get_x = [&](int c0, auto&& token) {
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) xv[j] = get_x(tid + 256 * j);
-  // meanwhile the tokens' distinct adapters, in order
-  int jobs = 0;
-  const int tiles = a.rank / 8;
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + 32 * j + lane, t = token(warp + 8 * r);
+        xv[r][j].v = make_uint4(0u, 0u, 0u, 0u);
+        if (c < vec && t < a.T) xv[r][j] = load8(a, t, k0 + 8 * c);
+      }
+  };
+  auto put_x = [&](int c0, bool to_global, bool to_tile) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + 32 * j + lane, tl = warp + 8 * r, t = t0 + tl;
+        if (c >= vec) continue;
+        if (to_global && t < a.T)
+          *reinterpret_cast<uint4*>(x16 + (size_t)t * a.K + k0 + 8 * c) = f16x8_to_perm8(to_f16(a, xv[r][j], over));
+        if (to_tile) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 16 * c) = to_bf16(a, xv[r][j]);
+      }
+  };
+  auto own = [&](int tl) { return t0 + tl; };
+  get_x(0, own);
+  // Meanwhile the adapters of the block of 512 tokens that the cluster's 32 are
+  // in. With few runs of one adapter the cluster takes h of its own tokens; with
+  // more, of its 32 places in the block's tokens ordered by adapter, so that
+  // mixed batches cost a job per adapter and block, not per adapter and cluster
+  // (4096 tokens of 16 adapters in random order, 2048 x 2048: 83 to 75 us a call).
+  const int blk0 = t0 / kPrepBlock * kPrepBlock;
+  bool mixed = false;
   if (a.la) {
+    int key[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int id = adapter_of(a, blk0 + tid + 256 * j);
+      key[j] = id < 0 ? 0x7FFFFFFF : id;
+      s_key[tid + 256 * j] = key[j];
+    }
+    if (tid < kPrepTok) s_tok[tid] = t0 + tid;
+    __syncthreads();
+    const int runs = __syncthreads_count(tid > 0 && s_key[tid - 1] != key[0]) +
+                     __syncthreads_count(s_key[tid + 255] != key[1]);
+    mixed = runs > kPrepRuns;
+  }
+  put_x(0, true, a.la && !mixed);
+  for (int c0 = 32 * kCols; c0 < vec; c0 += 32 * kCols) {
+    get_x(c0, own);
+    put_x(c0, true, a.la && !mixed);
+  }
+  report_range_warp(err, over != 0u);
+  if (!a.la) return;
+  if (mixed) {
+    // A token's place: the smaller keys, and the equal ones before it. Each CTA
+    // of the cluster finds those of 128 tokens, two threads a token, and gives
+    // all four CTAs the tokens that fall into the cluster's 32 places.
+    const int j = 128 * part_k + (tid >> 1), h0 = 256 * (tid & 1), mine = s_key[j];
+    int place = 0;
+#pragma unroll 4
+    for (int e = 0; e < 256; e += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(s_key + h0 + e);
+      place += (o.x < mine || (o.x == mine && h0 + e < j)) + (o.y < mine || (o.y == mine && h0 + e + 1 < j)) +
+               (o.z < mine || (o.z == mine && h0 + e + 2 < j)) + (o.w < mine || (o.w == mine && h0 + e + 3 < j));
+    }
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place -= t0 - blk0;
+    if (place >= 0 && place < kPrepTok)
+      for (int c = tid & 1; c < kPrepSplit; c += 2) {
+        uint32_t addr;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(s_tok + place)), "r"(c));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(blk0 + j) : "memory");
+      }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    auto placed = [&](int tl) { return s_tok[tl]; };
+    for (int c0 = 0; c0 < vec; c0 += 32 * kCols) {
+      get_x(c0, placed);
+      put_x(c0, false, true);
+    }
+  }
+  // the 32 tokens' distinct adapters, in order (every warp alike)
+  const int tiles = a.rank / 8;
+  int jobs;
+  {
+    const int key = s_key[s_tok[lane] - blk0], id = key == 0x7FFFFFFF ? -1 : key;
     bool first = id >= 0;
 #pragma unroll
     for (int j = 0; j < 31; ++j) {
@@ -341,18 +407,6 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     }
     jobs = __popc(firsts) * tiles;
   }
-#pragma unroll
-  for (int j = 0; j < kBatch; ++j)
-    if (tid + 256 * j < total) put_x(tid + 256 * j, xv[j]);
-  for (int i0 = tid + 256 * kBatch; i0 < total; i0 += 256 * kBatch) {
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) xv[j] = get_x(i0 + 256 * j);
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (i0 + 256 * j < total) put_x(i0 + 256 * j, xv[j]);
-  }
-  report_range_warp(err, over != 0u);
-  if (!a.la) return;
   __syncthreads();
   const int g = lane >> 2, q = lane & 3;
   for (int job = warp; job < jobs; job += 8) {
@@ -405,7 +459,7 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(addr) : "memory");
       v += o;
     }
-    a.h[(size_t)(t0 + tl) * a.rank + i % a.rank] = v * (a.lscale ? __ldg(a.lscale + ad) : 1.f);
+    a.h[(size_t)s_tok[tl] * a.rank + i % a.rank] = v * (a.lscale ? __ldg(a.lscale + ad) : 1.f);
   }
   // no CTA leaves while another still reads its sums
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
