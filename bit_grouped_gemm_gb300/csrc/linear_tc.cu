@@ -13,7 +13,7 @@
 // tile's tokens the tile gets rank K columns with h in A, zero in the rows of
 // other tokens, and B[a] in B: the MMAs then add each token's own product,
 // whatever the order of the tokens. They go by in stages of 16 columns, written
-// by four warps and spread between the tile's other chunks. h goes in as two
+// by two groups of four warps and spread between the tile's other chunks. h goes in as two
 // bf16 (the value and what its rounding left), each multiplied with B's own
 // bf16: the products are exact to 16 bits of h. A zero times an infinity or a NaN
 // would carry one adapter's broken B into other requests' rows, so B goes in with
@@ -25,8 +25,8 @@
 namespace moe {
 namespace lin {
 
-constexpr int kThreads = 352;             // TMA, 1 or 2 MMA, 4 adapter, 4 epilogue warps
-constexpr int kMma2Warp = 10;
+constexpr int kThreads = 480;             // TMA, 1 or 2 MMA, 2 x 4 adapter, 4 epilogue warps
+constexpr int kMma2Warp = 10, kLora2Warp = 11;
 constexpr int kTileM = 256;
 constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
 constexpr uint32_t kTmemCols = 512;
@@ -42,7 +42,7 @@ constexpr int kMaxLoraStages = 8;
 // list of the tile's adapters, barriers. A copy takes up to 4,500 cycles to
 // land, so a tile's pace is the ring's depth over that until its MMAs are slower:
 // narrow tiles get as many chunks as fit.
-constexpr int kIdsBytes = 3 * kTileM * 4;
+constexpr int kIdsBytes = 2 * 3 * kTileM * 4;
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 227 * 1024 - 1024;   // less alignment slack
 constexpr int kMaxStages = 12;
@@ -110,13 +110,13 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 
 // Barrier of the 128 adapter threads that tells whether all of them go on, so
 // that they leave their loop together and none is waited for in vain.
-__device__ __forceinline__ bool bar_and(bool v) {
+__device__ __forceinline__ bool bar_and(int bar, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, 1, 128, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n"
       " selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "r"(bar)
       : "memory");
   return r != 0;
 }
@@ -126,16 +126,20 @@ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
   return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);
 }
 
+__device__ __forceinline__ void bar_sync(int bar) {
+  asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+}
+
 // Places of the flagged entries among 256 (thread i of 128 holds entries i
 // and 128 + i) in their order, and their number. `cnt`: 8 ints.
-__device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra, int& rb) {
+__device__ __forceinline__ int rank_of(int bar, bool a, bool b, int i, int* cnt, int& ra, int& rb) {
   const int lane = i & 31, w = i >> 5;
   const unsigned ma = __ballot_sync(0xffffffffu, a), mb = __ballot_sync(0xffffffffu, b);
   if (lane == 0) {
     cnt[w] = __popc(ma);
     cnt[4 + w] = __popc(mb);
   }
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  bar_sync(bar);
   int n = 0;
   ra = rb = 0;
 #pragma unroll
@@ -144,7 +148,7 @@ __device__ __forceinline__ int rank_of(bool a, bool b, int i, int* cnt, int& ra,
     if (j == 4 + w) rb = n + __popc(mb & ((1u << lane) - 1u));
     n += cnt[j];
   }
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  bar_sync(bar);
   return n;
 }
 
@@ -157,10 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
   uint8_t* lora = smem + stages * p.stage_bytes;
-  int* s_ids = reinterpret_cast<int*>(lora + p.lora_stages * p.lora_stage_bytes);   // adapter per token
-  int* s_runs = s_ids + kTileM;                             // its runs' adapters
-  int* s_list = s_runs + kTileM;                            // its distinct adapters
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ids + (kLora ? 3 * kTileM : 0));
+  int* s_lora = reinterpret_cast<int*>(lora + p.lora_stages * p.lora_stage_bytes);   // adapter lists
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_lora + (kLora ? 2 * 3 * kTileM : 0));
   uint64_t* full = bars;                   // leader: both CTAs' operands landed
   uint64_t* empty = full + kMaxStages;              // chunk's MMAs done (both CTAs)
   uint64_t* acc_full = empty + kMaxStages;          // [2] tile's MMAs done (both CTAs)
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_steps = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2] by tile parity
-  int* s_cnt = reinterpret_cast<int*>(tmem_slot + 4);       // [8] adapters per 32 tokens
+  int* s_cnt2 = reinterpret_cast<int*>(tmem_slot + 4);      // [2][8] flagged entries per warp
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // CTA `rank` of pair `part` of the cluster; the pair's leader is its CTA 0
@@ -327,12 +329,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned long long t0 = globaltimer_ns();
     while (!try_wait_cluster(drain, 0, 100000) && globaltimer_ns() - t0 < 2 * p.err.limit_ns) {
     }
-  } else if (warp < 6) {
+  } else if (warp < 6 || warp >= kLora2Warp) {
     // ------------------------------------------------- adapters' K columns
     if (kLora) {
-      const int i = threadIdx.x - 64;   // 0..127: this thread's A row
+      // Two groups of four warps write alternate stages: one takes about 800
+      // cycles to fill one (its barriers and proxy fence), a stage's MMAs 256
+      // (4096 tokens of 16 adapters in turn at K = N = 2048: 68 us, with one group 75).
+      const int grp = warp < 6 ? 0 : 1, bar = 1 + grp;
+      const int i = threadIdx.x - (grp ? 32 * kLora2Warp : 64);   // 0..127: this thread's A row
+      int* s_ids = s_lora + 3 * kTileM * grp;          // the tile's adapter per token
+      int* s_runs = s_ids + kTileM;                    // its runs' adapters
+      int* s_list = s_runs + kTileM;                   // its distinct adapters
+      int* s_cnt = s_cnt2 + 8 * grp;
       int r0, r1;
-      uint32_t lcnt = 0, it = 0;
+      uint32_t sc = 0, it = 0;   // stages of the tiles before
       bool ok = true;
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const int m0 = (u % p.mt) * kTileM, n0 = (u / p.mt) * p.bn;
@@ -340,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id0 = token_adapter(p.a, m0 + i), id1 = token_adapter(p.a, m0 + 128 + i);
         s_ids[i] = id0;
         s_ids[128 + i] = id1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        bar_sync(bar);
         // where an adapter's run of tokens starts, then its first run
         const bool st0 = id0 >= 0 && (i == 0 || s_ids[i - 1] != id0);
         const bool st1 = id1 >= 0 && s_ids[127 + i] != id1;
-        const int runs = rank_of(st0, st1, i, s_cnt, r0, r1);
+        const int runs = rank_of(bar, st0, st1, i, s_cnt, r0, r1);
         if (st0) s_runs[r0] = id0;
         if (st1) s_runs[r1] = id1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        bar_sync(bar);
         bool f0 = i < runs, f1 = 128 + i < runs;
         const int ru0 = f0 ? s_runs[i] : -1, ru1 = f1 ? s_runs[128 + i] : -1;
         const int upto = f1 ? 128 + i : i;
@@ -359,15 +369,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             f1 &= !((o.x == ru1 && e < upto) || (o.y == ru1 && e + 1 < upto) ||
                     (o.z == ru1 && e + 2 < upto) || (o.w == ru1 && e + 3 < upto));
           }
-        const int nad = rank_of(f0, f1, i, s_cnt, r0, r1);
+        const int nad = rank_of(bar, f0, f1, i, s_cnt, r0, r1);
         if (f0) s_list[r0] = ru0;
         if (f1) s_list[r1] = ru1;
         // of the tile's rb x nad stages every split-th is this pair's
         const int nl = (rb * nad - part + split - 1) / split;
-        // the count of two tiles ago has been read once that tile is done
-        if (it >= 2) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
-        if (!(ok = bar_and(ok))) break;
-        if (i == 0) {
+        // the count of two tiles ago has been read once that tile is done (the second
+        // group does not look: with no stage in a tile nothing keeps that barrier
+        // from going on past the phase it would wait for)
+        if (it >= 2 && grp == 0) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
+        if (!(ok = bar_and(bar, ok))) break;
+        if (i == 0 && grp == 0) {
           s_steps[it & 1] = nl;
           mbar_arrive(&list_full[it & 1]);
         }
@@ -400,17 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (it == 0) pdl_wait();
-        load_h(0);
-        for (int j = 0; j < nl; ++j, ++lcnt) {
+        // (by the count of all stages: with an even number of buffers a group then
+        // has buffers of its own and meets each of their phases)
+        const int j0 = (grp ^ (int)sc) & 1;
+        load_h(j0);
+        for (int j = j0; j < nl; j += 2) {
+          const uint32_t lcnt = sc + j;
           const int ls = lcnt % p.lora_stages;
           uint8_t* stage = lora + ls * p.lora_stage_bytes;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = nv[e];
           const uint4 b0 = nb0, b1 = nb1;
-          load_h(j + 1);
+          load_h(j + 2);
           if (lcnt >= (uint32_t)p.lora_stages)
             ok = warp_wait(&lora_empty[ls], ((lcnt / p.lora_stages) & 1) ^ 1, abort_flag, p.err, 86);
-          if (!(ok = bar_and(ok))) break;
+          if (!(ok = bar_and(bar, ok))) break;
           const float f[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
           uint32_t hi[8], lo[8];
@@ -432,11 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(finite2(b1.x), finite2(b1.y), finite2(b1.z), finite2(b1.w));
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          bar_sync(bar);
           if (i == 0) arrive_cluster_shared(leader_addr(&lora_full[ls]));
         }
+        sc += nl;
         // (the next tile rewrites the list: every thread has read it)
-        if (!bar_and(ok)) break;
+        if (!bar_and(bar, ok)) break;
       }
     }
   } else {
@@ -605,7 +622,7 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   p.stage_bytes = lin::stage_bytes(bn);
   p.lora_stage_bytes = lin::lora_stage_bytes(bn);
   // two adapter stages at least, four where the tile is narrow
-  p.lora_stages = a.la ? (bn > 128 ? 2 : 4) : 0;
+  p.lora_stages = a.la ? (bn > 128 ? 2 : 4) : 0;   // (even: a group of writers each)
   const int fixed = (a.la ? lin::kIdsBytes : 0) + lin::kBarBytes + p.lora_stages * p.lora_stage_bytes;
   p.stages = (lin::kSmemMax - fixed) / p.stage_bytes;
   if (p.stages > lin::kMaxStages) p.stages = lin::kMaxStages;
