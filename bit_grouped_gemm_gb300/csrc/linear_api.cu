@@ -11,7 +11,7 @@ namespace {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-  size_t err, h, x16, w16, total;
+  size_t err, h, x16, w16, order, total;
 };
 
 constexpr int kWidths = 8;   // tile widths of the large product: 32, 64, .. 256
@@ -29,8 +29,9 @@ Layout make_layout(const moe_linear_desc& d) {
   if (d.max_tokens > kLinearSmallT) {
     L.x16 = take((size_t)d.max_tokens * d.in_features * 2);
     L.w16 = take((size_t)d.out_features * d.in_features * 2);
+    L.order = take((size_t)d.max_tokens * 4);
   } else {
-    L.x16 = L.w16 = 0;
+    L.x16 = L.w16 = L.order = 0;
   }
   L.total = o;
   return L;
@@ -203,7 +204,8 @@ moe_status moe_linear_forward(moe_linear_t p, const void* x, int x_type, long lo
     a.n_adapters = lora->n;
     a.rank = lora->rank;
     a.adapter = adapter;
-    a.h = reinterpret_cast<float*>(p->scratch + p->L.h);
+    a.h = p->at<float>(p->L.h);
+    a.order = p->at<int>(p->L.order);
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;

@@ -218,6 +218,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int half = p.bn >> 1;
   const int rb = (p.a.rank + 15) >> 4;   // stages per adapter
 
+  // warps 2 to 9: this thread's row of the tile at token place m0, its token in y
+  // and scale (read where the parts' sums meet by the adapter warps too)
+  bool live = false;
+  int y_row = 0;
+  float y_scale = 1.f;
+  auto set_row = [&](int m0) {
+    const int place = m0 + 128 * (int)rank + 32 * (warp & 3) + lane;
+    live = place < p.a.T;
+    y_row = live && kLora ? __ldcg(p.a.order + place) : place;
+    if (live && p.a.x_scale) y_scale = __ldg(p.a.x_scale + y_row);
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------- TMA, own halves
     pdl_begin();
@@ -267,20 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const int buf = kIssuers == 2 ? me : (int)(it & 1);
         const uint32_t acc = tmem + 256 * buf;
-        int nl = 0;
-        if (kLora) {
-          if (!(ok = warp_wait(&list_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 81))) break;
-          nl = s_steps[it & 1];
-        }
-        // this warp's adapter stages: the first one's place, and the chunks
-        // between two of them
-        int j = me;
-        const int gap = nl ? (nk - nk / 2) / (nl + 1) : 0;
-        int due = nk / 2 + gap * (me + 1);
         if (kIssuers == 1 && !(ok = warp_wait<true>(&acc_empty[buf], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 82))) break;
         tc_fence_after();
-        for (int c = me; c < nk; c += kIssuers) {
-          if (!(ok = warp_wait(&full[s], ph, abort_flag, p.err, 83))) break;
+        int c = me;
+        auto chunk = [&] {
+          if (!(ok = warp_wait(&full[s], ph, abort_flag, p.err, 83))) return;
           tc_fence_after();
           if (elect_one_sync()) {
             // (a descriptor's low bits are the address over 16)
@@ -295,8 +298,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             s -= stages;
             ph ^= 1;
           }
-          // the adapter stages that are due, evenly among the second half's
-          // chunks (fixed places: the sums' order is that of every run)
+        };
+        // The adapter stages come evenly among the second half's chunks (fixed
+        // places: the sums' order is that of every run). The first tile's list takes
+        // about a microsecond and is waited for there (4096 tokens of 2048 x 2048:
+        // 35.9 us, 36.9 with the wait before the first chunk).
+        int nl = 0, j = me;
+        if (kLora) {
+          if (it == 0)
+            for (; c + 1 < nk / 2 && ok; c += kIssuers) chunk();
+          if (ok) ok = warp_wait(&list_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 81);
+          if (!ok) break;
+          nl = s_steps[it & 1];
+        }
+        // the chunks between two of this warp's stages, and before the next one
+        const int gap = nl ? (nk - nk / 2) / (nl + 1) : 0;
+        int due = nk / 2 + gap * (me + 1);
+        for (; c < nk; c += kIssuers) {
+          chunk();
+          if (!ok) break;
           while (kLora && j < nl && (c + 1 >= due || c + kIssuers >= nk)) {
             if (!(ok = warp_wait<true>(&lora_full[ls], lph, abort_flag, p.err, 84))) break;
             tc_fence_after();
@@ -331,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 6 || warp >= kLora2Warp) {
     // ------------------------------------------------- adapters' K columns
-    if (kLora) {
+    if (!kLora) {
+      if (split > 1) set_row((pair % p.mt) * kTileM);
+    } else {
       // Two groups of four warps write alternate stages: one takes about 800
       // cycles to fill one (its barriers and proxy fence), a stage's MMAs 256
-      // (4096 tokens of 16 adapters in turn at K = N = 2048: 68 us, with one group 75).
+      // (128 tokens of 16 adapters, K = N = 2048: 19.7 us, with one group 21.7).
       const int grp = warp < 6 ? 0 : 1, bar = 1 + grp;
       const int i = threadIdx.x - (grp ? 32 * kLora2Warp : 64);   // 0..127: this thread's A row
       int* s_ids = s_lora + 3 * kTileM * grp;          // the tile's adapter per token
@@ -346,8 +368,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
         const int m0 = (u % p.mt) * kTileM, n0 = (u / p.mt) * p.bn;
+        // Are its places ordered? For the first tile found out here, as the launch
+        // before does, to have the list while that still runs.
+        bool ordered = true;
+        if (it == 0) {
+          const int blk0 = m0 / kOrderBlock * kOrderBlock, n = min(kOrderBlock, p.a.T - blk0);
+          static_assert(kOrderSamples == 128, "a sample per thread");
+          const int at = order_sample(i, n);
+          const unsigned changes = __ballot_sync(0xffffffffu, at < n && token_adapter(p.a, blk0 + at - 1) !=
+                                                                            token_adapter(p.a, blk0 + at));
+          if (lane == 0) s_cnt[i >> 5] = __popc(changes);
+          bar_sync(bar);
+          ordered = order_rule(s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3], n);
+          if (ordered) pdl_wait();
+        }
         // the tile's distinct adapters, in the order of their first tokens
-        const int id0 = token_adapter(p.a, m0 + i), id1 = token_adapter(p.a, m0 + 128 + i);
+        auto adapter_at = [&](int place) {
+          if (place >= p.a.T) return -1;
+          return token_adapter(p.a, ordered ? __ldcg(p.a.order + place) : place);
+        };
+        const int id0 = adapter_at(m0 + i), id1 = adapter_at(m0 + 128 + i);
         s_ids[i] = id0;
         s_ids[128 + i] = id1;
         bar_sync(bar);
@@ -411,7 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        if (it == 0) pdl_wait();
+        if (it == 0) {
+          pdl_wait();
+          if (split > 1) set_row(m0);
+        }
         // (by the count of all stages: with an even number of buffers a group then
         // has buffers of its own and meets each of their phases)
         const int j0 = (grp ^ (int)sc) & 1;
@@ -466,9 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int u = pair; u < p.tiles && ok; u += npairs, ++it) {
-      const int t = (u % p.mt) * kTileM + 128 * (int)rank + row, n0 = (u / p.mt) * p.bn;
-      const bool live = t < p.a.T;
-      const float sc = live && p.a.x_scale ? __ldg(p.a.x_scale + t) : 1.f;
+      const int n0 = (u / p.mt) * p.bn;
+      set_row((u % p.mt) * kTileM);
       if (!(ok = warp_wait(&acc_full[it & 1], (it >> 1) & 1, abort_flag, p.err, 87))) break;
       tc_fence_after();
       for (int c0 = 0; c0 < p.bn; c0 += 32) {
@@ -489,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_cluster_relaxed(acc_empty_l + 8 * (it & 1));
         }
         const int n = n0 + c0;
-        uint16_t* o = p.a.y + t * p.a.y_ld + n;
+        uint16_t* o = p.a.y + y_row * p.a.y_ld + n;
         if (split > 1) {
           // this part's sums, [column][row], where the operands were (all
           // of the pair's MMAs are done)
@@ -503,14 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * sc,
-                                 __uint_as_float(v[8 * q + 2 * e + 1]) * sc);
+              w[e] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * y_scale,
+                                 __uint_as_float(v[8 * q + 2 * e + 1]) * y_scale);
             reinterpret_cast<uint4*>(o)[q] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (n + e < p.a.N) o[e] = f32_to_bf16(__uint_as_float(v[e]) * sc);
+            if (n + e < p.a.N) o[e] = f32_to_bf16(__uint_as_float(v[e]) * y_scale);
         }
         __syncwarp();
       }
@@ -523,10 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync_all();
     if (warp >= 2 && warp < 10 && !*abort_flag) {
-      const int row = 32 * (warp & 3) + lane, t = (pair % p.mt) * kTileM + 128 * (int)rank + row;
+      const int row = 32 * (warp & 3) + lane;
       const int cols = p.bn / split, n0 = (pair / p.mt) * p.bn;
-      const bool live = t < p.a.T;
-      const float sc = live && p.a.x_scale ? __ldg(p.a.x_scale + t) : 1.f;
       const bool wide = (p.a.y_ld & 7) == 0 && (reinterpret_cast<uintptr_t>(p.a.y) & 15u) == 0;
       const int c_end = part * cols + (warp >= 6 ? cols : cols / 2);
       for (int c0 = part * cols + (warp >= 6 ? cols / 2 : 0); c0 < c_end; c0 += 16) {
@@ -543,20 +583,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int n = n0 + c0;
-        uint16_t* o = p.a.y + t * p.a.y_ld + n;
+        uint16_t* o = p.a.y + y_row * p.a.y_ld + n;
         if (!live) {
         } else if (wide && n + 16 <= p.a.N) {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             reinterpret_cast<uint4*>(o)[q] =
-                make_uint4(pack_bf16x2(v[8 * q] * sc, v[8 * q + 1] * sc),
-                           pack_bf16x2(v[8 * q + 2] * sc, v[8 * q + 3] * sc),
-                           pack_bf16x2(v[8 * q + 4] * sc, v[8 * q + 5] * sc),
-                           pack_bf16x2(v[8 * q + 6] * sc, v[8 * q + 7] * sc));
+                make_uint4(pack_bf16x2(v[8 * q] * y_scale, v[8 * q + 1] * y_scale),
+                           pack_bf16x2(v[8 * q + 2] * y_scale, v[8 * q + 3] * y_scale),
+                           pack_bf16x2(v[8 * q + 4] * y_scale, v[8 * q + 5] * y_scale),
+                           pack_bf16x2(v[8 * q + 6] * y_scale, v[8 * q + 7] * y_scale));
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (n + e < p.a.N) o[e] = f32_to_bf16(v[e] * sc);
+            if (n + e < p.a.N) o[e] = f32_to_bf16(v[e] * y_scale);
         }
       }
     }

@@ -234,6 +234,7 @@ struct LinearArgs {
   int n_adapters, rank;
   const int32_t* adapter;
   float* h;                      // scratch [T][rank]: scale * x A^T
+  int* order;                    // scratch [T]: a place's token (larger batches)
 };
 // Decode batches (T <= kLinearSmallT): the adapters' h, then the product on
 // mma.sync straight from the packed weights.
@@ -241,7 +242,20 @@ constexpr int kLinearSmallT = 32;
 cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st);
 // Above: x as fp16 rows x16 [T][K], W as fp16 w16 [N][K] (both with every
 // block of 8 columns in perm8 order) and the adapters' h in one launch, then
-// the product on SM pairs. mw: w16 with boxes of 64 x 16, 32, .. 128 rows.
+// the product on SM pairs. With adapters the rows of x16 and h are places: a
+// block of kOrderBlock tokens in which the adapter changes more than about 32
+// times from one token to the next has them ordered by adapter, other blocks as
+// they come; order[] says which token a place is, in either case. A tile of
+// the product then has few adapters. (4096 tokens of 8 adapters in random order,
+// 2048 x 2048: 42 us a call, 60 with the tokens as they come; rank 64: 54, 92.)
+constexpr int kOrderBlock = 2048, kOrderSamples = 128;
+// Both launches look at the same samples of a block of n tokens: token
+// order_sample(i) and the one before, i < kOrderSamples, where it is below n.
+// (All of a block in every CTA costs 2 us: its few lines are hot in L2.)
+__host__ __device__ inline int order_step(int n) { return (n + kOrderSamples - 1) / kOrderSamples; }
+__host__ __device__ inline int order_sample(int i, int n) { return 1 + i * order_step(n); }
+__host__ __device__ inline bool order_rule(int changes, int n) { return changes * order_step(n) > 32; }
+// mw: w16 with boxes of 64 x 16, 32, .. 128 rows.
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
                                int num_sms, cudaStream_t st);
 cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const CUtensorMap* mw,

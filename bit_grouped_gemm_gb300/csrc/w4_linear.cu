@@ -257,7 +257,6 @@ __global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const Linea
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepSplit = 4;
-constexpr int kPrepBlock = 512, kPrepRuns = 24;
 constexpr int kPrepWords = 2048;   // packed words per weight CTA
 
 // K columns of a token CTA (a multiple of 32), and bytes of a row of its tile
@@ -284,6 +283,73 @@ __device__ __forceinline__ void prep_weights(const LinearArgs& a, uint16_t* __re
   report_range_warp(err, bad);
 }
 
+// Orders the block of n tokens from blk0 by adapter modulo 256 (none: as 255), a
+// warp's tokens one after the other, and keeps the 32 tokens (and their adapters)
+// that get the cluster's places, from t0. bins: 8 x 256, tokens by warp and bin.
+// Every CTA does it by itself. (Out of line: most calls skip it.)
+__device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters, int blk0, int n, int t0,
+                                         uint16_t* bins, int* s_sum, int* s_tok, int* s_id) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int steps = (n + 255) / 256, w0 = 32 * steps * warp;
+  constexpr int kSteps = kOrderBlock / 256;
+  int id[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int j = w0 + 32 * i + lane;
+    id[i] = i < steps && j < n ? __ldcg(adapter + blk0 + j) : -1;
+    if ((unsigned)id[i] >= (unsigned)n_adapters) id[i] = -1;
+  }
+  reinterpret_cast<uint4*>(bins)[tid] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  // a token's number among its warp's of its bin, the bins' counts
+  int nth[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    if (i < steps) {
+      const int bin = w0 + 32 * i + lane < n ? id[i] & 255 : 256;
+      const unsigned same = __match_any_sync(0xffffffffu, bin);
+      const int before = bin < 256 ? bins[256 * warp + bin] : 0;
+      nth[i] = before + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (bin < 256 && (same >> lane) == 1u) bins[256 * warp + bin] = (uint16_t)(nth[i] + 1);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // thread b: where bin b starts, and each warp's part of it
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const int c = bins[256 * w + tid];
+    bins[256 * w + tid] = (uint16_t)count;
+    count += c;
+  }
+  int start = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, start, o);
+    if (lane >= o) start += v;
+  }
+  if (lane == 31) s_sum[warp] = start;
+  __syncthreads();
+  start -= count;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) start += w < warp ? s_sum[w] : 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) bins[256 * w + tid] += (uint16_t)start;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i)
+    if (i < steps && w0 + 32 * i + lane < n) {
+      const int place = bins[256 * warp + (id[i] & 255)] + nth[i] - (t0 - blk0);
+      if (place >= 0 && place < kPrepTok) {
+        s_tok[place] = blk0 + w0 + 32 * i + lane;
+        s_id[place] = id[i];
+      }
+    }
+  __syncthreads();
+}
+
 // kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
 // where the launch has at most two CTAs per SM (1024 tokens of 2048 x 2048: 20.3
 // against 22.9 us for the call), slower beyond (4096 tokens: 40.2 against 35.9).
@@ -292,8 +358,8 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
                        const DevErr err) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_id[kPrepTok], s_list[kPrepTok], s_tok[kPrepTok];
-  __shared__ __align__(16) int s_key[kPrepBlock];   // the block's adapters, none: the largest int
+  __shared__ int s_id[kPrepTok], s_list[kPrepTok], s_tok[kPrepTok], s_sum[8];
+  __shared__ __align__(16) uint16_t s_bin[8][256];   // tokens by warp and bin of adapters
   pdl_begin();
   if ((int)blockIdx.x >= nx) {
     prep_weights(a, w16, (int)blockIdx.x - nx, err);
@@ -320,80 +386,54 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
         if (c < vec && t < a.T) xv[r][j] = load8(a, t, k0 + 8 * c);
       }
   };
-  auto put_x = [&](int c0, bool to_global, bool to_tile) {
+  auto put_x = [&](int c0) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int c = c0 + 32 * j + lane, tl = warp + 8 * r, t = t0 + tl;
         if (c >= vec) continue;
-        if (to_global && t < a.T)
+        if (t < a.T)
           *reinterpret_cast<uint4*>(x16 + (size_t)t * a.K + k0 + 8 * c) = f16x8_to_perm8(to_f16(a, xv[r][j], over));
-        if (to_tile) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 16 * c) = to_bf16(a, xv[r][j]);
+        if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 16 * c) = to_bf16(a, xv[r][j]);
       }
   };
-  auto own = [&](int tl) { return t0 + tl; };
-  get_x(0, own);
-  // Meanwhile the adapters of the block of 512 tokens that the cluster's 32 are
-  // in. With few runs of one adapter the cluster takes h of its own tokens; with
-  // more, of its 32 places in the block's tokens ordered by adapter, so that
-  // mixed batches cost a job per adapter and block, not per adapter and cluster
-  // (4096 tokens of 16 adapters in random order, 2048 x 2048: 83 to 75 us a call).
-  const int blk0 = t0 / kPrepBlock * kPrepBlock;
-  bool mixed = false;
+  get_x(0, [&](int tl) { return t0 + tl; });
   if (a.la) {
-    int key[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int id = adapter_of(a, blk0 + tid + 256 * j);
-      key[j] = id < 0 ? 0x7FFFFFFF : id;
-      s_key[tid + 256 * j] = key[j];
+    // Meanwhile: are the block's tokens to be ordered by adapter?
+    const int blk0 = t0 / kOrderBlock * kOrderBlock, n = min(kOrderBlock, a.T - blk0);
+    const int at = order_sample(tid, n);
+    bool change = false;
+    if (tid < kOrderSamples && at < n) change = adapter_of(a, blk0 + at - 1) != adapter_of(a, blk0 + at);
+    if (tid < kPrepTok) {
+      s_tok[tid] = t0 + tid;
+      s_id[tid] = adapter_of(a, t0 + tid);
     }
-    if (tid < kPrepTok) s_tok[tid] = t0 + tid;
-    __syncthreads();
-    const int runs = __syncthreads_count(tid > 0 && s_key[tid - 1] != key[0]) +
-                     __syncthreads_count(s_key[tid + 255] != key[1]);
-    mixed = runs > kPrepRuns;
+    const bool ordered = order_rule(__syncthreads_count(change), n);
+    // (x's loads stay where they are, under the ids')
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        asm volatile("" : "+r"(xv[r][j].v.x), "+r"(xv[r][j].v.y), "+r"(xv[r][j].v.z), "+r"(xv[r][j].v.w));
+    if (ordered) {
+      order_block(a.adapter, a.n_adapters, blk0, n, t0, &s_bin[0][0], s_sum, s_tok, s_id);
+      get_x(0, [&](int tl) { return s_tok[tl]; });
+    }
+    if (part_k == 0 && tid < kPrepTok && t0 + tid < a.T) a.order[t0 + tid] = s_tok[tid];
   }
-  put_x(0, true, a.la && !mixed);
+  put_x(0);
   for (int c0 = 32 * kCols; c0 < vec; c0 += 32 * kCols) {
-    get_x(c0, own);
-    put_x(c0, true, a.la && !mixed);
+    get_x(c0, [&](int tl) { return a.la ? s_tok[tl] : t0 + tl; });
+    put_x(c0);
   }
   report_range_warp(err, over != 0u);
   if (!a.la) return;
-  if (mixed) {
-    // A token's place: the smaller keys, and the equal ones before it. Each CTA
-    // of the cluster finds those of 128 tokens, two threads a token, and gives
-    // all four CTAs the tokens that fall into the cluster's 32 places.
-    const int j = 128 * part_k + (tid >> 1), h0 = 256 * (tid & 1), mine = s_key[j];
-    int place = 0;
-#pragma unroll 4
-    for (int e = 0; e < 256; e += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(s_key + h0 + e);
-      place += (o.x < mine || (o.x == mine && h0 + e < j)) + (o.y < mine || (o.y == mine && h0 + e + 1 < j)) +
-               (o.z < mine || (o.z == mine && h0 + e + 2 < j)) + (o.w < mine || (o.w == mine && h0 + e + 3 < j));
-    }
-    place += __shfl_xor_sync(0xffffffffu, place, 1);
-    place -= t0 - blk0;
-    if (place >= 0 && place < kPrepTok)
-      for (int c = tid & 1; c < kPrepSplit; c += 2) {
-        uint32_t addr;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(s_tok + place)), "r"(c));
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(blk0 + j) : "memory");
-      }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    auto placed = [&](int tl) { return s_tok[tl]; };
-    for (int c0 = 0; c0 < vec; c0 += 32 * kCols) {
-      get_x(c0, placed);
-      put_x(c0, false, true);
-    }
-  }
   // the 32 tokens' distinct adapters, in order (every warp alike)
   const int tiles = a.rank / 8;
   int jobs;
   {
-    const int key = s_key[s_tok[lane] - blk0], id = key == 0x7FFFFFFF ? -1 : key;
+    const int id = s_id[lane];
     bool first = id >= 0;
 #pragma unroll
     for (int j = 0; j < 31; ++j) {
@@ -402,7 +442,6 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     }
     const unsigned firsts = __ballot_sync(0xffffffffu, first);
     if (warp == 0) {
-      s_id[lane] = id;
       if (first) s_list[__popc(firsts & ((1u << lane) - 1u))] = id;
     }
     jobs = __popc(firsts) * tiles;
@@ -459,7 +498,7 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(addr) : "memory");
       v += o;
     }
-    a.h[(size_t)s_tok[tl] * a.rank + i % a.rank] = v * (a.lscale ? __ldg(a.lscale + ad) : 1.f);
+    a.h[(size_t)(t0 + tl) * a.rank + i % a.rank] = v * (a.lscale ? __ldg(a.lscale + ad) : 1.f);
   }
   // no CTA leaves while another still reads its sums
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -518,6 +518,29 @@ def test_linear_large():
     Linear(1031, 2048, 4096, x="e4m3", rank=16, n=8, ids="runs").check()
 
 
+@pytest.mark.parametrize("T", [2047, 2049, 4500])
+def test_linear_orders_mixed_blocks_of_tokens(T):
+    # more adapters than bins, tokens without one, runs and random order block by block
+    Linear(T, 192, 136, rank=8, n=300).check()
+    g = gen(3)
+    mixed = torch.randint(-2, 6, (2048,), generator=g, device="cuda").tolist()
+    runs = [i // 300 for i in range(2048)]
+    Linear(T, 128, 72, x="e4m3", rank=24, ids=runs + mixed, x_pad=16, y_pad=3).check()
+    Linear(T, 128, 72, x="e4m3", rank=24, ids=mixed + runs).check()
+
+
+def test_linear_mixed_then_runs_on_one_handle():
+    h = bg.moe_linear_create(bg.linear_desc(256, 320, 4200, 16), 0)
+    for T, ids in ((4200, "mixed"), (300, "runs"), (4100, "runs"), (90, "mixed"), (2100, "mixed")):
+        c = Linear(T, 256, 320, rank=16, n=9, ids=ids)
+        assert c.run(handle=h) == 0
+        c.compare()
+        first = c.y.clone()
+        assert c.run(handle=h) == 0
+        assert torch.equal(c.y, first)
+    bg.moe_linear_destroy(h)
+
+
 @pytest.mark.parametrize("T", [3, 40, 200])
 def test_linear_repeats_bit_for_bit_on_one_handle(T):
     c = Linear(T, 1024, 1000, rank=16)
