@@ -239,7 +239,7 @@ struct LinearArgs {
 // Decode batches (T <= kLinearSmallT): the adapters' h, then the product on
 // mma.sync straight from the packed weights.
 constexpr int kLinearSmallT = 32;
-cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st);
+cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cudaStream_t st);
 // Above: x as fp16 rows x16 [T][K], W as fp16 w16 [N][K] (both with every
 // block of 8 columns in perm8 order) and the adapters' h in one launch, then
 // the product on SM pairs. With adapters the rows of x16 and h are places: a

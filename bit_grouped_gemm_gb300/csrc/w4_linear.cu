@@ -10,6 +10,8 @@
 // that goes before it writes x and W as fp16 and h.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "moe_common.cuh"
 
 namespace moe {
@@ -86,10 +88,10 @@ __device__ __forceinline__ bool sb_out_of_range(uint32_t s, uint32_t b) {
 // Decode batches, first launch: h[t][r] = scale[a] sum_k x[t][k] A[a][r][k],
 // one warp per (t, r).
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) lora_shrink_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs a) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (w >= a.T * a.rank) return;
   const int t = w / a.rank, r = w - t * a.rank;
   const int id = adapter_of(a, t);
@@ -117,19 +119,26 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const LinearArgs a) {
 // rows: lane (g, q) rebuilds the 16 weights of words 2q and 2q + 1 of rows g
 // and g + 8, in the order in which the nibbles come out (perm8), and takes the
 // same K positions of token g's row as B. The warps' sums are added in a fixed
-// order through shared memory. Weights are loaded before the wait for the
-// launch before. With adapters that launch is lora_shrink_kernel, and x and the
+// order through shared memory. All loads of two groups are in flight before the
+// first is used (24 tokens of 2048 x 2048, without adapters: 4.7 us, 6.1 with x
+// loaded where it is used), which takes 128 registers above 8 tokens: then a CTA
+// has its SM for itself. Weights are loaded before the wait for the launch
+// before. With adapters that launch is lora_shrink_kernel, and x and the
 // adapters' ids are older than it: all that does not need h runs beside it.
 // (h taken in this launch instead, once per cluster of 8 CTAs and shared over
-// distributed shared memory, was slower: 6.6 against 4.7 us at one token of
-// 2048 x 2048 and rank 16, 12.4 against 6.6 us at 16. Against 8 warps of twice
-// the groups, 16 warps: 3.2 against 4.6 us at one token without adapters.)
+// distributed shared memory, was slower when it was tried: 6.6 against 4.7 us at
+// one token of 2048 x 2048 and rank 16, 12.4 against 6.6 us at 16; now 4.3 and
+// 5.2. Against 8 warps of twice the groups, 16 warps: 3.2 against 4.6 us at one
+// token without adapters.)
 // ---------------------------------------------------------------------------
 constexpr int kSmRows = 16;
 constexpr int kSmWarps = 16;
 
-template <int NT>   // tiles of 8 tokens
-__global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const LinearArgs a, const DevErr err) {
+template <int NT, bool kE4m3>   // tiles of 8 tokens; the rows' type
+__global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
+    linear_small_kernel(const LinearArgs args, const DevErr err) {
+  LinearArgs a = args;
+  a.e4m3 = kE4m3;
   __shared__ float red[kSmWarps][kSmRows][8 * NT + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
@@ -183,6 +192,17 @@ __global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const Linea
       waited = true;
       ahead();
     }
+    Raw8 xr[kAhead][NT][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int wd = 0; wd < 2; ++wd) {
+          const int gr = gb + kSmWarps * i, t = 8 * nt + g;
+          xr[i][nt][wd].v = make_uint4(0u, 0u, 0u, 0u);
+          if (gr < kg && t < a.T) xr[i][nt][wd] = load8(a, t, 64 * gr + 8 * (2 * q + wd));
+        }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int gr = gb + kSmWarps * i;
@@ -197,12 +217,9 @@ __global__ void __launch_bounds__(32 * kSmWarps) linear_small_kernel(const Linea
         uint32_t oa[4], ob[4];
         dequant_word_f16_perm8(wd ? w0[i].y : w0[i].x, sa, ba, oa);
         dequant_word_f16_perm8(wd ? w1[i].y : w1[i].x, sb, bb, ob);
-        const int k = 64 * gr + 8 * (2 * q + wd);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int t = 8 * nt + g;
-          uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-          if (t < a.T) xv = f16x8_to_perm8(to_f16(a, load8(a, t, k), over));
+          const uint4 xv = f16x8_to_perm8(to_f16(a, xr[i][nt][wd], over));
           mma_m16n8k16_f16(acc[nt], oa[0], ob[0], oa[1], ob[1], xv.x, xv.y);
           mma_m16n8k16_f16(acc[nt], oa[2], ob[2], oa[3], ob[3], xv.z, xv.w);
         }
@@ -506,19 +523,31 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
 
 }  // namespace
 
-cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, cudaStream_t st) {
+cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cudaStream_t st) {
   static_assert(kLinearSmallT <= 32, "one output per thread: 16 rows of at most 32 tokens");
+  const int nt = (a.T + 7) / 8, ctas = (a.N + kSmRows - 1) / kSmRows;
   if (a.la) {
-    const cudaError_t e = launch_pdl(lora_shrink_kernel, dim3((a.T * a.rank + 7) / 8), dim3(256), 0, st, a);
+    // Above 8 tokens the product's CTAs find no room beside this launch's, which
+    // are then made fewer: so that each has an SM, if that can be had (2048 x
+    // 2048, rank 16, CTAs of 8, 16, 32 warps: 16 tokens 6.4, 5.2, 5.3 us, 32
+    // tokens 10.0, 9.9, 8.6; of 64 registers at 4 tokens 4.4, 4.8, 5.2).
+    auto shrink_ctas = [&](int warps) { return (a.T * a.rank + warps - 1) / warps; };
+    int warps = nt == 1 ? 8 : 16;
+    if (nt > 1 && shrink_ctas(16) + ctas > num_sms && shrink_ctas(32) + ctas <= num_sms) warps = 32;
+    const cudaError_t e = launch_pdl(lora_shrink_kernel, dim3(shrink_ctas(warps)), dim3(32 * warps), 0, st, a);
     if (e != cudaSuccess) return e;
   }
-  const int nt = (a.T + 7) / 8;
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3((a.N + kSmRows - 1) / kSmRows), dim3(32 * kSmWarps), 0, st, a, err);
+    return launch_pdl(kern, dim3(ctas), dim3(32 * kSmWarps), 0, st, a, err);
   };
-  return nt <= 1   ? go(linear_small_kernel<1>)
-         : nt <= 2 ? go(linear_small_kernel<2>)
-                   : go(linear_small_kernel<4>);
+  auto pick = [&](auto e4m3) {
+    constexpr bool k = decltype(e4m3)::value;
+    return nt <= 1   ? go(linear_small_kernel<1, k>)
+           : nt <= 2 ? go(linear_small_kernel<2, k>)
+           : nt <= 3 ? go(linear_small_kernel<3, k>)
+                     : go(linear_small_kernel<4, k>);
+  };
+  return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
