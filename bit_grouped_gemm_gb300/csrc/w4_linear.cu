@@ -88,7 +88,10 @@ __device__ __forceinline__ bool sb_out_of_range(uint32_t s, uint32_t b) {
 // Decode batches, first launch: h[t][r] = scale[a] sum_k x[t][k] A[a][r][k],
 // one warp per (t, r).
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs a) {
+template <bool kE4m3>
+__global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs args) {
+  LinearArgs a = args;
+  a.e4m3 = kE4m3;
   pdl_begin();
   const int lane = threadIdx.x & 31;
   const int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -100,12 +103,22 @@ __global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs a) {
     const uint16_t* ar = a.la + ((size_t)id * a.rank + r) * a.K;
 #pragma unroll 8
     for (int k = 8 * lane; k < a.K; k += 256) {
-      const uint4 xv = to_bf16(a, load8(a, t, k));
+      const Raw8 r = load8(a, t, k);
       const uint4 av = __ldg(reinterpret_cast<const uint4*>(ar + k));
-      const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, aw[4] = {av.x, av.y, av.z, av.w};
+      const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, xw[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s = fmaf(bf16_lo(xw[j]), bf16_lo(aw[j]), fmaf(bf16_hi(xw[j]), bf16_hi(aw[j]), s));
+      for (int j = 0; j < 4; ++j) {
+        float x0, x1;
+        if (a.e4m3) {
+          const uint32_t f = e4m3x2_to_f16x2(xw[j >> 1] >> (16 * (j & 1)));
+          x0 = f16_lo(f);
+          x1 = f16_hi(f);
+        } else {
+          x0 = bf16_lo(xw[j]);
+          x1 = bf16_hi(xw[j]);
+        }
+        s = fmaf(x0, bf16_lo(aw[j]), fmaf(x1, bf16_hi(aw[j]), s));
+      }
     }
   }
 #pragma unroll
@@ -370,10 +383,12 @@ __device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters,
 // kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
 // where the launch has at most two CTAs per SM (1024 tokens of 2048 x 2048: 20.3
 // against 22.9 us for the call), slower beyond (4096 tokens: 40.2 against 35.9).
-template <bool kDeep>
+template <bool kDeep, bool kE4m3>
 __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
-    linear_prep_kernel(const LinearArgs a, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
+    linear_prep_kernel(const LinearArgs args, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
                        const DevErr err) {
+  LinearArgs a = args;
+  a.e4m3 = kE4m3;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_id[kPrepTok], s_list[kPrepTok], s_tok[kPrepTok], s_sum[8];
   __shared__ __align__(16) uint16_t s_bin[8][256];   // tokens by warp and bin of adapters
@@ -534,7 +549,7 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cu
     auto shrink_ctas = [&](int warps) { return (a.T * a.rank + warps - 1) / warps; };
     int warps = nt == 1 ? 8 : 16;
     if (nt > 1 && shrink_ctas(16) + ctas > num_sms && shrink_ctas(32) + ctas <= num_sms) warps = 32;
-    const cudaError_t e = launch_pdl(lora_shrink_kernel, dim3(shrink_ctas(warps)), dim3(32 * warps), 0, st, a);
+    const cudaError_t e = launch_pdl(a.e4m3 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>, dim3(shrink_ctas(warps)), dim3(32 * warps), 0, st, a);
     if (e != cudaSuccess) return e;
   }
   auto go = [&](auto kern) {
@@ -563,7 +578,11 @@ cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16
                ? e
                : launch_pdl(kern, dim3(nx + nw), dim3(256), (size_t)smem, st, a, x16, w16, nx, err);
   };
-  return nx + nw <= 2 * num_sms ? go(linear_prep_kernel<true>) : go(linear_prep_kernel<false>);
+  auto pick = [&](auto e4m3) {
+    constexpr bool k = decltype(e4m3)::value;
+    return nx + nw <= 2 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
+  };
+  return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace moe
