@@ -209,7 +209,7 @@ moe_status moe_linear_forward(moe_linear_t p, const void* x, int x_type, long lo
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (T <= kLinearSmallT) {
+  if (linear_is_small(a, p->num_sms)) {
     e = launch_linear_small(a, p->err(), p->num_sms, st);
   } else {
     e = launch_linear_prep(a, p->at<uint16_t>(p->L.x16), p->at<uint16_t>(p->L.w16), p->err(),

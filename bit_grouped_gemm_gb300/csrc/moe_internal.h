@@ -236,9 +236,10 @@ struct LinearArgs {
   float* h;                      // scratch [T][rank]: scale * x A^T
   int* order;                    // scratch [T]: a place's token (larger batches)
 };
-// Decode batches (T <= kLinearSmallT): the adapters' h, then the product on
-// mma.sync straight from the packed weights.
+// Decode batches (T <= kLinearSmallT, and more at small sizes): the adapters' h,
+// then the product on mma.sync straight from the packed weights.
 constexpr int kLinearSmallT = 32;
+bool linear_is_small(const LinearArgs& a, int num_sms);
 cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cudaStream_t st);
 // Above: x as fp16 rows x16 [T][K], W as fp16 w16 [N][K] (both with every
 // block of 8 columns in perm8 order) and the adapters' h in one launch, then

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs args
 }
 
 // ---------------------------------------------------------------------------
-// Decode batches, the product: a CTA takes 16 weight rows and all tokens, its
+// Decode batches, the product: a CTA takes 16 weight rows and up to 32 tokens, its
 // 16 warps every 16th group of 64 K each. The packed words are the MMA's A
 // rows: lane (g, q) rebuilds the 16 weights of words 2q and 2q + 1 of rows g
 // and g + 8, in the order in which the nibbles come out (perm8), and takes the
@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   uint32_t over = 0u;
   bool bad = false, waited = a.la != nullptr;
-  // This thread's output: row tid % 16 of token tid / 16. What its adapter adds
+  // This thread's output: row tid % 16 of the CTA's token tid / 16. What its adapter adds
   // is loaded ahead, up to 16 ranks, so that only h is left to come when the
   // sums are done.
-  const int to = tid / kSmRows, no = n0 + tid % kSmRows;
+  const int t0 = 8 * NT * blockIdx.y, tl = tid / kSmRows;
+  const int to = tl < 8 * NT ? t0 + tl : a.T, no = n0 + tid % kSmRows;
   int id = -1;
   uint4 b0v = make_uint4(0u, 0u, 0u, 0u), b1v = b0v;
   float xsc = 1.f;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int wd = 0; wd < 2; ++wd) {
-          const int gr = gb + kSmWarps * i, t = 8 * nt + g;
+          const int gr = gb + kSmWarps * i, t = t0 + 8 * nt + g;
           xr[i][nt][wd].v = make_uint4(0u, 0u, 0u, 0u);
           if (gr < kg && t < a.T) xr[i][nt][wd] = load8(a, t, 64 * gr + 8 * (2 * q + wd));
         }
@@ -246,9 +247,9 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
   if (__any_sync(0xffffffffu, over != 0u || bad) && lane == 0) atomicOr(err.word, DEVERR_RANGE);
   __syncthreads();
   float v = 0.f;
-  if (to < 8 * NT) {
+  if (tl < 8 * NT) {
 #pragma unroll
-    for (int w = 0; w < kSmWarps; ++w) v += red[w][tid % kSmRows][to];
+    for (int w = 0; w < kSmWarps; ++w) v += red[w][tid % kSmRows][tl];
   }
   if (a.la) pdl_begin();   // h
   if (to >= a.T || no >= a.N) return;
@@ -536,14 +537,55 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Tiles of 8 tokens per CTA, and microseconds that the product of a decode batch
+// takes: rounds of CTAs over the SMs, each of them by K and tiles. Measured without adapters, one round of 2, 3, 4 tiles of bf16
+// at K = 1024 2.5, 3.0, 4.1, at 2048 3.7, 4.7, 6.6, at 4096 5.7, 7.6, 11.1 us,
+// two rounds of 4 tiles 8.1, 12.7, 22.0; of e4m3 2.0, 2.3, 2.9, 3.2, 3.6, 4.5,
+// 4.0, 4.8, 6.1, and 6.0, 7.7, 12.4. (Two CTAs of one tile are not better than
+// one of two: 16 tokens of 4096 x 1024 6.0 and 5.7, with adapters 10.0 and 7.4.)
+double small_cost(const LinearArgs& a, int num_sms, int* nt_out) {
+  const double k = a.K / 1024.0;
+  const int ctas = (a.N + kSmRows - 1) / kSmRows;
+  double best = 1e30;
+  for (int nt = a.T > 8 ? 2 : 1; nt <= 4; ++nt) {
+    const long long all = (long long)ctas * ((a.T + 8 * nt - 1) / (8 * nt));
+    const double c = 1.0 + (double)((all + num_sms - 1) / num_sms) * (a.e4m3 ? 1.0 + 0.3 * nt * k : 0.9 + 0.6 * nt * k);
+    if (c < best) {
+      best = c;
+      *nt_out = nt;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
-cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cudaStream_t st) {
-  static_assert(kLinearSmallT <= 32, "one output per thread: 16 rows of at most 32 tokens");
-  const int nt = (a.T + 7) / 8, ctas = (a.N + kSmRows - 1) / kSmRows;
+// Beyond 32 tokens small sizes stay with the decode batches' kernels while
+// conversion and tcgen05 product are estimated to take longer: these measured, at
+// 64 tokens without adapters, 8.3 us at K x N = 1024 x 1024, 10.9 at 2048 x 2048,
+// 13.2 at 4096 x 1024, 12.5 at 2048 x 4096, 17.9 at 4096 x 4096, and 5 to 10 us
+// more with adapters. (48 tokens of rank 16, both ways: 1024 x 1024 5.7 and 15.6
+// us, 2048 x 2048 10.6 and 17.1, 4096 x 1024 12.5 and 24.5, 4096 x 4096 31.9 and
+// 27.4.)
+bool linear_is_small(const LinearArgs& a, int num_sms) {
+  if (a.T <= kLinearSmallT) return true;
+  const double k = a.K / 1024.0;
+  int nt;
+  double small = small_cost(a, num_sms, &nt), large = 6.5 + 1.65 * k + 0.33 * k * (a.N / 1024.0);
   if (a.la) {
-    // Above 8 tokens the product's CTAs find no room beside this launch's, which
-    // are then made fewer: so that each has an SM, if that can be had (2048 x
+    small += 1.5 + 1.1 * k * ((double)a.T * a.rank / 1024.0);
+    large += 3.0 + 1.6 * k;
+  }
+  return small < large;
+}
+
+cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cudaStream_t st) {
+  int nt;
+  small_cost(a, num_sms, &nt);
+  const int ny = (a.T + 8 * nt - 1) / (8 * nt), rows = (a.N + kSmRows - 1) / kSmRows, ctas = rows * ny;
+  if (a.la) {
+    // Of more than one tile the product's CTAs find no room beside this launch's,
+    // which are then made fewer: so that each has an SM, if that can be had (2048 x
     // 2048, rank 16, CTAs of 8, 16, 32 warps: 16 tokens 6.4, 5.2, 5.3 us, 32
     // tokens 10.0, 9.9, 8.6; of 64 registers at 4 tokens 4.4, 4.8, 5.2).
     auto shrink_ctas = [&](int warps) { return (a.T * a.rank + warps - 1) / warps; };
@@ -553,13 +595,13 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cu
     if (e != cudaSuccess) return e;
   }
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(ctas), dim3(32 * kSmWarps), 0, st, a, err);
+    return launch_pdl(kern, dim3(rows, ny), dim3(32 * kSmWarps), 0, st, a, err);
   };
   auto pick = [&](auto e4m3) {
     constexpr bool k = decltype(e4m3)::value;
-    return nt <= 1   ? go(linear_small_kernel<1, k>)
-           : nt <= 2 ? go(linear_small_kernel<2, k>)
-           : nt <= 3 ? go(linear_small_kernel<3, k>)
+    return nt == 1   ? go(linear_small_kernel<1, k>)
+           : nt == 2 ? go(linear_small_kernel<2, k>)
+           : nt == 3 ? go(linear_small_kernel<3, k>)
                      : go(linear_small_kernel<4, k>);
   };
   return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});

@@ -682,6 +682,40 @@ def test_linear_rows_far_apart(T):
     bg.moe_linear_destroy(h)
 
 
+@pytest.mark.parametrize("T,K,N,rank,x", [
+    (7100, 64, 72, 8, "bf16"), (7100, 64, 71, 0, "e4m3"), (2300, 128, 8, 64, "bf16"), (1500, 320, 201, 24, "e4m3"),
+    (700, 1088, 999, 40, "bf16"), (520, 2048, 264, 16, "e4m3"), (257, 2048, 1032, 16, "bf16"),
+    (150, 4096, 1000, 24, "e4m3"), (65, 4096, 4104, 16, "bf16"), (40, 4096, 4104, 0, "bf16")])
+def test_linear_odd_sizes_beyond_decode_batches(T, K, N, rank, x):
+    Linear(T, K, N, x=x, rank=rank, n=11, x_pad=16, y_pad=3).check()
+    Linear(T, K, N, x=x, rank=rank, n=5, ids="runs", y_pad=8).check()
+
+
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_linear_keeps_broken_adapters_apart_in_large_batches(ids):
+    test_linear_keeps_broken_adapters_to_their_own_tokens(2500, ids)
+
+
+def test_linear_large_batch_in_a_graph():
+    test_linear_in_a_graph(1200)
+
+
+def test_linear_flags_values_in_a_large_batch():
+    test_linear_flags_values_beyond_the_operands(5000)
+
+
+def test_linear_rows_far_apart_in_a_large_batch():
+    test_linear_rows_far_apart(3000)
+
+
+def test_linear_small_sizes_of_many_tokens():
+    # several CTAs of tokens on the decode batches' kernels
+    for T in (33, 40, 41, 63, 96, 129, 250):
+        Linear(T, 256, 72, rank=24, n=5, y_pad=1, x_pad=32).check()
+        Linear(T, 512, 1000, x="e4m3", rank=8).check()
+        Linear(T, 1024, 264).check()
+
+
 # --------------------------------------------------------------- all together
 @pytest.mark.parametrize("T", [1, 5, 96])
 def test_adapted_layer(T):
