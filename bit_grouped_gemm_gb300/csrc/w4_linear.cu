@@ -382,8 +382,9 @@ __device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters,
 }
 
 // kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
-// where the launch has at most two CTAs per SM (1024 tokens of 2048 x 2048: 20.3
-// against 22.9 us for the call), slower beyond (4096 tokens: 40.2 against 35.9).
+// where the launch has at most four CTAs per SM (128, 1024, 2048 tokens of 2048 x
+// 2048: 13.6, 17.8, 24.7 us for the call against 14.8, 19.3, 26.0), slower beyond
+// (4096 tokens: 38.9 against 35.2).
 template <bool kDeep, bool kE4m3>
 __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
     linear_prep_kernel(const LinearArgs args, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
@@ -622,7 +623,7 @@ cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16
   };
   auto pick = [&](auto e4m3) {
     constexpr bool k = decltype(e4m3)::value;
-    return nx + nw <= 2 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
+    return nx + nw <= 4 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
   };
   return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
