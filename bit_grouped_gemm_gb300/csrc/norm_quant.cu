@@ -9,7 +9,9 @@
 // come from one reduction: the mean of squares needs x', and max|v| is
 // max|x' w| times the row's factor (rounding is monotone, so this is the largest
 // |v| to the bit). CTAs walk the rows and load the next one before they reduce
-// and store the last.
+// and store the last. 16384 rows of 4096 with a bf16 delta and group scales, 606
+// MB: 105 us a call (5.8 TB/s); 4096 rows of 2048 with an fp32 delta, 92 MB: 16.0;
+// one row 1.7 us in a graph.
 #include "moe_common.cuh"
 
 namespace moe {

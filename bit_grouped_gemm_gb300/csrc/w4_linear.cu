@@ -136,13 +136,15 @@ __global__ void __launch_bounds__(1024) lora_shrink_kernel(const LinearArgs args
 // first is used (24 tokens of 2048 x 2048, without adapters: 4.7 us, 6.1 with x
 // loaded where it is used), which takes 128 registers above 8 tokens: then a CTA
 // has its SM for itself. Weights are loaded before the wait for the launch
-// before. With adapters that launch is lora_shrink_kernel, and x and the
-// adapters' ids are older than it: all that does not need h runs beside it.
+// before. With adapters that launch is lora_shrink_kernel, and x and the adapters'
+// ids are older than it: all that does not need h runs beside it. Bound by
+// latency: one token of 2048 x 2048 2.9 us, with an adapter 4.3; 16 tokens 3.6
+// and 5.2.
 // (h taken in this launch instead, once per cluster of 8 CTAs and shared over
 // distributed shared memory, was slower when it was tried: 6.6 against 4.7 us at
-// one token of 2048 x 2048 and rank 16, 12.4 against 6.6 us at 16; now 4.3 and
-// 5.2. Against 8 warps of twice the groups, 16 warps: 3.2 against 4.6 us at one
-// token without adapters.)
+// one token of 2048 x 2048 and rank 16, 12.4 against 6.6 us at 16. Against 8 warps
+// of twice the groups, 16 warps: 3.2 against 4.6 us at one token without
+// adapters.)
 // ---------------------------------------------------------------------------
 constexpr int kSmRows = 16;
 constexpr int kSmWarps = 16;
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
 // 16 adapters: one chain of L2 round trips per adapter.)
 // The other CTAs rebuild 16384 packed weights each as fp16 in perm8 order.
+// Bound by latency and L2: about 10 us of the 55.6 at 4096 x 2048 x 4096.
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepSplit = 4;
