@@ -301,16 +301,29 @@ __host__ __device__ inline int prep_row_bytes(int K) { return prep_cols(K) * 2 +
 __device__ __forceinline__ void prep_weights(const LinearArgs& a, uint16_t* __restrict__ w16, int cta,
                                              const DevErr& err) {
   const long long words = (long long)a.N * (a.K / 8);
+  // loaded before the wait for the launch before, whose last CTAs this runs beside
+  constexpr int kN = kPrepWords / 256;
+  uint32_t q[kN], s[kN], b[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const long long wi = (long long)cta * kPrepWords + 256 * i + threadIdx.x;
+    q[i] = s[i] = b[i] = 0u;
+    if (wi < words) {
+      q[i] = __ldg(a.w.q + wi);
+      s[i] = __ldg(a.w.s + (wi >> 3));
+      b[i] = __ldg(a.w.b + (wi >> 3));
+    }
+  }
+  pdl_begin();
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kPrepWords / 256; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const long long wi = (long long)cta * kPrepWords + 256 * i + threadIdx.x;
     if (wi < words) {
-      const uint32_t s = __ldg(a.w.s + (wi >> 3)), b = __ldg(a.w.b + (wi >> 3));
-      bad |= sb_out_of_range(s, b);
+      bad |= sb_out_of_range(s[i], b[i]);
       uint32_t o[4];
-      dequant_word_f16_perm8(__ldg(a.w.q + wi), __half2half2(__float2half_rn(bf16_to_f32((uint16_t)s))),
-                             __half2half2(__float2half_rn(bf16_to_f32((uint16_t)b))), o);
+      dequant_word_f16_perm8(q[i], __half2half2(__float2half_rn(bf16_to_f32((uint16_t)s[i]))),
+                             __half2half2(__float2half_rn(bf16_to_f32((uint16_t)b[i]))), o);
       reinterpret_cast<uint4*>(w16)[wi] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
@@ -397,11 +410,11 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_id[kPrepTok], s_list[kPrepTok], s_tok[kPrepTok], s_sum[8];
   __shared__ __align__(16) uint16_t s_bin[8][256];   // tokens by warp and bin of adapters
-  pdl_begin();
   if ((int)blockIdx.x >= nx) {
     prep_weights(a, w16, (int)blockIdx.x - nx, err);
     return;
   }
+  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part_k = (int)blockIdx.x % kPrepSplit, t0 = (int)blockIdx.x / kPrepSplit * kPrepTok;
   const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
@@ -542,11 +555,12 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
 }
 
 // Tiles of 8 tokens per CTA, and microseconds that the product of a decode batch
-// takes: rounds of CTAs over the SMs, each of them by K and tiles. Measured without adapters, one round of 2, 3, 4 tiles of bf16
-// at K = 1024 2.5, 3.0, 4.1, at 2048 3.7, 4.7, 6.6, at 4096 5.7, 7.6, 11.1 us,
-// two rounds of 4 tiles 8.1, 12.7, 22.0; of e4m3 2.0, 2.3, 2.9, 3.2, 3.6, 4.5,
-// 4.0, 4.8, 6.1, and 6.0, 7.7, 12.4. (Two CTAs of one tile are not better than
-// one of two: 16 tokens of 4096 x 1024 6.0 and 5.7, with adapters 10.0 and 7.4.)
+// takes: rounds of CTAs over the SMs, each of them by K and tiles. Measured
+// without adapters, one round of 2, 3, 4 tiles of bf16 at K = 1024 2.5, 3.0, 4.1,
+// at 2048 3.7, 4.7, 6.6, at 4096 5.7, 7.6, 11.1 us, two rounds of 4 tiles 8.1,
+// 12.7, 22.0; of e4m3 2.0, 2.3, 2.9, 3.2, 3.6, 4.5, 4.0, 4.8, 6.1, and 6.0, 7.7,
+// 12.4. (Two CTAs of one tile are not better than one of two: 16 tokens of 4096 x
+// 1024 6.0 and 5.7, with adapters 10.0 and 7.4.)
 double small_cost(const LinearArgs& a, int num_sms, int* nt_out) {
   const double k = a.K / 1024.0;
   const int ctas = (a.N + kSmRows - 1) / kSmRows;
@@ -595,7 +609,8 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cu
     auto shrink_ctas = [&](int warps) { return (a.T * a.rank + warps - 1) / warps; };
     int warps = nt == 1 ? 8 : 16;
     if (nt > 1 && shrink_ctas(16) + ctas > num_sms && shrink_ctas(32) + ctas <= num_sms) warps = 32;
-    const cudaError_t e = launch_pdl(a.e4m3 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>, dim3(shrink_ctas(warps)), dim3(32 * warps), 0, st, a);
+    const cudaError_t e = launch_pdl(a.e4m3 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>,
+                                     dim3(shrink_ctas(warps)), dim3(32 * warps), 0, st, a);
     if (e != cudaSuccess) return e;
   }
   auto go = [&](auto kern) {
