@@ -286,12 +286,12 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // (One CTA per 16 tokens that went through the adapters one by one, its warps
 // splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
 // 16 adapters: one chain of L2 round trips per adapter.)
-// The other CTAs rebuild 16384 packed weights each as fp16 in perm8 order.
+// The other CTAs rebuild 8192 packed weights each as fp16 in perm8 order.
 // Bound by latency and L2: about 10 us of the 55.6 at 4096 x 2048 x 4096.
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepSplit = 4;
-constexpr int kPrepWords = 2048;   // packed words per weight CTA
+constexpr int kPrepWords = 1024;   // packed words per weight CTA
 
 // K columns of a token CTA (a multiple of 32), and bytes of a row of its tile
 // (64 more: 8 lanes of one 16-byte load then touch all banks)
@@ -398,9 +398,9 @@ __device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters,
 }
 
 // kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
-// where the launch has at most four CTAs per SM (128, 1024, 2048 tokens of 2048 x
-// 2048: 13.6, 17.8, 24.7 us for the call against 14.8, 19.3, 26.0), slower beyond
-// (4096 tokens: 38.9 against 35.2).
+// where the launch has at most four CTAs per SM, the shorter weight CTAs counted
+// half (128, 1024, 2048 tokens of 2048 x 2048: 13.6, 17.8, 24.7 us for the call
+// against 14.8, 19.3, 26.0), slower beyond (4096 tokens: 38.9 against 35.2).
 template <bool kDeep, bool kE4m3>
 __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
     linear_prep_kernel(const LinearArgs args, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
@@ -414,7 +414,6 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     prep_weights(a, w16, (int)blockIdx.x - nx, err);
     return;
   }
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part_k = (int)blockIdx.x % kPrepSplit, t0 = (int)blockIdx.x / kPrepSplit * kPrepTok;
   const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
@@ -448,16 +447,25 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
         if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 16 * c) = to_bf16(a, xv[r][j]);
       }
   };
+  // The adapters' ids are older than the launch before (x may be its output).
+  const int blk0 = t0 / kOrderBlock * kOrderBlock, n = min(kOrderBlock, a.T - blk0);
+  int id0 = -1, id1 = -1, own_id = -1;
+  if (a.la) {
+    const int at = order_sample(tid, n);
+    if (tid < kOrderSamples && at < n) {
+      id0 = adapter_of(a, blk0 + at - 1);
+      id1 = adapter_of(a, blk0 + at);
+    }
+    if (tid < kPrepTok) own_id = adapter_of(a, t0 + tid);
+  }
+  pdl_begin();
   get_x(0, [&](int tl) { return t0 + tl; });
   if (a.la) {
-    // Meanwhile: are the block's tokens to be ordered by adapter?
-    const int blk0 = t0 / kOrderBlock * kOrderBlock, n = min(kOrderBlock, a.T - blk0);
-    const int at = order_sample(tid, n);
-    bool change = false;
-    if (tid < kOrderSamples && at < n) change = adapter_of(a, blk0 + at - 1) != adapter_of(a, blk0 + at);
+    // are the block's tokens to be ordered by adapter?
+    const bool change = id0 != id1;
     if (tid < kPrepTok) {
       s_tok[tid] = t0 + tid;
-      s_id[tid] = adapter_of(a, t0 + tid);
+      s_id[tid] = own_id;
     }
     const bool ordered = order_rule(__syncthreads_count(change), n);
     // (x's loads stay where they are, under the ids')
@@ -535,8 +543,8 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
   }
   // the cluster's sums, each CTA a quarter of the entries
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int n = kPrepTok * a.rank;
-  for (int i = part_k * 256 + tid; i < n; i += 256 * kPrepSplit) {
+  const int sums = kPrepTok * a.rank;
+  for (int i = part_k * 256 + tid; i < sums; i += 256 * kPrepSplit) {
     const int tl = i / a.rank, ad = s_id[tl];
     if (ad < 0) continue;
     float v = 0.f;
@@ -641,7 +649,7 @@ cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16
   };
   auto pick = [&](auto e4m3) {
     constexpr bool k = decltype(e4m3)::value;
-    return nx + nw <= 4 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
+    return nx + nw / 2 <= 4 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
   };
   return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
