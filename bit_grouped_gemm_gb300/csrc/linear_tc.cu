@@ -21,10 +21,10 @@
 //
 // Every wait is bounded, as in gemm_tc2.cu.
 //
-// Bound by the tensor cores at many tokens: 4096 x 2048 x 4096 45 us without
-// adapters (1.5 PFLOP/s, conversion included), 55.6 with 8 of rank 32; the
-// product alone 47 us there (76% of the tensor pipe's time). Below 1000 tokens by
-// latency: 128 x 2048 x 2048 13.7 us, of which conversion and product each wait
+// Bound by the tensor cores at many tokens: 4096 x 2048 x 4096 43.7 us without
+// adapters (1.57 PFLOP/s, conversion included), 52.4 with 8 of rank 32; the
+// product alone 47 us cold (77% of the tensor pipe's time). Below 1000 tokens by
+// latency: 128 x 2048 x 2048 13.3 us, of which conversion and product each wait
 // for a ring of copies to fill.
 #include "pair.cuh"
 
@@ -623,12 +623,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (300), its operands' copies at 75 bytes per cycle into an SM, and at 8000 out
 // of L2. Of tiles that come out alike the widest is taken: fewer CTAs then read
 // the same lines. Measured for the call at K = 2048 with 8 adapters of rank 16
-// (widths 64, 128, 192, 224, 256): 512 x 2048 16.3, 15.2, 17.2, 18.6, 20.0 us;
-// 1024 x 2048 26.8, 17.8, 18.5, 19.9, 21.1; 4096 x 2048 70.4, 46.7, 40.0, 41.0,
-// 35.2; 4096 x 4096, e4m3 of rank 32, 133.6, 76.3, 61.7, 55.8, 57.3.
+// (widths 64, 128, 192, 224, 256): 512 x 2048 15.7, 14.7 (96: 14.4), 16.6, 18.1,
+// 19.5 us; 1024 x 2048 26.2, 17.1 (160: 17.0), 17.7, 19.0, 20.3; 4096 x 2048 69.5,
+// 45.7, 38.7, 39.6, 34.5; 4096 x 4096, e4m3 of rank 32, 130.2, 72.9, 58.1, 52.2,
+// 53.8.
 // With few tiles, two pairs of a cluster take half of K each, for the exchange of
-// their sums: 128 x 2048 13.7 against 15.1 us, 200 x 1000 at K = 4096 20.2
-// against 24.2; but 512 x 2048 16.6 against 15.2. (Four pairs: 19.2 against 12.3
+// their sums: 128 x 2048 13.3 against 14.6 us, 200 x 1000 at K = 4096 19.7
+// against 23.6; but 512 x 2048 16.0 against 14.7. (Four pairs: 19.2 against 12.3
 // at 128 x 2048 without adapters; the device holds 15 clusters of 8 such CTAs.)
 static void linear_shape(int T, int N, int K, int num_sms, int* bn_out, int* split_out) {
   const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2, nk = K / 64;

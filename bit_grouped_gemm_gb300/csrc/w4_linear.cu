@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
 // 16 adapters: one chain of L2 round trips per adapter.)
 // The other CTAs rebuild 8192 packed weights each as fp16 in perm8 order.
-// Bound by latency and L2: about 10 us of the 55.6 at 4096 x 2048 x 4096.
+// Weights and ids are loaded before the wait for the launch before. Bound by
+// latency and L2: about 8 us of the 52.4 at 4096 x 2048 x 4096.
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepSplit = 4;
