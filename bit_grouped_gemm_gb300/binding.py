@@ -16,7 +16,7 @@ from typing import Optional
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_w4.so")
 
-MOE_OK = 0
+MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_CAPACITY = 0, 1, 4
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_CUDA", 4: "MOE_ERR_CAPACITY", 5: "MOE_ERR_DEVICE_TIMEOUT",
                 6: "MOE_ERR_OPERAND_RANGE"}

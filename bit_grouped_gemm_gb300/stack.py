@@ -95,7 +95,9 @@ class AdaptedLayer:
     layer's first norm. ``norm1`` and ``norm2`` are bf16 [H]; ``proj`` is a
     (qweight, scales, biases) triple of an H x H matrix; ``adapters`` a
     ``binding.MoeLora`` (its tensors must outlive the layer) or None;
-    ``score`` a ``binding.MoeScoreDesc``.
+    ``score`` a ``binding.MoeScoreDesc``. A call takes up to ``max_tokens`` tokens,
+    or the plan's if these are fewer; wrong arguments are refused before the
+    first launch, so x is then as it was.
     """
 
     def __init__(self, plan: int, layer: DeviceLayer, norm1, norm2, proj, score,
@@ -104,7 +106,8 @@ class AdaptedLayer:
         dev = layer.router_w.device
         self.plan, self.layer, self.score, self.adapters = plan, layer, score, adapters
         self.norm1, self.norm2, self.proj = norm1, norm2, proj
-        self.alpha = alpha
+        self.alpha, self.max_tokens = alpha, max_tokens
+        self.plan_tokens = 0    # the largest T that the plan is known to take
         self.proj_c = binding.w4(*proj)
         rank = adapters.rank if adapters is not None else 0
         self.linear = binding.moe_linear_create(binding.linear_desc(H, H, max_tokens, rank),
@@ -122,9 +125,33 @@ class AdaptedLayer:
             binding.moe_linear_destroy(self.linear)
             self.linear = None
 
+    def _check(self, x, y, adapter) -> None:
+        H, dev = self.h8.shape[1], self.h8.device
+        rows = lambda t, dtype, shape: (isinstance(t, torch.Tensor) and t.dtype == dtype and
+                                        t.shape == shape and t.device == dev and t.is_contiguous())
+        T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+        if T > self.max_tokens:
+            raise binding.MoeError(binding.MOE_ERR_CAPACITY, "AdaptedLayer")
+        if T > self.plan_tokens:
+            # A call without logits tells of a T above the plan's before it looks
+            # at them, and launches nothing.
+            try:
+                binding.moe_route_scored(self.plan, None, T, self.score, stream=0)
+            except binding.MoeError as e:
+                if e.status == binding.MOE_ERR_CAPACITY:
+                    raise
+            self.plan_tokens = T
+        ok = self.linear is not None and T > 0 and rows(x, torch.bfloat16, (T, H))
+        ok = ok and (y is None or rows(y, torch.float32, (T, H)))
+        if adapter is not None:
+            ok = ok and self.adapters is not None and rows(adapter, torch.int32, (T,))
+        if not ok:
+            raise binding.MoeError(binding.MOE_ERR_INVALID_ARG, "AdaptedLayer")
+
     def __call__(self, x: torch.Tensor, y: Optional[torch.Tensor], adapter=None,
                  stream=None) -> torch.Tensor:
         """One pass over T = len(x) tokens; ``adapter`` is int32 [T] (-1: none)."""
+        self._check(x, y, adapter)
         T, H = x.shape
         L = self.layer
         first = binding.norm_desc(H, alpha=self.alpha, delta_f32=True)
