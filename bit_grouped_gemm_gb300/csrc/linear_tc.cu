@@ -92,7 +92,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 __device__ __forceinline__ int token_adapter(const LinearArgs& a, int t) {
-  const int id = t < a.T ? __ldg(a.adapter + t) : -1;
+  const int id = t < a.T ? __ldcg(a.adapter + t) : -1;
   return (unsigned)id < (unsigned)a.n_adapters ? id : -1;
 }
 
@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // What the launch before wrote (x16, W16, h) is read after pdl_wait; the
-  // adapters' ids are older: that launch waited for all before it.
+  // adapters' ids and the rows' scales are older, as that launch waited for all
+  // before it, and are read through L2.
 
   // this pair's chunks of K
   const int nk_all = p.a.K / 64, c_lo = part * nk_all / split, nk = (part + 1) * nk_all / split - c_lo;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int place = m0 + 128 * (int)rank + 32 * (warp & 3) + lane;
     live = place < p.a.T;
     y_row = live && kLora ? __ldcg(p.a.order + place) : place;
-    if (live && p.a.x_scale) y_scale = __ldg(p.a.x_scale + y_row);
+    if (live && p.a.x_scale) y_scale = __ldcg(p.a.x_scale + y_row);
   };
 
   if (warp == 0) {

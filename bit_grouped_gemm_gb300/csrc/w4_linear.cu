@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
 // 16 adapters: one chain of L2 round trips per adapter.)
 // The other CTAs rebuild 8192 packed weights each as fp16 in perm8 order.
-// Weights and ids are loaded before the wait for the launch before. Bound by
+// Weights are loaded before the wait for the launch before. Bound by
 // latency and L2: about 8 us of the 52.4 at 4096 x 2048 x 4096.
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
@@ -448,7 +448,7 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
         if (a.la) *reinterpret_cast<uint4*>(smem + tl * row_bytes + 16 * c) = to_bf16(a, xv[r][j]);
       }
   };
-  // The adapters' ids are older than the launch before (x may be its output).
+  pdl_begin();   // (x and the ids may be the launch before's output)
   const int blk0 = t0 / kOrderBlock * kOrderBlock, n = min(kOrderBlock, a.T - blk0);
   int id0 = -1, id1 = -1, own_id = -1;
   if (a.la) {
@@ -459,7 +459,6 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     }
     if (tid < kPrepTok) own_id = adapter_of(a, t0 + tid);
   }
-  pdl_begin();
   get_x(0, [&](int tl) { return t0 + tl; });
   if (a.la) {
     // are the block's tokens to be ordered by adapter?

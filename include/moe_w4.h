@@ -412,10 +412,10 @@ moe_status moe_linear_scratch_bytes(const moe_linear_desc* desc, size_t* bytes);
  * moe_linear_get_error; x A^T is kept to 16 significant bits. A token's row
  * depends on its own x, scale and adapter alone: infinities and NaNs of another
  * token or another adapter do not reach it (an adapter's own tokens get
- * unspecified values from them). Weights and
- * adapters are read under the rule for weights above; like them, `adapter`
- * and x must not be written by a kernel that the call's own launches could
- * overtake: any launch before the call on the same stream is waited for.
+ * unspecified values from them). Weights and adapters (a, b, scale) are read
+ * under the rule for weights above; x, x_scale and the ids in `adapter` only
+ * once every earlier launch on the stream has completed, so the launch just
+ * before the call may write them.
  * Calls on one handle must be ordered on the device. */
 moe_status moe_linear_forward(moe_linear_t linear, const void* x, int x_type, long long x_stride,
                               const float* x_scale, int T, const moe_w4* w,
