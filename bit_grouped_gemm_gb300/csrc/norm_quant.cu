@@ -26,7 +26,8 @@ struct NqParams {
   uint8_t* q;
   float* qs;
   long long x_ld, d_ld, o_ld;
-  int T, H, d_f32, group;   // group: 0 the row, 128
+  unsigned T;               // (a step past the last row then does not wrap)
+  int H, d_f32, group;      // group: 0 the row, 128
   float eps, alpha;
 };
 
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_quant_kernel(const NqPa
   const int nvec = p.H / 8;
   const int ngroups = p.group ? (p.H + p.group - 1) / p.group : 1;
   uint4 xr[NV], dr[NV * (kD == 2 ? 2 : 1)];
-  auto load = [&](int t) {
+  auto load = [&](unsigned t) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + TPR * i;
@@ -82,11 +83,11 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_quant_kernel(const NqPa
       }
     }
   };
-  int t = blockIdx.x * kRows + sub;
+  unsigned t = blockIdx.x * kRows + sub;
   load(t);
   // (the trip count is the CTA's, not the row's: every thread meets the barrier)
   int buf = 0;
-  for (int t0 = blockIdx.x * kRows; t0 < p.T; t0 += gridDim.x * kRows, t += gridDim.x * kRows, buf ^= 1) {
+  for (unsigned t0 = blockIdx.x * kRows; t0 < p.T; t0 += gridDim.x * kRows, t += gridDim.x * kRows, buf ^= 1) {
     const bool row = t < p.T;
     float v[NV][8];
     float ss = 0.f, mx = 0.f;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_quant_kernel(const NqPa
 template <int TPR, int NV, int kD>
 cudaError_t launch_nq(const NqParams& p, cudaStream_t st) {
   constexpr int kRows = cta_threads(TPR) / TPR;
-  const int ctas = (p.T + kRows - 1) / kRows;
+  const int ctas = (int)((p.T + kRows - 1) / kRows);
   static int resident[64] = {};   // CTAs the device holds at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -274,7 +275,7 @@ extern "C" moe_status moe_norm_quant(const moe_norm_desc* d, const uint16_t* x, 
   p.xn = xn_out;
   p.q = q_out;
   p.qs = q_scale;
-  p.T = T;
+  p.T = (unsigned)T;
   p.H = H;
   p.d_f32 = d->delta_f32;
   p.group = d->quant_group;
