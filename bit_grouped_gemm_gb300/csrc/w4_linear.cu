@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 }
 
 // ---------------------------------------------------------------------------
-// Larger batches, first launch, in clusters of 4 CTAs. The first nx CTAs are
-// token CTAs (they take longer): a cluster takes 32 tokens, each of its CTAs a
-// quarter of K. A CTA writes its part of x as fp16 rows in perm8 order and
+// Larger batches, first launch, in clusters of 4 CTAs, or 8 where the tokens'
+// tile of a quarter of K is beyond shared memory. The first nx CTAs are
+// token CTAs (they take longer): a cluster takes 32 tokens, each of its CTAs an
+// equal part of K. A CTA writes its part of x as fp16 rows in perm8 order and
 // keeps it in shared memory as bf16; then its 8 warps take jobs of (adapter
 // among the 32 tokens, 8 ranks) on mma.sync, each over the CTA's whole part of
 // K, and put the rows of the adapter's own tokens into shared memory. The
@@ -291,13 +292,15 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // latency and L2: about 8 us of the 52.4 at 4096 x 2048 x 4096.
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
-constexpr int kPrepSplit = 4;
 constexpr int kPrepWords = 1024;   // packed words per weight CTA
 
 // K columns of a token CTA (a multiple of 32), and bytes of a row of its tile
 // (64 more: 8 lanes of one 16-byte load then touch all banks)
-__host__ __device__ inline int prep_cols(int K) { return (K / 32 + kPrepSplit - 1) / kPrepSplit * 32; }
-__host__ __device__ inline int prep_row_bytes(int K) { return prep_cols(K) * 2 + 64; }
+__host__ __device__ constexpr int prep_cols(int K, int split) { return (K / 32 + split - 1) / split * 32; }
+__host__ __device__ constexpr int prep_row_bytes(int K, int split) { return prep_cols(K, split) * 2 + 64; }
+// shared memory of a token CTA beside its static 4.5 KB: the tile and the sums
+constexpr int prep_smem(int K, int rank, int split) { return kPrepTok * (prep_row_bytes(K, split) + rank * 4); }
+constexpr int kPrepSmemMax = 227 * 1024 - 5 * 1024;
 
 __device__ __forceinline__ void prep_weights(const LinearArgs& a, uint16_t* __restrict__ w16, int cta,
                                              const DevErr& err) {
@@ -402,8 +405,8 @@ __device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters,
 // where the launch has at most four CTAs per SM, the shorter weight CTAs counted
 // half (128, 1024, 2048 tokens of 2048 x 2048: 13.6, 17.8, 24.7 us for the call
 // against 14.8, 19.3, 26.0), slower beyond (4096 tokens: 38.9 against 35.2).
-template <bool kDeep, bool kE4m3>
-__global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
+template <int kSplit, bool kDeep, bool kE4m3>   // kSplit: parts of K, CTAs per cluster
+__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
     linear_prep_kernel(const LinearArgs args, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
                        const DevErr err) {
   LinearArgs a = args;
@@ -416,9 +419,9 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part_k = (int)blockIdx.x % kPrepSplit, t0 = (int)blockIdx.x / kPrepSplit * kPrepTok;
-  const int cols = prep_cols(a.K), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
-  const int row_bytes = prep_row_bytes(a.K);
+  const int part_k = (int)blockIdx.x % kSplit, t0 = (int)blockIdx.x / kSplit * kPrepTok;
+  const int cols = prep_cols(a.K, kSplit), k0 = part_k * cols, kn = max(0, min(cols, a.K - k0));
+  const int row_bytes = prep_row_bytes(a.K, kSplit);
   float* part = reinterpret_cast<float*>(smem + kPrepTok * row_bytes);   // [token][rank]
   // x, 8 columns at a time: a warp takes every 8th row, kCols vectors of each of
   // its 4 rows in flight per lane
@@ -541,15 +544,15 @@ __global__ void __cluster_dims__(kPrepSplit, 1, 1) __launch_bounds__(256, kDeep 
               make_float2(acc[mt][2 * h], acc[mt][2 * h + 1]);
       }
   }
-  // the cluster's sums, each CTA a quarter of the entries
+  // the cluster's sums, each CTA an equal part of the entries
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int sums = kPrepTok * a.rank;
-  for (int i = part_k * 256 + tid; i < sums; i += 256 * kPrepSplit) {
+  for (int i = part_k * 256 + tid; i < sums; i += 256 * kSplit) {
     const int tl = i / a.rank, ad = s_id[tl];
     if (ad < 0) continue;
     float v = 0.f;
 #pragma unroll
-    for (int c = 0; c < kPrepSplit; ++c) {
+    for (int c = 0; c < kSplit; ++c) {
       uint32_t addr;
       float o;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(part + i)), "r"(c));
@@ -637,10 +640,13 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cu
 cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16, DevErr err,
                                int num_sms, cudaStream_t st) {
   const long long words = (long long)a.N * (a.K / 8);
+  // (beyond K = 13,056 to 13,952, by rank; the largest sizes fit eight parts)
+  static_assert(prep_smem(16384, 128, 8) <= kPrepSmemMax, "K and rank at most");
+  const bool eight = a.la && prep_smem(a.K, a.rank, 4) > kPrepSmemMax;
+  const int split = eight ? 8 : 4, smem = a.la ? prep_smem(a.K, a.rank, split) : 0;
   int nw = (int)((words + kPrepWords - 1) / kPrepWords);
-  nw = (nw + kPrepSplit - 1) / kPrepSplit * kPrepSplit;   // whole clusters
-  const int nx = (a.T + kPrepTok - 1) / kPrepTok * kPrepSplit;
-  const int smem = a.la ? kPrepTok * (prep_row_bytes(a.K) + a.rank * 4) : 0;
+  nw = (nw + split - 1) / split * split;   // whole clusters
+  const int nx = (a.T + kPrepTok - 1) / kPrepTok * split;
   auto go = [&](auto kern) {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     return e != cudaSuccess
@@ -649,7 +655,9 @@ cudaError_t launch_linear_prep(const LinearArgs& a, uint16_t* x16, uint16_t* w16
   };
   auto pick = [&](auto e4m3) {
     constexpr bool k = decltype(e4m3)::value;
-    return nx + nw / 2 <= 4 * num_sms ? go(linear_prep_kernel<true, k>) : go(linear_prep_kernel<false, k>);
+    // (a tile of more than 100 KB leaves an SM no more CTAs than the deep kernel's)
+    if (eight) return go(linear_prep_kernel<8, true, k>);
+    return nx + nw / 2 <= 4 * num_sms ? go(linear_prep_kernel<4, true, k>) : go(linear_prep_kernel<4, false, k>);
   };
   return a.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
