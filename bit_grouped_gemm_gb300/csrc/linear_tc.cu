@@ -17,7 +17,8 @@
 // bf16 (the value and what its rounding left), each multiplied with B's own
 // bf16: the products are exact to 16 bits of h. A zero times an infinity or a NaN
 // would carry one adapter's broken B into other requests' rows, so B goes in with
-// these as zeros (which is why it does not come by TMA).
+// these as the largest bf16 (which is why it does not come by TMA): zero times
+// that is zero, and in the adapter's own rows no ordinary number is left.
 //
 // Every wait is bounded, as in gemm_tc2.cu.
 //
@@ -109,9 +110,10 @@ __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t smem_addr) {
   return d;
 }
 
-// Two bf16 with infinities and NaNs as zeros.
+// Two bf16 with infinities and NaNs as the largest finite value of their sign.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
-  return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+  const uint32_t no = __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+  return (w & ~(no & 0x7FFF7FFFu)) | (no & 0x7F7F7F7Fu);
 }
 
 // Barrier of the 128 adapter threads that tells whether all of them go on, so

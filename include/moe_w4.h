@@ -411,8 +411,9 @@ moe_status moe_linear_scratch_bytes(const moe_linear_desc* desc, size_t* bytes);
  * rows enter as fp16 under the operand contract above, reported by
  * moe_linear_get_error; x A^T is kept to 16 significant bits. A token's row
  * depends on its own x, scale and adapter alone: infinities and NaNs of another
- * token or another adapter do not reach it (an adapter's own tokens get
- * unspecified values from them). Weights and adapters (a, b, scale) are read
+ * token or another adapter do not reach it. An infinity or NaN in an adapter's
+ * own arrays shows in its tokens' outputs that it feeds, as an infinity, a NaN or
+ * a value of the size of the largest bf16 times x A^T. Weights and adapters (a, b, scale) are read
  * under the rule for weights above; x, x_scale and the ids in `adapter` only
  * once every earlier launch on the stream has completed, so the launch just
  * before the call may write them.
