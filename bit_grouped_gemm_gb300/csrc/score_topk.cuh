@@ -210,28 +210,31 @@ __device__ __forceinline__ int list_candidates(unsigned cand, int e0, int* list)
 // and what its rounding left), good to 1e-11, and only what 2e-10 cannot tell
 // goes to FP64. One score per lane, of the experts in doubt alone: a look at
 // every expert of the row took 8 us unrolled (its code is cold on the SM) and
-// 11 us in loops (each score is one long chain).
+// 11 us in loops (each score is one long chain). Sums and products whose rounding
+// is taken up by the pair are written as rounded operations: fused into one with
+// their neighbours, which the compiler may do to + and *, that rounding would count
+// twice (a sigmoid off by 4.6e-9).
 // ---------------------------------------------------------------------------
 struct F2 {
   float h, l;
 };
 __device__ __forceinline__ F2 sum_ordered(float a, float b) {   // |a| >= |b| or a = 0
-  const float s = a + b;
-  return {s, b - (s - a)};
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
 __device__ __forceinline__ F2 sum_any(float a, float b) {
-  const float s = a + b, t = s - a;
-  return {s, (a - (s - t)) + (b - t)};
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
 // c + a b for a constant c above |a b|
 __device__ __forceinline__ F2 mul_add(F2 a, F2 b, float ch, float cl) {
-  const float p = a.h * b.h;
+  const float p = __fmul_rn(a.h, b.h);
   const float e = fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h);
   const F2 s = sum_ordered(ch, p);
   return sum_ordered(s.h, s.l + (e + cl));
 }
 
-// exp(x), |x| <= 80, to a relative 1e-11: x = n ln 2 + 2 r with ln 2 split as
+// exp(x) to a relative 1e-11 for |x| <= 40, 4e-11 for |x| <= 80: x = n ln 2 + 2 r with ln 2 split as
 // 355/512 less a remainder (n 355/512 and its difference from x are exact),
 // then the exponential's series at r, |r| <= 0.174, up to r^3 in pairs and
 // from r^4 in floats (r^4/24's rounding: 2e-12), squared.
@@ -239,7 +242,7 @@ __device__ __forceinline__ F2 exp_f2(float x) {
   const float n = rintf(x * 1.44269504f);
   const float t = fmaf(n, -0.693359375f, x);
   const float ch = 0x1.bd0106p-13f, cl = -0x1.cf79acp-40f;   // 355/512 - ln 2
-  const float p = n * ch;
+  const float p = __fmul_rn(n, ch);
   F2 r = sum_any(t, p);
   r.l += fmaf(n, ch, -p) + n * cl;
   r.h *= 0.5f;
@@ -250,7 +253,7 @@ __device__ __forceinline__ F2 exp_f2(float x) {
   g = mul_add(r, g, 0.5f, 0.f);
   g = mul_add(r, g, 1.f, 0.f);
   g = mul_add(r, g, 1.f, 0.f);
-  const float sq = g.h * g.h;
+  const float sq = __fmul_rn(g.h, g.h);
   const F2 e = sum_ordered(sq, fmaf(g.h, g.h, -sq) + 2.f * g.h * g.l);
   const float k = __int_as_float(((int)n + 127) << 23);   // 2^n, |n| <= 116
   return {e.h * k, e.l * k};
