@@ -300,6 +300,34 @@ def moe_residual_add(plan: int, x, y, T: int, alpha: float, x_out=None, xn_out=N
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
+# The tensor types that stand for each of the header's element types (torch's
+# objects, filled in on first use).
+_BF16, _E4M3, _F32, _INT32, _WORDS = set(), set(), set(), set(), set()
+
+
+def _load_types() -> None:
+    import torch
+    for types, names in ((_BF16, "bfloat16 int16 uint16"), (_E4M3, "float8_e4m3fn uint8"),
+                         (_F32, "float32"), (_INT32, "int32"), (_WORDS, "int32 uint32")):
+        types.update(getattr(torch, n) for n in names.split())
+
+
+def _typed(t, types: set, where: str):
+    """Address of a tensor, which has to be of one of the types (None and
+    addresses are passed on)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype in types:
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
+    if not types:
+        _load_types()
+        return _typed(t, types, where)
+    names = ", ".join(sorted(map(str, types)))
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{where} (a tensor of {t.dtype} for {names})")
+
 
 def norm_desc(hidden: int, eps: float = 1e-6, alpha: float = 1.0, delta_f32: bool = False,
               quant_group: int = 0, x_stride: int = 0, delta_stride: int = 0,
@@ -311,20 +339,24 @@ def norm_desc(hidden: int, eps: float = 1e-6, alpha: float = 1.0, delta_f32: boo
 def moe_norm_quant(desc: MoeNormDesc, x, delta, weight, T: int, x_out=None, xn_out=None,
                    q_out=None, q_scale=None, stream=None) -> None:
     """Residual addition, RMS norm and e4m3 output (see header)."""
-    _status("moe_norm_quant", ctypes.byref(desc), _ptr(x), _ptr(delta), _ptr(weight), T,
-            _ptr(x_out), _ptr(xn_out), _ptr(q_out), _ptr(q_scale), _stream(stream))
+    at = "moe_norm_quant"
+    _status(at, ctypes.byref(desc), _typed(x, _BF16, at),
+            _typed(delta, _F32 if desc.delta_f32 else _BF16, at), _typed(weight, _BF16, at), T,
+            _typed(x_out, _BF16, at), _typed(xn_out, _BF16, at), _typed(q_out, _E4M3, at),
+            _typed(q_scale, _F32, at), _stream(stream))
 
 
 def moe_router_logits(plan: int, x, T: int, router_w, router_bias, logits, stream=None) -> None:
-    _status("moe_router_logits", plan, _ptr(x), T, _ptr(router_w), _ptr(router_bias), _ptr(logits),
-            _stream(stream))
+    at = "moe_router_logits"
+    _status(at, plan, _typed(x, _BF16, at), T, _typed(router_w, _BF16, at),
+            _typed(router_bias, _F32, at), _typed(logits, _F32, at), _stream(stream))
 
 
 def score_desc(score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
                renormalise: bool = True, scale: float = 1.0) -> MoeScoreDesc:
     """How ``moe_route_scored`` chooses (``bias`` must outlive the struct's use)."""
     return MoeScoreDesc(SCORES[score], groups, topk_groups, int(bool(renormalise)), float(scale),
-                        _ptr(bias))
+                        _typed(bias, _F32, "score_desc"))
 
 
 def moe_route_scored(plan: int, logits, T: int, desc: MoeScoreDesc,
@@ -332,7 +364,8 @@ def moe_route_scored(plan: int, logits, T: int, desc: MoeScoreDesc,
     """Routing by scores into the buffers that ``routing`` names; its empty
     fields receive the plan's own."""
     out = MoeRouting() if routing is None else routing
-    _status("moe_route_scored", plan, _ptr(logits), T, ctypes.byref(desc), ctypes.byref(out),
+    at = "moe_route_scored"
+    _status(at, plan, _typed(logits, _F32, at), T, ctypes.byref(desc), ctypes.byref(out),
             _stream(stream))
     return out
 
@@ -362,22 +395,33 @@ def moe_linear_destroy(linear: int) -> None:
 
 def w4(qweight, scales, biases) -> MoeW4:
     """``MoeW4`` of one matrix from its three tensors (which must outlive it)."""
-    return MoeW4(_ptr(qweight), _ptr(scales), _ptr(biases))
+    return MoeW4(_typed(qweight, _WORDS, "w4"), _typed(scales, _BF16, "w4"),
+                 _typed(biases, _BF16, "w4"))
 
 
 def lora(a, b, scale=None) -> MoeLora:
     """``MoeLora`` from tensors a [n, r, K], b [n, N, r] and scale [n]."""
-    return MoeLora(_ptr(a), _ptr(b), _ptr(scale), a.shape[0], a.shape[1])
+    n, r = a.shape[:2]
+    if (a.dim() != 3 or b.dim() != 3 or b.shape[0] != n or b.shape[2] != r or
+            not (a.is_contiguous() and b.is_contiguous()) or
+            (scale is not None and (scale.numel() != n or not scale.is_contiguous()))):
+        raise MoeError(MOE_ERR_INVALID_ARG, "lora (shapes)")
+    return MoeLora(_typed(a, _BF16, "lora"), _typed(b, _BF16, "lora"),
+                   _typed(scale, _F32, "lora"), n, r)
 
 
 def moe_linear_forward(linear: int, x, T: int, weight: MoeW4, y, x_scale=None,
                        lora: Optional[MoeLora] = None, adapter=None, x_stride: int = 0,
                        y_stride: int = 0, stream=None) -> None:
     """4-bit projection with adapters; x is a bf16 or float8_e4m3fn tensor."""
-    x_type = 1 if x.element_size() == 1 else 0
-    _status("moe_linear_forward", linear, _ptr(x), x_type, x_stride, _ptr(x_scale), T,
-            ctypes.byref(weight), None if lora is None else ctypes.byref(lora), _ptr(adapter),
-            _ptr(y), y_stride, _stream(stream))
+    at = "moe_linear_forward"
+    if not _E4M3:
+        _load_types()
+    e4m3 = x.dtype in _E4M3
+    _status(at, linear, x.data_ptr() if e4m3 else _typed(x, _BF16, at), int(e4m3), x_stride,
+            _typed(x_scale, _F32, at), T, ctypes.byref(weight),
+            None if lora is None else ctypes.byref(lora), _typed(adapter, _INT32, at),
+            _typed(y, _BF16, at), y_stride, _stream(stream))
 
 
 def moe_linear_get_error(linear: int) -> int:
