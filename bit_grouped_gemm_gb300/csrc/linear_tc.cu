@@ -39,11 +39,10 @@ constexpr int kOpBytes = 128 * 128;       // 128 rows x 64 16-bit columns
 constexpr uint32_t kTmemCols = 512;
 
 // An adapter stage: h and its rest (A, 128 rows x 16 bf16 each), B's BN / 2
-// rows. Narrow tiles leave shared memory for more of them than the two of a
-// full tile, and need them: a pair has one such tile, whose adapters all come at
-// once.
+// rows. Narrow tiles leave shared memory for four of them, where a full tile has
+// two, and need them: a pair has one such tile, whose adapters all come at once.
 constexpr int kLoraTile = 128 * 32;
-constexpr int kMaxLoraStages = 8;
+constexpr int kMaxLoraStages = 4;
 
 // Shared memory: the ring of operand chunks, the adapter stages, ids and runs and
 // list of the tile's adapters, barriers. A copy takes up to 4,500 cycles to
@@ -672,7 +671,7 @@ cudaError_t launch_linear_tc(const LinearArgs& a, const CUtensorMap& mx, const C
   p.stage_bytes = lin::stage_bytes(bn);
   p.lora_stage_bytes = lin::lora_stage_bytes(bn);
   // two adapter stages at least, four where the tile is narrow
-  p.lora_stages = a.la ? (bn > 128 ? 2 : 4) : 0;   // (even: a group of writers each)
+  p.lora_stages = a.la ? (bn > 128 ? 2 : lin::kMaxLoraStages) : 0;   // (even: a group of writers each)
   const int fixed = (a.la ? lin::kIdsBytes : 0) + lin::kBarBytes + p.lora_stages * p.lora_stage_bytes;
   p.stages = (lin::kSmemMax - fixed) / p.stage_bytes;
   if (p.stages > lin::kMaxStages) p.stages = lin::kMaxStages;

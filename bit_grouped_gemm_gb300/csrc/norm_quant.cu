@@ -27,7 +27,7 @@ struct NqParams {
   float* qs;
   long long x_ld, d_ld, o_ld;
   unsigned T;               // (a step past the last row then does not wrap)
-  int H, d_f32, group;      // group: 0 the row, 128
+  int H, group;             // group: 0 the row, 128
   float eps, alpha;
 };
 
@@ -277,7 +277,6 @@ extern "C" moe_status moe_norm_quant(const moe_norm_desc* d, const uint16_t* x, 
   p.qs = q_scale;
   p.T = (unsigned)T;
   p.H = H;
-  p.d_f32 = d->delta_f32;
   p.group = d->quant_group;
   p.eps = d->eps;
   p.alpha = d->alpha;
