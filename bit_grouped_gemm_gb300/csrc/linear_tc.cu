@@ -22,10 +22,10 @@
 //
 // Every wait is bounded, as in gemm_tc2.cu.
 //
-// Bound by the tensor cores at many tokens: 4096 x 2048 x 4096 43.7 us without
-// adapters (1.57 PFLOP/s, conversion included), 52.4 with 8 of rank 32; the
+// Bound by the tensor cores at many tokens: 4096 x 2048 x 4096 44.1 us without
+// adapters (1.56 PFLOP/s, conversion included), 53.2 with 8 of rank 32; the
 // product alone 47 us cold (77% of the tensor pipe's time). Below 1000 tokens by
-// latency: 128 x 2048 x 2048 13.3 us, of which conversion and product each wait
+// latency: 128 x 2048 x 2048 13.6 us, of which conversion and product each wait
 // for a ring of copies to fill.
 #include "pair.cuh"
 
@@ -625,13 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (300), its operands' copies at 75 bytes per cycle into an SM, and at 8000 out
 // of L2. Of tiles that come out alike the widest is taken: fewer CTAs then read
 // the same lines. Measured for the call at K = 2048 with 8 adapters of rank 16
-// (widths 64, 128, 192, 224, 256): 512 x 2048 15.7, 14.7 (96: 14.4), 16.6, 18.1,
-// 19.5 us; 1024 x 2048 26.2, 17.1 (160: 17.0), 17.7, 19.0, 20.3; 4096 x 2048 69.5,
-// 45.7, 38.7, 39.6, 34.5; 4096 x 4096, e4m3 of rank 32, 130.2, 72.9, 58.1, 52.2,
-// 53.8.
+// (widths 64, 128, 192, 224, 256): 512 x 2048 16.0, 15.2 (96: 14.8), 17.2, 18.6,
+// 20.1 us; 1024 x 2048 26.7, 17.4 (160: 17.4), 18.3, 19.5, 20.9; 4096 x 2048 70.1,
+// 46.0, 39.1, 39.8, 34.8; 4096 x 4096, e4m3 of rank 32, 132.0, 73.6, 58.9, 52.9,
+// 54.4.
 // With few tiles, two pairs of a cluster take half of K each, for the exchange of
-// their sums: 128 x 2048 13.3 against 14.6 us, 200 x 1000 at K = 4096 19.7
-// against 23.6; but 512 x 2048 16.0 against 14.7. (Four pairs: 19.2 against 12.3
+// their sums: 128 x 2048 13.6 against 14.9 us, 200 x 1000 at K = 4096 19.9
+// against 23.8; but 512 x 2048 16.4 against 15.2. (Four pairs: 19.2 against 12.3
 // at 128 x 2048 without adapters; the device holds 15 clusters of 8 such CTAs.)
 static void linear_shape(int T, int N, int K, int num_sms, int* bn_out, int* split_out) {
   const int mt = (T + lin::kTileM - 1) / lin::kTileM, pairs = num_sms / 2, nk = K / 64;

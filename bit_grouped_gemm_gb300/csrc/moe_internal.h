@@ -245,14 +245,19 @@ cudaError_t launch_linear_small(const LinearArgs& a, DevErr err, int num_sms, cu
 // block of 8 columns in perm8 order) and the adapters' h in one launch, then
 // the product on SM pairs. With adapters the rows of x16 and h are places: a
 // block of kOrderBlock tokens in which the adapter changes more than about 32
-// times from one token to the next has them ordered by adapter, other blocks as
-// they come; order[] says which token a place is, in either case. A tile of
-// the product then has few adapters. (4096 tokens of 8 adapters in random order,
-// 2048 x 2048: 42 us a call, 60 with the tokens as they come; rank 64: 54, 92.)
+// times from one token to the next, by the samples below, has them ordered by
+// adapter, other blocks as they come; order[] says which token a place is, in
+// either case. A tile of the product then has few adapters. (4096 tokens of 8
+// adapters in random order, 2048 x 2048: 41 us a call, 57 with the tokens as they
+// come; rank 64: 54, 126.)
 constexpr int kOrderBlock = 2048, kOrderSamples = 128;
 // Both launches look at the same samples of a block of n tokens: token
 // order_sample(i) and the one before, i < kOrderSamples, where it is below n.
-// (All of a block in every CTA costs 2 us: its few lines are hot in L2.)
+// (All of a block in every CTA costs 2 us: its few lines are hot in L2.) Of more
+// than 128 tokens they miss changes at regular places: equal runs whose length
+// divides the step (2, 4, 8 or 16 of a full block's 16) and that start at its
+// multiples never change from a sample's first token to its second, and stay as
+// they come.
 __host__ __device__ inline int order_step(int n) { return (n + kOrderSamples - 1) / kOrderSamples; }
 __host__ __device__ inline int order_sample(int i, int n) { return 1 + i * order_step(n); }
 __host__ __device__ inline bool order_rule(int changes, int n) { return changes * order_step(n) > 32; }

@@ -288,8 +288,11 @@ __global__ void __launch_bounds__(32 * kSmWarps) __maxnreg__(NT == 1 ? 64 : 128)
 // splitting K, took 20 us for 4096 tokens of 2048 and 80 us for 128 tokens of
 // 16 adapters: one chain of L2 round trips per adapter.)
 // The other CTAs rebuild 8192 packed weights each as fp16 in perm8 order.
-// Weights are loaded before the wait for the launch before. Bound by
-// latency and L2: about 8 us of the 52.4 at 4096 x 2048 x 4096.
+// Weights are loaded before the wait for the launch before; x and the adapters'
+// ids, which that launch may write, after it. Bound by latency and L2: about 8 us
+// of the 53.2 at 4096 x 2048 x 4096. (Eight parts of K: 4096 tokens of 14,336 x
+// 4096 with 8 adapters of rank 16 463 us, four parts at K = 13,056, the largest
+// that fits at every rank, 408.)
 // ---------------------------------------------------------------------------
 constexpr int kPrepTok = 32;
 constexpr int kPrepWords = 1024;   // packed words per weight CTA
@@ -403,8 +406,8 @@ __device__ __noinline__ void order_block(const int32_t* adapter, int n_adapters,
 
 // kDeep: twice the loads in flight per thread, for half the CTAs per SM: faster
 // where the launch has at most four CTAs per SM, the shorter weight CTAs counted
-// half (128, 1024, 2048 tokens of 2048 x 2048: 13.6, 17.8, 24.7 us for the call
-// against 14.8, 19.3, 26.0), slower beyond (4096 tokens: 38.9 against 35.2).
+// half (128, 1024, 2048 tokens of 2048 x 2048: 13.6, 17.3, 23.9 us for the call
+// against 14.6, 19.2, 25.9), slower beyond (4096 tokens: 37.1 against 34.8).
 template <int kSplit, bool kDeep, bool kE4m3>   // kSplit: parts of K, CTAs per cluster
 __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(256, kDeep ? 2 : 4)
     linear_prep_kernel(const LinearArgs args, uint16_t* __restrict__ x16, uint16_t* __restrict__ w16, int nx,
@@ -591,11 +594,12 @@ double small_cost(const LinearArgs& a, int num_sms, int* nt_out) {
 
 // Beyond 32 tokens small sizes stay with the decode batches' kernels while
 // conversion and tcgen05 product are estimated to take longer: these measured, at
-// 64 tokens without adapters, 8.3 us at K x N = 1024 x 1024, 10.9 at 2048 x 2048,
-// 13.2 at 4096 x 1024, 12.5 at 2048 x 4096, 17.9 at 4096 x 4096, and 5 to 10 us
-// more with adapters. (48 tokens of rank 16, both ways: 1024 x 1024 5.7 and 15.6
-// us, 2048 x 2048 10.6 and 17.1, 4096 x 1024 12.5 and 24.5, 4096 x 4096 31.9 and
-// 27.4.)
+// 48 and 64 tokens without adapters, 7.4 us at K x N = 1024 x 1024, 10.2 at 2048 x
+// 2048, 13.2 at 4096 x 1024, 12.8 at 2048 x 4096, 17.2 at 4096 x 4096 (the estimate
+// is 0.4 less to 1.2 more), and 6 to 11 us more with adapters. (48 bf16 tokens of
+// rank 16, both ways: 1024 x 1024 4.8 and 15.5 us, 2048 x 2048 10.7 and 17.1, 4096 x
+// 1024 9.6 and 24.1, 2048 x 4096 19.1 and 18.7, 4096 x 4096 31.9 and 28.2; without
+// adapters 3.0 and 7.4, 8.9 and 10.1, 8.1 and 13.2, 16.5 and 12.8, 28.6 and 17.1.)
 bool linear_is_small(const LinearArgs& a, int num_sms) {
   if (a.T <= kLinearSmallT) return true;
   const double k = a.K / 1024.0;

@@ -325,7 +325,8 @@ typedef struct {
  * x bf16, delta bf16 or f32, weight bf16 [H] or NULL; x_out and xn_out bf16,
  * q_out e4m3 bytes, q_scale f32 [T][1 or ceil(H/128)]. Each output may be
  * NULL, but not all; q_out and q_scale come together. x_out may equal x (with
- * the same rows); no other output may overlap an input or another output.
+ * the same rows); no other output may overlap an input or another output, each
+ * taken from its first row to the end of its last, with what a stride leaves out.
  * Pointers 16-byte aligned, strides multiples of 8 and at least H. Needs no
  * plan; runs on the current device. T >= 1. */
 moe_status moe_norm_quant(const moe_norm_desc* desc, const uint16_t* x, const void* delta,
@@ -405,7 +406,8 @@ moe_status moe_linear_scratch_bytes(const moe_linear_desc* desc, size_t* bytes);
  * e4m3 bytes with x_scale f32 [T] (moe_norm_quant's row scales) or NULL (1).
  * x_stride and y_stride: elements between rows, 0 = K and N; x_stride is a
  * multiple of 16, y_stride at least N. x, x_scale and the weights 16-byte
- * aligned, y and adapter 4-byte. y overlaps no input. Rows may come in any
+ * aligned, y and adapter 4-byte. y overlaps no input, each taken from its first
+ * row to the end of its last. Rows may come in any
  * order of adapters; rows of one adapter next to each other are fastest.
  * The sums are FP32; weights are rebuilt as fp16(q * scale + bias) and bf16
  * rows enter as fp16 under the operand contract above, reported by
