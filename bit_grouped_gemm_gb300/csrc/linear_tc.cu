@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;      // [2] leader: accumulator read by 8 warps
   uint64_t* lora_full = acc_empty + 2;     // leader: both CTAs wrote their adapter stage
   uint64_t* lora_empty = lora_full + kMaxLoraStages;   // adapter stage's MMAs done (both CTAs)
-  uint64_t* list_full = lora_empty + kMaxLoraStages;   // [2] the tile's adapter stages are known (own CTA)
+  uint64_t* list_full = lora_empty + kMaxLoraStages;   // [2] leader: the tile's adapter stages are known
   uint64_t* drain = list_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -422,12 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (f1) s_list[r1] = ru1;
         // of the tile's rb x nad stages every split-th is this pair's
         const int nl = (rb * nad - part + split - 1) / split;
-        // the count of two tiles ago has been read once that tile is done (the second
-        // group does not look: with no stage in a tile nothing keeps that barrier
-        // from going on past the phase it would wait for)
-        if (it >= 2 && grp == 0) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
+        // The count of two tiles ago has been read once that tile is done. Only the
+        // leader's first group looks, whose count the issuer waits for: for the
+        // others, with no stage in a tile, nothing keeps that barrier from going on
+        // past the phase they would wait for.
+        const bool counts = leader && grp == 0;
+        if (it >= 2 && counts) ok = warp_wait(&acc_full[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, p.err, 85);
         if (!(ok = bar_and(bar, ok))) break;
-        if (i == 0 && grp == 0) {
+        if (i == 0 && counts) {
           s_steps[it & 1] = nl;
           mbar_arrive(&list_full[it & 1]);
         }
