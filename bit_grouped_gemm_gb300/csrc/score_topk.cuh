@@ -383,6 +383,11 @@ __device__ __noinline__ unsigned fine_groups(const float* row, int gsz, const Sc
       k1 = a > k1 ? a : k1;
       k2 = lo > hi ? lo : hi;
     }
+    // (of a group with one open logit the list has that alone, the next p is 0)
+    if (!s.bias) {
+      k1 = k1 > (1ull << 62) ? k1 : 1ull << 62;
+      k2 = k2 > (1ull << 62) ? k2 : 1ull << 62;
+    }
     // (a group with a closed expert among its two best is -infinity)
     const bool shut = k1 <= 1ull || (gsz > 1 && k2 <= 1ull);
     const long long one = 1ll << 62;
