@@ -29,3 +29,22 @@ def test_groups_with_few_open_experts(E, groups, tg, k, score, mask, biased):
     logits[:40] = one.view(40, E)
     bias = 1e-9 * randn(g, E) if biased else None
     check_route(logits, E, k, bias=bias, score=score, groups=groups, topk_groups=tg)
+
+
+@pytest.mark.parametrize("E,k,groups,tg", [(464, 1, 1, 1), (344, 29, 1, 1), (440, 13, 11, 5), (56, 6, 2, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [LOW, -1e30, -2000.0, float("-inf")])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_chosen_experts_of_no_probability(E, k, groups, tg, score, mask, renorm):
+    """The bias makes a row choose masked experts, whose p is 0: so are the
+    weights, also where all of a row's choice is masked."""
+    g = gen(E)
+    T = 60
+    logits, bias = randn(g, T, E), 0.1 * randn(g, E)
+    shut = torch.arange(E, device="cuda") % 2 == 0
+    bias[shut] += 5.0
+    logits[:, shut] = mask
+    logits[20:40, shut & (torch.arange(E, device="cuda") % 8 == 0)] = 1.0    # some of the favoured are open
+    logits[50:] = mask                                                     # nothing else is open
+    got = check_route(logits, E, k, bias=bias, score=score, groups=groups, topk_groups=tg, renorm=renorm)
+    assert (got["topk_w"][:20] == 0).all()
