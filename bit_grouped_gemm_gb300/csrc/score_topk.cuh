@@ -337,25 +337,24 @@ __device__ __noinline__ int fine_order(const float* row, int k, const ScoreDev s
   const int e = lane < total ? list[lane] : 0;
   const float l = clean_logit(__ldg(row + e)), b = score_bias(s, e);
   const unsigned long long key = lane < total ? fine_score(s.sigmoid, l, b, m, z) : 0ull;
+  // A chosen one is too close to any other that is not the same score by
+  // definition (the neighbour alone would not do: equal scores may stand between).
   int rank = 0;
+  bool close = false;
 #pragma unroll 4
   for (int j = 0; j < total; ++j) {
     const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
+    const float ol = __shfl_sync(0xffffffffu, l, j), ob = __shfl_sync(0xffffffffu, b, j);
     rank += o > key || (o == key && j < lane);
+    const unsigned long long gap = o > key ? o - key : key - o;
+    close |= gap <= (unsigned long long)kFineSure && key > 1ull && !(l == ol && b == ob);
   }
-  // the lane that comes right after this one in the order
   __syncwarp();
   if (lane < total) list[rank] = lane;
   __syncwarp();
-  const int nx = rank + 1 < total ? list[rank + 1] : lane;
   const int mine_lane = lane < total ? list[lane] : 0;
   __syncwarp();
-  const unsigned long long nk = __shfl_sync(0xffffffffu, key, nx);
-  const float nl = __shfl_sync(0xffffffffu, l, nx), nb = __shfl_sync(0xffffffffu, b, nx);
-  // too close, unless the two are the same score by definition
-  const bool bad = lane < total && (key == 0ull || (rank < k && nx != lane && nk > 1ull &&
-                                                    key - nk <= (unsigned long long)kFineSure &&
-                                                    !(l == nl && b == nb)));
+  const bool bad = lane < total && (key == 0ull || (rank < k && close));
   const int mine = __shfl_sync(0xffffffffu, e, mine_lane);
   return __any_sync(0xffffffffu, bad) ? -1 : mine;
 }

@@ -48,3 +48,27 @@ def test_chosen_experts_of_no_probability(E, k, groups, tg, score, mask, renorm)
     logits[50:] = mask                                                     # nothing else is open
     got = check_route(logits, E, k, bias=bias, score=score, groups=groups, topk_groups=tg, renorm=renorm)
     assert (got["topk_w"][:20] == 0).all()
+
+
+@pytest.mark.parametrize("E,k", [(8, 1), (24, 5), (64, 3), (256, 8), (512, 10)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("level", [0.0, 0.25, 1.75])
+def test_equal_scores_before_a_slightly_larger_one(E, k, score, level):
+    """Many masked experts share one score (the bias alone), and one or two others,
+    often behind them in index order, lie above it by less than the second look
+    can tell: those are chosen first."""
+    g = gen(E + k)
+    T = 200
+    logits = torch.full((T, E), float("-inf"), device="cuda")
+    # clear winners for some of the k places, then those barely above
+    top = torch.stack([torch.randperm(E, generator=g, device="cuda")[:k + 1] for _ in range(T)])
+    clear = torch.randint(0, k, (T, 1), generator=g, device="cuda")
+    place = torch.arange(k + 1, device="cuda")
+    faint = -28.0 - 6.0 * torch.rand(T, k + 1, generator=g, device="cuda")
+    vals = torch.where(place < clear, 2.0 + 0.1 * place, torch.where(place <= clear + 1, faint, float("-inf")))
+    logits.scatter_(1, top, vals)
+    if score == "softmax":      # a row's sum of about one, from an expert that the bias keeps out
+        logits[:, 0] = 4.0
+    bias = torch.full((E,), level, device="cuda")
+    bias[0] = -3.0
+    check_route(logits, E, k, bias=bias, score=score)
