@@ -736,14 +736,14 @@ __device__ __forceinline__ void score_select(const float* __restrict__ row, int 
   }
   float pj = 0.f;
   if (s.renorm) {
-    // relative to the largest chosen logit, so that no sum underflows; a
-    // sigmoid far below zero is the exponential. An exponential below -745 (masks
+    // relative to the largest chosen logit, so that no sum underflows; a sigmoid
+    // below -20 is the exponential, to 2e-9. An exponential below -745 (masks
     // of the type's lowest value) is 0 in 64 bits too; under softmax its argument
     // is from the row's maximum, which is among the chosen without bias and groups
     const float best = key_value(__reduce_max_sync(0xffffffffu, order_key(open ? lj : -INFINITY)));
     const float arg = s.sigmoid ? best : s.bias || s.groups > 1 ? best - m : 0.f;
     if (open && best > -INFINITY && arg > -745.f) {
-      if (s.sigmoid) pj = best < -40.f ? expf(lj - best) : 1.0f / (1.0f + expf(-lj));
+      if (s.sigmoid) pj = lj > -20.f ? 1.0f / (1.0f + expf(-lj)) : expf(best > -20.f ? lj : lj - best);
       else if (!isinf(best) && rz > 0.f) pj = expf(lj - best);
     }
     float sum = pj;

@@ -72,3 +72,19 @@ def test_equal_scores_before_a_slightly_larger_one(E, k, score, level):
     bias = torch.full((E,), level, device="cuda")
     bias[0] = -3.0
     check_route(logits, E, k, bias=bias, score=score)
+
+
+@pytest.mark.parametrize("best", [5.0, 0.0, -15.0, -19.9, -20.0, -25.0, -39.0, -41.0, -300.0])
+@pytest.mark.parametrize("down", [3.0, 30.0, 49.5, 60.0])
+def test_renormalised_weights_far_below_the_largest(best, down):
+    """A chosen sigmoid e^-60 of the largest still has its weight, to FP32's
+    roundings (its argument's too), wherever the largest lies."""
+    T, E, k = 40, 64, 6
+    g = gen(3)
+    logits = best - down * torch.rand(T, E, generator=g, device="cuda")
+    logits[:, 5], logits[:, 9] = best, best - down
+    logits[:, 10:] = best - down - 1.0 - torch.rand(T, E - 10, generator=g, device="cuda")
+    bias = torch.zeros(E, device="cuda")
+    bias[[5, 9, 20, 30, 40, 50]] = 2.0
+    got = check_route(logits, E, k, bias=bias, score="sigmoid", renorm=True)
+    assert (got["topk_w"] > 0).all()
