@@ -83,6 +83,39 @@ class MoeLora(ctypes.Structure):
                 ("n", ctypes.c_int), ("rank", ctypes.c_int)]
 
 
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int)]
+
+
+class MoePagePool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("table", "ring", "owned", "owned_out", "ring_pos", "ring_pos_out")]
+
+
+class MoeTokenMap(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("length", "offsets", "slot", "position", "mask", "status")]
+
+
+class MoePageDesc(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("table_width", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("ring_size", ctypes.c_int), ("mask_words", ctypes.c_int)]
+
+
+class MoeAttnDesc(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("cache_type", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("max_requests", ctypes.c_int),
+                ("softmax_scale", ctypes.c_float), ("rotary_dim", ctypes.c_int),
+                ("rope_layout", ctypes.c_int), ("rope_scaling", ctypes.c_int),
+                ("rope_theta", ctypes.c_double), ("rope_factor", ctypes.c_double),
+                ("rope_low", ctypes.c_double), ("rope_high", ctypes.c_double),
+                ("rope_original", ctypes.c_int), ("rope_gain", ctypes.c_float),
+                ("wait_limit_ms", ctypes.c_int)]
+
+
 class MoeTiming(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * len(KERNEL_KINDS)),
                 ("launches", ctypes.c_longlong * len(KERNEL_KINDS))]
@@ -102,6 +135,7 @@ def load_library(path: Optional[str] = None):
                            "`python -m bit_grouped_gemm_gb300.build`")
     lib = ctypes.CDLL(path)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int
+    L = ctypes.c_longlong
     sig = {
         "moe_plan_create": (S, [ctypes.POINTER(MoePlanDesc), I, ctypes.POINTER(P)]),
         "moe_plan_destroy": (S, [P]),
@@ -133,6 +167,16 @@ def load_library(path: Optional[str] = None):
         "moe_linear_forward": (S, [P, P, I, ctypes.c_longlong, P, I, ctypes.POINTER(MoeW4),
                                    ctypes.POINTER(MoeLora), P, P, ctypes.c_longlong, P]),
         "moe_linear_get_error": (S, [P]),
+        "moe_page_map": (S, [ctypes.POINTER(MoePageDesc), P, P, P, ctypes.POINTER(MoePagePool),
+                             ctypes.POINTER(MoeTokenMap), P]),
+        "moe_attn_scratch_bytes": (S, [ctypes.POINTER(MoeAttnDesc),
+                                       ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_attn_create": (S, [ctypes.POINTER(MoeAttnDesc), I, ctypes.POINTER(P)]),
+        "moe_attn_destroy": (S, [P]),
+        "moe_attn_get_error": (S, [P]),
+        "moe_rope_store": (S, [P, P, L, P, L, P, L, I, P, P, P, L, ctypes.POINTER(MoeKvCache), P]),
+        "moe_tree_attention": (S, [P, P, L, I, ctypes.POINTER(MoeKvCache), P, I, I, P, P, P, I, P,
+                                   L, P]),
         "moe_route_noalloc": (S, [P, I, I, P, P, I, I, ctypes.POINTER(MoeRouting), P]),
         "moe_route_noalloc_get_error": (S, []),
         "moe_route_noalloc_debug_wait_timeout": (S, [I, P]),
@@ -302,13 +346,14 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 
 # The tensor types that stand for each of the header's element types (torch's
 # objects, filled in on first use).
-_BF16, _E4M3, _F32, _INT32, _WORDS = set(), set(), set(), set(), set()
+_BF16, _E4M3, _F32, _INT32, _WORDS, _INT64 = set(), set(), set(), set(), set(), set()
 
 
 def _load_types() -> None:
     import torch
     for types, names in ((_BF16, "bfloat16 int16 uint16"), (_E4M3, "float8_e4m3fn uint8"),
-                         (_F32, "float32"), (_INT32, "int32"), (_WORDS, "int32 uint32")):
+                         (_F32, "float32"), (_INT32, "int32"), (_WORDS, "int32 uint32"),
+                         (_INT64, "int64 uint64")):
         types.update(getattr(torch, n) for n in names.split())
 
 
@@ -427,6 +472,119 @@ def moe_linear_forward(linear: int, x, T: int, weight: MoeW4, y, x_scale=None,
 def moe_linear_get_error(linear: int) -> int:
     """Status code of the projection's device error word (read and cleared)."""
     return load_library().moe_linear_get_error(linear)
+
+
+def page_desc(requests: int, page_size: int, table_width: int, max_tokens: int, ring_size: int,
+              mask_words: int = 0) -> MoePageDesc:
+    return MoePageDesc(requests, page_size, table_width, max_tokens, ring_size, mask_words)
+
+
+def page_pool(table, ring, owned, ring_pos, owned_out=None, ring_pos_out=None) -> MoePagePool:
+    """``MoePagePool`` of int32 tensors (which must outlive it); the state is
+    updated in place where no tensor for the new one is given."""
+    at = "page_pool"
+    t = lambda x: _typed(x, _INT32, at)
+    return MoePagePool(t(table), t(ring), t(owned), t(owned if owned_out is None else owned_out),
+                       t(ring_pos), t(ring_pos if ring_pos_out is None else ring_pos_out))
+
+
+def token_map(length, offsets, slot, position, status, mask=None) -> MoeTokenMap:
+    """``MoeTokenMap`` of int32 tensors and an int64 or uint64 mask (which must outlive it)."""
+    at = "token_map"
+    t = lambda x: _typed(x, _INT32, at)
+    return MoeTokenMap(t(length), t(offsets), t(slot), t(position), _typed(mask, _INT64, at),
+                       t(status))
+
+
+def moe_page_map(desc: MoePageDesc, context, added, parent, pool: MoePagePool, out: MoeTokenMap,
+                 stream=None) -> None:
+    """Block tables, slots, positions and masks of a step's tokens (see header)."""
+    at = "moe_page_map"
+    _status(at, ctypes.byref(desc), _typed(context, _INT32, at), _typed(added, _INT32, at),
+            _typed(parent, _INT32, at), ctypes.byref(pool), ctypes.byref(out), _stream(stream))
+
+
+CACHE_TYPES = {"bf16": 0, "e4m3": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+
+
+def attn_desc(heads: int, kv_heads: int, head_dim: int, page_size: int, cache: str = "bf16",
+              max_tokens: int = 4096, max_requests: int = 256, softmax_scale: float = 0.0,
+              rotary_dim: Optional[int] = None, rope_layout: str = "half",
+              rope_scaling: str = "none", rope_theta: float = 10000.0, rope_factor: float = 1.0,
+              rope_low: float = 1.0, rope_high: float = 32.0, rope_original: int = 4096,
+              rope_gain: float = 1.0, wait_limit_ms: int = 0) -> MoeAttnDesc:
+    """``rotary_dim`` None: the whole head turns."""
+    return MoeAttnDesc(heads, kv_heads, head_dim, page_size, CACHE_TYPES[cache], max_tokens,
+                       max_requests, softmax_scale, head_dim if rotary_dim is None else rotary_dim,
+                       ROPE_LAYOUTS[rope_layout], ROPE_SCALINGS[rope_scaling], rope_theta,
+                       rope_factor, rope_low, rope_high, rope_original, rope_gain, wait_limit_ms)
+
+
+def moe_attn_scratch_bytes(desc: MoeAttnDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().moe_attn_scratch_bytes(ctypes.byref(desc), ctypes.byref(out)),
+           "moe_attn_scratch_bytes")
+    return out.value
+
+
+def moe_attn_create(desc: MoeAttnDesc, device: int = 0) -> int:
+    h = ctypes.c_void_p()
+    _check(load_library().moe_attn_create(ctypes.byref(desc), device, ctypes.byref(h)),
+           "moe_attn_create")
+    return h.value
+
+
+def moe_attn_destroy(attn: int) -> None:
+    _check(load_library().moe_attn_destroy(attn), "moe_attn_destroy")
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> MoeKvCache:
+    """``MoeKvCache`` of tensors k and v [pages, kv_heads, page_size, head_dim] and, for e4m3,
+    scales [kv_heads] (which must outlive it)."""
+    at = "kv_cache"
+    if not _E4M3:
+        _load_types()
+    kind = _BF16 if k_scale is None else _E4M3
+    if (k.dim() != 4 or k.shape != v.shape or not (k.is_contiguous() and v.is_contiguous()) or
+            (k_scale is None) != (v_scale is None) or
+            any(s is not None and (s.numel() != k.shape[1] or not s.is_contiguous())
+                for s in (k_scale, v_scale))):
+        raise MoeError(MOE_ERR_INVALID_ARG, at + " (shapes)")
+    return MoeKvCache(_typed(k, kind, at), _typed(v, kind, at), _typed(k_scale, _F32, at),
+                      _typed(v_scale, _F32, at), k.shape[0])
+
+
+def moe_rope_store(attn: int, q, k, v, T: int, position, slot, q_out, cache: MoeKvCache,
+                   q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, out_stride: int = 0,
+                   stream=None) -> None:
+    """Rotary positions of q and k, and the store of k and v into the cache (see header)."""
+    at = "moe_rope_store"
+    _status(at, attn, _typed(q, _BF16, at), q_stride, _typed(k, _BF16, at), k_stride,
+            _typed(v, _BF16, at), v_stride, T, _typed(position, _INT32, at),
+            _typed(slot, _INT32, at), _typed(q_out, _BF16, at), out_stride, ctypes.byref(cache),
+            _stream(stream))
+
+
+def moe_tree_attention(attn: int, q, T: int, cache: MoeKvCache, table, offsets, length, out,
+                       mask=None, q_stride: int = 0, out_stride: int = 0, stream=None) -> None:
+    """Attention over a paged cache (see header); ``table`` is [requests, table_width] and
+    ``mask`` [T, mask_words], both contiguous."""
+    at = "moe_tree_attention"
+    if (table.dim() != 2 or not table.is_contiguous() or
+            (mask is not None and (mask.dim() != 2 or not mask.is_contiguous()))):
+        raise MoeError(MOE_ERR_INVALID_ARG, at + " (shapes)")
+    _status(at, attn, _typed(q, _BF16, at), q_stride, T, ctypes.byref(cache),
+            _typed(table, _INT32, at), table.shape[1], table.shape[0],
+            _typed(offsets, _INT32, at), _typed(length, _INT32, at), _typed(mask, _INT64, at),
+            0 if mask is None else mask.shape[1], _typed(out, _BF16, at), out_stride,
+            _stream(stream))
+
+
+def moe_attn_get_error(attn: int) -> int:
+    """Status code of the handle's device error word (read and cleared)."""
+    return load_library().moe_attn_get_error(attn)
 
 
 def moe_get_error(plan: int) -> int:

@@ -17,7 +17,8 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_w4.so")
 SOURCES = ["route_kernels.cu", "gemm_tc.cu", "gemm_smallm.cu", "moe_w4_api.cu",
            "route_noalloc.cu", "decode_fused.cu", "gemm_tc2.cu", "norm_quant.cu", "route_scored.cu",
-           "w4_linear.cu", "linear_tc.cu", "linear_api.cu"]
+           "w4_linear.cu", "linear_tc.cu", "linear_api.cu", "page_map.cu", "rope_store.cu",
+           "tree_attn.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -428,6 +428,162 @@ moe_status moe_linear_forward(moe_linear_t linear, const void* x, int x_type, lo
 /* As moe_get_error, for a projection. */
 moe_status moe_linear_get_error(moe_linear_t linear);
 
+/* ------------------------------------------- attention over a paged cache ---
+ * Keys and values of all requests lie in pages of one cache,
+ *   k, v [pages][kv_heads][page_size][head_dim],
+ * bf16, or e4m3 with a scale per key-value head (value = code * scale). Slot s
+ * is row s % page_size of page s / page_size. A request's block table lists its
+ * pages in the order of its tokens. */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;    /* f32 [kv_heads], e4m3 only */
+  const float* v_scale;
+  int pages;
+} moe_kv_cache;
+
+/* Pages that requests own, and a ring of free ones. owned_out and ring_pos_out
+ * may be owned and ring_pos themselves (the state is then updated in place) or
+ * buffers that overlap nothing else. */
+typedef struct {
+  int32_t* table;          /* [requests][table_width] pages of each request, updated */
+  int32_t* ring;           /* [ring_size] free pages, updated */
+  const int32_t* owned;    /* [requests] pages of each request */
+  int32_t* owned_out;
+  const int32_t* ring_pos; /* [2]: first free entry of the ring, free pages */
+  int32_t* ring_pos_out;
+} moe_page_pool;
+
+/* What a step's kernels need to know of its tokens. mask may be NULL where
+ * mask_words is 0. */
+typedef struct {
+  int32_t* length;         /* [requests] tokens with this step's; 0: not served */
+  int32_t* offsets;        /* [requests + 1] first row of each request */
+  int32_t* slot;           /* [max_tokens] */
+  int32_t* position;       /* [max_tokens] */
+  uint64_t* mask;          /* [max_tokens][mask_words] */
+  int32_t* status;         /* [5], below */
+} moe_token_map;
+
+typedef struct {
+  int requests;            /* 1..4096 */
+  int page_size;           /* 16, 32, 64, 128 or 256 tokens */
+  int table_width;         /* pages per row of the table, 1..262144 */
+  int max_tokens;          /* rows of the token arrays, 1..2^20 */
+  int ring_size;           /* entries of the ring, 1..2^30 */
+  int mask_words;          /* 64-bit words of a mask row, 0..4 */
+} moe_page_desc;
+
+/* One step of a batch, from lengths that only the device knows: request b holds
+ * context[b] tokens and adds added[b] new ones; added[b] < 0 ends it.
+ *   - Token rows lie request after request: offsets[b] = sum of added before b,
+ *     at most max_tokens.
+ *   - A request that lacks pages takes them from the ring, in the order of the
+ *     requests. It is served if its arguments are sound (context[b] >= 0 and in
+ *     its pages, 0 <= owned[b] <= table_width, length within table_width pages,
+ *     rows within max_tokens, with masks at most 64 * mask_words new tokens) and
+ *     the ring holds its pages and those of all sound requests before it; else
+ *     its length is 0, its pages stay and it takes none.
+ *   - An ended request gives its pages to the ring's end, where all of them
+ *     fit; they can be taken from the next call on. Its length is 0.
+ *   - Row i of a served request has slot (context + i)'s and position context +
+ *     its depth. parent NULL: a chain, depth i. parent [rows]: each new token's
+ *     parent among the request's earlier new tokens (0..i-1) or -1, below the
+ *     context; depth is the number of ancestors. mask: bits of the ancestors and
+ *     the token itself, bit j for new token j.
+ *   - Rows of requests that are not served, and rows behind the last request
+ *     (up to max_tokens), get slot -1, position 0 and an empty mask.
+ *   - status: rows, pages taken, requests refused, pages lacking, and rows whose
+ *     parent is no earlier token (these count as -1).
+ * parent needs mask_words >= 1. All arrays 4-byte aligned, mask 8. No two of
+ * the written arrays overlap, nor a written one and one that is read but for
+ * the pairs named above; table and ring are both. */
+moe_status moe_page_map(const moe_page_desc* desc, const int32_t* context, const int32_t* added,
+                        const int32_t* parent, const moe_page_pool* pool, const moe_token_map* out,
+                        moe_stream_t stream);
+
+typedef enum { MOE_CACHE_BF16 = 0, MOE_CACHE_E4M3 = 1 } moe_cache_type;
+/* Which elements of a head turn together: i and i + rotary_dim / 2, or 2i and
+ * 2i + 1. */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
+/* Frequencies f_i = theta^(-2i / rotary_dim) for long contexts: as they are,
+ * all divided by `factor`, or by parts: with r = original f_i / 2 pi turns within
+ * the original length and g = clamp((r - low) / (high - low), 0, 1),
+ * f_i (g + (1 - g) / factor). */
+typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_BY_PARTS = 2 } moe_rope_scaling;
+
+typedef struct {
+  int heads;               /* query heads, a multiple of kv_heads, at most 128 of them each */
+  int kv_heads;            /* 1..256 */
+  int head_dim;            /* 64, 128 or 256 */
+  int page_size;           /* 16, 32, 64, 128 or 256 */
+  int cache_type;          /* moe_cache_type */
+  int max_tokens;          /* 1..2^20 */
+  int max_requests;        /* 1..4096 */
+  float softmax_scale;     /* 0: 1 / sqrt(head_dim) */
+  int rotary_dim;          /* leading elements of a head that turn: 0..head_dim, a multiple of 16 */
+  int rope_layout;         /* moe_rope_layout */
+  int rope_scaling;        /* moe_rope_scaling */
+  double rope_theta;
+  double rope_factor, rope_low, rope_high;   /* factor >= 1, low < high */
+  int rope_original;
+  float rope_gain;         /* factor of cosine and sine; 0: 1 */
+  int wait_limit_ms;       /* device bounded-wait limit (default 1000 if 0) */
+} moe_attn_desc;
+
+/* The attention of one layer shape: its frequencies, and scratch for sums of
+ * rows that several SMs share. Calls on one handle must be ordered on the
+ * device (two captured graphs that share a handle do not run at once); layers
+ * of one shape may share a handle. Calls work on the handle's device, whatever
+ * the current one; `stream` belongs to it. */
+typedef struct moe_attn* moe_attn_t;
+
+moe_status moe_attn_create(const moe_attn_desc* desc, int device, moe_attn_t* out);
+moe_status moe_attn_destroy(moe_attn_t attn);
+moe_status moe_attn_scratch_bytes(const moe_attn_desc* desc, size_t* bytes);
+
+/* Rotary positions of T rows of queries [heads][head_dim] and keys, and the
+ * store of keys and values [kv_heads][head_dim]:
+ *   (a, b) -> gain (a cos - b sin, b cos + a sin), angle position[t] f_i,
+ * the angle taken modulo a turn exactly for every int32 position. Keys and
+ * values go to slot[t] of the cache, each rounded once (e4m3: the value over its
+ * head's scale, clamped to +-448, a NaN kept); a slot outside the cache stores
+ * nothing. Two rows of one call with the same slot leave a mixture of theirs.
+ * Row strides in elements, 0 = dense; multiples of 8, and q, k, v, q_out 16-byte
+ * aligned (so q, k and v may be parts of one projection's rows). q_out may be q
+ * with the same stride; otherwise it overlaps no input. */
+moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride, const uint16_t* k,
+                          long long k_stride, const uint16_t* v, long long v_stride, int T,
+                          const int32_t* position, const int32_t* slot, uint16_t* q_out,
+                          long long out_stride, const moe_kv_cache* cache, moe_stream_t stream);
+
+/* Attention of new tokens over their requests' keys, the new ones included:
+ * request b has rows offsets[b]..offsets[b+1]-1 (n of them), keys 0..length[b]-1
+ * in the pages table[b], and context c = length[b] - n. Its row i sees key j if
+ *   j < c, or j - c <= i and (mask NULL or bit j - c of the row's mask).
+ *   out[t][h] = softmax(scale q[t][h] K^T over the keys seen) V  (bf16, rounded once)
+ * Key-value head h / (heads / kv_heads) serves query head h. mask: [T][mask_words],
+ * mask_words 1..4; new tokens past 64 * mask_words have no bit and are not seen.
+ * A row that sees no key, and every row of a request with length[b] < n, is zero.
+ * Rows before offsets[0] and from offsets[requests] on are left as they were.
+ * Keys and values that no row sees may hold anything; what a row does not see
+ * does not reach it, an infinity or a NaN neither. Offsets are taken within 0..T
+ * and lengths up to table_width pages; a longer length, and a table entry outside
+ * the cache, sets MOE_ERR_OPERAND_RANGE for moe_attn_get_error (the length is cut,
+ * the page read as zeros). Scores, softmax and sums are FP32, the weights of V
+ * are rounded to bf16. q_stride a multiple of 8, out_stride at least heads *
+ * head_dim and a multiple of 8; q, out and the cache 16-byte aligned. out overlaps
+ * no input. The result of a row does not depend on which other rows are in the
+ * call but for the order of its sums. */
+moe_status moe_tree_attention(moe_attn_t attn, const uint16_t* q, long long q_stride, int T,
+                              const moe_kv_cache* cache, const int32_t* table, int table_width,
+                              int requests, const int32_t* offsets, const int32_t* length,
+                              const uint64_t* mask, int mask_words, uint16_t* out,
+                              long long out_stride, moe_stream_t stream);
+
+/* As moe_get_error, for an attention handle. */
+moe_status moe_attn_get_error(moe_attn_t attn);
+
 /* Reads and clears the plan's device error word. Synchronises the device:
  * call it between layers or steps, never inside one. Returns MOE_OK,
  * MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out; reported first),
