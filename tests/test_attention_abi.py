@@ -125,11 +125,11 @@ def test_binding_checks_types():
             bg.token_map(i, i, bad, i, i)
     with pytest.raises(bg.MoeError):
         bg.token_map(i, i, i, i, i, mask=i)
-    k = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
-    k8, s = k.to(torch.float8_e4m3fn), torch.ones(1)
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    k8, s = k.to(torch.float8_e4m3fn), torch.ones(2)
     bg.kv_cache(k, k.clone())
     bg.kv_cache(k8, k8.clone(), s, s)
-    for args in ((k, k8), (k8, k8), (k, k, s, s), (k8, k8, s), (k8, k8, s, torch.ones(2)), (k[0], k[0]),
+    for args in ((k, k8), (k8, k8), (k, k, s, s), (k8, k8, s), (k8, k8, s, torch.ones(3)), (k[0], k[0]),
                  (k, k[:, :, :8]), (k.transpose(1, 2), k.transpose(1, 2)), (k.float(), k.float())):
         with pytest.raises(bg.MoeError):
             bg.kv_cache(*args)
