@@ -47,7 +47,9 @@ moe_status check_desc(const moe_attn_desc* d) {
   return MOE_OK;
 }
 
-size_t scratch_of(const moe_attn_desc&) { return kErrBytes + kTurnsBytes; }
+size_t scratch_of(const moe_attn_desc& d) {
+  return kErrBytes + kTurnsBytes + attn_scratch_bytes(d.head_dim);
+}
 
 // Turns per position of pair i, as a fraction of 2^64.
 unsigned long long turns_of(const moe_attn_desc& d, int i) {
@@ -302,7 +304,8 @@ moe_status moe_tree_attention(moe_attn_t p, const uint16_t* q, long long q_strid
   a.mask_words = mask_words;
   a.scale = p->d.softmax_scale > 0.0f ? p->d.softmax_scale : 1.0f / sqrtf((float)p->d.head_dim);
   a.cache = dev_of(*cache);
-  return launch_tree_attention(a, p->err(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_tree_attention(a, p->scratch + kErrBytes + kTurnsBytes, p->num_sms, p->err(),
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -40,6 +40,12 @@ cudaError_t allow_smem(const void* kernel, int bytes);
 bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void* base,
                uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
+// Tensor map of any rank: dims in elements from the innermost, strides in bytes
+// of the dimensions above it; 128-byte swizzle (box[0] * elem == 128) or none.
+// Places outside the tensor read as zeros.
+bool encode_nd(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
+               const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzled);
+
 // -------------------------------------------------------------- routing ---
 // Router logits: the tcgen05 path when router_tc_fits (and logits and bias
 // are 16-byte aligned), else the mma.sync paths. weights_early: the small-T

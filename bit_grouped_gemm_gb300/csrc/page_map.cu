@@ -251,7 +251,8 @@ extern "C" moe_status moe_page_map(const moe_page_desc* d, const int32_t* contex
                     {out->slot, 4 * M}, {out->position, 4 * M},
                     {out->status, 20}, {out->mask, 8 * M * d->mask_words},
                     {pool->owned, 4 * B}, {pool->ring_pos, 8},
-                    {context, 4 * B}, {added, 4 * B}, {parent, 4 * M}};
+                    {context, 4 * B}, {added, 4 * B},
+                    {parent, 4}};   // (as many parents as there are rows, which the device knows)
   constexpr int kWritten = 10, kAll = 15;
   for (int i = 0; i < kAll; ++i)
     if (!is_aligned(s[i].p, s[i].p == out->mask ? 8 : 4)) return MOE_ERR_INVALID_ARG;
