@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
   uint64_t* s_full = q_empty + 1;      // [2]
   uint64_t* p_full = s_full + 2;       // [2]
   uint64_t* pv_done = p_full + 2;
-  uint64_t* o_free = pv_done + 1;
+  uint64_t* o_full = pv_done + 1;
+  uint64_t* o_free = o_full + 1;
   uint64_t* drain = o_free + 1;
   Start* start = reinterpret_cast<Start*>(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 1);
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
       mbar_init(&p_full[i], kSoftWarps);
     }
     mbar_init(pv_done, 1);
+    mbar_init(o_full, 1);
     mbar_init(o_free, kSoftWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
               mma_f16_ts(tmem + 64 * c, pc + 8 * (kk & 3) + 64 * (kk >> 2),
                          smem_desc_sw128(slot_addr + i * kSlotBytes + 2048 * kk), kIdO, (t | kk) != 0);
             mma_commit(&empty[i]);
-            if (c == NC - 1) mma_commit(pv_done);
+            if (c == NC - 1) mma_commit(t + 1 < n ? pv_done : o_full);
           }
           __syncwarp();
         }
@@ -550,7 +552,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
     // share complete, and store nothing.
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    uint32_t base = 0, segs = 0, tiles = 0;   // operand chunks, parts and key tiles before this part
+    // operand chunks, parts and key tiles before this part; products that pv_done counts
+    uint32_t base = 0, segs = 0, tiles = 0, pvs = 0;
     AttnShared mine = {};
     while (walk.next(s)) {
       const int n = s.k1 - s.k0, rows = s.tokens * p.G;
@@ -616,7 +619,9 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
           const float old = m;
           if (grow && top > m) m = top;
           if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
-            wait(pv_done, (tiles - 1) & 1, 11);
+            // (the scores of this tile follow the product of the last but one: of pv_done's phases
+            // only the last product's can be open)
+            wait(pv_done, (pvs - 1) & 1, 11);
             tc_fence_after();
             const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
             l *= f;
@@ -671,12 +676,11 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
+        if (t + 1 < n) ++pvs;   // tile t's product
       }
       base += 2 * n * NC;
-      // the part's sums. (A wait tells two phases apart: the last scores say that the product of the
-      // last tile but two is done, so the one after it is waited for too.)
-      if (n > 1) wait(pv_done, tiles & 1, 13);
-      wait(pv_done, (tiles - 1) & 1, 14);
+      // the part's sums
+      wait(o_full, (segs - 1) & 1, 13);
       tc_fence_after();
       if (work) {
         s_max[128 * half + row] = l;

@@ -582,3 +582,12 @@ def test_refusals_with_a_handle():
     finally:
         for a in handle.values():
             bg.moe_attn_destroy(a)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,cache", [(2, 1, 64, "bf16"), (6, 2, 128, "e4m3"), (4, 1, 256, "bf16"), (16, 2, 128, "bf16")])
+def test_attention_many_key_tiles_per_sm(Hq, Hkv, D, cache):
+    """Batches in which every SM goes through many key tiles with few query rows."""
+    B = 160 // Hkv
+    h = torch.Generator().manual_seed(D)
+    lengths = torch.randint(600, 1800, (B,), generator=h).tolist()
+    run_attention(lengths, [1 + b % 3 for b in range(B)], Hq, Hkv, D, 64, cache)
