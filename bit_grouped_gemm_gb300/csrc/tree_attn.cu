@@ -35,33 +35,46 @@
 namespace moe {
 namespace {
 
-constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 bf16
+constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 constexpr int kRawBytes = 128 * 64;         // 128 rows of 64 e4m3
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 2;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512, kColS = 256;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
-constexpr int kMiscBytes = 4096;
+constexpr int kParts = 4;                    // parts told ahead
 
-template <int D, bool E>
+// E: an e4m3 cache. Two: two row tiles at a time.
+template <int D, bool E, bool Two>
 struct Shape {
-  static constexpr int NC = D / 64;
+  static constexpr int NC = D / 64;                  // chunks of 64 columns
+  static constexpr int GC = NC < 2 ? NC : 2;         // chunks that are loaded and waited for together
+  static constexpr int NG = NC / GC;                 // groups of a key tile's keys or values
+  static constexpr int kGroups = E ? 6 / GC : D == 64 ? 10 : 4;
+  static constexpr int kRaw = E ? (D == 64 ? 10 : 7) : 0;
+  static constexpr int QT = Two ? 2 : 1;             // row tiles at a time
+  static constexpr int QB = Two || D == 256 ? 1 : 2; // parts whose queries are held
+  static constexpr int OB = Two || D == 256 ? 1 : 2; // parts whose sums are held
   static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kConvWarp);
-  // operand slots, and (8-bit) slots of codes, in what Q leaves of 227 KB
-  static constexpr int kSlots = E ? (D == 256 ? 5 : 6) : (D == 256 ? 9 : 10);
-  static constexpr int kRaw = E ? (D == 256 ? 8 : 10) : 0;
-  static constexpr int kSmem = 1024 + kMiscBytes + (NC + kSlots) * kSlotBytes + kRaw * kRawBytes;
+  static constexpr int kGroupBytes = GC * kSlotBytes;
+  static constexpr int kQBytes = QT * NC * kSlotBytes;
+  static constexpr int kMisc = 5120 + (E ? kParts * 512 * QT : 0);
+  static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + kGroups * kGroupBytes + kRaw * kRawBytes;
+  static_assert(!Two || D <= 128, "tensor memory holds the sums of two row tiles of 128 columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kSlots > NC, "a tile's values and a chunk beside them");
+  // A group of values that is waited for from outside the products' order: the
+  // group that had its place before is one that a tile's scores have shown to be
+  // consumed (D 256 waits for the last product too).
+  static_assert(kGroups >= 3 * NG || D == 256, "phases told apart");
 };
 
 struct TaParams {
   CUtensorMap mq, mk, mv;
   AttnArgs a;
   AttnShared* shared;
-  float2* ml;          // [cta][2][128] maximum (log2) and sum
-  float* o;            // [cta][2][128][D]
+  float2* ml;          // [cta][2][128 QT] maximum (log2) and sum
+  float* o;            // [cta][2][128 QT][D]
   int G, R;            // query heads per key-value head, tokens per row tile
+  int step;            // tokens of a row tile, or of two
   DevErr err;
 };
 
@@ -84,10 +97,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
       : "memory");
 }
 
-// kind::f16 with bf16 operands, D fp32, A K-major; B K-major or (bit 16) not.
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-         ((128u >> 4) << 24);
+// kind::f16, D fp32, A K-major; operands bf16 or fp16, B K-major or (mn) not.
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int n, bool mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Values as the product's B operand: 16 keys (rows of 128 bytes) of 64 columns
+// per swizzle atom, 8 keys 1024 bytes on, the next 64 columns a slot on.
+__device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
+  uint64_t d = smem_desc_sw128(addr) & ~(0x3fffull << 16);
+  return d | (uint64_t)(kSlotBytes >> 4) << 16;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -96,9 +116,44 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void pair_sync(int quarter) {   // the two warps of a lane quarter
-  __syncwarp();
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+// (a.x b + c, a.y b + c), two lanes of one instruction
+__device__ __forceinline__ float2 fma2(float x, float y, float b, float c) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%5, %5};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x), "f"(y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Waits for the thread's loads from tensor memory, of which x is one: no use of
+// x comes before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                 "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
+                 "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                 "+r"(x[30]), "+r"(x[31])
+               :
+               : "memory");
 }
 
 // --------------------------------------------------------------- the walk ---
@@ -114,17 +169,17 @@ __device__ __forceinline__ Req req_of(const TaParams& p, int lo, int hi, int len
   r.n = max(hi - lo, 0);
   len = min(len, p.a.table_width << p.a.page_shift);
   r.ctx = len >= r.n ? len - r.n : -1;
-  r.tiles = (r.n + p.R - 1) / p.R;
+  r.tiles = (r.n + p.step - 1) / p.step;
   return r;
 }
 
 __device__ __forceinline__ int keys_of(const TaParams& p, const Req& r, int t) {
-  return r.ctx < 0 ? 0 : r.ctx + min(r.n, (t + 1) * p.R);
+  return r.ctx < 0 ? 0 : r.ctx + min(r.n, (t + 1) * p.step);
 }
 // cost of a request's first t row tiles under one head (all but the last are full)
 __device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r, int t) {
   long long c = (long long)t * (kItemCost + max(r.ctx, 0));
-  if (r.ctx >= 0) c += (long long)p.R * t * (t + 1) / 2;
+  if (r.ctx >= 0) c += (long long)p.step * t * (t + 1) / 2;
   return c;
 }
 __device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
@@ -135,47 +190,69 @@ __device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
 struct Start {
   long long at, share;   // cost before the CTA's first row tile; a CTA's cost
   int b, h, t;
+  Req r;
 };
 
-// A CTA's part of a row tile: key tiles [k0, k1) of nk.
-struct Seg {
+// A CTA's part of a row tile (or of two): key tiles [k0, k1) of nk.
+struct Part {
   int b, h, row, tok0, tokens, ctx, keys, k0, k1, nk;
-  long long at;    // the row tile's cost begins here
+  int place;       // of the sums in scratch, if others hold parts of the tile
+  int stop;        // the end of the CTA's parts
 };
 
-// All roles walk the same parts.
+// The CTA's parts, in order.
 struct Walk {
   const TaParams& p;
   long long c0, c1, at;
   int b, h, t;
   Req r;
-  int next_hi, next_len;
+  int lo, hi, len;     // of request b + 1, read ahead
+  AttnShared mine;     // the row tile that this CTA begins and others go on with
 
-  __device__ __forceinline__ void load() {
-    r = req_of(p, __ldg(p.a.offsets + b), __ldg(p.a.offsets + b + 1), __ldg(p.a.length + b));
+  __device__ __forceinline__ void ahead() {
+    if (b + 1 < p.a.requests) {
+      lo = __ldg(p.a.offsets + b + 1);
+      hi = __ldg(p.a.offsets + b + 2);
+      len = __ldg(p.a.length + b + 1);
+    }
   }
   __device__ __forceinline__ Walk(const TaParams& p_, const Start& s)
-      : p(p_), c0((long long)blockIdx.x * s.share), c1(c0 + s.share), at(s.at), b(s.b), h(s.h), t(s.t) {
-    if (b < p.a.requests) load();
+      : p(p_), c0((long long)blockIdx.x * s.share), c1(c0 + s.share), at(s.at), b(s.b), h(s.h), t(s.t), r(s.r),
+        mine{} {
+    ahead();
   }
-  // The next part of the CTA that has work (key tiles, or a row tile without
-  // keys that begins here); false at the end.
-  __device__ __forceinline__ bool next(Seg& s) {
+  // The next part that has work: key tiles, or a row tile without keys that
+  // begins here.
+  __device__ __forceinline__ bool next(Part& s) {
     while (b < p.a.requests && at < c1) {
       const int keys = keys_of(p, r, t), nk = (keys + 127) >> 7;
-      const long long cost = kItemCost + keys;
+      const long long cost = kItemCost + keys, share = c1 - c0;
+      const bool begins = at >= c0;
       s.b = b;
       s.h = h;
       s.row = r.row;
-      s.tok0 = t * p.R;
-      s.tokens = min(p.R, r.n - s.tok0);
+      s.tok0 = t * p.step;
+      s.tokens = min(p.step, r.n - s.tok0);
       s.ctx = r.ctx;
       s.keys = keys;
       s.nk = nk;
-      s.at = at;
       s.k0 = border(c0 - at, cost, nk);
       s.k1 = border(c1 - at, cost, nk);
-      const bool begins = at >= c0;
+      s.place = 2 * blockIdx.x + (begins ? 1 : 0);
+      s.stop = 0;
+      if (begins && at + cost > c1) {
+        // others go on: which hold a part
+        int first = blockIdx.x, last = (int)((at + cost - 1) / share);
+        if (s.k1 == 0) ++first;
+        if (border(last * share - at, cost, nk) == nk) --last;
+        if (nk && last > first) {
+          mine.row = s.row + s.tok0;
+          mine.tokens = s.tokens;
+          mine.head = h;
+          mine.first = first;
+          mine.count = last - first + 1;
+        }
+      }
       at += cost;
       if (++t == r.tiles) {
         t = 0;
@@ -183,11 +260,12 @@ struct Walk {
           h = 0;
           do {
             if (++b >= p.a.requests) break;
-            load();
+            r = req_of(p, lo, hi, len);
+            ahead();
           } while (r.n == 0);
         }
       }
-      if (s.k0 < s.k1 || (nk == 0 && begins) || (begins && s.at + cost > c1)) return true;
+      if (s.k0 < s.k1 || (nk == 0 && begins)) return true;
     }
     return false;
   }
@@ -247,17 +325,12 @@ __device__ __forceinline__ void find_start(const TaParams& p, Start* out, long l
         out->b = b;
         out->h = h;
         out->t = lo;
+        out->r = r;
         break;
       }
       before += p.a.kv_heads * head;
     }
   }
-}
-
-// Place in the operand ring, from a part's first chunk on, of the values of its
-// key tile i of n. Scores run one tile ahead: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ uint32_t value_chunk(int i, int n, int nc) {
-  return nc * (i + 1 < n ? 2 * i + 2 : 2 * n - 1);
 }
 
 // Bits of the keys that a row sees among the 64 from node index `a` (key minus
@@ -277,13 +350,16 @@ __device__ __forceinline__ unsigned long long seen_bits(int a, int i, const unsi
   return v;
 }
 
-// Sets the elements of 8 bf16 that are no finite numbers to zero; true if any.
+// Sets the elements of 8 bf16 (or fp16) that are no finite numbers to zero; true
+// if there are any.
+template <bool F16>
 __device__ __forceinline__ bool clear_unbounded(uint4& x) {
+  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
   uint32_t* w = reinterpret_cast<uint32_t*>(&x);
   bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
+    const bool lo = (w[i] & kExp) == kExp, hi = (w[i] & kExp << 16) == kExp << 16;
     if (lo) w[i] &= 0xffff0000u;
     if (hi) w[i] &= 0x0000ffffu;
     any |= lo || hi;
@@ -291,77 +367,93 @@ __device__ __forceinline__ bool clear_unbounded(uint4& x) {
   return any;
 }
 
-template <bool E>
-__device__ __forceinline__ float cache_value(const void* base, long long i) {
-  if constexpr (E) {
-    const uint16_t c = static_cast<const uint8_t*>(base)[i];
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-    return f16_lo(h);
-  } else {
-    return bf16_to_f32(static_cast<const uint16_t*>(base)[i]);
-  }
+// Two e4m3 as fp16, exactly; a NaN stays one.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return h;
 }
 
-// Two e4m3 (low half) as bf16x2, exactly; a NaN stays one.
-__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return pack_bf16x2(f16_lo(h), f16_hi(h));
+template <bool E>
+__device__ __forceinline__ float cache_value(const void* base, long long i) {
+  if constexpr (E)
+    return f16_lo(e4m3x2_f16x2(static_cast<const uint8_t*>(base)[i]));
+  else
+    return bf16_to_f32(static_cast<const uint16_t*>(base)[i]);
 }
 
 // ----------------------------------------------------------------- kernel ---
-template <int D, bool E>
-__global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(const __grid_constant__ TaParams p) {
-  using Sh = Shape<D, E>;
-  constexpr int NC = Sh::NC, kSlots = Sh::kSlots, kRaw = Sh::kRaw;
+template <int D, bool E, bool Two>
+__global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TaParams p) {
+  using Sh = Shape<D, E, Two>;
+  constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, kGroups = Sh::kGroups, kRaw = Sh::kRaw, QB = Sh::QB,
+                OB = Sh::OB, QT = Sh::QT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
-  uint8_t* slots = sq + NC * kSlotBytes;
-  uint8_t* raws = slots + kSlots * kSlotBytes;
+  uint8_t* groups = sq + QB * Sh::kQBytes;
+  uint8_t* raws = groups + kGroups * Sh::kGroupBytes;
   uint8_t* misc = raws + kRaw * kRawBytes;
-  float* s_max = reinterpret_cast<float*>(misc);                   // [2][2][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(misc + 2048);
-  uint64_t* empty = full + kSlots;
-  uint64_t* raw_full = empty + kSlots;
+  float* s_max = reinterpret_cast<float*>(misc);   // [2][2][128], then sums [2][128]
+  float* s_sum = s_max + 512;
+  float* s_qs = s_sum + 256;                       // [kParts][128 QT] factors of fp16 queries
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 * QT : 0));
+  uint64_t* empty = full + kGroups;
+  uint64_t* raw_full = empty + kGroups;
   uint64_t* raw_empty = raw_full + kRaw;
-  uint64_t* q_full = raw_empty + kRaw;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;      // [2]
-  uint64_t* p_full = s_full + 2;       // [2]
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* o_full = pv_done + 1;
-  uint64_t* o_free = o_full + 1;
-  uint64_t* drain = o_free + 1;
-  Start* start = reinterpret_cast<Start*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 1);
+  uint64_t* q_raw = raw_empty + kRaw;    // [QB] queries landed (e4m3)
+  uint64_t* q_full = q_raw + QB;         // [QB] queries ready
+  uint64_t* q_empty = q_full + QB;
+  uint64_t* s_full = q_empty + QB;       // [2] by key tile; Two: by row tile, as the next three
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;         // [OB]
+  uint64_t* o_free = o_full + 2;
+  uint64_t* pv_done = o_free + 2;
+  uint64_t* pair = pv_done + 1;          // [4]
+  uint64_t* part_full = pair + 4;        // [kParts]
+  uint64_t* part_empty = part_full + kParts;
+  uint64_t* drain = part_empty + kParts;
+  Part* parts = reinterpret_cast<Part*>(drain + 1);
+  Start* start = reinterpret_cast<Start*>(parts + kParts);
+  long long(*scan)[Sh::kThreads / 32] = reinterpret_cast<long long(*)[Sh::kThreads / 32]>(start + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(*scan + Sh::kThreads / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_unbounded = abort_flag + 1;
-  long long(*part)[Sh::kThreads / 32] = reinterpret_cast<long long(*)[Sh::kThreads / 32]>(misc + 2048 + 1024);
+  volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
+  static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 +
+                    8 * (2 * kGroups + 2 * kRaw + 3 * QB + 14 + 2 * kParts) + kParts * sizeof(Part) +
+                    sizeof(Start) + Sh::kThreads / 4 + 64 <= Sh::kMisc, "room for barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], E ? kConvWarps : 1);
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&full[i], E ? kConvWarps * GC : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kConvWarps);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < QB; ++i) {
+      mbar_init(&q_raw[i], 1);
+      mbar_init(&q_full[i], E ? kConvWarps : 1);
+      mbar_init(&q_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&p_full[i], Two ? kSoftWarps / 2 : kSoftWarps);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], Two ? kSoftWarps / 2 : kSoftWarps);
     }
     mbar_init(pv_done, 1);
-    mbar_init(o_full, 1);
-    mbar_init(o_free, kSoftWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&part_full[i], 1);
+      mbar_init(&part_empty[i], kSoftWarps);
+      s_unbounded[i] = 0;
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *s_unbounded = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.mq);
     tma_prefetch_desc(&p.mk);
@@ -373,11 +465,12 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
     tc_fence_before();
   }
   pdl_begin();
-  find_start<Sh::kThreads>(p, start, *part, blockIdx.x == 0);
+  find_start<Sh::kThreads>(p, start, *scan, blockIdx.x == 0);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // waits of a whole warp; after a wait that failed all others return at once
+  // A wait of a whole warp. After one that ran out every other wait fails at
+  // once, and each role leaves its loop.
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
     bool ok = mbar_try_wait(bar, parity) ||
               (!*abort_flag && mbar_wait(bar, parity, abort_flag, p.err.limit_ns));
@@ -388,324 +481,411 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
     }
     return ok;
   };
+  // Order of the loads and products. One row tile: the scores run one key tile
+  // ahead, K0 K1 V0 K2 V1 .., through the ends of parts, too, where the next
+  // part's queries have a place of their own (QB 2; at the very end a group's
+  // places are left out, so that V of tile u is always group NG (2u + 2)); else
+  // the part's last V comes before the next part's K0. Two row tiles: K0 V0 K1 V1.
 
-  Walk walk(p, *start);
-  Seg s;
   if (warp == kLoadWarp) {
     // ---------------------------------------------------- loads, by TMA
-    constexpr int kRing = E ? kRaw : kSlots, kBytes = E ? kRawBytes : kSlotBytes, kRow = E ? 64 : 128;
-    uint8_t* ring = E ? raws : slots;
-    uint64_t *rf = E ? raw_full : full, *re = E ? raw_empty : empty;
+    Walk walk(p, *start);
     const int page = 1 << p.a.page_shift, box = min(page, 128), nbox = 128 / box;
-    uint32_t cnt = 0, segs = 0;
+    const int my_box = box * (lane & (nbox - 1)), my_chunk = lane / nbox;   // (chunk of a group)
+    uint32_t cnt = 0, np = 0, segs = 0;    // groups (e4m3: chunks) loaded, parts told, parts loaded
     bool ok = true, bad = false;
+    Part s;
+    auto load = [&](const CUtensorMap* m, int h, int k, int id) {
+      const int y = (128 * k + my_box) & (page - 1);
+      if constexpr (E) {
+        for (int c = 0; c < NC && ok; ++c, ++cnt) {
+          const int i = cnt % kRaw;
+          if (!(ok = wait(&raw_empty[i], ((cnt / kRaw) & 1) ^ 1, 2))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[i], kRawBytes);
+          __syncwarp();
+          if (lane < nbox) tma_load_4d(raws + i * kRawBytes + my_box * 64, m, 64 * c, y, h, id, &raw_full[i]);
+        }
+      } else {
+        for (int g = 0; g < NG && ok; ++g, ++cnt) {
+          const int i = cnt % kGroups;
+          if (!(ok = wait(&empty[i], ((cnt / kGroups) & 1) ^ 1, 2))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[i], Sh::kGroupBytes);
+          __syncwarp();
+          if (my_chunk < GC)
+            tma_load_4d(groups + i * Sh::kGroupBytes + my_chunk * kSlotBytes + my_box * 128, m,
+                        64 * (g * GC + my_chunk), y, h, id, &full[i]);
+        }
+      }
+    };
+    auto tell = [&]() {   // a part to the other roles
+      if (!(ok = wait(&part_empty[np % kParts], ((np / kParts) & 1) ^ 1, 3))) return;
+      if (lane == 0) parts[np % kParts] = s;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_full[np % kParts]);
+      ++np;
+    };
+    bool have = false;      // values not loaded yet: key tile vk of head vh, pages vid
+    int vh = 0, vk = 0, vid = 0;
     while (ok && walk.next(s)) {
-      if (s.k0 >= s.k1) continue;
-      if (!(ok = wait(q_empty, (segs & 1) ^ 1, 1))) break;
+      if (s.nk == 0) {   // no keys: zeros
+        const int per_row = D / 8, n = s.tokens * p.G * per_row;
+        for (int i = lane; i < n; i += 32) {
+          const int r = i / per_row, tok = s.row + s.tok0 + r / p.G, head = s.h * p.G + r % p.G;
+          *reinterpret_cast<uint4*>(p.a.out + (long long)tok * p.a.o_ld + (long long)head * D + 8 * (i % per_row)) =
+              make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      tell();
+      if (!ok) break;
+      const int len_pages = (s.keys + page - 1) >> p.a.page_shift;
+      const int32_t* table = p.a.table + (long long)s.b * p.a.table_width;
+      // this lane's box of key tile k: its page's number; one past the cache (which reads as zeros) behind
+      // the keys, and for numbers outside
+      auto inside = [&](int k) { return k < s.k1 && ((128 * k + my_box) >> p.a.page_shift) < len_pages; };
+      auto entry = [&](int k) { return inside(k) ? __ldg(table + ((128 * k + my_box) >> p.a.page_shift)) : -1; };
+      int id0 = entry(s.k0), id1 = entry(s.k0 + 1);
+      if (QB == 1 && have) {
+        load(&p.mv, vh, vk, vid);
+        have = false;
+        if (!ok) break;
+      }
+      const int qb = segs % QB;
+      if (!(ok = wait(&q_empty[qb], ((segs / QB) & 1) ^ 1, 1))) break;
       if (elect_one_sync()) {
-        mbar_arrive_expect_tx(q_full, NC * 128 * p.G * p.R);
-        for (int c = 0; c < NC; ++c)
-          tma_load_3d(sq + c * kSlotBytes, &p.mq, 64 * c, s.h * p.G, s.row + s.tok0, q_full);
+        uint64_t* bar = E ? &q_raw[qb] : &q_full[qb];
+        mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
+        for (int q = 0; q < QT; ++q)
+          for (int c = 0; c < NC; ++c)
+            tma_load_3d(sq + qb * Sh::kQBytes + (q * NC + c) * kSlotBytes, &p.mq, 64 * c, s.h * p.G,
+                        s.row + s.tok0 + q * p.R, bar);
       }
       __syncwarp();
       ++segs;
-      const int len_pages = (s.keys + page - 1) >> p.a.page_shift;
-      const int32_t* table = p.a.table + (long long)s.b * p.a.table_width;
-      // this lane's box of key tile k: its page, or one past the cache (zeros)
-      auto page_of = [&](int k) {
-        const int i = (128 * k + lane * box) >> p.a.page_shift;
-        if (lane >= nbox || k >= s.k1 || i >= len_pages) return p.a.cache.pages;
-        const int id = __ldg(table + i);
-        if (id >= 0 && id < p.a.cache.pages) return id;
-        bad = true;
-        return p.a.cache.pages;
-      };
-      auto load = [&](const CUtensorMap* m, int k, int id) {
-        for (int c = 0; c < NC && ok; ++c, ++cnt) {
-          const int i = cnt % kRing;
-          if (!(ok = wait(&re[i], ((cnt / kRing) & 1) ^ 1, 2))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&rf[i], kBytes);
-          __syncwarp();
-          if (lane < nbox)
-            tma_load_4d(ring + i * kBytes + lane * box * kRow, m, 64 * c, (128 * k + lane * box) & (page - 1),
-                        s.h, id, &rf[i]);
-        }
-      };
-      int id = page_of(s.k0), ahead = page_of(s.k0 + 1);
-      load(&p.mk, s.k0, id);
       for (int k = s.k0; k < s.k1 && ok; ++k) {
-        const int later = page_of(k + 2);
-        if (k + 1 < s.k1) load(&p.mk, k + 1, ahead);
-        if (ok) load(&p.mv, k, id);
-        id = ahead;
-        ahead = later;
+        const int id2 = entry(k + 2);
+        int id = p.a.cache.pages;
+        if (inside(k)) {
+          if (id0 >= 0 && id0 < p.a.cache.pages) id = id0; else bad = true;
+        }
+        load(&p.mk, s.h, k, id);
+        if (Two) {
+          if (ok) load(&p.mv, s.h, k, id);
+        } else {
+          if (have && ok) load(&p.mv, vh, vk, vid);
+          have = true;
+          vh = s.h;
+          vk = k;
+          vid = id;
+        }
+        id0 = id1;
+        id1 = id2;
+      }
+    }
+    if (ok) {
+      s.stop = 1;
+      tell();
+      if (have && ok) {
+        if (QB == 2) cnt += E ? 0 : NG;
+        load(&p.mv, vh, vk, vid);
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
+    if (lane == 0) {
+      if (*abort_flag) walk.mine.count = 0;
+      p.shared[blockIdx.x] = walk.mine;
+    }
     if (!ok) {   // own copies land before shared memory is released
+      constexpr int kRing = E ? kRaw : kGroups;
       for (int i = 0; i < kRing; ++i) {
         const uint32_t uses = (cnt + kRing - 1 - i) / kRing;
-        if (uses) mbar_wait_drain(&rf[i], (uses - 1) & 1, p.err.limit_ns);
+        if (uses) mbar_wait_drain(E ? &raw_full[i] : &full[i], (uses - 1) & 1, p.err.limit_ns);
       }
-      if (segs) mbar_wait_drain(q_full, (segs - 1) & 1, p.err.limit_ns);
+      for (int i = 0; i < QB; ++i) {
+        const uint32_t uses = (segs + QB - 1 - i) / QB;
+        if (uses) mbar_wait_drain(E ? &q_raw[i] : &q_full[i], (uses - 1) & 1, p.err.limit_ns);
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- products
-    uint32_t cnt = 0, segs = 0, tiles = 0;
+    constexpr uint32_t kIdS = idesc_16(!E, 128, false), kIdO = idesc_16(!E, 64 * GC, true);
+    const uint32_t q_addr = smem_u32(sq), g_addr = smem_u32(groups);
+    uint32_t cnt = 0, segs = 0, u = 0;
     bool ok = true;
-    constexpr uint32_t kIdS = idesc_bf16(128, false), kIdO = idesc_bf16(64, true);
-    const uint32_t q_addr = smem_u32(sq), slot_addr = smem_u32(slots);
-    auto scores = [&](uint32_t n) {   // S[n & 1] = Q K^T
-      for (int c = 0; c < NC && ok; ++c, ++cnt) {
-        const int i = cnt % kSlots;
-        if (!(ok = wait(&full[i], (cnt / kSlots) & 1, 3))) break;
+    // scores of key tile in the groups from cnt on, row tile at `q`, into S buffer `buf`
+    auto scores = [&](uint32_t q, int buf, bool wait_keys, bool free_keys) {
+      for (int g = 0; g < NG && ok; ++g) {
+        const int i = (cnt + g) % kGroups;
+        if (wait_keys && !(ok = wait(&full[i], ((cnt + g) / kGroups) & 1, 4))) break;
         tc_fence_after();
         if (elect_one_sync()) {
+          const uint64_t qd = smem_desc_sw128(q + g * Sh::kGroupBytes);
+          const uint64_t kd = smem_desc_sw128(g_addr + i * Sh::kGroupBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss(tmem + kColS + 128 * (n & 1), smem_desc_sw128(q_addr + c * kSlotBytes + 32 * kk),
-                       smem_desc_sw128(slot_addr + i * kSlotBytes + 32 * kk), kIdS, (c | kk) != 0);
-          mma_commit(&empty[i]);
-          if (c == NC - 1) mma_commit(&s_full[n & 1]);
+          for (int c = 0; c < GC; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss(tmem + kColS + 128 * buf, qd + (c * kSlotBytes + 32 * kk) / 16,
+                         kd + (c * kSlotBytes + 32 * kk) / 16, kIdS, (g | c | kk) != 0);
+          if (free_keys) mma_commit(&empty[i]);
+          if (g == NG - 1) mma_commit(&s_full[buf]);
         }
         __syncwarp();
       }
     };
-    while (ok && walk.next(s)) {
-      const int n = s.k1 - s.k0;
-      if (n <= 0) continue;
-      if (!(ok = wait(q_full, segs & 1, 4))) break;
-      tc_fence_after();
-      scores(tiles);
-      for (int t = 0; t < n && ok; ++t, ++tiles) {
-        if (t + 1 < n) scores(tiles + 1);
-        if (!ok) break;
-        if (t == max(n - 2, 0)) {   // Q is free once the last scores' products are done
-          if (elect_one_sync()) mma_commit(q_empty);
-          __syncwarp();
-        }
-        if (!(ok = wait(&p_full[tiles & 1], (tiles >> 1) & 1, 5))) break;
-        if (t == 0 && !(ok = wait(o_free, (segs & 1) ^ 1, 6))) break;
+    // O (+)= P V with the values in the groups from cnt on
+    auto values = [&](uint32_t o, int buf, bool first, uint64_t* done, bool wait_values, bool free_values) {
+      for (int g = 0; g < NG && ok; ++g) {
+        const int i = (cnt + g) % kGroups;
+        if (wait_values && !(ok = wait(&full[i], ((cnt + g) / kGroups) & 1, 5))) break;
         tc_fence_after();
-        const uint32_t pc = tmem + kColS + 128 * (tiles & 1);
-        for (int c = 0; c < NC && ok; ++c, ++cnt) {
-          const int i = cnt % kSlots;
-          if (!(ok = wait(&full[i], (cnt / kSlots) & 1, 7))) break;
-          tc_fence_after();
-          if (elect_one_sync()) {
+        if (elect_one_sync()) {
+          const uint64_t vd = value_desc(g_addr + i * Sh::kGroupBytes);
+          const uint32_t pc = tmem + kColS + 128 * buf;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)   // 16 keys each; weights of keys 64.. lie 64 columns on
-              mma_f16_ts(tmem + 64 * c, pc + 8 * (kk & 3) + 64 * (kk >> 2),
-                         smem_desc_sw128(slot_addr + i * kSlotBytes + 2048 * kk), kIdO, (t | kk) != 0);
-            mma_commit(&empty[i]);
-            if (c == NC - 1) mma_commit(t + 1 < n ? pv_done : o_full);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
+            mma_f16_ts(o + 64 * GC * g, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)),
+                       vd + (2048 >> 4) * kk, kIdO, !first || kk);
+          if (free_values) mma_commit(&empty[i]);
+          if (g == NG - 1 && done) mma_commit(done);
         }
+        __syncwarp();
       }
-      ++segs;
+    };
+    if constexpr (Two) {
+      for (uint32_t np = 0; ok; ++np) {
+        if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
+        const Part& s = parts[np % kParts];
+        if (s.stop) break;
+        const int n = s.k1 - s.k0;
+        if (!(ok = wait(q_full, segs & 1, 7))) break;
+        scores(q_addr, 0, true, false);
+        if (ok) scores(q_addr + NC * kSlotBytes, 1, false, true);
+        for (int t = 0; t < n && ok; ++t, ++u) {
+          // (groups: K(t) at cnt, V(t), K(t + 1))
+          for (int q = 0; q < 2 && ok; ++q) {
+            if (!(ok = wait(&p_full[q], u & 1, 8))) break;
+            if (t == 0 && !(ok = wait(&o_free[q], (segs & 1) ^ 1, 9))) break;
+            cnt += NG;
+            values(tmem + 128 * q, q, t == 0, t + 1 == n ? &o_full[q] : nullptr, q == 0, q == 1);
+            cnt += NG;
+            if (t + 1 < n && ok) scores(q_addr + q * NC * kSlotBytes, q, q == 0, q == 1);
+            cnt -= 2 * NG;
+          }
+          cnt += 2 * NG;
+          if (t + 2 == n || n == 1) {
+            if (elect_one_sync()) mma_commit(q_empty);
+            __syncwarp();
+          }
+        }
+        ++segs;
+      }
+    } else {
+      bool have = false, first = false;    // key tile u - 1's values are to be added
+      int vob = 0;
+      auto add_values = [&](bool last) {
+        const uint32_t v = u - 1;
+        if (!(ok = wait(&p_full[v & 1], (v >> 1) & 1, 8))) return;
+        const int ob = vob % OB;
+        if (first && !(ok = wait(&o_free[ob], ((vob / OB) & 1) ^ 1, 9))) return;
+        values(tmem + 128 * ob, v & 1, first, last ? &o_full[ob] : pv_done, true, true);
+        cnt += NG;
+        have = false;
+      };
+      for (uint32_t np = 0; ok; ++np) {
+        if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
+        const Part& s = parts[np % kParts];
+        if (s.stop) break;
+        const int n = s.k1 - s.k0, qb = segs % QB;
+        if (QB == 1 && have) add_values(true);
+        if (!ok || !(ok = wait(&q_full[qb], (segs / QB) & 1, 7))) break;
+        for (int t = 0; t < n && ok; ++t) {
+          scores(q_addr + qb * Sh::kQBytes, u & 1, true, true);
+          cnt += NG;
+          if (t + 1 == n) {
+            if (elect_one_sync()) mma_commit(&q_empty[qb]);
+            __syncwarp();
+          }
+          if (have && ok) add_values(t == 0);
+          have = true;
+          first = t == 0;
+          vob = segs;
+          ++u;
+        }
+        ++segs;
+      }
+      if (have && ok) {
+        if (QB == 2) cnt += NG;
+        add_values(true);
+      }
     }
     if (elect_one_sync()) mma_commit(drain);
     __syncwarp();
     mbar_wait_drain(drain, 0, p.err.limit_ns);
   } else if (E && warp >= kConvWarp) {
-    // --------------------------------------------- e4m3 chunks to bf16
-    const int w = warp - kConvWarp;
-    uint32_t cnt = 0;
+    // ------------------- e4m3 chunks to fp16, exactly; queries to fp16, each
+    // row times the power of two that brings its largest element to 2^14..2^15
+    // (elements below 2^-31 of that one lose bits), which its scores undo
+    const int w = warp - kConvWarp, tid = 32 * w + lane;
+    uint32_t raw = 0, grp = 0, segs = 0, u = 0;
+    int vk = 0, vseen = 0, vkeys = 0;      // the key tile whose values come next, and of which part
+    uint32_t vpart = 0;
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const int chunks = 2 * NC * max(s.k1 - s.k0, 0);
-      for (int c = 0; c < chunks && ok; ++c, ++cnt) {
-        const int ri = cnt % max(kRaw, 1), si = cnt % kSlots;
-        if (!(ok = wait(&raw_full[ri], (cnt / max(kRaw, 1)) & 1, 8))) break;
+    // one key tile's keys or values; of values of a tile that not every row sees
+    // whole, what some row must not see is cleared: keys past the row tile's own,
+    // and what is no number (row r of the tile is key first + r)
+    auto convert = [&](bool clear, int first, int seen, int keys, uint32_t part) {
+      bool any = false;
+      for (int c = 0; c < NC && ok; ++c, ++raw) {
+        const int ri = raw % max(kRaw, 1), gi = grp % kGroups;
+        if (!(ok = wait(&raw_full[ri], (raw / max(kRaw, 1)) & 1, 10))) break;
         const uint8_t* src = raws + ri * kRawBytes;
-        uint4 x[4];
+        uint4 x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 16 * (32 * (4 * w + i) + lane));
-        if (!(ok = wait(&empty[si], ((cnt / kSlots) & 1) ^ 1, 9))) break;
-        uint8_t* dst = slots + si * kSlotBytes;
+        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 16 * (64 * i + tid));
+        if (c % GC == 0 && !(ok = wait(&empty[gi], ((grp / kGroups) & 1) ^ 1, 11))) break;
+        uint8_t* dst = groups + gi * Sh::kGroupBytes + (c % GC) * kSlotBytes;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int id = 32 * (4 * w + i) + lane, row = id >> 2, piece = 2 * (id & 3);
+        for (int i = 0; i < 8; ++i) {
+          const int id = 64 * i + tid, row = id >> 2, piece = 2 * (id & 3);
           const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[2 * j] = e4m3x2_bf16x2((uint16_t)v[j]);
-            o[2 * j + 1] = e4m3x2_bf16x2((uint16_t)(v[j] >> 16));
+            o[2 * j] = e4m3x2_f16x2(v[j]);
+            o[2 * j + 1] = e4m3x2_f16x2(v[j] >> 16);
           }
-          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * (piece ^ (row & 7))) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * ((piece + 1) ^ (row & 7))) =
-              make_uint4(o[4], o[5], o[6], o[7]);
+          uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+          if (clear && first + row >= seen) {
+            if (first + row >= keys) a = b = make_uint4(0, 0, 0, 0);
+            any |= clear_unbounded<true>(a);
+            any |= clear_unbounded<true>(b);
+          }
+          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * (piece ^ (row & 7))) = a;
+          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * ((piece + 1) ^ (row & 7))) = b;
         }
+        if (any) s_unbounded[part % kParts] = (int)part + 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&full[si]);
+          mbar_arrive(&full[gi]);
           mbar_arrive(&raw_empty[ri]);
         }
+        if (c % GC == GC - 1) ++grp;
       }
+    };
+    for (uint32_t np = 0; ok; ++np) {
+      if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
+      const Part s = parts[np % kParts];
+      if (s.stop) break;
+      const int n = s.k1 - s.k0, qb = segs % QB;
+      if (!(ok = wait(&q_raw[qb], (segs / QB) & 1, 12))) break;
+      for (int q = 0; q < QT; ++q) {   // 8 threads to a row
+        const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          const int r = r0 + (tid >> 3);
+          uint8_t* line = sq + qb * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
+          uint4 x[NC];
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
+            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
+          }
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          // exponent of the largest element, within what keeps both factors normal
+          const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
+          const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
+              v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          if ((tid & 7) == 0)
+            s_qs[(np % kParts) * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+      ++segs;
+      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+      auto keys_in = [&]() { convert(false, 0, 0, 0, 0); };
+      auto values_in = [&]() { convert(128 * (vk + 1) > vseen, 128 * vk, vseen, vkeys, vpart); };
+      for (int t = 0; t < n && ok; ++t, ++u) {
+        keys_in();
+        if (!Two && ok && (QB == 1 ? t > 0 : u > 0)) values_in();
+        vk = s.k0 + t;
+        vseen = seen;
+        vkeys = s.keys;
+        vpart = np;
+        if (Two && ok) values_in();
+      }
+      if (QB == 1 && !Two && ok) values_in();
+    }
+    if (QB == 2 && u && ok) {
+      grp += NG;
+      convert(128 * (vk + 1) > vseen, 128 * vk, vseen, vkeys, vpart);
     }
   } else {
     // ------------------------------------------------- softmax, output
-    // After a failed wait these warps run through, so that the barriers they
-    // share complete, and store nothing.
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    // operand chunks, parts and key tiles before this part; products that pv_done counts
-    uint32_t base = 0, segs = 0, tiles = 0, pvs = 0;
-    AttnShared mine = {};
-    while (walk.next(s)) {
-      const int n = s.k1 - s.k0, rows = s.tokens * p.G;
-      const bool live = row < rows, work = 32 * quarter < rows;
-      const int tok = s.tok0 + row / p.G, head = s.h * p.G + row % p.G;
-      uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)head * D + half * (D / 2);
-      const long long cost = kItemCost + s.keys, c0 = walk.c0, share = walk.c1 - walk.c0;
-      if (s.at >= c0 && s.at + cost > c0 + share) {
-        // this CTA begins a row tile that others go on with: which hold a part
-        int first = blockIdx.x, last = (int)((s.at + cost - 1) / share);
-        if (s.k1 == 0) ++first;
-        if (Walk::border(last * share - s.at, cost, s.nk) == s.nk) --last;
-        if (s.nk && last > first) {
-          mine.row = s.row + s.tok0;
-          mine.tokens = s.tokens;
-          mine.head = s.h;
-          mine.first = first;
-          mine.count = last - first + 1;
-        }
-      }
-      if (s.nk == 0) {   // no keys: zeros
-        if (live && s.at >= c0 && !*abort_flag)
-          for (int i = 0; i < D / 2; i += 8) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      if (n <= 0) continue;
-      ++segs;
-      const float ks = E ? p.a.cache.k_scale[s.h] : 1.0f;
-      const float c2 = p.a.scale * ks * 1.4426950408889634f;   // scores in log2
-      const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
-      // keys before `seen` are seen by every row of the tile
-      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-      float m = -INFINITY, l = 0.0f;
-      for (int t = 0; t < n; ++t, ++tiles) {
-        const int k = s.k0 + t, buf = tiles & 1;
-        const bool masked = 128 * (k + 1) > seen;
-        const uint32_t sc = tmem + lanes + kColS + 128 * buf + 64 * half;
-        unsigned long long vis = ~0ull;
-        if (masked) vis = live ? seen_bits(128 * k + 64 * half - s.ctx, tok, words, p.a.mask_words) : 0;
-        wait(&s_full[buf], (tiles >> 1) & 1, 10);
-        tc_fence_after();
-        if (work) {
-          uint32_t x[2][32];
-          tmem_ld_32x32b_x32(sc, x[0]);
-          tmem_ld_32x32b_x32(sc + 32, x[1]);
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const uint32_t w = (uint32_t)(vis >> (i & 32));
-              if (!(w >> (i & 31) & 1)) x[i >> 5][i & 31] = 0xff800000u;
-            }
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i >> 5][i & 31]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          s_max[256 * buf + 128 * half + row] = top;
-          pair_sync(quarter);
-          top = fmaxf(top, s_max[256 * buf + 128 * (half ^ 1) + row]) * c2;
-          // (NaN scores are left out of the maximum and make the sum NaN)
-          const bool grow = top > m + kGrowth || m == -INFINITY;
-          const float old = m;
-          if (grow && top > m) m = top;
-          if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
-            // (the scores of this tile follow the product of the last but one: of pv_done's phases
-            // only the last product's can be open)
-            wait(pv_done, (pvs - 1) & 1, 11);
-            tc_fence_after();
-            const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < D / 2; i += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tmem + lanes + half * (D / 2) + i, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_32x32b_x32(tmem + lanes + half * (D / 2) + i, o);
-            }
-          }
-          const float ref = m == -INFINITY ? 0.0f : m;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = ex2(fmaf(__uint_as_float(x[i >> 4][2 * i & 31]), c2, -ref));
-            const float b = ex2(fmaf(__uint_as_float(x[i >> 4][(2 * i & 31) + 1]), c2, -ref));
-            sum[2 * i & 3] += a;
-            sum[(2 * i & 3) + 1] += b;
-            w[i] = pack_bf16x2(a, b);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st_32x32b_x32(sc, w);
-          tmem_wait_st();
-        }
-        if (masked) {
-          // values that some row must not see: keys past the row tile's own are
-          // nobody's, others only where they are no numbers
-          const int key = threadIdx.x & 127, j = 128 * k + key;
-          const uint32_t at = base + value_chunk(t, n, NC);
-          bool any = false;
-          for (int c = 0; c < NC; ++c) {
-            const uint32_t i = (at + c) % kSlots;
-            wait(&full[i], ((at + c) / kSlots) & 1, 12);
-            if (j < seen) continue;
-            uint4* v = reinterpret_cast<uint4*>(slots + i * kSlotBytes + 128 * key);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4* piece = v + ((4 * half + q) ^ (key & 7));
-              uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
-              const bool un = clear_unbounded(y);
-              if (un || j >= s.keys) *piece = y;
-              any |= un;
-            }
-          }
-          if (any) *s_unbounded = (int)segs;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
-        if (t + 1 < n) ++pvs;   // tile t's product
-      }
-      base += 2 * n * NC;
-      // the part's sums
-      wait(o_full, (segs - 1) & 1, 13);
+    // One: 64 score columns and half of O's columns each; Two: a row tile each
+    constexpr int CW = Two ? 128 : 64, OW = Two ? D : D / 2;
+    const int q0 = Two ? half * p.R : 0, oc0 = Two ? 0 : half * OW;
+    uint32_t np = 0, segs = 0, u = 0, base = 0, pvs = 0, pairs = 0;
+    bool ok = true;
+    // exchange between the two warps of a lane quarter (One)
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pair[quarter]);
+      return wait(&pair[quarter], pairs++ & 1, 14);
+    };
+    // the sums of part `part`, the seg-th with keys
+    auto finish = [&](uint32_t part, uint32_t seg, float m, float l) {
+      const Part s = parts[part % kParts];
+      const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
+      const bool live = row < rows;
+      const int tok = s.tok0 + q0 + row / p.G, head = s.h * p.G + row % p.G;
+      if (!(ok = wait(&o_full[ob], (Two ? seg : seg / OB) & 1, 13))) return;
       tc_fence_after();
-      if (work) {
-        s_max[128 * half + row] = l;
-        pair_sync(quarter);
-        l += s_max[128 * (half ^ 1) + row];
-        pair_sync(quarter);   // read before the next part's maxima
+      if (32 * quarter < rows) {
+        if (!Two) {
+          s_sum[128 * half + row] = l;
+          if (!(ok = meet())) return;
+          l += s_sum[128 * (half ^ 1) + row];
+        }
         const bool whole = s.k0 == 0 && s.k1 == s.nk;
         const float inv = whole ? (l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / l) : 1.0f;
-        const int place = 2 * blockIdx.x + (s.k0 == 0 && s.at >= c0 ? 1 : 0);
-        const bool fix = *s_unbounded == (int)segs;
+        const bool fix = s_unbounded[part % kParts] == (int)part + 1;
+        const int at = (s.place * QT + (Two ? half : 0)) * 128 + row;   // in scratch
+        uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)head * D + oc0;
+        const uint32_t oc = tmem + lanes + 128 * ob + oc0;
+        const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1, end = min(s.keys, 128 * s.k1);
+        const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
 #pragma unroll 1
-        for (int i = 0; i < D / 2; i += 32) {
+        for (int i = 0; i < OW; i += 32) {
           uint32_t o[32];
           __syncwarp();
-          tmem_ld_32x32b_x32(tmem + lanes + half * (D / 2) + i, o);
-          tmem_wait_ld();
-          if (!live || *abort_flag) continue;
+          tmem_ld_32x32b_x32(oc + i, o);
+          tmem_wait_ld(o);
+          if (!live) continue;
           if (fix) {
-            const int end = min(s.keys, 128 * s.k1);
             for (int j = max(seen, 128 * s.k0); j < end; ++j) {
               if (!(seen_bits(j - s.ctx, tok, words, p.a.mask_words) & 1)) continue;
               const int id = p.a.table[(long long)s.b * p.a.table_width + (j >> p.a.page_shift)];
               if (id < 0 || id >= p.a.cache.pages) continue;
               const long long e = ((((long long)id * p.a.kv_heads + s.h) << p.a.page_shift) +
-                                   (j & ((1 << p.a.page_shift) - 1))) * D + half * (D / 2) + i;
+                                   (j & ((1 << p.a.page_shift) - 1))) * D + oc0 + i;
 #pragma unroll
               for (int q = 0; q < 32; ++q) {
                 const float v = cache_value<E>(p.a.cache.v, e + q);
@@ -723,21 +903,209 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
               *reinterpret_cast<uint4*>(out + i + q) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + ((long long)place * 128 + row) * D + half * (D / 2) + i);
+            uint4* dst = reinterpret_cast<uint4*>(p.o + (long long)at * D + oc0 + i);
 #pragma unroll
             for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
-        if (!whole && half == 0 && live) p.ml[place * 128 + row] = make_float2(m == -INFINITY ? 0.0f : m, l);
+        if (!whole && live && (Two || half == 0)) p.ml[at] = make_float2(m == -INFINITY ? 0.0f : m, l);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) {
+        mbar_arrive(&o_free[ob]);
+        mbar_arrive(&part_empty[part % kParts]);
+      }
+    };
+    bool have = false;          // the part before is to be finished
+    uint32_t last_part = 0;
+    float last_m = 0.0f, last_l = 0.0f;
+    for (; ok; ++np) {
+      if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
+      const Part s = parts[np % kParts];
+      if (s.stop) break;
+      const int n = s.k1 - s.k0, rows = max(min(s.tokens - q0, p.R), 0) * p.G;
+      const bool live = row < rows, work = 32 * quarter < rows;
+      const int tok = s.tok0 + q0 + row / p.G;
+      const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
+      // keys before `seen` are seen by every row
+      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+      // scores in log2; with fp16 weights the reference is 2^7 below the maximum
+      float c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
+      float m = -INFINITY, l = 0.0f;
+      for (int t = 0; t < n && ok; ++t, ++u) {
+        const int k = s.k0 + t, buf = Two ? half : u & 1;
+        const bool masked = 128 * (k + 1) > seen;
+        const uint32_t sc = tmem + lanes + kColS + 128 * buf + (Two ? 0 : 64 * half);
+        unsigned long long vis[CW / 64];
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < CW / 64; ++i)
+            vis[i] = live ? seen_bits(128 * k + (Two ? 64 * i : 64 * half) - s.ctx, tok, words, p.a.mask_words) : 0;
+        }
+        if (!(ok = wait(&s_full[buf], (Two ? u : u >> 1) & 1, 15))) break;
+        tc_fence_after();
+        if (E && t == 0) c2 = fmaxf(c2 * s_qs[(np % kParts) * 128 * QT + (Two ? 128 * half : 0) + row], 1e-37f);
+        if (work) {
+          // 32 scores from column i on, hidden ones -inf
+          auto hide = [&](uint32_t (&x)[32], int i) {
+            const uint32_t v = (uint32_t)(vis[i >> 6] >> (i & 32));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(v >> j & 1)) x[j] = 0xff800000u;
+          };
+          auto largest = [&](const uint32_t (&x)[32]) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              a = fmaxf(a, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+              b = fmaxf(b, fmaxf(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])));
+            }
+            return fmaxf(a, b);
+          };
+          uint32_t x[2][32];
+          float top = -INFINITY;
+          if constexpr (Two) {
+            tmem_ld_32x32b_x32(sc, x[0]);
+            tmem_wait_ld(x[0]);
+#pragma unroll
+            for (int i = 0; i < CW; i += 32) {
+              if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
+              if (masked) hide(x[i / 32 & 1], i);
+              top = fmaxf(top, largest(x[i / 32 & 1]));
+              if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
+            }
+          } else {
+            tmem_ld_32x32b_x32(sc, x[0]);
+            tmem_ld_32x32b_x32(sc + 32, x[1]);
+            tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            if (masked) {
+              hide(x[0], 0);
+              hide(x[1], 32);
+            }
+            top = fmaxf(largest(x[0]), largest(x[1]));
+            s_max[256 * buf + 128 * half + row] = top;
+            if (!(ok = meet())) break;
+            top = fmaxf(top, s_max[256 * buf + 128 * (half ^ 1) + row]);
+          }
+          top *= c2;
+          // (NaN scores are left out of the maximum and make the sum NaN)
+          const bool grow = top > m + kGrowth || m == -INFINITY;
+          const float old = m;
+          if (grow && top > m) m = top;
+          if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
+            // The last product has to be done. Two: these scores came after it.
+            // One: they came after the one before it, so only the last one's
+            // phase of pv_done can be open.
+            if (!Two) {
+              if (!(ok = wait(pv_done, (pvs - 1) & 1, 16))) break;
+              tc_fence_after();
+            }
+            const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
+            const uint32_t oc = tmem + lanes + 128 * (Two ? half : (int)(segs % OB)) + oc0;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < OW; i += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(oc + i, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_32x32b_x32(oc + i, o);
+            }
+          }
+          const float ref = (E ? 7.0f : 0.0f) - (m == -INFINITY ? 0.0f : m);
+          float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+          auto weights = [&](const uint32_t (&x)[32], uint32_t* w) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 a = fma2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), c2, ref);
+              a.x = ex2(a.x);
+              a.y = ex2(a.y);
+              sum[j & 1] = add2(sum[j & 1], a);
+              if constexpr (E) {
+                const __half2 hv = __floats2half2_rn(a.x, a.y);
+                w[j] = *reinterpret_cast<const uint32_t*>(&hv);
+              } else {
+                w[j] = pack_bf16x2(a.x, a.y);
+              }
+            }
+          };
+          if constexpr (Two) {
+            // the scores once more: a row's 128 do not fit the registers
+            tmem_ld_32x32b_x32(sc, x[0]);
+            tmem_wait_ld(x[0]);
+#pragma unroll
+            for (int i = 0; i < CW; i += 32) {
+              if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
+              if (masked) hide(x[i / 32 & 1], i);
+              uint32_t w[16];
+              weights(x[i / 32 & 1], w);
+              if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
+              tmem_st_32x32b_x16(sc + i / 2, w);
+            }
+          } else {
+            uint32_t w[32];
+            weights(x[0], w);
+            weights(x[1], w + 16);
+            tmem_st_32x32b_x32(sc, w);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_wait_st();
+        }
+        if (!E && masked) {
+          // values that some row must not see: keys past the row tile's own are
+          // nobody's, others only where they are no numbers. (Two: both groups
+          // of warps clear all of them, with the same result.)
+          if (D == 256 && t > 0 && !(ok = wait(pv_done, (pvs - 1) & 1, 17))) break;
+          const int key = threadIdx.x & 127, j = 128 * k + key;
+          const uint32_t at = Two ? base + NG * (2 * t + 1)
+                              : QB == 2 ? NG * (2 * u + 2)
+                                        : base + NG * (t + 1 < n ? 2 * t + 2 : 2 * n - 1);
+          bool any = false;
+          for (int g = 0; g < NG && ok; ++g) {
+            const uint32_t i = (at + g) % kGroups;
+            if (!(ok = wait(&full[i], ((at + g) / kGroups) & 1, 18))) break;
+            if (j < seen) continue;
+            for (int c = 0; c < GC; ++c) {
+              uint4* v = reinterpret_cast<uint4*>(groups + i * Sh::kGroupBytes + c * kSlotBytes + 128 * key);
+#pragma unroll
+              for (int q = 0; q < CW / 16; ++q) {
+                uint4* piece = v + ((Two ? q : 4 * half + q) ^ (key & 7));
+                uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
+                const bool un = clear_unbounded<false>(y);
+                if (un || j >= s.keys) *piece = y;
+                any |= un;
+              }
+            }
+          }
+          if (any) s_unbounded[np % kParts] = (int)np + 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (!ok) break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+        if (t + 1 < n) ++pvs;   // this tile's product, as pv_done counts it
+        if (t == 0 && have) {
+          // the part before: its last product ran while these weights were made
+          have = false;
+          finish(last_part, segs - 1, last_m, last_l);
+        }
+      }
+      base += 2 * n * NG;
+      last_part = np;
+      last_m = m;
+      last_l = l;
+      have = true;
+      ++segs;
+      if (Two && ok) {
+        have = false;
+        finish(np, segs - 1, m, l);
+      }
     }
-    if (threadIdx.x == 0) {
-      if (*abort_flag) mine.count = 0;
-      p.shared[blockIdx.x] = mine;
-    }
+    if (have && ok) finish(last_part, segs - 1, last_m, last_l);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -746,38 +1114,46 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1) tree_attn_kernel(con
   }
 }
 
-// Joins the parts of the row tiles that CTAs share: block (c, i) takes the rows
-// i, i + gridDim.y, .. of the tile that CTA c began. Its warps take alternate
-// parts, then add up through shared memory.
-constexpr int kJoinWarps = 8;
-template <int D>
+// Joins the parts of the row tiles that CTAs share: block (c, i) takes some rows
+// of the tile that CTA c began. A row has as many warps as 4 parts each need, up
+// to all 8, which take alternate parts and add up through shared memory.
+constexpr int kJoinWarps = 8, kJoinBlocks = 16;
+template <int D, int QT>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams p) {
   pdl_begin();
   const AttnShared s = p.shared[blockIdx.x];
-  constexpr int V = D / 32;
+  if (s.count == 0) return;
+  constexpr int V = D / 32, U = 4;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // (the CTA that began the tile holds its part in its second place)
-  auto place = [&](int i) { return 2 * (s.first + i) + (s.first + i == (int)blockIdx.x ? 1 : 0); };
-  for (int row = blockIdx.y; s.count && row < s.tokens * p.G; row += gridDim.y) {
+  int per = 1;                                   // warps of a row
+  while (per < kJoinWarps && per * U < s.count) per *= 2;
+  const int at_once = kJoinWarps / per, sub = warp % per, rows = s.tokens * p.G;
+  for (int row0 = blockIdx.y * at_once; row0 < rows; row0 += gridDim.y * at_once) {
+    const int row = row0 + warp / per;
+    const bool on = row < rows;
+    const int tok = row / p.G, place_row = tok / p.R * 128 + tok % p.R * p.G + row % p.G;
     float o[V] = {}, m = -INFINITY, l = 0.0f;
-    for (int i0 = warp; i0 < s.count; i0 += 4 * kJoinWarps) {
-      float x[4][V];
-      float2 ml[4];
+    for (int i0 = sub; on && i0 < s.count; i0 += U * per) {
+      float x[U][V];
+      float2 ml[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * kJoinWarps;
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * per, cta = s.first + i;
         ml[u] = make_float2(0.0f, 0.0f);
         if (i < s.count) {
-          const long long at = (long long)place(i) * 128 + row;
+          // (the CTA that began the tile holds its part in its second place)
+          const long long at = (2ll * cta + (cta == (int)blockIdx.x)) * 128 * QT + place_row;
           ml[u] = p.ml[at];
+          const float* src = p.o + at * D + V * lane;
 #pragma unroll
-          for (int v = 0; v < V; ++v) x[u][v] = p.o[at * D + lane + 32 * v];
+          for (int v = 0; v < V; v += 2)
+            *reinterpret_cast<float2*>(&x[u][v]) = *reinterpret_cast<const float2*>(src + v);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (ml[u].y == 0.0f) continue;
         const float mn = fmaxf(m, ml[u].x), f = ex2(m - mn), g = ex2(ml[u].x - mn);
         m = mn;
@@ -786,26 +1162,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams
         for (int v = 0; v < V; ++v) o[v] = o[v] * f + x[u][v] * g;
       }
     }
-    __syncthreads();
+    if (per > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = o[v];
-    if (lane == 0) s_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    float M = -INFINITY, L = 0.0f, f[kJoinWarps];
+      for (int v = 0; v < V; ++v) s_o[warp][V * lane + v] = o[v];
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (sub == 0) {
+        for (int w = warp + 1; w < warp + per; ++w) {
+          const float2 ml = s_ml[w];
+          if (ml.y == 0.0f) continue;
+          const float mn = fmaxf(m, ml.x), f = ex2(m - mn), g = ex2(ml.x - mn);
+          m = mn;
+          l = l * f + ml.y * g;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      f[w] = s_ml[w].y == 0.0f ? 0.0f : ex2(s_ml[w].x - M);
-      L += s_ml[w].y * f[w];
+          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][V * lane + v] * g;
+        }
+      }
+      __syncthreads();
     }
-    const float scale = L == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / L;
-    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
-      float sum = 0.0f;
+    if (on && sub == 0) {
+      const float scale = l == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / l;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.out + (long long)(s.row + tok) * p.a.o_ld +
+                                                  (long long)(s.head * p.G + row % p.G) * D) + V / 2 * lane;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) sum += s_ml[w].y == 0.0f ? 0.0f : s_o[w][d] * f[w];
-      p.a.out[(long long)(s.row + row / p.G) * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + d] =
-          f32_to_bf16(sum * scale);
+      for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(o[v] * scale, o[v + 1] * scale);
     }
   }
 }
@@ -823,15 +1203,25 @@ bool encode_maps(const AttnArgs& a, int G, int R, TaParams* p) {
          encode_nd(&p->mv, dt, 4, a.cache.v, cd, cs, cb, !a.e4m3);
 }
 
-template <int D, bool E>
-cudaError_t launch(const TaParams& p, int num_sms, cudaStream_t st) {
-  using Sh = Shape<D, E>;
-  auto kern = tree_attn_kernel<D, E>;
+template <int D, bool E, bool Two>
+cudaError_t launch(TaParams& p, int num_sms, cudaStream_t st) {
+  using Sh = Shape<D, E, Two>;
+  p.step = Sh::QT * p.R;
+  auto kern = tree_attn_kernel<D, E, Two>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Sh::kSmem);
   const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, st, p);
-  if (e == cudaSuccess) e = launch_pdl(tree_attn_join<D>, dim3(ctas, 16), dim3(32 * kJoinWarps), 0, st, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_attn_join<D, Sh::QT>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
   return e;
+}
+
+template <int D>
+cudaError_t launch_for(TaParams& p, bool two, int num_sms, cudaStream_t st) {
+  if constexpr (D <= 128) {
+    if (two) return p.a.e4m3 ? launch<D, true, true>(p, num_sms, st) : launch<D, false, true>(p, num_sms, st);
+  }
+  return p.a.e4m3 ? launch<D, true, false>(p, num_sms, st) : launch<D, false, false>(p, num_sms, st);
 }
 
 }  // namespace
@@ -845,13 +1235,12 @@ cudaError_t launch_tree_attention(const AttnArgs& a, void* scratch, int num_sms,
   p.err = err;
   p.shared = static_cast<AttnShared*>(scratch);
   p.o = reinterpret_cast<float*>(p.shared + kAttnMaxCtas);
-  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kAttnMaxCtas * 2 * 128 * a.head_dim);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kAttnMaxCtas * 2 * attn_rows(a.head_dim) * a.head_dim);
   if (!encode_maps(a, p.G, p.R, &p)) return cudaErrorInvalidValue;
-  switch (a.head_dim) {
-    case 64: return a.e4m3 ? launch<64, true>(p, num_sms, st) : launch<64, false>(p, num_sms, st);
-    case 128: return a.e4m3 ? launch<128, true>(p, num_sms, st) : launch<128, false>(p, num_sms, st);
-    default: return a.e4m3 ? launch<256, true>(p, num_sms, st) : launch<256, false>(p, num_sms, st);
-  }
+  const bool two = (long long)a.T * p.G >= 256ll * a.requests;
+  if (a.head_dim == 64) return launch_for<64>(p, two, num_sms, st);
+  if (a.head_dim == 128) return launch_for<128>(p, two, num_sms, st);
+  return launch_for<256>(p, two, num_sms, st);
 }
 
 }  // namespace moe

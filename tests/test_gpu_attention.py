@@ -591,3 +591,30 @@ def test_attention_many_key_tiles_per_sm(Hq, Hkv, D, cache):
     h = torch.Generator().manual_seed(D)
     lengths = torch.randint(600, 1800, (B,), generator=h).tolist()
     run_attention(lengths, [1 + b % 3 for b in range(B)], Hq, Hkv, D, 64, cache)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_zero_rows_between_others(D, cache):
+    """Requests without keys in long runs between served ones, on few and on many SMs."""
+    for rep in (1, 40):
+        lengths, news = [], []
+        for i in range(rep):
+            lengths += [200 + i, 0, 0, 0, 0, 0, 0, 33, 0, 5]
+            news += [1, 1, 2, 1, 1, 1, 3, 2, 1, 5]
+        run_attention(lengths, news, 4, 2, D, 16, cache)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 64), (16, 2, 128), (3, 1, 128), (4, 4, 64), (7, 1, 64)])
+def test_attention_prompts_of_many_row_tiles(Hq, Hkv, D, cache):
+    """Long chains, whose row tiles go two by two; odd ends of rows and of keys, several requests."""
+    run_attention([900, 333, 1500], [900, 200, 517], Hq, Hkv, D, 32, cache, seed=Hq)
+
+
+def test_attention_prompts_with_numbers_that_are_none():
+    def edit(d):
+        d["vc"][int(d["table"][0, 300 // 16]), 0, 300 % 16, 3::7] = float("nan")
+        d["vc"][int(d["table"][0, 555 // 16]), 0, 555 % 16, 1::9] = float("inf")
+    run_attention([600], [590], 4, 1, 64, 16, edit=edit)
+    run_attention([600], [590], 4, 1, 128, 16, edit=edit)
