@@ -29,6 +29,8 @@
 //     are replaced, and values that some row must not see are set to zero in
 //     shared memory (their NaN times weight 0 would be NaN) and, in rows that do
 //     see them, added at the end.
+#include <limits.h>
+
 #include "attn.h"
 #include "moe_common.cuh"
 
@@ -37,7 +39,8 @@ namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 constexpr int kRawBytes = 128 * 64;         // 128 rows of 64 e4m3
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 2;
+// warps 0..7 softmax, 8 loads, 9 products, 10..13 conversion (e4m3)
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512, kColS = 256;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
@@ -72,9 +75,11 @@ struct TaParams {
   AttnArgs a;
   AttnShared* shared;
   float2* ml;          // [cta][2][128 QT] maximum (log2) and sum
-  float* o;            // [cta][2][128 QT][D]
+  float* o;            // [cta][2][D][128 QT]: a warp stores a column of its 32 rows at a time
+  float inv_ctas;      // 1 / CTAs, a little more
   int G, R;            // query heads per key-value head, tokens per row tile
   int step;            // tokens of a row tile, or of two
+  unsigned inv_step;   // 2^31 / step, rounded up
   DevErr err;
 };
 
@@ -169,7 +174,8 @@ __device__ __forceinline__ Req req_of(const TaParams& p, int lo, int hi, int len
   r.n = max(hi - lo, 0);
   len = min(len, p.a.table_width << p.a.page_shift);
   r.ctx = len >= r.n ? len - r.n : -1;
-  r.tiles = (r.n + p.step - 1) / p.step;
+  // (exact: the quotient's error is below (2^20 + 2^8) 2^8 / 2^31 of one)
+  r.tiles = (int)((unsigned long long)(unsigned)(r.n + p.step - 1) * p.inv_step >> 31);
   return r;
 }
 
@@ -178,20 +184,21 @@ __device__ __forceinline__ int keys_of(const TaParams& p, const Req& r, int t) {
 }
 // cost of a request's first t row tiles under one head (all but the last are full)
 __device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r, int t) {
+  if (t == 0) return 0;
   long long c = (long long)t * (kItemCost + max(r.ctx, 0));
   if (r.ctx >= 0) c += (long long)p.step * t * (t + 1) / 2;
   return c;
 }
 __device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
-  if (r.n == 0) return 0;
-  return cost_before(p, r, r.tiles - 1) + kItemCost + keys_of(p, r, r.tiles - 1);
+  return r.n ? cost_before(p, r, r.tiles - 1) + kItemCost + keys_of(p, r, r.tiles - 1) : 0;
 }
-
-struct Start {
-  long long at, share;   // cost before the CTA's first row tile; a CTA's cost
-  int b, h, t;
-  Req r;
-};
+// floor(x / d) for 0 <= x, 0 < d, at most `most`
+__device__ __forceinline__ int quotient(long long x, long long d, int most) {
+  int q = min((int)__fdividef((float)x, (float)d), most);
+  while (q > 0 && q * d > x) --q;
+  while (q < most && (q + 1) * d <= x) ++q;
+  return q;
+}
 
 // A CTA's part of a row tile (or of two): key tiles [k0, k1) of nk.
 struct Part {
@@ -207,18 +214,94 @@ struct Walk {
   int b, h, t;
   Req r;
   int lo, hi, len;     // of request b + 1, read ahead
-  AttnShared mine;     // the row tile that this CTA begins and others go on with
+  long long from;      // the row tile that this CTA begins and others go on with: its cost, -1 none
+  Part* last;          // (in shared memory)
 
   __device__ __forceinline__ void ahead() {
     if (b + 1 < p.a.requests) {
-      lo = __ldg(p.a.offsets + b + 1);
-      hi = __ldg(p.a.offsets + b + 2);
-      len = __ldg(p.a.length + b + 1);
+      lo = __ldcg(p.a.offsets + b + 1);
+      hi = __ldcg(p.a.offsets + b + 2);
+      len = __ldcg(p.a.length + b + 1);
     }
   }
-  __device__ __forceinline__ Walk(const TaParams& p_, const Start& s)
-      : p(p_), c0((long long)blockIdx.x * s.share), c1(c0 + s.share), at(s.at), b(s.b), h(s.h), t(s.t), r(s.r),
-        mine{} {
+  __device__ __forceinline__ Req load(int i) const {
+    return req_of(p, __ldcg(p.a.offsets + i), __ldcg(p.a.offsets + i + 1), __ldcg(p.a.length + i));
+  }
+
+  // By a whole warp. Equal costs per CTA, at least what one key tile costs (a
+  // smaller part would have none): the costs of all requests are summed up, a
+  // run of them per lane, and the lane in whose run the CTA's cost begins looks
+  // for the row tile.
+  __device__ __forceinline__ explicit Walk(const TaParams& p_, Part* last_) : p(p_), last(last_) {}
+  __device__ __forceinline__ void begin() {
+    b = p.a.requests;
+    from = -1;
+    const int lane = threadIdx.x & 31, B = p.a.requests, per = (B + 31) / 32;
+    const int b0 = min(lane * per, B), b1 = min(b0 + per, B);
+    long long mine = 0;
+    Req first{};
+    for (int i0 = b0; i0 < b1; i0 += 4) {
+      // (four requests' loads at once)
+      int from_row[4], to_row[4], lens[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = min(i0 + j, b1 - 1);
+        from_row[j] = __ldcg(p.a.offsets + i);
+        to_row[j] = __ldcg(p.a.offsets + i + 1);
+        lens[j] = __ldcg(p.a.length + i);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i0 + j >= b1) break;
+        const Req q = req_of(p, from_row[j], to_row[j], lens[j]);
+        if (i0 + j == b0) first = q;
+        mine += cost_of(p, q);
+        if (blockIdx.x == 0 && q.n && lens[j] > (p.a.table_width << p.a.page_shift))
+          atomicOr(p.err.word, DEVERR_RANGE);
+      }
+    }
+    mine *= p.a.kv_heads;
+    __syncwarp();
+    long long before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
+    }
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    // (rounded up past the float's error: the shares cover the total)
+    const long long share = max((long long)((float)total * p.inv_ctas) + 1, (long long)(kItemCost + 128));
+    c0 = blockIdx.x * share;
+    c1 = c0 + share;
+    const bool owner = c0 >= before && c0 < before + mine;
+    const unsigned who = __ballot_sync(0xffffffffu, owner);
+    if (!who) return;
+    if (owner) {
+      r = first;
+      long long head = cost_of(p, r);
+      for (b = b0; c0 >= before + p.a.kv_heads * head;) {
+        before += p.a.kv_heads * head;
+        r = load(++b);
+        head = cost_of(p, r);
+      }
+      h = quotient(c0 - before, head, p.a.kv_heads - 1);
+      before += h * head;
+      t = 0;
+      for (int end = r.tiles; end - t > 1;) {
+        const int mid = (t + end) >> 1;
+        if (cost_before(p, r, mid) <= c0 - before) t = mid; else end = mid;
+      }
+      at = before + cost_before(p, r, t);
+    }
+    __syncwarp();
+    const int src = __ffs(who) - 1;
+    auto all = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+    at = __shfl_sync(0xffffffffu, at, src);
+    b = all(b);
+    h = all(h);
+    t = all(t);
+    r = {all(r.row), all(r.n), all(r.ctx), all(r.tiles)};
     ahead();
   }
   // The next part that has work: key tiles, or a row tile without keys that
@@ -226,7 +309,7 @@ struct Walk {
   __device__ __forceinline__ bool next(Part& s) {
     while (b < p.a.requests && at < c1) {
       const int keys = keys_of(p, r, t), nk = (keys + 127) >> 7;
-      const long long cost = kItemCost + keys, share = c1 - c0;
+      const long long cost = kItemCost + keys;
       const bool begins = at >= c0;
       s.b = b;
       s.h = h;
@@ -241,17 +324,8 @@ struct Walk {
       s.place = 2 * blockIdx.x + (begins ? 1 : 0);
       s.stop = 0;
       if (begins && at + cost > c1) {
-        // others go on: which hold a part
-        int first = blockIdx.x, last = (int)((at + cost - 1) / share);
-        if (s.k1 == 0) ++first;
-        if (border(last * share - at, cost, nk) == nk) --last;
-        if (nk && last > first) {
-          mine.row = s.row + s.tok0;
-          mine.tokens = s.tokens;
-          mine.head = h;
-          mine.first = first;
-          mine.count = last - first + 1;
-        }
+        from = at;
+        if ((threadIdx.x & 31) == 0) *last = s;
       }
       at += cost;
       if (++t == r.tiles) {
@@ -269,6 +343,24 @@ struct Walk {
     }
     return false;
   }
+  // The row tile that this CTA begins and others go on with: which hold a part.
+  __device__ __forceinline__ AttnShared shared() const {
+    AttnShared m = {};
+    if (from < 0 || last->nk == 0) return m;
+    const long long cost = kItemCost + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
+    const int n = quotient(x, share, kAttnMaxCtas);   // CTAs on, of the one where the tile ends
+    int first = blockIdx.x, end = blockIdx.x + n;
+    if (last->k1 == 0) ++first;
+    if (border(end * share - from, cost, last->nk) == last->nk) --end;
+    if (end > first) {
+      m.row = last->row + last->tok0;
+      m.tokens = last->tokens;
+      m.head = last->h;
+      m.first = first;
+      m.count = end - first + 1;
+    }
+    return m;
+  }
   // Key tile at which a cost x into a row tile falls.
   static __device__ __forceinline__ int border(long long x, long long cost, int nk) {
     if (x >= cost) return nk;
@@ -276,62 +368,6 @@ struct Walk {
     return (int)(k < 0 ? 0 : k > nk ? nk : k);
   }
 };
-
-// Equal costs per CTA, at least what one key tile costs (a smaller part would
-// have none), and where this CTA begins.
-template <int kThreads>
-__device__ __forceinline__ void find_start(const TaParams& p, Start* out, long long (&part)[kThreads / 32],
-                                           bool flag_lengths) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.a.requests;
-  const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
-  long long mine = 0;
-  for (int i = 0; i < per && b0 + i < B; ++i) {
-    const int b = b0 + i, len = p.a.length[b];
-    const Req r = req_of(p, p.a.offsets[b], p.a.offsets[b + 1], len);
-    mine += p.a.kv_heads * cost_of(p, r);
-    if (flag_lengths && r.n && len > (p.a.table_width << p.a.page_shift)) atomicOr(p.err.word, DEVERR_RANGE);
-  }
-  long long s = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += o;
-  }
-  if (lane == 31) part[warp] = s;
-  if (tid == 0) out->b = B;
-  __syncthreads();
-  long long before = s - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += part[i];
-    total += part[i];
-  }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)(kItemCost + 128));
-  const long long c0 = blockIdx.x * share;
-  if (tid == 0) out->share = share;
-  if (c0 >= before && c0 < before + mine) {
-    for (int b = b0;; ++b) {
-      const Req r = req_of(p, p.a.offsets[b], p.a.offsets[b + 1], p.a.length[b]);
-      const long long head = cost_of(p, r);
-      if (c0 < before + p.a.kv_heads * head) {
-        const int h = (int)((c0 - before) / head);
-        const long long x = c0 - before - h * head;
-        int lo = 0, hi = r.tiles;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (cost_before(p, r, mid) <= x) lo = mid; else hi = mid;
-        }
-        out->at = before + h * head + cost_before(p, r, lo);
-        out->b = b;
-        out->h = h;
-        out->t = lo;
-        out->r = r;
-        break;
-      }
-      before += p.a.kv_heads * head;
-    }
-  }
-}
 
 // Bits of the keys that a row sees among the 64 from node index `a` (key minus
 // context) on; token i of its request, words of its mask or NULL.
@@ -415,14 +451,12 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drain = part_empty + kParts;
   Part* parts = reinterpret_cast<Part*>(drain + 1);
-  Start* start = reinterpret_cast<Start*>(parts + kParts);
-  long long(*scan)[Sh::kThreads / 32] = reinterpret_cast<long long(*)[Sh::kThreads / 32]>(start + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(*scan + Sh::kThreads / 32);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + kParts + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
   static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 +
-                    8 * (2 * kGroups + 2 * kRaw + 3 * QB + 14 + 2 * kParts) + kParts * sizeof(Part) +
-                    sizeof(Start) + Sh::kThreads / 4 + 64 <= Sh::kMisc, "room for barriers");
+                    8 * (2 * kGroups + 2 * kRaw + 3 * QB + 14 + 2 * kParts) + (kParts + 1) * sizeof(Part) +
+                    64 <= Sh::kMisc, "room for barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -464,8 +498,6 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  pdl_begin();
-  find_start<Sh::kThreads>(p, start, *scan, blockIdx.x == 0);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -481,6 +513,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
     return ok;
   };
+  pdl_begin();
   // Order of the loads and products. One row tile: the scores run one key tile
   // ahead, K0 K1 V0 K2 V1 .., through the ends of parts, too, where the next
   // part's queries have a place of their own (QB 2; at the very end a group's
@@ -489,8 +522,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------- loads, by TMA
-    Walk walk(p, *start);
-    const int page = 1 << p.a.page_shift, box = min(page, 128), nbox = 128 / box;
+    Walk walk(p, parts + kParts);
+    walk.begin();
+    const int page = 1 << p.a.page_shift, box = min(page, 128), nbox = 128 / box, box_log = 31 - __clz(nbox);
     const int my_box = box * (lane & (nbox - 1)), my_chunk = lane / nbox;   // (chunk of a group)
     uint32_t cnt = 0, np = 0, segs = 0;    // groups (e4m3: chunks) loaded, parts told, parts loaded
     bool ok = true, bad = false;
@@ -536,22 +570,24 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         }
         continue;
       }
-      tell();
-      if (!ok) break;
-      const int len_pages = (s.keys + page - 1) >> p.a.page_shift;
+      const int end_page = (s.keys + page - 1) >> p.a.page_shift;
       const int32_t* table = p.a.table + (long long)s.b * p.a.table_width;
-      // this lane's box of key tile k: its page's number; one past the cache (which reads as zeros) behind
-      // the keys, and for numbers outside
-      auto inside = [&](int k) { return k < s.k1 && ((128 * k + my_box) >> p.a.page_shift) < len_pages; };
-      auto entry = [&](int k) { return inside(k) ? __ldg(table + ((128 * k + my_box) >> p.a.page_shift)) : -1; };
-      int id0 = entry(s.k0), id1 = entry(s.k0 + 1);
+      // Page numbers of 32 boxes, one per lane, and of the next 32, read ahead.
+      // Behind the keys, and for numbers outside the cache, the number past its
+      // last page, which reads as zeros.
+      auto numbers = [&](int b) {
+        const int i = ((b + lane) * box) >> p.a.page_shift;
+        return b + lane < (s.k1 << box_log) && i < end_page ? __ldcg(table + i) : -2;
+      };
+      int win = s.k0 << box_log, now = numbers(win), later = numbers(win + 32);
       if (QB == 1 && have) {
         load(&p.mv, vh, vk, vid);
         have = false;
         if (!ok) break;
       }
+      tell();
       const int qb = segs % QB;
-      if (!(ok = wait(&q_empty[qb], ((segs / QB) & 1) ^ 1, 1))) break;
+      if (!ok || !(ok = wait(&q_empty[qb], ((segs / QB) & 1) ^ 1, 1))) break;
       if (elect_one_sync()) {
         uint64_t* bar = E ? &q_raw[qb] : &q_full[qb];
         mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
@@ -563,10 +599,15 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       __syncwarp();
       ++segs;
       for (int k = s.k0; k < s.k1 && ok; ++k) {
-        const int id2 = entry(k + 2);
-        int id = p.a.cache.pages;
-        if (inside(k)) {
-          if (id0 >= 0 && id0 < p.a.cache.pages) id = id0; else bad = true;
+        int id = __shfl_sync(0xffffffffu, now, (k << box_log) - win + (lane & (nbox - 1)));
+        if ((k + 1) << box_log == win + 32) {
+          win += 32;
+          now = later;
+          later = numbers(win + 32);
+        }
+        if (id < 0 || id >= p.a.cache.pages) {
+          bad |= id != -2 || (((k << box_log) + (lane & (nbox - 1))) * box) >> p.a.page_shift < end_page;
+          id = p.a.cache.pages;
         }
         load(&p.mk, s.h, k, id);
         if (Two) {
@@ -578,8 +619,6 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           vk = k;
           vid = id;
         }
-        id0 = id1;
-        id1 = id2;
       }
     }
     if (ok) {
@@ -592,8 +631,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
     if (lane == 0) {
-      if (*abort_flag) walk.mine.count = 0;
-      p.shared[blockIdx.x] = walk.mine;
+      AttnShared m = walk.shared();
+      if (*abort_flag) m.count = 0;
+      p.shared[blockIdx.x] = m;
     }
     if (!ok) {   // own copies land before shared memory is released
       constexpr int kRing = E ? kRaw : kGroups;
@@ -740,14 +780,15 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         const int ri = raw % max(kRaw, 1), gi = grp % kGroups;
         if (!(ok = wait(&raw_full[ri], (raw / max(kRaw, 1)) & 1, 10))) break;
         const uint8_t* src = raws + ri * kRawBytes;
-        uint4 x[8];
+        constexpr int kThr = 32 * kConvWarps, kPer = 512 / kThr;   // 16-byte pieces per thread
+        uint4 x[kPer];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 16 * (64 * i + tid));
+        for (int i = 0; i < kPer; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 16 * (kThr * i + tid));
         if (c % GC == 0 && !(ok = wait(&empty[gi], ((grp / kGroups) & 1) ^ 1, 11))) break;
         uint8_t* dst = groups + gi * Sh::kGroupBytes + (c % GC) * kSlotBytes;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int id = 64 * i + tid, row = id >> 2, piece = 2 * (id & 3);
+        for (int i = 0; i < kPer; ++i) {
+          const int id = kThr * i + tid, row = id >> 2, piece = 2 * (id & 3);
           const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t o[8];
 #pragma unroll
@@ -782,7 +823,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       if (!(ok = wait(&q_raw[qb], (segs / QB) & 1, 12))) break;
       for (int q = 0; q < QT; ++q) {   // 8 threads to a row
         const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
+        for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
           const int r = r0 + (tid >> 3);
           uint8_t* line = sq + qb * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
           uint4 x[NC];
@@ -835,13 +876,14 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       grp += NG;
       convert(128 * (vk + 1) > vseen, 128 * vk, vseen, vkeys, vpart);
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ------------------------------------------------- softmax, output
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     // One: 64 score columns and half of O's columns each; Two: a row tile each
     constexpr int CW = Two ? 128 : 64, OW = Two ? D : D / 2;
     const int q0 = Two ? half * p.R : 0, oc0 = Two ? 0 : half * OW;
+    const int row_tok = q0 + row / p.G, row_g = row % p.G;   // token of the part, query head of the group
     uint32_t np = 0, segs = 0, u = 0, base = 0, pvs = 0, pairs = 0;
     bool ok = true;
     // exchange between the two warps of a lane quarter (One)
@@ -855,7 +897,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       const Part s = parts[part % kParts];
       const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
       const bool live = row < rows;
-      const int tok = s.tok0 + q0 + row / p.G, head = s.h * p.G + row % p.G;
+      const int tok = s.tok0 + row_tok, head = s.h * p.G + row_g;
       if (!(ok = wait(&o_full[ob], (Two ? seg : seg / OB) & 1, 13))) return;
       tc_fence_after();
       if (32 * quarter < rows) {
@@ -903,9 +945,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
               *reinterpret_cast<uint4*>(out + i + q) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + (long long)at * D + oc0 + i);
+            float* dst = p.o + ((long long)s.place * D + oc0 + i) * (128 * QT) + (Two ? 128 * half : 0) + row;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 32; ++q) dst[q * 128 * QT] = __uint_as_float(o[q]);
           }
         }
         if (!whole && live && (Two || half == 0)) p.ml[at] = make_float2(m == -INFINITY ? 0.0f : m, l);
@@ -926,7 +968,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       if (s.stop) break;
       const int n = s.k1 - s.k0, rows = max(min(s.tokens - q0, p.R), 0) * p.G;
       const bool live = row < rows, work = 32 * quarter < rows;
-      const int tok = s.tok0 + q0 + row / p.G;
+      const int tok = s.tok0 + row_tok;
       const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
       // keys before `seen` are seen by every row
       const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
@@ -963,28 +1005,20 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             }
             return fmaxf(a, b);
           };
+          // the scores are read twice, 32 at a time: 64 or 128 of them beside their
+          // weights would not fit the registers
           uint32_t x[2][32];
           float top = -INFINITY;
-          if constexpr (Two) {
-            tmem_ld_32x32b_x32(sc, x[0]);
-            tmem_wait_ld(x[0]);
+          tmem_ld_32x32b_x32(sc, x[0]);
+          tmem_wait_ld(x[0]);
 #pragma unroll
-            for (int i = 0; i < CW; i += 32) {
-              if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
-              if (masked) hide(x[i / 32 & 1], i);
-              top = fmaxf(top, largest(x[i / 32 & 1]));
-              if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
-            }
-          } else {
-            tmem_ld_32x32b_x32(sc, x[0]);
-            tmem_ld_32x32b_x32(sc + 32, x[1]);
-            tmem_wait_ld(x[0]);
-            tmem_wait_ld(x[1]);
-            if (masked) {
-              hide(x[0], 0);
-              hide(x[1], 32);
-            }
-            top = fmaxf(largest(x[0]), largest(x[1]));
+          for (int i = 0; i < CW; i += 32) {
+            if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
+            if (masked) hide(x[i / 32 & 1], i);
+            top = fmaxf(top, largest(x[i / 32 & 1]));
+            if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
+          }
+          if constexpr (!Two) {
             s_max[256 * buf + 128 * half + row] = top;
             if (!(ok = meet())) break;
             top = fmaxf(top, s_max[256 * buf + 128 * (half ^ 1) + row]);
@@ -1032,24 +1066,16 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
               }
             }
           };
-          if constexpr (Two) {
-            // the scores once more: a row's 128 do not fit the registers
-            tmem_ld_32x32b_x32(sc, x[0]);
-            tmem_wait_ld(x[0]);
+          tmem_ld_32x32b_x32(sc, x[0]);
+          tmem_wait_ld(x[0]);
 #pragma unroll
-            for (int i = 0; i < CW; i += 32) {
-              if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
-              if (masked) hide(x[i / 32 & 1], i);
-              uint32_t w[16];
-              weights(x[i / 32 & 1], w);
-              if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
-              tmem_st_32x32b_x16(sc + i / 2, w);
-            }
-          } else {
-            uint32_t w[32];
-            weights(x[0], w);
-            weights(x[1], w + 16);
-            tmem_st_32x32b_x32(sc, w);
+          for (int i = 0; i < CW; i += 32) {
+            if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
+            if (masked) hide(x[i / 32 & 1], i);
+            uint32_t w[16];
+            weights(x[i / 32 & 1], w);
+            if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
+            tmem_st_32x32b_x16(sc + i / 2, w);   // (in the place of scores that are read)
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
@@ -1114,26 +1140,30 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   }
 }
 
-// Joins the parts of the row tiles that CTAs share: block (c, i) takes some rows
-// of the tile that CTA c began. A row has as many warps as 4 parts each need, up
-// to all 8, which take alternate parts and add up through shared memory.
+// Joins the parts of the row tiles that CTAs share: block (c, y) takes some units
+// of the tile that CTA c began, a unit being 8 columns of 32 rows, a row per
+// lane. A unit has as many warps as 4 parts each need, up to all 8, which take
+// alternate parts and add up through shared memory.
 constexpr int kJoinWarps = 8, kJoinBlocks = 16;
 template <int D, int QT>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams p) {
   pdl_begin();
   const AttnShared s = p.shared[blockIdx.x];
   if (s.count == 0) return;
-  constexpr int V = D / 32, U = 4;
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float2 s_ml[kJoinWarps];
+  constexpr int V = 8, U = 4, kRows = 128 * QT;
+  __shared__ float s_o[kJoinWarps][V][32];
+  __shared__ float2 s_ml[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int per = 1;                                   // warps of a row
+  int per = 1;                                   // warps of a unit
   while (per < kJoinWarps && per * U < s.count) per *= 2;
-  const int at_once = kJoinWarps / per, sub = warp % per, rows = s.tokens * p.G;
-  for (int row0 = blockIdx.y * at_once; row0 < rows; row0 += gridDim.y * at_once) {
-    const int row = row0 + warp / per;
-    const bool on = row < rows;
-    const int tok = row / p.G, place_row = tok / p.R * 128 + tok % p.R * p.G + row % p.G;
+  const int at_once = kJoinWarps / per, sub = warp % per;
+  // row blocks: those of the first row tile that have rows, then the second's
+  const int rows0 = min(s.tokens, p.R) * p.G, rows1 = max(s.tokens - p.R, 0) * p.G;
+  const int blocks0 = (rows0 + 31) / 32, units = (blocks0 + (rows1 + 31) / 32) * (D / V);
+  for (int unit0 = blockIdx.y * at_once; unit0 < units; unit0 += gridDim.y * at_once) {
+    const int unit = unit0 + warp / per, rb = unit / (D / V), col = unit % (D / V) * V;
+    const int tile = rb >= blocks0, row = 32 * (tile ? rb - blocks0 : rb) + lane;
+    const bool on = unit < units && row < (tile ? rows1 : rows0);
     float o[V] = {}, m = -INFINITY, l = 0.0f;
     for (int i0 = sub; on && i0 < s.count; i0 += U * per) {
       float x[U][V];
@@ -1144,12 +1174,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams
         ml[u] = make_float2(0.0f, 0.0f);
         if (i < s.count) {
           // (the CTA that began the tile holds its part in its second place)
-          const long long at = (2ll * cta + (cta == (int)blockIdx.x)) * 128 * QT + place_row;
-          ml[u] = p.ml[at];
-          const float* src = p.o + at * D + V * lane;
+          const long long place = 2ll * cta + (cta == (int)blockIdx.x);
+          ml[u] = p.ml[place * kRows + 128 * tile + row];
 #pragma unroll
-          for (int v = 0; v < V; v += 2)
-            *reinterpret_cast<float2*>(&x[u][v]) = *reinterpret_cast<const float2*>(src + v);
+          for (int v = 0; v < V; ++v) x[u][v] = p.o[(place * D + col + v) * kRows + 128 * tile + row];
         }
       }
 #pragma unroll
@@ -1163,29 +1191,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams
       }
     }
     if (per > 1) {
+      __syncthreads();   // the last unit's sums are read
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_o[warp][V * lane + v] = o[v];
-      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      for (int v = 0; v < V; ++v) s_o[warp][v][lane] = o[v];
+      s_ml[warp][lane] = make_float2(m, l);
       __syncthreads();
       if (sub == 0) {
         for (int w = warp + 1; w < warp + per; ++w) {
-          const float2 ml = s_ml[w];
+          const float2 ml = s_ml[w][lane];
           if (ml.y == 0.0f) continue;
           const float mn = fmaxf(m, ml.x), f = ex2(m - mn), g = ex2(ml.x - mn);
           m = mn;
           l = l * f + ml.y * g;
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][V * lane + v] * g;
+          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][v][lane] * g;
         }
       }
-      __syncthreads();
     }
     if (on && sub == 0) {
       const float scale = l == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / l;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.out + (long long)(s.row + tok) * p.a.o_ld +
-                                                  (long long)(s.head * p.G + row % p.G) * D) + V / 2 * lane;
-#pragma unroll
-      for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(o[v] * scale, o[v + 1] * scale);
+      const int tok = s.row + tile * p.R + row / p.G;
+      *reinterpret_cast<uint4*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
+          make_uint4(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale),
+                     pack_bf16x2(o[4] * scale, o[5] * scale), pack_bf16x2(o[6] * scale, o[7] * scale));
     }
   }
 }
@@ -1207,9 +1235,11 @@ template <int D, bool E, bool Two>
 cudaError_t launch(TaParams& p, int num_sms, cudaStream_t st) {
   using Sh = Shape<D, E, Two>;
   p.step = Sh::QT * p.R;
+  p.inv_step = (unsigned)(((1u << 31) + p.step - 1u) / p.step);
   auto kern = tree_attn_kernel<D, E, Two>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Sh::kSmem);
   const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
+  p.inv_ctas = 1.000002f / ctas;
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, st, p);
   if (e == cudaSuccess)
     e = launch_pdl(tree_attn_join<D, Sh::QT>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
