@@ -39,8 +39,8 @@ namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 constexpr int kRawBytes = 128 * 64;         // 128 rows of 64 e4m3
-// warps 0..7 softmax, 8 loads, 9 products, 10..13 conversion (e4m3)
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
+// warps 0..7 softmax, 8 loads, 9 products, 10 the plan, 11..14 conversion (e4m3)
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 10, kConvWarp = 11, kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512, kColS = 256;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kConvWarp);
   static constexpr int kGroupBytes = GC * kSlotBytes;
   static constexpr int kQBytes = QT * NC * kSlotBytes;
-  static constexpr int kMisc = 5120 + (E ? kParts * 512 * QT : 0);
+  static constexpr int kMisc = 5632 + (E ? kParts * 512 * QT : 0);
   static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + kGroups * kGroupBytes + kRaw * kRawBytes;
   static_assert(!Two || D <= 128, "tensor memory holds the sums of two row tiles of 128 columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -369,6 +369,16 @@ struct Walk {
   }
 };
 
+// Page number of the lane-th box of a part's pages from key tile k on: -1 behind
+// the keys, kBadPage for a number outside the cache.
+constexpr int kBadPage = -2;
+__device__ __forceinline__ int first_pages(const TaParams& p, const Part& s, int k, int lane) {
+  const int key = 128 * k + lane * min(1 << p.a.page_shift, 128);
+  if (key >= min(s.keys, 128 * s.k1)) return -1;
+  const int id = __ldcg(p.a.table + (long long)s.b * p.a.table_width + (key >> p.a.page_shift));
+  return id >= 0 && id < p.a.cache.pages ? id : kBadPage;
+}
+
 // Bits of the keys that a row sees among the 64 from node index `a` (key minus
 // context) on; token i of its request, words of its mask or NULL.
 __device__ __forceinline__ unsigned long long low_bits(int n) {
@@ -419,12 +429,50 @@ __device__ __forceinline__ float cache_value(const void* base, long long i) {
 }
 
 // ----------------------------------------------------------------- kernel ---
+// Waits by a whole warp: true once the phase is over, false (and the CTA's abort
+// flag set) when the limit ran out or another role gave up. The part that has to
+// wait is a function of its own, out of the way of the roles' code: that of all
+// of them has to fit the instruction cache together.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, const DevErr* err,
+                                         int site) {
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kWaitSleepNs)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const bool late = globaltimer_ns() - t0 > err->limit_ns;
+    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+      if ((threadIdx.x & 31) == 0 && !*abort_flag) report_timeout(*err, site);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// A place in a ring of N and the parity of its phase.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <int D, bool E, bool Two>
 __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
   using Sh = Shape<D, E, Two>;
   constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, kGroups = Sh::kGroups, kRaw = Sh::kRaw, QB = Sh::QB,
-                OB = Sh::OB, QT = Sh::QT;
+                OB = Sh::OB, QT = Sh::QT, kRaw1 = kRaw ? kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
@@ -451,23 +499,23 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drain = part_empty + kParts;
   Part* parts = reinterpret_cast<Part*>(drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + kParts + 1);
+  int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
   static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 +
                     8 * (2 * kGroups + 2 * kRaw + 3 * QB + 14 + 2 * kParts) + (kParts + 1) * sizeof(Part) +
-                    64 <= Sh::kMisc, "room for barriers");
+                    128 * kParts + 64 <= Sh::kMisc, "room for barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&full[i], E ? kConvWarps * GC : 1);
+      mbar_init(&full[i], E ? GC : 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kConvWarps);
-    }
+#pragma unroll 1
+    for (int i = 0; i < 2 * kRaw; ++i) mbar_init(&raw_full[i], 1);
     for (int i = 0; i < QB; ++i) {
       mbar_init(&q_raw[i], 1);
       mbar_init(&q_full[i], E ? kConvWarps : 1);
@@ -480,8 +528,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       mbar_init(&o_free[i], Two ? kSoftWarps / 2 : kSoftWarps);
     }
     mbar_init(pv_done, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
-    for (int i = 0; i < kParts; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&pair[i], 2);
       mbar_init(&part_full[i], 1);
       mbar_init(&part_empty[i], kSoftWarps);
       s_unbounded[i] = 0;
@@ -501,17 +550,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // A wait of a whole warp. After one that ran out every other wait fails at
-  // once, and each role leaves its loop.
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-    bool ok = mbar_try_wait(bar, parity) ||
-              (!*abort_flag && mbar_wait(bar, parity, abort_flag, p.err.limit_ns));
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {
-      if (lane == 0 && !*abort_flag) report_timeout(p.err, site);
-      *abort_flag = 1;
-    }
-    return ok;
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           wait_longer(smem_u32(bar), parity, abort_flag, &p.err, site);
   };
   pdl_begin();
   // Order of the loads and products. One row tile: the scores run one key tile
@@ -520,49 +561,19 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   // places are left out, so that V of tile u is always group NG (2u + 2)); else
   // the part's last V comes before the next part's K0. Two row tiles: K0 V0 K1 V1.
 
-  if (warp == kLoadWarp) {
-    // ---------------------------------------------------- loads, by TMA
+  if (warp == kPlanWarp) {
+    // ------------------------------------- the CTA's parts, for all others
     Walk walk(p, parts + kParts);
     walk.begin();
-    const int page = 1 << p.a.page_shift, box = min(page, 128), nbox = 128 / box, box_log = 31 - __clz(nbox);
-    const int my_box = box * (lane & (nbox - 1)), my_chunk = lane / nbox;   // (chunk of a group)
-    uint32_t cnt = 0, np = 0, segs = 0;    // groups (e4m3: chunks) loaded, parts told, parts loaded
-    bool ok = true, bad = false;
+    Ring<kParts> at;
     Part s;
-    auto load = [&](const CUtensorMap* m, int h, int k, int id) {
-      const int y = (128 * k + my_box) & (page - 1);
-      if constexpr (E) {
-        for (int c = 0; c < NC && ok; ++c, ++cnt) {
-          const int i = cnt % kRaw;
-          if (!(ok = wait(&raw_empty[i], ((cnt / kRaw) & 1) ^ 1, 2))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&raw_full[i], kRawBytes);
-          __syncwarp();
-          if (lane < nbox) tma_load_4d(raws + i * kRawBytes + my_box * 64, m, 64 * c, y, h, id, &raw_full[i]);
-        }
-      } else {
-        for (int g = 0; g < NG && ok; ++g, ++cnt) {
-          const int i = cnt % kGroups;
-          if (!(ok = wait(&empty[i], ((cnt / kGroups) & 1) ^ 1, 2))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[i], Sh::kGroupBytes);
-          __syncwarp();
-          if (my_chunk < GC)
-            tma_load_4d(groups + i * Sh::kGroupBytes + my_chunk * kSlotBytes + my_box * 128, m,
-                        64 * (g * GC + my_chunk), y, h, id, &full[i]);
-        }
-      }
-    };
-    auto tell = [&]() {   // a part to the other roles
-      if (!(ok = wait(&part_empty[np % kParts], ((np / kParts) & 1) ^ 1, 3))) return;
-      if (lane == 0) parts[np % kParts] = s;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&part_full[np % kParts]);
-      ++np;
-    };
-    bool have = false;      // values not loaded yet: key tile vk of head vh, pages vid
-    int vh = 0, vk = 0, vid = 0;
-    while (ok && walk.next(s)) {
-      if (s.nk == 0) {   // no keys: zeros
+    bool more = true;
+    while (more) {
+      more = walk.next(s);
+      s.stop = !more;
+      if (more && s.nk == 0) {   // no keys: zeros
         const int per_row = D / 8, n = s.tokens * p.G * per_row;
+#pragma unroll 1
         for (int i = lane; i < n; i += 32) {
           const int r = i / per_row, tok = s.row + s.tok0 + r / p.G, head = s.h * p.G + r % p.G;
           *reinterpret_cast<uint4*>(p.a.out + (long long)tok * p.a.o_ld + (long long)head * D + 8 * (i % per_row)) =
@@ -570,150 +581,195 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         }
         continue;
       }
-      const int end_page = (s.keys + page - 1) >> p.a.page_shift;
-      const int32_t* table = p.a.table + (long long)s.b * p.a.table_width;
-      // Page numbers of 32 boxes, one per lane, and of the next 32, read ahead.
-      // Behind the keys, and for numbers outside the cache, the number past its
-      // last page, which reads as zeros.
-      auto numbers = [&](int b) {
-        const int i = ((b + lane) * box) >> p.a.page_shift;
-        return b + lane < (s.k1 << box_log) && i < end_page ? __ldcg(table + i) : -2;
-      };
-      int win = s.k0 << box_log, now = numbers(win), later = numbers(win + 32);
-      if (QB == 1 && have) {
-        load(&p.mv, vh, vk, vid);
-        have = false;
-        if (!ok) break;
-      }
-      tell();
-      const int qb = segs % QB;
-      if (!ok || !(ok = wait(&q_empty[qb], ((segs / QB) & 1) ^ 1, 1))) break;
-      if (elect_one_sync()) {
-        uint64_t* bar = E ? &q_raw[qb] : &q_full[qb];
-        mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
-        for (int q = 0; q < QT; ++q)
-          for (int c = 0; c < NC; ++c)
-            tma_load_3d(sq + qb * Sh::kQBytes + (q * NC + c) * kSlotBytes, &p.mq, 64 * c, s.h * p.G,
-                        s.row + s.tok0 + q * p.R, bar);
-      }
+      const int page = more ? first_pages(p, s, s.k0, lane) : 0;
+      if (!wait(&part_empty[at.i], at.phase ^ 1, 1)) break;
+      s_pages[32 * at.i + lane] = page;
+      if (lane == 0) parts[at.i] = s;
       __syncwarp();
-      ++segs;
-      for (int k = s.k0; k < s.k1 && ok; ++k) {
-        int id = __shfl_sync(0xffffffffu, now, (k << box_log) - win + (lane & (nbox - 1)));
-        if ((k + 1) << box_log == win + 32) {
-          win += 32;
-          now = later;
-          later = numbers(win + 32);
-        }
-        if (id < 0 || id >= p.a.cache.pages) {
-          bad |= id != -2 || (((k << box_log) + (lane & (nbox - 1))) * box) >> p.a.page_shift < end_page;
-          id = p.a.cache.pages;
-        }
-        load(&p.mk, s.h, k, id);
-        if (Two) {
-          if (ok) load(&p.mv, s.h, k, id);
-        } else {
-          if (have && ok) load(&p.mv, vh, vk, vid);
-          have = true;
-          vh = s.h;
-          vk = k;
-          vid = id;
-        }
-      }
+      if (lane == 0) mbar_arrive(&part_full[at.i]);
+      at.step();
     }
-    if (ok) {
-      s.stop = 1;
-      tell();
-      if (have && ok) {
-        if (QB == 2) cnt += E ? 0 : NG;
-        load(&p.mv, vh, vk, vid);
-      }
-    }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
     if (lane == 0) {
       AttnShared m = walk.shared();
       if (*abort_flag) m.count = 0;
       p.shared[blockIdx.x] = m;
     }
-    if (!ok) {   // own copies land before shared memory is released
-      constexpr int kRing = E ? kRaw : kGroups;
-      for (int i = 0; i < kRing; ++i) {
-        const uint32_t uses = (cnt + kRing - 1 - i) / kRing;
-        if (uses) mbar_wait_drain(E ? &raw_full[i] : &full[i], (uses - 1) & 1, p.err.limit_ns);
+  } else if (warp == kLoadWarp) {
+    // ---------------------------------------------------- loads, by TMA
+    const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
+    const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a group)
+    const int y_mask = (1 << p.a.page_shift) - 1;
+    Ring<E ? kRaw1 : kGroups> ring;
+    Ring<QB> qring;
+    Ring<kParts> at;
+    uint32_t loads = 0, segs = 0;
+    bool ok = true, bad = false, stop = false, have = false;
+    int vh = 0, vk = 0, vid = 0;      // values not loaded yet: key tile vk of head vh, pages vid
+    int k = 0, k1 = 0, k0 = 0, win = 0, now = 0, later = 0;
+    Part s;
+    while (ok) {
+      if (k == k1 && !stop) {
+        if (!(ok = wait(&part_full[at.i], at.phase, 2))) break;
+        s = parts[at.i];
+        stop = s.stop;
+        k0 = k = stop ? 0 : s.k0;
+        k1 = stop ? 0 : s.k1;
+        // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
+        win = 0;
+        now = s_pages[32 * at.i + lane];
+        later = stop ? 0 : first_pages(p, s, s.k0 + (32 >> box_log), lane);
+        at.step();
       }
-      for (int i = 0; i < QB; ++i) {
-        const uint32_t uses = (segs + QB - 1 - i) / QB;
-        if (uses) mbar_wait_drain(E ? &q_raw[i] : &q_full[i], (uses - 1) & 1, p.err.limit_ns);
+      const bool go = !stop && !(QB == 1 && !Two && have && k == k0);
+      if (!go && !have) break;
+      int id = 0;
+      if (go) {
+        if (k == k0) {
+          if (!(ok = wait(&q_empty[qring.i], qring.phase ^ 1, 3))) break;
+          if (elect_one_sync()) {
+            uint64_t* bar = E ? &q_raw[qring.i] : &q_full[qring.i];
+            mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
+#pragma unroll 1
+            for (int c = 0; c < QT * NC; ++c)
+              tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * (c % NC), s.h * p.G,
+                          s.row + s.tok0 + c / NC * p.R, bar);
+          }
+          __syncwarp();
+          qring.step();
+          ++segs;
+        }
+        id = __shfl_sync(0xffffffffu, now, ((k - k0) << box_log) - win + my_box);
+        if ((k + 1 - k0) << box_log == win + 32) {
+          win += 32;
+          now = later;
+          later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
+        }
+        bad |= id == kBadPage;
+        if (id < 0) id = p.a.cache.pages;   // reads as zeros
+      } else if (QB == 2 && !E) {
+        for (int g = 0; g < NG; ++g) ring.step();   // (the group that is left out)
+      }
+      // K of this tile; V of the one before, or (Two) of this one
+#pragma unroll 1
+      for (int op = go ? 0 : 1; op < (have || Two ? 2 : 1) && ok; ++op) {
+        const CUtensorMap* m = op ? &p.mv : &p.mk;
+        const int kk = op && !Two ? vk : k, hh = op && !Two ? vh : s.h, page = op && !Two ? vid : id;
+        const int y = (128 * kk + my_box * box) & y_mask;
+#pragma unroll 1
+        for (int g = 0; g < (E ? NC : NG); ++g) {
+          uint64_t* bar = E ? &raw_full[ring.i] : &full[ring.i];
+          if (!(ok = wait(E ? &raw_empty[ring.i] : &empty[ring.i], ring.phase ^ 1, 4))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar, E ? kRawBytes : Sh::kGroupBytes);
+          __syncwarp();
+          if (my_chunk < (E ? 1 : GC))
+            tma_load_4d(E ? raws + ring.i * kRawBytes + my_box * box * 64
+                          : groups + ring.i * Sh::kGroupBytes + my_chunk * kSlotBytes + my_box * box * 128,
+                        m, 64 * (E ? g : g * GC + my_chunk), y, hh, page, bar);
+          ring.step();
+          ++loads;
+        }
+      }
+      have = go && !Two;
+      vh = s.h;
+      vk = k;
+      vid = id;
+      k += go;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
+    if (!ok) {
+      // own copies land before shared memory is released: each place's last load
+      constexpr int kRing = E ? kRaw1 : kGroups;
+      const uint32_t n = min(loads, (uint32_t)kRing);
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint32_t i = (ring.i + kRing - 1 - j) % kRing, parity = i < ring.i ? ring.phase : ring.phase ^ 1;
+        mbar_wait_drain(E ? &raw_full[i] : &full[i], parity, p.err.limit_ns);
+      }
+      for (uint32_t j = 0; j < min(segs, (uint32_t)QB); ++j) {
+        const uint32_t i = (qring.i + QB - 1 - j) % QB, parity = i < qring.i ? qring.phase : qring.phase ^ 1;
+        mbar_wait_drain(E ? &q_raw[i] : &q_full[i], parity, p.err.limit_ns);
       }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- products
     constexpr uint32_t kIdS = idesc_16(!E, 128, false), kIdO = idesc_16(!E, 64 * GC, true);
-    const uint32_t q_addr = smem_u32(sq), g_addr = smem_u32(groups);
-    uint32_t cnt = 0, segs = 0, u = 0;
+    const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), gd0 = smem_desc_sw128(smem_u32(groups));
+    const uint64_t vd0 = value_desc(smem_u32(groups));
+    Ring<kGroups> ring;
+    Ring<QB> qring;
+    Ring<kParts> at;
+    uint32_t segs = 0, u = 0;
     bool ok = true;
-    // scores of key tile in the groups from cnt on, row tile at `q`, into S buffer `buf`
-    auto scores = [&](uint32_t q, int buf, bool wait_keys, bool free_keys) {
-      for (int g = 0; g < NG && ok; ++g) {
-        const int i = (cnt + g) % kGroups;
-        if (wait_keys && !(ok = wait(&full[i], ((cnt + g) / kGroups) & 1, 4))) break;
+    // Scores of the key tile in the groups from r on (keys waited for, and given
+    // back, if asked), row tile q's queries at descriptor qd, into S buffer `buf`.
+    auto scores = [&](Ring<kGroups> r, uint64_t qd, int buf, bool wait_keys, bool free_keys) {
+#pragma unroll 1
+      for (int g = 0; g < NG; ++g, r.step()) {
+        if (wait_keys && !(ok = wait(&full[r.i], r.phase, 5))) break;
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint64_t qd = smem_desc_sw128(q + g * Sh::kGroupBytes);
-          const uint64_t kd = smem_desc_sw128(g_addr + i * Sh::kGroupBytes);
+          const uint64_t a = qd + g * (Sh::kGroupBytes / 16), b = gd0 + r.i * (Sh::kGroupBytes / 16);
 #pragma unroll
           for (int c = 0; c < GC; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss(tmem + kColS + 128 * buf, qd + (c * kSlotBytes + 32 * kk) / 16,
-                         kd + (c * kSlotBytes + 32 * kk) / 16, kIdS, (g | c | kk) != 0);
-          if (free_keys) mma_commit(&empty[i]);
+              mma_f16_ss(tmem + kColS + 128 * buf, a + (c * kSlotBytes + 32 * kk) / 16,
+                         b + (c * kSlotBytes + 32 * kk) / 16, kIdS, g != 0 || (c | kk) != 0);
+          if (free_keys) mma_commit(&empty[r.i]);
           if (g == NG - 1) mma_commit(&s_full[buf]);
         }
         __syncwarp();
       }
     };
-    // O (+)= P V with the values in the groups from cnt on
-    auto values = [&](uint32_t o, int buf, bool first, uint64_t* done, bool wait_values, bool free_values) {
-      for (int g = 0; g < NG && ok; ++g) {
-        const int i = (cnt + g) % kGroups;
-        if (wait_values && !(ok = wait(&full[i], ((cnt + g) / kGroups) & 1, 5))) break;
+    // O (+)= P V with the values in the groups from r on.
+    auto values = [&](Ring<kGroups> r, uint32_t o, int buf, bool first, uint64_t* done, bool wait_values,
+                      bool free_values) {
+#pragma unroll 1
+      for (int g = 0; g < NG; ++g, r.step()) {
+        if (wait_values && !(ok = wait(&full[r.i], r.phase, 6))) break;
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint64_t vd = value_desc(g_addr + i * Sh::kGroupBytes);
+          const uint64_t b = vd0 + r.i * (Sh::kGroupBytes / 16);
           const uint32_t pc = tmem + kColS + 128 * buf;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
-            mma_f16_ts(o + 64 * GC * g, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)),
-                       vd + (2048 >> 4) * kk, kIdO, !first || kk);
-          if (free_values) mma_commit(&empty[i]);
+            mma_f16_ts(o + 64 * GC * g, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)), b + (2048 >> 4) * kk,
+                       kIdO, !first || kk != 0);
+          if (free_values) mma_commit(&empty[r.i]);
           if (g == NG - 1 && done) mma_commit(done);
         }
         __syncwarp();
       }
     };
+    auto skip = [&](Ring<kGroups>& r) {
+      for (int g = 0; g < NG; ++g) r.step();
+    };
     if constexpr (Two) {
-      for (uint32_t np = 0; ok; ++np) {
-        if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
-        const Part& s = parts[np % kParts];
-        if (s.stop) break;
-        const int n = s.k1 - s.k0;
-        if (!(ok = wait(q_full, segs & 1, 7))) break;
-        scores(q_addr, 0, true, false);
-        if (ok) scores(q_addr + NC * kSlotBytes, 1, false, true);
-        for (int t = 0; t < n && ok; ++t, ++u) {
-          // (groups: K(t) at cnt, V(t), K(t + 1))
-          for (int q = 0; q < 2 && ok; ++q) {
-            if (!(ok = wait(&p_full[q], u & 1, 8))) break;
-            if (t == 0 && !(ok = wait(&o_free[q], (segs & 1) ^ 1, 9))) break;
-            cnt += NG;
-            values(tmem + 128 * q, q, t == 0, t + 1 == n ? &o_full[q] : nullptr, q == 0, q == 1);
-            cnt += NG;
-            if (t + 1 < n && ok) scores(q_addr + q * NC * kSlotBytes, q, q == 0, q == 1);
-            cnt -= 2 * NG;
+      while (ok) {
+        if (!(ok = wait(&part_full[at.i], at.phase, 7))) break;
+        if (parts[at.i].stop) break;
+        const int n = parts[at.i].k1 - parts[at.i].k0;
+        at.step();
+        if (!(ok = wait(q_full, segs & 1, 8))) break;
+#pragma unroll 1
+        for (int t = -1; t < n && ok; ++t) {
+          // ring: V(t), if t is one, and K(t + 1) behind it
+          Ring<kGroups> keys = ring;
+          if (t >= 0) skip(keys);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            if (t >= 0) {
+              if (!(ok = wait(&p_full[q], u & 1, 9))) break;
+              if (t == 0 && !(ok = wait(&o_free[q], (segs & 1) ^ 1, 10))) break;
+              values(ring, tmem + 128 * q, q, t == 0, t + 1 == n ? &o_full[q] : nullptr, q == 0, q == 1);
+              if (!ok) break;
+            }
+            if (t + 1 < n) scores(keys, qd0 + q * (NC * kSlotBytes / 16), q, q == 0, q == 1);
+            if (!ok) break;
           }
-          cnt += 2 * NG;
-          if (t + 2 == n || n == 1) {
+          ring = keys;
+          if (t + 1 < n) skip(ring);
+          u += t >= 0;
+          if (t + 2 == n) {
             if (elect_one_sync()) mma_commit(q_empty);
             __syncwarp();
           }
@@ -721,42 +777,43 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         ++segs;
       }
     } else {
-      bool have = false, first = false;    // key tile u - 1's values are to be added
-      int vob = 0;
-      auto add_values = [&](bool last) {
-        const uint32_t v = u - 1;
-        if (!(ok = wait(&p_full[v & 1], (v >> 1) & 1, 8))) return;
-        const int ob = vob % OB;
-        if (first && !(ok = wait(&o_free[ob], ((vob / OB) & 1) ^ 1, 9))) return;
-        values(tmem + 128 * ob, v & 1, first, last ? &o_full[ob] : pv_done, true, true);
-        cnt += NG;
-        have = false;
-      };
-      for (uint32_t np = 0; ok; ++np) {
-        if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
-        const Part& s = parts[np % kParts];
-        if (s.stop) break;
-        const int n = s.k1 - s.k0, qb = segs % QB;
-        if (QB == 1 && have) add_values(true);
-        if (!ok || !(ok = wait(&q_full[qb], (segs / QB) & 1, 7))) break;
-        for (int t = 0; t < n && ok; ++t) {
-          scores(q_addr + qb * Sh::kQBytes, u & 1, true, true);
-          cnt += NG;
-          if (t + 1 == n) {
-            if (elect_one_sync()) mma_commit(&q_empty[qb]);
-            __syncwarp();
-          }
-          if (have && ok) add_values(t == 0);
-          have = true;
-          first = t == 0;
-          vob = segs;
-          ++u;
+      bool have = false, first = false, stop = false;   // key tile u - 1's values are to be added
+      int t = 0, n = 0;
+      uint32_t vob = 0;
+      while (ok) {
+        if (t == n && !stop) {
+          if (!(ok = wait(&part_full[at.i], at.phase, 7))) break;
+          stop = parts[at.i].stop;
+          n = stop ? 0 : parts[at.i].k1 - parts[at.i].k0;
+          t = 0;
+          at.step();
         }
-        ++segs;
-      }
-      if (have && ok) {
-        if (QB == 2) cnt += NG;
-        add_values(true);
+        const bool go = !stop && !(QB == 1 && have && t == 0);
+        if (!go && !have) break;
+        if (go) {
+          if (t == 0 && !(ok = wait(&q_full[qring.i], qring.phase, 8))) break;
+          scores(ring, qd0 + qring.i * (Sh::kQBytes / 16), u & 1, true, true);
+          if (!ok) break;
+          if (t + 1 == n) {
+            if (elect_one_sync()) mma_commit(&q_empty[qring.i]);
+            __syncwarp();
+            qring.step();
+          }
+        }
+        if (go || QB == 2) skip(ring);
+        if (have) {
+          const uint32_t v = u - 1, ob = vob % OB;
+          if (!(ok = wait(&p_full[v & 1], (v >> 1) & 1, 9))) break;
+          if (first && !(ok = wait(&o_free[ob], ((vob / OB) & 1) ^ 1, 10))) break;
+          values(ring, tmem + 128 * ob, v & 1, first, !go || t == 0 ? &o_full[ob] : pv_done, true, true);
+          skip(ring);
+        }
+        have = go;
+        first = t == 0;
+        vob = segs;
+        u += go;
+        t += go;
+        if (go && t == n) ++segs;
       }
     }
     if (elect_one_sync()) mma_commit(drain);
@@ -767,114 +824,132 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     // row times the power of two that brings its largest element to 2^14..2^15
     // (elements below 2^-31 of that one lose bits), which its scores undo
     const int w = warp - kConvWarp, tid = 32 * w + lane;
-    uint32_t raw = 0, grp = 0, segs = 0, u = 0;
+    // chunks loaded before the tile at hand, and their places in the operand ring
+    uint32_t raw = 0, chunk = 0;
     int vk = 0, vseen = 0, vkeys = 0;      // the key tile whose values come next, and of which part
-    uint32_t vpart = 0;
-    bool ok = true;
-    // one key tile's keys or values; of values of a tile that not every row sees
-    // whole, what some row must not see is cleared: keys past the row tile's own,
-    // and what is no number (row r of the tile is key first + r)
-    auto convert = [&](bool clear, int first, int seen, int keys, uint32_t part) {
-      bool any = false;
-      for (int c = 0; c < NC && ok; ++c, ++raw) {
-        const int ri = raw % max(kRaw, 1), gi = grp % kGroups;
-        if (!(ok = wait(&raw_full[ri], (raw / max(kRaw, 1)) & 1, 10))) break;
-        const uint8_t* src = raws + ri * kRawBytes;
-        constexpr int kThr = 32 * kConvWarps, kPer = 512 / kThr;   // 16-byte pieces per thread
-        uint4 x[kPer];
+    uint32_t vpart = 0, np = 0;
+    Ring<QB> qring;
+    Ring<kParts> at;
+    bool ok = true, stop = false, have = false;
+    int t = 0, n = 0, seen = 0;
+    Part s;
+    while (ok) {
+      if (t == n && !stop) {
+        if (!(ok = wait(&part_full[at.i], at.phase, 11))) break;
+        s = parts[at.i];
+        stop = s.stop;
+        n = stop ? 0 : s.k1 - s.k0;
+        t = 0;
+        if (!stop) {
+          seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+          if (!(ok = wait(&q_raw[qring.i], qring.phase, 12))) break;
+#pragma unroll 1
+          for (int q = 0; q < QT; ++q) {   // 8 threads to a row
+            const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
+              const int r = r0 + (tid >> 3);
+              uint8_t* line = sq + qring.i * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
+              uint4 x[NC];
+              uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 16 * (kThr * i + tid));
-        if (c % GC == 0 && !(ok = wait(&empty[gi], ((grp / kGroups) & 1) ^ 1, 11))) break;
-        uint8_t* dst = groups + gi * Sh::kGroupBytes + (c % GC) * kSlotBytes;
+              for (int c = 0; c < NC; ++c) {
+                x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
+                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int id = kThr * i + tid, row = id >> 2, piece = 2 * (id & 3);
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t o[8];
+                for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
+              }
+#pragma unroll
+              for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+              // exponent of the largest element, within what keeps both factors normal
+              const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
+              const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
+                  v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+              if ((tid & 7) == 0) s_qs[at.i * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[qring.i]);
+          qring.step();
+        }
+        at.step();
+        ++np;
+      }
+      const bool go = !stop && !(QB == 1 && !Two && have && t == 0);
+      if (!go && !have) break;
+      if (Two) {
+        vk = s.k0 + t;
+        vseen = seen;
+        vkeys = s.keys;
+        vpart = np - 1;
+      }
+      if (!go && QB == 2) chunk += NC;   // (the group that is left out)
+      // K of this tile; V of the one before, or (Two) of this one. Every chunk by
+      // one of the warps in turn: by all of them it would pay for its waits and
+      // barriers four times.
+      const int end = have || Two ? 2 * NC : NC;
+#pragma unroll 1
+      for (int c = go ? 0 : NC; c < end; ++c, ++raw, ++chunk) {
+        if (raw % kConvWarps != (uint32_t)w) continue;
+        const int ri = raw % kRaw1, gi = chunk / GC % kGroups;
+        if (!(ok = wait(&raw_full[ri], (raw / kRaw1) & 1, 13))) break;
+        if (!(ok = wait(&empty[gi], ((chunk / GC / kGroups) & 1) ^ 1, 14))) break;
+        const uint8_t* src = raws + ri * kRawBytes + 16 * lane;
+        // piece i of the lane: row 8 i + lane / 4, 16 columns
+        uint8_t* dst = groups + gi * Sh::kGroupBytes + chunk % GC * kSlotBytes + 128 * (lane >> 2);
+        const int p0 = 16 * ((2 * (lane & 3)) ^ (lane >> 2)), p1 = 16 * ((2 * (lane & 3) + 1) ^ (lane >> 2));
+#pragma unroll 1
+        for (int i = 0; i < 16; i += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 512 * (i + j));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[2 * j] = e4m3x2_f16x2(v[j]);
-            o[2 * j + 1] = e4m3x2_f16x2(v[j] >> 16);
+            const uint4 y = x[j];
+            *reinterpret_cast<uint4*>(dst + 1024 * (i + j) + p0) =
+                make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16), e4m3x2_f16x2(y.y), e4m3x2_f16x2(y.y >> 16));
+            *reinterpret_cast<uint4*>(dst + 1024 * (i + j) + p1) =
+                make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16), e4m3x2_f16x2(y.w), e4m3x2_f16x2(y.w >> 16));
           }
-          uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-          if (clear && first + row >= seen) {
-            if (first + row >= keys) a = b = make_uint4(0, 0, 0, 0);
-            any |= clear_unbounded<true>(a);
-            any |= clear_unbounded<true>(b);
-          }
-          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * (piece ^ (row & 7))) = a;
-          *reinterpret_cast<uint4*>(dst + 128 * row + 16 * ((piece + 1) ^ (row & 7))) = b;
         }
-        if (any) s_unbounded[part % kParts] = (int)part + 1;
+        if (c >= NC && 128 * (vk + 1) > vseen) {
+          // values of a tile that not every row sees whole: what some row must
+          // not see is cleared, keys past the row tile's own, and what is no number
+          bool any = false;
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) {
+            uint4* y = reinterpret_cast<uint4*>(dst + 512 * (i & ~1) + (i & 1 ? p1 : p0));
+            const int key = 128 * vk + 8 * (i >> 1) + (lane >> 2);
+            if (key < vseen) continue;
+            uint4 v = key < vkeys ? *y : make_uint4(0, 0, 0, 0);
+            any |= clear_unbounded<true>(v);
+            *y = v;
+          }
+          if (any) s_unbounded[vpart % kParts] = (int)vpart + 1;
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&full[gi]);
           mbar_arrive(&raw_empty[ri]);
         }
-        if (c % GC == GC - 1) ++grp;
       }
-    };
-    for (uint32_t np = 0; ok; ++np) {
-      if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
-      const Part s = parts[np % kParts];
-      if (s.stop) break;
-      const int n = s.k1 - s.k0, qb = segs % QB;
-      if (!(ok = wait(&q_raw[qb], (segs / QB) & 1, 12))) break;
-      for (int q = 0; q < QT; ++q) {   // 8 threads to a row
-        const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
-        for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
-          const int r = r0 + (tid >> 3);
-          uint8_t* line = sq + qb * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
-          uint4 x[NC];
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
-            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
-          }
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          // exponent of the largest element, within what keeps both factors normal
-          const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
-          const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
-              v[j] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
-            *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          if ((tid & 7) == 0)
-            s_qs[(np % kParts) * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
-      ++segs;
-      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-      auto keys_in = [&]() { convert(false, 0, 0, 0, 0); };
-      auto values_in = [&]() { convert(128 * (vk + 1) > vseen, 128 * vk, vseen, vkeys, vpart); };
-      for (int t = 0; t < n && ok; ++t, ++u) {
-        keys_in();
-        if (!Two && ok && (QB == 1 ? t > 0 : u > 0)) values_in();
-        vk = s.k0 + t;
-        vseen = seen;
-        vkeys = s.keys;
-        vpart = np;
-        if (Two && ok) values_in();
-      }
-      if (QB == 1 && !Two && ok) values_in();
-    }
-    if (QB == 2 && u && ok) {
-      grp += NG;
-      convert(128 * (vk + 1) > vseen, 128 * vk, vseen, vkeys, vpart);
+      have = go && !Two;
+      vk = s.k0 + t;
+      vseen = seen;
+      vkeys = s.keys;
+      vpart = np - 1;
+      t += go;
     }
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------- softmax, output
@@ -885,138 +960,92 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     const int q0 = Two ? half * p.R : 0, oc0 = Two ? 0 : half * OW;
     const int row_tok = q0 + row / p.G, row_g = row % p.G;   // token of the part, query head of the group
     uint32_t np = 0, segs = 0, u = 0, base = 0, pvs = 0, pairs = 0;
-    bool ok = true;
+    Ring<kParts> at;
+    bool ok = true, stop = false, have = false;   // have: the part before is to be finished
+    float last_m = 0.0f, last_l = 0.0f, m = 0.0f, l = 0.0f, c2 = 0.0f;
+    int t = 0, n = 0, seen = 0, tok = 0, k0 = 0;
+    bool live = false, work = false;
     // exchange between the two warps of a lane quarter (One)
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&pair[quarter]);
-      return wait(&pair[quarter], pairs++ & 1, 14);
+      return wait(&pair[quarter], pairs++ & 1, 15);
     };
-    // the sums of part `part`, the seg-th with keys
-    auto finish = [&](uint32_t part, uint32_t seg, float m, float l) {
-      const Part s = parts[part % kParts];
-      const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
-      const bool live = row < rows;
-      const int tok = s.tok0 + row_tok, head = s.h * p.G + row_g;
-      if (!(ok = wait(&o_full[ob], (Two ? seg : seg / OB) & 1, 13))) return;
-      tc_fence_after();
-      if (32 * quarter < rows) {
-        if (!Two) {
-          s_sum[128 * half + row] = l;
-          if (!(ok = meet())) return;
-          l += s_sum[128 * (half ^ 1) + row];
+    while (ok) {
+      if (t == n && !stop) {
+        if (!(ok = wait(&part_full[at.i], at.phase, 16))) break;
+        const Part& s = parts[at.i];
+        stop = s.stop;
+        if (!stop) {
+          base += 2 * n * NG;
+          k0 = s.k0;
+          n = s.k1 - k0;
+          t = 0;
+          tok = s.tok0 + row_tok;
+          const int rows = max(min(s.tokens - q0, p.R), 0) * p.G;
+          live = row < rows;
+          work = 32 * quarter < rows;
+          // keys before `seen` are seen by every row
+          seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+          // scores in log2
+          c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
+          m = -INFINITY;
+          l = 0.0f;
+          ++np;
+          at.step();
         }
-        const bool whole = s.k0 == 0 && s.k1 == s.nk;
-        const float inv = whole ? (l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / l) : 1.0f;
-        const bool fix = s_unbounded[part % kParts] == (int)part + 1;
-        const int at = (s.place * QT + (Two ? half : 0)) * 128 + row;   // in scratch
-        uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)head * D + oc0;
-        const uint32_t oc = tmem + lanes + 128 * ob + oc0;
-        const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1, end = min(s.keys, 128 * s.k1);
-        const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
-#pragma unroll 1
-        for (int i = 0; i < OW; i += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(oc + i, o);
-          tmem_wait_ld(o);
-          if (!live) continue;
-          if (fix) {
-            for (int j = max(seen, 128 * s.k0); j < end; ++j) {
-              if (!(seen_bits(j - s.ctx, tok, words, p.a.mask_words) & 1)) continue;
-              const int id = p.a.table[(long long)s.b * p.a.table_width + (j >> p.a.page_shift)];
-              if (id < 0 || id >= p.a.cache.pages) continue;
-              const long long e = ((((long long)id * p.a.kv_heads + s.h) << p.a.page_shift) +
-                                   (j & ((1 << p.a.page_shift) - 1))) * D + oc0 + i;
-#pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                const float v = cache_value<E>(p.a.cache.v, e + q);
-                if (!(fabsf(v) < INFINITY)) o[q] = __float_as_uint(__uint_as_float(o[q]) + v);
-              }
-            }
-          }
-          if (whole) {
-#pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack_bf16x2(__uint_as_float(o[q + 2 * j]) * inv, __uint_as_float(o[q + 2 * j + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + i + q) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            float* dst = p.o + ((long long)s.place * D + oc0 + i) * (128 * QT) + (Two ? 128 * half : 0) + row;
-#pragma unroll
-            for (int q = 0; q < 32; ++q) dst[q * 128 * QT] = __uint_as_float(o[q]);
-          }
-        }
-        if (!whole && live && (Two || half == 0)) p.ml[at] = make_float2(m == -INFINITY ? 0.0f : m, l);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&o_free[ob]);
-        mbar_arrive(&part_empty[part % kParts]);
-      }
-    };
-    bool have = false;          // the part before is to be finished
-    uint32_t last_part = 0;
-    float last_m = 0.0f, last_l = 0.0f;
-    for (; ok; ++np) {
-      if (!(ok = wait(&part_full[np % kParts], (np / kParts) & 1, 6))) break;
-      const Part s = parts[np % kParts];
-      if (s.stop) break;
-      const int n = s.k1 - s.k0, rows = max(min(s.tokens - q0, p.R), 0) * p.G;
-      const bool live = row < rows, work = 32 * quarter < rows;
-      const int tok = s.tok0 + row_tok;
-      const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
-      // keys before `seen` are seen by every row
-      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-      // scores in log2; with fp16 weights the reference is 2^7 below the maximum
-      float c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
-      float m = -INFINITY, l = 0.0f;
-      for (int t = 0; t < n && ok; ++t, ++u) {
-        const int k = s.k0 + t, buf = Two ? half : u & 1;
+      if (stop && !have) break;
+      const uint32_t part = np - 1, pi = part % kParts;   // the part at hand
+      if (!stop) {
+        const int k = k0 + t, buf = Two ? half : u & 1;
         const bool masked = 128 * (k + 1) > seen;
         const uint32_t sc = tmem + lanes + kColS + 128 * buf + (Two ? 0 : 64 * half);
-        unsigned long long vis[CW / 64];
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < CW / 64; ++i)
-            vis[i] = live ? seen_bits(128 * k + (Two ? 64 * i : 64 * half) - s.ctx, tok, words, p.a.mask_words) : 0;
-        }
-        if (!(ok = wait(&s_full[buf], (Two ? u : u >> 1) & 1, 15))) break;
+        if (!(ok = wait(&s_full[buf], (Two ? u : u >> 1) & 1, 17))) break;
         tc_fence_after();
-        if (E && t == 0) c2 = fmaxf(c2 * s_qs[(np % kParts) * 128 * QT + (Two ? 128 * half : 0) + row], 1e-37f);
+        if (E && t == 0) c2 = fmaxf(c2 * s_qs[pi * 128 * QT + (Two ? 128 * half : 0) + row], 1e-37f);
         if (work) {
-          // 32 scores from column i on, hidden ones -inf
-          auto hide = [&](uint32_t (&x)[32], int i) {
-            const uint32_t v = (uint32_t)(vis[i >> 6] >> (i & 32));
+          uint32_t x[2][32];
+          if (masked) {
+            // hidden scores are set to -inf in place
+            const unsigned long long* words =
+                p.a.mask ? p.a.mask + (long long)(parts[pi].row + tok) * p.a.mask_words : nullptr;
+            const int first = 128 * k + (Two ? 0 : 64 * half) - parts[pi].ctx;
+#pragma unroll 1
+            for (int i = 0; i < CW; i += 32) {
+              const uint32_t v = live ? (uint32_t)seen_bits(first + i, tok, words, p.a.mask_words) : 0;
+              if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
+              tmem_ld_32x32b_x32(sc + i, x[0]);
+              tmem_wait_ld(x[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(v >> j & 1)) x[j] = 0xff800000u;
-          };
-          auto largest = [&](const uint32_t (&x)[32]) {
+              for (int j = 0; j < 32; ++j)
+                if (!(v >> j & 1)) x[0][j] = 0xff800000u;
+              tmem_st_32x32b_x32(sc + i, x[0]);
+            }
+            tmem_wait_st();
+          }
+          auto largest = [&](const uint32_t (&y)[32]) {
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              a = fmaxf(a, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
-              b = fmaxf(b, fmaxf(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])));
+              a = fmaxf(a, fmaxf(__uint_as_float(y[j]), __uint_as_float(y[j + 1])));
+              b = fmaxf(b, fmaxf(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])));
             }
             return fmaxf(a, b);
           };
           // the scores are read twice, 32 at a time: 64 or 128 of them beside their
           // weights would not fit the registers
-          uint32_t x[2][32];
           float top = -INFINITY;
           tmem_ld_32x32b_x32(sc, x[0]);
           tmem_wait_ld(x[0]);
 #pragma unroll
-          for (int i = 0; i < CW; i += 32) {
-            if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
-            if (masked) hide(x[i / 32 & 1], i);
-            top = fmaxf(top, largest(x[i / 32 & 1]));
-            if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
+          for (int i = 0; i < CW; i += 64) {
+            tmem_ld_32x32b_x32(sc + i + 32, x[1]);
+            top = fmaxf(top, largest(x[0]));
+            tmem_wait_ld(x[1]);
+            tmem_ld_32x32b_x32(sc + (i + 64) % CW, x[0]);   // (at the end the first again, for the weights)
+            top = fmaxf(top, largest(x[1]));
+            tmem_wait_ld(x[0]);
           }
           if constexpr (!Two) {
             s_max[256 * buf + 128 * half + row] = top;
@@ -1033,28 +1062,30 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             // One: they came after the one before it, so only the last one's
             // phase of pv_done can be open.
             if (!Two) {
-              if (!(ok = wait(pv_done, (pvs - 1) & 1, 16))) break;
+              if (!(ok = wait(pv_done, (pvs - 1) & 1, 18))) break;
               tc_fence_after();
             }
             const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
             const uint32_t oc = tmem + lanes + 128 * (Two ? half : (int)(segs % OB)) + oc0;
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < OW; i += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(oc + i, o);
-              tmem_wait_ld(o);
+              tmem_ld_32x32b_x32(oc + i, x[1]);
+              tmem_wait_ld(x[1]);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_32x32b_x32(oc + i, o);
+              for (int j = 0; j < 32; ++j) x[1][j] = __float_as_uint(__uint_as_float(x[1][j]) * f);
+              tmem_st_32x32b_x32(oc + i, x[1]);
             }
           }
+          // with fp16 weights the reference is 2^7 below the maximum, which keeps
+          // small ones of long contexts above fp16's smallest
           const float ref = (E ? 7.0f : 0.0f) - (m == -INFINITY ? 0.0f : m);
           float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-          auto weights = [&](const uint32_t (&x)[32], uint32_t* w) {
+          auto weights = [&](const uint32_t (&y)[32], int i) {
+            uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              float2 a = fma2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), c2, ref);
+              float2 a = fma2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]), c2, ref);
               a.x = ex2(a.x);
               a.y = ex2(a.y);
               sum[j & 1] = add2(sum[j & 1], a);
@@ -1065,17 +1096,18 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
                 w[j] = pack_bf16x2(a.x, a.y);
               }
             }
-          };
-          tmem_ld_32x32b_x32(sc, x[0]);
-          tmem_wait_ld(x[0]);
-#pragma unroll
-          for (int i = 0; i < CW; i += 32) {
-            if (i + 32 < CW) tmem_ld_32x32b_x32(sc + i + 32, x[(i / 32 + 1) & 1]);
-            if (masked) hide(x[i / 32 & 1], i);
-            uint32_t w[16];
-            weights(x[i / 32 & 1], w);
-            if (i + 32 < CW) tmem_wait_ld(x[(i / 32 + 1) & 1]);
             tmem_st_32x32b_x16(sc + i / 2, w);   // (in the place of scores that are read)
+          };
+#pragma unroll
+          for (int i = 0; i < CW; i += 64) {
+            tmem_ld_32x32b_x32(sc + i + 32, x[1]);
+            tmem_wait_ld(x[1]);
+            weights(x[0], i);
+            if (i + 64 < CW) {
+              tmem_ld_32x32b_x32(sc + i + 64, x[0]);
+              tmem_wait_ld(x[0]);
+            }
+            weights(x[1], i + 32);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
@@ -1084,54 +1116,123 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           // values that some row must not see: keys past the row tile's own are
           // nobody's, others only where they are no numbers. (Two: both groups
           // of warps clear all of them, with the same result.)
-          if (D == 256 && t > 0 && !(ok = wait(pv_done, (pvs - 1) & 1, 17))) break;
-          const int key = threadIdx.x & 127, j = 128 * k + key;
-          const uint32_t at = Two ? base + NG * (2 * t + 1)
-                              : QB == 2 ? NG * (2 * u + 2)
-                                        : base + NG * (t + 1 < n ? 2 * t + 2 : 2 * n - 1);
+          if (D == 256 && t > 0 && !(ok = wait(pv_done, (pvs - 1) & 1, 19))) break;
+          const int key = threadIdx.x & 127, j = 128 * k + key, keys = parts[pi].keys;
+          const uint32_t place = Two ? base + NG * (2 * t + 1)
+                                 : QB == 2 ? NG * (2 * u + 2)
+                                           : base + NG * (t + 1 < n ? 2 * t + 2 : 2 * n - 1);
           bool any = false;
-          for (int g = 0; g < NG && ok; ++g) {
-            const uint32_t i = (at + g) % kGroups;
-            if (!(ok = wait(&full[i], ((at + g) / kGroups) & 1, 18))) break;
+#pragma unroll 1
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t i = (place + g) % kGroups;
+            if (!(ok = wait(&full[i], ((place + g) / kGroups) & 1, 20))) break;
             if (j < seen) continue;
-            for (int c = 0; c < GC; ++c) {
-              uint4* v = reinterpret_cast<uint4*>(groups + i * Sh::kGroupBytes + c * kSlotBytes + 128 * key);
-#pragma unroll
-              for (int q = 0; q < CW / 16; ++q) {
-                uint4* piece = v + ((Two ? q : 4 * half + q) ^ (key & 7));
-                uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
-                const bool un = clear_unbounded<false>(y);
-                if (un || j >= s.keys) *piece = y;
-                any |= un;
-              }
+#pragma unroll 1
+            for (int q = Two ? 0 : 4 * half; q < GC * 8; q += !Two && (q & 3) == 3 ? 5 : 1) {
+              // piece q % 8 of chunk q / 8; One: half of each chunk's pieces
+              uint4* piece = reinterpret_cast<uint4*>(groups + i * Sh::kGroupBytes + (q >> 3) * kSlotBytes + 128 * key) +
+                             ((q & 7) ^ (key & 7));
+              uint4 y = j < keys ? *piece : make_uint4(0, 0, 0, 0);
+              const bool un = clear_unbounded<false>(y);
+              if (un || j >= keys) *piece = y;
+              any |= un;
             }
           }
-          if (any) s_unbounded[np % kParts] = (int)np + 1;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (!ok) break;
+          if (any) s_unbounded[pi] = (int)np;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
-        if (t + 1 < n) ++pvs;   // this tile's product, as pv_done counts it
-        if (t == 0 && have) {
-          // the part before: its last product ran while these weights were made
-          have = false;
-          finish(last_part, segs - 1, last_m, last_l);
+        ++t;
+        ++u;
+        if (t < n) ++pvs;   // this tile's product, as pv_done counts it
+      }
+      // The sums of a part: Two, when its last weights are made; One, only after
+      // the next part's first ones, while its last product runs.
+      if (Two && !stop && t == n) {
+        have = true;
+        last_m = m;
+        last_l = l;
+        ++segs;
+      }
+      if (have && (Two || stop || t == 1)) {
+        have = false;
+        const uint32_t fp = Two || stop ? part : part - 1, seg = segs - 1;
+        const Part& s = parts[fp % kParts];
+        const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
+        if (!(ok = wait(&o_full[ob], (Two ? seg : seg / OB) & 1, 21))) break;
+        tc_fence_after();
+        if (32 * quarter < rows) {
+          if (!Two) {
+            s_sum[128 * half + row] = last_l;
+            if (!(ok = meet())) break;
+            last_l += s_sum[128 * (half ^ 1) + row];
+          }
+          const bool whole = s.k0 == 0 && s.k1 == s.nk, mine = row < rows;
+          const float inv = whole ? (last_l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / last_l) : 1.0f;
+          const int ftok = s.tok0 + row_tok, srow = (Two ? 128 * half : 0) + row;   // row in scratch
+          uint16_t* out = p.a.out + (long long)(s.row + ftok) * p.a.o_ld + (long long)(s.h * p.G + row_g) * D + oc0;
+          float* dst = p.o + ((long long)s.place * D + oc0) * (128 * QT) + srow;
+          const uint32_t oc = tmem + lanes + 128 * ob + oc0;
+          const bool fix = s_unbounded[fp % kParts] == (int)fp + 1;
+#pragma unroll 1
+          for (int i = 0; i < OW; i += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(oc + i, o);
+            tmem_wait_ld(o);
+            if (!mine) continue;
+            if (fix) {
+              const int from = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1, end = min(s.keys, 128 * s.k1);
+              const unsigned long long* words =
+                  p.a.mask ? p.a.mask + (long long)(s.row + ftok) * p.a.mask_words : nullptr;
+#pragma unroll 1
+              for (int j = max(from, 128 * s.k0); j < end; ++j) {
+                if (!(seen_bits(j - s.ctx, ftok, words, p.a.mask_words) & 1)) continue;
+                const int id = p.a.table[(long long)s.b * p.a.table_width + (j >> p.a.page_shift)];
+                if (id < 0 || id >= p.a.cache.pages) continue;
+                const long long e = ((((long long)id * p.a.kv_heads + s.h) << p.a.page_shift) +
+                                     (j & ((1 << p.a.page_shift) - 1))) * D + oc0 + i;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                  const float v = cache_value<E>(p.a.cache.v, e + q);
+                  if (!(fabsf(v) < INFINITY)) o[q] = __float_as_uint(__uint_as_float(o[q]) + v);
+                }
+              }
+            }
+            if (whole) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[j] = pack_bf16x2(__uint_as_float(o[q + 2 * j]) * inv, __uint_as_float(o[q + 2 * j + 1]) * inv);
+                *reinterpret_cast<uint4*>(out + i + q) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) dst[(i + q) * (128 * QT)] = __uint_as_float(o[q]);
+            }
+          }
+          if (!whole && mine && (Two || half == 0))
+            p.ml[s.place * 128 * QT + srow] = make_float2(last_m == -INFINITY ? 0.0f : last_m, last_l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&o_free[ob]);
+          mbar_arrive(&part_empty[fp % kParts]);
         }
       }
-      base += 2 * n * NG;
-      last_part = np;
-      last_m = m;
-      last_l = l;
-      have = true;
-      ++segs;
-      if (Two && ok) {
-        have = false;
-        finish(np, segs - 1, m, l);
+      if (!Two && !stop && t == n) {
+        have = true;
+        last_m = m;
+        last_l = l;
+        ++segs;
       }
     }
-    if (have && ok) finish(last_part, segs - 1, last_m, last_l);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
