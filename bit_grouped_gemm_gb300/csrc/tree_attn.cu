@@ -38,36 +38,39 @@ namespace moe {
 namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
-constexpr int kRawBytes = 128 * 64;         // 128 rows of 64 e4m3
-// warps 0..7 softmax, 8 loads, 9 products, 10 the plan, 11..14 conversion (e4m3)
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 10, kConvWarp = 11, kConvWarps = 4;
+// warps 0..7 softmax, 8 loads keys, 9 products, 10 plans, 11 loads values, 12..15 convert (e4m3)
+constexpr int kSoftWarps = 8, kKeyWarp = 8, kMmaWarp = 9, kPlanWarp = 10, kValueWarp = 11, kConvWarp = 12,
+              kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512, kColS = 256;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
 constexpr int kParts = 4;                    // parts told ahead
 
-// E: an e4m3 cache. Two: two row tiles at a time.
+// E: an e4m3 cache. Two: two row tiles at a time. Keys and values of a key tile
+// come in blocks of up to 128 columns, each kind with its own ring of them.
 template <int D, bool E, bool Two>
 struct Shape {
   static constexpr int NC = D / 64;                  // chunks of 64 columns
-  static constexpr int GC = NC < 2 ? NC : 2;         // chunks that are loaded and waited for together
-  static constexpr int NG = NC / GC;                 // groups of a key tile's keys or values
-  static constexpr int kGroups = E ? 6 / GC : D == 64 ? 10 : 4;
-  static constexpr int kRaw = E ? (D == 64 ? 10 : 7) : 0;
+  static constexpr int GC = NC < 2 ? NC : 2;         // chunks of a block
+  static constexpr int NG = NC / GC;                 // blocks of a tile
+  static constexpr int KS = D == 64 ? 4 : 2;         // blocks of keys held
+  static constexpr int VS = D == 64 ? 4 : E ? 1 : 2; // and of values
+  static constexpr int KR = E ? (D == 64 || (D == 128 && !Two) ? 3 : 2) : 0;   // 8-bit blocks of keys
+  static constexpr int VR = E ? (D == 64 ? 3 : D == 128 && !Two ? 2 : 1) : 0;   // and of values
   static constexpr int QT = Two ? 2 : 1;             // row tiles at a time
-  static constexpr int QB = Two || D == 256 ? 1 : 2; // parts whose queries are held
-  static constexpr int OB = Two || D == 256 ? 1 : 2; // parts whose sums are held
+  static constexpr int QB = Two || E || D == 256 ? 1 : 2;   // parts whose queries are held
+  static constexpr int OB = Two || D == 256 ? 1 : 2;        // parts whose sums are held
+  // A barrier less where a block is a tile and goes with the scores' or weights' two
+  // places: that the scores are there (the product is done) says that the block is free.
+  static constexpr bool kKeysWithScores = !Two && NG == 1 && KS == 2;
+  static constexpr bool kValuesWithProducts = !Two && NG == 1 && VS == 2;
   static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kConvWarp);
-  static constexpr int kGroupBytes = GC * kSlotBytes;
+  static constexpr int kBlock = GC * kSlotBytes, kRawBlock = kBlock / 2;
   static constexpr int kQBytes = QT * NC * kSlotBytes;
   static constexpr int kMisc = 5632 + (E ? kParts * 512 * QT : 0);
-  static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + kGroups * kGroupBytes + kRaw * kRawBytes;
+  static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + (KS + VS) * kBlock + (KR + VR) * kRawBlock;
   static_assert(!Two || D <= 128, "tensor memory holds the sums of two row tiles of 128 columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // A group of values that is waited for from outside the products' order: the
-  // group that had its place before is one that a tile's scores have shown to be
-  // consumed (D 256 waits for the last product too).
-  static_assert(kGroups >= 3 * NG || D == 256, "phases told apart");
 };
 
 struct TaParams {
@@ -456,7 +459,7 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile
 }
 
 // A place in a ring of N and the parity of its phase.
-template <int N>
+template <int N>   // (0 where a kernel has none)
 struct Ring {
   uint32_t i = 0, phase = 0;
   __device__ __forceinline__ void step() {
@@ -467,34 +470,53 @@ struct Ring {
   }
 };
 
+// Waits for a ring's last loads to land; i, phase: the place and parity of the next one.
+template <int kMost>
+__device__ __noinline__ void drain_ring(uint64_t* bars, uint32_t i, uint32_t phase, uint32_t loads, uint32_t places,
+                                        unsigned long long limit_ns) {
+  for (uint32_t j = 0; j < min(loads, places) && j < kMost; ++j) {
+    if (i-- == 0) {
+      i = places - 1;
+      phase ^= 1;
+    }
+    mbar_wait_drain(&bars[i], phase, limit_ns);
+  }
+}
+
 template <int D, bool E, bool Two>
 __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
   using Sh = Shape<D, E, Two>;
-  constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, kGroups = Sh::kGroups, kRaw = Sh::kRaw, QB = Sh::QB,
-                OB = Sh::OB, QT = Sh::QT, kRaw1 = kRaw ? kRaw : 1;
+  constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, KR = Sh::KR, VR = Sh::VR,
+                QB = Sh::QB, OB = Sh::OB, QT = Sh::QT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
-  uint8_t* groups = sq + QB * Sh::kQBytes;
-  uint8_t* raws = groups + kGroups * Sh::kGroupBytes;
-  uint8_t* misc = raws + kRaw * kRawBytes;
+  uint8_t* s_keys = sq + QB * Sh::kQBytes;
+  uint8_t* s_values = s_keys + KS * Sh::kBlock;
+  uint8_t* raw_keys = s_values + VS * Sh::kBlock;
+  uint8_t* raw_values = raw_keys + KR * Sh::kRawBlock;
+  uint8_t* misc = raw_values + VR * Sh::kRawBlock;
   float* s_max = reinterpret_cast<float*>(misc);   // [2][2][128], then sums [2][128]
   float* s_sum = s_max + 512;
   float* s_qs = s_sum + 256;                       // [kParts][128 QT] factors of fp16 queries
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 * QT : 0));
-  uint64_t* empty = full + kGroups;
-  uint64_t* raw_full = empty + kGroups;
-  uint64_t* raw_empty = raw_full + kRaw;
-  uint64_t* q_raw = raw_empty + kRaw;    // [QB] queries landed (e4m3)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 * QT : 0));
+  uint64_t* s_full = bars;               // [2] scores, by key tile; Two: by row tile, as the next four
+  uint64_t* p_full = s_full + 2;         // [2] weights
+  uint64_t* pv_done = p_full + 2;        // [2] products with values (Two: a part's last)
+  uint64_t* o_free = pv_done + 2;        // [OB] sums written
+  uint64_t* k_full = o_free + 2;
+  uint64_t* v_full = k_full + KS;
+  uint64_t* k_own = v_full + VS;         // blocks free again, where no barrier above says so
+  uint64_t* v_own = k_own + KS;
+  uint64_t* rk_full = v_own + VS;        // 8-bit blocks
+  uint64_t* rk_empty = rk_full + KR;
+  uint64_t* rv_full = rk_empty + KR;
+  uint64_t* rv_empty = rv_full + VR;
+  uint64_t* q_raw = rv_empty + VR;       // [QB] queries landed (e4m3)
   uint64_t* q_full = q_raw + QB;         // [QB] queries ready
   uint64_t* q_empty = q_full + QB;
-  uint64_t* s_full = q_empty + QB;       // [2] by key tile; Two: by row tile, as the next three
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;         // [OB]
-  uint64_t* o_free = o_full + 2;
-  uint64_t* pv_done = o_free + 2;
-  uint64_t* pair = pv_done + 1;          // [4]
+  uint64_t* pair = q_empty + QB;         // [4]
   uint64_t* part_full = pair + 4;        // [kParts]
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drain = part_empty + kParts;
@@ -503,39 +525,25 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
-  static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 +
-                    8 * (2 * kGroups + 2 * kRaw + 3 * QB + 14 + 2 * kParts) + (kParts + 1) * sizeof(Part) +
+  constexpr int kBars = 8 + 2 * (KS + VS + KR + VR) + 3 * QB + 4 + 2 * kParts + 1;
+  static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
+  uint64_t* k_free = Sh::kKeysWithScores ? s_full : k_own;
+  uint64_t* v_free = Sh::kValuesWithProducts ? pv_done : v_own;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    // arrivals that a phase takes: 1 but for these
 #pragma unroll 1
-    for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&full[i], E ? GC : 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < kBars; ++i) {
+      uint64_t* b = bars + i;
+      const bool soft = (b >= p_full && b < p_full + 2) || (b >= o_free && b < o_free + 2);
+      const bool conv = E && ((b >= k_full && b < k_own) || (b >= rk_empty && b < rv_full) ||
+                              (b >= rv_empty && b < q_raw) || (b >= q_full && b < q_empty));
+      mbar_init(b, soft ? (Two ? kSoftWarps / 2 : kSoftWarps) : conv ? kConvWarps
+                   : b >= pair && b < part_full ? 2 : b >= part_empty && b < drain ? kSoftWarps : 1);
     }
-#pragma unroll 1
-    for (int i = 0; i < 2 * kRaw; ++i) mbar_init(&raw_full[i], 1);
-    for (int i = 0; i < QB; ++i) {
-      mbar_init(&q_raw[i], 1);
-      mbar_init(&q_full[i], E ? kConvWarps : 1);
-      mbar_init(&q_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], Two ? kSoftWarps / 2 : kSoftWarps);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&o_free[i], Two ? kSoftWarps / 2 : kSoftWarps);
-    }
-    mbar_init(pv_done, 1);
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&pair[i], 2);
-      mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], kSoftWarps);
-      s_unbounded[i] = 0;
-    }
-    mbar_init(drain, 1);
+    for (int i = 0; i < kParts; ++i) s_unbounded[i] = 0;
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.mq);
@@ -555,20 +563,21 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
            wait_longer(smem_u32(bar), parity, abort_flag, &p.err, site);
   };
   pdl_begin();
-  // Order of the loads and products. One row tile: the scores run one key tile
-  // ahead, K0 K1 V0 K2 V1 .., through the ends of parts, too, where the next
-  // part's queries have a place of their own (QB 2; at the very end a group's
-  // places are left out, so that V of tile u is always group NG (2u + 2)); else
-  // the part's last V comes before the next part's K0. Two row tiles: K0 V0 K1 V1.
+  // Order of the products. One row tile: the scores run one key tile ahead, S0 S1
+  // O0 S2 O1 .., through the ends of parts, too, where the next part's queries
+  // have a place of their own (QB 2); else a part's last O comes before the next
+  // part's S0. Two row tiles a and b: Sa0 Sb0 | Oa0 Sa1 Ob0 Sb1 | ..
 
   if (warp == kPlanWarp) {
     // ------------------------------------- the CTA's parts, for all others
     Walk walk(p, parts + kParts);
     walk.begin();
     Ring<kParts> at;
+    Ring<QB> qring;
+    uint32_t loads = 0;
     Part s;
-    bool more = true;
-    while (more) {
+    bool more = true, ok = true;
+    while (more && ok) {
       more = walk.next(s);
       s.stop = !more;
       if (more && s.nk == 0) {   // no keys: zeros
@@ -582,165 +591,135 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         continue;
       }
       const int page = more ? first_pages(p, s, s.k0, lane) : 0;
-      if (!wait(&part_empty[at.i], at.phase ^ 1, 1)) break;
+      if (!(ok = wait(&part_empty[at.i], at.phase ^ 1, 1))) break;
       s_pages[32 * at.i + lane] = page;
       if (lane == 0) parts[at.i] = s;
       __syncwarp();
       if (lane == 0) mbar_arrive(&part_full[at.i]);
       at.step();
+      if (!more || !(ok = wait(&q_empty[qring.i], qring.phase ^ 1, 2))) break;
+      if (elect_one_sync()) {
+        uint64_t* bar = E ? &q_raw[qring.i] : &q_full[qring.i];
+        mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
+#pragma unroll 1
+        for (int c = 0; c < QT * NC; ++c)
+          tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * (c % NC), s.h * p.G,
+                      s.row + s.tok0 + c / NC * p.R, bar);
+      }
+      __syncwarp();
+      qring.step();
+      ++loads;
     }
+    // own copies land before shared memory is released
+    if (!ok) drain_ring<QB>(E ? q_raw : q_full, qring.i, qring.phase, loads, QB, p.err.limit_ns);
     if (lane == 0) {
       AttnShared m = walk.shared();
       if (*abort_flag) m.count = 0;
       p.shared[blockIdx.x] = m;
     }
-  } else if (warp == kLoadWarp) {
-    // ---------------------------------------------------- loads, by TMA
+  } else if (warp == kKeyWarp || warp == kValueWarp) {
+    // ------------------------------------- loads of keys or values, by TMA
+    const bool v = warp == kValueWarp;
     const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
-    const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a group)
+    const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a block)
     const int y_mask = (1 << p.a.page_shift) - 1;
-    Ring<E ? kRaw1 : kGroups> ring;
-    Ring<QB> qring;
+    constexpr int kBytes = E ? Sh::kRawBlock : Sh::kBlock, kRow = E ? 64 * GC : 128;
+    const CUtensorMap* map = v ? &p.mv : &p.mk;
+    uint64_t* bar_full = E ? (v ? rv_full : rk_full) : v ? v_full : k_full;
+    uint64_t* bar_free = E ? (v ? rv_empty : rk_empty) : v ? v_free : k_free;
+    uint8_t* ring = E ? (v ? raw_values : raw_keys) : v ? s_values : s_keys;
+    const uint32_t places = E ? (v ? VR : KR) : v ? VS : KS;
+    uint32_t i = 0, phase = 0, loads = 0;
     Ring<kParts> at;
-    uint32_t loads = 0, segs = 0;
-    bool ok = true, bad = false, stop = false, have = false;
-    int vh = 0, vk = 0, vid = 0;      // values not loaded yet: key tile vk of head vh, pages vid
-    int k = 0, k1 = 0, k0 = 0, win = 0, now = 0, later = 0;
-    Part s;
+    bool ok = true, bad = false;
     while (ok) {
-      if (k == k1 && !stop) {
-        if (!(ok = wait(&part_full[at.i], at.phase, 2))) break;
-        s = parts[at.i];
-        stop = s.stop;
-        k0 = k = stop ? 0 : s.k0;
-        k1 = stop ? 0 : s.k1;
-        // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
-        win = 0;
-        now = s_pages[32 * at.i + lane];
-        later = stop ? 0 : first_pages(p, s, s.k0 + (32 >> box_log), lane);
-        at.step();
-      }
-      const bool go = !stop && !(QB == 1 && !Two && have && k == k0);
-      if (!go && !have) break;
-      int id = 0;
-      if (go) {
-        if (k == k0) {
-          if (!(ok = wait(&q_empty[qring.i], qring.phase ^ 1, 3))) break;
-          if (elect_one_sync()) {
-            uint64_t* bar = E ? &q_raw[qring.i] : &q_full[qring.i];
-            mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
+      if (!(ok = wait(&part_full[at.i], at.phase, 3))) break;
+      const Part s = parts[at.i];
+      if (s.stop) break;
+      // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
+      int win = 0, now = s_pages[32 * at.i + lane], later = first_pages(p, s, s.k0 + (32 >> box_log), lane);
+      at.step();
 #pragma unroll 1
-            for (int c = 0; c < QT * NC; ++c)
-              tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * (c % NC), s.h * p.G,
-                          s.row + s.tok0 + c / NC * p.R, bar);
-          }
-          __syncwarp();
-          qring.step();
-          ++segs;
-        }
-        id = __shfl_sync(0xffffffffu, now, ((k - k0) << box_log) - win + my_box);
-        if ((k + 1 - k0) << box_log == win + 32) {
+      for (int k = s.k0; k < s.k1 && ok; ++k) {
+        int id = __shfl_sync(0xffffffffu, now, ((k - s.k0) << box_log) - win + my_box);
+        if ((k + 1 - s.k0) << box_log == win + 32) {
           win += 32;
           now = later;
           later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
         }
         bad |= id == kBadPage;
         if (id < 0) id = p.a.cache.pages;   // reads as zeros
-      } else if (QB == 2 && !E) {
-        for (int g = 0; g < NG; ++g) ring.step();   // (the group that is left out)
-      }
-      // K of this tile; V of the one before, or (Two) of this one
+        const int y = (128 * k + my_box * box) & y_mask;
 #pragma unroll 1
-      for (int op = go ? 0 : 1; op < (have || Two ? 2 : 1) && ok; ++op) {
-        const CUtensorMap* m = op ? &p.mv : &p.mk;
-        const int kk = op && !Two ? vk : k, hh = op && !Two ? vh : s.h, page = op && !Two ? vid : id;
-        const int y = (128 * kk + my_box * box) & y_mask;
-#pragma unroll 1
-        for (int g = 0; g < (E ? NC : NG); ++g) {
-          uint64_t* bar = E ? &raw_full[ring.i] : &full[ring.i];
-          if (!(ok = wait(E ? &raw_empty[ring.i] : &empty[ring.i], ring.phase ^ 1, 4))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar, E ? kRawBytes : Sh::kGroupBytes);
+        for (int g = 0; g < NG; ++g) {
+          if (!(ok = wait(&bar_free[i], phase ^ 1, 4))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar_full[i], kBytes);
           __syncwarp();
           if (my_chunk < (E ? 1 : GC))
-            tma_load_4d(E ? raws + ring.i * kRawBytes + my_box * box * 64
-                          : groups + ring.i * Sh::kGroupBytes + my_chunk * kSlotBytes + my_box * box * 128,
-                        m, 64 * (E ? g : g * GC + my_chunk), y, hh, page, bar);
-          ring.step();
+            tma_load_4d(ring + i * kBytes + my_chunk * kSlotBytes + my_box * box * kRow, map, 64 * (g * GC + my_chunk),
+                        y, s.h, id, &bar_full[i]);
           ++loads;
+          if (++i == places) {
+            i = 0;
+            phase ^= 1;
+          }
         }
       }
-      have = go && !Two;
-      vh = s.h;
-      vk = k;
-      vid = id;
-      k += go;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
-    if (!ok) {
-      // own copies land before shared memory is released: each place's last load
-      constexpr int kRing = E ? kRaw1 : kGroups;
-      const uint32_t n = min(loads, (uint32_t)kRing);
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint32_t i = (ring.i + kRing - 1 - j) % kRing, parity = i < ring.i ? ring.phase : ring.phase ^ 1;
-        mbar_wait_drain(E ? &raw_full[i] : &full[i], parity, p.err.limit_ns);
-      }
-      for (uint32_t j = 0; j < min(segs, (uint32_t)QB); ++j) {
-        const uint32_t i = (qring.i + QB - 1 - j) % QB, parity = i < qring.i ? qring.phase : qring.phase ^ 1;
-        mbar_wait_drain(E ? &q_raw[i] : &q_full[i], parity, p.err.limit_ns);
-      }
-    }
+    if (!ok) drain_ring<4>(bar_full, i, phase, loads, places, p.err.limit_ns);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- products
     constexpr uint32_t kIdS = idesc_16(!E, 128, false), kIdO = idesc_16(!E, 64 * GC, true);
-    const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), gd0 = smem_desc_sw128(smem_u32(groups));
-    const uint64_t vd0 = value_desc(smem_u32(groups));
-    Ring<kGroups> ring;
+    const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), kd0 = smem_desc_sw128(smem_u32(s_keys));
+    const uint64_t vd0 = value_desc(smem_u32(s_values));
+    Ring<KS> keys;
+    Ring<VS> vals;
     Ring<QB> qring;
     Ring<kParts> at;
     uint32_t segs = 0, u = 0;
     bool ok = true;
-    // Scores of the key tile in the groups from r on (keys waited for, and given
-    // back, if asked), row tile q's queries at descriptor qd, into S buffer `buf`.
-    auto scores = [&](Ring<kGroups> r, uint64_t qd, int buf, bool wait_keys, bool free_keys) {
+    // Scores of the key tile in the blocks from r on, row tile at descriptor qd,
+    // into S buffer `buf`; the first of Two does not give the keys back.
+    auto scores = [&](Ring<KS> r, uint64_t qd, int buf, bool first, bool last) {
 #pragma unroll 1
       for (int g = 0; g < NG; ++g, r.step()) {
-        if (wait_keys && !(ok = wait(&full[r.i], r.phase, 5))) break;
+        if (first && !(ok = wait(&k_full[r.i], r.phase, 5))) break;
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint64_t a = qd + g * (Sh::kGroupBytes / 16), b = gd0 + r.i * (Sh::kGroupBytes / 16);
+          const uint64_t a = qd + g * (Sh::kBlock / 16), b = kd0 + r.i * (Sh::kBlock / 16);
 #pragma unroll
           for (int c = 0; c < GC; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f16_ss(tmem + kColS + 128 * buf, a + (c * kSlotBytes + 32 * kk) / 16,
                          b + (c * kSlotBytes + 32 * kk) / 16, kIdS, g != 0 || (c | kk) != 0);
-          if (free_keys) mma_commit(&empty[r.i]);
+          if (!Sh::kKeysWithScores && last) mma_commit(&k_own[r.i]);
           if (g == NG - 1) mma_commit(&s_full[buf]);
         }
         __syncwarp();
       }
     };
-    // O (+)= P V with the values in the groups from r on.
-    auto values = [&](Ring<kGroups> r, uint32_t o, int buf, bool first, uint64_t* done, bool wait_values,
-                      bool free_values) {
+    // O (+)= P V with the values in the blocks from r on.
+    auto values = [&](Ring<VS> r, uint32_t o, int buf, bool begin, uint64_t* done, bool first, bool last) {
 #pragma unroll 1
       for (int g = 0; g < NG; ++g, r.step()) {
-        if (wait_values && !(ok = wait(&full[r.i], r.phase, 6))) break;
+        if (first && !(ok = wait(&v_full[r.i], r.phase, 6))) break;
         tc_fence_after();
         if (elect_one_sync()) {
-          const uint64_t b = vd0 + r.i * (Sh::kGroupBytes / 16);
+          const uint64_t b = vd0 + r.i * (Sh::kBlock / 16);
           const uint32_t pc = tmem + kColS + 128 * buf;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
             mma_f16_ts(o + 64 * GC * g, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)), b + (2048 >> 4) * kk,
-                       kIdO, !first || kk != 0);
-          if (free_values) mma_commit(&empty[r.i]);
+                       kIdO, !begin || kk != 0);
+          if (!Sh::kValuesWithProducts && last) mma_commit(&v_own[r.i]);
           if (g == NG - 1 && done) mma_commit(done);
         }
         __syncwarp();
       }
     };
-    auto skip = [&](Ring<kGroups>& r) {
+    auto skip = [&](auto& r) {
       for (int g = 0; g < NG; ++g) r.step();
     };
     if constexpr (Two) {
@@ -752,22 +731,19 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         if (!(ok = wait(q_full, segs & 1, 8))) break;
 #pragma unroll 1
         for (int t = -1; t < n && ok; ++t) {
-          // ring: V(t), if t is one, and K(t + 1) behind it
-          Ring<kGroups> keys = ring;
-          if (t >= 0) skip(keys);
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             if (t >= 0) {
               if (!(ok = wait(&p_full[q], u & 1, 9))) break;
               if (t == 0 && !(ok = wait(&o_free[q], (segs & 1) ^ 1, 10))) break;
-              values(ring, tmem + 128 * q, q, t == 0, t + 1 == n ? &o_full[q] : nullptr, q == 0, q == 1);
+              values(vals, tmem + 128 * q, q, t == 0, t + 1 == n ? &pv_done[q] : nullptr, q == 0, q == 1);
               if (!ok) break;
             }
             if (t + 1 < n) scores(keys, qd0 + q * (NC * kSlotBytes / 16), q, q == 0, q == 1);
             if (!ok) break;
           }
-          ring = keys;
-          if (t + 1 < n) skip(ring);
+          if (t + 1 < n) skip(keys);
+          if (t >= 0) skip(vals);
           u += t >= 0;
           if (t + 2 == n) {
             if (elect_one_sync()) mma_commit(q_empty);
@@ -792,21 +768,21 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         if (!go && !have) break;
         if (go) {
           if (t == 0 && !(ok = wait(&q_full[qring.i], qring.phase, 8))) break;
-          scores(ring, qd0 + qring.i * (Sh::kQBytes / 16), u & 1, true, true);
+          scores(keys, qd0 + qring.i * (Sh::kQBytes / 16), u & 1, true, true);
           if (!ok) break;
+          skip(keys);
           if (t + 1 == n) {
             if (elect_one_sync()) mma_commit(&q_empty[qring.i]);
             __syncwarp();
             qring.step();
           }
         }
-        if (go || QB == 2) skip(ring);
         if (have) {
-          const uint32_t v = u - 1, ob = vob % OB;
-          if (!(ok = wait(&p_full[v & 1], (v >> 1) & 1, 9))) break;
+          const uint32_t w = u - 1, ob = vob % OB;
+          if (!(ok = wait(&p_full[w & 1], (w >> 1) & 1, 9))) break;
           if (first && !(ok = wait(&o_free[ob], ((vob / OB) & 1) ^ 1, 10))) break;
-          values(ring, tmem + 128 * ob, v & 1, first, !go || t == 0 ? &o_full[ob] : pv_done, true, true);
-          skip(ring);
+          values(vals, tmem + 128 * ob, w & 1, first, &pv_done[w & 1], true, true);
+          skip(vals);
         }
         have = go;
         first = t == 0;
@@ -819,19 +795,21 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     if (elect_one_sync()) mma_commit(drain);
     __syncwarp();
     mbar_wait_drain(drain, 0, p.err.limit_ns);
-  } else if (E && warp >= kConvWarp) {
+  } else if (E && warp >= kConvWarp) {   // (8-bit caches have one place for queries)
     // ------------------- e4m3 chunks to fp16, exactly; queries to fp16, each
     // row times the power of two that brings its largest element to 2^14..2^15
     // (elements below 2^-31 of that one lose bits), which its scores undo
     const int w = warp - kConvWarp, tid = 32 * w + lane;
-    // chunks loaded before the tile at hand, and their places in the operand ring
-    uint32_t raw = 0, chunk = 0;
     int vk = 0, vseen = 0, vkeys = 0;      // the key tile whose values come next, and of which part
     uint32_t vpart = 0, np = 0;
+    Ring<KS> keys;
+    Ring<VS> vals;
+    Ring<KR> rkeys;
+    Ring<VR> rvals;
     Ring<QB> qring;
     Ring<kParts> at;
-    bool ok = true, stop = false, have = false;
-    int t = 0, n = 0, seen = 0;
+    bool ok = true, stop = false, have = false, fresh = false;   // fresh: the part's queries are to be converted
+    int t = 0, n = 0, seen = 0, slot = 0;
     Part s;
     while (ok) {
       if (t == n && !stop) {
@@ -840,108 +818,123 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         stop = s.stop;
         n = stop ? 0 : s.k1 - s.k0;
         t = 0;
-        if (!stop) {
-          seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-          if (!(ok = wait(&q_raw[qring.i], qring.phase, 12))) break;
-#pragma unroll 1
-          for (int q = 0; q < QT; ++q) {   // 8 threads to a row
-            const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
-#pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
-              const int r = r0 + (tid >> 3);
-              uint8_t* line = sq + qring.i * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
-              uint4 x[NC];
-              uint32_t top = 0;
-#pragma unroll
-              for (int c = 0; c < NC; ++c) {
-                x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
-                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
-              }
-#pragma unroll
-              for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-              // exponent of the largest element, within what keeps both factors normal
-              const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
-              const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-              for (int c = 0; c < NC; ++c) {
-                uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
-                  v[j] = *reinterpret_cast<const uint32_t*>(&hv);
-                }
-                *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-              if ((tid & 7) == 0) s_qs[at.i * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full[qring.i]);
-          qring.step();
-        }
+        fresh = !stop;
+        slot = at.i;
         at.step();
         ++np;
       }
-      const bool go = !stop && !(QB == 1 && !Two && have && t == 0);
+      const bool go = !stop && !(have && t == 0);   // (a part's last values before the next one's queries)
       if (!go && !have) break;
+      if (go && fresh) {
+        fresh = false;
+        seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+        if (!(ok = wait(&q_raw[qring.i], qring.phase, 12))) break;
+#pragma unroll 1
+        for (int q = 0; q < QT; ++q) {   // 8 threads to a row
+          const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
+            const int r = r0 + (tid >> 3);
+            uint8_t* line = sq + qring.i * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
+            uint4 x[NC];
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
+              const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            // exponent of the largest element, within what keeps both factors normal
+            const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
+            const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
+                v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+              }
+              *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            if ((tid & 7) == 0) s_qs[slot * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qring.i]);
+        qring.step();
+      }
       if (Two) {
         vk = s.k0 + t;
         vseen = seen;
         vkeys = s.keys;
         vpart = np - 1;
       }
-      if (!go && QB == 2) chunk += NC;   // (the group that is left out)
-      // K of this tile; V of the one before, or (Two) of this one. Every chunk by
-      // one of the warps in turn: by all of them it would pay for its waits and
-      // barriers four times.
-      const int end = have || Two ? 2 * NC : NC;
+      // K of this tile; V of the one before, or (Two) of this one. A warp has 32
+      // rows of a block.
 #pragma unroll 1
-      for (int c = go ? 0 : NC; c < end; ++c, ++raw, ++chunk) {
-        if (raw % kConvWarps != (uint32_t)w) continue;
-        const int ri = raw % kRaw1, gi = chunk / GC % kGroups;
-        if (!(ok = wait(&raw_full[ri], (raw / kRaw1) & 1, 13))) break;
-        if (!(ok = wait(&empty[gi], ((chunk / GC / kGroups) & 1) ^ 1, 14))) break;
-        const uint8_t* src = raws + ri * kRawBytes + 16 * lane;
-        // piece i of the lane: row 8 i + lane / 4, 16 columns
-        uint8_t* dst = groups + gi * Sh::kGroupBytes + chunk % GC * kSlotBytes + 128 * (lane >> 2);
-        const int p0 = 16 * ((2 * (lane & 3)) ^ (lane >> 2)), p1 = 16 * ((2 * (lane & 3) + 1) ^ (lane >> 2));
+      for (int op = go ? 0 : NG; op < (have || Two ? 2 * NG : NG); ++op) {
+        const bool v = op >= NG;
+        const uint32_t ri = v ? rvals.i : rkeys.i, bi = v ? vals.i : keys.i;
+        if (!(ok = wait(v ? &rv_full[ri] : &rk_full[ri], v ? rvals.phase : rkeys.phase, 13))) break;
+        if (!(ok = wait(v ? &v_free[bi] : &k_free[bi], (v ? vals.phase : keys.phase) ^ 1, 14))) break;
+        const uint8_t* src = (v ? raw_values : raw_keys) + ri * Sh::kRawBlock + 2048 * GC * w + 16 * lane;
+        // a lane's piece of 16 columns: 4 or 8 lanes to a row of 64 or 128 bytes
+        constexpr int kLanes = 4 * GC, kRows = 32 / kLanes, kPieces = 32 / kRows;
+        const int row = 32 * w + lane / kLanes, pc = lane % kLanes;
+        uint8_t* dst = (v ? s_values : s_keys) + bi * Sh::kBlock + (pc >> 2) * kSlotBytes + 128 * row;
+        // (the two chunks' lanes store their halves in opposite order: no bank is met twice)
+        const int odd = pc >> 2, p0 = 2 * (pc & 3) + odd, p1 = 2 * (pc & 3) + 1 - odd;
+        const bool clear = v && 128 * (vk + 1) > vseen;
+        bool any = false;
 #pragma unroll 1
-        for (int i = 0; i < 16; i += 4) {
+        for (int i = 0; i < kPieces; i += 4) {
           uint4 x[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 512 * (i + j));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 y = x[j];
-            *reinterpret_cast<uint4*>(dst + 1024 * (i + j) + p0) =
-                make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16), e4m3x2_f16x2(y.y), e4m3x2_f16x2(y.y >> 16));
-            *reinterpret_cast<uint4*>(dst + 1024 * (i + j) + p1) =
-                make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16), e4m3x2_f16x2(y.w), e4m3x2_f16x2(y.w >> 16));
+            const int r7 = (row + kRows * (i + j)) & 7;
+            uint8_t* line = dst + 128 * kRows * (i + j);
+            const uint4 lo = make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16), e4m3x2_f16x2(y.y),
+                                        e4m3x2_f16x2(y.y >> 16));
+            const uint4 hi = make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16), e4m3x2_f16x2(y.w),
+                                        e4m3x2_f16x2(y.w >> 16));
+            *reinterpret_cast<uint4*>(line + 16 * (p0 ^ r7)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(line + 16 * (p1 ^ r7)) = odd ? lo : hi;
           }
         }
-        if (c >= NC && 128 * (vk + 1) > vseen) {
+        if (clear) {
           // values of a tile that not every row sees whole: what some row must
           // not see is cleared, keys past the row tile's own, and what is no number
-          bool any = false;
 #pragma unroll 1
-          for (int i = 0; i < 32; ++i) {
-            uint4* y = reinterpret_cast<uint4*>(dst + 512 * (i & ~1) + (i & 1 ? p1 : p0));
-            const int key = 128 * vk + 8 * (i >> 1) + (lane >> 2);
+          for (int i = 0; i < 2 * kPieces; ++i) {
+            const int r = row + kRows * (i >> 1), key = 128 * vk + r;
+            uint4* y = reinterpret_cast<uint4*>(dst + 128 * kRows * (i >> 1) + 16 * ((i & 1 ? p1 : p0) ^ (r & 7)));
             if (key < vseen) continue;
-            uint4 v = key < vkeys ? *y : make_uint4(0, 0, 0, 0);
-            any |= clear_unbounded<true>(v);
-            *y = v;
+            uint4 x = key < vkeys ? *y : make_uint4(0, 0, 0, 0);
+            any |= clear_unbounded<true>(x);
+            *y = x;
           }
           if (any) s_unbounded[vpart % kParts] = (int)vpart + 1;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&full[gi]);
-          mbar_arrive(&raw_empty[ri]);
+          mbar_arrive(v ? &v_full[bi] : &k_full[bi]);
+          mbar_arrive(v ? &rv_empty[ri] : &rk_empty[ri]);
+        }
+        if (v) {
+          vals.step();
+          rvals.step();
+        } else {
+          keys.step();
+          rkeys.step();
         }
       }
       have = go && !Two;
@@ -959,7 +952,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     constexpr int CW = Two ? 128 : 64, OW = Two ? D : D / 2;
     const int q0 = Two ? half * p.R : 0, oc0 = Two ? 0 : half * OW;
     const int row_tok = q0 + row / p.G, row_g = row % p.G;   // token of the part, query head of the group
-    uint32_t np = 0, segs = 0, u = 0, base = 0, pvs = 0, pairs = 0;
+    uint32_t np = 0, segs = 0, u = 0, pairs = 0;
     Ring<kParts> at;
     bool ok = true, stop = false, have = false;   // have: the part before is to be finished
     float last_m = 0.0f, last_l = 0.0f, m = 0.0f, l = 0.0f, c2 = 0.0f;
@@ -977,7 +970,6 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         const Part& s = parts[at.i];
         stop = s.stop;
         if (!stop) {
-          base += 2 * n * NG;
           k0 = s.k0;
           n = s.k1 - k0;
           t = 0;
@@ -1058,11 +1050,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           const float old = m;
           if (grow && top > m) m = top;
           if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
-            // The last product has to be done. Two: these scores came after it.
-            // One: they came after the one before it, so only the last one's
-            // phase of pv_done can be open.
+            // The last product has to be done. (Two: these scores came after it.)
             if (!Two) {
-              if (!(ok = wait(pv_done, (pvs - 1) & 1, 18))) break;
+              if (!(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 18))) break;
               tc_fence_after();
             }
             const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
@@ -1116,21 +1106,21 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           // values that some row must not see: keys past the row tile's own are
           // nobody's, others only where they are no numbers. (Two: both groups
           // of warps clear all of them, with the same result.)
-          if (D == 256 && t > 0 && !(ok = wait(pv_done, (pvs - 1) & 1, 19))) break;
+          // The block that had the place before is consumed, so that the wait for
+          // this one is for its phase: these scores came after the product of tile
+          // u - 2; with two blocks to a tile the last product is waited for.
+          if (NG > 1 && u > 0 && !(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 19))) break;
           const int key = threadIdx.x & 127, j = 128 * k + key, keys = parts[pi].keys;
-          const uint32_t place = Two ? base + NG * (2 * t + 1)
-                                 : QB == 2 ? NG * (2 * u + 2)
-                                           : base + NG * (t + 1 < n ? 2 * t + 2 : 2 * n - 1);
           bool any = false;
 #pragma unroll 1
           for (int g = 0; g < NG; ++g) {
-            const uint32_t i = (place + g) % kGroups;
-            if (!(ok = wait(&full[i], ((place + g) / kGroups) & 1, 20))) break;
+            const uint32_t i = (u * NG + g) % VS;
+            if (!(ok = wait(&v_full[i], ((u * NG + g) / VS) & 1, 20))) break;
             if (j < seen) continue;
 #pragma unroll 1
             for (int q = Two ? 0 : 4 * half; q < GC * 8; q += !Two && (q & 3) == 3 ? 5 : 1) {
               // piece q % 8 of chunk q / 8; One: half of each chunk's pieces
-              uint4* piece = reinterpret_cast<uint4*>(groups + i * Sh::kGroupBytes + (q >> 3) * kSlotBytes + 128 * key) +
+              uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kBlock + (q >> 3) * kSlotBytes + 128 * key) +
                              ((q & 7) ^ (key & 7));
               uint4 y = j < keys ? *piece : make_uint4(0, 0, 0, 0);
               const bool un = clear_unbounded<false>(y);
@@ -1147,7 +1137,6 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[buf]);
         ++t;
         ++u;
-        if (t < n) ++pvs;   // this tile's product, as pv_done counts it
       }
       // The sums of a part: Two, when its last weights are made; One, only after
       // the next part's first ones, while its last product runs.
@@ -1162,7 +1151,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         const uint32_t fp = Two || stop ? part : part - 1, seg = segs - 1;
         const Part& s = parts[fp % kParts];
         const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
-        if (!(ok = wait(&o_full[ob], (Two ? seg : seg / OB) & 1, 21))) break;
+        // its last product: of the tile before this one, or of the last one
+        const uint32_t w = stop ? u - 1 : u - 2;
+        if (!(ok = wait(&pv_done[Two ? half : w & 1], (Two ? seg : w >> 1) & 1, 21))) break;
         tc_fence_after();
         if (32 * quarter < rows) {
           if (!Two) {
@@ -1325,7 +1316,7 @@ bool encode_maps(const AttnArgs& a, int G, int R, TaParams* p) {
   const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)R};
   const uint64_t cd[4] = {D, P, (uint64_t)a.kv_heads, (uint64_t)a.cache.pages};
   const uint64_t cs[3] = {D * e, D * e * P, D * e * P * a.kv_heads};
-  const uint32_t cb[4] = {64, (uint32_t)(P < 128 ? P : 128), 1, 1};
+  const uint32_t cb[4] = {a.e4m3 && D > 64 ? 128u : 64u, (uint32_t)(P < 128 ? P : 128), 1, 1};
   const auto dt = a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return encode_nd(&p->mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, qd, qs, qb, true) &&
          encode_nd(&p->mk, dt, 4, a.cache.k, cd, cs, cb, !a.e4m3) &&
