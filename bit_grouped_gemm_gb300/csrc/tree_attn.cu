@@ -79,7 +79,7 @@ struct TaParams {
   AttnShared* shared;
   float2* ml;          // [cta][2][128 QT] maximum (log2) and sum
   float* o;            // [cta][2][D][128 QT]: a warp stores a column of its 32 rows at a time
-  float inv_ctas;      // 1 / CTAs, a little more
+  unsigned long long inv_ctas;   // 2^64 / CTAs, rounded up
   int G, R;            // query heads per key-value head, tokens per row tile
   int step;            // tokens of a row tile, or of two
   unsigned inv_step;   // 2^31 / step, rounded up
@@ -195,12 +195,19 @@ __device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r
 __device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
   return r.n ? cost_before(p, r, r.tiles - 1) + kItemCost + keys_of(p, r, r.tiles - 1) : 0;
 }
-// floor(x / d) for 0 <= x, 0 < d, at most `most`
-__device__ __forceinline__ int quotient(long long x, long long d, int most) {
-  int q = min((int)__fdividef((float)x, (float)d), most);
-  while (q > 0 && q * d > x) --q;
-  while (q < most && (q + 1) * d <= x) ++q;
-  return q;
+// By a whole warp: the largest i below n (n >= 1) with f(i) <= x, for f increasing and
+// f(0) <= x; 32 places are tried at a time.
+template <class F>
+__device__ __forceinline__ int search(int n, long long x, F f) {
+  int lo = 0;
+#pragma unroll 1
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = (threadIdx.x & 31) * step;   // (lane 0: f(lo) <= x)
+    const int k = __popc(__ballot_sync(0xffffffffu, i < n && f(lo + i) <= x)) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
 }
 
 // A CTA's part of a row tile (or of two): key tiles [k0, k1) of nk.
@@ -231,18 +238,19 @@ struct Walk {
     return req_of(p, __ldcg(p.a.offsets + i), __ldcg(p.a.offsets + i + 1), __ldcg(p.a.length + i));
   }
 
+  __device__ __forceinline__ explicit Walk(const TaParams& p_, Part* last_) : p(p_), last(last_) {}
   // By a whole warp. Equal costs per CTA, at least what one key tile costs (a
   // smaller part would have none): the costs of all requests are summed up, a
-  // run of them per lane, and the lane in whose run the CTA's cost begins looks
-  // for the row tile.
-  __device__ __forceinline__ explicit Walk(const TaParams& p_, Part* last_) : p(p_), last(last_) {}
+  // run of them per lane; the lane in whose run the CTA's cost begins finds the
+  // request, and all lanes together the head and row tile.
   __device__ __forceinline__ void begin() {
     b = p.a.requests;
     from = -1;
-    const int lane = threadIdx.x & 31, B = p.a.requests, per = (B + 31) / 32;
-    const int b0 = min(lane * per, B), b1 = min(b0 + per, B);
+    const int lane = threadIdx.x & 31, B = p.a.requests, per = (B + 31) >> 5;
+    const int b0 = min(lane * per, B), b1 = min(b0 + per, B), cap = p.a.table_width << p.a.page_shift;
     long long mine = 0;
-    Req first{};
+    r = Req{};
+#pragma unroll 1
     for (int i0 = b0; i0 < b1; i0 += 4) {
       // (four requests' loads at once)
       int from_row[4], to_row[4], lens[4];
@@ -253,59 +261,58 @@ struct Walk {
         to_row[j] = __ldcg(p.a.offsets + i + 1);
         lens[j] = __ldcg(p.a.length + i);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (i0 + j >= b1) break;
-        const Req q = req_of(p, from_row[j], to_row[j], lens[j]);
-        if (i0 + j == b0) first = q;
+#pragma unroll 1
+      for (int j = 0; j < min(b1 - i0, 4); ++j) {
+        const Req q = req_of(p, from_row[0], to_row[0], lens[0]);
+        if (i0 + j == b0) r = q;
         mine += cost_of(p, q);
-        if (blockIdx.x == 0 && q.n && lens[j] > (p.a.table_width << p.a.page_shift))
-          atomicOr(p.err.word, DEVERR_RANGE);
+        if (blockIdx.x == 0 && q.n && lens[0] > cap) atomicOr(p.err.word, DEVERR_RANGE);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          from_row[x] = from_row[x + 1];
+          to_row[x] = to_row[x + 1];
+          lens[x] = lens[x + 1];
+        }
       }
     }
     mine *= p.a.kv_heads;
     __syncwarp();
     long long before = mine;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, before, d);
       if (lane >= d) before += o;
     }
     const long long total = __shfl_sync(0xffffffffu, before, 31);
     before -= mine;
-    // (rounded up past the float's error: the shares cover the total)
-    const long long share = max((long long)((float)total * p.inv_ctas) + 1, (long long)(kItemCost + 128));
+    // (a little more than the quotient: the shares cover the total)
+    const long long share = max((long long)__umul64hi(total, p.inv_ctas) + 1, (long long)(kItemCost + 128));
     c0 = blockIdx.x * share;
     c1 = c0 + share;
     const bool owner = c0 >= before && c0 < before + mine;
     const unsigned who = __ballot_sync(0xffffffffu, owner);
     if (!who) return;
+    long long head = 0;
     if (owner) {
-      r = first;
-      long long head = cost_of(p, r);
+      head = cost_of(p, r);
       for (b = b0; c0 >= before + p.a.kv_heads * head;) {
         before += p.a.kv_heads * head;
         r = load(++b);
         head = cost_of(p, r);
       }
-      h = quotient(c0 - before, head, p.a.kv_heads - 1);
-      before += h * head;
-      t = 0;
-      for (int end = r.tiles; end - t > 1;) {
-        const int mid = (t + end) >> 1;
-        if (cost_before(p, r, mid) <= c0 - before) t = mid; else end = mid;
-      }
-      at = before + cost_before(p, r, t);
     }
     __syncwarp();
     const int src = __ffs(who) - 1;
     auto all = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
-    at = __shfl_sync(0xffffffffu, at, src);
+    at = __shfl_sync(0xffffffffu, before, src);
+    head = __shfl_sync(0xffffffffu, head, src);
     b = all(b);
-    h = all(h);
-    t = all(t);
     r = {all(r.row), all(r.n), all(r.ctx), all(r.tiles)};
     ahead();
+    h = search(p.a.kv_heads, c0 - at, [&](int i) { return i * head; });
+    at += h * head;
+    t = search(r.tiles, c0 - at, [&](int i) { return cost_before(p, r, i); });
+    at += cost_before(p, r, t);
   }
   // The next part that has work: key tiles, or a row tile without keys that
   // begins here.
@@ -328,7 +335,7 @@ struct Walk {
       s.stop = 0;
       if (begins && at + cost > c1) {
         from = at;
-        if ((threadIdx.x & 31) == 0) *last = s;
+        if ((threadIdx.x & 31) == 0) *last = s;   // (for shared(), at the end)
       }
       at += cost;
       if (++t == r.tiles) {
@@ -351,7 +358,7 @@ struct Walk {
     AttnShared m = {};
     if (from < 0 || last->nk == 0) return m;
     const long long cost = kItemCost + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
-    const int n = quotient(x, share, kAttnMaxCtas);   // CTAs on, of the one where the tile ends
+    const int n = search(kAttnMaxCtas, x, [&](int i) { return i * share; });   // CTAs on, where the tile ends
     int first = blockIdx.x, end = blockIdx.x + n;
     if (last->k1 == 0) ++first;
     if (border(end * share - from, cost, last->nk) == last->nk) --end;
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       const bool soft = (b >= p_full && b < p_full + 2) || (b >= o_free && b < o_free + 2);
       const bool conv = E && ((b >= k_full && b < k_own) || (b >= rk_empty && b < rv_full) ||
                               (b >= rv_empty && b < q_raw) || (b >= q_full && b < q_empty));
-      mbar_init(b, soft ? (Two ? kSoftWarps / 2 : kSoftWarps) : conv ? kConvWarps
+      mbar_init(b, soft ? (Two ? kSoftWarps / 2 : kSoftWarps) : conv ? kConvWarps / 2
                    : b >= pair && b < part_full ? 2 : b >= part_empty && b < drain ? kSoftWarps : 1);
     }
     for (int i = 0; i < kParts; ++i) s_unbounded[i] = 0;
@@ -612,11 +619,10 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
     // own copies land before shared memory is released
     if (!ok) drain_ring<QB>(E ? q_raw : q_full, qring.i, qring.phase, loads, QB, p.err.limit_ns);
-    if (lane == 0) {
-      AttnShared m = walk.shared();
-      if (*abort_flag) m.count = 0;
-      p.shared[blockIdx.x] = m;
-    }
+    __syncwarp();
+    AttnShared m = walk.shared();
+    if (*abort_flag) m.count = 0;
+    if (lane == 0) p.shared[blockIdx.x] = m;
   } else if (warp == kKeyWarp || warp == kValueWarp) {
     // ------------------------------------- loads of keys or values, by TMA
     const bool v = warp == kValueWarp;
@@ -799,51 +805,38 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     // ------------------- e4m3 chunks to fp16, exactly; queries to fp16, each
     // row times the power of two that brings its largest element to 2^14..2^15
     // (elements below 2^-31 of that one lose bits), which its scores undo
-    const int w = warp - kConvWarp, tid = 32 * w + lane;
-    int vk = 0, vseen = 0, vkeys = 0;      // the key tile whose values come next, and of which part
-    uint32_t vpart = 0, np = 0;
-    Ring<KS> keys;
-    Ring<VS> vals;
-    Ring<KR> rkeys;
-    Ring<VR> rvals;
-    Ring<QB> qring;
+    // Two warps take the keys and the queries, two the values; a warp has 64 rows
+    // of a block.
+    const bool v = warp >= kConvWarp + 2;
+    const int w = (warp - kConvWarp) & 1, tid = 32 * w + lane;
+    uint64_t *rfull = v ? rv_full : rk_full, *rempty = v ? rv_empty : rk_empty;
+    uint64_t *bfull = v ? v_full : k_full, *bfree = v ? v_free : k_free;
+    uint8_t *raw = v ? raw_values : raw_keys, *blocks = v ? s_values : s_keys;
+    const uint32_t raw_places = v ? VR : KR, places = v ? VS : KS;
+    uint32_t ri = 0, rphase = 0, bi = 0, bphase = 0, np = 0;
     Ring<kParts> at;
-    bool ok = true, stop = false, have = false, fresh = false;   // fresh: the part's queries are to be converted
-    int t = 0, n = 0, seen = 0, slot = 0;
-    Part s;
+    bool ok = true;
     while (ok) {
-      if (t == n && !stop) {
-        if (!(ok = wait(&part_full[at.i], at.phase, 11))) break;
-        s = parts[at.i];
-        stop = s.stop;
-        n = stop ? 0 : s.k1 - s.k0;
-        t = 0;
-        fresh = !stop;
-        slot = at.i;
-        at.step();
-        ++np;
-      }
-      const bool go = !stop && !(have && t == 0);   // (a part's last values before the next one's queries)
-      if (!go && !have) break;
-      if (go && fresh) {
-        fresh = false;
-        seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-        if (!(ok = wait(&q_raw[qring.i], qring.phase, 12))) break;
+      if (!(ok = wait(&part_full[at.i], at.phase, 11))) break;
+      const Part s = parts[at.i];
+      if (s.stop) break;
+      if (!v) {
+        if (!(ok = wait(q_raw, np & 1, 12))) break;
 #pragma unroll 1
         for (int q = 0; q < QT; ++q) {   // 8 threads to a row
           const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
 #pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 4 * kConvWarps) {
+          for (int r0 = 0; r0 < rows; r0 += 8) {
             const int r = r0 + (tid >> 3);
-            uint8_t* line = sq + qring.i * Sh::kQBytes + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
+            uint8_t* line = sq + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
             uint4 x[NC];
             uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
-              const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+              const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
+              for (int j = 0; j < 4; ++j) top = max(top, max(y[j] & 0x7fffu, y[j] >> 16 & 0x7fffu));
             }
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -852,97 +845,83 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+              uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const __half2 hv = __floats2half2_rn(bf16_lo(v[j]) * f, bf16_hi(v[j]) * f);
-                v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+                const __half2 hv = __floats2half2_rn(bf16_lo(y[j]) * f, bf16_hi(y[j]) * f);
+                y[j] = *reinterpret_cast<const uint32_t*>(&hv);
               }
-              *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            if ((tid & 7) == 0) s_qs[slot * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+            if ((tid & 7) == 0) s_qs[at.i * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[qring.i]);
-        qring.step();
+        if (lane == 0) mbar_arrive(q_full);
       }
-      if (Two) {
-        vk = s.k0 + t;
-        vseen = seen;
-        vkeys = s.keys;
-        vpart = np - 1;
-      }
-      // K of this tile; V of the one before, or (Two) of this one. A warp has 32
-      // rows of a block.
+      at.step();
+      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
 #pragma unroll 1
-      for (int op = go ? 0 : NG; op < (have || Two ? 2 * NG : NG); ++op) {
-        const bool v = op >= NG;
-        const uint32_t ri = v ? rvals.i : rkeys.i, bi = v ? vals.i : keys.i;
-        if (!(ok = wait(v ? &rv_full[ri] : &rk_full[ri], v ? rvals.phase : rkeys.phase, 13))) break;
-        if (!(ok = wait(v ? &v_free[bi] : &k_free[bi], (v ? vals.phase : keys.phase) ^ 1, 14))) break;
-        const uint8_t* src = (v ? raw_values : raw_keys) + ri * Sh::kRawBlock + 2048 * GC * w + 16 * lane;
-        // a lane's piece of 16 columns: 4 or 8 lanes to a row of 64 or 128 bytes
-        constexpr int kLanes = 4 * GC, kRows = 32 / kLanes, kPieces = 32 / kRows;
-        const int row = 32 * w + lane / kLanes, pc = lane % kLanes;
-        uint8_t* dst = (v ? s_values : s_keys) + bi * Sh::kBlock + (pc >> 2) * kSlotBytes + 128 * row;
-        // (the two chunks' lanes store their halves in opposite order: no bank is met twice)
-        const int odd = pc >> 2, p0 = 2 * (pc & 3) + odd, p1 = 2 * (pc & 3) + 1 - odd;
-        const bool clear = v && 128 * (vk + 1) > vseen;
-        bool any = false;
+      for (int kb = NG * s.k0; kb < NG * s.k1; ++kb) {
+        const int k = kb / NG;
+        if (!(ok = wait(&rfull[ri], rphase, 13))) break;
+        if (!(ok = wait(&bfree[bi], bphase ^ 1, 14))) break;
+        // a lane's piece of 16 columns of chunk c: row 8 i + lane / 4 of the warp's 64
+        const int row = 64 * w + (lane >> 2), piece = lane & 3;
+        uint8_t* dst = blocks + bi * Sh::kBlock + 128 * row;
+        const uint8_t* src = raw + ri * Sh::kRawBlock + 64 * GC * row + 16 * piece;
+        const int p0 = 16 * ((2 * piece) ^ (row & 7)), p1 = 16 * ((2 * piece + 1) ^ (row & 7));
 #pragma unroll 1
-        for (int i = 0; i < kPieces; i += 4) {
+        for (int i = 0; i < 8 * GC; i += 4) {
           uint4 x[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 512 * (i + j));
+          for (int j = 0; j < 4; ++j) {
+            const int n = i + j;   // chunk n / 8
+            x[j] = *reinterpret_cast<const uint4*>(src + 64 * (n >> 3) + 512 * GC * (n & 7));
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            const int n = i + j;
             const uint4 y = x[j];
-            const int r7 = (row + kRows * (i + j)) & 7;
-            uint8_t* line = dst + 128 * kRows * (i + j);
-            const uint4 lo = make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16), e4m3x2_f16x2(y.y),
-                                        e4m3x2_f16x2(y.y >> 16));
-            const uint4 hi = make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16), e4m3x2_f16x2(y.w),
-                                        e4m3x2_f16x2(y.w >> 16));
-            *reinterpret_cast<uint4*>(line + 16 * (p0 ^ r7)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(line + 16 * (p1 ^ r7)) = odd ? lo : hi;
+            uint8_t* line = dst + (n >> 3) * kSlotBytes + 1024 * (n & 7);
+            *reinterpret_cast<uint4*>(line + p0) = make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16),
+                                                              e4m3x2_f16x2(y.y), e4m3x2_f16x2(y.y >> 16));
+            *reinterpret_cast<uint4*>(line + p1) = make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16),
+                                                              e4m3x2_f16x2(y.w), e4m3x2_f16x2(y.w >> 16));
           }
         }
-        if (clear) {
+        if (v && 128 * (k + 1) > seen) {
           // values of a tile that not every row sees whole: what some row must
           // not see is cleared, keys past the row tile's own, and what is no number
+          bool any = false;
 #pragma unroll 1
-          for (int i = 0; i < 2 * kPieces; ++i) {
-            const int r = row + kRows * (i >> 1), key = 128 * vk + r;
-            uint4* y = reinterpret_cast<uint4*>(dst + 128 * kRows * (i >> 1) + 16 * ((i & 1 ? p1 : p0) ^ (r & 7)));
-            if (key < vseen) continue;
-            uint4 x = key < vkeys ? *y : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 16 * GC; ++i) {
+            const int n = i >> 1, key = 128 * k + row + 8 * (n & 7);
+            uint4* y = reinterpret_cast<uint4*>(dst + (n >> 3) * kSlotBytes + 1024 * (n & 7) + (i & 1 ? p1 : p0));
+            if (key < seen) continue;
+            uint4 x = key < s.keys ? *y : make_uint4(0, 0, 0, 0);
             any |= clear_unbounded<true>(x);
             *y = x;
           }
-          if (any) s_unbounded[vpart % kParts] = (int)vpart + 1;
+          if (any) s_unbounded[np % kParts] = (int)np + 1;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(v ? &v_full[bi] : &k_full[bi]);
-          mbar_arrive(v ? &rv_empty[ri] : &rk_empty[ri]);
+          mbar_arrive(&bfull[bi]);
+          mbar_arrive(&rempty[ri]);
         }
-        if (v) {
-          vals.step();
-          rvals.step();
-        } else {
-          keys.step();
-          rkeys.step();
+        if (++ri == raw_places) {
+          ri = 0;
+          rphase ^= 1;
+        }
+        if (++bi == places) {
+          bi = 0;
+          bphase ^= 1;
         }
       }
-      have = go && !Two;
-      vk = s.k0 + t;
-      vseen = seen;
-      vkeys = s.keys;
-      vpart = np - 1;
-      t += go;
+      ++np;
     }
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------- softmax, output
@@ -1233,16 +1212,16 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
 }
 
 // Joins the parts of the row tiles that CTAs share: block (c, y) takes some units
-// of the tile that CTA c began, a unit being 8 columns of 32 rows, a row per
+// of the tile that CTA c began, a unit being 4 columns of 32 rows, a row per
 // lane. A unit has as many warps as 4 parts each need, up to all 8, which take
 // alternate parts and add up through shared memory.
 constexpr int kJoinWarps = 8, kJoinBlocks = 16;
 template <int D, int QT>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaParams p) {
   pdl_begin();
   const AttnShared s = p.shared[blockIdx.x];
   if (s.count == 0) return;
-  constexpr int V = 8, U = 4, kRows = 128 * QT;
+  constexpr int V = 4, U = 4, kRows = 128 * QT;
   __shared__ float s_o[kJoinWarps][V][32];
   __shared__ float2 s_ml[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1303,9 +1282,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join(const TaParams
     if (on && sub == 0) {
       const float scale = l == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / l;
       const int tok = s.row + tile * p.R + row / p.G;
-      *reinterpret_cast<uint4*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
-          make_uint4(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale),
-                     pack_bf16x2(o[4] * scale, o[5] * scale), pack_bf16x2(o[6] * scale, o[7] * scale));
+      *reinterpret_cast<uint2*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
+          make_uint2(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale));
     }
   }
 }
@@ -1331,7 +1309,7 @@ cudaError_t launch(TaParams& p, int num_sms, cudaStream_t st) {
   auto kern = tree_attn_kernel<D, E, Two>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Sh::kSmem);
   const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-  p.inv_ctas = 1.000002f / ctas;
+  p.inv_ctas = ~0ull / ctas + 1;
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, st, p);
   if (e == cudaSuccess)
     e = launch_pdl(tree_attn_join<D, Sh::QT>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
