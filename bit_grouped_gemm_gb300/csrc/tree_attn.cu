@@ -38,8 +38,10 @@ namespace moe {
 namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
-// warps 0..7 softmax, 8 loads keys, 9 products, 10 plans, 11 loads values, 12..15 convert (e4m3)
-constexpr int kSoftWarps = 8, kKeyWarp = 8, kMmaWarp = 9, kPlanWarp = 10, kValueWarp = 11, kConvWarp = 12,
+// warps 0..7 softmax, 8 loads, 9 products with keys, 10 plans, 11 products with values,
+// 12..15 convert (e4m3). (One warp for both kinds of product would bound the kernel: its
+// waits, commits and issue take longer than the products.)
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kScoreWarp = 9, kPlanWarp = 10, kSumWarp = 11, kConvWarp = 12,
               kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512, kColS = 256;
@@ -140,6 +142,17 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
+}
+
+// (with its wait)
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -510,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 * QT : 0));
   uint64_t* s_full = bars;               // [2] scores, by key tile; Two: by row tile, as the next four
   uint64_t* p_full = s_full + 2;         // [2] weights
-  uint64_t* pv_done = p_full + 2;        // [2] products with values (Two: a part's last)
+  uint64_t* pv_done = p_full + 2;        // [2] products with values
   uint64_t* o_free = pv_done + 2;        // [OB] sums written
   uint64_t* k_full = o_free + 2;
   uint64_t* v_full = k_full + KS;
@@ -526,13 +539,13 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint64_t* pair = q_empty + QB;         // [4]
   uint64_t* part_full = pair + 4;        // [kParts]
   uint64_t* part_empty = part_full + kParts;
-  uint64_t* drain = part_empty + kParts;
-  Part* parts = reinterpret_cast<Part*>(drain + 1);
+  uint64_t* drain = part_empty + kParts;   // [2]
+  Part* parts = reinterpret_cast<Part*>(drain + 2);
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
-  constexpr int kBars = 8 + 2 * (KS + VS + KR + VR) + 3 * QB + 4 + 2 * kParts + 1;
+  constexpr int kBars = 8 + 2 * (KS + VS + KR + VR) + 3 * QB + 4 + 2 * kParts + 2;
   static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
   uint64_t* k_free = Sh::kKeysWithScores ? s_full : k_own;
@@ -557,7 +570,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -570,11 +583,6 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
            wait_longer(smem_u32(bar), parity, abort_flag, &p.err, site);
   };
   pdl_begin();
-  // Order of the products. One row tile: the scores run one key tile ahead, S0 S1
-  // O0 S2 O1 .., through the ends of parts, too, where the next part's queries
-  // have a place of their own (QB 2); else a part's last O comes before the next
-  // part's S0. Two row tiles a and b: Sa0 Sb0 | Oa0 Sa1 Ob0 Sb1 | ..
-
   if (warp == kPlanWarp) {
     // ------------------------------------- the CTA's parts, for all others
     Walk walk(p, parts + kParts);
@@ -623,20 +631,19 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     AttnShared m = walk.shared();
     if (*abort_flag) m.count = 0;
     if (lane == 0) p.shared[blockIdx.x] = m;
-  } else if (warp == kKeyWarp || warp == kValueWarp) {
-    // ------------------------------------- loads of keys or values, by TMA
-    const bool v = warp == kValueWarp;
+  } else if (warp == kLoadWarp) {
+    // ---------------------------------------------------- loads, by TMA
     const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
     const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a block)
     const int y_mask = (1 << p.a.page_shift) - 1;
     constexpr int kBytes = E ? Sh::kRawBlock : Sh::kBlock, kRow = E ? 64 * GC : 128;
-    const CUtensorMap* map = v ? &p.mv : &p.mk;
-    uint64_t* bar_full = E ? (v ? rv_full : rk_full) : v ? v_full : k_full;
-    uint64_t* bar_free = E ? (v ? rv_empty : rk_empty) : v ? v_free : k_free;
-    uint8_t* ring = E ? (v ? raw_values : raw_keys) : v ? s_values : s_keys;
-    const uint32_t places = E ? (v ? VR : KR) : v ? VS : KS;
-    uint32_t i = 0, phase = 0, loads = 0;
+    constexpr int kKeys = E ? KR : KS, kValues = E ? VR : VS;
+    uint64_t *kf = E ? rk_full : k_full, *ke = E ? rk_empty : k_free, *vf = E ? rv_full : v_full,
+             *ve = E ? rv_empty : v_free;
+    Ring<kKeys> keys;
+    Ring<kValues> vals;
     Ring<kParts> at;
+    uint32_t nk = 0, nv = 0;   // blocks loaded
     bool ok = true, bad = false;
     while (ok) {
       if (!(ok = wait(&part_full[at.i], at.phase, 3))) break;
@@ -644,163 +651,141 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       if (s.stop) break;
       // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
       int win = 0, now = s_pages[32 * at.i + lane], later = first_pages(p, s, s.k0 + (32 >> box_log), lane);
+      int id = 0, before = 0;   // this lane's box's page, of the tile at hand and the one before
       at.step();
+      // K0 | K1 V0 | K2 V1 | .. | V(n - 1)
 #pragma unroll 1
-      for (int k = s.k0; k < s.k1 && ok; ++k) {
-        int id = __shfl_sync(0xffffffffu, now, ((k - s.k0) << box_log) - win + my_box);
-        if ((k + 1 - s.k0) << box_log == win + 32) {
-          win += 32;
-          now = later;
-          later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
+      for (int k = s.k0; k <= s.k1 && ok; ++k) {
+        if (k < s.k1) {
+          id = __shfl_sync(0xffffffffu, now, ((k - s.k0) << box_log) - win + my_box);
+          if ((k + 1 - s.k0) << box_log == win + 32) {
+            win += 32;
+            now = later;
+            later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
+          }
+          bad |= id == kBadPage;
+          if (id < 0) id = p.a.cache.pages;   // reads as zeros
         }
-        bad |= id == kBadPage;
-        if (id < 0) id = p.a.cache.pages;   // reads as zeros
-        const int y = (128 * k + my_box * box) & y_mask;
 #pragma unroll 1
-        for (int g = 0; g < NG; ++g) {
-          if (!(ok = wait(&bar_free[i], phase ^ 1, 4))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar_full[i], kBytes);
+        for (int op = k < s.k1 ? 0 : NG; op < (k > s.k0 ? 2 * NG : NG); ++op) {
+          const bool v = op >= NG;
+          const int i = v ? vals.i : keys.i, y = (128 * (k - v) + my_box * box) & y_mask;
+          const int c = (v ? op - NG : op) * GC + my_chunk;
+          uint64_t* bar = (v ? vf : kf) + i;
+          uint8_t* dst = (E ? (v ? raw_values : raw_keys) : v ? s_values : s_keys) + i * kBytes;
+          if (!(ok = wait((v ? ve : ke) + i, (v ? vals.phase : keys.phase) ^ 1, 4))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
           __syncwarp();
           if (my_chunk < (E ? 1 : GC))
-            tma_load_4d(ring + i * kBytes + my_chunk * kSlotBytes + my_box * box * kRow, map, 64 * (g * GC + my_chunk),
-                        y, s.h, id, &bar_full[i]);
-          ++loads;
-          if (++i == places) {
-            i = 0;
-            phase ^= 1;
+            tma_load_4d(dst + my_chunk * kSlotBytes + my_box * box * kRow, v ? &p.mv : &p.mk, 64 * c, y, s.h,
+                        v ? before : id, bar);
+          if (v) {
+            vals.step();
+            ++nv;
+          } else {
+            keys.step();
+            ++nk;
           }
         }
+        before = id;
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
-    if (!ok) drain_ring<4>(bar_full, i, phase, loads, places, p.err.limit_ns);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------- products
-    constexpr uint32_t kIdS = idesc_16(!E, 128, false), kIdO = idesc_16(!E, 64 * GC, true);
+    if (!ok) {
+      drain_ring<4>(kf, keys.i, keys.phase, nk, kKeys, p.err.limit_ns);
+      drain_ring<4>(vf, vals.i, vals.phase, nv, kValues, p.err.limit_ns);
+    }
+  } else if (warp == kScoreWarp) {
+    // ----------------------------------------------- S = Q K^T, by key tile
+    // (Two: for one row tile, then the other.) A place of scores is free once the
+    // product with the weights that took it is done.
+    constexpr uint32_t kId = idesc_16(!E, 128, false);
     const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), kd0 = smem_desc_sw128(smem_u32(s_keys));
-    const uint64_t vd0 = value_desc(smem_u32(s_values));
     Ring<KS> keys;
-    Ring<VS> vals;
     Ring<QB> qring;
     Ring<kParts> at;
-    uint32_t segs = 0, u = 0;
+    uint32_t u = 0;
     bool ok = true;
-    // Scores of the key tile in the blocks from r on, row tile at descriptor qd,
-    // into S buffer `buf`; the first of Two does not give the keys back.
-    auto scores = [&](Ring<KS> r, uint64_t qd, int buf, bool first, bool last) {
+    while (ok) {
+      if (!(ok = wait(&part_full[at.i], at.phase, 5))) break;
+      if (parts[at.i].stop) break;
+      int n = parts[at.i].k1 - parts[at.i].k0;
+      at.step();
+      if (!(ok = wait(&q_full[qring.i], qring.phase, 6))) break;
+      const uint64_t qd = qd0 + qring.i * (Sh::kQBytes / 16);
+      qring.step();
 #pragma unroll 1
-      for (int g = 0; g < NG; ++g, r.step()) {
-        if (first && !(ok = wait(&k_full[r.i], r.phase, 5))) break;
-        tc_fence_after();
-        if (elect_one_sync()) {
-          const uint64_t a = qd + g * (Sh::kBlock / 16), b = kd0 + r.i * (Sh::kBlock / 16);
+      for (; n > 0 && ok; --n, ++u) {
+#pragma unroll 1
+        for (int g = 0; g < NG * QT; ++g) {   // block by block; Two: both row tiles with the one block
+          const int buf = Two ? g : u & 1;
+          if ((Two ? g == 0 : true) && !(ok = wait(&k_full[keys.i], keys.phase, 7))) break;
+          if ((Two || g == 0) && !(ok = wait(&pv_done[buf], ((Two ? u : u >> 1) & 1) ^ 1, 8))) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint64_t a = qd + (Two ? g * (NC * kSlotBytes / 16) : g * (Sh::kBlock / 16));
+            const uint64_t b = kd0 + keys.i * (Sh::kBlock / 16);
 #pragma unroll
-          for (int c = 0; c < GC; ++c)
+            for (int c = 0; c < GC; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss(tmem + kColS + 128 * buf, a + (c * kSlotBytes + 32 * kk) / 16,
-                         b + (c * kSlotBytes + 32 * kk) / 16, kIdS, g != 0 || (c | kk) != 0);
-          if (!Sh::kKeysWithScores && last) mma_commit(&k_own[r.i]);
-          if (g == NG - 1) mma_commit(&s_full[buf]);
-        }
-        __syncwarp();
-      }
-    };
-    // O (+)= P V with the values in the blocks from r on.
-    auto values = [&](Ring<VS> r, uint32_t o, int buf, bool begin, uint64_t* done, bool first, bool last) {
-#pragma unroll 1
-      for (int g = 0; g < NG; ++g, r.step()) {
-        if (first && !(ok = wait(&v_full[r.i], r.phase, 6))) break;
-        tc_fence_after();
-        if (elect_one_sync()) {
-          const uint64_t b = vd0 + r.i * (Sh::kBlock / 16);
-          const uint32_t pc = tmem + kColS + 128 * buf;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
-            mma_f16_ts(o + 64 * GC * g, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)), b + (2048 >> 4) * kk,
-                       kIdO, !begin || kk != 0);
-          if (!Sh::kValuesWithProducts && last) mma_commit(&v_own[r.i]);
-          if (g == NG - 1 && done) mma_commit(done);
-        }
-        __syncwarp();
-      }
-    };
-    auto skip = [&](auto& r) {
-      for (int g = 0; g < NG; ++g) r.step();
-    };
-    if constexpr (Two) {
-      while (ok) {
-        if (!(ok = wait(&part_full[at.i], at.phase, 7))) break;
-        if (parts[at.i].stop) break;
-        const int n = parts[at.i].k1 - parts[at.i].k0;
-        at.step();
-        if (!(ok = wait(q_full, segs & 1, 8))) break;
-#pragma unroll 1
-        for (int t = -1; t < n && ok; ++t) {
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            if (t >= 0) {
-              if (!(ok = wait(&p_full[q], u & 1, 9))) break;
-              if (t == 0 && !(ok = wait(&o_free[q], (segs & 1) ^ 1, 10))) break;
-              values(vals, tmem + 128 * q, q, t == 0, t + 1 == n ? &pv_done[q] : nullptr, q == 0, q == 1);
-              if (!ok) break;
-            }
-            if (t + 1 < n) scores(keys, qd0 + q * (NC * kSlotBytes / 16), q, q == 0, q == 1);
-            if (!ok) break;
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_ss(tmem + kColS + 128 * buf, a + (c * kSlotBytes + 32 * kk) / 16,
+                           b + (c * kSlotBytes + 32 * kk) / 16, kId, (!Two && g != 0) || (c | kk) != 0);
+            if (!Sh::kKeysWithScores && (!Two || g == 1)) mma_commit(&k_own[keys.i]);
+            if (Two || g == NG - 1) mma_commit(&s_full[buf]);
+            if (n == 1 && g == NG * QT - 1) mma_commit(&q_empty[qring.i == 0 ? QB - 1 : qring.i - 1]);
           }
-          if (t + 1 < n) skip(keys);
-          if (t >= 0) skip(vals);
-          u += t >= 0;
-          if (t + 2 == n) {
-            if (elect_one_sync()) mma_commit(q_empty);
-            __syncwarp();
-          }
+          __syncwarp();
+          if (!Two || g == 1) keys.step();
         }
-        ++segs;
-      }
-    } else {
-      bool have = false, first = false, stop = false;   // key tile u - 1's values are to be added
-      int t = 0, n = 0;
-      uint32_t vob = 0;
-      while (ok) {
-        if (t == n && !stop) {
-          if (!(ok = wait(&part_full[at.i], at.phase, 7))) break;
-          stop = parts[at.i].stop;
-          n = stop ? 0 : parts[at.i].k1 - parts[at.i].k0;
-          t = 0;
-          at.step();
-        }
-        const bool go = !stop && !(QB == 1 && have && t == 0);
-        if (!go && !have) break;
-        if (go) {
-          if (t == 0 && !(ok = wait(&q_full[qring.i], qring.phase, 8))) break;
-          scores(keys, qd0 + qring.i * (Sh::kQBytes / 16), u & 1, true, true);
-          if (!ok) break;
-          skip(keys);
-          if (t + 1 == n) {
-            if (elect_one_sync()) mma_commit(&q_empty[qring.i]);
-            __syncwarp();
-            qring.step();
-          }
-        }
-        if (have) {
-          const uint32_t w = u - 1, ob = vob % OB;
-          if (!(ok = wait(&p_full[w & 1], (w >> 1) & 1, 9))) break;
-          if (first && !(ok = wait(&o_free[ob], ((vob / OB) & 1) ^ 1, 10))) break;
-          values(vals, tmem + 128 * ob, w & 1, first, &pv_done[w & 1], true, true);
-          skip(vals);
-        }
-        have = go;
-        first = t == 0;
-        vob = segs;
-        u += go;
-        t += go;
-        if (go && t == n) ++segs;
       }
     }
     if (elect_one_sync()) mma_commit(drain);
     __syncwarp();
     mbar_wait_drain(drain, 0, p.err.limit_ns);
+  } else if (warp == kSumWarp) {
+    // ---------------------------------------------------------- O += P V
+    constexpr uint32_t kId = idesc_16(!E, 64 * GC, true);
+    const uint64_t vd0 = value_desc(smem_u32(s_values));
+    Ring<VS> vals;
+    Ring<OB> oring;
+    Ring<kParts> at;
+    uint32_t u = 0;
+    bool ok = true;
+    while (ok) {
+      if (!(ok = wait(&part_full[at.i], at.phase, 9))) break;
+      if (parts[at.i].stop) break;
+      const int n = parts[at.i].k1 - parts[at.i].k0;
+      at.step();
+#pragma unroll 1
+      for (int t = 0; t < n && ok; ++t, ++u) {
+#pragma unroll 1
+        for (int g = 0; g < NG * QT; ++g) {
+          const int buf = Two ? g : u & 1;
+          if ((Two || g == 0) && !(ok = wait(&p_full[buf], (Two ? u : u >> 1) & 1, 10))) break;
+          if (t == 0 && (Two || g == 0) && !(ok = wait(&o_free[Two ? g : oring.i], oring.phase ^ 1, 11))) break;
+          if ((Two ? g == 0 : true) && !(ok = wait(&v_full[vals.i], vals.phase, 12))) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint64_t b = vd0 + vals.i * (Sh::kBlock / 16);
+            const uint32_t pc = tmem + kColS + 128 * buf;
+            const uint32_t o = tmem + (Two ? 128 * g : 128 * oring.i + 64 * GC * g);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
+              mma_f16_ts(o, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)), b + (2048 >> 4) * kk, kId,
+                         t != 0 || kk != 0);
+            if (!Sh::kValuesWithProducts && (!Two || g == 1)) mma_commit(&v_own[vals.i]);
+            if (Two || g == NG - 1) mma_commit(&pv_done[buf]);
+          }
+          __syncwarp();
+          if (!Two || g == 1) vals.step();
+        }
+      }
+      oring.step();
+    }
+    if (elect_one_sync()) mma_commit(drain + 1);
+    __syncwarp();
+    mbar_wait_drain(drain + 1, 0, p.err.limit_ns);
   } else if (E && warp >= kConvWarp) {   // (8-bit caches have one place for queries)
     // ------------------- e4m3 chunks to fp16, exactly; queries to fp16, each
     // row times the power of two that brings its largest element to 2^14..2^15
@@ -976,7 +961,10 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         tc_fence_after();
         if (E && t == 0) c2 = fmaxf(c2 * s_qs[pi * 128 * QT + (Two ? 128 * half : 0) + row], 1e-37f);
         if (work) {
-          uint32_t x[2][32];
+          // Chunks of 32 scores. One: a row's two stay in registers. Two: of four, the
+          // first three (fp16: two) stay; the others are read again for their weights.
+          constexpr int kKeep = Two && !E ? 3 : 2;
+          uint32_t x[kKeep][32];
           if (masked) {
             // hidden scores are set to -inf in place
             const unsigned long long* words =
@@ -1004,19 +992,37 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             }
             return fmaxf(a, b);
           };
-          // the scores are read twice, 32 at a time: 64 or 128 of them beside their
-          // weights would not fit the registers
-          float top = -INFINITY;
-          tmem_ld_32x32b_x32(sc, x[0]);
-          tmem_wait_ld(x[0]);
-#pragma unroll
-          for (int i = 0; i < CW; i += 64) {
-            tmem_ld_32x32b_x32(sc + i + 32, x[1]);
-            top = fmaxf(top, largest(x[0]));
-            tmem_wait_ld(x[1]);
-            tmem_ld_32x32b_x32(sc + (i + 64) % CW, x[0]);   // (at the end the first again, for the weights)
-            top = fmaxf(top, largest(x[1]));
+          float top;
+          if constexpr (Two) {
+            if constexpr (E) {
+              tmem_ld_32x32b_x32(sc + 64, x[0]);
+              tmem_ld_32x32b_x32(sc + 96, x[1]);
+              tmem_wait_ld(x[0]);
+              tmem_wait_ld(x[1]);
+              top = fmaxf(largest(x[0]), largest(x[1]));
+              tmem_ld_32x32b_x32(sc, x[0]);
+              tmem_ld_32x32b_x32(sc + 32, x[1]);
+              tmem_wait_ld(x[0]);
+              tmem_wait_ld(x[1]);
+              top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
+            } else {
+              tmem_ld_32x32b_x32(sc + 96, x[0]);
+              tmem_wait_ld(x[0]);
+              tmem_ld_32x32b_x32(sc + 32, x[1]);
+              tmem_ld_32x32b_x32(sc + 64, x[kKeep - 1]);
+              top = largest(x[0]);
+              tmem_ld_32x32b_x32(sc, x[0]);
+              tmem_wait_ld(x[0]);
+              tmem_wait_ld(x[1]);
+              tmem_wait_ld(x[kKeep - 1]);
+              top = fmaxf(fmaxf(top, largest(x[0])), fmaxf(largest(x[1]), largest(x[kKeep - 1])));
+            }
+          } else {
+            tmem_ld_32x32b_x32(sc, x[0]);
+            tmem_ld_32x32b_x32(sc + 32, x[1]);
             tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            top = fmaxf(largest(x[0]), largest(x[1]));
           }
           if constexpr (!Two) {
             s_max[256 * buf + 128 * half + row] = top;
@@ -1029,7 +1035,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           const float old = m;
           if (grow && top > m) m = top;
           if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
-            // The last product has to be done. (Two: these scores came after it.)
+            // The last product has to be done. (Two: these scores waited for it.)
             if (!Two) {
               if (!(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 18))) break;
               tc_fence_after();
@@ -1038,12 +1044,12 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             const uint32_t oc = tmem + lanes + 128 * (Two ? half : (int)(segs % OB)) + oc0;
             l *= f;
 #pragma unroll 1
-            for (int i = 0; i < OW; i += 32) {
-              tmem_ld_32x32b_x32(oc + i, x[1]);
-              tmem_wait_ld(x[1]);
+            for (int i = 0; i < OW; i += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(oc + i, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[1][j] = __float_as_uint(__uint_as_float(x[1][j]) * f);
-              tmem_st_32x32b_x32(oc + i, x[1]);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_32x32b_x16(oc + i, o);
             }
           }
           // with fp16 weights the reference is 2^7 below the maximum, which keeps
@@ -1067,16 +1073,23 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             }
             tmem_st_32x32b_x16(sc + i / 2, w);   // (in the place of scores that are read)
           };
-#pragma unroll
-          for (int i = 0; i < CW; i += 64) {
-            tmem_ld_32x32b_x32(sc + i + 32, x[1]);
-            tmem_wait_ld(x[1]);
-            weights(x[0], i);
-            if (i + 64 < CW) {
-              tmem_ld_32x32b_x32(sc + i + 64, x[0]);
+          weights(x[0], 0);
+          if constexpr (Two) {
+            tmem_ld_32x32b_x32(sc + (E ? 64 : 96), x[0]);
+            weights(x[1], 32);
+            if constexpr (E) {
+              tmem_ld_32x32b_x32(sc + 96, x[1]);
               tmem_wait_ld(x[0]);
+              tmem_wait_ld(x[1]);
+              weights(x[0], 64);
+              weights(x[1], 96);
+            } else {
+              weights(x[kKeep - 1], 64);
+              tmem_wait_ld(x[0]);
+              weights(x[0], 96);
             }
-            weights(x[1], i + 32);
+          } else {
+            weights(x[1], 32);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
@@ -1086,8 +1099,8 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           // nobody's, others only where they are no numbers. (Two: both groups
           // of warps clear all of them, with the same result.)
           // The block that had the place before is consumed, so that the wait for
-          // this one is for its phase: these scores came after the product of tile
-          // u - 2; with two blocks to a tile the last product is waited for.
+          // this one is for its phase: these scores waited for the product of tile
+          // u - 2; with two blocks to a tile the last product is waited for, too.
           if (NG > 1 && u > 0 && !(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 19))) break;
           const int key = threadIdx.x & 127, j = 128 * k + key, keys = parts[pi].keys;
           bool any = false;
@@ -1131,8 +1144,8 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
         const Part& s = parts[fp % kParts];
         const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
         // its last product: of the tile before this one, or of the last one
-        const uint32_t w = stop ? u - 1 : u - 2;
-        if (!(ok = wait(&pv_done[Two ? half : w & 1], (Two ? seg : w >> 1) & 1, 21))) break;
+        const uint32_t w = Two || stop ? u - 1 : u - 2;
+        if (!(ok = wait(&pv_done[Two ? half : w & 1], (Two ? w : w >> 1) & 1, 21))) break;
         tc_fence_after();
         if (32 * quarter < rows) {
           if (!Two) {
@@ -1205,15 +1218,15 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
 // Joins the parts of the row tiles that CTAs share: block (c, y) takes some units
-// of the tile that CTA c began, a unit being 4 columns of 32 rows, a row per
-// lane. A unit has as many warps as 4 parts each need, up to all 8, which take
+// of the tile that CTA c began, a unit being 8 columns of 32 rows, a row per
+// lane. A unit has as many warps as 2 parts each need, up to all 8, which take
 // alternate parts and add up through shared memory.
 constexpr int kJoinWarps = 8, kJoinBlocks = 16;
 template <int D, int QT>
@@ -1221,7 +1234,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
   pdl_begin();
   const AttnShared s = p.shared[blockIdx.x];
   if (s.count == 0) return;
-  constexpr int V = 4, U = 4, kRows = 128 * QT;
+  constexpr int V = 8, U = 2, kRows = 128 * QT;
   __shared__ float s_o[kJoinWarps][V][32];
   __shared__ float2 s_ml[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1282,8 +1295,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
     if (on && sub == 0) {
       const float scale = l == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / l;
       const int tok = s.row + tile * p.R + row / p.G;
-      *reinterpret_cast<uint2*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
-          make_uint2(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale));
+      *reinterpret_cast<uint4*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
+          make_uint4(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale),
+                     pack_bf16x2(o[4] * scale, o[5] * scale), pack_bf16x2(o[6] * scale, o[7] * scale));
     }
   }
 }
