@@ -42,17 +42,15 @@ struct AttnArgs {
 };
 
 // Scratch: a CTA leaves the sums of at most two row tiles that it shares with
-// other CTAs (or pairs of tiles, where tensor memory holds the sums of two), and
-// says which shared tile it begins.
+// other CTAs, each of up to 128 rows, and says which shared tile it begins.
 constexpr int kAttnMaxCtas = 160;
 struct AttnShared {
   int row, tokens, head;   // first token row, tokens and key-value head of the tile
   int first, count;        // CTAs that hold its parts; count 0: none
   int pad[3];
 };
-constexpr int attn_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 constexpr size_t attn_scratch_bytes(int head_dim) {
-  return kAttnMaxCtas * (sizeof(AttnShared) + 2 * (size_t)attn_rows(head_dim) * (head_dim + 2) * 4);
+  return kAttnMaxCtas * (sizeof(AttnShared) + 2 * 128 * ((size_t)head_dim + 2) * 4);
 }
 cudaError_t launch_tree_attention(const AttnArgs& a, void* scratch, int num_sms, DevErr err,
                                   cudaStream_t st);

@@ -44,34 +44,31 @@ constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 constexpr int kSoftWarps = 8, kLoadWarp = 8, kScoreWarp = 9, kPlanWarp = 10, kSumWarp = 11, kConvWarp = 12,
               kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
-constexpr uint32_t kTmemCols = 512, kColS = 256;
+constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
 constexpr int kParts = 4;                    // parts told ahead
 
-// E: an e4m3 cache. Two: two row tiles at a time. Keys and values of a key tile
-// come in blocks of up to 128 columns, each kind with its own ring of them.
-template <int D, bool E, bool Two>
+// E: an e4m3 cache. Keys and values of a key tile come in blocks of up to 128
+// columns, each kind with its own ring of them.
+template <int D, bool E>
 struct Shape {
   static constexpr int NC = D / 64;                  // chunks of 64 columns
   static constexpr int GC = NC < 2 ? NC : 2;         // chunks of a block
   static constexpr int NG = NC / GC;                 // blocks of a tile
   static constexpr int KS = D == 64 ? 4 : 2;         // blocks of keys held
   static constexpr int VS = D == 64 ? 4 : E ? 1 : 2; // and of values
-  static constexpr int KR = E ? (D == 64 || (D == 128 && !Two) ? 3 : 2) : 0;   // 8-bit blocks of keys
-  static constexpr int VR = E ? (D == 64 ? 3 : D == 128 && !Two ? 2 : 1) : 0;   // and of values
-  static constexpr int QT = Two ? 2 : 1;             // row tiles at a time
-  static constexpr int QB = Two || E || D == 256 ? 1 : 2;   // parts whose queries are held
-  static constexpr int OB = Two || D == 256 ? 1 : 2;        // parts whose sums are held
-  // A barrier less where a block is a tile and goes with the scores' or weights' two
-  // places: that the scores are there (the product is done) says that the block is free.
-  static constexpr bool kKeysWithScores = !Two && NG == 1 && KS == 2;
-  static constexpr bool kValuesWithProducts = !Two && NG == 1 && VS == 2;
+  static constexpr int KR = E ? (D == 256 ? 2 : 3) : 0;   // 8-bit blocks of keys
+  static constexpr int VR = E ? (D == 64 ? 3 : D == 128 ? 2 : 1) : 0;   // and of values
+  static constexpr int QB = E || D == 256 ? 1 : 2;   // parts whose queries are held
+  static constexpr int SB = D == 256 ? 2 : 3;        // key tiles whose scores or weights are held
+  static constexpr int OB = D == 64 ? 2 : 1;         // parts whose sums are held
+  static constexpr int kColS = 512 - 128 * SB;       // tensor memory: sums, then scores
   static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kConvWarp);
   static constexpr int kBlock = GC * kSlotBytes, kRawBlock = kBlock / 2;
-  static constexpr int kQBytes = QT * NC * kSlotBytes;
-  static constexpr int kMisc = 5632 + (E ? kParts * 512 * QT : 0);
+  static constexpr int kQBytes = NC * kSlotBytes;
+  static constexpr int kMisc = 5632 + (E ? kParts * 512 : 0);
   static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + (KS + VS) * kBlock + (KR + VR) * kRawBlock;
-  static_assert(!Two || D <= 128, "tensor memory holds the sums of two row tiles of 128 columns");
+  static_assert(OB * D <= kColS, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -79,12 +76,11 @@ struct TaParams {
   CUtensorMap mq, mk, mv;
   AttnArgs a;
   AttnShared* shared;
-  float2* ml;          // [cta][2][128 QT] maximum (log2) and sum
-  float* o;            // [cta][2][D][128 QT]: a warp stores a column of its 32 rows at a time
+  float2* ml;          // [cta][2][128] maximum (log2) and sum
+  float* o;            // [cta][2][D][128]: a warp stores a column of its 32 rows at a time
   unsigned long long inv_ctas;   // 2^64 / CTAs, rounded up
   int G, R;            // query heads per key-value head, tokens per row tile
-  int step;            // tokens of a row tile, or of two
-  unsigned inv_step;   // 2^31 / step, rounded up
+  unsigned inv_r;      // 2^31 / R, rounded up
   DevErr err;
 };
 
@@ -191,18 +187,18 @@ __device__ __forceinline__ Req req_of(const TaParams& p, int lo, int hi, int len
   len = min(len, p.a.table_width << p.a.page_shift);
   r.ctx = len >= r.n ? len - r.n : -1;
   // (exact: the quotient's error is below (2^20 + 2^8) 2^8 / 2^31 of one)
-  r.tiles = (int)((unsigned long long)(unsigned)(r.n + p.step - 1) * p.inv_step >> 31);
+  r.tiles = (int)((unsigned long long)(unsigned)(r.n + p.R - 1) * p.inv_r >> 31);
   return r;
 }
 
 __device__ __forceinline__ int keys_of(const TaParams& p, const Req& r, int t) {
-  return r.ctx < 0 ? 0 : r.ctx + min(r.n, (t + 1) * p.step);
+  return r.ctx < 0 ? 0 : r.ctx + min(r.n, (t + 1) * p.R);
 }
 // cost of a request's first t row tiles under one head (all but the last are full)
 __device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r, int t) {
   if (t == 0) return 0;
   long long c = (long long)t * (kItemCost + max(r.ctx, 0));
-  if (r.ctx >= 0) c += (long long)p.step * t * (t + 1) / 2;
+  if (r.ctx >= 0) c += (long long)p.R * t * (t + 1) / 2;
   return c;
 }
 __device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
@@ -223,7 +219,7 @@ __device__ __forceinline__ int search(int n, long long x, F f) {
   return lo;
 }
 
-// A CTA's part of a row tile (or of two): key tiles [k0, k1) of nk.
+// A CTA's part of a row tile: key tiles [k0, k1) of nk.
 struct Part {
   int b, h, row, tok0, tokens, ctx, keys, k0, k1, nk;
   int place;       // of the sums in scratch, if others hold parts of the tile
@@ -337,8 +333,8 @@ struct Walk {
       s.b = b;
       s.h = h;
       s.row = r.row;
-      s.tok0 = t * p.step;
-      s.tokens = min(p.step, r.n - s.tok0);
+      s.tok0 = t * p.R;
+      s.tokens = min(p.R, r.n - s.tok0);
       s.ctx = r.ctx;
       s.keys = keys;
       s.nk = nk;
@@ -503,12 +499,13 @@ __device__ __noinline__ void drain_ring(uint64_t* bars, uint32_t i, uint32_t pha
   }
 }
 
-template <int D, bool E, bool Two>
-__global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
+template <int D, bool E>
+__global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
-  using Sh = Shape<D, E, Two>;
+  using Sh = Shape<D, E>;
   constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, KR = Sh::KR, VR = Sh::VR,
-                QB = Sh::QB, OB = Sh::OB, QT = Sh::QT;
+                QB = Sh::QB, OB = Sh::OB, SB = Sh::SB;
+  constexpr uint32_t kColS = Sh::kColS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
@@ -517,27 +514,28 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint8_t* raw_keys = s_values + VS * Sh::kBlock;
   uint8_t* raw_values = raw_keys + KR * Sh::kRawBlock;
   uint8_t* misc = raw_values + VR * Sh::kRawBlock;
-  float* s_max = reinterpret_cast<float*>(misc);   // [2][2][128], then sums [2][128]
-  float* s_sum = s_max + 512;
-  float* s_qs = s_sum + 256;                       // [kParts][128 QT] factors of fp16 queries
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 * QT : 0));
-  uint64_t* s_full = bars;               // [2] scores, by key tile; Two: by row tile, as the next four
-  uint64_t* p_full = s_full + 2;         // [2] weights
-  uint64_t* pv_done = p_full + 2;        // [2] products with values
-  uint64_t* o_free = pv_done + 2;        // [OB] sums written
-  uint64_t* k_full = o_free + 2;
+  float* s_top = reinterpret_cast<float*>(misc);   // [2 groups][2][128] maxima handed on
+  float* s_sum = s_top + 512;                      // [2][128] a part's other group's sums
+  float* s_ref = s_sum + 256;                      // and the maxima that they refer to
+  float* s_qs = s_ref + 256;                       // [kParts][128] factors of fp16 queries
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 : 0));
+  uint64_t* s_full = bars;               // [SB] scores
+  uint64_t* p_full = s_full + SB;        // [SB] weights
+  uint64_t* pv_done = p_full + SB;       // [SB] products with values
+  uint64_t* o_free = pv_done + SB;       // [OB] sums written
+  uint64_t* k_full = o_free + OB;
   uint64_t* v_full = k_full + KS;
-  uint64_t* k_own = v_full + VS;         // blocks free again, where no barrier above says so
-  uint64_t* v_own = k_own + KS;
-  uint64_t* rk_full = v_own + VS;        // 8-bit blocks
+  uint64_t* k_free = v_full + VS;
+  uint64_t* v_free = k_free + KS;
+  uint64_t* rk_full = v_free + VS;       // 8-bit blocks
   uint64_t* rk_empty = rk_full + KR;
   uint64_t* rv_full = rk_empty + KR;
   uint64_t* rv_empty = rv_full + VR;
   uint64_t* q_raw = rv_empty + VR;       // [QB] queries landed (e4m3)
   uint64_t* q_full = q_raw + QB;         // [QB] queries ready
   uint64_t* q_empty = q_full + QB;
-  uint64_t* pair = q_empty + QB;         // [4]
-  uint64_t* part_full = pair + 4;        // [kParts]
+  uint64_t* hand = q_empty + QB;         // [4 quarters][2 groups][2] maxima handed on
+  uint64_t* part_full = hand + 16;       // [kParts]
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drain = part_empty + kParts;   // [2]
   Part* parts = reinterpret_cast<Part*>(drain + 2);
@@ -545,11 +543,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
-  constexpr int kBars = 8 + 2 * (KS + VS + KR + VR) + 3 * QB + 4 + 2 * kParts + 2;
-  static_assert((512 + 256 + (E ? kParts * 128 * QT : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
+  constexpr int kBars = 3 * SB + OB + 2 * (KS + VS + KR + VR) + 3 * QB + 16 + 2 * kParts + 2;
+  static_assert((512 + 512 + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
-  uint64_t* k_free = Sh::kKeysWithScores ? s_full : k_own;
-  uint64_t* v_free = Sh::kValuesWithProducts ? pv_done : v_own;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -557,11 +553,10 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
 #pragma unroll 1
     for (int i = 0; i < kBars; ++i) {
       uint64_t* b = bars + i;
-      const bool soft = (b >= p_full && b < p_full + 2) || (b >= o_free && b < o_free + 2);
-      const bool conv = E && ((b >= k_full && b < k_own) || (b >= rk_empty && b < rv_full) ||
+      const bool group = (b >= p_full && b < pv_done) || (b >= o_free && b < k_full);
+      const bool conv = E && ((b >= k_full && b < k_free) || (b >= rk_empty && b < rv_full) ||
                               (b >= rv_empty && b < q_raw) || (b >= q_full && b < q_empty));
-      mbar_init(b, soft ? (Two ? kSoftWarps / 2 : kSoftWarps) : conv ? kConvWarps / 2
-                   : b >= pair && b < part_full ? 2 : b >= part_empty && b < drain ? kSoftWarps : 1);
+      mbar_init(b, group ? kSoftWarps / 2 : b >= part_empty && b < drain ? kSoftWarps : conv ? kConvWarps / 2 : 1);
     }
     for (int i = 0; i < kParts; ++i) s_unbounded[i] = 0;
     *abort_flag = 0;
@@ -615,11 +610,10 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       if (!more || !(ok = wait(&q_empty[qring.i], qring.phase ^ 1, 2))) break;
       if (elect_one_sync()) {
         uint64_t* bar = E ? &q_raw[qring.i] : &q_full[qring.i];
-        mbar_arrive_expect_tx(bar, QT * NC * 128 * p.G * p.R);
+        mbar_arrive_expect_tx(bar, NC * 128 * p.G * p.R);
 #pragma unroll 1
-        for (int c = 0; c < QT * NC; ++c)
-          tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * (c % NC), s.h * p.G,
-                      s.row + s.tok0 + c / NC * p.R, bar);
+        for (int c = 0; c < NC; ++c)
+          tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * c, s.h * p.G, s.row + s.tok0, bar);
       }
       __syncwarp();
       qring.step();
@@ -697,14 +691,13 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
   } else if (warp == kScoreWarp) {
     // ----------------------------------------------- S = Q K^T, by key tile
-    // (Two: for one row tile, then the other.) A place of scores is free once the
-    // product with the weights that took it is done.
+    // (a place of scores is free once the product with the weights that took it is done)
     constexpr uint32_t kId = idesc_16(!E, 128, false);
     const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), kd0 = smem_desc_sw128(smem_u32(s_keys));
     Ring<KS> keys;
+    Ring<SB> sring;
     Ring<QB> qring;
     Ring<kParts> at;
-    uint32_t u = 0;
     bool ok = true;
     while (ok) {
       if (!(ok = wait(&part_full[at.i], at.phase, 5))) break;
@@ -713,32 +706,29 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       at.step();
       if (!(ok = wait(&q_full[qring.i], qring.phase, 6))) break;
       const uint64_t qd = qd0 + qring.i * (Sh::kQBytes / 16);
-      qring.step();
 #pragma unroll 1
-      for (; n > 0 && ok; --n, ++u) {
+      for (; n > 0 && ok; --n, sring.step()) {
+        if (!(ok = wait(&pv_done[sring.i], sring.phase ^ 1, 8))) break;
 #pragma unroll 1
-        for (int g = 0; g < NG * QT; ++g) {   // block by block; Two: both row tiles with the one block
-          const int buf = Two ? g : u & 1;
-          if ((Two ? g == 0 : true) && !(ok = wait(&k_full[keys.i], keys.phase, 7))) break;
-          if ((Two || g == 0) && !(ok = wait(&pv_done[buf], ((Two ? u : u >> 1) & 1) ^ 1, 8))) break;
+        for (int g = 0; g < NG; ++g, keys.step()) {
+          if (!(ok = wait(&k_full[keys.i], keys.phase, 7))) break;
           tc_fence_after();
           if (elect_one_sync()) {
-            const uint64_t a = qd + (Two ? g * (NC * kSlotBytes / 16) : g * (Sh::kBlock / 16));
-            const uint64_t b = kd0 + keys.i * (Sh::kBlock / 16);
+            const uint64_t a = qd + g * (Sh::kBlock / 16), b = kd0 + keys.i * (Sh::kBlock / 16);
 #pragma unroll
             for (int c = 0; c < GC; ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss(tmem + kColS + 128 * buf, a + (c * kSlotBytes + 32 * kk) / 16,
-                           b + (c * kSlotBytes + 32 * kk) / 16, kId, (!Two && g != 0) || (c | kk) != 0);
-            if (!Sh::kKeysWithScores && (!Two || g == 1)) mma_commit(&k_own[keys.i]);
-            if (Two || g == NG - 1) mma_commit(&s_full[buf]);
-            if (n == 1 && g == NG * QT - 1) mma_commit(&q_empty[qring.i == 0 ? QB - 1 : qring.i - 1]);
+                mma_f16_ss(tmem + kColS + 128 * sring.i, a + (c * kSlotBytes + 32 * kk) / 16,
+                           b + (c * kSlotBytes + 32 * kk) / 16, kId, g != 0 || (c | kk) != 0);
+            if (g == NG - 1) mma_commit(&s_full[sring.i]);
+            mma_commit(&k_free[keys.i]);
+            if (n == 1 && g == NG - 1) mma_commit(&q_empty[qring.i]);
           }
           __syncwarp();
-          if (!Two || g == 1) keys.step();
         }
       }
+      qring.step();
     }
     if (elect_one_sync()) mma_commit(drain);
     __syncwarp();
@@ -748,9 +738,9 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     constexpr uint32_t kId = idesc_16(!E, 64 * GC, true);
     const uint64_t vd0 = value_desc(smem_u32(s_values));
     Ring<VS> vals;
+    Ring<SB> sring;
     Ring<OB> oring;
     Ring<kParts> at;
-    uint32_t u = 0;
     bool ok = true;
     while (ok) {
       if (!(ok = wait(&part_full[at.i], at.phase, 9))) break;
@@ -758,27 +748,23 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       const int n = parts[at.i].k1 - parts[at.i].k0;
       at.step();
 #pragma unroll 1
-      for (int t = 0; t < n && ok; ++t, ++u) {
+      for (int t = 0; t < n && ok; ++t, sring.step()) {
+        if (!(ok = wait(&p_full[sring.i], sring.phase, 10))) break;
+        if (t == 0 && !(ok = wait(&o_free[oring.i], oring.phase ^ 1, 11))) break;
 #pragma unroll 1
-        for (int g = 0; g < NG * QT; ++g) {
-          const int buf = Two ? g : u & 1;
-          if ((Two || g == 0) && !(ok = wait(&p_full[buf], (Two ? u : u >> 1) & 1, 10))) break;
-          if (t == 0 && (Two || g == 0) && !(ok = wait(&o_free[Two ? g : oring.i], oring.phase ^ 1, 11))) break;
-          if ((Two ? g == 0 : true) && !(ok = wait(&v_full[vals.i], vals.phase, 12))) break;
+        for (int g = 0; g < NG; ++g, vals.step()) {
+          if (!(ok = wait(&v_full[vals.i], vals.phase, 12))) break;
           tc_fence_after();
           if (elect_one_sync()) {
             const uint64_t b = vd0 + vals.i * (Sh::kBlock / 16);
-            const uint32_t pc = tmem + kColS + 128 * buf;
-            const uint32_t o = tmem + (Two ? 128 * g : 128 * oring.i + 64 * GC * g);
+            const uint32_t pc = tmem + kColS + 128 * sring.i, o = tmem + D * oring.i + 64 * GC * g;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)   // 16 keys each; One: the second group's weights lie 64 columns on
-              mma_f16_ts(o, pc + (Two ? 8 * kk : 8 * (kk & 3) + 64 * (kk >> 2)), b + (2048 >> 4) * kk, kId,
-                         t != 0 || kk != 0);
-            if (!Sh::kValuesWithProducts && (!Two || g == 1)) mma_commit(&v_own[vals.i]);
-            if (Two || g == NG - 1) mma_commit(&pv_done[buf]);
+            for (int kk = 0; kk < 8; ++kk)   // 16 keys each
+              mma_f16_ts(o, pc + 8 * kk, b + (2048 >> 4) * kk, kId, t != 0 || kk != 0);
+            if (g == NG - 1) mma_commit(&pv_done[sring.i]);
+            mma_commit(&v_free[vals.i]);
           }
           __syncwarp();
-          if (!Two || g == 1) vals.step();
         }
       }
       oring.step();
@@ -807,39 +793,36 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
       if (s.stop) break;
       if (!v) {
         if (!(ok = wait(q_raw, np & 1, 12))) break;
+        const int rows = s.tokens * p.G;   // 8 threads to a row
 #pragma unroll 1
-        for (int q = 0; q < QT; ++q) {   // 8 threads to a row
-          const int rows = max(min(s.tokens - q * p.R, p.R), 0) * p.G;
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 8) {
-            const int r = r0 + (tid >> 3);
-            uint8_t* line = sq + q * NC * kSlotBytes + 128 * r + 16 * ((tid & 7) ^ (r & 7));
-            uint4 x[NC];
-            uint32_t top = 0;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          const int r = r0 + (tid >> 3);
+          uint8_t* line = sq + 128 * r + 16 * ((tid & 7) ^ (r & 7));
+          uint4 x[NC];
+          uint32_t top = 0;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
-              const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          for (int c = 0; c < NC; ++c) {
+            x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
+            const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) top = max(top, max(y[j] & 0x7fffu, y[j] >> 16 & 0x7fffu));
-            }
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            // exponent of the largest element, within what keeps both factors normal
-            const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
-            const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 hv = __floats2half2_rn(bf16_lo(y[j]) * f, bf16_hi(y[j]) * f);
-                y[j] = *reinterpret_cast<const uint32_t*>(&hv);
-              }
-              *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            if ((tid & 7) == 0) s_qs[at.i * 128 * QT + 128 * q + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+            for (int j = 0; j < 4; ++j) top = max(top, max(y[j] & 0x7fffu, y[j] >> 16 & 0x7fffu));
           }
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          // exponent of the largest element, within what keeps both factors normal
+          const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
+          const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 hv = __floats2half2_rn(bf16_lo(y[j]) * f, bf16_hi(y[j]) * f);
+              y[j] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          if ((tid & 7) == 0) s_qs[at.i * 128 + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -910,69 +893,53 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
     }
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------- softmax, output
-    const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+    // Two groups of 4 warps take alternate key tiles, a row per thread; a warp's
+    // lanes are those of its quarter of tensor memory. The running maximum goes
+    // from one group to the other, as soon as a tile's scores are read; each group
+    // keeps sums of its own, and the group of a part's last tile writes the part.
+    const int group = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    // One: 64 score columns and half of O's columns each; Two: a row tile each
-    constexpr int CW = Two ? 128 : 64, OW = Two ? D : D / 2;
-    const int q0 = Two ? half * p.R : 0, oc0 = Two ? 0 : half * OW;
-    const int row_tok = q0 + row / p.G, row_g = row % p.G;   // token of the part, query head of the group
-    uint32_t np = 0, segs = 0, u = 0, pairs = 0;
+    const int row_tok = row / p.G, row_g = row % p.G;   // token of the part, query head of the group
+    uint64_t* give = hand + 4 * quarter + 2 * group;
+    uint64_t* take = hand + 4 * quarter + 2 * (group ^ 1);
+    float* top_out = s_top + 256 * group + row;
+    const float* top_in = s_top + 256 * (group ^ 1) + row;
     Ring<kParts> at;
-    bool ok = true, stop = false, have = false;   // have: the part before is to be finished
-    float last_m = 0.0f, last_l = 0.0f, m = 0.0f, l = 0.0f, c2 = 0.0f;
-    int t = 0, n = 0, seen = 0, tok = 0, k0 = 0;
-    bool live = false, work = false;
-    // exchange between the two warps of a lane quarter (One)
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pair[quarter]);
-      return wait(&pair[quarter], pairs++ & 1, 15);
-    };
+    Ring<SB> sring;          // of key tile u
+    Ring<OB> oring;
+    uint32_t np = 0, u = 0, given = 0, taken = 0;
+    bool ok = true;
     while (ok) {
-      if (t == n && !stop) {
-        if (!(ok = wait(&part_full[at.i], at.phase, 16))) break;
-        const Part& s = parts[at.i];
-        stop = s.stop;
-        if (!stop) {
-          k0 = s.k0;
-          n = s.k1 - k0;
-          t = 0;
-          tok = s.tok0 + row_tok;
-          const int rows = max(min(s.tokens - q0, p.R), 0) * p.G;
-          live = row < rows;
-          work = 32 * quarter < rows;
-          // keys before `seen` are seen by every row
-          seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-          // scores in log2
-          c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
-          m = -INFINITY;
-          l = 0.0f;
-          ++np;
-          at.step();
-        }
-      }
-      if (stop && !have) break;
-      const uint32_t part = np - 1, pi = part % kParts;   // the part at hand
-      if (!stop) {
-        const int k = k0 + t, buf = Two ? half : u & 1;
-        const bool masked = 128 * (k + 1) > seen;
-        const uint32_t sc = tmem + lanes + kColS + 128 * buf + (Two ? 0 : 64 * half);
-        if (!(ok = wait(&s_full[buf], (Two ? u : u >> 1) & 1, 17))) break;
+      if (!(ok = wait(&part_full[at.i], at.phase, 16))) break;
+      const Part s = parts[at.i];
+      if (s.stop) break;
+      const int n = s.k1 - s.k0, rows = s.tokens * p.G, tok = s.tok0 + row_tok;
+      const bool live = row < rows, work = 32 * quarter < rows;
+      // keys before `seen` are seen by every row
+      const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+      const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
+      // scores in log2
+      float c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
+      float m = -INFINITY, l = 0.0f;   // the maximum referred to; sums of this group's tiles
+      int t = 0;
+      for (; t < n; ++t, ++u, sring.step()) {
+        if ((u & 1) != (uint32_t)group) continue;
+        const int k = s.k0 + t;
+        const bool masked = 128 * (k + 1) > seen, last = t + 1 == n;
+        const uint32_t sc = tmem + lanes + kColS + 128 * sring.i;
+        if (!(ok = wait(&s_full[sring.i], sring.phase, 17))) break;
         tc_fence_after();
-        if (E && t == 0) c2 = fmaxf(c2 * s_qs[pi * 128 * QT + (Two ? 128 * half : 0) + row], 1e-37f);
+        if (E && t < 2) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
         if (work) {
-          // Chunks of 32 scores. One: a row's two stay in registers. Two: of four, the
-          // first three (fp16: two) stay; the others are read again for their weights.
-          constexpr int kKeep = Two && !E ? 3 : 2;
+          // Chunks of 32 scores. Of the four, the first three (fp16: two) stay in
+          // registers; the others are read again for their weights.
+          constexpr int kKeep = E ? 2 : 3;
           uint32_t x[kKeep][32];
           if (masked) {
             // hidden scores are set to -inf in place
-            const unsigned long long* words =
-                p.a.mask ? p.a.mask + (long long)(parts[pi].row + tok) * p.a.mask_words : nullptr;
-            const int first = 128 * k + (Two ? 0 : 64 * half) - parts[pi].ctx;
 #pragma unroll 1
-            for (int i = 0; i < CW; i += 32) {
-              const uint32_t v = live ? (uint32_t)seen_bits(first + i, tok, words, p.a.mask_words) : 0;
+            for (int i = 0; i < 128; i += 32) {
+              const uint32_t v = live ? (uint32_t)seen_bits(128 * k + i - s.ctx, tok, words, p.a.mask_words) : 0;
               if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
               tmem_ld_32x32b_x32(sc + i, x[0]);
               tmem_wait_ld(x[0]);
@@ -993,58 +960,56 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             return fmaxf(a, b);
           };
           float top;
-          if constexpr (Two) {
-            if constexpr (E) {
-              tmem_ld_32x32b_x32(sc + 64, x[0]);
-              tmem_ld_32x32b_x32(sc + 96, x[1]);
-              tmem_wait_ld(x[0]);
-              tmem_wait_ld(x[1]);
-              top = fmaxf(largest(x[0]), largest(x[1]));
-              tmem_ld_32x32b_x32(sc, x[0]);
-              tmem_ld_32x32b_x32(sc + 32, x[1]);
-              tmem_wait_ld(x[0]);
-              tmem_wait_ld(x[1]);
-              top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
-            } else {
-              tmem_ld_32x32b_x32(sc + 96, x[0]);
-              tmem_wait_ld(x[0]);
-              tmem_ld_32x32b_x32(sc + 32, x[1]);
-              tmem_ld_32x32b_x32(sc + 64, x[kKeep - 1]);
-              top = largest(x[0]);
-              tmem_ld_32x32b_x32(sc, x[0]);
-              tmem_wait_ld(x[0]);
-              tmem_wait_ld(x[1]);
-              tmem_wait_ld(x[kKeep - 1]);
-              top = fmaxf(fmaxf(top, largest(x[0])), fmaxf(largest(x[1]), largest(x[kKeep - 1])));
-            }
-          } else {
+          if constexpr (E) {
+            tmem_ld_32x32b_x32(sc + 64, x[0]);
+            tmem_ld_32x32b_x32(sc + 96, x[1]);
+            tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            top = fmaxf(largest(x[0]), largest(x[1]));
             tmem_ld_32x32b_x32(sc, x[0]);
             tmem_ld_32x32b_x32(sc + 32, x[1]);
             tmem_wait_ld(x[0]);
             tmem_wait_ld(x[1]);
-            top = fmaxf(largest(x[0]), largest(x[1]));
-          }
-          if constexpr (!Two) {
-            s_max[256 * buf + 128 * half + row] = top;
-            if (!(ok = meet())) break;
-            top = fmaxf(top, s_max[256 * buf + 128 * (half ^ 1) + row]);
+            top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
+          } else {
+            tmem_ld_32x32b_x32(sc + 96, x[0]);
+            tmem_wait_ld(x[0]);
+            tmem_ld_32x32b_x32(sc + 32, x[1]);
+            tmem_ld_32x32b_x32(sc + 64, x[kKeep - 1]);
+            top = largest(x[0]);
+            tmem_ld_32x32b_x32(sc, x[0]);
+            tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            tmem_wait_ld(x[kKeep - 1]);
+            top = fmaxf(fmaxf(top, largest(x[0])), fmaxf(largest(x[1]), largest(x[kKeep - 1])));
           }
           top *= c2;
+          float old = -INFINITY;   // the maximum that O refers to
+          if (t > 0) {
+            if (!(ok = wait(&take[taken & 1], (taken >> 1) & 1, 15))) break;
+            old = top_in[128 * (taken & 1)];
+          }
           // (NaN scores are left out of the maximum and make the sum NaN)
-          const bool grow = top > m + kGrowth || m == -INFINITY;
-          const float old = m;
-          if (grow && top > m) m = top;
-          if (t > 0 && __any_sync(0xffffffffu, grow && old != -INFINITY)) {
-            // The last product has to be done. (Two: these scores waited for it.)
-            if (!Two) {
-              if (!(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 18))) break;
-              tc_fence_after();
-            }
-            const float f = grow && old != -INFINITY ? ex2(old - m) : 1.0f;
-            const uint32_t oc = tmem + lanes + 128 * (Two ? half : (int)(segs % OB)) + oc0;
-            l *= f;
+          const bool grow = top > old + kGrowth || old == -INFINITY;
+          const float now = grow && top > old ? top : old;
+          if (!last) {
+            top_out[128 * (given & 1)] = now;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&give[given & 1]);
+          }
+          if (m != now) {   // (this group's sums refer to an older one)
+            l *= m == -INFINITY ? 0.0f : ex2(m - now);
+            m = now;
+          }
+          if (__any_sync(0xffffffffu, grow && old != -INFINITY)) {
+            // the last product has to be done
+            const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
+            if (!(ok = wait(&pv_done[i], sring.i == 0 ? sring.phase ^ 1 : sring.phase, 18))) break;
+            tc_fence_after();
+            const float f = grow && old != -INFINITY ? ex2(old - now) : 1.0f;
+            const uint32_t oc = tmem + lanes + D * oring.i;
 #pragma unroll 1
-            for (int i = 0; i < OW; i += 16) {
+            for (int i = 0; i < D; i += 16) {
               uint32_t o[16];
               tmem_ld_32x32b_x16(oc + i, o);
 #pragma unroll
@@ -1054,7 +1019,7 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
           }
           // with fp16 weights the reference is 2^7 below the maximum, which keeps
           // small ones of long contexts above fp16's smallest
-          const float ref = (E ? 7.0f : 0.0f) - (m == -INFINITY ? 0.0f : m);
+          const float ref = (E ? 7.0f : 0.0f) - (now == -INFINITY ? 0.0f : now);
           float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
           auto weights = [&](const uint32_t (&y)[32], int i) {
             uint32_t w[16];
@@ -1074,35 +1039,39 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             tmem_st_32x32b_x16(sc + i / 2, w);   // (in the place of scores that are read)
           };
           weights(x[0], 0);
-          if constexpr (Two) {
-            tmem_ld_32x32b_x32(sc + (E ? 64 : 96), x[0]);
-            weights(x[1], 32);
-            if constexpr (E) {
-              tmem_ld_32x32b_x32(sc + 96, x[1]);
-              tmem_wait_ld(x[0]);
-              tmem_wait_ld(x[1]);
-              weights(x[0], 64);
-              weights(x[1], 96);
-            } else {
-              weights(x[kKeep - 1], 64);
-              tmem_wait_ld(x[0]);
-              weights(x[0], 96);
-            }
+          tmem_ld_32x32b_x32(sc + (E ? 64 : 96), x[0]);
+          weights(x[1], 32);
+          if constexpr (E) {
+            tmem_ld_32x32b_x32(sc + 96, x[1]);
+            tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            weights(x[0], 64);
+            weights(x[1], 96);
           } else {
-            weights(x[1], 32);
+            weights(x[kKeep - 1], 64);
+            tmem_wait_ld(x[0]);
+            weights(x[0], 96);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          // (the other group writes the part; what orders this is its wait for the product)
+          if (t + 2 == n) {
+            s_sum[128 * (np & 1) + row] = l;
+            s_ref[128 * (np & 1) + row] = m;
+          }
+          taken += t > 0;
+          given += !last;
           tmem_wait_st();
         }
         if (!E && masked) {
-          // values that some row must not see: keys past the row tile's own are
-          // nobody's, others only where they are no numbers. (Two: both groups
-          // of warps clear all of them, with the same result.)
-          // The block that had the place before is consumed, so that the wait for
-          // this one is for its phase: these scores waited for the product of tile
-          // u - 2; with two blocks to a tile the last product is waited for, too.
-          if (NG > 1 && u > 0 && !(ok = wait(&pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, 19))) break;
-          const int key = threadIdx.x & 127, j = 128 * k + key, keys = parts[pi].keys;
+          // Values that some row must not see: keys past the row tile's own are
+          // nobody's, others only where they are no numbers. The block that had the
+          // place before has to be consumed, so that the wait for this one is for its
+          // phase.
+          if (u > 0) {
+            const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
+            if (!(ok = wait(&pv_done[i], sring.i == 0 ? sring.phase ^ 1 : sring.phase, 19))) break;
+          }
+          const int key = threadIdx.x & 127, j = 128 * k + key;
           bool any = false;
 #pragma unroll 1
           for (int g = 0; g < NG; ++g) {
@@ -1110,74 +1079,54 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
             if (!(ok = wait(&v_full[i], ((u * NG + g) / VS) & 1, 20))) break;
             if (j < seen) continue;
 #pragma unroll 1
-            for (int q = Two ? 0 : 4 * half; q < GC * 8; q += !Two && (q & 3) == 3 ? 5 : 1) {
-              // piece q % 8 of chunk q / 8; One: half of each chunk's pieces
+            for (int q = 0; q < GC * 8; ++q) {   // piece q % 8 of chunk q / 8
               uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kBlock + (q >> 3) * kSlotBytes + 128 * key) +
                              ((q & 7) ^ (key & 7));
-              uint4 y = j < keys ? *piece : make_uint4(0, 0, 0, 0);
+              uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
               const bool un = clear_unbounded<false>(y);
-              if (un || j >= keys) *piece = y;
+              if (un || j >= s.keys) *piece = y;
               any |= un;
             }
           }
           if (!ok) break;
-          if (any) s_unbounded[pi] = (int)np;
+          if (any) s_unbounded[np % kParts] = (int)np + 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
-        ++t;
-        ++u;
-      }
-      // The sums of a part: Two, when its last weights are made; One, only after
-      // the next part's first ones, while its last product runs.
-      if (Two && !stop && t == n) {
-        have = true;
-        last_m = m;
-        last_l = l;
-        ++segs;
-      }
-      if (have && (Two || stop || t == 1)) {
-        have = false;
-        const uint32_t fp = Two || stop ? part : part - 1, seg = segs - 1;
-        const Part& s = parts[fp % kParts];
-        const int rows = max(min(s.tokens - q0, p.R), 0) * p.G, ob = Two ? half : seg % OB;
-        // its last product: of the tile before this one, or of the last one
-        const uint32_t w = Two || stop ? u - 1 : u - 2;
-        if (!(ok = wait(&pv_done[Two ? half : w & 1], (Two ? w : w >> 1) & 1, 21))) break;
+        if (lane == 0) mbar_arrive(&p_full[sring.i]);
+        if (!last) continue;
+
+        // ------------------------------------------------- the part's sums
+        if (!(ok = wait(&pv_done[sring.i], sring.phase, 21))) break;
         tc_fence_after();
-        if (32 * quarter < rows) {
-          if (!Two) {
-            s_sum[128 * half + row] = last_l;
-            if (!(ok = meet())) break;
-            last_l += s_sum[128 * (half ^ 1) + row];
+        if (work) {
+          if (n > 1) {
+            const float other = s_ref[128 * (np & 1) + row], x = s_sum[128 * (np & 1) + row];
+            l += other == m ? x : x * (other == -INFINITY ? 0.0f : ex2(other - m));   // (a NaN stays)
           }
-          const bool whole = s.k0 == 0 && s.k1 == s.nk, mine = row < rows;
-          const float inv = whole ? (last_l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / last_l) : 1.0f;
-          const int ftok = s.tok0 + row_tok, srow = (Two ? 128 * half : 0) + row;   // row in scratch
-          uint16_t* out = p.a.out + (long long)(s.row + ftok) * p.a.o_ld + (long long)(s.h * p.G + row_g) * D + oc0;
-          float* dst = p.o + ((long long)s.place * D + oc0) * (128 * QT) + srow;
-          const uint32_t oc = tmem + lanes + 128 * ob + oc0;
-          const bool fix = s_unbounded[fp % kParts] == (int)fp + 1;
+          const bool whole = s.k0 == 0 && s.k1 == s.nk;
+          const float inv = whole ? (l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / l) : 1.0f;
+          uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)(s.h * p.G + row_g) * D;
+          float* dst = p.o + (long long)s.place * D * 128 + row;
+          const uint32_t oc = tmem + lanes + D * oring.i;
+          const bool fix = s_unbounded[np % kParts] == (int)np + 1;
 #pragma unroll 1
-          for (int i = 0; i < OW; i += 32) {
+          for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
             __syncwarp();
             tmem_ld_32x32b_x32(oc + i, o);
             tmem_wait_ld(o);
-            if (!mine) continue;
+            if (!live) continue;
             if (fix) {
-              const int from = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1, end = min(s.keys, 128 * s.k1);
-              const unsigned long long* words =
-                  p.a.mask ? p.a.mask + (long long)(s.row + ftok) * p.a.mask_words : nullptr;
+              const int end = min(s.keys, 128 * s.k1);
 #pragma unroll 1
-              for (int j = max(from, 128 * s.k0); j < end; ++j) {
-                if (!(seen_bits(j - s.ctx, ftok, words, p.a.mask_words) & 1)) continue;
+              for (int j = max(seen, 128 * s.k0); j < end; ++j) {
+                if (!(seen_bits(j - s.ctx, tok, words, p.a.mask_words) & 1)) continue;
                 const int id = p.a.table[(long long)s.b * p.a.table_width + (j >> p.a.page_shift)];
                 if (id < 0 || id >= p.a.cache.pages) continue;
                 const long long e = ((((long long)id * p.a.kv_heads + s.h) << p.a.page_shift) +
-                                     (j & ((1 << p.a.page_shift) - 1))) * D + oc0 + i;
+                                     (j & ((1 << p.a.page_shift) - 1))) * D + i;
 #pragma unroll
                 for (int q = 0; q < 32; ++q) {
                   const float v = cache_value<E>(p.a.cache.v, e + q);
@@ -1196,25 +1145,20 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) dst[(i + q) * (128 * QT)] = __uint_as_float(o[q]);
+              for (int q = 0; q < 32; ++q) dst[(i + q) * 128] = __uint_as_float(o[q]);
             }
           }
-          if (!whole && mine && (Two || half == 0))
-            p.ml[s.place * 128 * QT + srow] = make_float2(last_m == -INFINITY ? 0.0f : last_m, last_l);
+          if (!whole && live) p.ml[s.place * 128 + row] = make_float2(m == -INFINITY ? 0.0f : m, l);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&o_free[ob]);
-          mbar_arrive(&part_empty[fp % kParts]);
-        }
+        if (lane == 0) mbar_arrive(&o_free[oring.i]);
       }
-      if (!Two && !stop && t == n) {
-        have = true;
-        last_m = m;
-        last_l = l;
-        ++segs;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_empty[at.i]);
+      at.step();
+      oring.step();
+      ++np;
     }
   }
   __syncthreads();
@@ -1229,25 +1173,22 @@ __global__ void __launch_bounds__(Shape<D, E, Two>::kThreads, 1)
 // lane. A unit has as many warps as 2 parts each need, up to all 8, which take
 // alternate parts and add up through shared memory.
 constexpr int kJoinWarps = 8, kJoinBlocks = 16;
-template <int D, int QT>
+template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaParams p) {
   pdl_begin();
   const AttnShared s = p.shared[blockIdx.x];
   if (s.count == 0) return;
-  constexpr int V = 8, U = 2, kRows = 128 * QT;
+  constexpr int V = 8, U = 2;
   __shared__ float s_o[kJoinWarps][V][32];
   __shared__ float2 s_ml[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per = 1;                                   // warps of a unit
   while (per < kJoinWarps && per * U < s.count) per *= 2;
   const int at_once = kJoinWarps / per, sub = warp % per;
-  // row blocks: those of the first row tile that have rows, then the second's
-  const int rows0 = min(s.tokens, p.R) * p.G, rows1 = max(s.tokens - p.R, 0) * p.G;
-  const int blocks0 = (rows0 + 31) / 32, units = (blocks0 + (rows1 + 31) / 32) * (D / V);
+  const int rows = s.tokens * p.G, units = (rows + 31) / 32 * (D / V);
   for (int unit0 = blockIdx.y * at_once; unit0 < units; unit0 += gridDim.y * at_once) {
-    const int unit = unit0 + warp / per, rb = unit / (D / V), col = unit % (D / V) * V;
-    const int tile = rb >= blocks0, row = 32 * (tile ? rb - blocks0 : rb) + lane;
-    const bool on = unit < units && row < (tile ? rows1 : rows0);
+    const int unit = unit0 + warp / per, col = unit % (D / V) * V, row = 32 * (unit / (D / V)) + lane;
+    const bool on = unit < units && row < rows;
     float o[V] = {}, m = -INFINITY, l = 0.0f;
     for (int i0 = sub; on && i0 < s.count; i0 += U * per) {
       float x[U][V];
@@ -1259,9 +1200,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
         if (i < s.count) {
           // (the CTA that began the tile holds its part in its second place)
           const long long place = 2ll * cta + (cta == (int)blockIdx.x);
-          ml[u] = p.ml[place * kRows + 128 * tile + row];
+          ml[u] = p.ml[place * 128 + row];
 #pragma unroll
-          for (int v = 0; v < V; ++v) x[u][v] = p.o[(place * D + col + v) * kRows + 128 * tile + row];
+          for (int v = 0; v < V; ++v) x[u][v] = p.o[(place * D + col + v) * 128 + row];
         }
       }
 #pragma unroll
@@ -1294,7 +1235,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
     }
     if (on && sub == 0) {
       const float scale = l == 0.0f ? 0.0f : (p.a.e4m3 ? p.a.cache.v_scale[s.head] : 1.0f) / l;
-      const int tok = s.row + tile * p.R + row / p.G;
+      const int tok = s.row + row / p.G;
       *reinterpret_cast<uint4*>(p.a.out + tok * p.a.o_ld + (long long)(s.head * p.G + row % p.G) * D + col) =
           make_uint4(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale),
                      pack_bf16x2(o[4] * scale, o[5] * scale), pack_bf16x2(o[6] * scale, o[7] * scale));
@@ -1315,27 +1256,15 @@ bool encode_maps(const AttnArgs& a, int G, int R, TaParams* p) {
          encode_nd(&p->mv, dt, 4, a.cache.v, cd, cs, cb, !a.e4m3);
 }
 
-template <int D, bool E, bool Two>
-cudaError_t launch(TaParams& p, int num_sms, cudaStream_t st) {
-  using Sh = Shape<D, E, Two>;
-  p.step = Sh::QT * p.R;
-  p.inv_step = (unsigned)(((1u << 31) + p.step - 1u) / p.step);
-  auto kern = tree_attn_kernel<D, E, Two>;
+template <int D, bool E>
+cudaError_t launch(const TaParams& p, int ctas, cudaStream_t st) {
+  using Sh = Shape<D, E>;
+  auto kern = tree_attn_kernel<D, E>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Sh::kSmem);
-  const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-  p.inv_ctas = ~0ull / ctas + 1;
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, st, p);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_attn_join<D, Sh::QT>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
+    e = launch_pdl(tree_attn_join<D>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
   return e;
-}
-
-template <int D>
-cudaError_t launch_for(TaParams& p, bool two, int num_sms, cudaStream_t st) {
-  if constexpr (D <= 128) {
-    if (two) return p.a.e4m3 ? launch<D, true, true>(p, num_sms, st) : launch<D, false, true>(p, num_sms, st);
-  }
-  return p.a.e4m3 ? launch<D, true, false>(p, num_sms, st) : launch<D, false, false>(p, num_sms, st);
 }
 
 }  // namespace
@@ -1349,12 +1278,14 @@ cudaError_t launch_tree_attention(const AttnArgs& a, void* scratch, int num_sms,
   p.err = err;
   p.shared = static_cast<AttnShared*>(scratch);
   p.o = reinterpret_cast<float*>(p.shared + kAttnMaxCtas);
-  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kAttnMaxCtas * 2 * attn_rows(a.head_dim) * a.head_dim);
+  p.ml = reinterpret_cast<float2*>(p.o + (size_t)kAttnMaxCtas * 2 * 128 * a.head_dim);
   if (!encode_maps(a, p.G, p.R, &p)) return cudaErrorInvalidValue;
-  const bool two = (long long)a.T * p.G >= 256ll * a.requests;
-  if (a.head_dim == 64) return launch_for<64>(p, two, num_sms, st);
-  if (a.head_dim == 128) return launch_for<128>(p, two, num_sms, st);
-  return launch_for<256>(p, two, num_sms, st);
+  const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
+  p.inv_ctas = ~0ull / ctas + 1;
+  p.inv_r = ((1u << 31) + p.R - 1u) / p.R;
+  if (a.head_dim == 64) return a.e4m3 ? launch<64, true>(p, ctas, st) : launch<64, false>(p, ctas, st);
+  if (a.head_dim == 128) return a.e4m3 ? launch<128, true>(p, ctas, st) : launch<128, false>(p, ctas, st);
+  return a.e4m3 ? launch<256, true>(p, ctas, st) : launch<256, false>(p, ctas, st);
 }
 
 }  // namespace moe
