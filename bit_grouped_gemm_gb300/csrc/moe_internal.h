@@ -41,10 +41,11 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const voi
                uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
 // Tensor map of any rank: dims in elements from the innermost, strides in bytes
-// of the dimensions above it; 128-byte swizzle (box[0] * elem == 128) or none.
+// of the dimensions above it; box[0] * elem is the swizzle's span, if there is one.
 // Places outside the tensor read as zeros.
 bool encode_nd(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
-               const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzled);
+               const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+               CUtensorMapSwizzle swizzle);
 
 // -------------------------------------------------------------- routing ---
 // Router logits: the tcgen05 path when router_tc_fits (and logits and bias

@@ -73,7 +73,8 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const voi
 }
 
 bool encode_nd(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
-               const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzled) {
+               const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+               CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = get_encode();
   if (!enc || rank < 2 || rank > 5) return false;
   cuuint64_t d[5], st[4];
@@ -85,8 +86,7 @@ bool encode_nd(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* bas
     if (i) st[i - 1] = strides[i - 1];
   }
   CUresult r = enc(m, dt, rank, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

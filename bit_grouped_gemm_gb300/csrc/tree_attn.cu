@@ -38,11 +38,11 @@ namespace moe {
 namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
-// warps 0..7 softmax, 8 loads, 9 products with keys, 10 plans, 11 products with values,
-// 12..15 convert (e4m3). (One warp for both kinds of product would bound the kernel: its
-// waits, commits and issue take longer than the products.)
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kScoreWarp = 9, kPlanWarp = 10, kSumWarp = 11, kConvWarp = 12,
-              kConvWarps = 4;
+// warps 0..7 softmax, 8 loads (bf16: keys), 9 products with keys, 10 plans, 11 products with
+// values, 12 loads values (bf16) or 12..15 convert (e4m3). (One warp for both kinds of product
+// would bound the kernel: its waits, issue and commits take longer than the products.)
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kScoreWarp = 9, kPlanWarp = 10, kSumWarp = 11, kValueWarp = 12,
+              kConvWarp = 12, kConvWarps = 4;
 constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
@@ -55,19 +55,22 @@ struct Shape {
   static constexpr int NC = D / 64;                  // chunks of 64 columns
   static constexpr int GC = NC < 2 ? NC : 2;         // chunks of a block
   static constexpr int NG = NC / GC;                 // blocks of a tile
-  static constexpr int KS = D == 64 ? 4 : 2;         // blocks of keys held
-  static constexpr int VS = D == 64 ? 4 : E ? 1 : 2; // and of values
-  static constexpr int KR = E ? (D == 256 ? 2 : 3) : 0;   // 8-bit blocks of keys
-  static constexpr int VR = E ? (D == 64 ? 3 : D == 128 ? 2 : 1) : 0;   // and of values
+  static constexpr int KS = D == 64 ? 4 : E ? (D == 128 ? 4 : 3) : 2;   // blocks of keys held
+  static constexpr int VS = D == 64 ? 4 : 2;         // and of values
+  static constexpr int VR = E ? (D == 64 ? 4 : D == 128 ? 3 : 2) : 0;   // 8-bit blocks of values
   static constexpr int QB = E || D == 256 ? 1 : 2;   // parts whose queries are held
   static constexpr int SB = D == 256 ? 2 : 3;        // key tiles whose scores or weights are held
   static constexpr int OB = D == 64 ? 2 : 1;         // parts whose sums are held
   static constexpr int kColS = 512 - 128 * SB;       // tensor memory: sums, then scores
-  static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kConvWarp);
-  static constexpr int kBlock = GC * kSlotBytes, kRawBlock = kBlock / 2;
+  static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kValueWarp + 1);
+  static constexpr int kKeyRow = E ? 64 * GC : 128;  // bytes of a block's row (bf16: of each chunk's)
+  static constexpr int kVBlock = GC * kSlotBytes, kRawBlock = 128 * 64 * GC, kKBlock = E ? kRawBlock : kVBlock;
   static constexpr int kQBytes = NC * kSlotBytes;
+  // 8-bit queries, two terms of kRawBlock per 128 columns, lie where the 16-bit ones
+  // were, or behind them where rows of 64 columns would overlap
+  static constexpr int kQ8 = E && D == 64 ? kSlotBytes : 0;
   static constexpr int kMisc = 5632 + (E ? kParts * 512 : 0);
-  static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + (KS + VS) * kBlock + (KR + VR) * kRawBlock;
+  static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + kQ8 + KS * kKBlock + VS * kVBlock + VR * kRawBlock;
   static_assert(OB * D <= kColS, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -94,12 +97,27 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_q(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_kv(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 
@@ -107,6 +125,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
 __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int n, bool mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// kind::f8f6f4 with e4m3 operands, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// An operand of 64-byte rows, 64-byte swizzle: 8 rows 512 bytes on.
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | 1ull << 16 | (uint64_t)(512 >> 4) << 32 | 1ull << 46 | 4ull << 61;
 }
 
 // Values as the product's B operand: 16 keys (rows of 128 bytes) of 64 columns
@@ -439,6 +466,12 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {
   return h;
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {   // (a NaN stays one)
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 template <bool E>
 __device__ __forceinline__ float cache_value(const void* base, long long i) {
   if constexpr (E)
@@ -448,6 +481,36 @@ __device__ __forceinline__ float cache_value(const void* base, long long i) {
 }
 
 // ----------------------------------------------------------------- kernel ---
+// Barriers by their shared-memory addresses: a role's warp runs alone, so that every
+// instruction of its loop costs it a latency, conversions of pointers among them.
+using Bar = uint32_t;
+__device__ __forceinline__ bool bar_try(Bar b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void bar_arrive(Bar b) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ void bar_expect(Bar b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_commit(Bar b) {   // once the products issued so far are done
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ bool bar_drain(Bar b, uint32_t parity, unsigned long long limit_ns) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!bar_try(b, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // Waits by a whole warp: true once the phase is over, false (and the CTA's abort
 // flag set) when the limit ran out or another role gave up. The part that has to
 // wait is a function of its own, out of the way of the roles' code: that of all
@@ -488,14 +551,14 @@ struct Ring {
 
 // Waits for a ring's last loads to land; i, phase: the place and parity of the next one.
 template <int kMost>
-__device__ __noinline__ void drain_ring(uint64_t* bars, uint32_t i, uint32_t phase, uint32_t loads, uint32_t places,
+__device__ __noinline__ void drain_ring(Bar bars, uint32_t i, uint32_t phase, uint32_t loads, uint32_t places,
                                         unsigned long long limit_ns) {
   for (uint32_t j = 0; j < min(loads, places) && j < kMost; ++j) {
     if (i-- == 0) {
       i = places - 1;
       phase ^= 1;
     }
-    mbar_wait_drain(&bars[i], phase, limit_ns);
+    bar_drain(bars + 8 * i, phase, limit_ns);
   }
 }
 
@@ -503,47 +566,45 @@ template <int D, bool E>
 __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
   using Sh = Shape<D, E>;
-  constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, KR = Sh::KR, VR = Sh::VR,
+  constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, VR = Sh::VR,
                 QB = Sh::QB, OB = Sh::OB, SB = Sh::SB;
   constexpr uint32_t kColS = Sh::kColS;
+  constexpr int kBars = 3 * SB + OB + 2 * (KS + VS + VR) + 3 * QB + 16 + 2 * kParts + 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
-  uint8_t* s_keys = sq + QB * Sh::kQBytes;
-  uint8_t* s_values = s_keys + KS * Sh::kBlock;
-  uint8_t* raw_keys = s_values + VS * Sh::kBlock;
-  uint8_t* raw_values = raw_keys + KR * Sh::kRawBlock;
+  uint8_t* s_keys = sq + QB * Sh::kQBytes + Sh::kQ8;
+  uint8_t* s_values = s_keys + KS * Sh::kKBlock;
+  uint8_t* raw_values = s_values + VS * Sh::kVBlock;
   uint8_t* misc = raw_values + VR * Sh::kRawBlock;
   float* s_top = reinterpret_cast<float*>(misc);   // [2 groups][2][128] maxima handed on
   float* s_sum = s_top + 512;                      // [2][128] a part's other group's sums
   float* s_ref = s_sum + 256;                      // and the maxima that they refer to
-  float* s_qs = s_ref + 256;                       // [kParts][128] factors of fp16 queries
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 : 0));
-  uint64_t* s_full = bars;               // [SB] scores
-  uint64_t* p_full = s_full + SB;        // [SB] weights
-  uint64_t* pv_done = p_full + SB;       // [SB] products with values
-  uint64_t* o_free = pv_done + SB;       // [OB] sums written
-  uint64_t* k_full = o_free + OB;
-  uint64_t* v_full = k_full + KS;
-  uint64_t* k_free = v_full + VS;
-  uint64_t* v_free = k_free + KS;
-  uint64_t* rk_full = v_free + VS;       // 8-bit blocks
-  uint64_t* rk_empty = rk_full + KR;
-  uint64_t* rv_full = rk_empty + KR;
-  uint64_t* rv_empty = rv_full + VR;
-  uint64_t* q_raw = rv_empty + VR;       // [QB] queries landed (e4m3)
-  uint64_t* q_full = q_raw + QB;         // [QB] queries ready
-  uint64_t* q_empty = q_full + QB;
-  uint64_t* hand = q_empty + QB;         // [4 quarters][2 groups][2] maxima handed on
-  uint64_t* part_full = hand + 16;       // [kParts]
-  uint64_t* part_empty = part_full + kParts;
-  uint64_t* drain = part_empty + kParts;   // [2]
-  Part* parts = reinterpret_cast<Part*>(drain + 2);
+  float* s_qs = s_ref + 256;                       // [kParts][128] factors of 8-bit queries
+  uint64_t* bar_words = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 : 0));
+  const Bar bars = smem_u32(bar_words);
+  const Bar s_full = bars;                   // [SB] scores
+  const Bar p_full = s_full + 8 * SB;        // [SB] weights
+  const Bar pv_done = p_full + 8 * SB;       // [SB] products with values
+  const Bar o_free = pv_done + 8 * SB;       // [OB] sums written
+  const Bar k_full = o_free + 8 * OB;        // [KS]
+  const Bar k_free = k_full + 8 * KS;
+  const Bar v_full = k_free + 8 * KS;        // [VS]
+  const Bar v_free = v_full + 8 * VS;
+  const Bar rv_full = v_free + 8 * VS;       // [VR]
+  const Bar rv_free = rv_full + 8 * VR;
+  const Bar q_raw = rv_free + 8 * VR;        // [QB] queries landed (e4m3)
+  const Bar q_full = q_raw + 8 * QB;         // [QB] queries ready
+  const Bar q_empty = q_full + 8 * QB;
+  const Bar hand = q_empty + 8 * QB;         // [4 quarters][2 groups][2] maxima handed on
+  const Bar part_full = hand + 8 * 16;       // [kParts]
+  const Bar part_empty = part_full + 8 * kParts;
+  const Bar drain = part_empty + 8 * kParts;   // [2]
+  Part* parts = reinterpret_cast<Part*>(bar_words + kBars);
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
-  constexpr int kBars = 3 * SB + OB + 2 * (KS + VS + KR + VR) + 3 * QB + 16 + 2 * kParts + 2;
   static_assert((512 + 512 + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
 
@@ -552,11 +613,12 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // arrivals that a phase takes: 1 but for these
 #pragma unroll 1
     for (int i = 0; i < kBars; ++i) {
-      uint64_t* b = bars + i;
+      const Bar b = bars + 8 * i;
       const bool group = (b >= p_full && b < pv_done) || (b >= o_free && b < k_full);
-      const bool conv = E && ((b >= k_full && b < k_free) || (b >= rk_empty && b < rv_full) ||
-                              (b >= rv_empty && b < q_raw) || (b >= q_full && b < q_empty));
-      mbar_init(b, group ? kSoftWarps / 2 : b >= part_empty && b < drain ? kSoftWarps : conv ? kConvWarps / 2 : 1);
+      const bool conv = E && ((b >= v_full && b < v_free) || (b >= rv_free && b < q_raw) ||
+                              (b >= q_full && b < q_empty));
+      mbar_init(bar_words + i, group ? kSoftWarps / 2 : b >= part_empty && b < drain ? kSoftWarps
+                               : conv ? kConvWarps : 1);
     }
     for (int i = 0; i < kParts; ++i) s_unbounded[i] = 0;
     *abort_flag = 0;
@@ -573,9 +635,9 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-           wait_longer(smem_u32(bar), parity, abort_flag, &p.err, site);
+  auto wait = [&](Bar bar, uint32_t parity, int site) {
+    return __all_sync(0xffffffffu, bar_try(bar, parity)) ||
+           wait_longer(bar, parity, abort_flag, &p.err, site);
   };
   pdl_begin();
   if (warp == kPlanWarp) {
@@ -601,19 +663,19 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         continue;
       }
       const int page = more ? first_pages(p, s, s.k0, lane) : 0;
-      if (!(ok = wait(&part_empty[at.i], at.phase ^ 1, 1))) break;
+      if (!(ok = wait(part_empty + 8 * at.i, at.phase ^ 1, 1))) break;
       s_pages[32 * at.i + lane] = page;
       if (lane == 0) parts[at.i] = s;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&part_full[at.i]);
+      if (lane == 0) bar_arrive(part_full + 8 * at.i);
       at.step();
-      if (!more || !(ok = wait(&q_empty[qring.i], qring.phase ^ 1, 2))) break;
+      if (!more || !(ok = wait(q_empty + 8 * qring.i, qring.phase ^ 1, 2))) break;
       if (elect_one_sync()) {
-        uint64_t* bar = E ? &q_raw[qring.i] : &q_full[qring.i];
-        mbar_arrive_expect_tx(bar, NC * 128 * p.G * p.R);
+        const Bar bar = (E ? q_raw : q_full) + 8 * qring.i;
+        bar_expect(bar, NC * 128 * p.G * p.R);
 #pragma unroll 1
         for (int c = 0; c < NC; ++c)
-          tma_load_3d(sq + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * c, s.h * p.G, s.row + s.tok0, bar);
+          tma_load_q(smem_u32(sq) + qring.i * Sh::kQBytes + c * kSlotBytes, &p.mq, 64 * c, s.h * p.G, s.row + s.tok0, bar);
       }
       __syncwarp();
       qring.step();
@@ -625,114 +687,121 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     AttnShared m = walk.shared();
     if (*abort_flag) m.count = 0;
     if (lane == 0) p.shared[blockIdx.x] = m;
-  } else if (warp == kLoadWarp) {
-    // ---------------------------------------------------- loads, by TMA
+  } else if (warp == kLoadWarp || (!E && warp == kValueWarp)) {
+    // ------------------------- loads by TMA: bf16, keys or values; e4m3, both
+    const bool keys_too = E || warp == kLoadWarp, values_too = E || warp == kValueWarp;
     const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
     const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a block)
     const int y_mask = (1 << p.a.page_shift) - 1;
-    constexpr int kBytes = E ? Sh::kRawBlock : Sh::kBlock, kRow = E ? 64 * GC : 128;
-    constexpr int kKeys = E ? KR : KS, kValues = E ? VR : VS;
-    uint64_t *kf = E ? rk_full : k_full, *ke = E ? rk_empty : k_free, *vf = E ? rv_full : v_full,
-             *ve = E ? rv_empty : v_free;
-    Ring<kKeys> keys;
+    const bool mine = my_chunk < (E ? 1 : GC);
+    const uint32_t offset = my_chunk * kSlotBytes + my_box * box * Sh::kKeyRow;
+    const uint32_t k_to = smem_u32(s_keys) + offset, v_to = smem_u32(E ? raw_values : s_values) + offset;
+    constexpr int kVBytes = E ? Sh::kRawBlock : Sh::kVBlock, kValues = E ? VR : VS;
+    const Bar vf = E ? rv_full : v_full, ve = E ? rv_free : v_free;
+    Ring<KS> keys;
     Ring<kValues> vals;
     Ring<kParts> at;
     uint32_t nk = 0, nv = 0;   // blocks loaded
     bool ok = true, bad = false;
+    auto load = [&](Bar full, uint32_t bytes, uint32_t to, const CUtensorMap* map, int g, int y, int h, int id) {
+      if (lane == 0) bar_expect(full, bytes);
+      __syncwarp();
+      if (mine) tma_load_kv(to, map, 64 * (g * GC + my_chunk), y, h, id, full);
+    };
     while (ok) {
-      if (!(ok = wait(&part_full[at.i], at.phase, 3))) break;
+      if (!(ok = wait(part_full + 8 * at.i, at.phase, 3))) break;
       const Part s = parts[at.i];
       if (s.stop) break;
       // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
-      int win = 0, now = s_pages[32 * at.i + lane], later = first_pages(p, s, s.k0 + (32 >> box_log), lane);
-      int id = 0, before = 0;   // this lane's box's page, of the tile at hand and the one before
+      int now = s_pages[32 * at.i + lane], later = first_pages(p, s, s.k0 + (32 >> box_log), lane);
+      int src = my_box;   // the lane that holds the number
       at.step();
-      // K0 | K1 V0 | K2 V1 | .. | V(n - 1)
 #pragma unroll 1
-      for (int k = s.k0; k <= s.k1 && ok; ++k) {
-        if (k < s.k1) {
-          id = __shfl_sync(0xffffffffu, now, ((k - s.k0) << box_log) - win + my_box);
-          if ((k + 1 - s.k0) << box_log == win + 32) {
-            win += 32;
-            now = later;
-            later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
-          }
-          bad |= id == kBadPage;
-          if (id < 0) id = p.a.cache.pages;   // reads as zeros
+      for (int k = s.k0; k < s.k1 && ok; ++k) {
+        int id = __shfl_sync(0xffffffffu, now, src);
+        src += nbox;
+        if (src >= 32) {
+          src -= 32;
+          now = later;
+          later = first_pages(p, s, k + 1 + (32 >> box_log), lane);
         }
+        bad |= id == kBadPage;
+        if (id < 0) id = p.a.cache.pages;   // reads as zeros
+        const int y = (128 * k + my_box * box) & y_mask;
+        if (keys_too) {
 #pragma unroll 1
-        for (int op = k < s.k1 ? 0 : NG; op < (k > s.k0 ? 2 * NG : NG); ++op) {
-          const bool v = op >= NG;
-          const int i = v ? vals.i : keys.i, y = (128 * (k - v) + my_box * box) & y_mask;
-          const int c = (v ? op - NG : op) * GC + my_chunk;
-          uint64_t* bar = (v ? vf : kf) + i;
-          uint8_t* dst = (E ? (v ? raw_values : raw_keys) : v ? s_values : s_keys) + i * kBytes;
-          if (!(ok = wait((v ? ve : ke) + i, (v ? vals.phase : keys.phase) ^ 1, 4))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
-          __syncwarp();
-          if (my_chunk < (E ? 1 : GC))
-            tma_load_4d(dst + my_chunk * kSlotBytes + my_box * box * kRow, v ? &p.mv : &p.mk, 64 * c, y, s.h,
-                        v ? before : id, bar);
-          if (v) {
-            vals.step();
-            ++nv;
-          } else {
-            keys.step();
-            ++nk;
+          for (int g = 0; g < NG; ++g, keys.step(), ++nk) {
+            if (!(ok = wait(k_free + 8 * keys.i, keys.phase ^ 1, 4))) break;
+            load(k_full + 8 * keys.i, Sh::kKBlock, k_to + keys.i * Sh::kKBlock, &p.mk, g, y, s.h, id);
           }
         }
-        before = id;
+        if (values_too) {
+#pragma unroll 1
+          for (int g = 0; g < NG; ++g, vals.step(), ++nv) {
+            if (!ok || !(ok = wait(ve + 8 * vals.i, vals.phase ^ 1, 4))) break;
+            load(vf + 8 * vals.i, kVBytes, v_to + vals.i * kVBytes, &p.mv, g, y, s.h, id);
+          }
+        }
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
     if (!ok) {
-      drain_ring<4>(kf, keys.i, keys.phase, nk, kKeys, p.err.limit_ns);
+      drain_ring<4>(k_full, keys.i, keys.phase, nk, KS, p.err.limit_ns);
       drain_ring<4>(vf, vals.i, vals.phase, nv, kValues, p.err.limit_ns);
     }
   } else if (warp == kScoreWarp) {
     // ----------------------------------------------- S = Q K^T, by key tile
     // (a place of scores is free once the product with the weights that took it is done)
-    constexpr uint32_t kId = idesc_16(!E, 128, false);
-    const uint64_t qd0 = smem_desc_sw128(smem_u32(sq)), kd0 = smem_desc_sw128(smem_u32(s_keys));
+    // e4m3: the queries' two terms times the codes as they lie in the cache.
+    constexpr uint32_t kId = E ? idesc_e4m3(128) : idesc_16(true, 128, false);
+    const uint32_t q_addr = smem_u32(sq) + Sh::kQ8, k_addr = smem_u32(s_keys);
+    const uint64_t qd0 = E && D == 64 ? smem_desc_sw64(q_addr) : smem_desc_sw128(q_addr);
+    const uint64_t kd0 = E && D == 64 ? smem_desc_sw64(k_addr) : smem_desc_sw128(k_addr);
     Ring<KS> keys;
     Ring<SB> sring;
     Ring<QB> qring;
     Ring<kParts> at;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(&part_full[at.i], at.phase, 5))) break;
+      if (!(ok = wait(part_full + 8 * at.i, at.phase, 5))) break;
       if (parts[at.i].stop) break;
       int n = parts[at.i].k1 - parts[at.i].k0;
       at.step();
-      if (!(ok = wait(&q_full[qring.i], qring.phase, 6))) break;
+      if (!(ok = wait(q_full + 8 * qring.i, qring.phase, 6))) break;
       const uint64_t qd = qd0 + qring.i * (Sh::kQBytes / 16);
 #pragma unroll 1
       for (; n > 0 && ok; --n, sring.step()) {
-        if (!(ok = wait(&pv_done[sring.i], sring.phase ^ 1, 8))) break;
+        if (!(ok = wait(pv_done + 8 * sring.i, sring.phase ^ 1, 8))) break;
 #pragma unroll 1
         for (int g = 0; g < NG; ++g, keys.step()) {
-          if (!(ok = wait(&k_full[keys.i], keys.phase, 7))) break;
+          if (!(ok = wait(k_full + 8 * keys.i, keys.phase, 7))) break;
           tc_fence_after();
           if (elect_one_sync()) {
-            const uint64_t a = qd + g * (Sh::kBlock / 16), b = kd0 + keys.i * (Sh::kBlock / 16);
+            const uint64_t a = qd + g * (Sh::kKBlock / 16), b = kd0 + keys.i * (Sh::kKBlock / 16);
+            const uint32_t d = tmem + kColS + 128 * sring.i;
 #pragma unroll
-            for (int c = 0; c < GC; ++c)
+            for (int c = 0; c < 2; ++c)   // e4m3: the two terms
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss(tmem + kColS + 128 * sring.i, a + (c * kSlotBytes + 32 * kk) / 16,
-                           b + (c * kSlotBytes + 32 * kk) / 16, kId, g != 0 || (c | kk) != 0);
-            if (g == NG - 1) mma_commit(&s_full[sring.i]);
-            mma_commit(&k_free[keys.i]);
-            if (n == 1 && g == NG - 1) mma_commit(&q_empty[qring.i]);
+              for (int kk = 0; kk < (E ? 2 * GC : 4); ++kk) {
+                if constexpr (E) {
+                  mma_f8_ss(d, a + (c * NG * Sh::kKBlock + 32 * kk) / 16, b + 2 * kk, kId, g != 0 || (c | kk) != 0);
+                } else if (c < GC) {
+                  mma_f16_ss(d, a + (c * kSlotBytes + 32 * kk) / 16, b + (c * kSlotBytes + 32 * kk) / 16, kId,
+                             g != 0 || (c | kk) != 0);
+                }
+              }
+            if (g == NG - 1) bar_commit(s_full + 8 * sring.i);
+            bar_commit(k_free + 8 * keys.i);
+            if (n == 1 && g == NG - 1) bar_commit(q_empty + 8 * qring.i);
           }
           __syncwarp();
         }
       }
       qring.step();
     }
-    if (elect_one_sync()) mma_commit(drain);
+    if (elect_one_sync()) bar_commit(drain);
     __syncwarp();
-    mbar_wait_drain(drain, 0, p.err.limit_ns);
+    bar_drain(drain, 0, p.err.limit_ns);
   } else if (warp == kSumWarp) {
     // ---------------------------------------------------------- O += P V
     constexpr uint32_t kId = idesc_16(!E, 64 * GC, true);
@@ -743,130 +812,133 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     Ring<kParts> at;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(&part_full[at.i], at.phase, 9))) break;
+      if (!(ok = wait(part_full + 8 * at.i, at.phase, 9))) break;
       if (parts[at.i].stop) break;
       const int n = parts[at.i].k1 - parts[at.i].k0;
       at.step();
 #pragma unroll 1
       for (int t = 0; t < n && ok; ++t, sring.step()) {
-        if (!(ok = wait(&p_full[sring.i], sring.phase, 10))) break;
-        if (t == 0 && !(ok = wait(&o_free[oring.i], oring.phase ^ 1, 11))) break;
+        if (!(ok = wait(p_full + 8 * sring.i, sring.phase, 10))) break;
+        if (t == 0 && !(ok = wait(o_free + 8 * oring.i, oring.phase ^ 1, 11))) break;
 #pragma unroll 1
         for (int g = 0; g < NG; ++g, vals.step()) {
-          if (!(ok = wait(&v_full[vals.i], vals.phase, 12))) break;
+          if (!(ok = wait(v_full + 8 * vals.i, vals.phase, 12))) break;
           tc_fence_after();
           if (elect_one_sync()) {
-            const uint64_t b = vd0 + vals.i * (Sh::kBlock / 16);
+            const uint64_t b = vd0 + vals.i * (Sh::kVBlock / 16);
             const uint32_t pc = tmem + kColS + 128 * sring.i, o = tmem + D * oring.i + 64 * GC * g;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)   // 16 keys each
               mma_f16_ts(o, pc + 8 * kk, b + (2048 >> 4) * kk, kId, t != 0 || kk != 0);
-            if (g == NG - 1) mma_commit(&pv_done[sring.i]);
-            mma_commit(&v_free[vals.i]);
+            if (g == NG - 1) bar_commit(pv_done + 8 * sring.i);
+            bar_commit(v_free + 8 * vals.i);
           }
           __syncwarp();
         }
       }
       oring.step();
     }
-    if (elect_one_sync()) mma_commit(drain + 1);
+    if (elect_one_sync()) bar_commit(drain + 8);
     __syncwarp();
-    mbar_wait_drain(drain + 1, 0, p.err.limit_ns);
-  } else if (E && warp >= kConvWarp) {   // (8-bit caches have one place for queries)
-    // ------------------- e4m3 chunks to fp16, exactly; queries to fp16, each
-    // row times the power of two that brings its largest element to 2^14..2^15
-    // (elements below 2^-31 of that one lose bits), which its scores undo
-    // Two warps take the keys and the queries, two the values; a warp has 64 rows
-    // of a block.
-    const bool v = warp >= kConvWarp + 2;
-    const int w = (warp - kConvWarp) & 1, tid = 32 * w + lane;
-    uint64_t *rfull = v ? rv_full : rk_full, *rempty = v ? rv_empty : rk_empty;
-    uint64_t *bfull = v ? v_full : k_full, *bfree = v ? v_free : k_free;
-    uint8_t *raw = v ? raw_values : raw_keys, *blocks = v ? s_values : s_keys;
-    const uint32_t raw_places = v ? VR : KR, places = v ? VS : KS;
-    uint32_t ri = 0, rphase = 0, bi = 0, bphase = 0, np = 0;
+    bar_drain(drain + 8, 0, p.err.limit_ns);
+  } else if (E && warp >= kConvWarp) {
+    // --------------------------- queries to two e4m3 terms, values to fp16
+    // A row of queries is multiplied by the power of two that brings its largest
+    // element to 2^7..2^8, and its scores by the inverse. The first term is the
+    // nearest e4m3, the second the nearest to what is left: of a bf16's 8 bits 4
+    // each, exactly down to 2^-10 of the row's largest element, and smaller elements
+    // to 2^-18 of it. The codes of values are fp16 values; a warp has 32 rows of a block.
+    const int w = warp - kConvWarp;
+    Ring<VR> rvals;
+    Ring<VS> vals;
     Ring<kParts> at;
+    uint32_t np = 0;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(&part_full[at.i], at.phase, 11))) break;
+      if (!(ok = wait(part_full + 8 * at.i, at.phase, 11))) break;
       const Part s = parts[at.i];
       if (s.stop) break;
-      if (!v) {
-        if (!(ok = wait(q_raw, np & 1, 12))) break;
-        const int rows = s.tokens * p.G;   // 8 threads to a row
+      if (!(ok = wait(q_raw, np & 1, 12))) break;
+      const int rows = s.tokens * p.G;   // 8 lanes to a row, each 8 elements of every chunk
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          const int r = r0 + (tid >> 3);
-          uint8_t* line = sq + 128 * r + 16 * ((tid & 7) ^ (r & 7));
-          uint4 x[NC];
-          uint32_t top = 0;
+      for (int r0 = 4 * w; r0 < rows; r0 += 4 * kConvWarps) {
+        const int r = r0 + (lane >> 3), piece = lane & 7;
+        const uint8_t* line = sq + 128 * r + 16 * (piece ^ (r & 7));
+        uint4 x[NC];
+        uint32_t top = 0;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
-            const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        for (int c = 0; c < NC; ++c) {
+          x[c] = *reinterpret_cast<const uint4*>(line + c * kSlotBytes);
+          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(y[j] & 0x7fffu, y[j] >> 16 & 0x7fffu));
-          }
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          // exponent of the largest element, within what keeps both factors normal
-          const int e = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -100);
-          const float f = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 hv = __floats2half2_rn(bf16_lo(y[j]) * f, bf16_hi(y[j]) * f);
-              y[j] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
-            *reinterpret_cast<uint4*>(line + c * kSlotBytes) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-          if ((tid & 7) == 0) s_qs[at.i * 128 + r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+          for (int j = 0; j < 4; ++j) top = max(top, max(y[j] & 0x7fffu, y[j] >> 16 & 0x7fffu));
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        // exponent of the largest element, within what keeps both factors normal
+        const int e = top >= 0x7f80u ? 7 : max((int)(top >> 7) - 127, -100);
+        const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+        __syncwarp();   // the row is read: its terms take its place
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // (times 0: an infinity becomes a NaN, as nearly all of its row's results are)
+            const float a0 = bf16_lo(y[j]) * f, b0 = bf16_hi(y[j]) * f;
+            const float a = a0 + 0.0f * a0, b = b0 + 0.0f * b0;
+            hi[j] = e4m3x2(a, b);
+            const uint32_t h2 = e4m3x2_f16x2(hi[j]);
+            lo[j] = e4m3x2(a - f16_lo(h2), b - f16_hi(h2));
+          }
+          // columns 64 c + 8 piece on: 8 bytes of the row of block c / GC
+          const int byte = 64 * (c % GC) + 8 * piece, row_bytes = 64 * GC;
+          const int at16 = D == 64 ? (byte >> 4) ^ (r >> 1 & 3) : (byte >> 4) ^ (r & 7);
+          uint8_t* dst = sq + Sh::kQ8 + c / GC * Sh::kKBlock + row_bytes * r + 16 * at16 + (byte & 8);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2*>(dst + NG * Sh::kKBlock) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        }
+        if (piece == 0) s_qs[at.i * 128 + r] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(q_full);
       at.step();
       const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
+      // a lane's piece of 16 columns of chunk c: row 8 i + lane / 4 of the warp's 32
+      const int row = 32 * w + (lane >> 2), piece = lane & 3;
+      const int p0 = 16 * ((2 * piece) ^ (row & 7)), p1 = 16 * ((2 * piece + 1) ^ (row & 7));
 #pragma unroll 1
-      for (int kb = NG * s.k0; kb < NG * s.k1; ++kb) {
-        const int k = kb / NG;
-        if (!(ok = wait(&rfull[ri], rphase, 13))) break;
-        if (!(ok = wait(&bfree[bi], bphase ^ 1, 14))) break;
-        // a lane's piece of 16 columns of chunk c: row 8 i + lane / 4 of the warp's 64
-        const int row = 64 * w + (lane >> 2), piece = lane & 3;
-        uint8_t* dst = blocks + bi * Sh::kBlock + 128 * row;
-        const uint8_t* src = raw + ri * Sh::kRawBlock + 64 * GC * row + 16 * piece;
-        const int p0 = 16 * ((2 * piece) ^ (row & 7)), p1 = 16 * ((2 * piece + 1) ^ (row & 7));
+      for (int kb = NG * s.k0; kb < NG * s.k1; ++kb, rvals.step(), vals.step()) {
+        if (!(ok = wait(rv_full + 8 * rvals.i, rvals.phase, 13))) break;
+        if (!(ok = wait(v_free + 8 * vals.i, vals.phase ^ 1, 14))) break;
+        uint8_t* dst = s_values + vals.i * Sh::kVBlock + 128 * row;
+        const uint8_t* src = raw_values + rvals.i * Sh::kRawBlock + 64 * GC * row + 16 * piece;
 #pragma unroll 1
-        for (int i = 0; i < 8 * GC; i += 4) {
+        for (int c = 0; c < GC; ++c) {
           uint4 x[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = i + j;   // chunk n / 8
-            x[j] = *reinterpret_cast<const uint4*>(src + 64 * (n >> 3) + 512 * GC * (n & 7));
-          }
+          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 64 * c + 512 * GC * j);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int n = i + j;
             const uint4 y = x[j];
-            uint8_t* line = dst + (n >> 3) * kSlotBytes + 1024 * (n & 7);
+            uint8_t* line = dst + c * kSlotBytes + 1024 * j;
             *reinterpret_cast<uint4*>(line + p0) = make_uint4(e4m3x2_f16x2(y.x), e4m3x2_f16x2(y.x >> 16),
                                                               e4m3x2_f16x2(y.y), e4m3x2_f16x2(y.y >> 16));
             *reinterpret_cast<uint4*>(line + p1) = make_uint4(e4m3x2_f16x2(y.z), e4m3x2_f16x2(y.z >> 16),
                                                               e4m3x2_f16x2(y.w), e4m3x2_f16x2(y.w >> 16));
           }
         }
-        if (v && 128 * (k + 1) > seen) {
+        const int k = kb / NG;
+        if (128 * (k + 1) > seen) {
           // values of a tile that not every row sees whole: what some row must
           // not see is cleared, keys past the row tile's own, and what is no number
           bool any = false;
 #pragma unroll 1
-          for (int i = 0; i < 16 * GC; ++i) {
-            const int n = i >> 1, key = 128 * k + row + 8 * (n & 7);
-            uint4* y = reinterpret_cast<uint4*>(dst + (n >> 3) * kSlotBytes + 1024 * (n & 7) + (i & 1 ? p1 : p0));
+          for (int i = 0; i < 8 * GC; ++i) {
+            const int n = i >> 1, key = 128 * k + row + 8 * (n & 3);
+            uint4* y = reinterpret_cast<uint4*>(dst + (n >> 2) * kSlotBytes + 1024 * (n & 3) + (i & 1 ? p1 : p0));
             if (key < seen) continue;
             uint4 x = key < s.keys ? *y : make_uint4(0, 0, 0, 0);
             any |= clear_unbounded<true>(x);
@@ -877,16 +949,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bfull[bi]);
-          mbar_arrive(&rempty[ri]);
-        }
-        if (++ri == raw_places) {
-          ri = 0;
-          rphase ^= 1;
-        }
-        if (++bi == places) {
-          bi = 0;
-          bphase ^= 1;
+          bar_arrive(v_full + 8 * vals.i);
+          bar_arrive(rv_free + 8 * rvals.i);
         }
       }
       ++np;
@@ -900,8 +964,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     const int group = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int row_tok = row / p.G, row_g = row % p.G;   // token of the part, query head of the group
-    uint64_t* give = hand + 4 * quarter + 2 * group;
-    uint64_t* take = hand + 4 * quarter + 2 * (group ^ 1);
+    const Bar give = hand + 8 * (4 * quarter + 2 * group);
+    const Bar take = hand + 8 * (4 * quarter + 2 * (group ^ 1));
     float* top_out = s_top + 256 * group + row;
     const float* top_in = s_top + 256 * (group ^ 1) + row;
     Ring<kParts> at;
@@ -910,7 +974,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     uint32_t np = 0, u = 0, given = 0, taken = 0;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(&part_full[at.i], at.phase, 16))) break;
+      if (!(ok = wait(part_full + 8 * at.i, at.phase, 16))) break;
       const Part s = parts[at.i];
       if (s.stop) break;
       const int n = s.k1 - s.k0, rows = s.tokens * p.G, tok = s.tok0 + row_tok;
@@ -927,14 +991,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         const int k = s.k0 + t;
         const bool masked = 128 * (k + 1) > seen, last = t + 1 == n;
         const uint32_t sc = tmem + lanes + kColS + 128 * sring.i;
-        if (!(ok = wait(&s_full[sring.i], sring.phase, 17))) break;
+        if (!(ok = wait(s_full + 8 * sring.i, sring.phase, 17))) break;
         tc_fence_after();
         if (E && t < 2) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
         if (work) {
-          // Chunks of 32 scores. Of the four, the first three (fp16: two) stay in
-          // registers; the others are read again for their weights.
-          constexpr int kKeep = E ? 2 : 3;
-          uint32_t x[kKeep][32];
+          // Chunks of 32 scores. Of the four, the first two stay in registers; the
+          // others are read again for their weights.
+          uint32_t x[2][32];
           if (masked) {
             // hidden scores are set to -inf in place
 #pragma unroll 1
@@ -960,33 +1023,20 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             return fmaxf(a, b);
           };
           float top;
-          if constexpr (E) {
-            tmem_ld_32x32b_x32(sc + 64, x[0]);
-            tmem_ld_32x32b_x32(sc + 96, x[1]);
-            tmem_wait_ld(x[0]);
-            tmem_wait_ld(x[1]);
-            top = fmaxf(largest(x[0]), largest(x[1]));
-            tmem_ld_32x32b_x32(sc, x[0]);
-            tmem_ld_32x32b_x32(sc + 32, x[1]);
-            tmem_wait_ld(x[0]);
-            tmem_wait_ld(x[1]);
-            top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
-          } else {
-            tmem_ld_32x32b_x32(sc + 96, x[0]);
-            tmem_wait_ld(x[0]);
-            tmem_ld_32x32b_x32(sc + 32, x[1]);
-            tmem_ld_32x32b_x32(sc + 64, x[kKeep - 1]);
-            top = largest(x[0]);
-            tmem_ld_32x32b_x32(sc, x[0]);
-            tmem_wait_ld(x[0]);
-            tmem_wait_ld(x[1]);
-            tmem_wait_ld(x[kKeep - 1]);
-            top = fmaxf(fmaxf(top, largest(x[0])), fmaxf(largest(x[1]), largest(x[kKeep - 1])));
-          }
+          tmem_ld_32x32b_x32(sc + 64, x[0]);
+          tmem_ld_32x32b_x32(sc + 96, x[1]);
+          tmem_wait_ld(x[0]);
+          tmem_wait_ld(x[1]);
+          top = fmaxf(largest(x[0]), largest(x[1]));
+          tmem_ld_32x32b_x32(sc, x[0]);
+          tmem_ld_32x32b_x32(sc + 32, x[1]);
+          tmem_wait_ld(x[0]);
+          tmem_wait_ld(x[1]);
+          top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
           top *= c2;
           float old = -INFINITY;   // the maximum that O refers to
           if (t > 0) {
-            if (!(ok = wait(&take[taken & 1], (taken >> 1) & 1, 15))) break;
+            if (!(ok = wait(take + 8 * (taken & 1), (taken >> 1) & 1, 15))) break;
             old = top_in[128 * (taken & 1)];
           }
           // (NaN scores are left out of the maximum and make the sum NaN)
@@ -995,7 +1045,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           if (!last) {
             top_out[128 * (given & 1)] = now;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&give[given & 1]);
+            if (lane == 0) bar_arrive(give + 8 * (given & 1));
           }
           if (m != now) {   // (this group's sums refer to an older one)
             l *= m == -INFINITY ? 0.0f : ex2(m - now);
@@ -1004,7 +1054,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           if (__any_sync(0xffffffffu, grow && old != -INFINITY)) {
             // the last product has to be done
             const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
-            if (!(ok = wait(&pv_done[i], sring.i == 0 ? sring.phase ^ 1 : sring.phase, 18))) break;
+            if (!(ok = wait(pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 18))) break;
             tc_fence_after();
             const float f = grow && old != -INFINITY ? ex2(old - now) : 1.0f;
             const uint32_t oc = tmem + lanes + D * oring.i;
@@ -1039,19 +1089,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             tmem_st_32x32b_x16(sc + i / 2, w);   // (in the place of scores that are read)
           };
           weights(x[0], 0);
-          tmem_ld_32x32b_x32(sc + (E ? 64 : 96), x[0]);
+          tmem_ld_32x32b_x32(sc + 64, x[0]);
           weights(x[1], 32);
-          if constexpr (E) {
-            tmem_ld_32x32b_x32(sc + 96, x[1]);
-            tmem_wait_ld(x[0]);
-            tmem_wait_ld(x[1]);
-            weights(x[0], 64);
-            weights(x[1], 96);
-          } else {
-            weights(x[kKeep - 1], 64);
-            tmem_wait_ld(x[0]);
-            weights(x[0], 96);
-          }
+          tmem_ld_32x32b_x32(sc + 96, x[1]);
+          tmem_wait_ld(x[0]);
+          tmem_wait_ld(x[1]);
+          weights(x[0], 64);
+          weights(x[1], 96);
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           // (the other group writes the part; what orders this is its wait for the product)
           if (t + 2 == n) {
@@ -1069,18 +1113,18 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           // phase.
           if (u > 0) {
             const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
-            if (!(ok = wait(&pv_done[i], sring.i == 0 ? sring.phase ^ 1 : sring.phase, 19))) break;
+            if (!(ok = wait(pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 19))) break;
           }
           const int key = threadIdx.x & 127, j = 128 * k + key;
           bool any = false;
 #pragma unroll 1
           for (int g = 0; g < NG; ++g) {
             const uint32_t i = (u * NG + g) % VS;
-            if (!(ok = wait(&v_full[i], ((u * NG + g) / VS) & 1, 20))) break;
+            if (!(ok = wait(v_full + 8 * i, ((u * NG + g) / VS) & 1, 20))) break;
             if (j < seen) continue;
 #pragma unroll 1
             for (int q = 0; q < GC * 8; ++q) {   // piece q % 8 of chunk q / 8
-              uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kBlock + (q >> 3) * kSlotBytes + 128 * key) +
+              uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kVBlock + (q >> 3) * kSlotBytes + 128 * key) +
                              ((q & 7) ^ (key & 7));
               uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
               const bool un = clear_unbounded<false>(y);
@@ -1094,11 +1138,11 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sring.i]);
+        if (lane == 0) bar_arrive(p_full + 8 * sring.i);
         if (!last) continue;
 
         // ------------------------------------------------- the part's sums
-        if (!(ok = wait(&pv_done[sring.i], sring.phase, 21))) break;
+        if (!(ok = wait(pv_done + 8 * sring.i, sring.phase, 21))) break;
         tc_fence_after();
         if (work) {
           if (n > 1) {
@@ -1152,10 +1196,10 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[oring.i]);
+        if (lane == 0) bar_arrive(o_free + 8 * oring.i);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&part_empty[at.i]);
+      if (lane == 0) bar_arrive(part_empty + 8 * at.i);
       at.step();
       oring.step();
       ++np;
@@ -1249,11 +1293,14 @@ bool encode_maps(const AttnArgs& a, int G, int R, TaParams* p) {
   const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)R};
   const uint64_t cd[4] = {D, P, (uint64_t)a.kv_heads, (uint64_t)a.cache.pages};
   const uint64_t cs[3] = {D * e, D * e * P, D * e * P * a.kv_heads};
-  const uint32_t cb[4] = {a.e4m3 && D > 64 ? 128u : 64u, (uint32_t)(P < 128 ? P : 128), 1, 1};
+  const uint32_t rows = (uint32_t)(P < 128 ? P : 128), cb[4] = {a.e4m3 && D > 64 ? 128u : 64u, rows, 1, 1};
   const auto dt = a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return encode_nd(&p->mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, qd, qs, qb, true) &&
-         encode_nd(&p->mk, dt, 4, a.cache.k, cd, cs, cb, !a.e4m3) &&
-         encode_nd(&p->mv, dt, 4, a.cache.v, cd, cs, cb, !a.e4m3);
+  // keys are operands as they land; 8-bit values go through the converting warps
+  const auto key_rows = a.e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  return encode_nd(&p->mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_nd(&p->mk, dt, 4, a.cache.k, cd, cs, cb, key_rows) &&
+         encode_nd(&p->mv, dt, 4, a.cache.v, cd, cs, cb,
+                   a.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D, bool E>
