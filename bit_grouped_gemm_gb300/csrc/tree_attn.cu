@@ -38,12 +38,13 @@ namespace moe {
 namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
-// warps 0..7 softmax, 8 loads (bf16: keys), 9 products with keys, 10 plans, 11 products with
-// values, 12 loads values (bf16) or 12..15 convert (e4m3). (One warp for both kinds of product
-// would bound the kernel: its waits, issue and commits take longer than the products.)
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kScoreWarp = 9, kPlanWarp = 10, kSumWarp = 11, kValueWarp = 12,
+// warps 0..7 softmax, 8 plans, 9 products with keys, 10 loads (bf16: keys), 11 products with
+// values, 12 loads values (bf16) or 12..15 convert (e4m3). One warp for both kinds of product
+// would bound the kernel: its waits, issue and commits take longer than the products. Warp 8
+// shares its scheduler with the softmax of rows 0..31, often the only ones: it has little to do.
+constexpr int kSoftWarps = 8, kPlanWarp = 8, kScoreWarp = 9, kLoadWarp = 10, kSumWarp = 11, kValueWarp = 12,
               kConvWarp = 12, kConvWarps = 4;
-constexpr int kItemCost = 128;              // of a row tile beside its keys, in keys
+constexpr int kItemCost = 384;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
 constexpr int kParts = 4;                    // parts told ahead
@@ -562,6 +563,47 @@ __device__ __noinline__ void drain_ring(Bar bars, uint32_t i, uint32_t phase, ui
   }
 }
 
+// The barriers. Each role works out their addresses for itself, from a base that
+// the compiler cannot see through: addresses shared by the roles would all be held
+// in registers throughout, at the cost of the softmax, which has none to spare.
+template <int D, bool E>
+struct Bars {
+  using Sh = Shape<D, E>;
+  static constexpr int kCount = 3 * Sh::SB + Sh::OB + 2 * (Sh::KS + Sh::VS + Sh::VR) + 3 * Sh::QB + 16 + 2 * kParts + 2;
+  Bar s_full;      // [SB] scores
+  Bar p_full;      // [SB] weights
+  Bar pv_done;     // [SB] products with values
+  Bar o_free;      // [OB] sums written
+  Bar k_full, k_free;     // [KS]
+  Bar v_full, v_free;     // [VS]
+  Bar rv_full, rv_free;   // [VR]
+  Bar q_raw;       // [QB] queries landed (e4m3)
+  Bar q_full;      // [QB] queries ready
+  Bar q_empty;
+  Bar hand;        // [4 quarters][2 groups][2] maxima handed on
+  Bar part_full, part_empty;   // [kParts]
+  Bar drain;       // [2]
+  __device__ __forceinline__ explicit Bars(uint32_t words) {
+    asm volatile("mov.u32 %0, %1;" : "=r"(s_full) : "r"(words));
+    p_full = s_full + 8 * Sh::SB;
+    pv_done = p_full + 8 * Sh::SB;
+    o_free = pv_done + 8 * Sh::SB;
+    k_full = o_free + 8 * Sh::OB;
+    k_free = k_full + 8 * Sh::KS;
+    v_full = k_free + 8 * Sh::KS;
+    v_free = v_full + 8 * Sh::VS;
+    rv_full = v_free + 8 * Sh::VS;
+    rv_free = rv_full + 8 * Sh::VR;
+    q_raw = rv_free + 8 * Sh::VR;
+    q_full = q_raw + 8 * Sh::QB;
+    q_empty = q_full + 8 * Sh::QB;
+    hand = q_empty + 8 * Sh::QB;
+    part_full = hand + 8 * 16;
+    part_empty = part_full + 8 * kParts;
+    drain = part_empty + 8 * kParts;
+  }
+};
+
 template <int D, bool E>
 __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
@@ -569,7 +611,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, VR = Sh::VR,
                 QB = Sh::QB, OB = Sh::OB, SB = Sh::SB;
   constexpr uint32_t kColS = Sh::kColS;
-  constexpr int kBars = 3 * SB + OB + 2 * (KS + VS + VR) + 3 * QB + 16 + 2 * kParts + 2;
+  constexpr int kBars = Bars<D, E>::kCount;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
@@ -582,24 +624,6 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   float* s_ref = s_sum + 256;                      // and the maxima that they refer to
   float* s_qs = s_ref + 256;                       // [kParts][128] factors of 8-bit queries
   uint64_t* bar_words = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 : 0));
-  const Bar bars = smem_u32(bar_words);
-  const Bar s_full = bars;                   // [SB] scores
-  const Bar p_full = s_full + 8 * SB;        // [SB] weights
-  const Bar pv_done = p_full + 8 * SB;       // [SB] products with values
-  const Bar o_free = pv_done + 8 * SB;       // [OB] sums written
-  const Bar k_full = o_free + 8 * OB;        // [KS]
-  const Bar k_free = k_full + 8 * KS;
-  const Bar v_full = k_free + 8 * KS;        // [VS]
-  const Bar v_free = v_full + 8 * VS;
-  const Bar rv_full = v_free + 8 * VS;       // [VR]
-  const Bar rv_free = rv_full + 8 * VR;
-  const Bar q_raw = rv_free + 8 * VR;        // [QB] queries landed (e4m3)
-  const Bar q_full = q_raw + 8 * QB;         // [QB] queries ready
-  const Bar q_empty = q_full + 8 * QB;
-  const Bar hand = q_empty + 8 * QB;         // [4 quarters][2 groups][2] maxima handed on
-  const Bar part_full = hand + 8 * 16;       // [kParts]
-  const Bar part_empty = part_full + 8 * kParts;
-  const Bar drain = part_empty + 8 * kParts;   // [2]
   Part* parts = reinterpret_cast<Part*>(bar_words + kBars);
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
@@ -609,20 +633,20 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < kBars) {
     // arrivals that a phase takes: 1 but for these
-#pragma unroll 1
-    for (int i = 0; i < kBars; ++i) {
-      const Bar b = bars + 8 * i;
-      const bool group = (b >= p_full && b < pv_done) || (b >= o_free && b < k_full);
-      const bool conv = E && ((b >= v_full && b < v_free) || (b >= rv_free && b < q_raw) ||
-                              (b >= q_full && b < q_empty));
-      mbar_init(bar_words + i, group ? kSoftWarps / 2 : b >= part_empty && b < drain ? kSoftWarps
-                               : conv ? kConvWarps : 1);
-    }
-    for (int i = 0; i < kParts; ++i) s_unbounded[i] = 0;
-    *abort_flag = 0;
+    const Bars<D, E> bs(smem_u32(bar_words));
+    const Bar b = bs.s_full + 8 * threadIdx.x;
+    const bool group = (b >= bs.p_full && b < bs.pv_done) || (b >= bs.o_free && b < bs.k_full);
+    const bool conv = E && ((b >= bs.v_full && b < bs.v_free) || (b >= bs.rv_free && b < bs.q_raw) ||
+                            (b >= bs.q_full && b < bs.q_empty));
+    mbar_init(bar_words + threadIdx.x, group ? kSoftWarps / 2 : b >= bs.part_empty && b < bs.drain ? kSoftWarps
+                                       : conv ? kConvWarps : 1);
     fence_mbar_init();
+  }
+  if (threadIdx.x < kParts) s_unbounded[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
     tma_prefetch_desc(&p.mq);
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
@@ -641,6 +665,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   };
   pdl_begin();
   if (warp == kPlanWarp) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------------------- the CTA's parts, for all others
     Walk walk(p, parts + kParts);
     walk.begin();
@@ -663,15 +688,15 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         continue;
       }
       const int page = more ? first_pages(p, s, s.k0, lane) : 0;
-      if (!(ok = wait(part_empty + 8 * at.i, at.phase ^ 1, 1))) break;
+      if (!(ok = wait(bs.part_empty + 8 * at.i, at.phase ^ 1, 1))) break;
       s_pages[32 * at.i + lane] = page;
       if (lane == 0) parts[at.i] = s;
       __syncwarp();
-      if (lane == 0) bar_arrive(part_full + 8 * at.i);
+      if (lane == 0) bar_arrive(bs.part_full + 8 * at.i);
       at.step();
-      if (!more || !(ok = wait(q_empty + 8 * qring.i, qring.phase ^ 1, 2))) break;
+      if (!more || !(ok = wait(bs.q_empty + 8 * qring.i, qring.phase ^ 1, 2))) break;
       if (elect_one_sync()) {
-        const Bar bar = (E ? q_raw : q_full) + 8 * qring.i;
+        const Bar bar = (E ? bs.q_raw : bs.q_full) + 8 * qring.i;
         bar_expect(bar, NC * 128 * p.G * p.R);
 #pragma unroll 1
         for (int c = 0; c < NC; ++c)
@@ -682,12 +707,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       ++loads;
     }
     // own copies land before shared memory is released
-    if (!ok) drain_ring<QB>(E ? q_raw : q_full, qring.i, qring.phase, loads, QB, p.err.limit_ns);
+    if (!ok) drain_ring<QB>(E ? bs.q_raw : bs.q_full, qring.i, qring.phase, loads, QB, p.err.limit_ns);
     __syncwarp();
     AttnShared m = walk.shared();
     if (*abort_flag) m.count = 0;
     if (lane == 0) p.shared[blockIdx.x] = m;
   } else if (warp == kLoadWarp || (!E && warp == kValueWarp)) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------- loads by TMA: bf16, keys or values; e4m3, both
     const bool keys_too = E || warp == kLoadWarp, values_too = E || warp == kValueWarp;
     const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
@@ -697,7 +723,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     const uint32_t offset = my_chunk * kSlotBytes + my_box * box * Sh::kKeyRow;
     const uint32_t k_to = smem_u32(s_keys) + offset, v_to = smem_u32(E ? raw_values : s_values) + offset;
     constexpr int kVBytes = E ? Sh::kRawBlock : Sh::kVBlock, kValues = E ? VR : VS;
-    const Bar vf = E ? rv_full : v_full, ve = E ? rv_free : v_free;
+    const Bar vf = E ? bs.rv_full : bs.v_full, ve = E ? bs.rv_free : bs.v_free;
     Ring<KS> keys;
     Ring<kValues> vals;
     Ring<kParts> at;
@@ -709,7 +735,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       if (mine) tma_load_kv(to, map, 64 * (g * GC + my_chunk), y, h, id, full);
     };
     while (ok) {
-      if (!(ok = wait(part_full + 8 * at.i, at.phase, 3))) break;
+      if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 3))) break;
       const Part s = parts[at.i];
       if (s.stop) break;
       // page numbers of 32 boxes, one per lane, and of the next 32, read ahead
@@ -731,8 +757,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         if (keys_too) {
 #pragma unroll 1
           for (int g = 0; g < NG; ++g, keys.step(), ++nk) {
-            if (!(ok = wait(k_free + 8 * keys.i, keys.phase ^ 1, 4))) break;
-            load(k_full + 8 * keys.i, Sh::kKBlock, k_to + keys.i * Sh::kKBlock, &p.mk, g, y, s.h, id);
+            if (!(ok = wait(bs.k_free + 8 * keys.i, keys.phase ^ 1, 4))) break;
+            load(bs.k_full + 8 * keys.i, Sh::kKBlock, k_to + keys.i * Sh::kKBlock, &p.mk, g, y, s.h, id);
           }
         }
         if (values_too) {
@@ -746,10 +772,11 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
     if (!ok) {
-      drain_ring<4>(k_full, keys.i, keys.phase, nk, KS, p.err.limit_ns);
+      drain_ring<4>(bs.k_full, keys.i, keys.phase, nk, KS, p.err.limit_ns);
       drain_ring<4>(vf, vals.i, vals.phase, nv, kValues, p.err.limit_ns);
     }
   } else if (warp == kScoreWarp) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // ----------------------------------------------- S = Q K^T, by key tile
     // (a place of scores is free once the product with the weights that took it is done)
     // e4m3: the queries' two terms times the codes as they lie in the cache.
@@ -763,18 +790,18 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     Ring<kParts> at;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(part_full + 8 * at.i, at.phase, 5))) break;
+      if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 5))) break;
       if (parts[at.i].stop) break;
       int n = parts[at.i].k1 - parts[at.i].k0;
       at.step();
-      if (!(ok = wait(q_full + 8 * qring.i, qring.phase, 6))) break;
+      if (!(ok = wait(bs.q_full + 8 * qring.i, qring.phase, 6))) break;
       const uint64_t qd = qd0 + qring.i * (Sh::kQBytes / 16);
 #pragma unroll 1
       for (; n > 0 && ok; --n, sring.step()) {
-        if (!(ok = wait(pv_done + 8 * sring.i, sring.phase ^ 1, 8))) break;
+        if (!(ok = wait(bs.pv_done + 8 * sring.i, sring.phase ^ 1, 8))) break;
 #pragma unroll 1
         for (int g = 0; g < NG; ++g, keys.step()) {
-          if (!(ok = wait(k_full + 8 * keys.i, keys.phase, 7))) break;
+          if (!(ok = wait(bs.k_full + 8 * keys.i, keys.phase, 7))) break;
           tc_fence_after();
           if (elect_one_sync()) {
             const uint64_t a = qd + g * (Sh::kKBlock / 16), b = kd0 + keys.i * (Sh::kKBlock / 16);
@@ -790,19 +817,20 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
                              g != 0 || (c | kk) != 0);
                 }
               }
-            if (g == NG - 1) bar_commit(s_full + 8 * sring.i);
-            bar_commit(k_free + 8 * keys.i);
-            if (n == 1 && g == NG - 1) bar_commit(q_empty + 8 * qring.i);
+            if (g == NG - 1) bar_commit(bs.s_full + 8 * sring.i);
+            bar_commit(bs.k_free + 8 * keys.i);
+            if (n == 1 && g == NG - 1) bar_commit(bs.q_empty + 8 * qring.i);
           }
           __syncwarp();
         }
       }
       qring.step();
     }
-    if (elect_one_sync()) bar_commit(drain);
+    if (elect_one_sync()) bar_commit(bs.drain);
     __syncwarp();
-    bar_drain(drain, 0, p.err.limit_ns);
+    bar_drain(bs.drain, 0, p.err.limit_ns);
   } else if (warp == kSumWarp) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // ---------------------------------------------------------- O += P V
     constexpr uint32_t kId = idesc_16(!E, 64 * GC, true);
     const uint64_t vd0 = value_desc(smem_u32(s_values));
@@ -812,17 +840,17 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     Ring<kParts> at;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(part_full + 8 * at.i, at.phase, 9))) break;
+      if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 9))) break;
       if (parts[at.i].stop) break;
       const int n = parts[at.i].k1 - parts[at.i].k0;
       at.step();
 #pragma unroll 1
       for (int t = 0; t < n && ok; ++t, sring.step()) {
-        if (!(ok = wait(p_full + 8 * sring.i, sring.phase, 10))) break;
-        if (t == 0 && !(ok = wait(o_free + 8 * oring.i, oring.phase ^ 1, 11))) break;
+        if (!(ok = wait(bs.p_full + 8 * sring.i, sring.phase, 10))) break;
+        if (t == 0 && !(ok = wait(bs.o_free + 8 * oring.i, oring.phase ^ 1, 11))) break;
 #pragma unroll 1
         for (int g = 0; g < NG; ++g, vals.step()) {
-          if (!(ok = wait(v_full + 8 * vals.i, vals.phase, 12))) break;
+          if (!(ok = wait(bs.v_full + 8 * vals.i, vals.phase, 12))) break;
           tc_fence_after();
           if (elect_one_sync()) {
             const uint64_t b = vd0 + vals.i * (Sh::kVBlock / 16);
@@ -830,18 +858,19 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)   // 16 keys each
               mma_f16_ts(o, pc + 8 * kk, b + (2048 >> 4) * kk, kId, t != 0 || kk != 0);
-            if (g == NG - 1) bar_commit(pv_done + 8 * sring.i);
-            bar_commit(v_free + 8 * vals.i);
+            if (g == NG - 1) bar_commit(bs.pv_done + 8 * sring.i);
+            bar_commit(bs.v_free + 8 * vals.i);
           }
           __syncwarp();
         }
       }
       oring.step();
     }
-    if (elect_one_sync()) bar_commit(drain + 8);
+    if (elect_one_sync()) bar_commit(bs.drain + 8);
     __syncwarp();
-    bar_drain(drain + 8, 0, p.err.limit_ns);
+    bar_drain(bs.drain + 8, 0, p.err.limit_ns);
   } else if (E && warp >= kConvWarp) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // --------------------------- queries to two e4m3 terms, values to fp16
     // A row of queries is multiplied by the power of two that brings its largest
     // element to 2^7..2^8, and its scores by the inverse. The first term is the
@@ -855,10 +884,10 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     uint32_t np = 0;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(part_full + 8 * at.i, at.phase, 11))) break;
+      if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 11))) break;
       const Part s = parts[at.i];
       if (s.stop) break;
-      if (!(ok = wait(q_raw, np & 1, 12))) break;
+      if (!(ok = wait(bs.q_raw, np & 1, 12))) break;
       const int rows = s.tokens * p.G;   // 8 lanes to a row, each 8 elements of every chunk
 #pragma unroll 1
       for (int r0 = 4 * w; r0 < rows; r0 += 4 * kConvWarps) {
@@ -903,7 +932,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(q_full);
+      if (lane == 0) bar_arrive(bs.q_full);
       at.step();
       const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
       // a lane's piece of 16 columns of chunk c: row 8 i + lane / 4 of the warp's 32
@@ -911,8 +940,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       const int p0 = 16 * ((2 * piece) ^ (row & 7)), p1 = 16 * ((2 * piece + 1) ^ (row & 7));
 #pragma unroll 1
       for (int kb = NG * s.k0; kb < NG * s.k1; ++kb, rvals.step(), vals.step()) {
-        if (!(ok = wait(rv_full + 8 * rvals.i, rvals.phase, 13))) break;
-        if (!(ok = wait(v_free + 8 * vals.i, vals.phase ^ 1, 14))) break;
+        if (!(ok = wait(bs.rv_full + 8 * rvals.i, rvals.phase, 13))) break;
+        if (!(ok = wait(bs.v_free + 8 * vals.i, vals.phase ^ 1, 14))) break;
         uint8_t* dst = s_values + vals.i * Sh::kVBlock + 128 * row;
         const uint8_t* src = raw_values + rvals.i * Sh::kRawBlock + 64 * GC * row + 16 * piece;
 #pragma unroll 1
@@ -949,13 +978,14 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(v_full + 8 * vals.i);
-          bar_arrive(rv_free + 8 * rvals.i);
+          bar_arrive(bs.v_full + 8 * vals.i);
+          bar_arrive(bs.rv_free + 8 * rvals.i);
         }
       }
       ++np;
     }
   } else if (warp < kSoftWarps) {
+    const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------------------------------- softmax, output
     // Two groups of 4 warps take alternate key tiles, a row per thread; a warp's
     // lanes are those of its quarter of tensor memory. The running maximum goes
@@ -963,9 +993,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // keeps sums of its own, and the group of a part's last tile writes the part.
     const int group = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const int row_tok = row / p.G, row_g = row % p.G;   // token of the part, query head of the group
-    const Bar give = hand + 8 * (4 * quarter + 2 * group);
-    const Bar take = hand + 8 * (4 * quarter + 2 * (group ^ 1));
+    const Bar give = bs.hand + 8 * (4 * quarter + 2 * group);
+    const Bar take = bs.hand + 8 * (4 * quarter + 2 * (group ^ 1));
     float* top_out = s_top + 256 * group + row;
     const float* top_in = s_top + 256 * (group ^ 1) + row;
     Ring<kParts> at;
@@ -974,24 +1003,28 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     uint32_t np = 0, u = 0, given = 0, taken = 0;
     bool ok = true;
     while (ok) {
-      if (!(ok = wait(part_full + 8 * at.i, at.phase, 16))) break;
-      const Part s = parts[at.i];
+      if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 16))) break;
+      // (what the loop does not need at every tile is read again where it is used:
+      // registers are short)
+      const Part& s = parts[at.i];
       if (s.stop) break;
-      const int n = s.k1 - s.k0, rows = s.tokens * p.G, tok = s.tok0 + row_tok;
-      const bool live = row < rows, work = 32 * quarter < rows;
+      const int k0 = s.k0, n = s.k1 - k0;
+      const bool work = 32 * quarter < s.tokens * p.G;
       // keys before `seen` are seen by every row
       const int seen = p.a.mask ? s.ctx : s.ctx + s.tok0 + 1;
-      const unsigned long long* words = p.a.mask ? p.a.mask + (long long)(s.row + tok) * p.a.mask_words : nullptr;
+      auto token = [&] { return s.tok0 + row / p.G; };
+      auto mask_words = [&] {
+        return p.a.mask ? p.a.mask + (long long)(s.row + token()) * p.a.mask_words : nullptr;
+      };
       // scores in log2
       float c2 = p.a.scale * (E ? p.a.cache.k_scale[s.h] : 1.0f) * 1.4426950408889634f;
       float m = -INFINITY, l = 0.0f;   // the maximum referred to; sums of this group's tiles
       int t = 0;
       for (; t < n; ++t, ++u, sring.step()) {
         if ((u & 1) != (uint32_t)group) continue;
-        const int k = s.k0 + t;
-        const bool masked = 128 * (k + 1) > seen, last = t + 1 == n;
+        const bool masked = 128 * (k0 + t + 1) > seen, last = t + 1 == n;
         const uint32_t sc = tmem + lanes + kColS + 128 * sring.i;
-        if (!(ok = wait(s_full + 8 * sring.i, sring.phase, 17))) break;
+        if (!(ok = wait(bs.s_full + 8 * sring.i, sring.phase, 17))) break;
         tc_fence_after();
         if (E && t < 2) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
         if (work) {
@@ -1000,9 +1033,12 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           uint32_t x[2][32];
           if (masked) {
             // hidden scores are set to -inf in place
+            const int tok = token(), a = 128 * (k0 + t) - s.ctx;
+            const bool live = row < s.tokens * p.G;
+            const unsigned long long* words = mask_words();
 #pragma unroll 1
             for (int i = 0; i < 128; i += 32) {
-              const uint32_t v = live ? (uint32_t)seen_bits(128 * k + i - s.ctx, tok, words, p.a.mask_words) : 0;
+              const uint32_t v = live ? (uint32_t)seen_bits(a + i, tok, words, p.a.mask_words) : 0;
               if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
               tmem_ld_32x32b_x32(sc + i, x[0]);
               tmem_wait_ld(x[0]);
@@ -1022,12 +1058,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             }
             return fmaxf(a, b);
           };
-          float top;
-          tmem_ld_32x32b_x32(sc + 64, x[0]);
-          tmem_ld_32x32b_x32(sc + 96, x[1]);
-          tmem_wait_ld(x[0]);
-          tmem_wait_ld(x[1]);
-          top = fmaxf(largest(x[0]), largest(x[1]));
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int i = 96; i >= 64; i -= 32) {
+            tmem_ld_32x32b_x32(sc + i, x[0]);
+            tmem_wait_ld(x[0]);
+            top = fmaxf(top, largest(x[0]));
+          }
           tmem_ld_32x32b_x32(sc, x[0]);
           tmem_ld_32x32b_x32(sc + 32, x[1]);
           tmem_wait_ld(x[0]);
@@ -1054,7 +1091,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           if (__any_sync(0xffffffffu, grow && old != -INFINITY)) {
             // the last product has to be done
             const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
-            if (!(ok = wait(pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 18))) break;
+            if (!(ok = wait(bs.pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 18))) break;
             tc_fence_after();
             const float f = grow && old != -INFINITY ? ex2(old - now) : 1.0f;
             const uint32_t oc = tmem + lanes + D * oring.i;
@@ -1113,22 +1150,22 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           // phase.
           if (u > 0) {
             const uint32_t i = sring.i == 0 ? SB - 1 : sring.i - 1;
-            if (!(ok = wait(pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 19))) break;
+            if (!(ok = wait(bs.pv_done + 8 * i, sring.i == 0 ? sring.phase ^ 1 : sring.phase, 19))) break;
           }
-          const int key = threadIdx.x & 127, j = 128 * k + key;
+          const int key = threadIdx.x & 127, j = 128 * (k0 + t) + key, keys = s.keys;
           bool any = false;
 #pragma unroll 1
           for (int g = 0; g < NG; ++g) {
             const uint32_t i = (u * NG + g) % VS;
-            if (!(ok = wait(v_full + 8 * i, ((u * NG + g) / VS) & 1, 20))) break;
+            if (!(ok = wait(bs.v_full + 8 * i, ((u * NG + g) / VS) & 1, 20))) break;
             if (j < seen) continue;
 #pragma unroll 1
             for (int q = 0; q < GC * 8; ++q) {   // piece q % 8 of chunk q / 8
               uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kVBlock + (q >> 3) * kSlotBytes + 128 * key) +
                              ((q & 7) ^ (key & 7));
-              uint4 y = j < s.keys ? *piece : make_uint4(0, 0, 0, 0);
+              uint4 y = j < keys ? *piece : make_uint4(0, 0, 0, 0);
               const bool un = clear_unbounded<false>(y);
-              if (un || j >= s.keys) *piece = y;
+              if (un || j >= keys) *piece = y;
               any |= un;
             }
           }
@@ -1138,20 +1175,21 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(p_full + 8 * sring.i);
+        if (lane == 0) bar_arrive(bs.p_full + 8 * sring.i);
         if (!last) continue;
 
         // ------------------------------------------------- the part's sums
-        if (!(ok = wait(pv_done + 8 * sring.i, sring.phase, 21))) break;
+        if (!(ok = wait(bs.pv_done + 8 * sring.i, sring.phase, 21))) break;
         tc_fence_after();
         if (work) {
           if (n > 1) {
             const float other = s_ref[128 * (np & 1) + row], x = s_sum[128 * (np & 1) + row];
             l += other == m ? x : x * (other == -INFINITY ? 0.0f : ex2(other - m));   // (a NaN stays)
           }
-          const bool whole = s.k0 == 0 && s.k1 == s.nk;
+          const bool whole = k0 == 0 && n == s.nk, live = row < s.tokens * p.G;
           const float inv = whole ? (l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / l) : 1.0f;
-          uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)(s.h * p.G + row_g) * D;
+          const int tok = token();
+          uint16_t* out = p.a.out + (long long)(s.row + tok) * p.a.o_ld + (long long)(s.h * p.G + row % p.G) * D;
           float* dst = p.o + (long long)s.place * D * 128 + row;
           const uint32_t oc = tmem + lanes + D * oring.i;
           const bool fix = s_unbounded[np % kParts] == (int)np + 1;
@@ -1163,9 +1201,10 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             tmem_wait_ld(o);
             if (!live) continue;
             if (fix) {
+              const unsigned long long* words = mask_words();
               const int end = min(s.keys, 128 * s.k1);
 #pragma unroll 1
-              for (int j = max(seen, 128 * s.k0); j < end; ++j) {
+              for (int j = max(seen, 128 * k0); j < end; ++j) {
                 if (!(seen_bits(j - s.ctx, tok, words, p.a.mask_words) & 1)) continue;
                 const int id = p.a.table[(long long)s.b * p.a.table_width + (j >> p.a.page_shift)];
                 if (id < 0 || id >= p.a.cache.pages) continue;
@@ -1196,10 +1235,10 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(o_free + 8 * oring.i);
+        if (lane == 0) bar_arrive(bs.o_free + 8 * oring.i);
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(part_empty + 8 * at.i);
+      if (lane == 0) bar_arrive(bs.part_empty + 8 * at.i);
       at.step();
       oring.step();
       ++np;
@@ -1212,27 +1251,64 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   }
 }
 
-// Joins the parts of the row tiles that CTAs share: block (c, y) takes some units
-// of the tile that CTA c began, a unit being 8 columns of 32 rows, a row per
-// lane. A unit has as many warps as 2 parts each need, up to all 8, which take
-// alternate parts and add up through shared memory.
-constexpr int kJoinWarps = 8, kJoinBlocks = 16;
+// Joins the parts of the row tiles that CTAs share. A unit is 8 columns of 32
+// rows, a row per lane; it has as many warps as 2 parts each need, up to all 8 of
+// a block, which take alternate parts and add up through shared memory. The units
+// of all shared tiles, in groups that fill a block, are dealt over the grid.
+constexpr int kJoinWarps = 8, kJoinGrid = 5;     // blocks per SM
+__device__ __forceinline__ int join_log_per(int count) {   // log2 of a unit's warps
+  return count <= 2 ? 0 : count <= 4 ? 1 : count <= 8 ? 2 : 3;
+}
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinGrid) tree_attn_join(const TaParams p, int ctas) {
   pdl_begin();
-  const AttnShared s = p.shared[blockIdx.x];
-  if (s.count == 0) return;
-  constexpr int V = 8, U = 2;
+  constexpr int V = 8, U = 2, kCols = D / V, kRuns = kAttnMaxCtas / 32;
   __shared__ float s_o[kJoinWarps][V][32];
   __shared__ float2 s_ml[kJoinWarps][32];
+  __shared__ AttnShared s_tiles[kAttnMaxCtas];
+  __shared__ int s_groups[kAttnMaxCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int per = 1;                                   // warps of a unit
-  while (per < kJoinWarps && per * U < s.count) per *= 2;
-  const int at_once = kJoinWarps / per, sub = warp % per;
-  const int rows = s.tokens * p.G, units = (rows + 31) / 32 * (D / V);
-  for (int unit0 = blockIdx.y * at_once; unit0 < units; unit0 += gridDim.y * at_once) {
-    const int unit = unit0 + warp / per, col = unit % (D / V) * V, row = 32 * (unit / (D / V)) + lane;
-    const bool on = unit < units && row < rows;
+  static_assert(kAttnMaxCtas <= 32 * kJoinWarps, "a thread per CTA");
+  if (threadIdx.x < kAttnMaxCtas) {
+    AttnShared s = {};
+    if ((int)threadIdx.x < ctas) s = p.shared[threadIdx.x];
+    s_tiles[threadIdx.x] = s;
+    const int units = (s.tokens * p.G + 31) / 32 * kCols, log_once = 3 - join_log_per(s.count);
+    s_groups[threadIdx.x] = s.count ? (units + (1 << log_once) - 1) >> log_once : 0;
+  }
+  __syncthreads();
+  // groups of the tiles that CTAs kRuns * lane on begin, and of all before
+  int groups[kRuns], before = 0;
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    groups[i] = s_groups[kRuns * lane + i];
+    before += groups[i];
+  }
+  int mine = before;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += o;
+  }
+  const int total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  for (int g = blockIdx.x; g < total; g += gridDim.x) {
+    // the tile of group g
+    const int owner = __ffs(__ballot_sync(0xffffffffu, g >= before && g < before + mine)) - 1;
+    int c = 0, rest = g - before;
+#pragma unroll
+    for (int i = 0; i < kRuns - 1; ++i)
+      if (c == i && rest >= groups[i]) {
+        rest -= groups[i];
+        ++c;
+      }
+    c = __shfl_sync(0xffffffffu, kRuns * lane + c, owner);
+    rest = __shfl_sync(0xffffffffu, rest, owner);
+    const AttnShared s = s_tiles[c];
+    const int log_per = join_log_per(s.count), per = 1 << log_per, sub = warp & (per - 1);
+    const int rows = s.tokens * p.G, unit = (rest << (3 - log_per)) + (warp >> log_per);
+    const int col = unit % kCols * V, row = 32 * (unit / kCols) + lane;
+    const bool on = row < rows;
     float o[V] = {}, m = -INFINITY, l = 0.0f;
     for (int i0 = sub; on && i0 < s.count; i0 += U * per) {
       float x[U][V];
@@ -1243,7 +1319,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
         ml[u] = make_float2(0.0f, 0.0f);
         if (i < s.count) {
           // (the CTA that began the tile holds its part in its second place)
-          const long long place = 2ll * cta + (cta == (int)blockIdx.x);
+          const long long place = 2ll * cta + (cta == c);
           ml[u] = p.ml[place * 128 + row];
 #pragma unroll
           for (int v = 0; v < V; ++v) x[u][v] = p.o[(place * D + col + v) * 128 + row];
@@ -1252,15 +1328,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (ml[u].y == 0.0f) continue;
-        const float mn = fmaxf(m, ml[u].x), f = ex2(m - mn), g = ex2(ml[u].x - mn);
+        const float mn = fmaxf(m, ml[u].x), f = ex2(m - mn), e = ex2(ml[u].x - mn);
         m = mn;
-        l = l * f + ml[u].y * g;
+        l = l * f + ml[u].y * e;
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = o[v] * f + x[u][v] * g;
+        for (int v = 0; v < V; ++v) o[v] = o[v] * f + x[u][v] * e;
       }
     }
     if (per > 1) {
-      __syncthreads();   // the last unit's sums are read
+      __syncthreads();   // the last group's sums are read
 #pragma unroll
       for (int v = 0; v < V; ++v) s_o[warp][v][lane] = o[v];
       s_ml[warp][lane] = make_float2(m, l);
@@ -1269,11 +1345,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 5) tree_attn_join(const TaPar
         for (int w = warp + 1; w < warp + per; ++w) {
           const float2 ml = s_ml[w][lane];
           if (ml.y == 0.0f) continue;
-          const float mn = fmaxf(m, ml.x), f = ex2(m - mn), g = ex2(ml.x - mn);
+          const float mn = fmaxf(m, ml.x), f = ex2(m - mn), e = ex2(ml.x - mn);
           m = mn;
-          l = l * f + ml.y * g;
+          l = l * f + ml.y * e;
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][v][lane] * g;
+          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][v][lane] * e;
         }
       }
     }
@@ -1310,7 +1386,7 @@ cudaError_t launch(const TaParams& p, int ctas, cudaStream_t st) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Sh::kSmem);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, st, p);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_attn_join<D>, dim3(ctas, kJoinBlocks), dim3(32 * kJoinWarps), 0, st, p);
+    e = launch_pdl(tree_attn_join<D>, dim3(ctas * kJoinGrid), dim3(32 * kJoinWarps), 0, st, p, ctas);
   return e;
 }
 
