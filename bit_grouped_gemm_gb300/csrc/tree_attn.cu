@@ -38,12 +38,12 @@ namespace moe {
 namespace {
 
 constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
-// warps 0..7 softmax, 8 plans, 9 products with keys, 10 loads (bf16: keys), 11 products with
-// values, 12 loads values (bf16) or 12..15 convert (e4m3). One warp for both kinds of product
-// would bound the kernel: its waits, issue and commits take longer than the products. Warp 8
-// shares its scheduler with the softmax of rows 0..31, often the only ones: it has little to do.
-constexpr int kSoftWarps = 8, kPlanWarp = 8, kScoreWarp = 9, kLoadWarp = 10, kSumWarp = 11, kValueWarp = 12,
-              kConvWarp = 12, kConvWarps = 4;
+// Warps: groups of 4 for the softmax; then one that plans, one for products with keys, one
+// that loads, one for products with values; for e4m3 four that convert. One warp for both
+// kinds of product would bound the kernel: its waits, issue and commits take longer than the
+// products. The planner has little to do and shares its scheduler with the softmax of rows
+// 0..31, often the only ones.
+constexpr int kPlan = 0, kScore = 1, kLoad = 2, kSum = 3, kConv = 4, kConvWarps = 4;
 constexpr int kItemCost = 384;              // of a row tile beside its keys, in keys
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
@@ -63,14 +63,17 @@ struct Shape {
   static constexpr int SB = D == 256 ? 2 : 3;        // key tiles whose scores or weights are held
   static constexpr int OB = D == 64 ? 2 : 1;         // parts whose sums are held
   static constexpr int kColS = 512 - 128 * SB;       // tensor memory: sums, then scores
-  static constexpr int kThreads = 32 * (E ? kConvWarp + kConvWarps : kValueWarp + 1);
+  // groups of softmax warps, which take key tiles in turn: as many as there are places for
+  // scores, or as the registers of a CTA allow beside the warps that convert
+  static constexpr int SG = E ? 2 : SB;
+  static constexpr int kSoftWarps = 4 * SG, kThreads = 32 * (kSoftWarps + kConv + (E ? kConvWarps : 0));
   static constexpr int kKeyRow = E ? 64 * GC : 128;  // bytes of a block's row (bf16: of each chunk's)
   static constexpr int kVBlock = GC * kSlotBytes, kRawBlock = 128 * 64 * GC, kKBlock = E ? kRawBlock : kVBlock;
   static constexpr int kQBytes = NC * kSlotBytes;
   // 8-bit queries, two terms of kRawBlock per 128 columns, lie where the 16-bit ones
   // were, or behind them where rows of 64 columns would overlap
   static constexpr int kQ8 = E && D == 64 ? kSlotBytes : 0;
-  static constexpr int kMisc = 5632 + (E ? kParts * 512 : 0);
+  static constexpr int kMisc = 2560 + 1024 * SG + 1024 * kParts * (SG - 1) + (E ? kParts * 512 : 0);
   static constexpr int kSmem = 1024 + kMisc + QB * kQBytes + kQ8 + KS * kKBlock + VS * kVBlock + VR * kRawBlock;
   static_assert(OB * D <= kColS, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -569,7 +572,7 @@ __device__ __noinline__ void drain_ring(Bar bars, uint32_t i, uint32_t phase, ui
 template <int D, bool E>
 struct Bars {
   using Sh = Shape<D, E>;
-  static constexpr int kCount = 3 * Sh::SB + Sh::OB + 2 * (Sh::KS + Sh::VS + Sh::VR) + 3 * Sh::QB + 16 + 2 * kParts + 2;
+  static constexpr int kCount = 3 * Sh::SB + Sh::OB + 2 * (Sh::KS + Sh::VS + Sh::VR) + 3 * Sh::QB + 8 * Sh::SG + 2 * kParts + 2;
   Bar s_full;      // [SB] scores
   Bar p_full;      // [SB] weights
   Bar pv_done;     // [SB] products with values
@@ -580,7 +583,7 @@ struct Bars {
   Bar q_raw;       // [QB] queries landed (e4m3)
   Bar q_full;      // [QB] queries ready
   Bar q_empty;
-  Bar hand;        // [4 quarters][2 groups][2] maxima handed on
+  Bar hand;        // [4 quarters][SG][2] maxima handed on
   Bar part_full, part_empty;   // [kParts]
   Bar drain;       // [2]
   __device__ __forceinline__ explicit Bars(uint32_t words) {
@@ -598,7 +601,7 @@ struct Bars {
     q_full = q_raw + 8 * Sh::QB;
     q_empty = q_full + 8 * Sh::QB;
     hand = q_empty + 8 * Sh::QB;
-    part_full = hand + 8 * 16;
+    part_full = hand + 8 * 8 * Sh::SG;
     part_empty = part_full + 8 * kParts;
     drain = part_empty + 8 * kParts;
   }
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p) {
   using Sh = Shape<D, E>;
   constexpr int NC = Sh::NC, GC = Sh::GC, NG = Sh::NG, KS = Sh::KS, VS = Sh::VS, VR = Sh::VR,
-                QB = Sh::QB, OB = Sh::OB, SB = Sh::SB;
+                QB = Sh::QB, OB = Sh::OB, SB = Sh::SB, SG = Sh::SG;
   constexpr uint32_t kColS = Sh::kColS;
   constexpr int kBars = Bars<D, E>::kCount;
   extern __shared__ uint8_t smem_raw[];
@@ -619,20 +622,20 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   uint8_t* s_values = s_keys + KS * Sh::kKBlock;
   uint8_t* raw_values = s_values + VS * Sh::kVBlock;
   uint8_t* misc = raw_values + VR * Sh::kRawBlock;
-  float* s_top = reinterpret_cast<float*>(misc);   // [2 groups][2][128] maxima handed on
-  float* s_sum = s_top + 512;                      // [2][128] a part's other group's sums
-  float* s_ref = s_sum + 256;                      // and the maxima that they refer to
-  float* s_qs = s_ref + 256;                       // [kParts][128] factors of 8-bit queries
+  float* s_top = reinterpret_cast<float*>(misc);   // [SG][2][128] maxima handed on
+  // [kParts][SG - 1][128] a part's sums of the other groups, and the maxima that they refer to
+  float2* s_sum = reinterpret_cast<float2*>(s_top + 256 * SG);
+  float* s_qs = reinterpret_cast<float*>(s_sum + 128 * kParts * (SG - 1));   // [kParts][128] factors of 8-bit queries
   uint64_t* bar_words = reinterpret_cast<uint64_t*>(s_qs + (E ? kParts * 128 : 0));
   Part* parts = reinterpret_cast<Part*>(bar_words + kBars);
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
-  static_assert((512 + 512 + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
+  static_assert((256 * SG + 256 * kParts * (SG - 1) + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, role = warp - Sh::kSoftWarps;
   if (threadIdx.x < kBars) {
     // arrivals that a phase takes: 1 but for these
     const Bars<D, E> bs(smem_u32(bar_words));
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     const bool group = (b >= bs.p_full && b < bs.pv_done) || (b >= bs.o_free && b < bs.k_full);
     const bool conv = E && ((b >= bs.v_full && b < bs.v_free) || (b >= bs.rv_free && b < bs.q_raw) ||
                             (b >= bs.q_full && b < bs.q_empty));
-    mbar_init(bar_words + threadIdx.x, group ? kSoftWarps / 2 : b >= bs.part_empty && b < bs.drain ? kSoftWarps
+    mbar_init(bar_words + threadIdx.x, group ? 4 : b >= bs.part_empty && b < bs.drain ? Sh::kSoftWarps
                                        : conv ? kConvWarps : 1);
     fence_mbar_init();
   }
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
   }
-  if (warp == kScoreWarp) {
+  if (role == kScore) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
            wait_longer(bar, parity, abort_flag, &p.err, site);
   };
   pdl_begin();
-  if (warp == kPlanWarp) {
+  if (role == kPlan) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------------------- the CTA's parts, for all others
     Walk walk(p, parts + kParts);
@@ -712,10 +715,9 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     AttnShared m = walk.shared();
     if (*abort_flag) m.count = 0;
     if (lane == 0) p.shared[blockIdx.x] = m;
-  } else if (warp == kLoadWarp || (!E && warp == kValueWarp)) {
+  } else if (role == kLoad) {
     const Bars<D, E> bs(smem_u32(bar_words));
-    // ------------------------- loads by TMA: bf16, keys or values; e4m3, both
-    const bool keys_too = E || warp == kLoadWarp, values_too = E || warp == kValueWarp;
+    // ------------------------- loads by TMA: a tile's keys, then the last tile's values
     const int box_log = max(7 - p.a.page_shift, 0), nbox = 1 << box_log, box = 128 >> box_log;
     const int my_box = lane & (nbox - 1), my_chunk = lane >> box_log;   // (chunk of a block)
     const int y_mask = (1 << p.a.page_shift) - 1;
@@ -728,11 +730,19 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     Ring<kValues> vals;
     Ring<kParts> at;
     uint32_t nk = 0, nv = 0;   // blocks loaded
-    bool ok = true, bad = false;
+    int v_id = -1, v_y = 0, v_h = 0;   // of the last tile's values
+    bool ok = true, bad = false, due = false;
     auto load = [&](Bar full, uint32_t bytes, uint32_t to, const CUtensorMap* map, int g, int y, int h, int id) {
       if (lane == 0) bar_expect(full, bytes);
       __syncwarp();
       if (mine) tma_load_kv(to, map, 64 * (g * GC + my_chunk), y, h, id, full);
+    };
+    auto values = [&] {
+#pragma unroll 1
+      for (int g = 0; g < NG; ++g, vals.step(), ++nv) {
+        if (!(ok = wait(ve + 8 * vals.i, vals.phase ^ 1, 4))) break;
+        load(vf + 8 * vals.i, kVBytes, v_to + vals.i * kVBytes, &p.mv, g, v_y, v_h, v_id);
+      }
     };
     while (ok) {
       if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 3))) break;
@@ -754,28 +764,25 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         bad |= id == kBadPage;
         if (id < 0) id = p.a.cache.pages;   // reads as zeros
         const int y = (128 * k + my_box * box) & y_mask;
-        if (keys_too) {
 #pragma unroll 1
-          for (int g = 0; g < NG; ++g, keys.step(), ++nk) {
-            if (!(ok = wait(bs.k_free + 8 * keys.i, keys.phase ^ 1, 4))) break;
-            load(bs.k_full + 8 * keys.i, Sh::kKBlock, k_to + keys.i * Sh::kKBlock, &p.mk, g, y, s.h, id);
-          }
+        for (int g = 0; g < NG; ++g, keys.step(), ++nk) {
+          if (!(ok = wait(bs.k_free + 8 * keys.i, keys.phase ^ 1, 4))) break;
+          load(bs.k_full + 8 * keys.i, Sh::kKBlock, k_to + keys.i * Sh::kKBlock, &p.mk, g, y, s.h, id);
         }
-        if (values_too) {
-#pragma unroll 1
-          for (int g = 0; g < NG; ++g, vals.step(), ++nv) {
-            if (!ok || !(ok = wait(ve + 8 * vals.i, vals.phase ^ 1, 4))) break;
-            load(vf + 8 * vals.i, kVBytes, v_to + vals.i * kVBytes, &p.mv, g, y, s.h, id);
-          }
-        }
+        if (due && ok) values();
+        due = true;
+        v_id = id;
+        v_y = y;
+        v_h = s.h;
       }
     }
+    if (due && ok) values();
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err.word, DEVERR_RANGE);
     if (!ok) {
       drain_ring<4>(bs.k_full, keys.i, keys.phase, nk, KS, p.err.limit_ns);
       drain_ring<4>(vf, vals.i, vals.phase, nv, kValues, p.err.limit_ns);
     }
-  } else if (warp == kScoreWarp) {
+  } else if (role == kScore) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // ----------------------------------------------- S = Q K^T, by key tile
     // (a place of scores is free once the product with the weights that took it is done)
@@ -829,7 +836,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     if (elect_one_sync()) bar_commit(bs.drain);
     __syncwarp();
     bar_drain(bs.drain, 0, p.err.limit_ns);
-  } else if (warp == kSumWarp) {
+  } else if (role == kSum) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // ---------------------------------------------------------- O += P V
     constexpr uint32_t kId = idesc_16(!E, 64 * GC, true);
@@ -869,7 +876,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     if (elect_one_sync()) bar_commit(bs.drain + 8);
     __syncwarp();
     bar_drain(bs.drain + 8, 0, p.err.limit_ns);
-  } else if (E && warp >= kConvWarp) {
+  } else if (E && role >= kConv) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // --------------------------- queries to two e4m3 terms, values to fp16
     // A row of queries is multiplied by the power of two that brings its largest
@@ -877,7 +884,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // nearest e4m3, the second the nearest to what is left: of a bf16's 8 bits 4
     // each, exactly down to 2^-10 of the row's largest element, and smaller elements
     // to 2^-18 of it. The codes of values are fp16 values; a warp has 32 rows of a block.
-    const int w = warp - kConvWarp;
+    const int w = role - kConv;
     Ring<VR> rvals;
     Ring<VS> vals;
     Ring<kParts> at;
@@ -984,23 +991,25 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       }
       ++np;
     }
-  } else if (warp < kSoftWarps) {
+  } else if (role < 0) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------------------------------- softmax, output
-    // Two groups of 4 warps take alternate key tiles, a row per thread; a warp's
-    // lanes are those of its quarter of tensor memory. The running maximum goes
-    // from one group to the other, as soon as a tile's scores are read; each group
-    // keeps sums of its own, and the group of a part's last tile writes the part.
+    // Groups of 4 warps take key tiles in turn, a row per thread; a warp's lanes
+    // are those of its quarter of tensor memory. The running maximum goes from one
+    // group to the next, as soon as a tile's scores are read; each group keeps sums
+    // of its own, and the group of a part's last tile writes the part.
     const int group = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const Bar give = bs.hand + 8 * (4 * quarter + 2 * group);
-    const Bar take = bs.hand + 8 * (4 * quarter + 2 * (group ^ 1));
+    const int from = group == 0 ? SG - 1 : group - 1;
+    const Bar give = bs.hand + 8 * (2 * SG * quarter + 2 * group);
+    const Bar take = bs.hand + 8 * (2 * SG * quarter + 2 * from);
     float* top_out = s_top + 256 * group + row;
-    const float* top_in = s_top + 256 * (group ^ 1) + row;
+    const float* top_in = s_top + 256 * from + row;
     Ring<kParts> at;
     Ring<SB> sring;          // of key tile u
     Ring<OB> oring;
     uint32_t np = 0, u = 0, given = 0, taken = 0;
+    int turn = 0;            // the group that key tile u is for
     bool ok = true;
     while (ok) {
       if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 16))) break;
@@ -1021,34 +1030,33 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
       float m = -INFINITY, l = 0.0f;   // the maximum referred to; sums of this group's tiles
       int t = 0;
       for (; t < n; ++t, ++u, sring.step()) {
-        if ((u & 1) != (uint32_t)group) continue;
+        const bool mine = turn == group;
+        turn = turn == SG - 1 ? 0 : turn + 1;
+        if (!mine) continue;
         const bool masked = 128 * (k0 + t + 1) > seen, last = t + 1 == n;
         const uint32_t sc = tmem + lanes + kColS + 128 * sring.i;
         if (!(ok = wait(bs.s_full + 8 * sring.i, sring.phase, 17))) break;
         tc_fence_after();
-        if (E && t < 2) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
+        if (E && t < SG) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
         if (work) {
           // Chunks of 32 scores. Of the four, the first two stay in registers; the
-          // others are read again for their weights.
+          // others are read again for their weights. Hidden scores become -inf.
           uint32_t x[2][32];
+          const unsigned long long* words = nullptr;
+          int tok = 0, a = 0;
           if (masked) {
-            // hidden scores are set to -inf in place
-            const int tok = token(), a = 128 * (k0 + t) - s.ctx;
-            const bool live = row < s.tokens * p.G;
-            const unsigned long long* words = mask_words();
-#pragma unroll 1
-            for (int i = 0; i < 128; i += 32) {
-              const uint32_t v = live ? (uint32_t)seen_bits(a + i, tok, words, p.a.mask_words) : 0;
-              if (__all_sync(0xffffffffu, v == 0xffffffffu)) continue;
-              tmem_ld_32x32b_x32(sc + i, x[0]);
-              tmem_wait_ld(x[0]);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(v >> j & 1)) x[0][j] = 0xff800000u;
-              tmem_st_32x32b_x32(sc + i, x[0]);
-            }
-            tmem_wait_st();
+            tok = token();
+            a = 128 * (k0 + t) - s.ctx;
+            words = mask_words();
           }
+          auto hide = [&](uint32_t (&y)[32], int i) {
+            const uint32_t v = row < s.tokens * p.G ? (uint32_t)seen_bits(a + i, tok, words, p.a.mask_words) : 0;
+            if (__all_sync(0xffffffffu, v == 0xffffffffu)) return;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(v >> j & 1)) y[j] = 0xff800000u;
+            if (i >= 64) tmem_st_32x32b_x32(sc + i, y);
+          };
           auto largest = [&](const uint32_t (&y)[32]) {
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -1059,16 +1067,23 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             return fmaxf(a, b);
           };
           float top = -INFINITY;
+          // (a loop: with the chunks' loads all at once the compiler spills)
 #pragma unroll 1
-          for (int i = 96; i >= 64; i -= 32) {
+          for (int i = 64; i < 128; i += 32) {
             tmem_ld_32x32b_x32(sc + i, x[0]);
             tmem_wait_ld(x[0]);
+            if (masked) hide(x[0], i);
             top = fmaxf(top, largest(x[0]));
           }
           tmem_ld_32x32b_x32(sc, x[0]);
           tmem_ld_32x32b_x32(sc + 32, x[1]);
           tmem_wait_ld(x[0]);
           tmem_wait_ld(x[1]);
+          if (masked) {
+            hide(x[0], 0);
+            hide(x[1], 32);
+            tmem_wait_st();
+          }
           top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
           top *= c2;
           float old = -INFINITY;   // the maximum that O refers to
@@ -1083,10 +1098,6 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             top_out[128 * (given & 1)] = now;
             __syncwarp();
             if (lane == 0) bar_arrive(give + 8 * (given & 1));
-          }
-          if (m != now) {   // (this group's sums refer to an older one)
-            l *= m == -INFINITY ? 0.0f : ex2(m - now);
-            m = now;
           }
           if (__any_sync(0xffffffffu, grow && old != -INFINITY)) {
             // the last product has to be done
@@ -1133,12 +1144,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           tmem_wait_ld(x[1]);
           weights(x[0], 64);
           weights(x[1], 96);
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          // (the other group writes the part; what orders this is its wait for the product)
-          if (t + 2 == n) {
-            s_sum[128 * (np & 1) + row] = l;
-            s_ref[128 * (np & 1) + row] = m;
+          if (m != now) {   // (this group's sums refer to an older one)
+            l *= m == -INFINITY ? 0.0f : ex2(m - now);
+            m = now;
           }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          // (another group writes the part; what orders this is its wait for the product)
+          if (!last && t + SG >= n) s_sum[128 * ((SG - 1) * at.i + n - 2 - t) + row] = make_float2(m, l);
           taken += t > 0;
           given += !last;
           tmem_wait_st();
@@ -1159,14 +1171,29 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             const uint32_t i = (u * NG + g) % VS;
             if (!(ok = wait(bs.v_full + 8 * i, ((u * NG + g) / VS) & 1, 20))) break;
             if (j < seen) continue;
+            // piece q % 8 of chunk q / 8
+            auto piece = [&](int q) {
+              return reinterpret_cast<uint4*>(s_values + i * Sh::kVBlock + (q >> 3) * kSlotBytes + 128 * key) +
+                     ((q & 7) ^ (key & 7));
+            };
+            if (j >= keys) {
+#pragma unroll
+              for (int q = 0; q < GC * 8; ++q) *piece(q) = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint32_t un = 0;   // (an exponent of all ones carries into its half's top bit)
+#pragma unroll
+            for (int q = 0; q < GC * 8; ++q) {
+              const uint4 y = *piece(q);
+              un |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                    ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (!(un & 0x80008000u)) continue;
+            any = true;
 #pragma unroll 1
-            for (int q = 0; q < GC * 8; ++q) {   // piece q % 8 of chunk q / 8
-              uint4* piece = reinterpret_cast<uint4*>(s_values + i * Sh::kVBlock + (q >> 3) * kSlotBytes + 128 * key) +
-                             ((q & 7) ^ (key & 7));
-              uint4 y = j < keys ? *piece : make_uint4(0, 0, 0, 0);
-              const bool un = clear_unbounded<false>(y);
-              if (un || j >= keys) *piece = y;
-              any |= un;
+            for (int q = 0; q < GC * 8; ++q) {
+              uint4 y = *piece(q);
+              if (clear_unbounded<false>(y)) *piece(q) = y;
             }
           }
           if (!ok) break;
@@ -1181,10 +1208,13 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         // ------------------------------------------------- the part's sums
         if (!(ok = wait(bs.pv_done + 8 * sring.i, sring.phase, 21))) break;
         tc_fence_after();
+        bool freed = false;
         if (work) {
-          if (n > 1) {
-            const float other = s_ref[128 * (np & 1) + row], x = s_sum[128 * (np & 1) + row];
-            l += other == m ? x : x * (other == -INFINITY ? 0.0f : ex2(other - m));   // (a NaN stays)
+#pragma unroll
+          for (int i = 0; i < SG - 1; ++i) {
+            if (i + 1 >= n) break;
+            const float2 x = s_sum[128 * ((SG - 1) * at.i + i) + row];
+            l += x.x == m ? x.y : x.y * (x.x == -INFINITY ? 0.0f : ex2(x.x - m));   // (a NaN stays)
           }
           const bool whole = k0 == 0 && n == s.nk, live = row < s.tokens * p.G;
           const float inv = whole ? (l == 0.0f ? 0.0f : (E ? p.a.cache.v_scale[s.h] : 1.0f) / l) : 1.0f;
@@ -1193,8 +1223,33 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           float* dst = p.o + (long long)s.place * D * 128 + row;
           const uint32_t oc = tmem + lanes + D * oring.i;
           const bool fix = s_unbounded[np % kParts] == (int)np + 1;
+          if constexpr (D <= 128) {
+            // a whole row tile's results fit in registers: the next part has the sums'
+            // place before they are stored
+            if (whole && !fix) {
+              uint32_t w[D / 2];
+#pragma unroll
+              for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(oc + i, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  w[i / 2 + j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+              }
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(bs.o_free + 8 * oring.i);
+              freed = true;
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < D / 2; i += 4)
+                  *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+              }
+            }
+          }
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
+          for (int i = freed ? D : 0; i < D; i += 32) {
             uint32_t o[32];
             __syncwarp();
             tmem_ld_32x32b_x32(oc + i, o);
@@ -1235,7 +1290,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(bs.o_free + 8 * oring.i);
+        if (lane == 0 && !freed) bar_arrive(bs.o_free + 8 * oring.i);
       }
       __syncwarp();
       if (lane == 0) bar_arrive(bs.part_empty + 8 * at.i);
@@ -1245,7 +1300,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == kScoreWarp) {
+  if (role == kScore) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
