@@ -6,6 +6,8 @@ the ``MoeExperts`` structs the C ABI takes. ``run_stack`` chains layers with
 the residual update ``x <- bf16(x + alpha * moe(rmsnorm(x)))``, every step
 through the C ABI. ``AdaptedLayer`` is a served layer around the block: a 4-bit
 projection with per-request adapters, then the experts on a scored routing.
+``PagedBatch`` keeps the cache pages of a batch of requests, and
+``CachedAttention`` is the attention half of a layer over them.
 """
 from __future__ import annotations
 
@@ -80,6 +82,138 @@ def run_stack(plan: int, x: torch.Tensor, xn: torch.Tensor, layers: List[DeviceL
                                       L.shared_c, y_buf, stream)
             binding.moe_residual_add(plan, x, y_buf, T, alpha, x, xn, stream)
     return x
+
+
+def _rows(t, dtype, shape, dev) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and
+            t.device == dev and t.is_contiguous())
+
+
+class PagedBatch:
+    """The cache pages of up to ``requests`` requests, ``table_width`` each at most, and
+    what a step's kernels need to know of its tokens; all of it on the device, where
+    moe_page_map keeps it, so that a captured step follows lengths that change.
+
+    Pages 0..``pages``-1 are free at first. ``offsets``, ``length``, ``slot``,
+    ``position``, ``mask`` (None without ``mask_words``) and ``status`` hold the last
+    step's.
+    """
+
+    def __init__(self, requests: int, page_size: int, table_width: int, pages: int,
+                 max_tokens: int, mask_words: int = 0, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.desc = binding.page_desc(requests, page_size, table_width, max_tokens, pages, mask_words)
+        self.table = torch.zeros(requests, table_width, **i32)
+        self.ring = torch.arange(pages, **i32)
+        self.owned = torch.zeros(requests, **i32)
+        self.ring_pos = torch.tensor([0, pages], **i32)
+        self.length = torch.zeros(requests, **i32)
+        self.offsets = torch.zeros(requests + 1, **i32)
+        self.slot = torch.full((max_tokens,), -1, **i32)
+        self.position = torch.zeros(max_tokens, **i32)
+        self.status = torch.zeros(5, **i32)
+        self.mask = torch.zeros(max_tokens, mask_words, dtype=torch.int64,
+                                device=device) if mask_words else None
+        self.pool = binding.page_pool(self.table, self.ring, self.owned, self.ring_pos)
+        self.map = binding.token_map(self.length, self.offsets, self.slot, self.position,
+                                     self.status, self.mask)
+
+    def step(self, context: torch.Tensor, added: torch.Tensor,
+             parent: Optional[torch.Tensor] = None, stream=None) -> None:
+        """The next step: request b holds ``context[b]`` tokens and adds ``added[b]``
+        (negative: it ends); ``parent`` int32 [max_tokens] makes trees of the new ones."""
+        B, M, dev = self.desc.requests, self.desc.max_tokens, self.table.device
+        ok = _rows(context, torch.int32, (B,), dev) and _rows(added, torch.int32, (B,), dev)
+        if parent is not None:
+            ok = ok and self.mask is not None and _rows(parent, torch.int32, (M,), dev)
+        if not ok:
+            raise binding.MoeError(binding.MOE_ERR_INVALID_ARG, "PagedBatch")
+        binding.moe_page_map(self.desc, context, added, parent, self.pool, self.map, stream)
+
+
+class CachedAttention:
+    """The attention half of a pre-norm layer on the residual stream x (bf16 [T, H],
+    in place), with keys and values of a ``PagedBatch`` in a cache of its own:
+
+        x = x + alpha * y;  h8, hs = e4m3(rmsnorm(x) * norm)   y: the last layer's output
+        q, k, v = projection(h8) with adapters    4-bit, H -> (heads + 2 kv_heads) D
+        q, k turned by their positions;  cache[slot] = k, v
+        a = attention of q over the requests' pages
+        x = x + output(a)                         4-bit, heads D -> H
+
+    ``attn`` is a handle of ``desc`` (layers of one shape may share it), ``qkv`` and
+    ``out`` are (qweight, scales, biases) triples, ``norm`` bf16 [H], ``k`` and ``v``
+    the cache [pages, kv_heads, page_size, D], with scales for e4m3; ``adapters`` a
+    ``binding.MoeLora`` of the first projection, or None. What a caller passes must
+    outlive the layer. Rows of x behind the batch's last token are changed, but no
+    other row depends on them. A call takes up to ``max_tokens`` rows; wrong arguments
+    are refused before the first launch, so x is then as it was.
+    """
+
+    def __init__(self, attn: int, desc, norm, qkv, out, k, v, k_scale=None, v_scale=None,
+                 adapters=None, max_tokens: int = 4096, alpha: float = 1.0):
+        H, dev = norm.shape[0], norm.device
+        self.attn, self.desc, self.norm, self.adapters = attn, desc, norm, adapters
+        self.max_tokens, self.alpha = min(max_tokens, desc.max_tokens), alpha
+        self.q_cols, self.kv_cols = desc.heads * desc.head_dim, desc.kv_heads * desc.head_dim
+        cols = self.q_cols + 2 * self.kv_cols
+        shape = (k.shape[0], desc.kv_heads, desc.page_size, desc.head_dim)
+        if tuple(k.shape) != shape or (k_scale is not None) != (desc.cache_type != 0):
+            raise binding.MoeError(binding.MOE_ERR_INVALID_ARG, "CachedAttention")
+        self.kept = (qkv, out, k, v, k_scale, v_scale)
+        self.qkv_c, self.out_c = binding.w4(*qkv), binding.w4(*out)
+        self.cache = binding.kv_cache(k, v, k_scale, v_scale)
+        rank, M = adapters.rank if adapters is not None else 0, self.max_tokens
+        self.project = binding.moe_linear_create(binding.linear_desc(H, cols, M, rank), dev.index or 0)
+        self.output = binding.moe_linear_create(binding.linear_desc(self.q_cols, H, M), dev.index or 0)
+        empty = lambda *shape, dt: torch.empty(shape, dtype=dt, device=dev)
+        self.h8 = empty(M, H, dt=torch.float8_e4m3fn)
+        self.hs = empty(M, 1, dt=torch.float32)
+        self.qkv = empty(M, cols, dt=torch.bfloat16)
+        # (attention leaves rows behind the last token as they are)
+        self.a = torch.zeros(M, self.q_cols, dtype=torch.bfloat16, device=dev)
+        self.d = empty(M, H, dt=torch.bfloat16)
+
+    def close(self) -> None:
+        for name in ("project", "output"):
+            if getattr(self, name):
+                binding.moe_linear_destroy(getattr(self, name))
+                setattr(self, name, None)
+
+    def _check(self, x, y, batch, adapter) -> None:
+        H, dev = self.h8.shape[1], self.h8.device
+        T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+        if T > self.max_tokens or batch.desc.requests > self.desc.max_requests:
+            raise binding.MoeError(binding.MOE_ERR_CAPACITY, "CachedAttention")
+        ok = self.project is not None and T > 0 and _rows(x, torch.bfloat16, (T, H), dev)
+        ok = ok and (y is None or _rows(y, torch.float32, (T, H), dev))
+        ok = ok and batch.table.device == dev and T <= batch.desc.max_tokens
+        ok = ok and batch.desc.page_size == self.desc.page_size
+        if adapter is not None:
+            ok = ok and self.adapters is not None and _rows(adapter, torch.int32, (T,), dev)
+        if not ok:
+            raise binding.MoeError(binding.MOE_ERR_INVALID_ARG, "CachedAttention")
+
+    def __call__(self, x: torch.Tensor, y: Optional[torch.Tensor], batch: PagedBatch, adapter=None,
+                 stream=None) -> torch.Tensor:
+        """One pass over the rows of ``batch``'s last step, T = len(x) of them with what
+        pads them; ``adapter`` is int32 [T] (-1: none)."""
+        self._check(x, y, batch, adapter)
+        T, H = x.shape
+        row, heads = self.qkv.shape[1], self.q_cols
+        q, k, v = (self.qkv.data_ptr() + 2 * c for c in (0, heads, heads + self.kv_cols))
+        binding.moe_norm_quant(binding.norm_desc(H, alpha=self.alpha, delta_f32=True), x, y, self.norm,
+                               T, x_out=x, q_out=self.h8, q_scale=self.hs, stream=stream)
+        binding.moe_linear_forward(self.project, self.h8, T, self.qkv_c, self.qkv, x_scale=self.hs,
+                                   lora=self.adapters if adapter is not None else None,
+                                   adapter=adapter, stream=stream)
+        binding.moe_rope_store(self.attn, q, k, v, T, batch.position, batch.slot, q, self.cache,
+                               q_stride=row, k_stride=row, v_stride=row, out_stride=row, stream=stream)
+        binding.moe_tree_attention(self.attn, q, T, self.cache, batch.table, batch.offsets,
+                                   batch.length, self.a, mask=batch.mask, q_stride=row, stream=stream)
+        binding.moe_linear_forward(self.output, self.a, T, self.out_c, self.d, stream=stream)
+        binding.moe_norm_quant(binding.norm_desc(H), x, self.d, None, T, x_out=x, stream=stream)
+        return x
 
 
 class AdaptedLayer:
