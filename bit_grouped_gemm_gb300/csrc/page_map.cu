@@ -9,9 +9,9 @@
 //
 // Bound by latency: a dozen dependent loads and barriers. One cluster of up to 8
 // CTAs: every CTA repeats the sums (they fit one pass of its threads), and one
-// cluster barrier separates the reads of the pool's state from its update in
-// place, which a grid of independent CTAs could not order.
-#include "pair.cuh"
+// cluster barrier, which the rows' work hides, separates the reads of the pool's
+// state from its update in place, which a grid of independent CTAs could not order.
+#include "moe_common.cuh"
 #include "spans.h"
 
 namespace moe {
@@ -51,6 +51,9 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
   return before + s - v;
 }
 
+// The i-th of the ring's cap entries from `head` on, 0 <= i <= cap <= 2^30.
+__device__ __forceinline__ int entry_of(int head, int i, int cap) { return head + i - (head + i >= cap ? cap : 0); }
+
 // A request as the rows see it: first row, first page taken (in ring order),
 // context, pages owned (negative: not served).
 struct __align__(16) PmReq {
@@ -72,14 +75,19 @@ __global__ void __launch_bounds__(kPmThreads) page_map_kernel(const PmParams p) 
   const int head = (int)((unsigned)p.pool.ring_pos[0] % (unsigned)cap);
   const int free_pages = min(max(p.pool.ring_pos[1], 0), cap);
 
+  // (the first request's, the only one of up to 512, before the first sum waits)
+  const bool some = b0 < p.B;
+  const int add0 = some ? p.added[b0] : 0, ctx0 = some ? p.context[b0] : 0, own0 = some ? p.pool.owned[b0] : 0;
+
   // rows: sums of up to 4096 lengths below 2^31 fit 64 bits
-  unsigned long long mine = 0, total_rows = 0;
-  for (int i = 0; i < per && b0 + i < p.B; ++i) mine += max(p.added[b0 + i], 0);
+  unsigned long long mine = max(add0, 0), total_rows = 0;
+  for (int i = 1; i < per && b0 + i < p.B; ++i) mine += max(p.added[b0 + i], 0);
   unsigned long long row = block_scan(mine, s_part, total_rows);
   // pages needed (low half) and given back (high half), each at most B * width <= 2^30
   unsigned long long pages = 0;
   for (int i = 0; i < per && b0 + i < p.B; ++i) {
-    const int b = b0 + i, add = p.added[b], ctx = p.context[b], own = p.pool.owned[b];
+    const int b = b0 + i, add = i ? p.added[b] : add0, ctx = i ? p.context[b] : ctx0,
+              own = i ? p.pool.owned[b] : own0;
     const long long n = max(add, 0), len = ctx + n;
     const int want = (int)min((len + (1 << p.shift) - 1) >> p.shift, (long long)p.width + 1);
     const bool owns = own >= 0 && own <= p.width;
@@ -126,6 +134,9 @@ __global__ void __launch_bounds__(kPmThreads) page_map_kernel(const PmParams p) 
   if (came) atomicMax(&s_came, came);
   if (refused) atomicAdd(&s_refused, refused);
   __syncthreads();
+  // What the CTAs read and others update in place, owned and ring_pos, is read. (Pages
+  // given back go to entries of the ring that no row takes.)
+  if (nctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   // ------------------------------------------------------------- the rows
   int bad = 0;
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(kPmThreads) page_map_kernel(const PmParams p) 
         if (pg < r.owned) {
           id = *entry;
         } else {
-          id = p.pool.ring[(int)(((long long)head + r.first + pg - r.owned) % cap)];
+          id = p.pool.ring[entry_of(head, r.first + pg - r.owned, cap)];
           if ((j & (page - 1)) == 0) *entry = id;
         }
         if (id >= 0 && id <= (0x7fffffff >> p.shift) - 1) slot = (id << p.shift) | (j & (page - 1));
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(kPmThreads) page_map_kernel(const PmParams p) 
 
   // ------------------------------------- the pool's state, all reads done
   __syncthreads();
-  if (nctas > 1) cluster_sync_all();
+  if (nctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int b = rank * kPmThreads + tid; b <= p.B; b += nctas * kPmThreads) {
     const PmReq r = req[b];
     p.out.offsets[b] = r.row;
@@ -202,14 +213,13 @@ __global__ void __launch_bounds__(kPmThreads) page_map_kernel(const PmParams p) 
       const PmReq r = req[b];
       if (r.owned > -2) continue;
       for (int i = lane; i < -2 - r.owned; i += 32)
-        p.pool.ring[(int)(((long long)head + free_pages + r.first + i) % cap)] =
-            p.pool.table[(long long)b * p.width + i];
+        p.pool.ring[entry_of(head, free_pages + r.first + i, cap)] = p.pool.table[(long long)b * p.width + i];
     }
   if (tid == 0) {
     if (s_bad) atomicAdd(p.out.status + 4, s_bad);
     if (rank == 0) {
       const long long lack = (long long)(total_pages & 0xffffffffu) - free_pages;
-      p.pool.ring_pos_out[0] = (int)(((long long)head + s_taken) % cap);
+      p.pool.ring_pos_out[0] = entry_of(head, s_taken, cap);
       p.pool.ring_pos_out[1] = free_pages - s_taken + s_came;
       p.out.status[0] = rows;
       p.out.status[1] = s_taken;

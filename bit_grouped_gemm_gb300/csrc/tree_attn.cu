@@ -8,27 +8,42 @@
 //   * A row tile is up to 128 query rows of one request and key-value head: R =
 //     128 / G tokens times the G query heads that share the head's keys, so one
 //     read of a key serves all of them. Its keys come in tiles of 128.
-//   * Scores: S = Q K^T (M 128, N 128, K head_dim), Q and K in shared memory as
-//     chunks of 64 columns (128-byte rows, 128-byte swizzle), S in tensor memory,
-//     two buffers. Two groups of 4 warps take 64 columns each of every row, one
-//     row per thread; the weights go back into the scores' place as bf16, and
-//     O += P V takes them from there (V as stored: its keys are the product's K,
-//     so it is the operand with the other major order). The product of the next
-//     tile's scores runs while a tile's weights are computed.
-//   * The maximum that weights refer to is moved, and O in tensor memory scaled,
-//     only when a row's maximum has grown by 2^8: weights stay below 2^8, far
-//     from overflow, and the sums are exact in the same way.
-//   * Keys and values arrive by TMA, a box per page. An 8-bit cache is converted
-//     to bf16 (exact) by 4 further warps between its own ring and the operands'.
+//   * One persistent CTA per SM, its warps in roles: one plans the CTA's parts and
+//     loads their queries, one loads keys and values by TMA (a box per page), one
+//     issues S = Q K^T, one O += P V, and groups of 4 warps do the softmax, a row
+//     per thread, the groups taking key tiles in turn. Scores lie in tensor memory,
+//     2 or 3 tiles of them; a tile's weights go back into its scores' place, as the
+//     product's A operand. The values are its B operand as stored (their keys are
+//     the product's K: the other major order).
+//   * The running maximum goes from group to group through shared memory. O in
+//     tensor memory is scaled only when a row's maximum has grown by 2^8: weights
+//     stay below 2^8, far from overflow, and the sums are as exact.
+//   * An e4m3 cache: the codes of the keys are the product's operand as they lie in
+//     the cache, times queries in two e4m3 terms. Four more warps make these, and
+//     turn values to fp16 (exact; the weights are then fp16 as well). Converting
+//     the keys too took 55 us where this takes 43 (2 contexts of 16384 tokens, trees
+//     of 8), and 157 where it takes 130 (76 contexts of 16000, one token each).
 //   * A split of the keys gives every CTA the same work: all row tiles side by
-//     side, each as long as its keys, are cut into equal lengths, one per CTA, at
-//     tile borders. A row tile that several CTAs share leaves its parts' sums in
-//     scratch, and a second kernel joins them.
+//     side, each as long as its keys and kItemCost, are cut into equal lengths, one
+//     per CTA, at key tiles' borders. A row tile that several CTAs share leaves its
+//     parts' sums in scratch, in FP32, and a second kernel joins them.
 //   * Rows differ in the keys that they see only from the first new token on;
 //     tiles past it are masked. What is not seen may be infinite or NaN: scores
 //     are replaced, and values that some row must not see are set to zero in
 //     shared memory (their NaN times weight 0 would be NaN) and, in rows that do
 //     see them, added at the end.
+//
+// Measured (in a graph; 16 query heads, 2 key-value heads, pages of 64, one GB300):
+// one token of each of 76 contexts of 16000, bf16: head_dim 64 102 us, 128 185, 256
+// 353 (6.1, 6.7, 7.1 TB/s: memory); e4m3 107, 130, 227 (2.9, 4.8, 5.5 TB/s: a tile's
+// way through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need
+// 700 to 2,800). 2 prompts of 2000 tokens behind 2096: 107, 132, 227 us (0.67, 1.08,
+// 1.26 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
+// 1,024: its chain of 4,400 (S 950, softmax 2,400, P V 1,050) runs in 3 tiles at a
+// time, which is all that tensor memory has place for; and 5,000 more go where a
+// row tile ends (masked tile, sums read and stored). The least for one token is
+// about 11 us: two launches, the split's arithmetic 1, loads 1.5, the chain 2.5,
+// sums out 1, join 3.
 #include <limits.h>
 
 #include "attn.h"
@@ -44,7 +59,10 @@ constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 // products. The planner has little to do and shares its scheduler with the softmax of rows
 // 0..31, often the only ones.
 constexpr int kPlan = 0, kScore = 1, kLoad = 2, kSum = 3, kConv = 4, kConvWarps = 4;
-constexpr int kItemCost = 384;              // of a row tile beside its keys, in keys
+// Cost of a row tile beside its keys, in keys, for equal shares. Measured: a batch of 76 tokens,
+// drafted trees, one token: 128 40.5, 41.7, 14.3 us; 256 35.1, 36.5, 14.3; 384 33.3, 35.3, 14.1;
+// 512 33.1, 34.4, 15.7 (a share is at least a tile and its cost: fewer SMs).
+constexpr int kItemCost = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
 constexpr int kParts = 4;                    // parts told ahead
@@ -883,7 +901,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // element to 2^7..2^8, and its scores by the inverse. The first term is the
     // nearest e4m3, the second the nearest to what is left: of a bf16's 8 bits 4
     // each, exactly down to 2^-10 of the row's largest element, and smaller elements
-    // to 2^-18 of it. The codes of values are fp16 values; a warp has 32 rows of a block.
+    // to 2^-17 of it. The codes of values are fp16 values; a warp has 32 rows of a block.
     const int w = role - kConv;
     Ring<VR> rvals;
     Ring<VS> vals;
@@ -1310,6 +1328,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
 // rows, a row per lane; it has as many warps as 2 parts each need, up to all 8 of
 // a block, which take alternate parts and add up through shared memory. The units
 // of all shared tiles, in groups that fill a block, are dealt over the grid.
+// (16 blocks per CTA that may have begun a tile took 15 us for 152 tiles of 2 parts,
+// most of them waiting for their description; this takes 7.)
 constexpr int kJoinWarps = 8, kJoinGrid = 5;     // blocks per SM
 __device__ __forceinline__ int join_log_per(int count) {   // log2 of a unit's warps
   return count <= 2 ? 0 : count <= 4 ? 1 : count <= 8 ? 2 : 3;
