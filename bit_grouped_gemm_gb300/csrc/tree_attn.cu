@@ -243,15 +243,15 @@ __device__ __forceinline__ Req req_of(const TaParams& p, int lo, int hi, int len
 __device__ __forceinline__ int keys_of(const TaParams& p, const Req& r, int t) {
   return r.ctx < 0 ? 0 : r.ctx + min(r.n, (t + 1) * p.R);
 }
-// cost of a request's first t row tiles under one head (all but the last are full)
-__device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r, int t) {
-  if (t == 0) return 0;
-  long long c = (long long)t * (kItemCost + max(r.ctx, 0));
-  if (r.ctx >= 0) c += (long long)p.R * t * (t + 1) / 2;
-  return c;
+// cost of a request's first t row tiles under one head (all but the last are full), with
+// `item` for each beside its keys. (Rows without keys are written by the one warp that plans.)
+__device__ __forceinline__ long long cost_before(const TaParams& p, const Req& r, int t, int item) {
+  if (r.ctx < 0) return (long long)t * kItemCost;
+  return (long long)t * (item + r.ctx) + (long long)p.R * t * (t + 1) / 2;
 }
-__device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r) {
-  return r.n ? cost_before(p, r, r.tiles - 1) + kItemCost + keys_of(p, r, r.tiles - 1) : 0;
+__device__ __forceinline__ long long cost_of(const TaParams& p, const Req& r, int item) {
+  if (r.ctx < 0) return (long long)r.tiles * kItemCost;
+  return r.n ? cost_before(p, r, r.tiles - 1, item) + item + r.ctx + r.n : 0;
 }
 // By a whole warp: the largest i below n (n >= 1) with f(i) <= x, for f increasing and
 // f(0) <= x; 32 places are tried at a time.
@@ -282,6 +282,7 @@ struct Walk {
   int b, h, t;
   Req r;
   int lo, hi, len;     // of request b + 1, read ahead
+  int item;            // cost of a row tile beside its keys
   long long from;      // the row tile that this CTA begins and others go on with: its cost, -1 none
   Part* last;          // (in shared memory)
 
@@ -307,6 +308,7 @@ struct Walk {
     const int lane = threadIdx.x & 31, B = p.a.requests, per = (B + 31) >> 5;
     const int b0 = min(lane * per, B), b1 = min(b0 + per, B), cap = p.a.table_width << p.a.page_shift;
     long long mine = 0;
+    int tiles = 0, longest = 0;
     r = Req{};
 #pragma unroll 1
     for (int i0 = b0; i0 < b1; i0 += 4) {
@@ -323,7 +325,9 @@ struct Walk {
       for (int j = 0; j < min(b1 - i0, 4); ++j) {
         const Req q = req_of(p, from_row[0], to_row[0], lens[0]);
         if (i0 + j == b0) r = q;
-        mine += cost_of(p, q);
+        mine += cost_of(p, q, 0);
+        tiles += q.ctx < 0 ? 0 : q.tiles;
+        longest = max(longest, q.ctx + q.n);
         if (blockIdx.x == 0 && q.n && lens[0] > cap) atomicOr(p.err.word, DEVERR_RANGE);
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
@@ -334,17 +338,35 @@ struct Walk {
       }
     }
     mine *= p.a.kv_heads;
+    tiles *= p.a.kv_heads;   // (below 2^28)
     __syncwarp();
     long long before = mine;
+    int tiles_before = tiles;
 #pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, before, d);
-      if (lane >= d) before += o;
+      const int ot = __shfl_up_sync(0xffffffffu, tiles_before, d);
+      if (lane >= d) {
+        before += o;
+        tiles_before += ot;
+      }
     }
-    const long long total = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
+    long long total = __shfl_sync(0xffffffffu, before, 31);
+    const int all_tiles = __shfl_sync(0xffffffffu, tiles_before, 31);
+    // A share holds at least a row tile's cost and one key tile. Where that would leave half
+    // of the SMs idle the cost is taken lower, but the longest row tile is in 16 parts at most, which
+    // its warps join in one round. Measured so and without, one token of 2000, 4 of 2000, 4
+    // trees of 16 behind 1000 (head_dim 128): 13.8 and 14.3, 14.8 and 15.3, 15.1 and 16.1 us;
+    // with single key tiles however long the row tiles are, one token of 8000 19.5 for 16.2;
+    // with the lower cost whenever an SM is idle, 7 trees of 61 (head_dim 64) 19.7 for 18.7.
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    item = 2 * (total + (long long)all_tiles * kItemCost) >= (long long)gridDim.x * (kItemCost + 128)
+               ? kItemCost : min(kItemCost, max(1, longest / 16 - 128));
+    total += (long long)all_tiles * item;
+    mine += (long long)tiles * item;
+    before += (long long)tiles_before * item - mine;
     // (a little more than the quotient: the shares cover the total)
-    const long long share = max((long long)__umul64hi(total, p.inv_ctas) + 1, (long long)(kItemCost + 128));
+    const long long share = max((long long)__umul64hi(total, p.inv_ctas) + 1, (long long)(item + 128));
     c0 = blockIdx.x * share;
     c1 = c0 + share;
     const bool owner = c0 >= before && c0 < before + mine;
@@ -352,11 +374,11 @@ struct Walk {
     if (!who) return;
     long long head = 0;
     if (owner) {
-      head = cost_of(p, r);
+      head = cost_of(p, r, item);
       for (b = b0; c0 >= before + p.a.kv_heads * head;) {
         before += p.a.kv_heads * head;
         r = load(++b);
-        head = cost_of(p, r);
+        head = cost_of(p, r, item);
       }
     }
     __syncwarp();
@@ -369,15 +391,15 @@ struct Walk {
     ahead();
     h = search(p.a.kv_heads, c0 - at, [&](int i) { return i * head; });
     at += h * head;
-    t = search(r.tiles, c0 - at, [&](int i) { return cost_before(p, r, i); });
-    at += cost_before(p, r, t);
+    t = search(r.tiles, c0 - at, [&](int i) { return cost_before(p, r, i, item); });
+    at += cost_before(p, r, t, item);
   }
   // The next part that has work: key tiles, or a row tile without keys that
   // begins here.
   __device__ __forceinline__ bool next(Part& s) {
     while (b < p.a.requests && at < c1) {
       const int keys = keys_of(p, r, t), nk = (keys + 127) >> 7;
-      const long long cost = kItemCost + keys;
+      const long long cost = r.ctx < 0 ? kItemCost : item + keys;
       const bool begins = at >= c0;
       s.b = b;
       s.h = h;
@@ -387,8 +409,8 @@ struct Walk {
       s.ctx = r.ctx;
       s.keys = keys;
       s.nk = nk;
-      s.k0 = border(c0 - at, cost, nk);
-      s.k1 = border(c1 - at, cost, nk);
+      s.k0 = border(c0 - at, cost, nk, item);
+      s.k1 = border(c1 - at, cost, nk, item);
       s.place = 2 * blockIdx.x + (begins ? 1 : 0);
       s.stop = 0;
       if (begins && at + cost > c1) {
@@ -415,11 +437,11 @@ struct Walk {
   __device__ __forceinline__ AttnShared shared() const {
     AttnShared m = {};
     if (from < 0 || last->nk == 0) return m;
-    const long long cost = kItemCost + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
+    const long long cost = item + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
     const int n = search(kAttnMaxCtas, x, [&](int i) { return i * share; });   // CTAs on, where the tile ends
     int first = blockIdx.x, end = blockIdx.x + n;
     if (last->k1 == 0) ++first;
-    if (border(end * share - from, cost, last->nk) == last->nk) --end;
+    if (border(end * share - from, cost, last->nk, item) == last->nk) --end;
     if (end > first) {
       m.row = last->row + last->tok0;
       m.tokens = last->tokens;
@@ -430,9 +452,9 @@ struct Walk {
     return m;
   }
   // Key tile at which a cost x into a row tile falls.
-  static __device__ __forceinline__ int border(long long x, long long cost, int nk) {
+  static __device__ __forceinline__ int border(long long x, long long cost, int nk, int item) {
     if (x >= cost) return nk;
-    const long long k = (x - kItemCost + 64) >> 7;
+    const long long k = (x - item + 64) >> 7;
     return (int)(k < 0 ? 0 : k > nk ? nk : k);
   }
 };
