@@ -37,7 +37,7 @@
 // one token of each of 76 contexts of 16000, bf16: head_dim 64 102 us, 128 185, 256
 // 353 (6.1, 6.7, 7.1 TB/s: memory); e4m3 107, 130, 227 (2.9, 4.8, 5.5 TB/s: a tile's
 // way through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need
-// 700 to 2,800). 2 prompts of 2000 tokens behind 2096: 107, 132, 227 us (0.67, 1.08,
+// 700 to 2,800). 2 prompts of 2000 tokens behind 4096: 107, 132, 227 us (0.67, 1.08,
 // 1.26 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
 // 1,024: its chain of 4,400 (S 950, softmax 2,400, P V 1,050) runs in 3 tiles at a
 // time, which is all that tensor memory has place for; and 5,000 more go where a
@@ -338,7 +338,7 @@ struct Walk {
       }
     }
     mine *= p.a.kv_heads;
-    tiles *= p.a.kv_heads;   // (below 2^28)
+    tiles *= p.a.kv_heads;   // (below 2^29 where the requests' rows are apart)
     __syncwarp();
     long long before = mine;
     int tiles_before = tiles;
@@ -375,7 +375,8 @@ struct Walk {
     long long head = 0;
     if (owner) {
       head = cost_of(p, r, item);
-      for (b = b0; c0 >= before + p.a.kv_heads * head;) {
+      // (bounded: offsets that go back and forth can make the sums overflow)
+      for (b = b0; b + 1 < b1 && c0 >= before + p.a.kv_heads * head;) {
         before += p.a.kv_heads * head;
         r = load(++b);
         head = cost_of(p, r, item);
@@ -388,6 +389,7 @@ struct Walk {
     head = __shfl_sync(0xffffffffu, head, src);
     b = all(b);
     r = {all(r.row), all(r.n), all(r.ctx), all(r.tiles)};
+    if (r.tiles == 0) b = p.a.requests;
     ahead();
     h = search(p.a.kv_heads, c0 - at, [&](int i) { return i * head; });
     at += h * head;
@@ -439,7 +441,7 @@ struct Walk {
     if (from < 0 || last->nk == 0) return m;
     const long long cost = item + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
     const int n = search(kAttnMaxCtas, x, [&](int i) { return i * share; });   // CTAs on, where the tile ends
-    int first = blockIdx.x, end = blockIdx.x + n;
+    int first = blockIdx.x, end = min(blockIdx.x + n, gridDim.x - 1);
     if (last->k1 == 0) ++first;
     if (border(end * share - from, cost, last->nk, item) == last->nk) --end;
     if (end > first) {

@@ -1,0 +1,184 @@
+"""Attention over a paged cache at the ends of its ranges: caches beyond 2^31 elements, 4096
+requests, queries of a wide range over an e4m3 cache, contexts and row tiles that SMs share in
+every way, two graphs on one handle."""
+import math
+
+import pytest
+import torch
+
+import bit_grouped_gemm_gb300 as bg
+
+from . import attention_ref as ref
+from .attention_ref import DEV, i32
+from .test_gpu_attention import PageCase, run_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_grouped_gemm_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_cache_beyond_32_bits(cache):
+    """Pages on both sides of elements 2^31 and, for bf16, of bytes 2^32 and 2^33: what is stored
+    there is what attention reads."""
+    Hkv, page, D, pages = 2, 256, 256, 36000          # 4.7e9 elements each
+    T, ctx = 5, 600
+    dt = torch.bfloat16 if cache == "bf16" else torch.float8_e4m3fn
+    kc, vc = (torch.empty(pages, Hkv, page, D, dtype=dt, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((Hkv,), 0.02, device=DEV) for _ in range(2)) if cache == "e4m3" else (None, None)
+    ids = [16383, 35999, 16384, 32767, 0, 32768]
+    for p in ids:
+        kc[p], vc[p] = 0, 0
+    g = torch.Generator(device=DEV).manual_seed(1)
+    total = ctx + T
+    need = -(-total // page)
+    table = i32([ids[:need], ids[need:2 * need]])
+    n = 2 * total
+    pos = torch.arange(total).repeat(2)
+    slot = torch.cat([torch.tensor([table[b, j // page].item() * page + j % page for j in range(total)])
+                      for b in range(2)])
+    assert int(slot.max()) * Hkv * D > 2 ** 32
+    r = lambda h: torch.randn(n, h * D, generator=g, device=DEV).bfloat16()
+    q, k, v = r(4), r(Hkv), r(Hkv)
+    a = bg.moe_attn_create(bg.attn_desc(4, Hkv, D, page, cache=cache, max_tokens=n, rotary_dim=0), 0)
+    c = bg.kv_cache(kc, vc, ks, vs)
+    try:
+        bg.moe_rope_store(a, q, k, v, n, i32(pos), i32(slot), torch.empty_like(q), c)
+        at = slot.to(DEV)
+        for store, x, s in ((kc, k, ks), (vc, v, vs)):
+            got = store[at // page, :, at % page].float().double()
+            want = x.double().view(n, Hkv, D)
+            if s is None:
+                assert torch.equal(got, want)
+            else:
+                want = (want / 0.02).clamp(-448, 448)
+                assert ((got - want).abs() <= torch.clamp(want.abs() * 2.0 ** -4, min=2.0 ** -10) * 1.001).all()
+        qn = torch.cat([q[total - T:total], q[2 * total - T:]]).contiguous()
+        out = torch.zeros(2 * T, 4 * D, dtype=torch.bfloat16, device=DEV)
+        bg.moe_tree_attention(a, qn, 2 * T, c, table, i32([0, T, 2 * T]), i32([total, total]), out)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+        want, bound = ref.attention(qn.view(2 * T, 4, D), kc, vc, ks, vs, table, [total, total], [T, T], None,
+                                    1 / math.sqrt(D))
+        assert ((out.double().view(2 * T, 4, D) - want).abs() <= bound).all()
+    finally:
+        bg.moe_attn_destroy(a)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_4096_requests(cache):
+    """The most requests: some not served, some without tokens, contexts of 0 to 200."""
+    h = torch.Generator().manual_seed(4)
+    r = lambda hi: torch.randint(0, hi, (4096,), generator=h).tolist()
+    news = [x % 3 for x in r(6)]
+    lengths = [c + n if i % 11 else n - 1 for i, (c, n) in enumerate(zip(r(200), news))]
+    run_attention([max(x, 0) for x in lengths], news, 4, 1, 64, 16, cache)
+
+
+def test_a_page_map_of_4096_requests():
+    h = torch.Generator().manual_seed(8)
+    r = lambda hi: torch.randint(0, hi, (4096,), generator=h).tolist()
+    context, added, page = r(300), [x - 1 if x < 3 else x for x in r(6)], 32
+    owned = [-(-c // page) for c in context]
+    rows = sum(max(a, 0) for a in added)
+    need = sum(max(0, -(-(c + max(a, 0)) // page) - o) for c, a, o in zip(context, added, owned))
+    cap = need + sum(owned) + 1
+    PageCase(page, 11, rows + 5, cap, 1, context, added, owned, [cap - 1, need], seed=8).check()
+
+
+def test_queries_of_a_wide_range_over_8_bit_keys():
+    """Queries with a few elements of 2^9 times the others: kept exactly down to 2^-10 of the row's
+    largest, below that to 2^-17 of it, which adds scale 2^-17 max|q| sum|k| to a score's error
+    (and an element of 2^-20 of it is lost at most by itself)."""
+    D, Hq, Hkv, page, L = 128, 8, 2, 64, 900
+    g, h = torch.Generator(device=DEV).manual_seed(5), torch.Generator().manual_seed(5)
+    table, pages = ref.table_of(h, [L], page)
+    kc, vc, ks, vs = ref.cache_of(g, pages, Hkv, page, D, "e4m3")
+    q = torch.randn(4, Hq, D, generator=g, device=DEV)
+    q[:, :, ::37] *= 512.0
+    q[1] *= 2.0 ** -60                 # all small, all large: the row's own scale
+    q[2, :, 1::2] *= 2.0 ** -12
+    q[3] = 0
+    kc.view(torch.uint8)[..., ::37] = 0      # the large elements see no keys: the small ones decide
+    q = q.bfloat16()
+    out = torch.zeros(4, Hq * D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, cache="e4m3", max_tokens=4, rotary_dim=0), 0)
+    try:
+        bg.moe_tree_attention(a, q, 4, bg.kv_cache(kc, vc, ks, vs), table, i32([0, 4]), i32([L]), out)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    scale = 1 / math.sqrt(D)
+    want, bound = ref.attention(q, kc, vc, ks, vs, table, [L], [4], None, scale)
+    j = torch.arange(L, device=DEV)
+    ids = table[0].long()[j // page]
+    for head in range(Hq):
+        kv = head // (Hq // Hkv)
+        k = kc[ids, kv, j % page].float().double() * ks[kv].double()
+        v = vc[ids, kv, j % page].float().double() * vs[kv].double()
+        for t in range(4):
+            p = torch.softmax((k @ q[t, head].double()) * scale, 0)
+            es = scale * 2.0 ** -17 * float(q[t, head].abs().max()) * k.abs().sum(1).amax()
+            more = (p @ v.abs()) * 2 * torch.expm1(2 * es)
+            off = (out.view(4, Hq, D)[t, head].double() - want[t, head]).abs()
+            assert (off <= bound[t, head] + more).all(), (t, head)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,cache", [(16, 2, 128, "bf16"), (8, 1, 64, "e4m3"), (4, 4, 256, "bf16"),
+                                           (6, 2, 256, "e4m3")])
+def test_row_tiles_shared_in_every_way(Hq, Hkv, D, cache):
+    """Few and many SMs per row tile: single key tiles, whole shares, one long context among
+    short ones, keys that end just before and behind key tiles' borders."""
+    for lengths in ([129], [255, 1], [2049], [4000, 17, 128], [127, 128, 129, 640], [9000],
+                    [20000, 3, 500] + [64] * 20, [385] * 30):
+        run_attention(lengths, [1 + i % 2 * min(1, n - 1) for i, n in enumerate(lengths)], Hq, Hkv, D, 64, cache)
+    run_attention([700, 2500, 40], [64, 30, 40], Hq, Hkv, D, 64, cache, words=1)
+    run_attention([700, 300], [700, 300], Hq, Hkv, D, 64, cache)
+
+
+def test_two_graphs_of_one_handle():
+    """Graphs that share a handle, replayed one after the other and mixed with plain calls."""
+    D, Hq, Hkv, page = 128, 8, 2, 32
+    g = torch.Generator(device=DEV).manual_seed(9)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, max_tokens=64, rotary_dim=0), 0)
+    cases = []
+    for seed, (lengths, news) in enumerate((([3000, 50], [1, 3]), ([260], [40]))):
+        table, pages = ref.table_of(torch.Generator().manual_seed(seed), lengths, page)
+        kc, vc, _, _ = ref.cache_of(g, pages, Hkv, page, D, "bf16")
+        T = sum(news)
+        q = torch.randn(T, Hq * D, generator=g, device=DEV).bfloat16()
+        out = torch.zeros_like(q)
+        off = i32([sum(news[:i]) for i in range(len(news) + 1)])
+        cases.append(dict(q=q, T=T, cache=bg.kv_cache(kc, vc), kept=(kc, vc), table=table, off=off,
+                          length=i32(lengths), out=out))
+    run = lambda c: bg.moe_tree_attention(a, c["q"], c["T"], c["cache"], c["table"], c["off"], c["length"],
+                                          c["out"])
+    try:
+        want = []
+        for c in cases:
+            run(c)
+            torch.cuda.synchronize()
+            want.append(c["out"].clone())
+        graphs = []
+        for c in cases:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run(c)
+            graphs.append(graph)
+        for i in (0, 1, 1, 0, 1):
+            for c in cases:
+                c["out"].zero_()
+            graphs[i].replay()
+            run(cases[1 - i])
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            for c, w in zip(cases, want):
+                assert torch.equal(c["out"], w)
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
