@@ -44,13 +44,8 @@ struct AttnArgs {
 // Scratch: a CTA leaves the sums of at most two row tiles that it shares with
 // other CTAs, each of up to 128 rows, and says which shared tile it begins.
 constexpr int kAttnMaxCtas = 160;
-struct AttnShared {
-  int row, tokens, head;   // first token row, tokens and key-value head of the tile
-  int first, count;        // CTAs that hold its parts; count 0: none
-  int pad[3];
-};
 constexpr size_t attn_scratch_bytes(int head_dim) {
-  return kAttnMaxCtas * (sizeof(AttnShared) + 2 * 128 * ((size_t)head_dim + 2) * 4);
+  return kAttnMaxCtas * (8 + 2 * 128 * ((size_t)head_dim + 2) * 4);
 }
 cudaError_t launch_tree_attention(const AttnArgs& a, void* scratch, int num_sms, DevErr err,
                                   cudaStream_t st);

@@ -100,7 +100,7 @@ struct Shape {
 struct TaParams {
   CUtensorMap mq, mk, mv;
   AttnArgs a;
-  AttnShared* shared;
+  unsigned long long* shared;    // [cta] the tile that it begins and shares, packed
   float2* ml;          // [cta][2][128] maximum (log2) and sum
   float* o;            // [cta][2][D][128]: a warp stores a column of its 32 rows at a time
   unsigned long long inv_ctas;   // 2^64 / CTAs, rounded up
@@ -275,6 +275,22 @@ struct Part {
   int stop;        // the end of the CTA's parts
 };
 
+// A row tile that several CTAs share: its first token row, tokens and key-value head, and the
+// CTAs that hold its parts (count 0: none). In 8 bytes, since every block of the join reads
+// all of them.
+struct Tile {
+  int row, tokens, head, first, count;
+};
+__device__ __forceinline__ unsigned long long packed(const Tile& m) {
+  static_assert(kAttnMaxCtas < 256, "fields of 8 bits");
+  return (unsigned long long)(unsigned)m.row << 32 |
+         (unsigned)(m.tokens << 24 | m.head << 16 | m.first << 8 | m.count);
+}
+__device__ __forceinline__ Tile unpacked(unsigned long long x) {
+  const unsigned y = (unsigned)x;
+  return {(int)(x >> 32), (int)(y >> 24), (int)(y >> 16 & 255), (int)(y >> 8 & 255), (int)(y & 255)};
+}
+
 // The CTA's parts, in order.
 struct Walk {
   const TaParams& p;
@@ -436,8 +452,8 @@ struct Walk {
     return false;
   }
   // The row tile that this CTA begins and others go on with: which hold a part.
-  __device__ __forceinline__ AttnShared shared() const {
-    AttnShared m = {};
+  __device__ __forceinline__ Tile shared() const {
+    Tile m = {};
     if (from < 0 || last->nk == 0) return m;
     const long long cost = item + last->keys, share = c1 - c0, x = from + cost - 1 - c0;
     const int n = search(kAttnMaxCtas, x, [&](int i) { return i * share; });   // CTAs on, where the tile ends
@@ -754,9 +770,9 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // own copies land before shared memory is released
     if (!ok) drain_ring<QB>(E ? bs.q_raw : bs.q_full, qring.i, qring.phase, loads, QB, p.err.limit_ns);
     __syncwarp();
-    AttnShared m = walk.shared();
+    Tile m = walk.shared();
     if (*abort_flag) m.count = 0;
-    if (lane == 0) p.shared[blockIdx.x] = m;
+    if (lane == 0) p.shared[blockIdx.x] = packed(m);
   } else if (role == kLoad) {
     const Bars<D, E> bs(smem_u32(bar_words));
     // ------------------------- loads by TMA: a tile's keys, then the last tile's values
@@ -1351,27 +1367,29 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
 // Joins the parts of the row tiles that CTAs share. A unit is 8 columns of 32
 // rows, a row per lane; it has as many warps as 2 parts each need, up to all 8 of
 // a block, which take alternate parts and add up through shared memory. The units
-// of all shared tiles, in groups that fill a block, are dealt over the grid.
-// (16 blocks per CTA that may have begun a tile took 15 us for 152 tiles of 2 parts,
-// most of them waiting for their description; this takes 7.)
-constexpr int kJoinWarps = 8, kJoinGrid = 5;     // blocks per SM
+// of all shared tiles, in groups that fill a block, are dealt over the grid. Bound
+// by its launch and four round trips where rows are few, else by reading the parts.
+// Blocks per SM 5 (48 registers each, which spill), 3 and 2: one token 12.5, 11.0,
+// 10.8 us, 32 trees of 128 rows 28.9, 27.1, 27.9, 2 long contexts 42.4, 40.2, 39.3.
+// (16 blocks for each CTA that may have begun a tile: 15 us for the trees alone.)
+constexpr int kJoinWarps = 8, kJoinGrid = 2;
 __device__ __forceinline__ int join_log_per(int count) {   // log2 of a unit's warps
   return count <= 2 ? 0 : count <= 4 ? 1 : count <= 8 ? 2 : 3;
 }
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinGrid) tree_attn_join(const TaParams p, int ctas) {
   pdl_begin();
-  constexpr int V = 8, U = 2, kCols = D / V, kRuns = kAttnMaxCtas / 32;
+  constexpr int V = 8, U = 3, kCols = D / V, kRuns = kAttnMaxCtas / 32;
   __shared__ float s_o[kJoinWarps][V][32];
   __shared__ float2 s_ml[kJoinWarps][32];
-  __shared__ AttnShared s_tiles[kAttnMaxCtas];
+  __shared__ unsigned long long s_tiles[kAttnMaxCtas];
   __shared__ int s_groups[kAttnMaxCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kAttnMaxCtas <= 32 * kJoinWarps, "a thread per CTA");
   if (threadIdx.x < kAttnMaxCtas) {
-    AttnShared s = {};
-    if ((int)threadIdx.x < ctas) s = p.shared[threadIdx.x];
-    s_tiles[threadIdx.x] = s;
+    const unsigned long long x = (int)threadIdx.x < ctas ? p.shared[threadIdx.x] : 0;
+    const Tile s = unpacked(x);
+    s_tiles[threadIdx.x] = x;
     const int units = (s.tokens * p.G + 31) / 32 * kCols, log_once = 3 - join_log_per(s.count);
     s_groups[threadIdx.x] = s.count ? (units + (1 << log_once) - 1) >> log_once : 0;
   }
@@ -1403,7 +1421,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinGrid) tree_attn_join(con
       }
     c = __shfl_sync(0xffffffffu, kRuns * lane + c, owner);
     rest = __shfl_sync(0xffffffffu, rest, owner);
-    const AttnShared s = s_tiles[c];
+    const Tile s = unpacked(s_tiles[c]);
     const int log_per = join_log_per(s.count), per = 1 << log_per, sub = warp & (per - 1);
     const int rows = s.tokens * p.G, unit = (rest << (3 - log_per)) + (warp >> log_per);
     const int col = unit % kCols * V, row = 32 * (unit / kCols) + lane;
@@ -1441,14 +1459,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinGrid) tree_attn_join(con
       s_ml[warp][lane] = make_float2(m, l);
       __syncthreads();
       if (sub == 0) {
-        for (int w = warp + 1; w < warp + per; ++w) {
-          const float2 ml = s_ml[w][lane];
-          if (ml.y == 0.0f) continue;
-          const float mn = fmaxf(m, ml.x), f = ex2(m - mn), e = ex2(ml.x - mn);
-          m = mn;
-          l = l * f + ml.y * e;
+        float2 ml[kJoinWarps];
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[v] = o[v] * f + s_o[w][v][lane] * e;
+        for (int w = 0; w < kJoinWarps; ++w) {
+          ml[w] = w < per ? s_ml[warp + w][lane] : make_float2(0.0f, 0.0f);
+          if (ml[w].y != 0.0f) m = fmaxf(m, ml[w].x);   // (warp w = 0: its own)
+        }
+        l = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          if (ml[w].y == 0.0f) continue;
+          const float e = ex2(ml[w].x - m);
+          l += ml[w].y * e;
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += s_o[warp + w][v][lane] * e;
         }
       }
     }
@@ -1498,7 +1524,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, void* scratch, int num_sms,
   p.G = a.heads / a.kv_heads;
   p.R = 128 / p.G;
   p.err = err;
-  p.shared = static_cast<AttnShared*>(scratch);
+  p.shared = static_cast<unsigned long long*>(scratch);
   p.o = reinterpret_cast<float*>(p.shared + kAttnMaxCtas);
   p.ml = reinterpret_cast<float2*>(p.o + (size_t)kAttnMaxCtas * 2 * 128 * a.head_dim);
   if (!encode_maps(a, p.G, p.R, &p)) return cudaErrorInvalidValue;

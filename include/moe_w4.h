@@ -562,7 +562,7 @@ moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride
  * in the pages table[b], and context c = length[b] - n. Its row i sees key j if
  *   j < c, or j - c <= i and (mask NULL or bit j - c of the row's mask).
  *   out[t][h] = softmax(scale q[t][h] K^T over the keys seen) V  (bf16, rounded once)
- * Key-value head h / (heads / kv_heads) serves query head h. mask: [T][mask_words],
+ * Offsets ascend. Key-value head h / (heads / kv_heads) serves query head h. mask: [T][mask_words],
  * mask_words 1..4; new tokens past 64 * mask_words have no bit and are not seen.
  * A row that sees no key, and every row of a request with length[b] < n, is zero.
  * Rows before offsets[0] and from offsets[requests] on are left as they were.
