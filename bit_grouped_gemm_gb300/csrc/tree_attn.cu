@@ -59,10 +59,11 @@ constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 16-bit elements
 // products. The planner has little to do and shares its scheduler with the softmax of rows
 // 0..31, often the only ones.
 constexpr int kPlan = 0, kScore = 1, kLoad = 2, kSum = 3, kConv = 4, kConvWarps = 4;
-// Cost of a row tile beside its keys, in keys, for equal shares. Measured: a batch of 76 tokens,
-// drafted trees, one token: 128 40.5, 41.7, 14.3 us; 256 35.1, 36.5, 14.3; 384 33.3, 35.3, 14.1;
-// 512 33.1, 34.4, 15.7 (a share is at least a tile and its cost: fewer SMs).
-constexpr int kItemCost = 384;
+// Cost of a row tile beside its keys, in keys, for equal shares. Measured with 192, 256, 320, 384
+// and 512: 64 tokens behind 1 to 16384 (head_dim 128) 28.4, 28.3, 28.4, 28.3, 28.7 us, 300 behind 1
+// to 1500 38.6, 37.3, 37.6, 38.7, 39.9, 32 trees of 16 behind 1 to 8192 (head_dim 256) 29.8, 28.6,
+// 28.2, 27.9, 28.0, 7 trees of 61 (head_dim 64, e4m3) 17.3, 17.0, 16.2, 16.8, 16.5.
+constexpr int kItemCost = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrowth = 8.0f;             // log2 by which a maximum may be exceeded
 constexpr int kParts = 4;                    // parts told ahead
@@ -369,15 +370,16 @@ struct Walk {
     }
     long long total = __shfl_sync(0xffffffffu, before, 31);
     const int all_tiles = __shfl_sync(0xffffffffu, tiles_before, 31);
-    // A share holds at least a row tile's cost and one key tile. Where that would leave half
-    // of the SMs idle the cost is taken lower, but the longest row tile is in 16 parts at most, which
-    // its warps join in one round. Measured so and without, one token of 2000, 4 of 2000, 4
-    // trees of 16 behind 1000 (head_dim 128): 13.8 and 14.3, 14.8 and 15.3, 15.1 and 16.1 us;
-    // with single key tiles however long the row tiles are, one token of 8000 19.5 for 16.2;
-    // with the lower cost whenever an SM is idle, 7 trees of 61 (head_dim 64) 19.7 for 18.7.
+    // A share holds at least a row tile's cost and one key tile. Where that would leave SMs
+    // idle the cost is taken lower: to nothing for few row tiles, whose key tiles then go
+    // singly, else to a key tile, so that an SM does not begin many short ones; but the
+    // longest row tile is in 16 parts at most, which its warps join in one round. Measured
+    // (head_dim 128) so and with the whole cost: one token of 2000 11.1 and 11.5 us, 4 trees of
+    // 16 behind 1000 13.0 and 14.2, 32 behind 1 to 2000 16.3 and 18.7; with no cost whatever
+    // the number, the last 27.7; in more parts, one token of 8000 16.6 for 13.3.
     longest = __reduce_max_sync(0xffffffffu, longest);
-    item = 2 * (total + (long long)all_tiles * kItemCost) >= (long long)gridDim.x * (kItemCost + 128)
-               ? kItemCost : min(kItemCost, max(1, longest / 16 - 128));
+    item = total + (long long)all_tiles * kItemCost >= (long long)gridDim.x * (kItemCost + 128)
+               ? kItemCost : min(kItemCost, max(8 * all_tiles <= gridDim.x ? 1 : 128, longest / 16 - 128));
     total += (long long)all_tiles * item;
     mine += (long long)tiles * item;
     before += (long long)tiles_before * item - mine;
