@@ -506,11 +506,9 @@ __device__ __forceinline__ unsigned long long seen_bits(int a, int i, const unsi
   return v;
 }
 
-// Sets the elements of 8 bf16 (or fp16) that are no finite numbers to zero; true
-// if there are any.
-template <bool F16>
+// Sets the elements of 8 bf16 that are no finite numbers to zero; true if there are any.
 __device__ __forceinline__ bool clear_unbounded(uint4& x) {
-  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+  constexpr uint32_t kExp = 0x7f80u;
   uint32_t* w = reinterpret_cast<uint32_t*>(&x);
   bool any = false;
 #pragma unroll
@@ -521,6 +519,13 @@ __device__ __forceinline__ bool clear_unbounded(uint4& x) {
     any |= lo || hi;
   }
   return any;
+}
+
+// Sets those of 4 e4m3 codes that are NaNs (all ones but for the sign) to zero; true if there are any.
+__device__ __forceinline__ bool clear_nan_codes(uint32_t& x) {
+  const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  x &= ~((nan >> 7) * 0xffu);
+  return nan != 0;
 }
 
 // Two e4m3 as fp16, exactly; a NaN stays one.
@@ -1011,11 +1016,24 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         if (!(ok = wait(bs.v_free + 8 * vals.i, vals.phase ^ 1, 14))) break;
         uint8_t* dst = s_values + vals.i * Sh::kVBlock + 128 * row;
         const uint8_t* src = raw_values + rvals.i * Sh::kRawBlock + 64 * GC * row + 16 * piece;
+        const int key0 = 128 * (kb / NG) + row;
+        const bool masked = 128 * (kb / NG + 1) > seen;
+        bool any = false;
 #pragma unroll 1
         for (int c = 0; c < GC; ++c) {
           uint4 x[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(src + 64 * c + 512 * GC * j);
+          if (masked) {
+            // values of a tile that not every row sees whole: what some row must not see
+            // is cleared, keys past the row tile's own, and what is no number
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (key0 + 8 * j < seen) continue;
+              if (key0 + 8 * j >= s.keys) x[j] = make_uint4(0, 0, 0, 0);
+              any |= clear_nan_codes(x[j].x) | clear_nan_codes(x[j].y) | clear_nan_codes(x[j].z) | clear_nan_codes(x[j].w);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 y = x[j];
@@ -1026,22 +1044,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
                                                               e4m3x2_f16x2(y.w), e4m3x2_f16x2(y.w >> 16));
           }
         }
-        const int k = kb / NG;
-        if (128 * (k + 1) > seen) {
-          // values of a tile that not every row sees whole: what some row must
-          // not see is cleared, keys past the row tile's own, and what is no number
-          bool any = false;
-#pragma unroll 1
-          for (int i = 0; i < 8 * GC; ++i) {
-            const int n = i >> 1, key = 128 * k + row + 8 * (n & 3);
-            uint4* y = reinterpret_cast<uint4*>(dst + (n >> 2) * kSlotBytes + 1024 * (n & 3) + (i & 1 ? p1 : p0));
-            if (key < seen) continue;
-            uint4 x = key < s.keys ? *y : make_uint4(0, 0, 0, 0);
-            any |= clear_unbounded<true>(x);
-            *y = x;
-          }
-          if (any) s_unbounded[np % kParts] = (int)np + 1;
-        }
+        if (any) s_unbounded[np % kParts] = (int)np + 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -1253,7 +1256,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
 #pragma unroll 1
             for (int q = 0; q < GC * 8; ++q) {
               uint4 y = *piece(q);
-              if (clear_unbounded<false>(y)) *piece(q) = y;
+              if (clear_unbounded(y)) *piece(q) = y;
             }
           }
           if (!ok) break;
