@@ -21,8 +21,8 @@
 //   * An e4m3 cache: the codes of the keys are the product's operand as they lie in
 //     the cache, times queries in two e4m3 terms. Four more warps make these, and
 //     turn values to fp16 (exact; the weights are then fp16 as well). Converting
-//     the keys too took 55 us where this takes 43 (2 contexts of 16384 tokens, trees
-//     of 8), and 157 where it takes 130 (76 contexts of 16000, one token each).
+//     the keys too took 55 us where this took 45 (2 contexts of 131072 tokens, trees
+//     of 8), and 157 where it took 117 (76 contexts of 16000, one token each).
 //   * A split of the keys gives every CTA the same work: all row tiles side by
 //     side, each as long as its keys and kItemCost, are cut into equal lengths, one
 //     per CTA, at key tiles' borders. A row tile that several CTAs share leaves its
@@ -34,16 +34,16 @@
 //     see them, added at the end.
 //
 // Measured (in a graph; 16 query heads, 2 key-value heads, pages of 64, one GB300):
-// one token of each of 76 contexts of 16000, bf16: head_dim 64 102 us, 128 185, 256
-// 353 (6.1, 6.7, 7.1 TB/s: memory); e4m3 107, 130, 227 (2.9, 4.8, 5.5 TB/s: a tile's
+// one token of each of 76 contexts of 16000, bf16: head_dim 64 101 us, 128 184, 256
+// 351 (6.2, 6.8, 7.1 TB/s: memory); e4m3 99, 117, 219 (3.2, 5.3, 5.7 TB/s: a tile's
 // way through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need
-// 700 to 2,800). 2 prompts of 2000 tokens behind 4096: 107, 132, 227 us (0.67, 1.08,
-// 1.26 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
+// 700 to 2,800). 2 prompts of 2000 tokens behind 4096: 107, 132, 229 us (0.67, 1.08,
+// 1.25 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
 // 1,024: its chain of 4,400 (S 950, softmax 2,400, P V 1,050) runs in 3 tiles at a
 // time, which is all that tensor memory has place for; and 5,000 more go where a
-// row tile ends (masked tile, sums read and stored). The least for one token is
-// about 11 us: two launches, the split's arithmetic 1, loads 1.5, the chain 2.5,
-// sums out 1, join 3.
+// row tile ends (masked tile, sums read and stored). One token of one context of
+// 120, 2000 and 32000: 8.7, 11.0, 17.8 us: two launches, planning 2, a page's
+// number and loads 1.5, the chain 2.5, sums out 1, join 2.
 #include <limits.h>
 
 #include "attn.h"
