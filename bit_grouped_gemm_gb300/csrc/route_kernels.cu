@@ -48,12 +48,16 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  int& have = allowed[{kernel, dev}];
-  if (bytes <= have) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) have = bytes;
-  return e;
+  try {   // (the map may be out of memory; no exception leaves a C entry)
+    std::lock_guard<std::mutex> lock(mu);
+    int& have = allowed[{kernel, dev}];
+    if (bytes <= have) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) have = bytes;
+    return e;
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 // 2D row-major tensor map: `rows` x `cols` elements, box `box_cols` x `box_rows`,

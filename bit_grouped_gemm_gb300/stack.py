@@ -89,10 +89,16 @@ def _rows(t, dtype, shape, dev) -> bool:
             t.device == dev and t.is_contiguous())
 
 
+def _here(dev) -> bool:
+    """Whether calls that run on the current device run on ``dev``."""
+    return dev.type != "cuda" or dev.index == torch.cuda.current_device()
+
+
 class PagedBatch:
     """The cache pages of up to ``requests`` requests, ``table_width`` each at most, and
     what a step's kernels need to know of its tokens; all of it on the device, where
-    moe_page_map keeps it, so that a captured step follows lengths that change.
+    moe_page_map keeps it, so that a captured step follows lengths that change. Calls
+    are made with its device as the current one.
 
     Pages 0..``pages``-1 are free at first. ``offsets``, ``length``, ``slot``,
     ``position``, ``mask`` (None without ``mask_words``) and ``status`` hold the last
@@ -123,7 +129,7 @@ class PagedBatch:
         """The next step: request b holds ``context[b]`` tokens and adds ``added[b]``
         (negative: it ends); ``parent`` int32 [max_tokens] makes trees of the new ones."""
         B, M, dev = self.desc.requests, self.desc.max_tokens, self.table.device
-        ok = _rows(context, torch.int32, (B,), dev) and _rows(added, torch.int32, (B,), dev)
+        ok = _here(dev) and _rows(context, torch.int32, (B,), dev) and _rows(added, torch.int32, (B,), dev)
         if parent is not None:
             ok = ok and self.mask is not None and _rows(parent, torch.int32, (M,), dev)
         if not ok:
@@ -146,8 +152,9 @@ class CachedAttention:
     the cache [pages, kv_heads, page_size, D], with scales for e4m3; ``adapters`` a
     ``binding.MoeLora`` of the first projection, or None. What a caller passes must
     outlive the layer. Rows of x behind the batch's last token are changed, but no
-    other row depends on them. A call takes up to ``max_tokens`` rows; wrong arguments
-    are refused before the first launch, so x is then as it was.
+    other row depends on them. A call takes up to ``max_tokens`` rows, with the layer's
+    device as the current one; wrong arguments are refused before the first launch, so x
+    is then as it was.
     """
 
     def __init__(self, attn: int, desc, norm, qkv, out, k, v, k_scale=None, v_scale=None,
@@ -185,7 +192,7 @@ class CachedAttention:
         T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
         if T > self.max_tokens or batch.desc.requests > self.desc.max_requests:
             raise binding.MoeError(binding.MOE_ERR_CAPACITY, "CachedAttention")
-        ok = self.project is not None and T > 0 and _rows(x, torch.bfloat16, (T, H), dev)
+        ok = self.project is not None and _here(dev) and T > 0 and _rows(x, torch.bfloat16, (T, H), dev)
         ok = ok and (y is None or _rows(y, torch.float32, (T, H), dev))
         ok = ok and batch.table.device == dev and T <= batch.desc.max_tokens
         ok = ok and batch.desc.page_size == self.desc.page_size

@@ -497,7 +497,8 @@ typedef struct {
  *     parent is no earlier token (these count as -1).
  * parent needs mask_words >= 1. All arrays 4-byte aligned, mask 8. No two of
  * the written arrays overlap, nor a written one and one that is read but for
- * the pairs named above; table and ring are both. */
+ * the pairs named above; table and ring are both. Needs no handle; runs on the
+ * current device. */
 moe_status moe_page_map(const moe_page_desc* desc, const int32_t* context, const int32_t* added,
                         const int32_t* parent, const moe_page_pool* pool, const moe_token_map* out,
                         moe_stream_t stream);

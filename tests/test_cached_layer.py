@@ -119,3 +119,16 @@ def test_steps_are_checked(monkeypatch, args):
     with pytest.raises(binding.MoeError):
         p.step(ids(B), ids(B), ids(T - 1))
     assert calls == ["moe_page_map"]
+
+
+def test_another_current_device_is_refused(monkeypatch):
+    dev = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert not stack._here(dev) and stack._here(torch.device("cuda", 0)) and stack._here(torch.device("cpu"))
+    calls, layer = make(monkeypatch)
+    p = batch()
+    monkeypatch.setattr(stack, "_here", lambda d: False)
+    for call in (lambda: layer(rows(), None, p), lambda: p.step(ids(B), ids(B))):
+        with pytest.raises(binding.MoeError):
+            call()
+    assert not calls
