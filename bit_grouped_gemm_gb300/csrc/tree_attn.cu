@@ -1098,6 +1098,12 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
         if (!mine) continue;
         const bool masked = 128 * (k0 + t + 1) > seen, last = t + 1 == n;
         const uint32_t sc = tmem + lanes + kColS + 128 * sring.i;
+        // the maximum that O refers to (as a rule there before the scores are)
+        float old = -INFINITY;
+        if (work && t > 0) {
+          if (!(ok = wait(take + 8 * (taken & 1), (taken >> 1) & 1, 15))) break;
+          old = top_in[128 * (taken & 1)];
+        }
         if (!(ok = wait(bs.s_full + 8 * sring.i, sring.phase, 17))) break;
         tc_fence_after();
         if (E && t < SG) c2 = fmaxf(c2 * s_qs[at.i * 128 + row], 1e-37f);   // (this group's first tile)
@@ -1149,11 +1155,6 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           }
           top = fmaxf(top, fmaxf(largest(x[0]), largest(x[1])));
           top *= c2;
-          float old = -INFINITY;   // the maximum that O refers to
-          if (t > 0) {
-            if (!(ok = wait(take + 8 * (taken & 1), (taken >> 1) & 1, 15))) break;
-            old = top_in[128 * (taken & 1)];
-          }
           // (NaN scores are left out of the maximum and make the sum NaN)
           const bool grow = top > old + kGrowth || old == -INFINITY;
           const float now = grow && top > old ? top : old;
