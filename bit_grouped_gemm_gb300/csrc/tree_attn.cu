@@ -35,7 +35,7 @@
 //
 // Measured (in a graph; 16 query heads, 2 key-value heads, pages of 64, one GB300):
 // one token of each of 76 contexts of 16000, bf16: head_dim 64 101 us, 128 184, 256
-// 351 (6.2, 6.8, 7.1 TB/s: memory); e4m3 99, 117, 219 (3.2, 5.3, 5.7 TB/s: a tile's
+// 351 (6.2, 6.8, 7.1 TB/s: memory); e4m3 99, 112, 218 (3.2, 5.6, 5.7 TB/s: a tile's
 // way through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need
 // 700 to 2,800). 2 prompts of 2000 tokens behind 4096: 107, 132, 229 us (0.67, 1.08,
 // 1.25 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
