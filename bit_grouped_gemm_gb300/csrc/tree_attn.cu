@@ -583,10 +583,14 @@ __device__ __forceinline__ bool bar_drain(Bar b, uint32_t parity, unsigned long 
 // Waits by a whole warp: true once the phase is over, false (and the CTA's abort
 // flag set) when the limit ran out or another role gave up. The part that has to
 // wait is a function of its own, out of the way of the roles' code: that of all
-// of them has to fit the instruction cache together.
+// of them has to fit the instruction cache together. The planner (sites 1 and 2)
+// may wait for as long as a part takes: its limit runs from the last key tile
+// whose scores were issued, told behind the flag.
+constexpr int kProgress = 1 + kParts;
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, const DevErr* err,
                                          int site) {
-  const unsigned long long t0 = globaltimer_ns();
+  unsigned long long t0 = globaltimer_ns();
+  int seen = abort_flag[kProgress];
   for (;;) {
     uint32_t ok;
     asm volatile(
@@ -597,8 +601,14 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile
         : "r"(bar), "r"(parity), "r"(kWaitSleepNs)
         : "memory");
     if (__all_sync(0xffffffffu, ok)) return true;
-    const bool late = globaltimer_ns() - t0 > err->limit_ns;
-    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+    const bool late = globaltimer_ns() - t0 > err->limit_ns, aborted = *abort_flag != 0;
+    if (__any_sync(0xffffffffu, late || aborted)) {
+      const int now = abort_flag[kProgress];
+      if (site <= 2 && !__any_sync(0xffffffffu, aborted) && __any_sync(0xffffffffu, now != seen)) {
+        seen = now;
+        t0 = globaltimer_ns();
+        continue;
+      }
       if ((threadIdx.x & 31) == 0 && !*abort_flag) report_timeout(*err, site);
       *abort_flag = 1;
       return false;
@@ -696,7 +706,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_unbounded = abort_flag + 1;   // [kParts] a part's number where values were cleared
+  // [kParts] a part's number where values were cleared; behind them how many scores were issued
+  volatile int* s_unbounded = abort_flag + 1;
   static_assert((256 * SG + 256 * kParts * (SG - 1) + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
 
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   }
   if (threadIdx.x < kParts) s_unbounded[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[kProgress] = 0;
     tma_prefetch_desc(&p.mq);
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
@@ -860,6 +871,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     Ring<SB> sring;
     Ring<QB> qring;
     Ring<kParts> at;
+    int issued = 0;
     bool ok = true;
     while (ok) {
       if (!(ok = wait(bs.part_full + 8 * at.i, at.phase, 5))) break;
@@ -892,6 +904,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             if (g == NG - 1) bar_commit(bs.s_full + 8 * sring.i);
             bar_commit(bs.k_free + 8 * keys.i);
             if (n == 1 && g == NG - 1) bar_commit(bs.q_empty + 8 * qring.i);
+            abort_flag[kProgress] = ++issued;
           }
           __syncwarp();
         }

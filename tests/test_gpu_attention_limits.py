@@ -182,3 +182,27 @@ def test_two_graphs_of_one_handle():
         assert bg.moe_attn_get_error(a) == 0
     finally:
         bg.moe_attn_destroy(a)
+
+
+@pytest.mark.parametrize("D,cache", [(256, "bf16"), (64, "e4m3")])
+def test_long_parts_within_a_short_wait_limit(D, cache):
+    """A limit of 1 ms is for what the device waits for, not for how long an SM's work takes:
+    200 row tiles of 200,000 keys take their SMs several ms each."""
+    B, L, page, Hq, Hkv = 100, 200000, 256, 8, 2
+    g, h = torch.Generator(device=DEV).manual_seed(3), torch.Generator().manual_seed(3)
+    one, pages = ref.table_of(h, [L], page)
+    kc, vc, ks, vs = ref.cache_of(g, pages, Hkv, page, D, cache)
+    table = one.expand(B, -1).contiguous()      # the requests share their pages
+    q = torch.randn(B, Hq, D, generator=g, device=DEV).bfloat16()
+    out = torch.zeros(B, Hq * D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, cache=cache, max_tokens=B, max_requests=B, rotary_dim=0,
+                                        wait_limit_ms=1), 0)
+    try:
+        bg.moe_tree_attention(a, q, B, bg.kv_cache(kc, vc, ks, vs), table, i32(range(B + 1)), i32([L] * B), out)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    for b in (0, 57, 99):
+        want, bound = ref.attention(q[b:b + 1], kc, vc, ks, vs, one, [L], [1], None, 1 / math.sqrt(D))
+        assert ((out[b:b + 1].double().view(1, Hq, D) - want).abs() <= bound).all()
