@@ -583,14 +583,15 @@ __device__ __forceinline__ bool bar_drain(Bar b, uint32_t parity, unsigned long 
 // Waits by a whole warp: true once the phase is over, false (and the CTA's abort
 // flag set) when the limit ran out or another role gave up. The part that has to
 // wait is a function of its own, out of the way of the roles' code: that of all
-// of them has to fit the instruction cache together. The planner (sites 1 and 2)
-// may wait for as long as a part takes: its limit runs from the last key tile
-// whose scores were issued, told behind the flag.
+// of them has to fit the instruction cache together. The limit runs from the
+// CTA's last step, told behind the flag: the key tiles whose scores were issued
+// and the row tiles without keys that were written. A long part may thus take its
+// time, while the planner waits for its end, or the others for a part.
 constexpr int kProgress = 1 + kParts;
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, const DevErr* err,
                                          int site) {
   unsigned long long t0 = globaltimer_ns();
-  int seen = abort_flag[kProgress];
+  int seen = abort_flag[kProgress] + abort_flag[kProgress + 1];
   for (;;) {
     uint32_t ok;
     asm volatile(
@@ -603,8 +604,8 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile
     if (__all_sync(0xffffffffu, ok)) return true;
     const bool late = globaltimer_ns() - t0 > err->limit_ns, aborted = *abort_flag != 0;
     if (__any_sync(0xffffffffu, late || aborted)) {
-      const int now = abort_flag[kProgress];
-      if (site <= 2 && !__any_sync(0xffffffffu, aborted) && __any_sync(0xffffffffu, now != seen)) {
+      const int now = abort_flag[kProgress] + abort_flag[kProgress + 1];
+      if (!__any_sync(0xffffffffu, aborted) && __any_sync(0xffffffffu, now != seen)) {
         seen = now;
         t0 = globaltimer_ns();
         continue;
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   int* s_pages = reinterpret_cast<int*>(parts + kParts + 1);    // [kParts][32] a part's first pages
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pages + 32 * kParts);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // [kParts] a part's number where values were cleared; behind them how many scores were issued
+  // [kParts] a part's number where values were cleared; behind them the CTA's steps
   volatile int* s_unbounded = abort_flag + 1;
   static_assert((256 * SG + 256 * kParts * (SG - 1) + (E ? kParts * 128 : 0)) * 4 + 8 * kBars + (kParts + 1) * sizeof(Part) +
                     128 * kParts + 64 <= Sh::kMisc, "room for barriers");
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   }
   if (threadIdx.x < kParts) s_unbounded[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
-    abort_flag[0] = abort_flag[kProgress] = 0;
+    abort_flag[0] = abort_flag[kProgress] = abort_flag[kProgress + 1] = 0;
     tma_prefetch_desc(&p.mq);
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
@@ -764,6 +765,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
           *reinterpret_cast<uint4*>(p.a.out + (long long)tok * p.a.o_ld + (long long)head * D + 8 * (i % per_row)) =
               make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
+        if (lane == 0) abort_flag[kProgress + 1] = abort_flag[kProgress + 1] + 1;
         continue;
       }
       const int page = more ? first_pages(p, s, s.k0, lane) : 0;

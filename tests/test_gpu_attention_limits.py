@@ -206,3 +206,25 @@ def test_long_parts_within_a_short_wait_limit(D, cache):
     for b in (0, 57, 99):
         want, bound = ref.attention(q[b:b + 1], kc, vc, ks, vs, one, [L], [1], None, 1 / math.sqrt(D))
         assert ((out[b:b + 1].double().view(1, Hq, D) - want).abs() <= bound).all()
+
+
+def test_many_rows_without_keys_within_a_short_wait_limit():
+    """A limit of 1 ms while an SM writes zeros for longer than that, before a request with keys."""
+    D, Hq, Hkv, page, n = 256, 16, 1, 16, 150000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    kc, vc, _, _ = ref.cache_of(g, 4, Hkv, page, D, "bf16")
+    table = i32([[0, 0, 0], [2, 1, 3]])
+    q = torch.randn(n + 3, Hq * D, generator=g, device=DEV).bfloat16()
+    out = torch.full_like(q, 5.0)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, max_tokens=n + 3, max_requests=2, rotary_dim=0,
+                                        wait_limit_ms=1), 0)
+    try:
+        bg.moe_tree_attention(a, q, n + 3, bg.kv_cache(kc, vc), table, i32([0, n, n + 3]), i32([40, 40]), out)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    assert not out[:n].any()
+    want, bound = ref.attention(q[n:].view(3, Hq, D), kc, vc, None, None, table[1:], [40], [3], None,
+                                1 / math.sqrt(D))
+    assert ((out[n:].double().view(3, Hq, D) - want).abs() <= bound).all()
