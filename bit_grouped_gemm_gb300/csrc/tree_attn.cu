@@ -230,12 +230,12 @@ struct Req {
 
 __device__ __forceinline__ Req req_of(const TaParams& p, int lo, int hi, int len) {
   lo = min(max(lo, 0), p.a.T);
-  hi = min(max(hi, 0), p.a.T);
+  const int added = max(hi, lo) - lo;   // (rows past T are not here, but the length counts them)
   Req r;
   r.row = lo;
-  r.n = max(hi - lo, 0);
+  r.n = min(added, p.a.T - lo);
   len = min(len, p.a.table_width << p.a.page_shift);
-  r.ctx = len >= r.n ? len - r.n : -1;
+  r.ctx = len >= added ? len - added : -1;
   // (exact: the quotient's error is below (2^20 + 2^8) 2^8 / 2^31 of one)
   r.tiles = (int)((unsigned long long)(unsigned)(r.n + p.R - 1) * p.inv_r >> 31);
   return r;

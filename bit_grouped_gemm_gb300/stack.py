@@ -152,7 +152,7 @@ class CachedAttention:
     the cache [pages, kv_heads, page_size, D], with scales for e4m3; ``adapters`` a
     ``binding.MoeLora`` of the first projection, or None. What a caller passes must
     outlive the layer. Rows of x behind the batch's last token are changed, but no
-    other row depends on them. A call takes up to ``max_tokens`` rows, with the layer's
+    other row depends on them; tokens of the step past the rows of x store nothing. A call takes up to ``max_tokens`` rows, with the layer's
     device as the current one; wrong arguments are refused before the first launch, so x
     is then as it was.
     """

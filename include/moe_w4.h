@@ -568,9 +568,10 @@ moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride
  * A row that sees no key, and every row of a request with length[b] < n, is zero.
  * Rows before offsets[0] and from offsets[requests] on are left as they were.
  * Keys and values that no row sees may hold anything; what a row does not see
- * does not reach it, an infinity or a NaN neither. Offsets are taken within 0..T
- * and lengths up to table_width pages; a longer length, and a table entry outside
- * the cache, sets MOE_ERR_OPERAND_RANGE for moe_attn_get_error (the length is cut,
+ * does not reach it, an infinity or a NaN neither. Rows from T on are not there
+ * (n counts them, so the others keep their context and results), offsets below 0
+ * count as 0, and lengths go up to table_width pages; a longer length, and a table
+ * entry outside the cache, sets MOE_ERR_OPERAND_RANGE for moe_attn_get_error (the length is cut,
  * the page read as zeros). Scores, softmax and sums are FP32; the weights of V
  * are rounded to bf16, with an e4m3 cache to fp16 instead, where weights below
  * 2^-32 of a row's largest count as zero. With an e4m3 cache a row's queries are
