@@ -225,11 +225,12 @@ moe_status moe_rope_store(moe_attn_t p, const uint16_t* q, long long q_stride, c
                      {slot, 4 * (size_t)T},          c[2], c[3]};
   const Span out{q_out, rows_bytes(T, a.o_ld, qc)};
   const bool in_place = q_out == q && a.o_ld == a.q_ld;
-  for (const Span& x : in) {
+  for (int i = 0; i < 7; ++i) {
+    const Span& x = in[i];
     // in place, q's rows may lie between those of k and v: the parts of one
     // projection's rows, which the rows' own columns keep apart
-    const bool fused = in_place && ((x.p == k && a.k_ld == a.q_ld) || (x.p == v && a.v_ld == a.q_ld));
-    if (!(in_place && x.p == q) && !fused && clash(out, x)) return MOE_ERR_INVALID_ARG;
+    const bool fused = in_place && ((i == 1 && a.k_ld == a.q_ld) || (i == 2 && a.v_ld == a.q_ld));
+    if (!(in_place && i == 0) && !fused && clash(out, x)) return MOE_ERR_INVALID_ARG;
     if (fused) {
       const long long d = (const uint16_t*)x.p - q, r = ((d % a.q_ld) + a.q_ld) % a.q_ld;
       if (clash(out, x) && !(r >= qc && r + kc <= a.q_ld)) return MOE_ERR_INVALID_ARG;
