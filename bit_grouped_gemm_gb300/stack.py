@@ -151,10 +151,11 @@ class CachedAttention:
     ``out`` are (qweight, scales, biases) triples, ``norm`` bf16 [H], ``k`` and ``v``
     the cache [pages, kv_heads, page_size, D], with scales for e4m3; ``adapters`` a
     ``binding.MoeLora`` of the first projection, or None. What a caller passes must
-    outlive the layer. Rows of x behind the batch's last token are changed, but no
-    other row depends on them; tokens of the step past the rows of x store nothing. A call takes up to ``max_tokens`` rows, with the layer's
-    device as the current one; wrong arguments are refused before the first launch, so x
-    is then as it was.
+    outlive the layer. The cache has at least the batch's pages. Rows of x behind the
+    batch's last token are changed, but no other row depends on them; tokens of the step
+    past the rows of x store nothing. A call takes up to ``max_tokens`` rows, with the
+    layer's device as the current one; wrong arguments are refused before the first
+    launch, so x is then as it was.
     """
 
     def __init__(self, attn: int, desc, norm, qkv, out, k, v, k_scale=None, v_scale=None,
@@ -196,6 +197,7 @@ class CachedAttention:
         ok = ok and (y is None or _rows(y, torch.float32, (T, H), dev))
         ok = ok and batch.table.device == dev and T <= batch.desc.max_tokens
         ok = ok and batch.desc.page_size == self.desc.page_size
+        ok = ok and batch.desc.ring_size <= self.cache.pages
         if adapter is not None:
             ok = ok and self.adapters is not None and _rows(adapter, torch.int32, (T,), dev)
         if not ok:

@@ -132,3 +132,16 @@ def test_another_current_device_is_refused(monkeypatch):
         with pytest.raises(binding.MoeError):
             call()
     assert not calls
+
+
+@pytest.mark.parametrize("pages,fits", [(4, True), (5, True), (6, False)])
+def test_a_batch_with_more_pages_than_the_cache_is_refused(monkeypatch, pages, fits):
+    calls, layer = make(monkeypatch)
+    p = stack.PagedBatch(B, PAGE, 4, pages, T, device="cpu")
+    if fits:
+        layer(rows(), None, p)
+        assert len(calls) == 6
+        return
+    with pytest.raises(binding.MoeError) as e:
+        layer(rows(), None, p)
+    assert e.value.status == INVALID and not calls
