@@ -166,7 +166,14 @@ class CachedAttention:
         self.q_cols, self.kv_cols = desc.heads * desc.head_dim, desc.kv_heads * desc.head_dim
         cols = self.q_cols + 2 * self.kv_cols
         shape = (k.shape[0], desc.kv_heads, desc.page_size, desc.head_dim)
-        if tuple(k.shape) != shape or (k_scale is not None) != (desc.cache_type != 0):
+        # (types are checked where the structs are made; an address has no size)
+        fits = lambda t, n: isinstance(t, int) or (t.numel() == n and t.device == dev and t.is_contiguous())
+        ok = fits(norm, H) and norm.dtype == torch.bfloat16 and tuple(k.shape) == shape
+        ok = ok and fits(k, k.numel()) and fits(v, k.numel()) and (k_scale is not None) == (desc.cache_type != 0)
+        ok = ok and all(s is None or fits(s, desc.kv_heads) for s in (k_scale, v_scale))
+        for w, n, m in ((qkv, cols, H), (out, H, self.q_cols)):
+            ok = ok and fits(w[0], n * m // 8) and fits(w[1], n * m // 64) and fits(w[2], n * m // 64)
+        if not ok:
             raise binding.MoeError(binding.MOE_ERR_INVALID_ARG, "CachedAttention")
         self.kept = (qkv, out, k, v, k_scale, v_scale)
         self.qkv_c, self.out_c = binding.w4(*qkv), binding.w4(*out)

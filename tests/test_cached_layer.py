@@ -145,3 +145,33 @@ def test_a_batch_with_more_pages_than_the_cache_is_refused(monkeypatch, pages, f
     with pytest.raises(binding.MoeError) as e:
         layer(rows(), None, p)
     assert e.value.status == INVALID and not calls
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(qkv=triple(256, H)), dict(qkv=triple(512, 2 * H)), dict(out=triple(2 * H, 256)), dict(out=triple(H, 128)),
+    dict(qkv=(triple(512, H)[0], bf16(512, 1), bf16(512, 2))),
+    dict(out=(triple(H, 256)[0], bf16(H, 4), bf16(H, 8)[:, ::2])),
+    dict(out=tuple(t.to("meta") for t in triple(H, 256))), dict(norm=bf16(H).float()),
+    dict(norm=bf16(2 * H)[::2]), dict(norm=bf16(2 * H)), dict(k=bf16(5, 2, PAGE, 64).to("meta")),
+    dict(v=bf16(5, 2, PAGE, 64).to("meta")), dict(v=bf16(5, PAGE, 2, 64).transpose(1, 2)),
+])
+def test_a_layers_tensors_have_its_sizes(monkeypatch, bad):
+    """Kernels read these by the layer's sizes: others would be read behind their ends."""
+    calls = Calls(monkeypatch)
+    d = binding.attn_desc(4, 2, 64, PAGE, max_tokens=T, max_requests=B)
+    arg = dict(norm=bf16(H), qkv=triple(512, H), out=triple(H, 256), k=bf16(5, 2, PAGE, 64), v=bf16(5, 2, PAGE, 64))
+    stack.CachedAttention(1, d, **arg, max_tokens=T)
+    with pytest.raises(binding.MoeError) as e:
+        stack.CachedAttention(1, d, **{**arg, **bad}, max_tokens=T)
+    assert e.value.status == INVALID and not calls
+
+
+@pytest.mark.parametrize("scale", [torch.ones(3), torch.ones(4)[::2], torch.ones(2).to("meta")])
+def test_scales_have_a_value_per_head(monkeypatch, scale):
+    for kw in (dict(k_scale=scale), dict(v_scale=scale)):
+        with pytest.raises(binding.MoeError):
+            make(monkeypatch, "e4m3", **kw)
