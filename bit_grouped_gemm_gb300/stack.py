@@ -180,7 +180,11 @@ class CachedAttention:
         self.cache = binding.kv_cache(k, v, k_scale, v_scale)
         rank, M = adapters.rank if adapters is not None else 0, self.max_tokens
         self.project = binding.moe_linear_create(binding.linear_desc(H, cols, M, rank), dev.index or 0)
-        self.output = binding.moe_linear_create(binding.linear_desc(self.q_cols, H, M), dev.index or 0)
+        try:
+            self.output = binding.moe_linear_create(binding.linear_desc(self.q_cols, H, M), dev.index or 0)
+        except binding.MoeError:
+            binding.moe_linear_destroy(self.project)
+            raise
         empty = lambda *shape, dt: torch.empty(shape, dtype=dt, device=dev)
         self.h8 = empty(M, H, dt=torch.float8_e4m3fn)
         self.hs = empty(M, 1, dt=torch.float32)

@@ -175,3 +175,21 @@ def test_scales_have_a_value_per_head(monkeypatch, scale):
     for kw in (dict(k_scale=scale), dict(v_scale=scale)):
         with pytest.raises(binding.MoeError):
             make(monkeypatch, "e4m3", **kw)
+
+
+def test_a_layer_that_is_refused_keeps_no_handle(monkeypatch):
+    made, gone = [], []
+
+    def create(desc, device):
+        if made:
+            raise binding.MoeError(3, "moe_linear_create")
+        made.append(7)
+        return 7
+    calls = Calls(monkeypatch)
+    monkeypatch.setattr(binding, "moe_linear_create", create)
+    monkeypatch.setattr(binding, "moe_linear_destroy", gone.append)
+    d = binding.attn_desc(4, 2, 64, PAGE, max_tokens=T, max_requests=B)
+    with pytest.raises(binding.MoeError):
+        stack.CachedAttention(1, d, bf16(H), triple(512, H), triple(H, 256), bf16(5, 2, PAGE, 64),
+                              bf16(5, 2, PAGE, 64), max_tokens=T)
+    assert made == gone and not calls
