@@ -94,6 +94,12 @@ def _here(dev) -> bool:
     return dev.type != "cuda" or dev.index == torch.cuda.current_device()
 
 
+def _settle(dev) -> None:
+    """Waits for what the current stream still has to fill: the first call may come on another."""
+    if dev.type == "cuda":
+        torch.cuda.current_stream(dev).synchronize()
+
+
 class PagedBatch:
     """The cache pages of up to ``requests`` requests, ``table_width`` each at most, and
     what a step's kernels need to know of its tokens; all of it on the device, where
@@ -123,6 +129,7 @@ class PagedBatch:
         self.pool = binding.page_pool(self.table, self.ring, self.owned, self.ring_pos)
         self.map = binding.token_map(self.length, self.offsets, self.slot, self.position,
                                      self.status, self.mask)
+        _settle(self.table.device)
 
     def step(self, context: torch.Tensor, added: torch.Tensor,
              parent: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -192,6 +199,7 @@ class CachedAttention:
         # (attention leaves rows behind the last token as they are)
         self.a = torch.zeros(M, self.q_cols, dtype=torch.bfloat16, device=dev)
         self.d = empty(M, H, dt=torch.bfloat16)
+        _settle(dev)
 
     def close(self) -> None:
         for name in ("project", "output"):

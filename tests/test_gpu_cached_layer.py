@@ -276,3 +276,36 @@ def test_two_layers_of_two_batches_on_two_streams():
     for a, b in zip(want, got):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+def test_the_first_step_may_come_on_another_stream():
+    """A batch and a layer made on a stream that is busy, used at once on another one: their first
+    state is there."""
+    want = None
+    x0 = torch.randn(70, H, generator=torch.Generator(device=DEV).manual_seed(13), device=DEV).bfloat16()
+    context, added = i32([0] * B), i32([60, 3, 0, 2])
+    for rep in range(3):
+        torch.full((1 << 20,), 2 ** 30 + 5, dtype=torch.int32, device=DEV)     # (what the allocator hands out next)
+        torch.cuda.synchronize()
+        makes, runs = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.stream(makes):
+            torch.cuda._sleep(50 * 10 ** 6)
+            s = Served()
+        with torch.cuda.stream(runs):
+            s.batch.step(context, added)
+        torch.cuda.synchronize()
+        assert s.batch.status.tolist() == [65, 6, 0, 0, 0] and s.batch.length.tolist() == [60, 3, 0, 2]
+        assert s.batch.table[:, 0].tolist() == [0, 4, 0, 5] and s.batch.ring_pos.tolist() == [6, 34]
+        with torch.cuda.stream(makes):
+            L = Layer(1, "bf16", 40, adapters=False)
+            torch.cuda._sleep(50 * 10 ** 6)
+            layer = stack.CachedAttention(L.attn, L.layer.desc, L.norm, L.qkv_w, L.out_w, L.k, L.v, max_tokens=M)
+        with torch.cuda.stream(runs):
+            x = x0.clone()
+            layer(x, None, s.batch)
+        torch.cuda.synchronize()
+        assert (layer.a[65:70] == 0).all()
+        want = x if want is None else want
+        assert torch.equal(x, want)
+        layer.close()
+        L.close()
