@@ -1,5 +1,5 @@
 """Attention over a paged cache where the call and the batch differ in size: fewer rows than the
-batch's step has."""
+batch's step has, and few requests with new tokens among many idle ones."""
 import math
 
 import pytest
@@ -77,3 +77,64 @@ def test_a_prompt_cut_after_some_row_tiles():
     with Batch([1100], [1000], Hq=8, Hkv=1, D=128) as b:
         b.run(333)
         b.check(333)
+
+
+def idle_but(at, B, L, n=1):
+    """Lengths and new tokens of a batch in which only the requests `at` have any."""
+    lengths, news = [17 + b % 5 for b in range(B)], [0] * B
+    for b in at:
+        lengths[b], news[b] = L, n
+    return lengths, news
+
+
+@pytest.mark.parametrize("cache,D", [("bf16", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("at", [[0], [2100], [4095], [0, 4095], [0, 1, 33, 64, 66, 2000, 4094], list(range(3, 4096, 97)),
+                                list(range(1000, 1300))])
+def test_few_requests_among_4096(cache, D, at):
+    """Idle requests in front, between and behind, under a wait limit of 1 ms."""
+    lengths, news = idle_but(at, 4096, 500)
+    lengths[at[-1]], news[at[-1]] = 1500, 3
+    with Batch(lengths, news, D=D, cache=cache, limit=1) as b:
+        b.run()
+        b.check()
+
+
+def test_served_and_unserved_requests_among_idle_ones():
+    """Requests that get no keys (zeros) and idle ones, in runs of all lengths up to 40."""
+    lengths, news = [], []
+    for i in range(40):
+        lengths += [300 + i, 1] + [9] * i
+        news += [1 + i % 3, 2] + [0] * i
+    with Batch(lengths, news, D=64, limit=1) as b:
+        b.run()
+        b.check()
+
+
+def graph_ms(run):
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            run()
+    times = []
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        graph.replay()
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / 10)
+    return sorted(times)[3]
+
+
+def test_idle_requests_behind_the_last_one_take_no_time():
+    """One token takes the same time whether the idle requests of a batch come before or behind it:
+    the SM that has it does not go through those behind, one after the other (717 against 79 us)."""
+    took = []
+    for at in (4095, 0):
+        with Batch(*idle_but([at], 4096, 2000), Hq=16, Hkv=2, D=128, page=64) as b:
+            took.append(graph_ms(b.run))
+            b.check()
+    assert took[1] < 3 * took[0], took
