@@ -347,7 +347,7 @@ struct Walk {
         }
         mine += cost_of(p, q, 0);
         tiles += q.ctx < 0 ? 0 : q.tiles;
-        longest = max(longest, q.ctx + q.n);
+        longest = max(longest, q.n > 0 && q.ctx >= 0 ? q.ctx + q.n : 0);   // (of those with work)
         if (blockIdx.x == 0 && q.n && lens[0] > cap) atomicOr(p.err.word, DEVERR_RANGE);
 #pragma unroll
         for (int x = 0; x < 3; ++x) {

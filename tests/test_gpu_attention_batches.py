@@ -138,3 +138,22 @@ def test_idle_requests_behind_the_last_one_take_no_time():
             took.append(graph_ms(b.run))
             b.check()
     assert took[1] < 3 * took[0], took
+
+
+@pytest.mark.parametrize("idle,n", [(100000, 0), (9000, 0), (0, 3)])
+def test_requests_without_keys_to_read_do_not_change_the_split(idle, n):
+    """A token beside a long idle context, or beside rows without keys, is shared by the SMs as
+    alone: the same sums in the same order."""
+    with Batch([2000], [1], Hq=16, Hkv=2, D=128, page=64) as b:
+        b.run()
+        b.check()
+        want = b.out.clone()
+    with Batch([2000, idle], [1, n], Hq=16, Hkv=2, D=128, page=64) as b:
+        # the same inputs
+        with Batch([2000], [1], Hq=16, Hkv=2, D=128, page=64) as one:
+            b.q[:1] = one.q
+            for mine, its in ((b.kc, one.kc), (b.vc, one.vc)):
+                mine[b.table[0, :32].long()] = its[one.table[0, :32].long()]
+        b.run()
+        b.check()
+        assert torch.equal(b.out[:1], want)
