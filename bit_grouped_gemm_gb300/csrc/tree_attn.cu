@@ -981,7 +981,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
     // A row of queries is multiplied by the power of two that brings its largest
     // element to 2^7..2^8, and its scores by the inverse. The first term is the
     // nearest e4m3, the second the nearest to what is left: of a bf16's 8 bits 4
-    // each, exactly down to 2^-10 of the row's largest element, and smaller elements
+    // each, exactly down to 2^-9 of the row's largest element (the second term's steps
+    // end at 2^-9, the last bit of an element of 2^-2), and smaller elements
     // to 2^-17 of it. The codes of values are fp16 values; a warp has 32 rows of a block.
     const int w = role - kConv;
     Ring<VR> rvals;

@@ -575,7 +575,7 @@ moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride
  * the page read as zeros). Scores, softmax and sums are FP32; the weights of V
  * are rounded to bf16, with an e4m3 cache to fp16 instead, where weights below
  * 2^-32 of a row's largest count as zero. With an e4m3 cache a row's queries are
- * kept exactly down to 2^-10 of its largest element, smaller ones to 2^-17 of it,
+ * kept exactly down to 2^-9 of its largest element, smaller ones to 2^-17 of it,
  * and an infinity among them counts as a NaN; scales are positive and finite.
  * q_stride a multiple of 8, out_stride at least heads *
  * head_dim and a multiple of 8; q, out and the cache 16-byte aligned. out overlaps

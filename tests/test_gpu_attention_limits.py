@@ -228,3 +228,42 @@ def test_many_rows_without_keys_within_a_short_wait_limit():
     want, bound = ref.attention(q[n:].view(3, Hq, D), kc, vc, None, None, table[1:], [40], [3], None,
                                 1 / math.sqrt(D))
     assert ((out[n:].double().view(3, Hq, D) - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("largest", [128.0, 2.0 ** -40, 255.0, 129.0 * 2.0 ** 20])
+@pytest.mark.parametrize("below", [0, 4, 8, 9, 10, 13])
+def test_which_queries_over_8_bit_keys_are_exact(below, largest):
+    """128 heads, whose queries hold one large element that meets zero keys, and two elements 2^-below
+    of its power of two, of all mantissas: a step of the last bit shows in the two keys' weights.
+    Exact down to 2^-9; below that an element is off by at most 2^-17 of the largest."""
+    D, Hq, page = 64, 128, 16
+    unit = 2.0 ** math.floor(math.log2(largest))
+    small = unit * 2.0 ** -below
+    q = torch.zeros(1, Hq, D, device=DEV)
+    q[:, :, 0] = largest
+    q[0, :, 1] = small * (1 + torch.arange(128, device=DEV) / 128)
+    q[:, :, 2] = small
+    assert torch.equal(q.bfloat16().float(), q)
+    q = q.bfloat16()
+    kc, vc = (torch.zeros(1, 1, page, D, device=DEV) for _ in range(2))
+    kc[0, 0, 0, 1], kc[0, 0, 1, 2], vc[0, 0, 0, 0], vc[0, 0, 1, 1] = 448.0, 448.0, 1.0, 1.0
+    kc, vc = kc.to(torch.float8_e4m3fn), vc.to(torch.float8_e4m3fn)
+    one = torch.ones(1, device=DEV)
+    # the difference of the two scores is 0.05 per step of the last bit
+    scale = 0.05 * 128 / (448.0 * small)
+    table = i32([[0]])
+    out = torch.zeros(1, Hq * D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, 1, D, page, cache="e4m3", max_tokens=1, softmax_scale=scale, rotary_dim=0), 0)
+    try:
+        bg.moe_tree_attention(a, q, 1, bg.kv_cache(kc, vc, one, one), table, i32([0, 1]), i32([2]), out)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    want, bound = ref.attention(q, kc, vc, one, one, table, [2], [1], None, scale)
+    if below > 9:
+        p = want[0, :, :1]
+        off = 2 * scale * 448.0 * 2.0 ** -17 * largest     # both elements' scores
+        bound = bound + want * math.expm1(off)
+    assert ((out.double().view(1, Hq, D) - want).abs() <= bound).all()
