@@ -5,8 +5,10 @@
 //
 // The angle is kept in turns as a 64-bit fixed-point fraction: pos times the
 // frequency's fraction, modulo 2^64, is the fraction of a turn for every int32
-// position, to 2^-33 turns; its top 32 bits go to sincospi. A float product pos
-// * f would lose the angle of far positions (0.06 rad at position 10^6).
+// position; its top 32 bits go to sincospi. The fractions come from doubles, right to
+// 2^-55 turns per position: 2^-35 at position 10^6, 2^-24 at the ends of int32; the
+// argument's rounding to FP32 is up to 2^-26. A float product pos * f would lose the
+// angle of far positions (0.06 rad at position 10^6).
 //
 // Bound by memory: every row is read once and written once. A thread takes 16
 // elements of a head (8 pairs where they turn) and up to 4 heads of the same

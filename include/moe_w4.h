@@ -546,8 +546,9 @@ moe_status moe_attn_scratch_bytes(const moe_attn_desc* desc, size_t* bytes);
 /* Rotary positions of T rows of queries [heads][head_dim] and keys, and the
  * store of keys and values [kv_heads][head_dim]:
  *   (a, b) -> gain (a cos - b sin, b cos + a sin), angle position[t] f_i,
- * the angle taken modulo a turn exactly for every int32 position. Keys and
- * values go to slot[t] of the cache, each rounded once (e4m3: the value over its
+ * the angle taken modulo a turn as a 64-bit fixed-point fraction, of frequencies in
+ * double precision: right to 2^-24 of a turn at the ends of int32, and to 2^-26 (the
+ * FP32 argument of sine and cosine) for positions up to 2^29. Keys and values go to slot[t] of the cache, each rounded once (e4m3: the value over its
  * head's scale, clamped to +-448, a NaN kept); a slot outside the cache stores
  * nothing. Two rows of one call with the same slot leave a mixture of theirs.
  * Row strides in elements, 0 = dense; multiples of 8, and q, k, v, q_out 16-byte

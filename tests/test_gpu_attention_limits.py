@@ -267,3 +267,47 @@ def test_which_queries_over_8_bit_keys_are_exact(below, largest):
         off = 2 * scale * 448.0 * 2.0 ** -17 * largest     # both elements' scores
         bound = bound + want * math.expm1(off)
     assert ((out.double().view(1, Hq, D) - want).abs() <= bound).all()
+
+
+def fractions_of_a_turn(R, theta, positions):
+    """[positions, R / 2] turns modulo one, from 60 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    out = torch.empty(len(positions), R // 2, dtype=torch.float64)
+    for i in range(R // 2):
+        # turns per position in units of 2^-160
+        f = int(Decimal(theta) ** (Decimal(-2 * i) / Decimal(R)) / two_pi * Decimal(2) ** 160)
+        for t, p in enumerate(positions):
+            out[t, i] = math.ldexp((p * f) % (1 << 160) >> 96, -64)
+    return out
+
+
+@pytest.mark.parametrize("theta", [10000.0, 500000.0])
+@pytest.mark.parametrize("far", [1000000, 2 ** 29, 2 ** 31 - 1])
+def test_angles_of_far_positions(far, theta):
+    """Cosines and sines of angles near quarter turns, where an angle's own error shows, against 60
+    digits: 2^-55 of a turn per position, 2^-26 for the FP32 argument, 2 units in the last place for
+    sincospi, and the results' rounding."""
+    D, T = 64, 2000
+    h = torch.Generator().manual_seed(far % 1000)
+    pos = torch.randint(far // 2, far, (T,), generator=h)
+    pos[::2] *= -1
+    pos[0], pos[1] = far, -far
+    x = torch.zeros(T, 3, D, dtype=torch.bfloat16, device=DEV)
+    x[..., :D // 2] = 1.0
+    kc, vc = (torch.zeros(1, 1, 16, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(1, 1, D, 16, max_tokens=T, rope_theta=theta), 0)
+    try:
+        bg.moe_rope_store(a, x, x[:, 1], x[:, 2], T, i32(pos), i32([-1] * T), out, bg.kv_cache(kc, vc),
+                          q_stride=3 * D, k_stride=3 * D, v_stride=3 * D)
+        torch.cuda.synchronize()
+    finally:
+        bg.moe_attn_destroy(a)
+    angle = 2 * math.pi * fractions_of_a_turn(D, theta, pos.tolist())
+    want = torch.cat([torch.cos(angle), torch.sin(angle)], 1)
+    assert float(want.abs().min()) < 2.0 ** -14
+    off = 2 * math.pi * (2.0 ** -55 * pos.abs().double() + 2.0 ** -26)[:, None]
+    tol = (off + 2.0 ** -22 * want.abs()) * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    assert ((out.double().cpu() - want).abs() <= tol).all()
