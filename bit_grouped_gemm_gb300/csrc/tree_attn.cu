@@ -1356,7 +1356,8 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
             if (!live) continue;
             if (fix) {
               const unsigned long long* words = mask_words();
-              const int end = min(s.keys, 128 * s.k1);
+              // (new tokens without a bit are seen by none)
+              const int end = min(min(s.keys, 128 * s.k1), words ? s.ctx + 64 * p.a.mask_words : INT_MAX);
 #pragma unroll 1
               for (int j = max(seen, 128 * k0); j < end; ++j) {
                 if (!(seen_bits(j - s.ctx, tok, words, p.a.mask_words) & 1)) continue;

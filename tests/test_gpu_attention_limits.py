@@ -311,3 +311,52 @@ def test_angles_of_far_positions(far, theta):
     off = 2 * math.pi * (2.0 ** -55 * pos.abs().double() + 2.0 ** -26)[:, None]
     tol = (off + 2.0 ** -22 * want.abs()) * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
     assert ((out.double().cpu() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("D,cache", [(256, "bf16"), (64, "e4m3")])
+def test_values_that_are_no_numbers_within_a_short_wait_limit(D, cache):
+    """A limit of 1 ms, and many new tokens under masks of one word, values without a number among
+    those that have a bit and those that have none: an SM looks only at keys that a row can see."""
+    n, ctx, page, Hq, Hkv = 20000, 100, 64, 8, 1
+    L = ctx + n
+    g, h = torch.Generator(device=DEV).manual_seed(3), torch.Generator().manual_seed(3)
+    table, pages = ref.table_of(h, [L], page)
+    kc, vc, ks, vs = ref.cache_of(g, pages, Hkv, page, D, cache)
+    nan = torch.tensor([float("nan")], device=DEV).to(vc.dtype)
+    raw = torch.uint8 if cache == "e4m3" else torch.int16
+    for token in (3, 40, 1000, 19990):
+        j = ctx + token
+        vc.view(raw)[int(table[0, j // page]), 0, j % page, token % 7::9] = nan.view(raw)
+    q = torch.randn(n, Hq, D, generator=g, device=DEV).bfloat16()
+    own = torch.arange(n, device=DEV).clamp_max(63)
+    mask = torch.randint(-2 ** 62, 2 ** 62, (n, 1), generator=g, device=DEV)
+    mask &= torch.where(own[:, None] == 63, torch.full_like(mask, -1), (1 << (own[:, None] + 1).clamp_max(62)) - 1)
+    out = torch.zeros(n, Hq * D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, cache=cache, max_tokens=n, max_requests=1, rotary_dim=0,
+                                        wait_limit_ms=1), 0)
+    try:
+        bg.moe_tree_attention(a, q, n, bg.kv_cache(kc, vc, ks, vs), table, i32([0, n]), i32([L]), out, mask=mask)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    # the keys that anyone sees: the context and the first 64 new tokens
+    j = torch.arange(ctx + 64, device=DEV)
+    ids = table[0].long()[j // page]
+    k, v = (c[ids, 0, j % page].float().double() * (1.0 if s is None else s[0].double()) for c, s in ((kc, ks), (vc, vs)))
+    see = torch.ones(n, ctx + 64, dtype=torch.bool, device=DEV)
+    see[:, ctx:] = ((mask >> torch.arange(64, device=DEV)) & 1).bool() & (j[ctx:] - ctx <= torch.arange(n, device=DEV)[:, None])
+    got = out.view(n, Hq, D)
+    for t0 in range(0, n, 4000):
+        rows = slice(t0, t0 + 4000)
+        s = (torch.einsum("thd,kd->thk", q[rows].double(), k) / math.sqrt(D)).masked_fill(~see[rows, None], -math.inf)
+        p = torch.softmax(s, 2)
+        bad = torch.einsum("tk,kd->td", see[rows].float(), torch.isnan(v).float()) > 0
+        assert torch.equal(torch.isnan(got[rows]), bad[:, None].expand(-1, Hq, -1))
+        v0 = torch.nan_to_num(v, nan=0.0)
+        want, A = torch.einsum("thk,kd->thd", p, v0), torch.einsum("thk,kd->thd", p, v0.abs())
+        # the weights' rounding and the output's, and scores of D products in FP32
+        es = (D + 8) * 2.0 ** -23 * torch.einsum("thd,kd->thk", q[rows].double().abs(), k.abs()).amax(2) / math.sqrt(D)
+        bound = A * (2.0 ** -8 + 4 * es[:, :, None] + 2 * (2.0 ** -20 + 2 * L * 2.0 ** -23)) + 2.0 ** -8 * want.abs()
+        off = ((got[rows].double() - want).abs() - bound).masked_fill(bad[:, None], -1.0)
+        assert (off <= 0).all()
