@@ -11,6 +11,11 @@
 // CTAs: every CTA repeats the sums (they fit one pass of its threads), and one
 // cluster barrier, which the rows' work hides, separates the reads of the pool's
 // state from its update in place, which a grid of independent CTAs could not order.
+//
+// Measured (in a graph): one token 3.3 us, 256 trees of 16 5.6. The 8 CTAs take all rows,
+// padding among them: 64 tokens in 4096, 65,536 and 2^20 rows 3.9, 8.3, 85 us; 65,536 and
+// 2^20 rows of prompts 15.9, 226 us. A chain given as 256 parents is 256 loads one after
+// the other, 41 us; without parents a chain costs nothing.
 #include "moe_common.cuh"
 #include "spans.h"
 

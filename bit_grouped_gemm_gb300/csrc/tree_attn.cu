@@ -34,15 +34,18 @@
 //     see them, added at the end.
 //
 // Measured (in a graph; 16 query heads, 2 key-value heads, pages of 64, one GB300):
-// one token of each of 76 contexts of 16000, bf16: head_dim 64 101 us, 128 184, 256
-// 351 (6.2, 6.8, 7.1 TB/s: memory); e4m3 99, 112, 218 (3.2, 5.6, 5.7 TB/s: a tile's
-// way through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need
-// 700 to 2,800). 2 prompts of 2000 tokens behind 4096: 107, 132, 229 us (0.67, 1.08,
-// 1.25 PFLOP/s). There a key tile takes 1,500 cycles at head_dim 128, its products
+// one token of each of 76 contexts of 16000, bf16: head_dim 64 98 us, 128 182, 256 348
+// (6.3, 6.9, 7.2 TB/s: memory); e4m3 92, 110, 222 (3.4, 5.7, 5.6 TB/s: a tile's way
+// through the roles, 1,400 cycles at 64 to 3,000 at 256, of which its bytes need 700 to
+// 2,800). 76 are a row tile per SM, so that nothing is split; 60, 100 and 200 contexts at
+// head_dim 128: bf16 153, 248, 476 us (6.4, 6.6, 6.9 TB/s), e4m3 102, 163, 317 (4.8, 5.0,
+// 5.2). 2 prompts of 2000 tokens behind 4096 at head_dim 64, 128, 256: bf16 103, 129, 230
+// us (0.81, 1.29, 1.45 PFLOP/s), e4m3 113, 141, 261 (every row tile turns its values to
+// fp16 anew). There a key tile takes 1,500 cycles at head_dim 128 in bf16, its products
 // 1,024: its chain of 4,400 (S 950, softmax 2,400, P V 1,050) runs in 3 tiles at a
 // time, which is all that tensor memory has place for; and 5,000 more go where a
 // row tile ends (masked tile, sums read and stored). One token of one context of
-// 120, 2000 and 32000: 8.7, 11.0, 17.8 us: two launches, planning 2, a page's
+// 120, 2000 and 32000: 8.3, 10.9, 18.1 us: two launches, planning 2, a page's
 // number and loads 1.5, the chain 2.5, sums out 1, join 2.
 #include <limits.h>
 
@@ -376,10 +379,11 @@ struct Walk {
     // A share holds at least a row tile's cost and one key tile. Where that would leave SMs
     // idle the cost is taken lower: to nothing for few row tiles, whose key tiles then go
     // singly, else to a key tile, so that an SM does not begin many short ones; but the
-    // longest row tile is in 16 parts at most, which its warps join in one round. Measured
-    // (head_dim 128) so and with the whole cost: one token of 2000 11.1 and 11.5 us, 4 trees of
-    // 16 behind 1000 13.0 and 14.2, 32 behind 1 to 2000 16.3 and 18.7; with no cost whatever
-    // the number, the last 27.7; in more parts, one token of 8000 16.6 for 13.3.
+    // longest row tile, if of up to 7,168 keys, is in 16 parts at most, which its warps join in
+    // one round (a longer one bears the whole cost: 9,000 keys go in 21). Measured (head_dim
+    // 128) so and with the whole cost: one token of 2000 11.1 and 11.5 us, 4 trees of 16 behind
+    // 1000 13.0 and 14.2, 32 behind 1 to 2000 16.3 and 18.7; with no cost whatever the number,
+    // the last 27.7; in more parts, one token of 8000 16.6 for 13.3.
     longest = __reduce_max_sync(0xffffffffu, longest);
     item = total + (long long)all_tiles * kItemCost >= (long long)gridDim.x * (kItemCost + 128)
                ? kItemCost : min(kItemCost, max(8 * all_tiles <= gridDim.x ? 1 : 128, longest / 16 - 128));

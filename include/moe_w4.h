@@ -497,8 +497,11 @@ typedef struct {
  *     parent is no earlier token (these count as -1).
  * parent needs mask_words >= 1. All arrays 4-byte aligned, mask 8. No two of
  * the written arrays overlap, nor a written one and one that is read but for
- * the pairs named above; table and ring are both. Needs no handle; runs on the
- * current device. */
+ * the pairs named above; table and ring are both. Calls on one pool are ordered on the
+ * device. The new tokens of a tree have the slots of their rows: whoever accepts a path
+ * of it whose rows are not consecutive moves its keys and values, or stores them again,
+ * before the next step counts them as context. Needs no handle; runs on the current
+ * device. */
 moe_status moe_page_map(const moe_page_desc* desc, const int32_t* context, const int32_t* added,
                         const int32_t* parent, const moe_page_pool* pool, const moe_token_map* out,
                         moe_stream_t stream);
@@ -510,7 +513,10 @@ typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
 /* Frequencies f_i = theta^(-2i / rotary_dim) for long contexts: as they are,
  * all divided by `factor`, or by parts: with r = original f_i / 2 pi turns within
  * the original length and g = clamp((r - low) / (high - low), 0, 1),
- * f_i (g + (1 - g) / factor). */
+ * f_i (g + (1 - g) / factor). The ramp is over the turns; a checkpoint whose ramp is over
+ * the pair's index between two rounded ends has other frequencies (up to 41% at theta
+ * 10000, original 32768, low 1, high 32, factor 4 and 64 elements that turn), which this
+ * does not give. */
 typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_BY_PARTS = 2 } moe_rope_scaling;
 
 typedef struct {
@@ -566,7 +572,8 @@ moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride
  *   out[t][h] = softmax(scale q[t][h] K^T over the keys seen) V  (bf16, rounded once)
  * Offsets ascend. Key-value head h / (heads / kv_heads) serves query head h. mask: [T][mask_words],
  * mask_words 1..4; new tokens past 64 * mask_words have no bit and are not seen.
- * A row that sees no key, and every row of a request with length[b] < n, is zero.
+ * A row that sees no key, or none whose score is above -infinity, is zero, and so is
+ * every row of a request with length[b] < n.
  * Rows before offsets[0] and from offsets[requests] on are left as they were.
  * Keys and values that no row sees may hold anything; what a row does not see
  * does not reach it, an infinity or a NaN neither. Rows from T on are not there
