@@ -606,14 +606,18 @@ __device__ __forceinline__ bool bar_drain(Bar b, uint32_t parity, unsigned long 
 // flag set) when the limit ran out or another role gave up. The part that has to
 // wait is a function of its own, out of the way of the roles' code: that of all
 // of them has to fit the instruction cache together. The limit runs from the
-// CTA's last step, told behind the flag: the key tiles whose scores were issued
-// and the row tiles without keys that were written. A long part may thus take its
-// time, while the planner waits for its end, or the others for a part.
+// CTA's last step, told behind the flag: the key tiles whose scores were issued, the
+// row tiles without keys that were written, and, at head_dim 256, each 32 columns of
+// values that are no numbers that a warp has added. A long part may thus take its time,
+// while the planner waits for its end, or the others for a part.
 constexpr int kProgress = 1 + kParts;
+__device__ __forceinline__ int steps_of(volatile int* abort_flag) {
+  return abort_flag[kProgress] + abort_flag[kProgress + 1] + abort_flag[kProgress + 2];
+}
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag, const DevErr* err,
                                          int site) {
   unsigned long long t0 = globaltimer_ns();
-  int seen = abort_flag[kProgress] + abort_flag[kProgress + 1];
+  int seen = steps_of(abort_flag);
   for (;;) {
     uint32_t ok;
     asm volatile(
@@ -626,7 +630,7 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile
     if (__all_sync(0xffffffffu, ok)) return true;
     const bool late = globaltimer_ns() - t0 > err->limit_ns, aborted = *abort_flag != 0;
     if (__any_sync(0xffffffffu, late || aborted)) {
-      const int now = abort_flag[kProgress] + abort_flag[kProgress + 1];
+      const int now = steps_of(abort_flag);
       if (!__any_sync(0xffffffffu, aborted) && __any_sync(0xffffffffu, now != seen)) {
         seen = now;
         t0 = globaltimer_ns();
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
   }
   if (threadIdx.x < kParts) s_unbounded[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
-    abort_flag[0] = abort_flag[kProgress] = abort_flag[kProgress + 1] = 0;
+    abort_flag[0] = abort_flag[kProgress] = abort_flag[kProgress + 1] = abort_flag[kProgress + 2] = 0;
     tma_prefetch_desc(&p.mq);
     tma_prefetch_desc(&p.mk);
     tma_prefetch_desc(&p.mv);
@@ -1375,6 +1379,10 @@ __global__ void __launch_bounds__(Shape<D, E>::kThreads, 1)
                   if (!(fabsf(v) < INFINITY)) o[q] = __float_as_uint(__uint_as_float(o[q]) + v);
                 }
               }
+              // (a part's 256 keys at most take a row's warp 1 ms at head_dim 256, half of that below,
+              // where one more address held in registers cost 2 contexts of 131072 in e4m3 2%)
+              if constexpr (D == 256)
+                if (lane == 0) atomicAdd(const_cast<int*>(abort_flag) + kProgress + 2, 1);
             }
             if (whole) {
 #pragma unroll

@@ -360,3 +360,34 @@ def test_values_that_are_no_numbers_within_a_short_wait_limit(D, cache):
         bound = A * (2.0 ** -8 + 4 * es[:, :, None] + 2 * (2.0 ** -20 + 2 * L * 2.0 ** -23)) + 2.0 ** -8 * want.abs()
         off = ((got[rows].double() - want).abs() - bound).masked_fill(bad[:, None], -1.0)
         assert (off <= 0).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [256, 128, 64])
+def test_no_value_a_number_within_a_short_wait_limit(D, cache):
+    """A limit of 1 ms where all values of 64 trees of 256 tokens are NaN: at head_dim 256 an SM takes
+    longer than that to add them to the rows that see them."""
+    B, n, ctx, page, Hq, Hkv = 64, 256, 500, 16, 8 * 256 // D, 8 * 256 // D
+    L = ctx + n
+    g, h = torch.Generator(device=DEV).manual_seed(3), torch.Generator().manual_seed(3)
+    table, pages = ref.table_of(h, [L] * B, page)
+    kc, vc, ks, vs = ref.cache_of(g, pages, Hkv, page, D, cache)
+    raw = torch.uint8 if cache == "e4m3" else torch.int16
+    vc.view(raw)[..., 1:] = torch.tensor([float("nan")], device=DEV).to(vc.dtype).view(raw)
+    vc[..., 0] = 1.0                       # one column of numbers: its result is the weights' sum
+    q = torch.randn(n * B, Hq, D, generator=g, device=DEV).bfloat16()
+    mask = torch.full((n * B, 4), -1, dtype=torch.int64, device=DEV)
+    out = torch.zeros(n * B, Hq, D, dtype=torch.bfloat16, device=DEV)
+    a = bg.moe_attn_create(bg.attn_desc(Hq, Hkv, D, page, cache=cache, max_tokens=n * B, max_requests=B, rotary_dim=0,
+                                        wait_limit_ms=1), 0)
+    try:
+        bg.moe_tree_attention(a, q, n * B, bg.kv_cache(kc, vc, ks, vs), table, i32(range(0, n * B + 1, n)), i32([L] * B),
+                              out, mask=mask)
+        torch.cuda.synchronize()
+        assert bg.moe_attn_get_error(a) == 0
+    finally:
+        bg.moe_attn_destroy(a)
+    assert torch.isnan(out[..., 1:]).all()
+    one = vs[:, None].expand(Hkv, 1).view(1, Hq) if vs is not None else torch.ones(1, Hq, device=DEV)
+    # weights rounded to bf16, their sum in FP32, and the result's rounding
+    assert ((out[..., 0].float() / one - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -12).all()
