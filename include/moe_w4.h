@@ -581,8 +581,8 @@ moe_status moe_rope_store(moe_attn_t attn, const uint16_t* q, long long q_stride
  * count as 0, and lengths go up to table_width pages; a longer length, and a table
  * entry outside the cache, sets MOE_ERR_OPERAND_RANGE for moe_attn_get_error (the length is cut,
  * the page read as zeros). Scores, softmax and sums are FP32; the weights of V
- * are rounded to bf16, with an e4m3 cache to fp16 instead, where weights below
- * 2^-32 of a row's largest count as zero. With an e4m3 cache a row's queries are
+ * are rounded to bf16, with an e4m3 cache to fp16 instead, in steps of 2^-31 of a
+ * row's largest for weights below 2^-21 of it; those below 2^-32 count as zero. With an e4m3 cache a row's queries are
  * kept exactly down to 2^-9 of its largest element, smaller ones to 2^-17 of it,
  * and an infinity among them counts as a NaN; scales are positive and finite.
  * q_stride a multiple of 8, out_stride at least heads *
